@@ -385,6 +385,109 @@ moe_status moe_graph_capture_end(void* capture_stream, moe_graph* graph);
 moe_status moe_graph_launch(moe_graph graph, void* stream);
 moe_status moe_graph_destroy(moe_graph graph);
 
+/* ---------------------------------------------------------------------------------------------
+ * Attention and the paged key/value cache: what a decoder block needs around the MoE layer.
+ *   csdn/6a462027 §4.3 (a block is attention, then the MoE FFN); csdn/6a919c0d §3.3 (a paged cache).
+ * H query heads share H_kv key/value heads (H % H_kv == 0): query head h reads key/value head
+ *   h / (H / H_kv). Heads of D elements, D % 8 == 0, 8 <= D <= 256; q, k, v and out are `dt` (bf16 or
+ *   fp32); scores, softmax statistics and sums are fp32. `scale` (> 0, finite) multiplies the scores.
+ * Token strides are in elements: token t of q is at q + t * q_stride, its heads [H][D] dense, so q, k
+ *   and v may be slices of one fused projection. Every pointer and every token stride in bytes is a
+ *   multiple of 16; anything else is MOE_ERR_INVALID_ARG.
+ * A row that sees no key has out = 0 and lse = -inf. lse (nullable) is the natural logarithm of the sum
+ *   of the exponentials of the scaled scores, fp32.
+ * A non-finite key or value reaches only the rows that see its position.
+ *
+ * moe_attention_prompt — attention over packed prompts. Sequence i has the query tokens
+ *   q_offsets[i] .. q_offsets[i+1]-1 and the keys kv_offsets[i] .. kv_offsets[i+1]-1 (int32 device
+ *   arrays [n_seqs + 1], offsets[0] = 0, non-decreasing, last entry Tq / Tkv; kv_offsets NULL: the
+ *   same as q_offsets, Tkv = Tq). With MOE_ATTN_CAUSAL query token t of L_q sees the first
+ *   t + 1 + L_kv - L_q keys (clipped to [0, L_kv]): the queries are the last L_q of L_kv positions;
+ *   without it every key. Lengths of 0 are valid.
+ * In:  q [Tq, H, D], k, v [Tkv, H_kv, D] (token strides q_stride, k_stride, v_stride).
+ * Out: out [Tq, H, D] (token stride out_stride), lse [Tq, H] or NULL.
+ * Workspace: at least 256 bytes, prepared with moe_workspace_init (status word).
+ * Device checks: offsets that decrease or leave [0, Tq] / [0, Tkv] record MOE_ERR_DEVICE_CHECK
+ *   (detail = sequence) and that sequence's rows are not computed.
+ */
+enum { MOE_ATTN_CAUSAL = 1 };
+moe_status moe_attention_prompt(const void* q, const void* k, const void* v, const int32_t* q_offsets,
+                                const int32_t* kv_offsets, int n_seqs, int Tq, int Tkv, int H, int H_kv, int D,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride, float scale,
+                                int flags, moe_dtype dt, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/* A paged key/value cache. All arrays are device memory that the caller owns; the struct itself is read
+ * on the host during each call. A slot holds one sequence: position p of slot s is row p % page_size of
+ * page table[s][p / page_size]. Pages may be shared between slots; refs counts the table entries that
+ * name a page, and a page is free exactly when its count is 0. table entries past a slot's pages are -1.
+ * A partly filled last page that is shared is copied when its slot grows, so no slot ever sees another's
+ * writes. Allocation always takes the lowest free pages, in the order of the call's entries, so that
+ * every result is reproducible. */
+typedef struct {
+  void* k;         /* [n_layers][n_pages][H_kv][page_size][D] (dt) */
+  void* v;         /* the same */
+  int32_t* table;  /* [n_slots][table_width] */
+  int32_t* lens;   /* [n_slots] positions held */
+  int32_t* refs;   /* [n_pages] */
+  int n_layers, n_pages, page_size; /* page_size 16, 32, 64, 128 or 256 */
+  int n_slots, table_width, H_kv, D;
+  moe_dtype dt;
+} moe_kv_cache;
+
+/* Scratch for the calls below on this cache (0 on bad sizes). moe_cache_workspace_init prepares it, once;
+ * moe_cache_clear empties the cache (every slot length 0, every page free). The status word of the
+ * workspace is read with moe_get_device_status. Calls on one cache must not overlap in time. */
+size_t moe_cache_workspace_bytes(const moe_kv_cache* cache);
+moe_status moe_cache_workspace_init(const moe_kv_cache* cache, void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_cache_clear(const moe_kv_cache* cache, void* stream);
+
+/* moe_cache_resize — slot slots[i] gets length new_lens[i] (n entries, distinct slots, n <= n_slots).
+ *   First every shrinking slot gives up its pages past the new length, then growing slots get pages
+ *   (0 frees a slot; a smaller length takes drafted tokens back). New positions hold nothing yet: write
+ *   them with moe_cache_write, once per layer.
+ * moe_cache_fork — slot dst[i] becomes a copy of slot src[i]: what dst[i] held is released first, full
+ *   pages are shared, a partly filled last page is copied (all layers). Every dst is distinct and no
+ *   dst is a src.
+ * moe_cache_compact — with L pages in use, the j-th used page at or above L moves to the j-th free page
+ *   below L (all layers), and the tables follow: the pool's upper part is then free. n_live (device
+ *   int32, nullable) receives L.
+ * moe_cache_copy_pages — page dst[i] gets page src[i]'s contents (all layers); tables and counts are
+ *   untouched. No dst may also be a src or appear twice (its contents would be unspecified).
+ * moe_cache_write — tokens offsets[i] .. offsets[i+1]-1 of k_new, v_new [total, H_kv, D] become
+ *   positions pos[i], pos[i]+1, ... of slot slots[i] in one layer.
+ * Device checks (MOE_ERR_DEVICE_CHECK, detail = entry or token; the entry is skipped, the rest goes on):
+ *   a slot or page out of range, a slot named twice (the first entry counts), a length outside
+ *   [0, table_width * page_size], a dst that is also a src, a position at or past the slot's length, a
+ *   write into a shared page, and pages running out: entries are served in order while the free pages
+ *   last, and an entry that does not fit leaves its slot as it was (a fork's dst: empty). */
+moe_status moe_cache_resize(const moe_kv_cache* cache, const int32_t* slots, const int32_t* new_lens, int n,
+                            void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_cache_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* workspace,
+                          size_t ws_bytes, void* stream);
+moe_status moe_cache_compact(const moe_kv_cache* cache, int32_t* n_live, void* workspace, size_t ws_bytes,
+                             void* stream);
+moe_status moe_cache_copy_pages(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n,
+                                void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_cache_write(const moe_kv_cache* cache, int layer, const int32_t* slots, const int32_t* offsets,
+                           const int32_t* pos, int n, int total, const void* k_new, const void* v_new,
+                           int64_t k_stride, int64_t v_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* moe_attention_decode — one query token for each of n sequences over the cache: row i attends the
+ *   lens[slots[i]] positions of slot slots[i] (its own new token included, once written).
+ *   shared_len (a multiple of page_size, 0: none) says that the first shared_len positions of all n
+ *   slots are the same pages (as moe_cache_fork leaves them): their keys are read once for the whole
+ *   batch, the rest once per sequence, and the parts are joined.
+ * In:  q [n, H, D] (token stride q_stride), slots [n].  Out: out [n, H, D] (out_stride), lse [n, H] or NULL.
+ * Workspace: moe_attention_workspace_bytes(n, H, D) bytes, prepared with moe_workspace_init.
+ * Device checks: a slot or page out of range, or a slot shorter than shared_len or with other pages there,
+ *   records MOE_ERR_DEVICE_CHECK (detail = row); an out-of-range slot's row is 0, the others' rows then
+ *   follow the first slot's pages. */
+size_t moe_attention_workspace_bytes(int n, int H, int D);
+moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
+                                int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,
+                                float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,10 +26,13 @@ MOE_DTYPE_BF16 = 1
 PATH_AUTO, PATH_TENSOR, PATH_STREAM, PATH_SIMT, PATH_TENSOR_PAIR, PATH_TENSOR_T = 0, 1, 2, 3, 4, 5
 GATES_RENORMALISE = 1
 CAPACITY_REROUTE = 2
+ATTN_CAUSAL = 1
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_i64 = ctypes.c_int64
+_f = ctypes.c_float
 
 # name -> argument types (all return int moe_status unless listed in _RESTYPES)
 SIGNATURES = {
@@ -70,9 +73,22 @@ SIGNATURES = {
     "moe_get_device_status": [_p, _p, _p],
     "moe_status_string": [_i],
     "moe_selftest_wait_timeout": [_p, _sz, _i, _p],
+    "moe_attention_prompt": [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i64, _i64, _i64, _f, _i, _i, _p, _p, _p,
+                             _sz, _p],
+    "moe_attention_workspace_bytes": [_i, _i, _i],
+    "moe_attention_decode": [_p, _i, _p, _p, _i, _i, _i64, _i64, _i, _f, _p, _p, _p, _sz, _p],
+    "moe_cache_workspace_bytes": [_p],
+    "moe_cache_workspace_init": [_p, _p, _sz, _p],
+    "moe_cache_clear": [_p, _p],
+    "moe_cache_resize": [_p, _p, _p, _i, _p, _sz, _p],
+    "moe_cache_fork": [_p, _p, _p, _i, _p, _sz, _p],
+    "moe_cache_compact": [_p, _p, _p, _sz, _p],
+    "moe_cache_copy_pages": [_p, _p, _p, _i, _p, _sz, _p],
+    "moe_cache_write": [_p, _i, _p, _p, _p, _i, _i, _p, _p, _i64, _i64, _p, _sz, _p],
 }
 _RESTYPES = {"moe_workspace_bytes": ctypes.c_size_t, "moe_status_string": ctypes.c_char_p,
-             "moe_qweight_bytes": ctypes.c_size_t, "moe_qscale_bytes": ctypes.c_size_t}
+             "moe_qweight_bytes": ctypes.c_size_t, "moe_qscale_bytes": ctypes.c_size_t,
+             "moe_attention_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t}
 
 _LIB = None
 

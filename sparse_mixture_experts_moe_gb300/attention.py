@@ -1,0 +1,292 @@
+"""Attention and the paged key/value cache around the MoE layer (moe_attention_*, moe_cache_* of include/moe.h).
+
+    attn = Attention(heads=32, kv_heads=8, head_dim=128, dtype=torch.bfloat16)
+    out = attn.prompt(q, k, v, offsets)               # packed prompts, causal
+    cache = KVCache.create(n_layers, n_pages, page_size, n_slots, max_len, kv_heads=8, head_dim=128,
+                           dtype=torch.bfloat16, device="cuda")
+    cache.resize(slots, new_lens)                     # pages for the new positions (0 frees a slot)
+    cache.write(k, v, slots, offsets, pos, layer=l)   # their keys and values, once per layer
+    out = attn.decode(q, cache, slots, layer=l, shared_len=n)   # one token a sequence
+    cache.fork(src, dst)                              # samples of one sequence share its full pages
+
+Everything is enqueued on the current stream, or on `stream`; nothing synchronises, except that the first call
+on a stream (and one that needs a larger workspace) waits for its workspace to be cleared. Index tensors (offsets,
+slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the work is
+done by the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _lib
+from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
+
+
+class _Cache(ctypes.Structure):
+    """moe_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("n_layers", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_slots", ctypes.c_int), ("table_width", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("dt", ctypes.c_int)]
+
+
+def _heads(t, name, heads, dim, dtype, device):
+    """Checks a [T, heads, dim] tensor whose heads are dense within a token; returns (T, token stride)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.dtype != dtype or t.device != device:
+        raise ValueError(f"moe: expected {name} [T, {heads}, {dim}] in {dtype} on {device}, got {tuple(t.shape)} in "
+                         f"{t.dtype} on {t.device}")
+    T, (st, sh, sd) = t.shape[0], t.stride()
+    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+        raise ValueError(f"moe: {name} must have dense heads within a token (strides {t.stride()})")
+    # a single token's stride means nothing: any valid one will do
+    return T, (heads * dim if T < 2 else st)
+
+
+def _ints(t, name, n, device):
+    """Checks an int32 index tensor of n entries (None: any number); returns its length."""
+    import torch
+    if t.dim() != 1 or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"moe: {name} must be a contiguous one-dimensional int32 tensor on {device}")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"moe: {name} has {t.shape[0]} entries; the call needs {n}")
+    return t.shape[0]
+
+
+def _on_cuda(device, what):
+    if device.type != "cuda":
+        raise ValueError(f"moe: {what} must be CUDA tensors (got {device})")
+
+
+class _Workspaces:
+    """Zeroed workspaces, one for each stream that calls arrive on, so that calls on different streams never
+    share scratch memory. Each is kept for good: work in flight may use one that a larger one replaced, or
+    that a graph recorded."""
+
+    def __init__(self):
+        self._of = {}
+        self._old = []
+
+    def get(self, stream, nbytes, device):
+        ws = self._of.get(stream)
+        if ws is None or ws[1] < nbytes:
+            import torch
+            if ws is not None:
+                self._old.append(ws)
+            t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            ws = (t, nbytes, t.data_ptr())
+            if torch.cuda.is_current_stream_capturing():
+                self._old.append(ws)  # zeroed by the graph being recorded, so for that recording only
+            else:
+                torch.cuda.current_stream(device).synchronize()  # zeroed before any stream uses it
+                self._of[stream] = ws
+        return ws
+
+    def status(self):
+        """(status, detail) of the first device-side error of any of them; clears it."""
+        for stream, ws in self._of.items():
+            st, detail = _lib.get_device_status(ws[0], stream)
+            if st != MOE_OK:
+                return st, detail
+        return MOE_OK, 0
+
+
+class KVCache:
+    """A paged key/value cache over tensors that the caller owns: k, v [layers, pages, kv_heads, page_size,
+    head_dim] (bf16 or fp32), table [slots, width], lens [slots], refs [pages] (int32). KVCache.create
+    allocates an empty one."""
+
+    def __init__(self, k, v, table, lens, refs):
+        import torch
+        if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("KVCache: expected k and v [layers, pages, kv_heads, page_size, head_dim] alike")
+        if table.dim() != 2 or lens.shape != table.shape[:1] or refs.shape != k.shape[1:2]:
+            raise ValueError("KVCache: expected table [slots, width], lens [slots], refs [pages]")
+        for name, t in (("table", table), ("lens", lens), ("refs", refs)):
+            if t.dtype != torch.int32:
+                raise ValueError(f"KVCache: {name} must be int32")
+        if any(t.device != k.device for t in (v, table, lens, refs)):
+            raise ValueError("KVCache: all tensors must be on one device")
+        self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
+        self.n_layers, self.n_pages, self.kv_heads, self.page_size, self.head_dim = (int(x) for x in k.shape)
+        self.n_slots, self.width = (int(x) for x in table.shape)
+        self.dtype, self.device = k.dtype, k.device
+        self.dt = _lib.dtype_code(k)
+        self._c = _Cache(_ptr(k), _ptr(v), _ptr(table), _ptr(lens), _ptr(refs), self.n_layers, self.n_pages,
+                         self.page_size, self.n_slots, self.width, self.kv_heads, self.head_dim, self.dt)
+        self._ref = ctypes.addressof(self._c)
+        self._lib = _lib.lib()
+        self._bytes = int(self._lib.moe_cache_workspace_bytes(self._ref))
+        if self._bytes == 0:
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_cache_workspace_bytes")
+        self._ws = _Workspaces()
+
+    @classmethod
+    def create(cls, n_layers, n_pages, page_size, n_slots, max_len, kv_heads, head_dim, dtype, device="cuda"):
+        """An empty cache: n_pages pages of page_size positions, n_slots sequences of at most max_len."""
+        import torch
+        width = max(1, -(-max_len // page_size))
+        k = torch.empty((n_layers, n_pages, kv_heads, page_size, head_dim), dtype=dtype, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(k, torch.empty_like(k), torch.full((n_slots, width), -1, **i32), torch.zeros(n_slots, **i32),
+                   torch.zeros(n_pages, **i32))
+
+    def _workspace(self, stream):
+        return self._ws.get(stream, self._bytes, self.device)
+
+    def clear(self, stream=None):
+        """Empties every slot and frees every page."""
+        _check(self._lib.moe_cache_clear(self._ref, _stream(stream)), "moe_cache_clear")
+
+    def resize(self, slots, new_lens, stream=None):
+        """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
+        n = _ints(slots, "slots", None, self.device)
+        _ints(new_lens, "new_lens", n, self.device)
+        s = _stream(stream)
+        ws = self._workspace(s)
+        _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
+               "moe_cache_resize")
+
+    def write(self, k, v, slots, offsets, pos, layer=0, stream=None):
+        """Tokens offsets[i] .. offsets[i+1]-1 of k, v [total, kv_heads, head_dim] become positions pos[i], pos[i]+1,
+        ... of slot slots[i] in one layer."""
+        total, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, self.device)
+        tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, self.device)
+        if tv != total:
+            raise ValueError(f"moe: k has {total} tokens, v has {tv}")
+        n = _ints(slots, "slots", None, self.device)
+        _ints(offsets, "offsets", n + 1, self.device)
+        _ints(pos, "pos", n, self.device)
+        s = _stream(stream)
+        ws = self._workspace(s)
+        _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
+                                         k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
+
+    def fork(self, src, dst, stream=None):
+        """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
+        n = _ints(src, "src", None, self.device)
+        _ints(dst, "dst", n, self.device)
+        s = _stream(stream)
+        ws = self._workspace(s)
+        _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
+
+    def compact(self, n_live=None, stream=None):
+        """Moves the pages in use to the pool's lowest page numbers; returns their number, a one-entry int32
+        tensor (n_live, if given)."""
+        import torch
+        if n_live is None:
+            if stream is not None:
+                raise ValueError("moe: pass n_live with an explicit stream")
+            n_live = torch.empty(1, dtype=torch.int32, device=self.device)
+        _ints(n_live, "n_live", 1, self.device)
+        s = _stream(stream)
+        ws = self._workspace(s)
+        _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
+        return n_live
+
+    def copy_pages(self, src, dst, stream=None):
+        """Page dst[i] gets page src[i]'s contents in every layer."""
+        n = _ints(src, "src", None, self.device)
+        _ints(dst, "dst", n, self.device)
+        s = _stream(stream)
+        ws = self._workspace(s)
+        _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
+               "moe_cache_copy_pages")
+
+    def device_status(self):
+        """(status, detail) of the first device-side error since the last call; synchronises."""
+        return self._ws.status()
+
+
+class Attention:
+    """Attention of `heads` query heads over `kv_heads` key/value heads of head_dim elements. Holds a workspace."""
+
+    def __init__(self, heads, kv_heads, head_dim, dtype, scale=None):
+        import torch
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"unsupported dtype {dtype}")
+        self.heads, self.kv_heads, self.head_dim, self.dtype = int(heads), int(kv_heads), int(head_dim), dtype
+        self.dt = _lib.MOE_DTYPE_BF16 if dtype == torch.bfloat16 else _lib.MOE_DTYPE_F32
+        if (self.heads < 1 or self.kv_heads < 1 or self.heads % self.kv_heads or self.head_dim % 8
+                or not 8 <= self.head_dim <= 256):
+            raise ValueError("Attention: heads must be a multiple of kv_heads, head_dim a multiple of 8 from 8 to 256")
+        self.scale = float(scale) if scale is not None else self.head_dim ** -0.5
+        self._lib = _lib.lib()
+        self._ws = _Workspaces()
+        self._need = {}
+
+    def _workspace(self, stream, n, device):
+        need = self._need.get(n)
+        if need is None:
+            need = int(self._lib.moe_attention_workspace_bytes(n, self.heads, self.head_dim))
+            if need == 0:
+                raise MoeError(MOE_ERR_INVALID_ARG, "moe_attention_workspace_bytes")
+            self._need[n] = need
+        return self._ws.get(stream, need, device)
+
+    def _out(self, q, out, lse, stream):
+        import torch
+        if out is None:
+            if stream is not None:  # a tensor made here belongs to the current stream
+                raise ValueError("moe: pass out with an explicit stream")
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            so = self.heads * self.head_dim
+        else:
+            to, so = _heads(out, "out", self.heads, self.head_dim, self.dtype, q.device)
+            if to != q.shape[0]:
+                raise ValueError(f"moe: expected out {tuple(q.shape)}, got {tuple(out.shape)}")
+        if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or lse.dtype != torch.float32
+                                or lse.device != q.device or not lse.is_contiguous()):
+            raise ValueError(f"moe: expected lse {tuple(q.shape[:2])}, float32, contiguous, on {q.device}")
+        return out, so
+
+    def prompt(self, q, k, v, q_offsets, kv_offsets=None, causal=True, out=None, lse=None, stream=None):
+        """Attention over packed prompts: q [Tq, heads, head_dim], k and v [Tkv, kv_heads, head_dim]; sequence i has
+        queries q_offsets[i] .. q_offsets[i+1]-1 and keys kv_offsets[i] .. kv_offsets[i+1]-1 (the same where
+        kv_offsets is None). causal: the queries are the last positions of their sequence. Returns out like q;
+        lse [Tq, heads] (float32, optional) receives the logarithms of the softmax sums."""
+        device = q.device
+        _on_cuda(device, "q, k and v")
+        Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, device)
+        Tk, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, device)
+        Tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, device)
+        if Tv != Tk or (kv_offsets is None and Tk != Tq):
+            raise ValueError(f"moe: k has {Tk} tokens, v has {Tv}, q has {Tq}")
+        n = _ints(q_offsets, "q_offsets", None, device) - 1
+        if n < 0:
+            raise ValueError("moe: q_offsets has one entry more than there are sequences")
+        if kv_offsets is not None:
+            _ints(kv_offsets, "kv_offsets", n + 1, device)
+        out, so = self._out(q, out, lse, stream)
+        s = _stream(stream)
+        ws = self._workspace(s, 0, device)
+        _check(self._lib.moe_attention_prompt(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
+            None if kv_offsets is None else kv_offsets.data_ptr(), n, Tq, Tk, self.heads, self.kv_heads, self.head_dim,
+            qs, ks, vs, so, self.scale, _lib.ATTN_CAUSAL if causal else 0, self.dt, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws[2], ws[1], s), "moe_attention_prompt")
+        return out
+
+    def decode(self, q, cache, slots, layer=0, shared_len=0, out=None, lse=None, stream=None):
+        """One token for each sequence: q [n, heads, head_dim] attends the positions of slot slots[i] of the cache.
+        shared_len: how many first positions of all n slots are the same pages (a multiple of the page size),
+        read once for the whole batch."""
+        device = q.device
+        _on_cuda(device, "q")
+        if cache.device != device or cache.kv_heads != self.kv_heads or cache.head_dim != self.head_dim:
+            raise ValueError(f"moe: the cache holds {cache.kv_heads} heads of {cache.head_dim} on {cache.device}")
+        if cache.dtype != self.dtype:
+            raise ValueError(f"moe: the cache is in {cache.dtype}, the attention in {self.dtype}")
+        n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, device)
+        _ints(slots, "slots", n, device)
+        out, so = self._out(q, out, lse, stream)
+        s = _stream(stream)
+        ws = self._workspace(s, n, device)
+        _check(self._lib.moe_attention_decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so,
+                                              shared_len, self.scale, out.data_ptr(),
+                                              None if lse is None else lse.data_ptr(), ws[2], ws[1], s),
+               "moe_attention_decode")
+        return out
+
+    def device_status(self):
+        """(status, detail) of the first device-side error since the last call; synchronises."""
+        return self._ws.status()

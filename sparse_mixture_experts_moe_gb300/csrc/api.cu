@@ -78,6 +78,8 @@ bool sizes_ok(int T, int d, int F, int E, int k, int dt) {
   return true;
 }
 
+}  // namespace
+
 uint64_t wait_timeout_ns() {
   const char* s = std::getenv("MOE_WAIT_TIMEOUT_MS");
   long long ms = s != nullptr ? std::atoll(s) : 2000;
@@ -85,7 +87,11 @@ uint64_t wait_timeout_ns() {
   return (uint64_t)ms * 1000000ull;
 }
 
+namespace {
+
 inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+}  // namespace
 
 // The TMA-fed kernels' tensor maps are built by the driver's cuTensorMapEncodeTiled, which needs a
 // context current on the calling host thread. The runtime makes the device's primary context current
@@ -109,6 +115,8 @@ void bind_primary_context() {
   int dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess) (void)cudaSetDevice(dev);
 }
+
+namespace {
 
 template <typename P>
 inline P* at(void* ws, size_t off) { return reinterpret_cast<P*>(static_cast<uint8_t*>(ws) + off); }

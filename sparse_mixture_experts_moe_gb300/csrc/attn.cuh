@@ -1,0 +1,124 @@
+// Shared declarations of the attention and cache kernels (internal to the library).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// Packed rows: the G = H / H_kv query heads that share a key/value head are laid side by side, row
+// r = token * G + g, so that one key/value tile serves all of them and short prompts or single tokens
+// still fill a tile's rows.
+struct PromptArgs {
+  const void *q, *k, *v;
+  const int32_t *qo, *ko;  // [n + 1] each
+  int n, Tq, Tkv, H, Hkv, D;
+  long long qs, ks, vs, os;  // token strides in elements
+  float scale;
+  int causal, dt;
+  void* out;
+  float* lse;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+struct CacheView {
+  void *k, *v;
+  int32_t *table, *lens, *refs;
+  int n_layers, n_pages, page_size, page_shift, n_slots, width, Hkv, D, dt;
+  long long layer_elems() const { return (long long)n_pages * Hkv * page_size * D; }
+};
+
+struct DecodeArgs {
+  const void* q;
+  long long qs, os;
+  const int32_t* slots;
+  int n, H, shared;
+  float scale;
+  CacheView c;
+  const void *k, *v;  // the layer's pages
+  void* out;
+  float* lse;
+  float* part;  // partial results, see PartView
+  int* status;
+  uint64_t timeout_ns;
+};
+
+// Workspace of one decode call. A piece is the attention of one row over a part of its keys: the sum of
+// the weighted values (D floats), the weights' sum l and the reference m (in log2 units) that the
+// weights 2^(s - m) were taken against. A row's pieces join as out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// Pieces that a call may have: 4 a row, and enough for every SM to hold several pieces of many rows.
+constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
+
+cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);
+cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
+
+struct CacheWs {
+  int* status;       // workspace header
+  int32_t* claim_d;  // [n_slots] zero between calls: which entry names the slot (as dst)
+  int32_t* claim_s;  // [n_slots] zero between calls: the slot is a source
+  int4* entry;       // [n_slots]
+  int32_t* freel;    // [n_pages] pages found free, ascending
+  int2* copies;      // [max(n_slots, n_pages)] (src, dst) pages
+  int32_t* map;      // [n_pages] where a moved page went
+  int32_t* counts;   // [0] number of copies, [1] pages in use
+};
+cudaError_t launch_cache_resize(const CacheView& c, const CacheWs& w, const int32_t* slots, const int32_t* new_lens, int n,
+                                cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheView& c, const CacheWs& w, const int32_t* src, const int32_t* dst, int n,
+                              cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheView& c, const CacheWs& w, int32_t* n_live, cudaStream_t s);
+cudaError_t launch_cache_copy(const CacheView& c, const CacheWs& w, const int32_t* src, const int32_t* dst, int n,
+                              cudaStream_t s);
+cudaError_t launch_cache_write(const CacheView& c, const CacheWs& w, int layer, const int32_t* slots,
+                               const int32_t* offsets, const int32_t* pos, int n, int total, const void* k, const void* v,
+                               long long ks, long long vs, cudaStream_t s);
+
+// ------------------------------------------------------------------ device helpers
+// A tile slot of packed prompts: with R rows a tile, sequence i (L_i tokens) owns the slots
+// floor(q_offsets[i] G / R) + i up to the next sequence's first, which are never fewer than its
+// ceil(L_i G / R) tiles. So tile slots are found from the offsets alone, with no scan over the
+// sequences' tile counts: the largest i whose first slot is <= s, by bisection.
+__device__ __forceinline__ int find_tile_seq(const int32_t* qo, int n, int G, int R, long long s) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)qo[mid] * G / R + mid <= s) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+inline long long prompt_tile_slots(int Tq, int n, int G, int R) { return (long long)Tq * G / R + n; }
+
+// Sequence i of a prompt call, its offsets checked (a bad one is recorded and has no rows).
+struct Seq {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Seq load_seq(const PromptArgs& a, int i) {
+  Seq s;
+  s.q0 = a.qo[i];
+  s.k0 = a.ko[i];
+  const int q1 = a.qo[i + 1], k1 = a.ko[i + 1];
+  s.nq = q1 - s.q0;
+  s.nk = k1 - s.k0;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || s.k0 < 0 || k1 < s.k0 || k1 > a.Tkv) {
+    record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
+    s.nq = 0;
+    s.nk = 0;
+  }
+  return s;
+}
+// Keys that query token t sees.
+__device__ __forceinline__ int visible_keys(int t, int nq, int nk, int causal) {
+  if (!causal) return nk;
+  const int lim = t + 1 + nk - nq;
+  return lim < 0 ? 0 : (lim > nk ? nk : lim);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // the hardware 2^x, ~2 ulp; 2^-inf = 0
+  return y;
+}
+
+}  // namespace moe

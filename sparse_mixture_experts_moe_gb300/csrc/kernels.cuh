@@ -143,6 +143,10 @@ bool encode_tmap_plain(EncodeTiledFn enc, CUtensorMap* m, CUtensorMapDataType ty
                        const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box);
 
 int device_sm_count();
+// The bound of a device-side wait (MOE_WAIT_TIMEOUT_MS, 2 s by default).
+uint64_t wait_timeout_ns();
+// Makes the device's primary context current on the calling thread (needed before a tensor map is encoded).
+void bind_primary_context();
 // The current device's L2 size in bytes. A streaming GEMM whose touched weights (at most rows experts)
 // come to less than three L2s copies them at L2 evict-first priority, so that what the step reads
 // again (the router's weights, the activations) stays in L2: one-token steps ran 2-3% faster. With
