@@ -52,6 +52,8 @@ struct DecodeArgs {
 constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
 
 cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);
+// bf16, D <= 128, at least one key.
+cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s);
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
 
 struct CacheWs {

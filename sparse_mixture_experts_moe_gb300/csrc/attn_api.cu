@@ -124,6 +124,11 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
   a.out = out; a.lse = lse;
   a.status = static_cast<int*>(workspace);
   a.timeout_ns = wait_timeout_ns();
+  // The tensor cores take bf16 heads of up to 128 elements (a tile of longer ones does not fit in TMEM).
+  if (dt == MOE_DTYPE_BF16 && D <= 128 && Tkv > 0) {
+    bind_primary_context();
+    return cuda_status(launch_attn_prompt_tc(a, (cudaStream_t)stream));
+  }
   return cuda_status(launch_attn_prompt_simt(a, (cudaStream_t)stream));
 }
 
