@@ -476,13 +476,14 @@ moe_status moe_cache_write(const moe_kv_cache* cache, int layer, const int32_t* 
 /* moe_attention_decode — one query token for each of n sequences over the cache: row i attends the
  *   lens[slots[i]] positions of slot slots[i] (its own new token included, once written).
  *   shared_len (a multiple of page_size, 0: none) says that the first shared_len positions of all n
- *   slots are the same pages (as moe_cache_fork leaves them): their keys are read once for the whole
- *   batch, the rest once per sequence, and the parts are joined.
+ *   slots (of a shorter slot: as many as it has) are the same pages, as moe_cache_fork leaves them: their
+ *   keys are read once for the whole batch, the rest once per sequence, and the parts are joined. The
+ *   first slot holds at least shared_len positions.
  * In:  q [n, H, D] (token stride q_stride), slots [n].  Out: out [n, H, D] (out_stride), lse [n, H] or NULL.
  * Workspace: moe_attention_workspace_bytes(n, H, D) bytes, prepared with moe_workspace_init.
- * Device checks: a slot or page out of range, or a slot shorter than shared_len or with other pages there,
- *   records MOE_ERR_DEVICE_CHECK (detail = row); an out-of-range slot's row is 0, the others' rows then
- *   follow the first slot's pages. */
+ * Device checks: a slot or page out of range, or a slot with other pages in the shared part, records
+ *   MOE_ERR_DEVICE_CHECK (detail = row). An out-of-range slot's row is 0; a row with other pages there may
+ *   attend either. */
 size_t moe_attention_workspace_bytes(int n, int H, int D);
 moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
                                 int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,

@@ -54,6 +54,10 @@ constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
 cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);
 // bf16, D <= 128, at least one key.
 cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s);
+cudaError_t launch_attn_decode_tc(const DecodeArgs& a, cudaStream_t s);
+// The shared keys of a decode batch: `splits` pieces of every row, part_o [(sequence, head)][splits][D] unnormalised.
+int attn_shared_splits(const DecodeArgs& a);
+cudaError_t launch_attn_shared_tc(const DecodeArgs& a, int splits, float* part_o, float2* part_ml, cudaStream_t s);
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
 
 struct CacheWs {

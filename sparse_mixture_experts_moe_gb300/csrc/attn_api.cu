@@ -164,6 +164,10 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(kWsHeaderBytes));
   a.status = static_cast<int*>(workspace);
   a.timeout_ns = wait_timeout_ns();
+  if (cache->dt == MOE_DTYPE_BF16 && cache->D <= 128) {
+    bind_primary_context();
+    return cuda_status(launch_attn_decode_tc(a, (cudaStream_t)stream));
+  }
   return cuda_status(launch_attn_decode_simt(a, (cudaStream_t)stream));
 }
 

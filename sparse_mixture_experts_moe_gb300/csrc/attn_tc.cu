@@ -73,9 +73,10 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // One row again, key by key (a warp; lane owns 4 consecutive elements): only keys below lim take part.
-__device__ __forceinline__ void exact_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                       long long ks, long long vs, int D, int lim, float c2, float (&o)[4], float& m,
-                                       float& l) {
+// at(j, k, v) gives key j's element offsets.
+template <typename At>
+__device__ __forceinline__ void exact_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v, At at,
+                                          int D, int lim, float c2, float (&o)[4], float& m, float& l) {
   const int d = (int)(threadIdx.x & 31) * 4;
   const bool on = d < D;
   float qv[4] = {0.f, 0.f, 0.f, 0.f};
@@ -88,9 +89,11 @@ __device__ __forceinline__ void exact_row(const __nv_bfloat16* q, const __nv_bfl
   for (int e = 0; e < 4; ++e) o[e] = 0.f;
   for (int j = 0; j < lim; ++j) {
     float s = 0.f;
+    long long ko, vo;
+    at(j, ko, vo);
     if (on)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(qv[e], __bfloat162float(k[j * ks + d + e]), s);
+      for (int e = 0; e < 4; ++e) s = fmaf(qv[e], __bfloat162float(k[ko + d + e]), s);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
     s *= c2;
@@ -99,7 +102,7 @@ __device__ __forceinline__ void exact_row(const __nv_bfloat16* q, const __nv_bfl
     m = mn;
     if (on)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = fmaf(p, __bfloat162float(v[j * vs + d + e]), o[e] * a);
+      for (int e = 0; e < 4; ++e) o[e] = fmaf(p, __bfloat162float(v[vo + d + e]), o[e] * a);
   }
 }
 
@@ -334,7 +337,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
     const int R = row0 + t * TM + r;
     const bool valid = r < nrow_t;
-    const int lim = !valid ? 0 : (SHARED ? n_keys : visible_keys(R / G, sq.nq, sq.nk, pa.causal));
+    int lim = 0;
+    if (valid && SHARED) {  // a slot shorter than the shared keys sees its own length of them
+      const int slot = sa.d.slots[R / G];
+      lim = slot < 0 || slot >= sa.d.c.n_slots ? 0 : max(0, min(n_keys, sa.d.c.lens[slot] - key0));
+    } else if (valid) {
+      lim = visible_keys(R / G, sq.nq, sq.nk, pa.causal);
+    }
     const float c2 = (SHARED ? sa.d.scale : pa.scale) * 1.4426950408889634f;
     const float thr = kRescale / c2;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
@@ -415,12 +424,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       const int tok = R / G, h = hk * G + R % G;
       if (SHARED) {
         const long long piece = ((long long)tok * H + h) * sa.splits + blockIdx.z;
+        bool fine = true;
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
           uint32_t o[32];
           if (n > 0) {
             tmem_ld_32x32b_x32(tO + 32 * c, o);
             tmem_ld_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (lim == 0) o[i] = 0;
+            fine = fine && fabsf(__uint_as_float(o[i])) <= 3.0e38f;
           }
           if (valid) {
             float4* dst = reinterpret_cast<float4*>(sa.part_o + piece * D + 32 * c);
@@ -432,6 +447,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           }
         }
         if (valid) sa.part_ml[piece] = make_float2(m * c2, l);
+        uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && lim < n_keys);
+        while (again != 0) {
+          const int w = __ffs(again) - 1;
+          again &= again - 1;
+          const int Rw = __shfl_sync(0xffffffffu, R, w), limw = __shfl_sync(0xffffffffu, lim, w);
+          const int tw = Rw / G, hw = hk * G + Rw % G;
+          const CacheView& cv = sa.d.c;
+          const int32_t* row = cv.table + (long long)sa.d.slots[tw] * cv.width;
+          float o[4], mw, lw;
+          exact_row((const __nv_bfloat16*)sa.d.q + (long long)tw * sa.d.qs + (long long)hw * D,
+                    (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v,
+                    [&](int j, long long& ko, long long& vo) {
+                      const int p = key0 + j;
+                      int page = row[p >> cv.page_shift];
+                      page = page < 0 || page >= cv.n_pages ? 0 : page;
+                      ko = vo = (((long long)page * Hkv + hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
+                    },
+                    D, limw, c2, o, mw, lw);
+          const long long pw = ((long long)tw * H + hw) * sa.splits + blockIdx.z;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (lane * 4 + e < D) sa.part_o[pw * D + lane * 4 + e] = o[e];
+          if (lane == 0) sa.part_ml[pw] = make_float2(mw, lw);
+        }
       } else {
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         __nv_bfloat16* dst = (__nv_bfloat16*)pa.out + (long long)(sq.q0 + tok) * pa.os + (long long)h * D;
@@ -474,8 +513,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           float o[4], mw, lw;
           exact_row((const __nv_bfloat16*)pa.q + (long long)(sq.q0 + tw) * pa.qs + (long long)hw * D,
                     (const __nv_bfloat16*)pa.k + (long long)sq.k0 * pa.ks + (long long)hk * D,
-                    (const __nv_bfloat16*)pa.v + (long long)sq.k0 * pa.vs + (long long)hk * D, pa.ks, pa.vs, D, limw, c2, o,
-                    mw, lw);
+                    (const __nv_bfloat16*)pa.v + (long long)sq.k0 * pa.vs + (long long)hk * D,
+                    [&](int j, long long& ko, long long& vo) {
+                      ko = (long long)j * pa.ks;
+                      vo = (long long)j * pa.vs;
+                    },
+                    D, limw, c2, o, mw, lw);
           const float iw = lw == 0.f ? 0.f : 1.0f / lw;
           __nv_bfloat16* dw = (__nv_bfloat16*)pa.out + (long long)(sq.q0 + tw) * pa.os + (long long)hw * D;
 #pragma unroll
@@ -524,6 +567,39 @@ cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)(slots * a.Hkv));
   return a.D <= 64 ? launch<64, false>(tk, tv, a, none, grid, (int)slots, s)
                    : launch<128, false>(tk, tv, a, none, grid, (int)slots, s);
+}
+
+// One CTA an SM takes 256 rows of one key/value head; as many splits of the keys as there are SMs left over.
+int attn_shared_splits(const DecodeArgs& a) {
+  const long long units = (long long)a.c.Hkv * ((a.n * (long long)(a.H / a.c.Hkv) + 2 * TM - 1) / (2 * TM));
+  const int blocks = (a.shared + BK - 1) / BK;
+  long long splits = device_sm_count() / units;
+  splits = splits < 1 ? 1 : (splits > blocks ? blocks : splits);
+  const int per = (blocks + (int)splits - 1) / (int)splits;
+  return (blocks + per - 1) / per;  // no empty split
+}
+
+cudaError_t launch_attn_shared_tc(const DecodeArgs& a, int splits, float* part_o, float2* part_ml, cudaStream_t s) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  CUtensorMap tk{}, tv{};
+  const cuuint64_t dims[2] = {(cuuint64_t)a.c.D, (cuuint64_t)a.c.n_pages * a.c.Hkv * a.c.page_size};
+  const cuuint64_t str[1] = {(cuuint64_t)a.c.D * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(a.c.page_size < BK ? a.c.page_size : BK)};
+  if (!encode_tmap(enc, &tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, 2, dims, str, box) ||
+      !encode_tmap(enc, &tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 2, dims, str, box))
+    return cudaErrorInvalidValue;
+  SharedArgs sa;
+  sa.d = a;
+  sa.splits = splits;
+  const int blocks = (a.shared + BK - 1) / BK;
+  sa.per = (blocks + splits - 1) / splits * BK;
+  sa.part_o = part_o;
+  sa.part_ml = part_ml;
+  const PromptArgs none{};
+  const long long pairs = (a.n * (long long)(a.H / a.c.Hkv) + 2 * TM - 1) / (2 * TM);
+  const dim3 grid((unsigned)a.c.Hkv, (unsigned)pairs, (unsigned)splits);
+  return a.c.D <= 64 ? launch<64, true>(tk, tv, none, sa, grid, 0, s) : launch<128, true>(tk, tv, none, sa, grid, 0, s);
 }
 
 }  // namespace moe
