@@ -17,6 +17,7 @@ done by the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _lib
 from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
@@ -30,31 +31,48 @@ class _Cache(ctypes.Structure):
                 ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("dt", ctypes.c_int)]
 
 
-def _heads(t, name, heads, dim, dtype, device):
-    """Checks a [T, heads, dim] tensor whose heads are dense within a token; returns (T, token stride)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.dtype != dtype or t.device != device:
-        raise ValueError(f"moe: expected {name} [T, {heads}, {dim}] in {dtype} on {device}, got {tuple(t.shape)} in "
+# The checks below run on every call, where a decode step's kernels take a few microseconds: each looks at a
+# tensor's attributes once and formats a message only when it refuses.
+def _heads(t, name, heads, dim, dtype, dev):
+    """Checks a [T, heads, dim] tensor on CUDA device `dev` whose heads are dense within a token; returns (T, token
+    stride)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"moe: expected {name} [T, {heads}, {dim}] in {dtype} on cuda:{dev}, got {tuple(shape)} in "
                          f"{t.dtype} on {t.device}")
-    T, (st, sh, sd) = t.shape[0], t.stride()
-    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"moe: {name} must have dense heads within a token (strides {t.stride()})")
     # a single token's stride means nothing: any valid one will do
-    return T, (heads * dim if T < 2 else st)
+    T = shape[0]
+    return T, (st if T > 1 else heads * dim)
 
 
-def _ints(t, name, n, device):
-    """Checks an int32 index tensor of n entries (None: any number); returns its length."""
+def _ints(t, name, n, dev):
+    """Checks an int32 index tensor of n entries (None: any number) on CUDA device `dev`; returns its length."""
+    shape = t.shape
+    if len(shape) != 1 or t.dtype is not _int32() or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"moe: {name} must be a contiguous one-dimensional int32 tensor on cuda:{dev}")
+    if n is not None and shape[0] != n:
+        raise ValueError(f"moe: {name} has {shape[0]} entries; the call needs {n}")
+    return shape[0]
+
+
+def _stream_of(stream, dev):
+    """The stream's handle; None: the device's current one (its handle alone, without a stream object around it)."""
+    return _raw_stream()(dev) if stream is None else _stream(stream)
+
+
+@functools.lru_cache(None)
+def _int32():
     import torch
-    if t.dim() != 1 or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"moe: {name} must be a contiguous one-dimensional int32 tensor on {device}")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"moe: {name} has {t.shape[0]} entries; the call needs {n}")
-    return t.shape[0]
+    return torch.int32
 
 
-def _on_cuda(device, what):
-    if device.type != "cuda":
-        raise ValueError(f"moe: {what} must be CUDA tensors (got {device})")
+@functools.lru_cache(None)
+def _raw_stream():
+    import torch
+    return torch._C._cuda_getCurrentRawStream
 
 
 class _Workspaces:
@@ -66,18 +84,18 @@ class _Workspaces:
         self._of = {}
         self._old = []
 
-    def get(self, stream, nbytes, device):
+    def get(self, stream, nbytes, dev):
         ws = self._of.get(stream)
         if ws is None or ws[1] < nbytes:
             import torch
             if ws is not None:
                 self._old.append(ws)
-            t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            t = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
             ws = (t, nbytes, t.data_ptr())
             if torch.cuda.is_current_stream_capturing():
                 self._old.append(ws)  # zeroed by the graph being recorded, so for that recording only
             else:
-                torch.cuda.current_stream(device).synchronize()  # zeroed before any stream uses it
+                torch.cuda.current_stream(dev).synchronize()  # zeroed before any stream uses it
                 self._of[stream] = ws
         return ws
 
@@ -119,6 +137,7 @@ class KVCache:
         if self._bytes == 0:
             raise MoeError(MOE_ERR_INVALID_ARG, "moe_cache_workspace_bytes")
         self._ws = _Workspaces()
+        self._dev = k.get_device()
 
     @classmethod
     def create(cls, n_layers, n_pages, page_size, n_slots, max_len, kv_heads, head_dim, dtype, device="cuda"):
@@ -131,17 +150,17 @@ class KVCache:
                    torch.zeros(n_pages, **i32))
 
     def _workspace(self, stream):
-        return self._ws.get(stream, self._bytes, self.device)
+        return self._ws.get(stream, self._bytes, self._dev)
 
     def clear(self, stream=None):
         """Empties every slot and frees every page."""
-        _check(self._lib.moe_cache_clear(self._ref, _stream(stream)), "moe_cache_clear")
+        _check(self._lib.moe_cache_clear(self._ref, _stream_of(stream, self._dev)), "moe_cache_clear")
 
     def resize(self, slots, new_lens, stream=None):
         """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
-        n = _ints(slots, "slots", None, self.device)
-        _ints(new_lens, "new_lens", n, self.device)
-        s = _stream(stream)
+        n = _ints(slots, "slots", None, self._dev)
+        _ints(new_lens, "new_lens", n, self._dev)
+        s = _stream_of(stream, self._dev)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_resize")
@@ -149,23 +168,23 @@ class KVCache:
     def write(self, k, v, slots, offsets, pos, layer=0, stream=None):
         """Tokens offsets[i] .. offsets[i+1]-1 of k, v [total, kv_heads, head_dim] become positions pos[i], pos[i]+1,
         ... of slot slots[i] in one layer."""
-        total, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, self.device)
-        tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, self.device)
+        total, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, self._dev)
+        tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, self._dev)
         if tv != total:
             raise ValueError(f"moe: k has {total} tokens, v has {tv}")
-        n = _ints(slots, "slots", None, self.device)
-        _ints(offsets, "offsets", n + 1, self.device)
-        _ints(pos, "pos", n, self.device)
-        s = _stream(stream)
+        n = _ints(slots, "slots", None, self._dev)
+        _ints(offsets, "offsets", n + 1, self._dev)
+        _ints(pos, "pos", n, self._dev)
+        s = _stream_of(stream, self._dev)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
                                          k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
-        n = _ints(src, "src", None, self.device)
-        _ints(dst, "dst", n, self.device)
-        s = _stream(stream)
+        n = _ints(src, "src", None, self._dev)
+        _ints(dst, "dst", n, self._dev)
+        s = _stream_of(stream, self._dev)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
 
@@ -176,18 +195,18 @@ class KVCache:
         if n_live is None:
             if stream is not None:
                 raise ValueError("moe: pass n_live with an explicit stream")
-            n_live = torch.empty(1, dtype=torch.int32, device=self.device)
-        _ints(n_live, "n_live", 1, self.device)
-        s = _stream(stream)
+            n_live = torch.empty(1, dtype=torch.int32, device=self._dev)
+        _ints(n_live, "n_live", 1, self._dev)
+        s = _stream_of(stream, self._dev)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
         return n_live
 
     def copy_pages(self, src, dst, stream=None):
         """Page dst[i] gets page src[i]'s contents in every layer."""
-        n = _ints(src, "src", None, self.device)
-        _ints(dst, "dst", n, self.device)
-        s = _stream(stream)
+        n = _ints(src, "src", None, self._dev)
+        _ints(dst, "dst", n, self._dev)
+        s = _stream_of(stream, self._dev)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_copy_pages")
@@ -211,32 +230,35 @@ class Attention:
             raise ValueError("Attention: heads must be a multiple of kv_heads, head_dim a multiple of 8 from 8 to 256")
         self.scale = float(scale) if scale is not None else self.head_dim ** -0.5
         self._lib = _lib.lib()
+        self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
         self._ws = _Workspaces()
         self._need = {}
 
-    def _workspace(self, stream, n, device):
+    def _workspace(self, stream, n, dev):
         need = self._need.get(n)
         if need is None:
             need = int(self._lib.moe_attention_workspace_bytes(n, self.heads, self.head_dim))
             if need == 0:
                 raise MoeError(MOE_ERR_INVALID_ARG, "moe_attention_workspace_bytes")
             self._need[n] = need
-        return self._ws.get(stream, need, device)
+        return self._ws.get(stream, need, dev)
 
-    def _out(self, q, out, lse, stream):
-        import torch
+    def _out(self, q, out, lse, stream, dev):
         if out is None:
+            import torch
             if stream is not None:  # a tensor made here belongs to the current stream
                 raise ValueError("moe: pass out with an explicit stream")
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             so = self.heads * self.head_dim
         else:
-            to, so = _heads(out, "out", self.heads, self.head_dim, self.dtype, q.device)
+            to, so = _heads(out, "out", self.heads, self.head_dim, self.dtype, dev)
             if to != q.shape[0]:
                 raise ValueError(f"moe: expected out {tuple(q.shape)}, got {tuple(out.shape)}")
-        if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or lse.dtype != torch.float32
-                                or lse.device != q.device or not lse.is_contiguous()):
-            raise ValueError(f"moe: expected lse {tuple(q.shape[:2])}, float32, contiguous, on {q.device}")
+        if lse is not None:
+            import torch
+            if (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.get_device() != dev
+                    or not lse.is_contiguous()):
+                raise ValueError(f"moe: expected lse {tuple(q.shape[:2])}, float32, contiguous, on {q.device}")
         return out, so
 
     def prompt(self, q, k, v, q_offsets, kv_offsets=None, causal=True, out=None, lse=None, stream=None):
@@ -244,22 +266,23 @@ class Attention:
         queries q_offsets[i] .. q_offsets[i+1]-1 and keys kv_offsets[i] .. kv_offsets[i+1]-1 (the same where
         kv_offsets is None). causal: the queries are the last positions of their sequence. Returns out like q;
         lse [Tq, heads] (float32, optional) receives the logarithms of the softmax sums."""
-        device = q.device
-        _on_cuda(device, "q, k and v")
-        Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, device)
-        Tk, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, device)
-        Tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, device)
+        dev = q.get_device()
+        if dev < 0:
+            raise ValueError(f"moe: q, k and v must be CUDA tensors (got one on {q.device})")
+        Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
+        Tk, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, dev)
+        Tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, dev)
         if Tv != Tk or (kv_offsets is None and Tk != Tq):
             raise ValueError(f"moe: k has {Tk} tokens, v has {Tv}, q has {Tq}")
-        n = _ints(q_offsets, "q_offsets", None, device) - 1
+        n = _ints(q_offsets, "q_offsets", None, dev) - 1
         if n < 0:
             raise ValueError("moe: q_offsets has one entry more than there are sequences")
         if kv_offsets is not None:
-            _ints(kv_offsets, "kv_offsets", n + 1, device)
-        out, so = self._out(q, out, lse, stream)
-        s = _stream(stream)
-        ws = self._workspace(s, 0, device)
-        _check(self._lib.moe_attention_prompt(
+            _ints(kv_offsets, "kv_offsets", n + 1, dev)
+        out, so = self._out(q, out, lse, stream, dev)
+        s = _stream_of(stream, dev)
+        ws = self._workspace(s, 0, dev)
+        _check(self._prompt(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
             None if kv_offsets is None else kv_offsets.data_ptr(), n, Tq, Tk, self.heads, self.kv_heads, self.head_dim,
             qs, ks, vs, so, self.scale, _lib.ATTN_CAUSAL if causal else 0, self.dt, out.data_ptr(),
@@ -270,20 +293,17 @@ class Attention:
         """One token for each sequence: q [n, heads, head_dim] attends the positions of slot slots[i] of the cache.
         shared_len: how many first positions of all n slots are the same pages (a multiple of the page size),
         read once for the whole batch."""
-        device = q.device
-        _on_cuda(device, "q")
-        if cache.device != device or cache.kv_heads != self.kv_heads or cache.head_dim != self.head_dim:
-            raise ValueError(f"moe: the cache holds {cache.kv_heads} heads of {cache.head_dim} on {cache.device}")
-        if cache.dtype != self.dtype:
-            raise ValueError(f"moe: the cache is in {cache.dtype}, the attention in {self.dtype}")
-        n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, device)
-        _ints(slots, "slots", n, device)
-        out, so = self._out(q, out, lse, stream)
-        s = _stream(stream)
-        ws = self._workspace(s, n, device)
-        _check(self._lib.moe_attention_decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so,
-                                              shared_len, self.scale, out.data_ptr(),
-                                              None if lse is None else lse.data_ptr(), ws[2], ws[1], s),
+        dev = cache._dev
+        if cache.kv_heads != self.kv_heads or cache.head_dim != self.head_dim or cache.dtype is not self.dtype:
+            raise ValueError(f"moe: the cache holds {cache.kv_heads} heads of {cache.head_dim} in {cache.dtype}, the "
+                             f"attention {self.kv_heads} of {self.head_dim} in {self.dtype}")
+        n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
+        _ints(slots, "slots", n, dev)
+        out, so = self._out(q, out, lse, stream, dev)
+        s = _stream_of(stream, dev)
+        ws = self._workspace(s, n, dev)
+        _check(self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
+                            out.data_ptr(), None if lse is None else lse.data_ptr(), ws[2], ws[1], s),
                "moe_attention_decode")
         return out
 
