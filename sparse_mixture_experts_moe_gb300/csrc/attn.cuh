@@ -121,6 +121,40 @@ __device__ __forceinline__ int visible_keys(int t, int nq, int nk, int causal) {
   return lim < 0 ? 0 : (lim > nk ? nk : lim);
 }
 
+// try_wait that may sleep for up to 20 us. Without the hint it comes back after some tens of cycles, and warps that
+// spin on it fill the queue that the MMA warp's own instructions pass through.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// wait_or_abort for a whole converged warp: every branch is on a vote, so the warp never diverges, and what
+// follows a wait of more than 20 us is laid out away from the loop that waits (an instruction cache miss costs
+// the MMA warp more than the wait itself).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag,
+                                          int* status, int role) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity)), 1)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_long(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > timeout_ns)) {
+      if ((threadIdx.x & 31) == 0) {
+        record_error(status, MOE_ERR_DEVICE_TIMEOUT, role);
+        *abort_flag = 1;
+      }
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // the hardware 2^x, ~2 ulp; 2^-inf = 0

@@ -247,7 +247,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar0 + 8 * stage, phase, a.d.timeout_ns, abort_flag, a.d.status, 61));
+    if (ok) ok = warp_wait(bar0 + 8 * stage, phase, a.d.timeout_ns, abort_flag, a.d.status, 61);
     const int key = a.d.shared + cu.b * kBlock + warp * kKeys, left = len - key;
     if (ok && left > 0) {
       const uint32_t sk = ring + stage * 2 * kHalf<DP>, sv = sk + kHalf<DP>;

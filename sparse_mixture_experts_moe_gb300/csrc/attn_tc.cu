@@ -37,6 +37,7 @@ constexpr int TM = 128;       // rows per tile
 // Registers: 12 warps of 168 at launch (64512); the softmax warps take 216 each (a row of 128 scores stays in
 // registers), the other four keep 72: 8 * 32 * 216 + 4 * 32 * 72 = 64512.
 constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;
 constexpr int kMaxSmem = 232448;
 constexpr float kRescale = 8.0f;  // log2 units
 
@@ -70,7 +71,22 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
 
 // One row again, key by key (a warp; lane owns 4 consecutive elements): only keys below lim take part.
 // at(j, k, v) gives key j's element offsets.
@@ -134,7 +150,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 2,
                 ODONE = PFULL + 2, DONE = ODONE + 2;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the shuffle tells the compiler that the warp number is the same in all lanes)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   griddep_wait();
 
   // ---- the CTA's rows and keys
@@ -184,7 +201,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -195,9 +212,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 8) {
+  if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // all four warps of the group, 10 and 11 idle
-    if (warp == 9 && lane == 0) {
+    if (warp == kSoftWarps + 1 && lane == 0) {
       // -------------------------------------------------------------- loads
       int stage = 0;
       uint32_t phase = 0, filled = 0, fill_phase = 0;
@@ -239,72 +256,96 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       for (int s = 0; s < C::kStages; ++s)
         if (filled & (1u << s)) mbar_wait_bounded(bar(FULL + s), (fill_phase >> s) & 1u, timeout_ns);
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kSoftWarps) {
       // -------------------------------------------------------------- MMAs
+      // The whole warp walks the loop and one elected thread issues: descriptors and addresses then stay in uniform
+      // registers. Inside a one-lane branch every MMA first moved its operands there, which took as long as
+      // the MMA itself (about 70 of 64 cycles).
+      const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int n0 = __shfl_sync(0xffffffffu, nb0, 0), n1 = __shfl_sync(0xffffffffu, nb1, 0), nn = max(n0, n1);
       constexpr uint32_t idesc_qk = make_idesc_bf16_f32(TM, BK, false);
       constexpr uint32_t idesc_pv = make_idesc_bf16_f32(TM, DP, true);
       int stage = 0;
       uint32_t phase = 0;
       auto wait = [&](int b, uint32_t ph) {
-        const bool ok = wait_or_abort(bar(b), ph, timeout_ns, abort_flag, status, 52);
+        const bool ok = warp_wait(bar(b), ph, timeout_ns, abort_flag, status, 52);
         tc_fence_after();
         return ok;
+      };
+      // three barriers at once: the tests go out together, as each takes about 100 cycles to answer (and waits in the
+      // warp's queue behind the MMAs issued before it)
+      auto wait3 = [&](int b0, uint32_t p0, int b1, uint32_t p1, int b2, uint32_t p2) {
+        const bool r0 = mbar_try_wait_long(bar(b0), p0), r1 = mbar_try_wait_long(bar(b1), p1),
+                   r2 = mbar_try_wait_long(bar(b2), p2);
+        if (!__builtin_expect(__all_sync(0xffffffffu, r0 && r1 && r2), 1)) {
+          if (!warp_wait(bar(b0), p0, timeout_ns, abort_flag, status, 52)) return false;
+          if (!warp_wait(bar(b1), p1, timeout_ns, abort_flag, status, 52)) return false;
+          if (!warp_wait(bar(b2), p2, timeout_ns, abort_flag, status, 52)) return false;
+        }
+        tc_fence_after();
+        return true;
       };
       auto qk = [&](int t, int st) {
         const uint64_t a = make_smem_desc_sw128(sQ + t * C::kTileBytes, 16, 1024);
         const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes, 16, 1024);
+        if (!leader) return;
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk / 4) * (TM * 128) + (kk % 4) * 32) >> 4);
-          tc_mma_f16(tmem + t * BK, a + off, b + off, idesc_qk, kk != 0);
+          tc_mma_f16(tm + t * BK, a + off, b + off, idesc_qk, kk != 0);
         }
         tc_commit(bar(SFULL + t));
       };
       auto pv = [&](int t, int st, bool acc) {
         const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes, BK * 128, 1024);
+        if (!leader) return;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          tc_mma_f16_ta(tmem + 256 + t * DP, tmem + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+          tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
                         acc || kk != 0);
         tc_commit(bar(ODONE + t));
       };
       auto next = [&]() { if (++stage == C::kStages) { stage = 0; phase ^= 1u; } };
-      if (nb > 0) {
+      if (nn > 0) {
         bool ok = wait(FULL + stage, phase);
+#pragma unroll 1
         for (int t = 0; t < 2 && ok; ++t)
-          if ((t ? nb1 : nb0) > 0) {
+          if ((t ? n1 : n0) > 0) {
             ok = wait(QFULL + t, 0);
             if (ok) qk(t, stage);
           }
-        tc_commit(bar(EMPTY + stage));
+        if (leader) tc_commit(bar(EMPTY + stage));
         next();
-        for (int j = 0; j < nb && ok; ++j) {
+        for (int j = 0; j < nn && ok; ++j) {
           const int vs = stage;
           const uint32_t vp = phase;
           next();
           const int ks = stage;
           const uint32_t kp = phase;
-          if (j + 1 < nb) next();
-          bool v_in = false, k_in = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            const int n = t ? nb1 : nb0;
-            if (j < n) {
-              ok = wait(PFULL + t, j & 1) && (v_in || wait(FULL + vs, vp));
-              v_in = true;
-              if (ok) pv(t, vs, j > 0);
-            }
-            if (ok && j + 1 < n) {
-              ok = k_in || wait(FULL + ks, kp);
-              k_in = true;
-              if (ok) qk(t, ks);
-            }
+          if (j + 1 < nn) next();
+          // V(j), K(j+1) and the first tile's P(j)
+          const bool more = j + 1 < nn;
+          const int pb = PFULL + (j < n0 ? 0 : 1);
+          ok = wait3(FULL + vs, vp, more ? FULL + ks : FULL + vs, more ? kp : vp, pb, j & 1);
+          if (!ok) break;
+          if (j < n0) {
+            pv(0, vs, j > 0);
+            if (j + 1 < n0) qk(0, ks);
+            if (j < n1) ok = wait(PFULL + 1, j & 1);
           }
-          tc_commit(bar(EMPTY + vs));
-          if (j + 1 < nb) tc_commit(bar(EMPTY + ks));
+          if (ok && j < n1) {
+            pv(1, vs, j > 0);
+            if (j + 1 < n1) qk(1, ks);
+          }
+          if (leader) {
+            tc_commit(bar(EMPTY + vs));
+            if (j + 1 < nn) tc_commit(bar(EMPTY + ks));
+          }
         }
       }
       // every MMA has completed before TMEM and shared memory go away
-      tc_commit(bar(DONE));
+      if (leader) tc_commit(bar(DONE));
       mbar_wait_bounded(bar(DONE), 0, timeout_ns);
     }
   } else {
@@ -351,7 +392,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar(SFULL + t), j & 1, timeout_ns, abort_flag, status, 53));
+      ok = warp_wait(bar(SFULL + t), j & 1, timeout_ns, abort_flag, status, 53);
       if (!ok) break;
       tc_fence_after();
       uint32_t s[4][32];
@@ -366,16 +407,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           for (int i = 0; i < 32; ++i)
             if (32 * c + i >= left) s[c][i] = 0xff800000u;  // -inf
       }
-      float mx = -INFINITY;
+      // four chains of three-input maxima (max drops a NaN score: the maximum is never NaN)
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          mx = fmaxf(mx, fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
+      for (int i = 0; i < 64; ++i)
+        mx4[i & 3] = max3(mx4[i & 3], __uint_as_float(s[i >> 4][2 * (i & 15)]), __uint_as_float(s[i >> 4][2 * (i & 15) + 1]));
+      const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
       if (__any_sync(0xffffffffu, mx > m + thr)) {
         const bool up = mx > m + thr;
         if (j > 0) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(bar(ODONE + t), (j - 1) & 1, timeout_ns, abort_flag, status, 53));
+          ok = warp_wait(bar(ODONE + t), (j - 1) & 1, timeout_ns, abort_flag, status, 53);
           if (!ok) break;
           tc_fence_after();
           const float a = up ? ex2((m - mx) * c2) : 1.0f;
@@ -394,17 +435,37 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       }
       const float mc = m == -INFINITY ? 0.f : -m * c2;
       const uint64_t c2p = f2_pack(c2, c2), mcp = f2_pack(mc, mc);
+      // in batches of 16: the arguments and powers of one batch are issued before the sums and packing of the one
+      // before, so that nothing waits for a power of two just asked for
       uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int c = 2 * h + (i >> 4), e = 2 * (i & 15);
-          const uint64_t x = ffma2(((uint64_t)s[c][e + 1] << 32) | s[c][e], c2p, mcp);
-          const float a = ex2(f2_lo(x)), b = ex2(f2_hi(x));
-          if (i & 1) sum1 = fadd2(sum1, f2_pack(a, b)); else sum0 = fadd2(sum0, f2_pack(a, b));
-          p[i] = pack_bf16x2(a, b);
+        for (int b = 0; b < 5; ++b) {
+          if (b < 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t* v = &s[2 * h + (b >> 1)][16 * (b & 1) + 2 * i];
+              const uint64_t x = ffma2(((uint64_t)v[1] << 32) | v[0], c2p, mcp);
+              v[0] = (uint32_t)x;
+              v[1] = (uint32_t)(x >> 32);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t& v = s[2 * h + (b >> 1)][16 * (b & 1) + i];
+              v = __float_as_uint(ex2(__uint_as_float(v)));
+            }
+          }
+          if (b > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t* v = &s[2 * h + ((b - 1) >> 1)][16 * ((b - 1) & 1) + 2 * i];
+              const uint64_t x = ((uint64_t)v[1] << 32) | v[0];
+              if (i & 1) sum1 = fadd2(sum1, x); else sum0 = fadd2(sum0, x);
+              p[8 * (b - 1) + i] = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+            }
+          }
         }
         tmem_st_32x32b_x32(tS + 32 * h, p);
       }
@@ -417,7 +478,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
     // ---- the rows' results
     if (ok && n > 0) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar(ODONE + t), (n - 1) & 1, timeout_ns, abort_flag, status, 53));
+      ok = warp_wait(bar(ODONE + t), (n - 1) & 1, timeout_ns, abort_flag, status, 53);
       tc_fence_after();
     }
     if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
@@ -531,7 +592,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
