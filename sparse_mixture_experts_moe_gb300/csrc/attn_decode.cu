@@ -3,16 +3,17 @@
 // once), each sequence's own keys (here), and the join of the pieces.
 //
 // Own keys are an HBM stream: every key and value is read once and meets the G rows of its head group, far
-// too few to fill a 128-row tile, so the products are m16n8k16 MMAs with the rows padded to 16.
-//   work    a segment is (sequence, key/value head, group of 16 rows); its keys go in blocks of 64. All
-//           segments' blocks laid end to end are cut into equal runs, one a CTA: lengths live on the device and
+// too few to fill a 128-row tile. The products are m16n8k16 MMAs with the keys on the long side,
+//   S^T = K Q^T (16 keys x 8 rows),   O^T += V^T P^T (16 elements x 8 rows),
+// so that a group of up to 8 rows wastes nothing (rows on the 16 side took twice the MMAs and accumulator
+// registers); groups of more than 8 rows take two n-tiles for each load of K and V.
+//   work    a segment is (sequence, key/value head, group of 8 or 16 rows); its keys go in units of 64. All
+//           segments' units laid end to end are cut into equal runs, one a CTA: lengths live on the device and
 //           differ wildly, and equal runs keep every SM streaming whatever they are. A segment cut by a run's end
 //           leaves pieces that the join adds up, in order.
-//   warps   4, each with 16 keys of every block, its own ring of TMA copies (16 rows of K and V, swizzled: a box
-//           never crosses a page) and its own running maximum: no barrier between warps until a segment
-//           ends. Two CTAs an SM with 3 stages hold 2 x 4 x 2 x 8 KB = 128 KB in flight, more than the
-//           latency of HBM times its rate (about 50 KB an SM).
-// Piece (segment s, CTA c) has number s + c: going along the blocks, s or c grows by one from piece to piece.
+//   warps   one loads units by TMA into a ring (boxes never cross a page), running ahead over segment ends; eight
+//           take 16 keys each, four to a unit, with their own running maximum, and meet only where a segment ends.
+// Piece (segment s, CTA c) has number s + c: going along the units, s or c grows by one from piece to piece.
 #include <cuda.h>
 
 #include "attn.cuh"
@@ -21,29 +22,41 @@
 namespace moe {
 namespace {
 
-constexpr int kSlice = 2048;   // sequences a launch takes: their block counts are scanned in shared memory
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kKeys = 16;      // keys of a warp's chunk
-constexpr int kBlock = kWarps * kKeys;
-constexpr int kStages = 3;
-constexpr int kCtasPerSm = 2;
+constexpr int kSlice = 2048;   // sequences a launch takes: their unit counts are scanned in shared memory
+constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);
+constexpr int kKeys = 16;      // keys of a warp
+constexpr int kUnit = 4 * kKeys;
+constexpr int kScan = 256;     // threads that scan the lengths
 
-template <int DP> constexpr int kHalf = DP * kKeys * 2;  // bytes of a chunk's K (or V)
+template <int DP, int NT> struct Cfg {
+  static constexpr int kHalf = DP * kUnit * 2;  // bytes of a unit's K (or V)
+  // Even: the units of a stage then all belong to one group of warps, which sees every phase of its barrier. (With an
+  // odd ring a group meets a stage every other phase, whose parity cannot tell "loaded" from "not yet".)
+  static constexpr int kStages = DP == 64 ? 8 : 4;
+  static_assert(kStages % 2 == 0, "a stage belongs to one group of consumer warps");
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kLd = DP + 4;            // floats of a row in the merge buffer: no bank conflicts
+};
 
-template <int DP> __host__ __device__ constexpr size_t own_smem(int n) {
-  return 1024 + (size_t)kWarps * kStages * 2 * kHalf<DP> + 16 * DP * 4 + 2 * kWarps * 16 * 4 + 8 * kWarps * kStages + 16 +
-         4 * (size_t)(n + 1) + 4 * kThreads;
+template <int DP, int NT> __host__ __device__ constexpr size_t own_smem(int n) {
+  using C = Cfg<DP, NT>;
+  return 1024 + (size_t)C::kStages * 2 * C::kHalf + (size_t)kWarps * C::kRows * C::kLd * 4 + 2 * kWarps * C::kRows * 4 +
+         16 * C::kStages + 16 + 4 * (size_t)(n + 1) + 4 * kScan;
 }
+static_assert(own_smem<128, 1>(kSlice) <= 232448 && own_smem<128, 2>(kSlice) <= 232448 &&
+              own_smem<64, 2>(kSlice) <= 232448, "shared memory");
 
 struct OwnArgs {
   DecodeArgs d;
   float* o;        // [piece][rows][D]
   float2* ml;      // [piece][rows]
-  int32_t* prefix; // [n + 1] blocks of one head group before sequence i, then [n + 1] = blocks per CTA
+  int32_t* prefix; // [n + 1] units of one head group before sequence i, then [n + 1] = units per CTA
   const float* sh_o;      // [(sequence, head)][splits][D]
   const float2* sh_ml;
   int splits;      // pieces of a row over the shared keys
   int first;       // sequence number of the slice's first row (for errors)
+  int R;           // rows of a piece: min(G, 8 NT)
+  int RG;          // row groups of a key/value head
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -60,9 +73,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A walk over the blocks of a run.
+// The transpose of an 8 x 8 matrix of 16-bit values, one row a group of four lanes.
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+// A walk over the units of a run.
 struct Cursor {
-  int i, hr, b, nb;  // sequence, head group, block, blocks of the sequence
+  int i, hr, b, nb;  // sequence, head group, unit, units of the sequence
 };
 __device__ __forceinline__ void advance(Cursor& c, const int* P, int n, int HR) {
   if (++c.b < c.nb) return;
@@ -75,38 +96,45 @@ __device__ __forceinline__ void advance(Cursor& c, const int* P, int n, int HR) 
   } while (c.nb == 0);
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int DP, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
 decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16,
                   const __grid_constant__ OwnArgs a) {
-  constexpr int KS = DP / 16;  // k-steps of the scores
+  using C = Cfg<DP, NT>;
+  constexpr int KS = DP / 16;  // k-steps of the scores, d-tiles of the output
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  float* buf = reinterpret_cast<float*>(gbase + kWarps * kStages * 2 * kHalf<DP>);  // [16][DP]
-  float* sm_m = buf + 16 * DP;        // [warps][16]
-  float* sm_l = sm_m + kWarps * 16;   // [warps][16]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm_l + kWarps * 16);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kStages);
-  int* P = reinterpret_cast<int*>(bars + kWarps * kStages + 2);  // [n + 1]
-  const int n = a.d.n, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int* sums = P + n + 1;              // [kThreads]
+  float* buf = reinterpret_cast<float*>(gbase + C::kStages * 2 * C::kHalf);  // [warps][rows][kLd]
+  float* sm_m = buf + kWarps * C::kRows * C::kLd;  // [warps][rows]
+  float* sm_l = sm_m + kWarps * C::kRows;          // [warps][rows]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm_l + kWarps * C::kRows);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * C::kStages);
+  int* P = reinterpret_cast<int*>(bars + 2 * C::kStages + 2);  // [n + 1]
+  const int n = a.d.n, tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  int* sums = P + n + 1;                           // [kScan]
   const CacheView& c = a.d.c;
-  const int G = a.d.H / c.Hkv, RG = (G + 15) / 16, HR = c.Hkv * RG, R = G < 16 ? G : 16, D = c.D;
+  const int G = a.d.H / c.Hkv, HR = c.Hkv * a.RG, D = c.D;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  constexpr int FULL = 0, EMPTY = C::kStages;
 
   if (tid == 0) {
-    for (int s = 0; s < kWarps * kStages; ++s) mbar_init(smem_u32(bars + s), 1);
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(bar(FULL + s), 1); mbar_init(bar(EMPTY + s), 4); }
     fence_mbar_init();
     *abort_flag = 0;
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  griddep_wait();
+  // After the shared part's kernel this one need not wait for it: that kernel lets dependents start only once it has
+  // itself waited for everything before it, and what it writes is read by the join alone (for which this grid waits
+  // at its end). Alone, it waits here.
+  if (a.d.shared == 0) griddep_wait();
   griddep_launch_dependents();
 
-  // ---- blocks of every sequence, scanned
-  const int chunk = (n + kThreads - 1) / kThreads, i0 = min(n, tid * chunk), i1 = min(n, i0 + chunk);
+  // ---- units of every sequence, scanned
+  const int chunk = (n + kScan - 1) / kScan, i0 = min(n, tid * chunk), i1 = tid < kScan ? min(n, i0 + chunk) : i0;
   int mine = 0;
   for (int i = i0; i < i1; ++i) {
     const int s = a.d.slots[i];
@@ -117,35 +145,48 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (blockIdx.x == 0) record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + i);
       len = 0;
     }
-    const int nb = len > a.d.shared ? (len - a.d.shared + kBlock - 1) / kBlock : 0;
+    const int nb = len > a.d.shared ? (len - a.d.shared + kUnit - 1) / kUnit : 0;
     P[i + 1] = nb;
     mine += nb;
   }
-  sums[tid] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    int v[kThreads / 32], t = 0;
+  if (n <= 32) {  // one warp's scan
+    if (warp == 0) {
+      int incl = mine;
 #pragma unroll
-    for (int j = 0; j < kThreads / 32; ++j) {
-      v[j] = t;
-      t += sums[lane * (kThreads / 32) + j];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (lane < n) P[lane + 1] = incl;
+      if (lane == 0) P[0] = 0;
     }
-    int incl = t;
+  } else {
+    if (tid < kScan) sums[tid] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      int v[kScan / 32], t = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
+      for (int j = 0; j < kScan / 32; ++j) {
+        v[j] = t;
+        t += sums[lane * (kScan / 32) + j];
+      }
+      int incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+#pragma unroll
+      for (int j = 0; j < kScan / 32; ++j) sums[lane * (kScan / 32) + j] = incl - t + v[j];
     }
-#pragma unroll
-    for (int j = 0; j < kThreads / 32; ++j) sums[lane * (kThreads / 32) + j] = incl - t + v[j];
+    __syncthreads();
+    int run = tid < kScan ? sums[tid] : 0;
+    for (int i = i0; i < i1; ++i) {
+      run += P[i + 1];
+      P[i + 1] = run;
+    }
+    if (tid == 0) P[0] = 0;
   }
-  __syncthreads();
-  int run = sums[tid];
-  for (int i = i0; i < i1; ++i) {
-    run += P[i + 1];
-    P[i + 1] = run;
-  }
-  if (tid == 0) P[0] = 0;
   __syncthreads();
   const long long total = (long long)P[n] * HR;
   const int per = (int)((total + gridDim.x - 1) / gridDim.x);
@@ -153,23 +194,11 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int i = tid; i <= n; i += kThreads) a.prefix[i] = P[i];
     if (tid == 0) a.prefix[n + 1] = per;
   }
-  // that the slots share what the caller says they share
-  if (a.d.shared > 0) {
-    const int s0 = a.d.slots[0], pages = a.d.shared >> c.page_shift;
-    if (s0 >= 0 && s0 < c.n_slots)
-      for (long long x = (long long)blockIdx.x * kThreads + tid; x < (long long)n * pages; x += (long long)gridDim.x * kThreads) {
-        const int i = (int)(x / pages), p = (int)(x % pages), s = a.d.slots[i];
-        if (s < 0 || s >= c.n_slots || (p << c.page_shift) >= c.lens[s]) continue;
-        const int page = c.table[(long long)s * c.width + p];
-        if (page < 0 || page >= c.n_pages || page != c.table[(long long)s0 * c.width + p])
-          record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + i);
-      }
-  }
   const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
-  if (begin >= end) return;
+  const int count = end > begin ? (int)(end - begin) : 0;
 
-  Cursor cu;
-  {
+  Cursor cu{0, 0, 0, 0};
+  if (count > 0) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -181,251 +210,300 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     cu.hr = r / cu.nb;
     cu.b = r % cu.nb;
   }
-  Cursor ld = cu;
-  const int count = (int)(end - begin);
-  const uint32_t ring = base + warp * kStages * 2 * kHalf<DP>;
-  const uint32_t bar0 = smem_u32(bars + warp * kStages);
 
-  // ---- this warp's copies, kStages chunks ahead
-  int ld_slot_i = -1, ld_slot = 0;
-  uint32_t issued = 0;
-  auto issue = [&](int stage) {
-    if (ld.i != ld_slot_i) { ld_slot_i = ld.i; ld_slot = a.d.slots[ld.i]; }
-    const int key = a.d.shared + ld.b * kBlock + warp * kKeys, len = c.lens[ld_slot];
-    if (key < len) {
-      int page = c.table[(long long)ld_slot * c.width + (key >> c.page_shift)];
-      if (page < 0 || page >= c.n_pages) {
-        record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + ld.i);
-        page = 0;
-      }
-      const int row = (page * c.Hkv + ld.hr / RG) * c.page_size + (key & (c.page_size - 1));
-      const uint32_t dst = ring + stage * 2 * kHalf<DP>, b = bar0 + 8 * stage;
-      mbar_arrive_expect_tx(b, 2 * kHalf<DP>);
-#pragma unroll
-      for (int h = 0; h < DP / 64; ++h) {
-        tma_load_2d(dst + h * 2048, &tmK, 64 * h, row, b);
-        tma_load_2d(dst + kHalf<DP> + h * 2048, &tmV, 64 * h, row, b);
-      }
-    } else {
-      mbar_arrive(bar0 + 8 * stage);  // nothing of this block for this warp
-    }
-    issued |= 1u << stage;
-    advance(ld, P, n, HR);
-  };
-  __syncwarp();
-  if (lane == 0)
-    for (int s = 0; s < kStages && s < count; ++s) issue(s);
-
-  const float c2 = a.d.scale * 1.4426950408889634f, thr = 8.0f / c2;
-  const int g = lane >> 2, t4 = lane & 3;
-  uint32_t q[KS][4];
-  float o[DP / 8][4], m[2], l[2];
-  int cur_i = -1, cur_hr = -1, len = 0, slot = 0;
-  int stage = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-
-  for (int x = 0; x < count; ++x) {
-    if (cu.i != cur_i || cu.hr != cur_hr) {  // a new segment: its rows as A fragments
-      if (cu.i != cur_i) {
-        slot = a.d.slots[cu.i];
-        len = c.lens[slot];
-      }
-      cur_i = cu.i;
-      cur_hr = cu.hr;
-      const int hk = cu.hr / RG, r0 = (cu.hr % RG) * 16, nr = min(R, G - r0);
-      const __nv_bfloat16* qp = (const __nv_bfloat16*)a.d.q + (long long)cu.i * a.d.qs + (long long)(hk * G + r0) * D;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = g + 8 * (e & 1), col = 16 * k + 2 * t4 + 8 * (e >> 1);
-          q[k][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
+  if (warp == kWarps) {
+    if (lane == 0 && count > 0) {
+      // -------------------------------------------------------------- loads
+      int stage = 0, slot = 0, len = 0, cur = -1;
+      uint32_t phase = 0, filled = 0, fill_phase = 0;
+      const int box = min(c.page_size, kUnit);
+      for (int x = 0; x < count; ++x, advance(cu, P, n, HR)) {
+        if (cu.i != cur) {
+          cur = cu.i;
+          slot = a.d.slots[cur];
+          len = c.lens[slot];
         }
+        if (!wait_or_abort(bar(EMPTY + stage), phase ^ 1u, a.d.timeout_ns, abort_flag, a.d.status, 62)) break;
+        const int key = a.d.shared + cu.b * kUnit, rows = min(kUnit, (len - key + kKeys - 1) & ~(kKeys - 1));
+        const uint32_t dst = base + stage * 2 * C::kHalf, b = bar(FULL + stage);
+        mbar_arrive_expect_tx(b, 2u * (uint32_t)(rows * DP * 2));
+        for (int r = 0; r < rows;) {
+          const int nr = rows - r >= box ? box : kKeys;  // whole boxes, then 16 rows at a time
+          int page = c.table[(long long)slot * c.width + ((key + r) >> c.page_shift)];
+          if (page < 0 || page >= c.n_pages) {
+            record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + cur);
+            page = 0;
+          }
+          const int row = (page * c.Hkv + cu.hr / a.RG) * c.page_size + ((key + r) & (c.page_size - 1));
+          const CUtensorMap *mk = nr == box ? &tmK : &tmK16, *mv = nr == box ? &tmV : &tmV16;
 #pragma unroll
-      for (int j = 0; j < DP / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
+          for (int h = 0; h < DP / 64; ++h) {
+            tma_load_2d(dst + h * (kUnit * 128) + r * 128, mk, 64 * h, row, b);
+            tma_load_2d(dst + C::kHalf + h * (kUnit * 128) + r * 128, mv, 64 * h, row, b);
+          }
+          r += nr;
+        }
+        filled |= 1u << stage;
+        fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+      }
+      // copies in flight land before shared memory goes away
+      for (int s = 0; s < C::kStages; ++s)
+        if (filled & (1u << s)) mbar_wait_bounded(bar(FULL + s), (fill_phase >> s) & 1u, a.d.timeout_ns);
     }
-    if (ok) ok = warp_wait(bar0 + 8 * stage, phase, a.d.timeout_ns, abort_flag, a.d.status, 61);
-    const int key = a.d.shared + cu.b * kBlock + warp * kKeys, left = len - key;
-    if (ok && left > 0) {
-      const uint32_t sk = ring + stage * 2 * kHalf<DP>, sv = sk + kHalf<DP>;
-      if (left < kKeys) {  // positions past the end hold anything: zero their values
-        for (int z = lane; z < (kKeys - left) * (DP / 64) * 8; z += 32) {
-          const int rr = left + z / ((DP / 64) * 8), u = z % ((DP / 64) * 8);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sv + (u >> 3) * 2048 + rr * 128 + (u & 7) * 16), "r"(0)
-                       : "memory");
+  } else {
+    // that the slots share what the caller says they share
+    if (a.d.shared > 0) {
+      const int s0 = a.d.slots[0], pages = a.d.shared >> c.page_shift;
+      if (s0 >= 0 && s0 < c.n_slots)
+        for (long long x = (long long)blockIdx.x * (32 * kWarps) + tid; x < (long long)n * pages;
+             x += (long long)gridDim.x * (32 * kWarps)) {
+          const int i = (int)(x / pages), p = (int)(x % pages), s = a.d.slots[i];
+          if (s < 0 || s >= c.n_slots || (p << c.page_shift) >= c.lens[s]) continue;
+          const int page = c.table[(long long)s * c.width + p];
+          if (page < 0 || page >= c.n_pages || page != c.table[(long long)s0 * c.width + p])
+            record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + i);
+        }
+    }
+    const float c2 = a.d.scale * 1.4426950408889634f, thr = 8.0f / c2;
+    const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, group = warp >> 2;
+    const int mi = lane >> 3, l8 = lane & 7;
+    uint32_t q[KS][NT][2];
+    float o[KS][NT][4], m[NT][2], l[NT][2];
+    int cur_i = -1, cur_hr = -1, len = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int x = 0; x < count; ++x) {
+      if (cu.i != cur_i || cu.hr != cur_hr) {  // a new segment: its rows as B fragments
+        if (cu.i != cur_i) len = c.lens[a.d.slots[cu.i]];
+        cur_i = cu.i;
+        cur_hr = cu.hr;
+        const int hk = cu.hr / a.RG, r0 = (cu.hr % a.RG) * C::kRows, nr = min(a.R, G - r0);
+        const __nv_bfloat16* qp = (const __nv_bfloat16*)a.d.q + (long long)cu.i * a.d.qs + (long long)(hk * G + r0) * D;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = 8 * t + g, col = 16 * k + 2 * t4 + 8 * e;
+              q[k][t][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
+              o[k][t][2 * e] = o[k][t][2 * e + 1] = 0.f;
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          m[t][0] = m[t][1] = -INFINITY;
+          l[t][0] = l[t][1] = 0.f;
+        }
+      }
+      if ((x & 1) == group) {
+        if (ok) ok = warp_wait(bar(FULL + stage), phase, a.d.timeout_ns, abort_flag, a.d.status, 61);
+        const int left = len - (a.d.shared + cu.b * kUnit + quarter * kKeys);  // keys of this warp's 16
+        if (ok && left > 0) {
+          const uint32_t sk = base + stage * 2 * C::kHalf + quarter * (kKeys * 128), sv = sk + C::kHalf;
+          if (left < kKeys) {  // positions past the end hold anything: zero their values
+            for (int z = lane; z < (kKeys - left) * (DP / 8); z += 32) {
+              const int rr = left + z / (DP / 8), u = z % (DP / 8);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sv + (u >> 3) * (kUnit * 128) + rr * 128 + (u & 7) * 16), "r"(0)
+                           : "memory");
+            }
+            __syncwarp();
+          }
+          float s[NT][4];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int row = (mi & 1) * 8 + l8, u = 2 * k + (mi >> 1);
+            uint32_t f[4];
+            ldsm4(sk + (u >> 3) * (kUnit * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), f);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(s[t], f, q[k][t][0], q[k][t][1]);
+          }
+          if (left < kKeys)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (g + 8 * (e >> 1) >= left) s[t][e] = -INFINITY;
+          // the maxima are only reduced, and O rescaled, when one rises by more than 2^8 (as in attn_tc.cu)
+          bool rise = false;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            rise = rise || fmaxf(s[t][0], s[t][2]) > m[t][0] + thr || fmaxf(s[t][1], s[t][3]) > m[t][1] + thr;
+          if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float mx = fmaxf(fmaxf(s[t][r], s[t][2 + r]), -INFINITY);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                if (mx > m[t][r] + thr) {
+                  const float al = ex2((m[t][r] - mx) * c2);
+                  l[t][r] *= al;
+#pragma unroll
+                  for (int k = 0; k < KS; ++k) { o[k][t][r] *= al; o[k][t][2 + r] *= al; }
+                  m[t][r] = mx;
+                }
+              }
+          }
+          uint32_t p[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float mc0 = m[t][0] == -INFINITY ? 0.f : m[t][0] * c2, mc1 = m[t][1] == -INFINITY ? 0.f : m[t][1] * c2;
+            const float p0 = ex2(fmaf(s[t][0], c2, -mc0)), p1 = ex2(fmaf(s[t][1], c2, -mc1));
+            const float p2 = ex2(fmaf(s[t][2], c2, -mc0)), p3 = ex2(fmaf(s[t][3], c2, -mc1));
+            l[t][0] += p0 + p2;
+            l[t][1] += p1 + p3;
+            p[t][0] = movm_t(pack_bf16x2(p0, p1));
+            p[t][1] = movm_t(pack_bf16x2(p2, p3));
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int row = (mi >> 1) * 8 + l8, u = 2 * k + (mi & 1);
+            uint32_t f[4];
+            ldsm4t(sv + (u >> 3) * (kUnit * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), f);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(o[k][t], f, p[t][0], p[t][1]);
+          }
+          if (left < kKeys) fence_proxy_async_smem();  // the zeros above before the next copy into this stage
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(bar(EMPTY + stage));
       }
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-      for (int kp = 0; kp < KS / 2; ++kp)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int row = 8 * nt + (lane & 7), u = 4 * kp + (lane >> 3);
-          uint32_t b[4];
-          ldsm4(sk + (u >> 3) * 2048 + row * 128 + (((u & 7) ^ (row & 7)) << 4), b);
-          mma16816(s[nt], q[2 * kp], b[0], b[1]);
-          mma16816(s[nt], q[2 * kp + 1], b[2], b[3]);
-        }
-      if (left < kKeys)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (8 * nt + 2 * t4 + (e & 1) >= left) s[nt][e] = -INFINITY;
-      float mx[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-      }
-      // rescaled only when a maximum rises by more than 2^8 (as in attn_tc.cu)
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + thr || mx[1] > m[1] + thr)) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (mx[r] > m[r] + thr) {
-            const float al = ex2((m[r] - mx[r]) * c2);
-            l[r] *= al;
-#pragma unroll
-            for (int j = 0; j < DP / 8; ++j) { o[j][2 * r] *= al; o[j][2 * r + 1] *= al; }
-            m[r] = mx[r];
-          }
-      }
-      uint32_t p[4];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float mc = m[r] == -INFINITY ? 0.f : m[r] * c2;
-        const float p0 = ex2(fmaf(s[0][2 * r], c2, -mc)), p1 = ex2(fmaf(s[0][2 * r + 1], c2, -mc));
-        const float p2 = ex2(fmaf(s[1][2 * r], c2, -mc)), p3 = ex2(fmaf(s[1][2 * r + 1], c2, -mc));
-        l[r] += (p0 + p1) + (p2 + p3);
-        p[r] = pack_bf16x2(p0, p1);
-        p[2 + r] = pack_bf16x2(p2, p3);
-      }
-#pragma unroll
-      for (int np = 0; np < DP / 16; ++np) {
-        const int mi = lane >> 3, row = (mi & 1) * 8 + (lane & 7), u = 2 * np + (mi >> 1);
-        uint32_t b[4];
-        ldsm4t(sv + (u >> 3) * 2048 + row * 128 + (((u & 7) ^ (row & 7)) << 4), b);
-        mma16816(o[2 * np], p, b[0], b[1]);
-        mma16816(o[2 * np + 1], p, b[2], b[3]);
-      }
-    }
-    if (left < kKeys) fence_proxy_async_smem();  // the zeros above before the next copy into this stage
-    __syncwarp();
-    if (lane == 0 && x + kStages < count) issue(stage);
-    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
 
-    const Cursor was = cu;
-    advance(cu, P, n, HR);
-    if (x + 1 < count && cu.i == was.i && cu.hr == was.hr) continue;
-    // ---- the segment (or the run) ends: the four warps' parts become one piece
+      const Cursor was = cu;
+      advance(cu, P, n, HR);
+      if (x + 1 < count && cu.i == was.i && cu.hr == was.hr) continue;
+      // ---- the segment (or the run) ends: the eight warps' parts become one piece
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t4 == 0) {
-        sm_m[warp * 16 + g + 8 * r] = m[r];
-        sm_l[warp * 16 + g + 8 * r] = l[r];
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], w);
+          if (g == 0) {
+            sm_m[warp * C::kRows + 8 * t + 2 * t4 + r] = m[t][r];
+            sm_l[warp * C::kRows + 8 * t + 2 * t4 + r] = l[t][r];
+          }
+        }
+      consumers_sync();
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 8 * t + 2 * t4 + r;
+          float M = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < kWarps; ++y) M = fmaxf(M, sm_m[y * C::kRows + row]);
+          const float w = M == -INFINITY ? 0.f : ex2((m[t][r] - M) * c2);
+          float* d = buf + (warp * C::kRows + row) * C::kLd + g;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            d[16 * k] = o[k][t][r] * w;
+            d[16 * k + 8] = o[k][t][2 + r] * w;
+          }
+        }
+      consumers_sync();
+      const int nr = min(a.R, G - (was.hr % a.RG) * C::kRows);
+      const long long piece = (long long)was.i * HR + was.hr + blockIdx.x;
+      for (int z = tid; z < nr * (D / 4); z += 32 * kWarps) {
+        const int row = z / (D / 4), col = (z % (D / 4)) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) {
+          const float4 u = *reinterpret_cast<const float4*>(buf + (y * C::kRows + row) * C::kLd + col);
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        *reinterpret_cast<float4*>(a.o + (piece * a.R + row) * D + col) = v;
       }
+      if (tid < nr) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) M = fmaxf(M, sm_m[y * C::kRows + tid]);
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y)
+          if (M != -INFINITY) L += sm_l[y * C::kRows + tid] * ex2((sm_m[y * C::kRows + tid] - M) * c2);
+        a.ml[piece * a.R + tid] = make_float2(M * c2, L);
+      }
+      consumers_sync();
     }
-    __syncthreads();
-    float w[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int y = 0; y < kWarps; ++y) M = fmaxf(M, sm_m[y * 16 + g + 8 * r]);
-      w[r] = M == -INFINITY ? 0.f : ex2((m[r] - M) * c2);
-    }
-    for (int y = 0; y < kWarps; ++y) {
-      if (warp == y)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (g + 8 * r < R)
-#pragma unroll
-            for (int j = 0; j < DP / 8; ++j) {
-              float2* d = reinterpret_cast<float2*>(buf + (g + 8 * r) * DP + 8 * j + 2 * t4);
-              float2 v = make_float2(o[j][2 * r] * w[r], o[j][2 * r + 1] * w[r]);
-              if (y > 0) { const float2 before = *d; v.x += before.x; v.y += before.y; }
-              *d = v;
-            }
-      __syncthreads();
-    }
-    const int nr = min(R, G - (was.hr % RG) * 16);
-    const long long piece = (long long)was.i * HR + was.hr + blockIdx.x;
-    for (int z = tid; z < nr * (D / 4); z += kThreads) {
-      const int row = z / (D / 4), col = (z % (D / 4)) * 4;
-      *reinterpret_cast<float4*>(a.o + (piece * R + row) * D + col) = *reinterpret_cast<const float4*>(buf + row * DP + col);
-    }
-    if (tid < nr) {
-      float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int y = 0; y < kWarps; ++y) M = fmaxf(M, sm_m[y * 16 + tid]);
-#pragma unroll
-      for (int y = 0; y < kWarps; ++y)
-        if (M != -INFINITY) L += sm_l[y * 16 + tid] * ex2((sm_m[y * 16 + tid] - M) * c2);
-      a.ml[piece * R + tid] = make_float2(M * c2, L);
-    }
-    __syncthreads();
   }
-  // copies still in flight (after a wait that gave up) land before shared memory goes away
-  if (!ok && lane == 0)
-    for (int s = 0; s < kStages; ++s)
-      if (issued & (1u << s)) {
-        mbar_wait_bounded(bar0 + 8 * s, 0, a.d.timeout_ns);
-        mbar_wait_bounded(bar0 + 8 * s, 1, a.d.timeout_ns);
-      }
+  if (a.d.shared > 0) griddep_wait();
 }
 
-// One warp a (sequence, head): its pieces over the shared keys, then over its own, in order.
+// One CTA a (sequence, head): its pieces over the shared keys, then over its own. Four warps take every fourth piece
+// and add up in a fixed order.
 __global__ void __launch_bounds__(128)
 decode_join_kernel(const __grid_constant__ OwnArgs a) {
+  __shared__ float4 part[4][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const CacheView& c = a.d.c;
-  const int H = a.d.H, G = H / c.Hkv, RG = (G + 15) / 16, HR = c.Hkv * RG, R = G < 16 ? G : 16, D = c.D;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)a.d.n * H) return;
-  const int i = (int)(row / H), h = (int)(row % H), hr = (h / G) * RG + (h % G) / 16, r = (h % G) % 16;
-  const int s = a.d.slots[i];
+  const int H = a.d.H, G = H / c.Hkv, HR = c.Hkv * a.RG, D = c.D;
+  const int row = blockIdx.x, i = row / H, h = row % H, hk = h / G, hg = h % G, rows = G < a.R ? G : a.R;
+  const int hr = hk * a.RG + hg / rows, r = hg % rows;
+  const int s = a.d.slots[i], b0 = a.prefix[i], b1 = a.prefix[i + 1], per = a.prefix[a.d.n + 1];
   const bool valid = s >= 0 && s < c.n_slots;
-  const int b = a.prefix[i + 1] - a.prefix[i], per = a.prefix[a.d.n + 1];
-  const int shared = valid ? a.splits : 0;
+  const int b = b1 - b0, shared = valid ? a.splits : 0;
   int own = 0;
   long long p0 = 0;
   if (valid && b > 0) {
-    const long long start = (long long)a.prefix[i] * HR + (long long)hr * b;
-    const int c0 = (int)(start / per), c1 = (int)((start + b - 1) / per);
+    const long long start = (long long)b0 * HR + (long long)hr * b, last = start + b - 1;
+    int c0, c1;
+    if (last < (1ll << 31)) { c0 = (int)start / per; c1 = (int)last / per; }
+    else { c0 = (int)(start / per); c1 = (int)(last / per); }
     own = c1 - c0 + 1;
     p0 = (long long)i * HR + hr + c0;
   }
   const int count = shared + own;
-  auto ml = [&](int x) { return x < shared ? a.sh_ml[row * a.splits + x] : a.ml[(p0 + x - shared) * R + r]; };
-  float M = -INFINITY;
-  for (int x = lane; x < count; x += 32) M = fmaxf(M, ml(x).x);
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-  const float ref = M == -INFINITY ? 0.f : M;
+  auto ml = [&](int x) { return x < shared ? a.sh_ml[(long long)row * a.splits + x] : a.ml[(p0 + x - shared) * a.R + r]; };
+  auto src = [&](int x) {
+    return reinterpret_cast<const float4*>(x < shared ? a.sh_o + ((long long)row * a.splits + x) * D
+                                                      : a.o + ((p0 + x - shared) * a.R + r) * D) + lane;
+  };
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int x0 = 0; x0 < count; x0 += 32) {
-    float2 v = make_float2(-INFINITY, 0.f);
-    if (x0 + lane < count) v = ml(x0 + lane);
-    const float wv = ex2(v.x - ref), lw = wv * v.y;
-    const int m = min(32, count - x0);
-#pragma unroll 4
-    for (int y = 0; y < m; ++y) {
-      const float w = __shfl_sync(0xffffffffu, wv, y);
-      l += __shfl_sync(0xffffffffu, lw, y);
-      const int x = x0 + y;
-      const float* src = x < shared ? a.sh_o + (row * a.splits + x) * D : a.o + ((p0 + x - shared) * R + r) * D;
-      if (lane * 4 < D) {
-        const float4 u = *reinterpret_cast<const float4*>(src + lane * 4);
+  float l = 0.f, M = -INFINITY;
+  const bool on = lane * 4 < D;
+  if (count <= 32) {  // the usual case: one lane a piece, the weights computed once; the values are on their way meanwhile
+    const float2 v = lane < count ? ml(lane) : make_float2(-INFINITY, 0.f);
+    float4 u[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) u[y] = warp + 4 * y < count && on ? *src(warp + 4 * y) : make_float4(0.f, 0.f, 0.f, 0.f);
+    M = fmaxf(v.x, -INFINITY);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    const float wv = ex2(v.x - (M == -INFINITY ? 0.f : M));
+    l = wv * v.y;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const float w = __shfl_sync(0xffffffffu, wv, (warp + 4 * y) & 31);
+      o.x = fmaf(w, u[y].x, o.x);
+      o.y = fmaf(w, u[y].y, o.y);
+      o.z = fmaf(w, u[y].z, o.z);
+      o.w = fmaf(w, u[y].w, o.w);
+    }
+  } else {
+    for (int x = lane; x < count; x += 32) M = fmaxf(M, ml(x).x);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    const float ref = M == -INFINITY ? 0.f : M;
+    for (int x = lane; x < count; x += 32) {
+      const float2 v = ml(x);
+      l += ex2(v.x - ref) * v.y;
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    for (int x = warp; x < count; x += 4) {
+      const float w = ex2(ml(x).x - ref);
+      if (on) {
+        const float4 u = *src(x);
         o.x = fmaf(w, u.x, o.x);
         o.y = fmaf(w, u.y, o.y);
         o.z = fmaf(w, u.z, o.z);
@@ -433,8 +511,16 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
       }
     }
   }
+  part[warp][lane] = o;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int y = 1; y < 4; ++y) {
+    const float4 u = part[y][lane];
+    o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
+  }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  if (lane * 4 < D) {
+  if (on) {
     uint2 u;
     u.x = pack_bf16x2(o.x * inv, o.y * inv);
     u.y = pack_bf16x2(o.z * inv, o.w * inv);
@@ -450,12 +536,13 @@ bool encode_pages(EncodeTiledFn enc, CUtensorMap* m, const void* p, const CacheV
   return encode_tmap(enc, m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 2, dims, str, box);
 }
 
-template <int DP>
-cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const OwnArgs& o, int ctas, cudaStream_t s) {
-  const size_t smem = own_smem<DP>(o.d.n);
-  const cudaError_t e = cudaFuncSetAttribute(decode_own_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int DP, int NT>
+cudaError_t launch_own(const CUtensorMap (&tm)[4], const OwnArgs& o, int ctas, cudaStream_t s) {
+  const size_t smem = own_smem<DP, NT>(o.d.n);
+  auto kern = decode_own_kernel<DP, NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_own_kernel<DP>, dim3(ctas), dim3(kThreads), smem, s, tk, tv, o);
+  return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, tm[0], tm[1], tm[2], tm[3], o);
 }
 
 }  // namespace
@@ -463,11 +550,14 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const OwnAr
 cudaError_t launch_attn_decode_tc(const DecodeArgs& all, cudaStream_t s) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return cudaErrorNotSupported;
-  CUtensorMap ok{}, ov{};
-  if (!encode_pages(enc, &ok, all.k, all.c, kKeys) || !encode_pages(enc, &ov, all.v, all.c, kKeys))
+  CUtensorMap tm[4] = {};
+  const int box = all.c.page_size < kUnit ? all.c.page_size : kUnit;
+  if (!encode_pages(enc, &tm[0], all.k, all.c, box) || !encode_pages(enc, &tm[1], all.v, all.c, box) ||
+      !encode_pages(enc, &tm[2], all.k, all.c, kKeys) || !encode_pages(enc, &tm[3], all.v, all.c, kKeys))
     return cudaErrorInvalidValue;
-  const int G = all.H / all.c.Hkv, RG = (G + 15) / 16, HR = all.c.Hkv * RG, R = G < 16 ? G : 16, D = all.c.D;
-  const int ctas = device_sm_count() * kCtasPerSm;
+  const int G = all.H / all.c.Hkv, NT = G <= 8 ? 1 : 2, RG = (G + 8 * NT - 1) / (8 * NT), HR = all.c.Hkv * RG;
+  const int R = G < 8 * NT ? G : 8 * NT, D = all.c.D;
+  const int ctas = device_sm_count();
   for (int first = 0; first < all.n; first += kSlice) {
     DecodeArgs d = all;
     d.n = all.n - first < kSlice ? all.n - first : kSlice;
@@ -479,6 +569,8 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, cudaStream_t s) {
     o.d = d;
     o.first = first;
     o.splits = 0;
+    o.R = R;
+    o.RG = RG;
     // pieces: own ones [(n HR + ctas)][R], then the shared ones [n H][splits]; see decode_pieces
     const long long own_rows = ((long long)d.n * HR + ctas) * R;
     o.o = all.part;
@@ -492,10 +584,11 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, cudaStream_t s) {
     if (own_rows + sh_rows + 2 * kSlice > decode_pieces((long long)all.n * all.H)) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     if (d.shared > 0) e = launch_attn_shared_tc(d, o.splits, sh, const_cast<float2*>(o.sh_ml), s);
-    if (e == cudaSuccess)
-      e = D <= 64 ? launch_own<64>(ok, ov, o, ctas, s) : launch_own<128>(ok, ov, o, ctas, s);
-    if (e == cudaSuccess)
-      e = launch_pdl(decode_join_kernel, dim3((unsigned)(((long long)d.n * d.H + 3) / 4)), dim3(128), 0, s, o);
+    if (e == cudaSuccess) {
+      if (D <= 64) e = NT == 1 ? launch_own<64, 1>(tm, o, ctas, s) : launch_own<64, 2>(tm, o, ctas, s);
+      else e = NT == 1 ? launch_own<128, 1>(tm, o, ctas, s) : launch_own<128, 2>(tm, o, ctas, s);
+    }
+    if (e == cudaSuccess) e = launch_pdl(decode_join_kernel, dim3((unsigned)((long long)d.n * d.H)), dim3(128), 0, s, o);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

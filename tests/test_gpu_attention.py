@@ -232,6 +232,15 @@ def test_decode_ragged(seed, dtype):
     run_decode(lens, shared, *r.choice([(8, 2), (8, 8), (12, 2)]), r.choice([64, 128]), dtype, seed=seed)
 
 
+@pytest.mark.parametrize("H,Hk,D,page", [(8, 8, 64, 16), (16, 8, 128, 64), (64, 4, 128, 32), (128, 8, 64, 128)])
+def test_decode_long_runs(H, Hk, D, page):
+    """Enough keys that every CTA walks many blocks of several sequences, its ring round and round."""
+    r = random.Random(H)
+    shared = 2 * page
+    lens = [shared + r.choice([0, 1, 63, 64, 65, r.randint(500, 1900), r.randint(1000, 1900)]) for _ in range(40)]
+    run_decode(lens, shared, H, Hk, D, BF16, page, seed=H)
+
+
 def test_decode_many_rows_of_one_head():
     """More rows of a key/value head than one tile of the shared part holds."""
     run_decode([160 + i % 7 for i in range(80)], 144, 16, 2, 64, BF16)
