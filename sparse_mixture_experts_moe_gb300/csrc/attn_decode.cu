@@ -10,7 +10,9 @@
 //   work    a segment is (sequence, key/value head, group of 8 or 16 rows); its keys go in units of 64. All
 //           segments' units laid end to end are cut into equal runs, one a CTA: lengths live on the device and
 //           differ wildly, and equal runs keep every SM streaming whatever they are. A segment cut by a run's end
-//           leaves pieces that the join adds up, in order.
+//           leaves pieces that the join adds up, in order. A segment's end costs about as much as kEnd units (the
+//           warps meet, a piece is written, new rows are fetched), so each segment is laid out with that many
+//           empty units in front: without them runs of short segments took twice as long as the rest.
 //   warps   one loads units by TMA into a ring (boxes never cross a page), running ahead over segment ends; eight
 //           take 16 keys each, four to a unit, with their own running maximum, and meet only where a segment ends.
 // Piece (segment s, CTA c) has number s + c: going along the units, s or c grows by one from piece to piece.
@@ -27,6 +29,7 @@ constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = 16;      // keys of a warp
 constexpr int kUnit = 4 * kKeys;
 constexpr int kScan = 256;     // threads that scan the lengths
+constexpr int kEnd = 2;        // units that a segment's end is worth
 
 template <int DP, int NT> struct Cfg {
   static constexpr int kHalf = DP * kUnit * 2;  // bytes of a unit's K (or V)
@@ -50,7 +53,8 @@ struct OwnArgs {
   DecodeArgs d;
   float* o;        // [piece][rows][D]
   float2* ml;      // [piece][rows]
-  int32_t* prefix; // [n + 1] units of one head group before sequence i, then [n + 1] = units per CTA
+  int32_t* prefix; // [n + 1] units of one head group before sequence i (kEnd a segment included), then [n + 1] =
+                   // units per CTA
   const float* sh_o;      // [(sequence, head)][splits][D]
   const float2* sh_ml;
   int splits;      // pieces of a row over the shared keys
@@ -81,19 +85,21 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
-// A walk over the units of a run.
+// A walk over the units of a run. b counts from 0 over the kEnd empty units and the nb - kEnd with keys.
 struct Cursor {
   int i, hr, b, nb;  // sequence, head group, unit, units of the sequence
 };
-__device__ __forceinline__ void advance(Cursor& c, const int* P, int n, int HR) {
-  if (++c.b < c.nb) return;
-  c.b = 0;
-  if (++c.hr < HR) return;
+// To the next unit with keys: returns how many units it is away.
+__device__ __forceinline__ int advance(Cursor& c, const int* P, int n, int HR) {
+  if (++c.b < c.nb) return 1;
+  c.b = kEnd;
+  if (++c.hr < HR) return 1 + kEnd;
   c.hr = 0;
   do {
-    if (++c.i >= n) return;
+    if (++c.i >= n) return 1 << 30;
     c.nb = P[c.i + 1] - P[c.i];
   } while (c.nb == 0);
+  return 1 + kEnd;
 }
 
 template <int DP, int NT>
@@ -145,7 +151,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (blockIdx.x == 0) record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + i);
       len = 0;
     }
-    const int nb = len > a.d.shared ? (len - a.d.shared + kUnit - 1) / kUnit : 0;
+    const int nb = len > a.d.shared ? (len - a.d.shared + kUnit - 1) / kUnit + kEnd : 0;
     P[i + 1] = nb;
     mine += nb;
   }
@@ -195,7 +201,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (tid == 0) a.prefix[n + 1] = per;
   }
   const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
-  const int count = end > begin ? (int)(end - begin) : 0;
+  int count = end > begin ? (int)(end - begin) : 0;  // units of the run, from the one at cu on
 
   Cursor cu{0, 0, 0, 0};
   if (count > 0) {
@@ -209,22 +215,26 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int r = (int)(begin - (long long)P[lo] * HR);
     cu.hr = r / cu.nb;
     cu.b = r % cu.nb;
+    if (cu.b < kEnd) {  // the run starts among a segment's empty units
+      count -= kEnd - cu.b;
+      cu.b = kEnd;
+    }
   }
 
   if (warp == kWarps) {
-    if (lane == 0 && count > 0) {
+    if (lane == 0) {
       // -------------------------------------------------------------- loads
       int stage = 0, slot = 0, len = 0, cur = -1;
       uint32_t phase = 0, filled = 0, fill_phase = 0;
       const int box = min(c.page_size, kUnit);
-      for (int x = 0; x < count; ++x, advance(cu, P, n, HR)) {
+      for (int left = count; left > 0; left -= advance(cu, P, n, HR)) {
         if (cu.i != cur) {
           cur = cu.i;
           slot = a.d.slots[cur];
           len = c.lens[slot];
         }
         if (!wait_or_abort(bar(EMPTY + stage), phase ^ 1u, a.d.timeout_ns, abort_flag, a.d.status, 62)) break;
-        const int key = a.d.shared + cu.b * kUnit, rows = min(kUnit, (len - key + kKeys - 1) & ~(kKeys - 1));
+        const int key = a.d.shared + (cu.b - kEnd) * kUnit, rows = min(kUnit, (len - key + kKeys - 1) & ~(kKeys - 1));
         const uint32_t dst = base + stage * 2 * C::kHalf, b = bar(FULL + stage);
         mbar_arrive_expect_tx(b, 2u * (uint32_t)(rows * DP * 2));
         for (int r = 0; r < rows;) {
@@ -268,27 +278,40 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const float c2 = a.d.scale * 1.4426950408889634f, thr = 8.0f / c2;
     const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, group = warp >> 2;
     const int mi = lane >> 3, l8 = lane & 7;
-    uint32_t q[KS][NT][2];
+    uint32_t q[KS][NT][2], qn[KS][NT][2];
     float o[KS][NT][4], m[NT][2], l[NT][2];
-    int cur_i = -1, cur_hr = -1, len = 0;
-    int stage = 0;
+    int len = 0, len_n = 0;
+    int stage = 0, x = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int x = 0; x < count; ++x) {
-      if (cu.i != cur_i || cu.hr != cur_hr) {  // a new segment: its rows as B fragments
-        if (cu.i != cur_i) len = c.lens[a.d.slots[cu.i]];
-        cur_i = cu.i;
-        cur_hr = cu.hr;
-        const int hk = cu.hr / a.RG, r0 = (cu.hr % a.RG) * C::kRows, nr = min(a.R, G - r0);
-        const __nv_bfloat16* qp = (const __nv_bfloat16*)a.d.q + (long long)cu.i * a.d.qs + (long long)(hk * G + r0) * D;
+    // the rows of the segment at `at`, as B fragments
+    auto fetch = [&](const Cursor& at) {
+      len_n = c.lens[a.d.slots[at.i]];
+      const int hk = at.hr / a.RG, r0 = (at.hr % a.RG) * C::kRows, nr = min(a.R, G - r0);
+      const __nv_bfloat16* qp = (const __nv_bfloat16*)a.d.q + (long long)at.i * a.d.qs + (long long)(hk * G + r0) * D;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * t + g, col = 16 * k + 2 * t4 + 8 * e;
+            qn[k][t][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
+          }
+    };
+    bool fresh = true;
+    if (count > 0) fetch(cu);
+    for (int run = count; run > 0; ++x) {
+      if (fresh) {
+        fresh = false;
+        len = len_n;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int row = 8 * t + g, col = 16 * k + 2 * t4 + 8 * e;
-              q[k][t][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
+              q[k][t][e] = qn[k][t][e];
               o[k][t][2 * e] = o[k][t][2 * e + 1] = 0.f;
             }
 #pragma unroll
@@ -299,7 +322,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       if ((x & 1) == group) {
         if (ok) ok = warp_wait(bar(FULL + stage), phase, a.d.timeout_ns, abort_flag, a.d.status, 61);
-        const int left = len - (a.d.shared + cu.b * kUnit + quarter * kKeys);  // keys of this warp's 16
+        const int left = len - (a.d.shared + (cu.b - kEnd) * kUnit + quarter * kKeys);  // keys of this warp's 16
         if (ok && left > 0) {
           const uint32_t sk = base + stage * 2 * C::kHalf + quarter * (kKeys * 128), sv = sk + C::kHalf;
           if (left < kKeys) {  // positions past the end hold anything: zero their values
@@ -376,9 +399,11 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
 
       const Cursor was = cu;
-      advance(cu, P, n, HR);
-      if (x + 1 < count && cu.i == was.i && cu.hr == was.hr) continue;
-      // ---- the segment (or the run) ends: the eight warps' parts become one piece
+      run -= advance(cu, P, n, HR);
+      if (run > 0 && cu.i == was.i && cu.hr == was.hr) continue;
+      // ---- the segment (or the run) ends: the eight warps' parts become one piece, while the next rows are on their way
+      fresh = true;
+      if (run > 0) fetch(cu);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -453,7 +478,7 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
   int own = 0;
   long long p0 = 0;
   if (valid && b > 0) {
-    const long long start = (long long)b0 * HR + (long long)hr * b, last = start + b - 1;
+    const long long start = (long long)b0 * HR + (long long)hr * b + kEnd, last = start + (b - kEnd) - 1;
     int c0, c1;
     if (last < (1ll << 31)) { c0 = (int)start / per; c1 = (int)last / per; }
     else { c0 = (int)(start / per); c1 = (int)(last / per); }
