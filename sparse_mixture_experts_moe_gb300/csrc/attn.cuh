@@ -114,6 +114,36 @@ __device__ __forceinline__ Seq load_seq(const PromptArgs& a, int i) {
   }
   return s;
 }
+// The same by a warp: 32 places a step, and the four offsets in one load.
+__device__ __forceinline__ int find_tile_seq_warp(const int32_t* qo, int n, int G, int R, long long s) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;  // the answer is in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 31) / 32, i = lo + lane * step;
+    const bool at = lane * step < len && (long long)qo[i] * G / R + i <= s;
+    const int k = __popc(__ballot_sync(0xffffffffu, at)) - 1;  // (the first place always is, but for bad offsets)
+    const int skip = (k < 0 ? 0 : k) * step;
+    lo += skip;
+    len = len - skip < step ? len - skip : step;
+  }
+  return lo;
+}
+__device__ __forceinline__ Seq load_seq_warp(const PromptArgs& a, int i) {
+  const int lane = threadIdx.x & 31;
+  const int v = (lane & 2 ? a.ko : a.qo)[i + (lane & 1)];
+  Seq s;
+  s.q0 = __shfl_sync(0xffffffffu, v, 0);
+  s.k0 = __shfl_sync(0xffffffffu, v, 2);
+  const int q1 = __shfl_sync(0xffffffffu, v, 1), k1 = __shfl_sync(0xffffffffu, v, 3);
+  s.nq = q1 - s.q0;
+  s.nk = k1 - s.k0;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || s.k0 < 0 || k1 < s.k0 || k1 > a.Tkv) {
+    if (threadIdx.x == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
+    s.nq = 0;
+    s.nk = 0;
+  }
+  return s;
+}
 // Keys that query token t sees.
 __device__ __forceinline__ int visible_keys(int t, int nq, int nk, int causal) {
   if (!causal) return nk;

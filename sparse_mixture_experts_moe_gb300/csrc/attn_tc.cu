@@ -152,41 +152,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
   // (the shuffle tells the compiler that the warp number is the same in all lanes)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  griddep_wait();
-
-  // ---- the CTA's rows and keys
-  const int H = SHARED ? sa.d.H : pa.H, Hkv = SHARED ? sa.d.c.Hkv : pa.Hkv, D = SHARED ? sa.d.c.D : pa.D;
-  const int G = H / Hkv;
-  int* status = SHARED ? sa.d.status : pa.status;
-  const uint64_t timeout_ns = SHARED ? sa.d.timeout_ns : pa.timeout_ns;
-  int hk, row0, nrows;        // packed rows row0 .. row0 + nrows - 1 of the sequence (or batch)
-  int key0 = 0, n_keys;       // keys of this CTA
-  int lim_t[2];               // keys that each tile's last row sees (relative to key0)
-  Seq sq{0, 0, 0, 0};
-  if (SHARED) {
-    hk = blockIdx.x;
-    row0 = blockIdx.y * 2 * TM;
-    nrows = min(2 * TM, sa.d.n * G - row0);
-    key0 = blockIdx.z * sa.per;
-    n_keys = min(sa.per, sa.d.shared - key0);
-    lim_t[0] = n_keys;
-    lim_t[1] = nrows > TM ? n_keys : 0;
-  } else {
-    hk = blockIdx.x % Hkv;
-    const int slot = n_slots - 1 - (int)(blockIdx.x / Hkv);
-    const int i = find_tile_seq(pa.qo, pa.n, G, 2 * TM, slot);
-    sq = load_seq(pa, i);
-    const long long r0 = ((long long)slot - ((long long)sq.q0 * G / (2 * TM) + i)) * (2 * TM);
-    if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
-    row0 = (int)r0;
-    nrows = min(2 * TM, sq.nq * G - row0);
-    key0 = 0;
-    lim_t[0] = visible_keys((row0 + min(nrows, TM) - 1) / G, sq.nq, sq.nk, pa.causal);
-    lim_t[1] = nrows > TM ? visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, pa.causal) : 0;
-    n_keys = max(lim_t[0], lim_t[1]);
-  }
-  const int nb0 = (lim_t[0] + BK - 1) / BK, nb1 = (lim_t[1] + BK - 1) / BK, nb = max(nb0, nb1);
-
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(bar(FULL + s), 1); mbar_init(bar(EMPTY + s), 1); }
     for (int t = 0; t < 2; ++t) {
@@ -208,9 +173,44 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Only now: a dependent kernel that starts on this SM may allocate TMEM before it waits for this grid.
-  griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  // Only after TMEM is allocated: a dependent kernel that starts on this SM may allocate some before it waits for this
+  // grid. And only after the wait: the decode's own-key kernel relies on everything before this grid being done.
+  griddep_launch_dependents();
+
+  // ---- the CTA's rows and keys
+  const int H = SHARED ? sa.d.H : pa.H, Hkv = SHARED ? sa.d.c.Hkv : pa.Hkv, D = SHARED ? sa.d.c.D : pa.D;
+  const int G = H / Hkv;
+  int* status = SHARED ? sa.d.status : pa.status;
+  const uint64_t timeout_ns = SHARED ? sa.d.timeout_ns : pa.timeout_ns;
+  int hk, row0, nrows;        // packed rows row0 .. row0 + nrows - 1 of the sequence (or batch)
+  int key0 = 0, n_keys;       // keys of this CTA
+  int lim_t[2];               // keys that each tile's last row sees (relative to key0)
+  Seq sq{0, 0, 0, 0};
+  if (SHARED) {
+    hk = blockIdx.x;
+    row0 = blockIdx.y * 2 * TM;
+    nrows = min(2 * TM, sa.d.n * G - row0);
+    key0 = blockIdx.z * sa.per;
+    n_keys = min(sa.per, sa.d.shared - key0);
+    lim_t[0] = n_keys;
+    lim_t[1] = nrows > TM ? n_keys : 0;
+  } else {
+    hk = blockIdx.x % Hkv;
+    const int slot = n_slots - 1 - (int)(blockIdx.x / Hkv);
+    const int i = find_tile_seq_warp(pa.qo, pa.n, G, 2 * TM, slot);
+    sq = load_seq_warp(pa, i);
+    const long long r0 = ((long long)slot - ((long long)sq.q0 * G / (2 * TM) + i)) * (2 * TM);
+    const bool none = r0 < 0 || r0 >= (long long)sq.nq * G;  // a slot that no tile fills
+    row0 = none ? 0 : (int)r0;
+    nrows = none ? 0 : min(2 * TM, sq.nq * G - row0);
+    key0 = 0;
+    lim_t[0] = none ? 0 : visible_keys((row0 + min(nrows, TM) - 1) / G, sq.nq, sq.nk, pa.causal);
+    lim_t[1] = nrows > TM ? visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, pa.causal) : 0;
+    n_keys = max(lim_t[0], lim_t[1]);
+  }
+  const int nb0 = (lim_t[0] + BK - 1) / BK, nb1 = (lim_t[1] + BK - 1) / BK, nb = max(nb0, nb1);
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // all four warps of the group, 10 and 11 idle
@@ -355,35 +355,40 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const int q4 = warp & 3;                     // TMEM lanes 32 q4 ..
     const int nrow_t = min(TM, nrows - t * TM);  // rows of this tile (<= 0: none)
     const int n = t ? nb1 : nb0;
-    // Q tile to shared memory as the swizzled K-major operand, zeros past the rows and past D
+    const int R = row0 + t * TM + r;
+    const bool valid = r < nrow_t;
+    const int tok = valid ? R / G : 0, h = hk * G + (valid ? R % G : 0);
+    // Q tile to shared memory as the swizzled K-major operand, zeros past the rows and past D: each warp its 32 rows,
+    // kLanes lanes a row, every load in flight before the first store
+    constexpr int kLanes = DP / 8, kIter = kLanes;  // 32 rows / (32 / kLanes) rows a step
     if (n > 0) {
-      constexpr int U = DP / 8;
-      const __nv_bfloat16* qbase = (const __nv_bfloat16*)(SHARED ? sa.d.q : pa.q);
-      const long long qs = SHARED ? sa.d.qs : pa.qs;
-#pragma unroll 4
-      for (int i = r; i < TM * U; i += 128) {
-        const int rr = i / U, u = i % U;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (rr < nrow_t && u * 8 < D) {
-          const int R = row0 + t * TM + rr, tok = R / G, h = hk * G + R % G;
-          x = *reinterpret_cast<const uint4*>(qbase + (long long)((SHARED ? 0 : sq.q0) + tok) * qs + (long long)h * D + u * 8);
-        }
+      const __nv_bfloat16* qrow = (const __nv_bfloat16*)(SHARED ? sa.d.q : pa.q) +
+                                  (long long)((SHARED ? 0 : sq.q0) + tok) * (SHARED ? sa.d.qs : pa.qs) + (long long)h * D;
+      uint4 x[kIter];
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int rr = i * (32 / kLanes) + lane / kLanes, u = lane % kLanes;
+        const __nv_bfloat16* src = (const __nv_bfloat16*)__shfl_sync(0xffffffffu, (unsigned long long)qrow, rr);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (32 * q4 + rr < nrow_t && u * 8 < D) x[i] = *reinterpret_cast<const uint4*>(src + u * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int rr = 32 * q4 + i * (32 / kLanes) + lane / kLanes, u = lane % kLanes;
         const uint32_t dst = sQ + t * C::kTileBytes + (u / 8) * (TM * 128) + rr * 128 + (((u & 7) ^ (rr & 7)) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w)
                      : "memory");
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(QFULL + t));
     }
-    const int R = row0 + t * TM + r;
-    const bool valid = r < nrow_t;
     int lim = 0;
     if (valid && SHARED) {  // a slot shorter than the shared keys sees its own length of them
-      const int slot = sa.d.slots[R / G];
+      const int slot = sa.d.slots[tok];
       lim = slot < 0 || slot >= sa.d.c.n_slots ? 0 : max(0, min(n_keys, sa.d.c.lens[slot] - key0));
     } else if (valid) {
-      lim = visible_keys(R / G, sq.nq, sq.nk, pa.causal);
+      lim = visible_keys(tok, sq.nq, sq.nk, pa.causal);
     }
     const float c2 = (SHARED ? sa.d.scale : pa.scale) * 1.4426950408889634f;
     const float thr = kRescale / c2;
@@ -482,7 +487,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       tc_fence_after();
     }
     if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-      const int tok = R / G, h = hk * G + R % G;
       if (SHARED) {
         const long long piece = ((long long)tok * H + h) * sa.splits + blockIdx.z;
         bool fine = true;
@@ -512,8 +516,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         while (again != 0) {
           const int w = __ffs(again) - 1;
           again &= again - 1;
-          const int Rw = __shfl_sync(0xffffffffu, R, w), limw = __shfl_sync(0xffffffffu, lim, w);
-          const int tw = Rw / G, hw = hk * G + Rw % G;
+          const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
+          const int limw = __shfl_sync(0xffffffffu, lim, w);
           const CacheView& cv = sa.d.c;
           const int32_t* row = cv.table + (long long)sa.d.slots[tw] * cv.width;
           float o[4], mw, lw;
@@ -534,7 +538,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
       } else {
         const float inv = l == 0.f ? 0.f : 1.0f / l;
-        __nv_bfloat16* dst = (__nv_bfloat16*)pa.out + (long long)(sq.q0 + tok) * pa.os + (long long)h * D;
+        // the rows go through this warp's part of the Q tile (its last QK is done), so that whole rows are stored at once
+        __nv_bfloat16* orow = (__nv_bfloat16*)pa.out + (long long)(sq.q0 + tok) * pa.os + (long long)h * D;
+        const uint32_t stg = sQ + t * C::kTileBytes + 32 * q4 * (DP * 2);
         bool fine = true;
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
@@ -543,25 +549,31 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             tmem_ld_32x32b_x32(tO + 32 * c, o);
             tmem_ld_wait();
           }
-          if (lim == 0)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+            o[i] = lim == 0 ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
             fine = fine && fabsf(__uint_as_float(o[i])) <= 3.0e38f;
           }
-          if (valid)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (32 * c + 8 * i < D) {
-                uint4 x;
-                x.x = pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]));
-                x.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
-                x.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
-                x.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
-                *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = x;
-              }
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t dst = stg + lane * (DP * 2) + (((4 * c + i) ^ (lane & 7)) * 16);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                         "r"(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]))),
+                         "r"(pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]))),
+                         "r"(pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]))),
+                         "r"(pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])))
+                         : "memory");
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int rr = i * (32 / kLanes) + lane / kLanes, u = lane % kLanes;
+          __nv_bfloat16* dst = (__nv_bfloat16*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr);
+          uint4 x;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                       : "r"(stg + rr * (DP * 2) + ((u ^ (rr & 7)) * 16)) : "memory");
+          if (32 * q4 + rr < nrow_t && u * 8 < D) *reinterpret_cast<uint4*>(dst + u * 8) = x;
         }
         if (valid && pa.lse != nullptr)
           pa.lse[(long long)(sq.q0 + tok) * H + h] = lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
@@ -569,8 +581,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         while (again != 0) {
           const int w = __ffs(again) - 1;
           again &= again - 1;
-          const int Rw = __shfl_sync(0xffffffffu, R, w), limw = __shfl_sync(0xffffffffu, lim, w);
-          const int tw = Rw / G, hw = hk * G + Rw % G;
+          const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
+          const int limw = __shfl_sync(0xffffffffu, lim, w);
           float o[4], mw, lw;
           exact_row((const __nv_bfloat16*)pa.q + (long long)(sq.q0 + tw) * pa.qs + (long long)hw * D,
                     (const __nv_bfloat16*)pa.k + (long long)sq.k0 * pa.ks + (long long)hk * D,
