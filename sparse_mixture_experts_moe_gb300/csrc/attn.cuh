@@ -65,6 +65,7 @@ struct CacheWs {
   int32_t* claim_d;  // [n_slots] zero between calls: which entry names the slot (as dst)
   int32_t* claim_s;  // [n_slots] zero between calls: the slot is a source
   int4* entry;       // [n_slots]
+  int4* entry2;      // [n_slots]
   int32_t* freel;    // [n_pages] pages found free, ascending
   int2* copies;      // [max(n_slots, n_pages)] (src, dst) pages
   int32_t* map;      // [n_pages] where a moved page went

@@ -30,7 +30,7 @@ bool cache_sizes_ok(const moe_kv_cache* c) {
   if (c == nullptr || !dtype_ok(c->dt) || !heads_ok(c->H_kv, c->H_kv, c->D)) return false;
   if (c->n_layers < 1 || c->n_layers > 4096 || c->n_pages < 1 || c->n_pages >= (1 << 30)) return false;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return false;
-  if (c->n_slots < 1 || c->table_width < 1 || (long long)c->n_slots * c->table_width >= (1ll << 31)) return false;
+  if (c->n_slots < 1 || c->n_slots >= (1 << 30) || c->table_width < 1 || (long long)c->n_slots * c->table_width >= (1ll << 31)) return false;
   if ((long long)c->table_width * c->page_size >= (1ll << 31)) return false;
   // the rows of a layer are numbered with 32 bits
   return (long long)c->n_pages * c->H_kv * c->page_size < (1ll << 31);
@@ -50,7 +50,7 @@ CacheView view_of(const moe_kv_cache* c) {
 }
 
 struct CacheLayout {
-  size_t claim_d, claim_s, counts, zeroed, entry, freel, copies, map, end;
+  size_t claim_d, claim_s, counts, zeroed, entry, entry2, freel, copies, map, end;
   explicit CacheLayout(const moe_kv_cache* c) {
     const size_t slots = c->n_slots, pages = c->n_pages;
     size_t o = align256(kWsHeaderBytes);
@@ -59,6 +59,7 @@ struct CacheLayout {
     counts = o; o += 256;
     zeroed = o;  // everything up to here starts at zero
     entry = o; o += align256(slots * 16);
+    entry2 = o; o += align256(slots * 16);
     freel = o; o += align256(pages * 4);
     copies = o; o += align256((slots > pages ? slots : pages) * 8);
     map = o; o += align256(pages * 4);
@@ -74,6 +75,7 @@ CacheWs cache_ws(const moe_kv_cache* c, void* ws) {
   w.claim_s = reinterpret_cast<int32_t*>(b + L.claim_s);
   w.counts = reinterpret_cast<int32_t*>(b + L.counts);
   w.entry = reinterpret_cast<int4*>(b + L.entry);
+  w.entry2 = reinterpret_cast<int4*>(b + L.entry2);
   w.freel = reinterpret_cast<int32_t*>(b + L.freel);
   w.copies = reinterpret_cast<int2*>(b + L.copies);
   w.map = reinterpret_cast<int32_t*>(b + L.map);

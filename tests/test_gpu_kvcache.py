@@ -157,7 +157,7 @@ def test_clear():
     assert (c.table == -1).all() and (c.lens == 0).all() and (c.refs == 0).all()
 
 
-@pytest.mark.parametrize("pages,slots,width", [(5000, 1500, 3), (9000, 40, 700), (70000, 64, 40)])
+@pytest.mark.parametrize("pages,slots,width", [(5000, 1500, 3), (9000, 40, 700), (70000, 64, 40), (24000, 100, 400)])
 def test_large_tables(pages, slots, width):
     """More pages and slots than the table kernels handle in one step."""
     c, m = pair(layers=1, pages=pages, slots=slots, width=width, Hk=1, D=8)
