@@ -433,7 +433,14 @@ typedef struct {
   int n_layers, n_pages, page_size; /* page_size 16, 32, 64, 128 or 256 */
   int n_slots, table_width, H_kv, D;
   moe_dtype dt;
+  const void* plan; /* NULL, or host memory that moe_cache_plan wrote for this cache */
 } moe_kv_cache;
+
+/* moe_cache_plan — writes what moe_attention_decode otherwise prepares in every call (the copy descriptors of a bf16
+ * cache's pages, for all layers) to `plan`, moe_cache_plan_bytes() bytes of host memory. It holds for the k, v and
+ * sizes of `cache`: a call whose cache differs from its plan's is MOE_ERR_INVALID_ARG. Needs a GPU. */
+size_t moe_cache_plan_bytes(void);
+moe_status moe_cache_plan(const moe_kv_cache* cache, void* plan, size_t bytes);
 
 /* Scratch for the calls below on this cache (0 on bad sizes). moe_cache_workspace_init prepares it, once;
  * moe_cache_clear empties the cache (every slot length 0, every page free). The status word of the

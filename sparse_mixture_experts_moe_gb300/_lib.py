@@ -77,6 +77,8 @@ SIGNATURES = {
                              _sz, _p],
     "moe_attention_workspace_bytes": [_i, _i, _i],
     "moe_attention_decode": [_p, _i, _p, _p, _i, _i, _i64, _i64, _i, _f, _p, _p, _p, _sz, _p],
+    "moe_cache_plan_bytes": [],
+    "moe_cache_plan": [_p, _p, _sz],
     "moe_cache_workspace_bytes": [_p],
     "moe_cache_workspace_init": [_p, _p, _sz, _p],
     "moe_cache_clear": [_p, _p],
@@ -88,7 +90,8 @@ SIGNATURES = {
 }
 _RESTYPES = {"moe_workspace_bytes": ctypes.c_size_t, "moe_status_string": ctypes.c_char_p,
              "moe_qweight_bytes": ctypes.c_size_t, "moe_qscale_bytes": ctypes.c_size_t,
-             "moe_attention_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t}
+             "moe_attention_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t,
+             "moe_cache_plan_bytes": ctypes.c_size_t}
 
 _LIB = None
 

@@ -17,10 +17,12 @@ done by the library's kernels.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 from . import _lib
 from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
+
+
+_PROMPT_WORKSPACE = 256  # moe_attention_prompt: the status word alone
 
 
 class _Cache(ctypes.Structure):
@@ -28,7 +30,7 @@ class _Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
                 ("refs", ctypes.c_void_p), ("n_layers", ctypes.c_int), ("n_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("n_slots", ctypes.c_int), ("table_width", ctypes.c_int),
-                ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("dt", ctypes.c_int)]
+                ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("dt", ctypes.c_int), ("plan", ctypes.c_void_p)]
 
 
 # The checks below run on every call, where a decode step's kernels take a few microseconds: each looks at a
@@ -48,31 +50,32 @@ def _heads(t, name, heads, dim, dtype, dev):
     return T, (st if T > 1 else heads * dim)
 
 
-def _ints(t, name, n, dev):
+def _ints(t, name, n, dev, i32):
     """Checks an int32 index tensor of n entries (None: any number) on CUDA device `dev`; returns its length."""
     shape = t.shape
-    if len(shape) != 1 or t.dtype is not _int32() or t.get_device() != dev or not t.is_contiguous():
+    if len(shape) != 1 or t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"moe: {name} must be a contiguous one-dimensional int32 tensor on cuda:{dev}")
     if n is not None and shape[0] != n:
         raise ValueError(f"moe: {name} has {shape[0]} entries; the call needs {n}")
     return shape[0]
 
 
-def _stream_of(stream, dev):
-    """The stream's handle; None: the device's current one (its handle alone, without a stream object around it)."""
-    return _raw_stream()(dev) if stream is None else _stream(stream)
+class _Bound:
+    """What the classes below look up once, not in every call."""
 
+    def __init__(self):
+        import torch
+        self._lib = _lib.lib()
+        self._i32 = torch.int32
+        self._f32 = torch.float32
+        self._empty = torch.empty
+        # the current stream's handle alone, without a stream object around it
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._ws = _Workspaces()
 
-@functools.lru_cache(None)
-def _int32():
-    import torch
-    return torch.int32
-
-
-@functools.lru_cache(None)
-def _raw_stream():
-    import torch
-    return torch._C._cuda_getCurrentRawStream
+    def device_status(self):
+        """(status, detail) of the first device-side error since the last call; synchronises."""
+        return self._ws.status()
 
 
 class _Workspaces:
@@ -108,7 +111,7 @@ class _Workspaces:
         return MOE_OK, 0
 
 
-class KVCache:
+class KVCache(_Bound):
     """A paged key/value cache over tensors that the caller owns: k, v [layers, pages, kv_heads, page_size,
     head_dim] (bf16 or fp32), table [slots, width], lens [slots], refs [pages] (int32). KVCache.create
     allocates an empty one."""
@@ -132,12 +135,16 @@ class KVCache:
         self._c = _Cache(_ptr(k), _ptr(v), _ptr(table), _ptr(lens), _ptr(refs), self.n_layers, self.n_pages,
                          self.page_size, self.n_slots, self.width, self.kv_heads, self.head_dim, self.dt)
         self._ref = ctypes.addressof(self._c)
-        self._lib = _lib.lib()
+        super().__init__()
         self._bytes = int(self._lib.moe_cache_workspace_bytes(self._ref))
         if self._bytes == 0:
             raise MoeError(MOE_ERR_INVALID_ARG, "moe_cache_workspace_bytes")
-        self._ws = _Workspaces()
         self._dev = k.get_device()
+        self._key = (self.kv_heads, self.head_dim, self.dtype)
+        n = int(self._lib.moe_cache_plan_bytes())
+        self._plan = ctypes.create_string_buffer(n)
+        _check(self._lib.moe_cache_plan(self._ref, ctypes.addressof(self._plan), n), "moe_cache_plan")
+        self._c.plan = ctypes.addressof(self._plan)
 
     @classmethod
     def create(cls, n_layers, n_pages, page_size, n_slots, max_len, kv_heads, head_dim, dtype, device="cuda"):
@@ -154,13 +161,14 @@ class KVCache:
 
     def clear(self, stream=None):
         """Empties every slot and frees every page."""
-        _check(self._lib.moe_cache_clear(self._ref, _stream_of(stream, self._dev)), "moe_cache_clear")
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        _check(self._lib.moe_cache_clear(self._ref, s), "moe_cache_clear")
 
     def resize(self, slots, new_lens, stream=None):
         """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
-        n = _ints(slots, "slots", None, self._dev)
-        _ints(new_lens, "new_lens", n, self._dev)
-        s = _stream_of(stream, self._dev)
+        n = _ints(slots, "slots", None, self._dev, self._i32)
+        _ints(new_lens, "new_lens", n, self._dev, self._i32)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_resize")
@@ -172,51 +180,46 @@ class KVCache:
         tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, self._dev)
         if tv != total:
             raise ValueError(f"moe: k has {total} tokens, v has {tv}")
-        n = _ints(slots, "slots", None, self._dev)
-        _ints(offsets, "offsets", n + 1, self._dev)
-        _ints(pos, "pos", n, self._dev)
-        s = _stream_of(stream, self._dev)
+        n = _ints(slots, "slots", None, self._dev, self._i32)
+        _ints(offsets, "offsets", n + 1, self._dev, self._i32)
+        _ints(pos, "pos", n, self._dev, self._i32)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
                                          k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
-        n = _ints(src, "src", None, self._dev)
-        _ints(dst, "dst", n, self._dev)
-        s = _stream_of(stream, self._dev)
+        n = _ints(src, "src", None, self._dev, self._i32)
+        _ints(dst, "dst", n, self._dev, self._i32)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
 
     def compact(self, n_live=None, stream=None):
         """Moves the pages in use to the pool's lowest page numbers; returns their number, a one-entry int32
         tensor (n_live, if given)."""
-        import torch
         if n_live is None:
             if stream is not None:
                 raise ValueError("moe: pass n_live with an explicit stream")
-            n_live = torch.empty(1, dtype=torch.int32, device=self._dev)
-        _ints(n_live, "n_live", 1, self._dev)
-        s = _stream_of(stream, self._dev)
+            n_live = self._empty(1, dtype=self._i32, device=self.device)
+        _ints(n_live, "n_live", 1, self._dev, self._i32)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
         return n_live
 
     def copy_pages(self, src, dst, stream=None):
         """Page dst[i] gets page src[i]'s contents in every layer."""
-        n = _ints(src, "src", None, self._dev)
-        _ints(dst, "dst", n, self._dev)
-        s = _stream_of(stream, self._dev)
+        n = _ints(src, "src", None, self._dev, self._i32)
+        _ints(dst, "dst", n, self._dev, self._i32)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_copy_pages")
 
-    def device_status(self):
-        """(status, detail) of the first device-side error since the last call; synchronises."""
-        return self._ws.status()
 
-
-class Attention:
+class Attention(_Bound):
     """Attention of `heads` query heads over `kv_heads` key/value heads of head_dim elements. Holds a workspace."""
 
     def __init__(self, heads, kv_heads, head_dim, dtype, scale=None):
@@ -229,9 +232,9 @@ class Attention:
                 or not 8 <= self.head_dim <= 256):
             raise ValueError("Attention: heads must be a multiple of kv_heads, head_dim a multiple of 8 from 8 to 256")
         self.scale = float(scale) if scale is not None else self.head_dim ** -0.5
-        self._lib = _lib.lib()
+        super().__init__()
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
-        self._ws = _Workspaces()
+        self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
 
     def _workspace(self, stream, n, dev):
@@ -245,18 +248,16 @@ class Attention:
 
     def _out(self, q, out, lse, stream, dev):
         if out is None:
-            import torch
             if stream is not None:  # a tensor made here belongs to the current stream
                 raise ValueError("moe: pass out with an explicit stream")
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = self._empty(q.shape, dtype=self.dtype, device=q.device)
             so = self.heads * self.head_dim
         else:
             to, so = _heads(out, "out", self.heads, self.head_dim, self.dtype, dev)
             if to != q.shape[0]:
                 raise ValueError(f"moe: expected out {tuple(q.shape)}, got {tuple(out.shape)}")
         if lse is not None:
-            import torch
-            if (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.get_device() != dev
+            if (lse.shape != q.shape[:2] or lse.dtype is not self._f32 or lse.get_device() != dev
                     or not lse.is_contiguous()):
                 raise ValueError(f"moe: expected lse {tuple(q.shape[:2])}, float32, contiguous, on {q.device}")
         return out, so
@@ -274,14 +275,14 @@ class Attention:
         Tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, dev)
         if Tv != Tk or (kv_offsets is None and Tk != Tq):
             raise ValueError(f"moe: k has {Tk} tokens, v has {Tv}, q has {Tq}")
-        n = _ints(q_offsets, "q_offsets", None, dev) - 1
+        n = _ints(q_offsets, "q_offsets", None, dev, self._i32) - 1
         if n < 0:
             raise ValueError("moe: q_offsets has one entry more than there are sequences")
         if kv_offsets is not None:
-            _ints(kv_offsets, "kv_offsets", n + 1, dev)
+            _ints(kv_offsets, "kv_offsets", n + 1, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
-        s = _stream_of(stream, dev)
-        ws = self._workspace(s, 0, dev)
+        s = self._raw_stream(dev) if stream is None else _stream(stream)
+        ws = self._ws.get(s, _PROMPT_WORKSPACE, dev)
         _check(self._prompt(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
             None if kv_offsets is None else kv_offsets.data_ptr(), n, Tq, Tk, self.heads, self.kv_heads, self.head_dim,
@@ -294,19 +295,15 @@ class Attention:
         shared_len: how many first positions of all n slots are the same pages (a multiple of the page size),
         read once for the whole batch."""
         dev = cache._dev
-        if cache.kv_heads != self.kv_heads or cache.head_dim != self.head_dim or cache.dtype is not self.dtype:
+        if cache._key != self._key:
             raise ValueError(f"moe: the cache holds {cache.kv_heads} heads of {cache.head_dim} in {cache.dtype}, the "
                              f"attention {self.kv_heads} of {self.head_dim} in {self.dtype}")
         n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
-        _ints(slots, "slots", n, dev)
+        _ints(slots, "slots", n, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
-        s = _stream_of(stream, dev)
+        s = self._raw_stream(dev) if stream is None else _stream(stream)
         ws = self._workspace(s, n, dev)
         _check(self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
                             out.data_ptr(), None if lse is None else lse.data_ptr(), ws[2], ws[1], s),
                "moe_attention_decode")
         return out
-
-    def device_status(self):
-        """(status, detail) of the first device-side error since the last call; synchronises."""
-        return self._ws.status()

@@ -1,7 +1,10 @@
 // Shared declarations of the attention and cache kernels (internal to the library).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "common.cuh"
 
@@ -30,6 +33,25 @@ struct CacheView {
   long long layer_elems() const { return (long long)n_pages * Hkv * page_size * D; }
 };
 
+// Copy descriptors of a bf16 cache's pages: a layer's page rows ((page H_kv + head) page_size + row) x D, the layer as
+// the third coordinate; boxes of 64 elements x 16, min(page_size, 64) and min(page_size, 128) rows.
+struct CacheMaps {
+  CUtensorMap k16, v16, k64, v64, k128, v128;
+};
+bool encode_cache_maps(const CacheView& c, CacheMaps* m);
+
+// Sets a kernel's dynamic shared memory limit, once a device: the last device it was set for is remembered (setting it
+// again is harmless, so a race between threads is too).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kern, size_t bytes, std::atomic<int>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || done.load(std::memory_order_relaxed) == dev + 1) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.store(dev + 1, std::memory_order_relaxed);
+  return e;
+}
+
 struct DecodeArgs {
   const void* q;
   long long qs, os;
@@ -38,6 +60,7 @@ struct DecodeArgs {
   float scale;
   CacheView c;
   const void *k, *v;  // the layer's pages
+  int layer;
   void* out;
   float* lse;
   float* part;  // partial results, see PartView
@@ -54,10 +77,11 @@ constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
 cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);
 // bf16, D <= 128, at least one key.
 cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s);
-cudaError_t launch_attn_decode_tc(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_attn_decode_tc(const DecodeArgs& a, const CacheMaps& m, cudaStream_t s);
 // The shared keys of a decode batch: `splits` pieces of every row, part_o [(sequence, head)][splits][D] unnormalised.
 int attn_shared_splits(const DecodeArgs& a);
-cudaError_t launch_attn_shared_tc(const DecodeArgs& a, int splits, float* part_o, float2* part_ml, cudaStream_t s);
+cudaError_t launch_attn_shared_tc(const DecodeArgs& a, const CacheMaps& m, int splits, float* part_o, float2* part_ml,
+                                  cudaStream_t s);
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
 
 struct CacheWs {

@@ -1,6 +1,7 @@
 // C ABI of the attention and cache operators (include/moe.h): host-side validation, workspace layout and
 // the choice of kernel. As in api.cu, every argument is checked before any CUDA call.
 #include <cmath>
+#include <cstring>
 
 #include "attn.cuh"
 #include "kernels.cuh"
@@ -85,6 +86,18 @@ bool cache_call_ok(const moe_kv_cache* c, const void* ws, size_t ws_bytes) {
   return cache_ok(c) && workspace_ok(ws, ws_bytes, CacheLayout(c).end);
 }
 
+// What moe_cache_plan writes: the descriptors, and the cache that they describe.
+struct CachePlan {
+  CacheMaps maps;
+  const void *k, *v;
+  int n_layers, n_pages, page_size, H_kv, D;
+};
+bool plan_holds(const CachePlan& p, const moe_kv_cache* c) {
+  return p.k == c->k && p.v == c->v && p.n_layers == c->n_layers && p.n_pages == c->n_pages &&
+         p.page_size == c->page_size && p.H_kv == c->H_kv && p.D == c->D;
+}
+bool planned(const moe_kv_cache* c) { return c->dt == MOE_DTYPE_BF16 && c->D <= 128; }
+
 size_t decode_ws_bytes(int n, int H, int D) {
   return align256(kWsHeaderBytes) + align256((size_t)decode_pieces((long long)n * H) * (D + 2) * 4);
 }
@@ -166,11 +179,35 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(kWsHeaderBytes));
   a.status = static_cast<int*>(workspace);
   a.timeout_ns = wait_timeout_ns();
-  if (cache->dt == MOE_DTYPE_BF16 && cache->D <= 128) {
-    bind_primary_context();
-    return cuda_status(launch_attn_decode_tc(a, (cudaStream_t)stream));
+  a.layer = layer;
+  if (planned(cache)) {
+    CachePlan p;
+    if (cache->plan != nullptr) {
+      std::memcpy(&p, cache->plan, sizeof(p));
+      if (!plan_holds(p, cache)) return MOE_ERR_INVALID_ARG;
+    } else {
+      bind_primary_context();
+      if (!encode_cache_maps(a.c, &p.maps)) return MOE_ERR_CUDA;
+    }
+    return cuda_status(launch_attn_decode_tc(a, p.maps, (cudaStream_t)stream));
   }
   return cuda_status(launch_attn_decode_simt(a, (cudaStream_t)stream));
+}
+
+size_t moe_cache_plan_bytes(void) { return sizeof(CachePlan); }
+
+moe_status moe_cache_plan(const moe_kv_cache* cache, void* plan, size_t bytes) {
+  if (!cache_ok(cache) || plan == nullptr || bytes < sizeof(CachePlan)) return MOE_ERR_INVALID_ARG;
+  CachePlan p{};
+  p.k = cache->k; p.v = cache->v;
+  p.n_layers = cache->n_layers; p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+  p.H_kv = cache->H_kv; p.D = cache->D;
+  if (planned(cache)) {  // other caches take the CUDA cores, which need no descriptors
+    bind_primary_context();
+    if (!encode_cache_maps(view_of(cache), &p.maps)) return MOE_ERR_CUDA;
+  }
+  std::memcpy(plan, &p, sizeof(p));
+  return MOE_OK;
 }
 
 size_t moe_cache_workspace_bytes(const moe_kv_cache* cache) {

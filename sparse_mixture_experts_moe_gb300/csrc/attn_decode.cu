@@ -248,8 +248,8 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           const CUtensorMap *mk = nr == box ? &tmK : &tmK16, *mv = nr == box ? &tmV : &tmV16;
 #pragma unroll
           for (int h = 0; h < DP / 64; ++h) {
-            tma_load_2d(dst + h * (kUnit * 128) + r * 128, mk, 64 * h, row, b);
-            tma_load_2d(dst + C::kHalf + h * (kUnit * 128) + r * 128, mv, 64 * h, row, b);
+            tma_load_3d(dst + h * (kUnit * 128) + r * 128, mk, 64 * h, row, a.d.layer, b);
+            tma_load_3d(dst + C::kHalf + h * (kUnit * 128) + r * 128, mv, 64 * h, row, a.d.layer, b);
           }
           r += nr;
         }
@@ -554,32 +554,32 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
   if (a.d.lse != nullptr && lane == 0) a.d.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
-bool encode_pages(EncodeTiledFn enc, CUtensorMap* m, const void* p, const CacheView& c, int rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)c.D, (cuuint64_t)c.n_pages * c.Hkv * c.page_size};
-  const cuuint64_t str[1] = {(cuuint64_t)c.D * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)rows};
-  return encode_tmap(enc, m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 2, dims, str, box);
-}
-
 template <int DP, int NT>
-cudaError_t launch_own(const CUtensorMap (&tm)[4], const OwnArgs& o, int ctas, cudaStream_t s) {
-  const size_t smem = own_smem<DP, NT>(o.d.n);
+cudaError_t launch_own(const CacheMaps& m, const OwnArgs& o, int ctas, cudaStream_t s) {
+  static std::atomic<int> done{0};
   auto kern = decode_own_kernel<DP, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem(kern, own_smem<DP, NT>(kSlice), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, tm[0], tm[1], tm[2], tm[3], o);
+  return launch_pdl(kern, dim3(ctas), dim3(kThreads), own_smem<DP, NT>(o.d.n), s, m.k64, m.v64, m.k16, m.v16, o);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_decode_tc(const DecodeArgs& all, cudaStream_t s) {
+bool encode_cache_maps(const CacheView& c, CacheMaps* m) {
   EncodeTiledFn enc = tensor_map_encoder();
-  if (enc == nullptr) return cudaErrorNotSupported;
-  CUtensorMap tm[4] = {};
-  const int box = all.c.page_size < kUnit ? all.c.page_size : kUnit;
-  if (!encode_pages(enc, &tm[0], all.k, all.c, box) || !encode_pages(enc, &tm[1], all.v, all.c, box) ||
-      !encode_pages(enc, &tm[2], all.k, all.c, kKeys) || !encode_pages(enc, &tm[3], all.v, all.c, kKeys))
-    return cudaErrorInvalidValue;
+  if (enc == nullptr) return false;
+  const cuuint64_t rows = (cuuint64_t)c.n_pages * c.Hkv * c.page_size;
+  const cuuint64_t dims[3] = {(cuuint64_t)c.D, rows, (cuuint64_t)c.n_layers};
+  const cuuint64_t str[2] = {(cuuint64_t)c.D * 2, rows * c.D * 2};
+  auto one = [&](CUtensorMap* t, const void* p, int most) {
+    const cuuint32_t box[3] = {64, (cuuint32_t)(c.page_size < most ? c.page_size : most), 1};
+    return encode_tmap(enc, t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 3, dims, str, box);
+  };
+  return one(&m->k16, c.k, kKeys) && one(&m->v16, c.v, kKeys) && one(&m->k64, c.k, kUnit) && one(&m->v64, c.v, kUnit) &&
+         one(&m->k128, c.k, 128) && one(&m->v128, c.v, 128);
+}
+
+cudaError_t launch_attn_decode_tc(const DecodeArgs& all, const CacheMaps& m, cudaStream_t s) {
   const int G = all.H / all.c.Hkv, NT = G <= 8 ? 1 : 2, RG = (G + 8 * NT - 1) / (8 * NT), HR = all.c.Hkv * RG;
   const int R = G < 8 * NT ? G : 8 * NT, D = all.c.D;
   const int ctas = device_sm_count();
@@ -608,10 +608,10 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, cudaStream_t s) {
     o.prefix = reinterpret_cast<int32_t*>(const_cast<float2*>(o.sh_ml) + sh_rows);
     if (own_rows + sh_rows + 2 * kSlice > decode_pieces((long long)all.n * all.H)) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
-    if (d.shared > 0) e = launch_attn_shared_tc(d, o.splits, sh, const_cast<float2*>(o.sh_ml), s);
+    if (d.shared > 0) e = launch_attn_shared_tc(d, m, o.splits, sh, const_cast<float2*>(o.sh_ml), s);
     if (e == cudaSuccess) {
-      if (D <= 64) e = NT == 1 ? launch_own<64, 1>(tm, o, ctas, s) : launch_own<64, 2>(tm, o, ctas, s);
-      else e = NT == 1 ? launch_own<128, 1>(tm, o, ctas, s) : launch_own<128, 2>(tm, o, ctas, s);
+      if (D <= 64) e = NT == 1 ? launch_own<64, 1>(m, o, ctas, s) : launch_own<64, 2>(m, o, ctas, s);
+      else e = NT == 1 ? launch_own<128, 1>(m, o, ctas, s) : launch_own<128, 2>(m, o, ctas, s);
     }
     if (e == cudaSuccess) e = launch_pdl(decode_join_kernel, dim3((unsigned)((long long)d.n * d.H)), dim3(128), 0, s, o);
     if (e != cudaSuccess) return e;

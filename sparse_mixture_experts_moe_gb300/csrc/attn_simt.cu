@@ -264,8 +264,9 @@ decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int splits) {
 template <typename T, int ROWS, bool PAGED>
 cudaError_t launch(const PromptArgs& pa, const DecodeArgs& da, dim3 grid, int n_tiles, int splits, cudaStream_t s) {
   auto kern = attn_simt_kernel<T, ROWS, PAGED>;
+  static std::atomic<int> done{0};
   const size_t smem = simt_smem(ROWS, PAGED ? da.c.D : pa.D);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem(kern, simt_smem(ROWS, 256), done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), smem, s, pa, da, n_tiles, splits);
 }

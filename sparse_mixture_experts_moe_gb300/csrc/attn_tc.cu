@@ -242,7 +242,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int g = (page * Hkv + hk) * sa.d.c.page_size + ((j0 + r) & (sa.d.c.page_size - 1));
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
-              tma_load_2d(dst + c * (BK * 128) + r * 128, tm, 64 * c, g, bar(FULL + stage));
+              tma_load_3d(dst + c * (BK * 128) + r * 128, tm, 64 * c, g, sa.d.layer, bar(FULL + stage));
           }
         } else {
 #pragma unroll
@@ -620,8 +620,9 @@ bool encode3(EncodeTiledFn enc, CUtensorMap* m, const void* p, int D, int Hkv, i
 template <int DP, bool SHARED>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PromptArgs& pa, const SharedArgs& sa, dim3 grid,
                    int n_slots, cudaStream_t s) {
+  static std::atomic<int> done{0};
   auto kern = attn_tc_kernel<DP, SHARED>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<DP>::kSmem);
+  const cudaError_t e = allow_smem(kern, Cfg<DP>::kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), Cfg<DP>::kSmem, s, tk, tv, pa, sa, n_slots);
 }
@@ -652,16 +653,8 @@ int attn_shared_splits(const DecodeArgs& a) {
   return (blocks + per - 1) / per;  // no empty split
 }
 
-cudaError_t launch_attn_shared_tc(const DecodeArgs& a, int splits, float* part_o, float2* part_ml, cudaStream_t s) {
-  EncodeTiledFn enc = tensor_map_encoder();
-  if (enc == nullptr) return cudaErrorNotSupported;
-  CUtensorMap tk{}, tv{};
-  const cuuint64_t dims[2] = {(cuuint64_t)a.c.D, (cuuint64_t)a.c.n_pages * a.c.Hkv * a.c.page_size};
-  const cuuint64_t str[1] = {(cuuint64_t)a.c.D * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(a.c.page_size < BK ? a.c.page_size : BK)};
-  if (!encode_tmap(enc, &tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, 2, dims, str, box) ||
-      !encode_tmap(enc, &tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 2, dims, str, box))
-    return cudaErrorInvalidValue;
+cudaError_t launch_attn_shared_tc(const DecodeArgs& a, const CacheMaps& m, int splits, float* part_o, float2* part_ml,
+                                  cudaStream_t s) {
   SharedArgs sa;
   sa.d = a;
   sa.splits = splits;
@@ -672,7 +665,8 @@ cudaError_t launch_attn_shared_tc(const DecodeArgs& a, int splits, float* part_o
   const PromptArgs none{};
   const long long pairs = (a.n * (long long)(a.H / a.c.Hkv) + 2 * TM - 1) / (2 * TM);
   const dim3 grid((unsigned)a.c.Hkv, (unsigned)pairs, (unsigned)splits);
-  return a.c.D <= 64 ? launch<64, true>(tk, tv, none, sa, grid, 0, s) : launch<128, true>(tk, tv, none, sa, grid, 0, s);
+  return a.c.D <= 64 ? launch<64, true>(m.k128, m.v128, none, sa, grid, 0, s)
+                     : launch<128, true>(m.k128, m.v128, none, sa, grid, 0, s);
 }
 
 }  // namespace moe

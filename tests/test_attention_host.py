@@ -105,6 +105,23 @@ def test_cache_call_refusals():
     assert decode(c, n=0) == OK
 
 
+def test_plans():
+    lib, n = _lib.lib(), _lib.lib().moe_cache_plan_bytes()
+    buf = ctypes.create_string_buffer(n)
+    at = ctypes.addressof(buf)
+    c = cache(dt=0)  # an fp32 cache needs no descriptors, so its plan can be made without a GPU
+    assert lib.moe_cache_plan(ctypes.addressof(c), at, n) == OK
+    for args in [(None, at, n), (ctypes.addressof(c), None, n), (ctypes.addressof(c), at, n - 1)]:
+        assert lib.moe_cache_plan(*args) == BAD
+    bad = cache(page_size=24)
+    assert lib.moe_cache_plan(ctypes.addressof(bad), at, n) == BAD
+    # a plan of another cache is refused
+    for kw in [dict(k=FAKE + 256), dict(n_pages=101), dict(n_layers=1), dict(page_size=32), dict(H_kv=4), dict(D=32)]:
+        other = cache(**kw)
+        other.plan = at
+        assert decode(other, H=8, qs=512, os=512, shared=0) == BAD
+
+
 def test_null_cache():
     lib = _lib.lib()
     assert lib.moe_cache_workspace_bytes(None) == 0
