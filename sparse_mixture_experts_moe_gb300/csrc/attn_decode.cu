@@ -13,9 +13,13 @@
 //           leaves pieces that the join adds up, in order. A segment's end costs about as much as kEnd units (the
 //           warps meet, a piece is written, new rows are fetched), so each segment is laid out with that many
 //           empty units in front: without them runs of short segments took twice as long as the rest.
-//   warps   one loads units by TMA into a ring (boxes never cross a page), running ahead over segment ends; eight
+//           Beside a shared part there are two runs for each SM, taken from a counter: the SMs that the shared
+//           part leaves free start at once, the others as its CTAs end.
+//   warps   two load units by TMA into a ring (boxes never cross a page), running ahead over segment ends; eight
 //           take 16 keys each, four to a unit, with their own running maximum, and meet only where a segment ends.
-// Piece (segment s, CTA c) has number s + c: going along the units, s or c grows by one from piece to piece.
+//           Loaders and the two groups of four take every other unit: one loader could issue a unit only every
+//           1350 cycles (barrier, page number and four copies in sequence).
+// Piece (segment s, run c) has number s + c: going along the units, s or c grows by one from piece to piece.
 #include <cuda.h>
 
 #include "attn.cuh"
@@ -25,11 +29,12 @@ namespace moe {
 namespace {
 
 constexpr int kSlice = 2048;   // sequences a launch takes: their unit counts are scanned in shared memory
-constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 8, kLoaders = 2, kThreads = 32 * (kWarps + kLoaders);
 constexpr int kKeys = 16;      // keys of a warp
 constexpr int kUnit = 4 * kKeys;
 constexpr int kScan = 256;     // threads that scan the lengths
 constexpr int kEnd = 2;        // units that a segment's end is worth
+constexpr int kQueue = 2;      // runs that the loading warp may be ahead
 
 template <int DP, int NT> struct Cfg {
   static constexpr int kHalf = DP * kUnit * 2;  // bytes of a unit's K (or V)
@@ -44,7 +49,7 @@ template <int DP, int NT> struct Cfg {
 template <int DP, int NT> __host__ __device__ constexpr size_t own_smem(int n) {
   using C = Cfg<DP, NT>;
   return 1024 + (size_t)C::kStages * 2 * C::kHalf + (size_t)kWarps * C::kRows * C::kLd * 4 + 2 * kWarps * C::kRows * 4 +
-         16 * C::kStages + 16 + 4 * (size_t)(n + 1) + 4 * kScan;
+         16 * C::kStages + 16 * kQueue + 4 * kQueue + 16 + 4 * (size_t)(2 * n + 1) + 4 * kScan;
 }
 static_assert(own_smem<128, 1>(kSlice) <= 232448 && own_smem<128, 2>(kSlice) <= 232448 &&
               own_smem<64, 2>(kSlice) <= 232448, "shared memory");
@@ -59,6 +64,9 @@ struct OwnArgs {
   const float2* sh_ml;
   int splits;      // pieces of a row over the shared keys
   int first;       // sequence number of the slice's first row (for errors)
+  int* next_run;   // nullable: runs are taken from this counter (zero before the call; the join sets it back)
+  int n_runs;      // runs that the units are cut into (at most); without the counter one a CTA
+  int min_run;     // units of a run, at least
   int R;           // rows of a piece: min(G, 8 NT)
   int RG;          // row groups of a key/value head
 };
@@ -117,17 +125,20 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   float* sm_m = buf + kWarps * C::kRows * C::kLd;  // [warps][rows]
   float* sm_l = sm_m + kWarps * C::kRows;          // [warps][rows]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm_l + kWarps * C::kRows);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * C::kStages);
-  int* P = reinterpret_cast<int*>(bars + 2 * C::kStages + 2);  // [n + 1]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * C::kStages + 2 * kQueue);
+  volatile int* queue = abort_flag + 4;                    // [kQueue]
+  int* P = const_cast<int*>(abort_flag + 4 + kQueue);      // [n + 1]
+  int* lens = P + a.d.n + 1;                               // [n] (0: nothing to read)
   const int n = a.d.n, tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  int* sums = P + n + 1;                           // [kScan]
+  int* sums = lens + n;                            // [kScan]
   const CacheView& c = a.d.c;
   const int G = a.d.H / c.Hkv, HR = c.Hkv * a.RG, D = c.D;
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  constexpr int FULL = 0, EMPTY = C::kStages;
+  constexpr int FULL = 0, EMPTY = C::kStages, RFULL = 2 * C::kStages, REMPTY = RFULL + kQueue;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(bar(FULL + s), 1); mbar_init(bar(EMPTY + s), 4); }
+    for (int s = 0; s < kQueue; ++s) { mbar_init(bar(RFULL + s), 1); mbar_init(bar(REMPTY + s), kWarps + 1); }
     fence_mbar_init();
     *abort_flag = 0;
     tma_prefetch_desc(&tmK);
@@ -153,6 +164,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     const int nb = len > a.d.shared ? (len - a.d.shared + kUnit - 1) / kUnit + kEnd : 0;
     P[i + 1] = nb;
+    lens[i] = len;
     mine += nb;
   }
   if (n <= 32) {  // one warp's scan
@@ -195,16 +207,15 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
   __syncthreads();
   const long long total = (long long)P[n] * HR;
-  const int per = (int)((total + gridDim.x - 1) / gridDim.x);
+  const int per = max((int)((total + a.n_runs - 1) / a.n_runs), a.min_run);
   if (blockIdx.x == 0) {
     for (int i = tid; i <= n; i += kThreads) a.prefix[i] = P[i];
     if (tid == 0) a.prefix[n + 1] = per;
   }
-  const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
-  int count = end > begin ? (int)(end - begin) : 0;  // units of the run, from the one at cu on
-
-  Cursor cu{0, 0, 0, 0};
-  if (count > 0) {
+  // Where a run begins; returns the units from there to its end, empty ones included (0 or less: nothing to do).
+  auto start_run = [&](int run, Cursor& cu) {
+    const long long begin = (long long)run * per, end = min(total, begin + per);
+    if (end <= begin) return 0;
     int lo = 0, hi = n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -215,52 +226,86 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int r = (int)(begin - (long long)P[lo] * HR);
     cu.hr = r / cu.nb;
     cu.b = r % cu.nb;
+    int count = (int)(end - begin);
     if (cu.b < kEnd) {  // the run starts among a segment's empty units
       count -= kEnd - cu.b;
       cu.b = kEnd;
     }
-  }
+    return count;
+  };
+  Cursor cu{0, 0, 0, 0};
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
     if (lane == 0) {
-      // -------------------------------------------------------------- loads
-      int stage = 0, slot = 0, len = 0, cur = -1;
-      uint32_t phase = 0, filled = 0, fill_phase = 0;
+      // -------------------------------------------------------------- loads: the first loader takes the runs
+      const int loader = warp - kWarps;
+      int stage = 0, slot = 0, len = 0, cur = -1, rq = 0, x = 0;
+      uint32_t phase = 0, filled = 0, fill_phase = 0, rphase = 0;
       const int box = min(c.page_size, kUnit);
-      for (int left = count; left > 0; left -= advance(cu, P, n, HR)) {
-        if (cu.i != cur) {
-          cur = cu.i;
-          slot = a.d.slots[cur];
-          len = c.lens[slot];
+      auto take = [&]() { return a.next_run != nullptr ? atomicAdd(a.next_run, 1) : a.n_runs; };
+      int run = 0, next = 0;
+      if (loader == 0) next = a.next_run != nullptr ? take() : (int)blockIdx.x;
+      bool ok = true;
+      while (ok) {
+        if (loader == 0) {
+          // the run's number to the other warps (one past the last ends them), and the next one asked for
+          run = next;
+          if (!wait_or_abort(bar(REMPTY + rq), rphase ^ 1u, a.d.timeout_ns, abort_flag, a.d.status, 63)) break;
+          queue[rq] = run;
+          mbar_arrive(bar(RFULL + rq));
+          if (run < a.n_runs) next = take();
+        } else {
+          if (!wait_or_abort(bar(RFULL + rq), rphase, a.d.timeout_ns, abort_flag, a.d.status, 63)) break;
+          run = queue[rq];
+          mbar_arrive(bar(REMPTY + rq));
         }
-        if (!wait_or_abort(bar(EMPTY + stage), phase ^ 1u, a.d.timeout_ns, abort_flag, a.d.status, 62)) break;
-        const int key = a.d.shared + (cu.b - kEnd) * kUnit, rows = min(kUnit, (len - key + kKeys - 1) & ~(kKeys - 1));
-        const uint32_t dst = base + stage * 2 * C::kHalf, b = bar(FULL + stage);
-        mbar_arrive_expect_tx(b, 2u * (uint32_t)(rows * DP * 2));
-        for (int r = 0; r < rows;) {
-          const int nr = rows - r >= box ? box : kKeys;  // whole boxes, then 16 rows at a time
-          int page = c.table[(long long)slot * c.width + ((key + r) >> c.page_shift)];
-          if (page < 0 || page >= c.n_pages) {
-            record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + cur);
-            page = 0;
-          }
-          const int row = (page * c.Hkv + cu.hr / a.RG) * c.page_size + ((key + r) & (c.page_size - 1));
-          const CUtensorMap *mk = nr == box ? &tmK : &tmK16, *mv = nr == box ? &tmV : &tmV16;
+        if (++rq == kQueue) { rq = 0; rphase ^= 1u; }
+        if (run >= a.n_runs) break;
+        for (int left = start_run(run, cu); left > 0; left -= advance(cu, P, n, HR), ++x) {
+          if ((x & 1) == loader) {
+            if (cu.i != cur) {
+              cur = cu.i;
+              slot = a.d.slots[cur];
+              len = lens[cur];
+            }
+            const int key = a.d.shared + (cu.b - kEnd) * kUnit, rows = min(kUnit, (len - key + kKeys - 1) & ~(kKeys - 1));
+            const int32_t* row_pages = c.table + (long long)slot * c.width;
+            int page = row_pages[key >> c.page_shift];  // on its way during the wait
+            if (!wait_or_abort(bar(EMPTY + stage), phase ^ 1u, a.d.timeout_ns, abort_flag, a.d.status, 62)) {
+              ok = false;
+              break;
+            }
+            const uint32_t dst = base + stage * 2 * C::kHalf, b = bar(FULL + stage);
+            mbar_arrive_expect_tx(b, 2u * (uint32_t)(rows * DP * 2));
+            for (int r = 0; r < rows;) {
+              const int nr = rows - r >= box ? box : kKeys;  // whole boxes, then 16 rows at a time
+              if (r > 0) page = row_pages[(key + r) >> c.page_shift];
+              if (page < 0 || page >= c.n_pages) {
+                record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + cur);
+                page = 0;
+              }
+              const int row = (page * c.Hkv + cu.hr / a.RG) * c.page_size + ((key + r) & (c.page_size - 1));
+              const CUtensorMap *mk = nr == box ? &tmK : &tmK16, *mv = nr == box ? &tmV : &tmV16;
 #pragma unroll
-          for (int h = 0; h < DP / 64; ++h) {
-            tma_load_3d(dst + h * (kUnit * 128) + r * 128, mk, 64 * h, row, a.d.layer, b);
-            tma_load_3d(dst + C::kHalf + h * (kUnit * 128) + r * 128, mv, 64 * h, row, a.d.layer, b);
+              for (int h = 0; h < DP / 64; ++h) {
+                tma_load_3d(dst + h * (kUnit * 128) + r * 128, mk, 64 * h, row, a.d.layer, b);
+                tma_load_3d(dst + C::kHalf + h * (kUnit * 128) + r * 128, mv, 64 * h, row, a.d.layer, b);
+              }
+              r += nr;
+            }
+            filled |= 1u << stage;
+            fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
           }
-          r += nr;
+          if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
-        filled |= 1u << stage;
-        fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
-        if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
       }
       // copies in flight land before shared memory goes away
       for (int s = 0; s < C::kStages; ++s)
         if (filled & (1u << s)) mbar_wait_bounded(bar(FULL + s), (fill_phase >> s) & 1u, a.d.timeout_ns);
     }
+    // The idle lanes stay here: one that went ahead into the wait for the shared part's grid below would hold up the
+    // lane that loads.
+    __syncwarp();
   } else {
     // that the slots share what the caller says they share
     if (a.d.shared > 0) {
@@ -286,7 +331,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     bool ok = true;
     // the rows of the segment at `at`, as B fragments
     auto fetch = [&](const Cursor& at) {
-      len_n = c.lens[a.d.slots[at.i]];
+      len_n = lens[at.i];
       const int hk = at.hr / a.RG, r0 = (at.hr % a.RG) * C::kRows, nr = min(a.R, G - r0);
       const __nv_bfloat16* qp = (const __nv_bfloat16*)a.d.q + (long long)at.i * a.d.qs + (long long)(hk * G + r0) * D;
 #pragma unroll
@@ -299,9 +344,24 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             qn[k][t][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
           }
     };
-    bool fresh = true;
-    if (count > 0) fetch(cu);
-    for (int run = count; run > 0; ++x) {
+    int rq = 0, run = 0, run_no = 0;
+    uint32_t rphase = 0;
+    // the next run with anything in it, at cu; false after the last
+    auto next_run = [&]() {
+      for (run = 0; run <= 0;) {
+        if (!warp_wait(bar(RFULL + rq), rphase, a.d.timeout_ns, abort_flag, a.d.status, 64)) return false;
+        run_no = queue[rq];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(REMPTY + rq));
+        if (++rq == kQueue) { rq = 0; rphase ^= 1u; }
+        if (run_no >= a.n_runs) return false;
+        run = start_run(run_no, cu);
+      }
+      return true;
+    };
+    bool fresh = true, more = next_run();
+    if (more) fetch(cu);
+    for (; more; ++x) {
       if (fresh) {
         fresh = false;
         len = len_n;
@@ -333,17 +393,23 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
             __syncwarp();
           }
-          float s[NT][4];
+          float s[NT][4], odd[NT][4];  // even and odd k-steps: two chains of dependent MMAs instead of one
 #pragma unroll
-          for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = odd[t][e] = 0.f;
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             const int row = (mi & 1) * 8 + l8, u = 2 * k + (mi >> 1);
             uint32_t f[4];
             ldsm4(sk + (u >> 3) * (kUnit * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), f);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(s[t], f, q[k][t][0], q[k][t][1]);
+            for (int t = 0; t < NT; ++t) mma16816(k & 1 ? odd[t] : s[t], f, q[k][t][0], q[k][t][1]);
           }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] += odd[t][e];
           if (left < kKeys)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -399,11 +465,13 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
 
       const Cursor was = cu;
+      const int was_run = run_no;
       run -= advance(cu, P, n, HR);
       if (run > 0 && cu.i == was.i && cu.hr == was.hr) continue;
       // ---- the segment (or the run) ends: the eight warps' parts become one piece, while the next rows are on their way
       fresh = true;
-      if (run > 0) fetch(cu);
+      if (run <= 0) more = next_run();
+      if (more) fetch(cu);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -434,7 +502,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
       consumers_sync();
       const int nr = min(a.R, G - (was.hr % a.RG) * C::kRows);
-      const long long piece = (long long)was.i * HR + was.hr + blockIdx.x;
+      const long long piece = (long long)was.i * HR + was.hr + was_run;
       for (int z = tid; z < nr * (D / 4); z += 32 * kWarps) {
         const int row = z / (D / 4), col = (z % (D / 4)) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -467,6 +535,7 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
   __shared__ float4 part[4][32];
   griddep_wait();
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.next_run != nullptr) *a.next_run = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const CacheView& c = a.d.c;
   const int H = a.d.H, G = H / c.Hkv, HR = c.Hkv * a.RG, D = c.D;
@@ -596,8 +665,11 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, const CacheMaps& m, cud
     o.splits = 0;
     o.R = R;
     o.RG = RG;
-    // pieces: own ones [(n HR + ctas)][R], then the shared ones [n H][splits]; see decode_pieces
-    const long long own_rows = ((long long)d.n * HR + ctas) * R;
+    o.next_run = d.shared > 0 ? d.status + 6 : nullptr;
+    o.n_runs = d.shared > 0 ? 2 * ctas : ctas;
+    o.min_run = d.shared > 0 ? 6 : 1;
+    // pieces: own ones [(n HR + runs)][R], then the shared ones [n H][splits]; see decode_pieces
+    const long long own_rows = ((long long)d.n * HR + o.n_runs) * R;
     o.o = all.part;
     float* sh = all.part + own_rows * D;
     if (d.shared > 0) o.splits = attn_shared_splits(d);

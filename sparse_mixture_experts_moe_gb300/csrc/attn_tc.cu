@@ -643,11 +643,13 @@ cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s) {
                    : launch<128, false>(tk, tv, a, none, grid, (int)slots, s);
 }
 
-// One CTA an SM takes 256 rows of one key/value head; as many splits of the keys as there are SMs left over.
+// One CTA an SM takes 256 rows of one key/value head, the keys split over the SMs; about a tenth of those (where splits
+// can be had) are left to the own keys, which run beside. 64 sequences behind 32768 positions, own keys up to 2048:
+// see launch_attn_decode_tc.
 int attn_shared_splits(const DecodeArgs& a) {
   const long long units = (long long)a.c.Hkv * ((a.n * (long long)(a.H / a.c.Hkv) + 2 * TM - 1) / (2 * TM));
   const int blocks = (a.shared + BK - 1) / BK;
-  long long splits = device_sm_count() / units;
+  long long splits = (device_sm_count() - device_sm_count() / 6) / units;
   splits = splits < 1 ? 1 : (splits > blocks ? blocks : splits);
   const int per = (blocks + (int)splits - 1) / (int)splits;
   return (blocks + per - 1) / per;  // no empty split
