@@ -13,8 +13,10 @@
 //           leaves pieces that the join adds up, in order. A segment's end costs about as much as kEnd units (the
 //           warps meet, a piece is written, new rows are fetched), so each segment is laid out with that many
 //           empty units in front: without them runs of short segments took twice as long as the rest.
-//           Beside a shared part there are two runs for each SM, taken from a counter: the SMs that the shared
-//           part leaves free start at once, the others as its CTAs end.
+//           Beside a shared part there are four runs for each SM, taken from a counter: the SMs that the shared
+//           part leaves free start at once, the others as its CTAs end. (64 sequences of up to 2048 own positions
+//           behind 32768: 114 us with two runs, 108 with four, 109 with six; a sixth of the SMs left free against
+//           none: 108 against 111 us, and 8 sequences behind 8192: 22.7 against 27.6.)
 //   warps   two load units by TMA into a ring (boxes never cross a page), running ahead over segment ends; eight
 //           take 16 keys each, four to a unit, with their own running maximum, and meet only where a segment ends.
 //           Loaders and the two groups of four take every other unit: one loader could issue a unit only every
@@ -528,19 +530,22 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   if (a.d.shared > 0) griddep_wait();
 }
 
-// One CTA a (sequence, head): its pieces over the shared keys, then over its own. Four warps take every fourth piece
-// and add up in a fixed order.
+// A (sequence, head)'s pieces over the shared keys, then over its own, by WPR warps that take every WPR-th piece and add
+// up in a fixed order: 4 while there are few rows, 1 (four rows a CTA) when the rows alone fill the GPU.
+template <int WPR>
 __global__ void __launch_bounds__(128)
 decode_join_kernel(const __grid_constant__ OwnArgs a) {
-  __shared__ float4 part[4][32];
+  __shared__ float4 part[WPR == 1 ? 1 : WPR][32];
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.next_run != nullptr) *a.next_run = 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WPR;
   const CacheView& c = a.d.c;
   const int H = a.d.H, G = H / c.Hkv, HR = c.Hkv * a.RG, D = c.D;
-  const int row = blockIdx.x, i = row / H, h = row % H, hk = h / G, hg = h % G, rows = G < a.R ? G : a.R;
-  const int hr = hk * a.RG + hg / rows, r = hg % rows;
+  const int row = blockIdx.x * (4 / WPR) + (threadIdx.x >> 5) / WPR;
+  if (row >= a.d.n * H) return;  // (with WPR = 4 there is a CTA a row)
+  const int i = row / H, h = row % H, hk = h / G, hg = h % G;
+  const int hr = hk * a.RG + hg / a.R, r = hg % a.R;
   const int s = a.d.slots[i], b0 = a.prefix[i], b1 = a.prefix[i + 1], per = a.prefix[a.d.n + 1];
   const bool valid = s >= 0 && s < c.n_slots;
   const int b = b1 - b0, shared = valid ? a.splits : 0;
@@ -563,11 +568,12 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f, M = -INFINITY;
   const bool on = lane * 4 < D;
-  if (count <= 32) {  // the usual case: one lane a piece, the weights computed once; the values are on their way meanwhile
+  if (count <= 32) {  // the usual case: one lane a piece, the weights computed once, the values on their way meanwhile
     const float2 v = lane < count ? ml(lane) : make_float2(-INFINITY, 0.f);
     float4 u[8];
 #pragma unroll
-    for (int y = 0; y < 8; ++y) u[y] = warp + 4 * y < count && on ? *src(warp + 4 * y) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int y = 0; y < 8; ++y)
+      u[y] = warp + WPR * y < count && on ? *src(warp + WPR * y) : make_float4(0.f, 0.f, 0.f, 0.f);
     M = fmaxf(v.x, -INFINITY);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
@@ -575,13 +581,21 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
     l = wv * v.y;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    for (int y0 = 0; y0 * WPR < 32; y0 += 8) {
+      if (y0 > 0) {
+        if (warp + WPR * y0 >= count) break;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const float w = __shfl_sync(0xffffffffu, wv, (warp + 4 * y) & 31);
-      o.x = fmaf(w, u[y].x, o.x);
-      o.y = fmaf(w, u[y].y, o.y);
-      o.z = fmaf(w, u[y].z, o.z);
-      o.w = fmaf(w, u[y].w, o.w);
+        for (int y = 0; y < 8; ++y)
+          u[y] = warp + WPR * (y0 + y) < count && on ? *src(warp + WPR * (y0 + y)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xffffffffu, wv, (warp + WPR * (y0 + y)) & 31);
+        o.x = fmaf(w, u[y].x, o.x);
+        o.y = fmaf(w, u[y].y, o.y);
+        o.z = fmaf(w, u[y].z, o.z);
+        o.w = fmaf(w, u[y].w, o.w);
+      }
     }
   } else {
     for (int x = lane; x < count; x += 32) M = fmaxf(M, ml(x).x);
@@ -594,7 +608,8 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
     }
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    for (int x = warp; x < count; x += 4) {
+#pragma unroll 4
+    for (int x = warp; x < count; x += WPR) {
       const float w = ex2(ml(x).x - ref);
       if (on) {
         const float4 u = *src(x);
@@ -605,13 +620,15 @@ decode_join_kernel(const __grid_constant__ OwnArgs a) {
       }
     }
   }
-  part[warp][lane] = o;
-  __syncthreads();
-  if (warp != 0) return;
+  if (WPR > 1) {
+    part[warp % WPR][lane] = o;
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-  for (int y = 1; y < 4; ++y) {
-    const float4 u = part[y][lane];
-    o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
+    for (int y = 1; y < WPR; ++y) {
+      const float4 u = part[y][lane];
+      o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   if (on) {
@@ -666,7 +683,7 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, const CacheMaps& m, cud
     o.R = R;
     o.RG = RG;
     o.next_run = d.shared > 0 ? d.status + 6 : nullptr;
-    o.n_runs = d.shared > 0 ? 2 * ctas : ctas;
+    o.n_runs = d.shared > 0 ? 4 * ctas : ctas;
     o.min_run = d.shared > 0 ? 6 : 1;
     // pieces: own ones [(n HR + runs)][R], then the shared ones [n H][splits]; see decode_pieces
     const long long own_rows = ((long long)d.n * HR + o.n_runs) * R;
@@ -685,7 +702,10 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, const CacheMaps& m, cud
       if (D <= 64) e = NT == 1 ? launch_own<64, 1>(m, o, ctas, s) : launch_own<64, 2>(m, o, ctas, s);
       else e = NT == 1 ? launch_own<128, 1>(m, o, ctas, s) : launch_own<128, 2>(m, o, ctas, s);
     }
-    if (e == cudaSuccess) e = launch_pdl(decode_join_kernel, dim3((unsigned)((long long)d.n * d.H)), dim3(128), 0, s, o);
+    const int rows = d.n * d.H;
+    if (e == cudaSuccess)
+      e = rows <= 8 * ctas ? launch_pdl(decode_join_kernel<4>, dim3((unsigned)rows), dim3(128), 0, s, o)
+                           : launch_pdl(decode_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, o);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -643,7 +643,7 @@ cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s) {
                    : launch<128, false>(tk, tv, a, none, grid, (int)slots, s);
 }
 
-// One CTA an SM takes 256 rows of one key/value head, the keys split over the SMs; about a tenth of those (where splits
+// One CTA an SM takes 256 rows of one key/value head, the keys split over the SMs; about a sixth of those (where splits
 // can be had) are left to the own keys, which run beside. 64 sequences behind 32768 positions, own keys up to 2048:
 // see launch_attn_decode_tc.
 int attn_shared_splits(const DecodeArgs& a) {
