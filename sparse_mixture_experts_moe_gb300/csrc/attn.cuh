@@ -163,7 +163,7 @@ __device__ __forceinline__ Seq load_seq_warp(const PromptArgs& a, int i) {
   s.nq = q1 - s.q0;
   s.nk = k1 - s.k0;
   if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || s.k0 < 0 || k1 < s.k0 || k1 > a.Tkv) {
-    if (threadIdx.x == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
+    if (lane == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
     s.nq = 0;
     s.nk = 0;
   }

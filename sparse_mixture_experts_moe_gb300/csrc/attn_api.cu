@@ -118,7 +118,8 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
     return MOE_ERR_INVALID_ARG;
   if (n_seqs < 0 || Tq < 0 || Tkv < 0 || (Tq > 0 && n_seqs == 0)) return MOE_ERR_INVALID_ARG;
   if (kv_offsets == nullptr && Tkv != Tq) return MOE_ERR_INVALID_ARG;
-  if ((long long)Tq * H >= (1ll << 31) || (long long)Tq * H / H_kv + n_seqs >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
+  // rows and work items are numbered with 32 bits
+  if ((long long)Tq * H + (long long)n_seqs * H_kv >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
   if (!stride_ok(q_stride, (long long)H * D, dt) || !stride_ok(out_stride, (long long)H * D, dt) ||
       !stride_ok(k_stride, (long long)H_kv * D, dt) || !stride_ok(v_stride, (long long)H_kv * D, dt))
     return MOE_ERR_INVALID_ARG;
@@ -181,12 +182,12 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   a.timeout_ns = wait_timeout_ns();
   a.layer = layer;
   if (planned(cache)) {
+    bind_primary_context();
     CachePlan p;
     if (cache->plan != nullptr) {
       std::memcpy(&p, cache->plan, sizeof(p));
       if (!plan_holds(p, cache)) return MOE_ERR_INVALID_ARG;
     } else {
-      bind_primary_context();
       if (!encode_cache_maps(a.c, &p.maps)) return MOE_ERR_CUDA;
     }
     return cuda_status(launch_attn_decode_tc(a, p.maps, (cudaStream_t)stream));
