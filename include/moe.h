@@ -373,7 +373,9 @@ moe_status moe_forward_q(const void* x, const void* w_r, const float* b_r, const
  * moe_graph_capture_begin / moe_graph_capture_end: the general form. begin returns a private
  *      stream in capture; every moe_* call given that stream is recorded, not run; end stops the
  *      capture, instantiates what was recorded into *graph and destroys the stream (always, also
- *      on error). Use it for moe_forward_q or for a sequence of the separate entry points. */
+ *      on error). Use it for moe_forward_q or for a sequence of the separate entry points.
+ * moe_stream_capture_id: a number for the recording that `stream` is part of (this library's or any other
+ *      of the process), 0 outside one. Calls recorded into one graph can share a workspace of that graph's own. */
 typedef struct moe_graph_s* moe_graph;
 moe_status moe_graph_capture_begin(void** capture_stream);
 moe_status moe_forward_graph_create(const void* x, const void* w_r, const float* b_r, const void* w1,
@@ -382,6 +384,7 @@ moe_status moe_forward_graph_create(const void* x, const void* w_r, const float*
                                     int32_t* topk_idx, float* topk_gate, int32_t* counts, float* router_stats,
                                     void* workspace, size_t ws_bytes, moe_graph* graph);
 moe_status moe_graph_capture_end(void* capture_stream, moe_graph* graph);
+unsigned long long moe_stream_capture_id(void* stream);
 moe_status moe_graph_launch(moe_graph graph, void* stream);
 moe_status moe_graph_destroy(moe_graph graph);
 

@@ -59,6 +59,7 @@ SIGNATURES = {
     "moe_graph_launch": [_p, _p],
     "moe_graph_capture_begin": [_p],
     "moe_graph_capture_end": [_p, _p],
+    "moe_stream_capture_id": [_p],
     "moe_qweight_bytes": [_i, _i, _i, _i],
     "moe_qscale_bytes": [_i, _i, _i],
     "moe_quantize_weights": [_p, _i, _i, _i, _i, _i, _p, _p, _p],
@@ -91,7 +92,7 @@ SIGNATURES = {
 _RESTYPES = {"moe_workspace_bytes": ctypes.c_size_t, "moe_status_string": ctypes.c_char_p,
              "moe_qweight_bytes": ctypes.c_size_t, "moe_qscale_bytes": ctypes.c_size_t,
              "moe_attention_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t,
-             "moe_cache_plan_bytes": ctypes.c_size_t}
+             "moe_cache_plan_bytes": ctypes.c_size_t, "moe_stream_capture_id": ctypes.c_ulonglong}
 
 _LIB = None
 

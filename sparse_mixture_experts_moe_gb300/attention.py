@@ -10,7 +10,8 @@
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
 Everything is enqueued on the current stream, or on `stream`; nothing synchronises, except that the first call
-on a stream (and one that needs a larger workspace) waits for its workspace to be cleared. Index tensors (offsets,
+on a `stream` other than the current one (and one that needs a larger workspace) waits for the current one. Calls can
+be recorded into a graph (torch.cuda.graph, GraphCapture). Index tensors (offsets,
 slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the work is
 done by the library's kernels.
 """
@@ -22,7 +23,9 @@ from . import _lib
 from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
 
 
-_PROMPT_WORKSPACE = 256  # moe_attention_prompt: the status word alone
+_HEADER = 256           # bytes of a workspace's header
+_HEADER_USED = 64       # of these: status and counters, the rest stays zero
+_PROMPT_WORKSPACE = _HEADER  # moe_attention_prompt needs no more
 
 
 class _Cache(ctypes.Structure):
@@ -71,7 +74,10 @@ class _Bound:
         self._empty = torch.empty
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
-        self._ws = _Workspaces()
+        self._ws = _Workspaces(self._lib, self._init_workspace)
+
+    def _init_workspace(self, ptr, nbytes, stream):
+        return self._lib.moe_workspace_init(ptr, nbytes, stream)
 
     def device_status(self):
         """(status, detail) of the first device-side error since the last call; synchronises."""
@@ -79,35 +85,54 @@ class _Bound:
 
 
 class _Workspaces:
-    """Zeroed workspaces, one for each stream that calls arrive on, so that calls on different streams never
-    share scratch memory. Each is kept for good: work in flight may use one that a larger one replaced, or
-    that a graph recorded."""
+    """Prepared workspaces, one for each stream that calls arrive on, so that calls on different streams never
+    share scratch memory, and one for each graph recording (and stream of it): the graph prepares it at its
+    first use, and nothing else uses it, however late and on whatever stream the graph runs. (A recording on a stream that
+    calls have used before takes that stream's: its replays are to be ordered with further calls there.) Each is
+    kept for good: work in flight may use one that a larger one replaced."""
 
-    def __init__(self):
-        self._of = {}
+    def __init__(self, lib, init):
+        self._lib, self._init = lib, init
+        self._of = {}        # stream -> (tensor, bytes, address)
+        self._recorded = {}  # (stream, recording) -> the same
         self._old = []
 
     def get(self, stream, nbytes, dev):
         ws = self._of.get(stream)
-        if ws is None or ws[1] < nbytes:
-            import torch
-            if ws is not None:
-                self._old.append(ws)
-            t = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-            ws = (t, nbytes, t.data_ptr())
-            if torch.cuda.is_current_stream_capturing():
-                self._old.append(ws)  # zeroed by the graph being recorded, so for that recording only
-            else:
-                torch.cuda.current_stream(dev).synchronize()  # zeroed before any stream uses it
-                self._of[stream] = ws
+        return ws if ws is not None and ws[1] >= nbytes else self._make(stream, nbytes, dev)
+
+    def _make(self, stream, nbytes, dev):
+        import torch
+        recording = self._lib.moe_stream_capture_id(stream)
+        of, key = (self._recorded, (stream, recording)) if recording else (self._of, stream)
+        ws = of.get(key)
+        if ws is not None:
+            if ws[1] >= nbytes:
+                return ws
+            self._old.append(ws)
+        t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+        current = torch.cuda.current_stream(dev)
+        if current.cuda_stream != (stream or 0):
+            current.synchronize()  # what used this memory before, on the stream that it was allocated for
+        ws = of[key] = (t, nbytes, t.data_ptr())
+        _check(self._init(ws[2], nbytes, stream), "workspace_init")
         return ws
 
     def status(self):
         """(status, detail) of the first device-side error of any of them; clears it."""
+        import torch
         for stream, ws in self._of.items():
             st, detail = _lib.get_device_status(ws[0], stream)
             if st != MOE_OK:
                 return st, detail
+        if self._recorded:
+            torch.cuda.synchronize(next(iter(self._recorded.values()))[0].device)
+        for ws in self._recorded.values():
+            # a graph that has not run yet has not prepared its workspace: the header's unused words tell
+            if not ws[0][_HEADER_USED:_HEADER].any():
+                st, detail = _lib.get_device_status(ws[0])
+                if st != MOE_OK:
+                    return st, detail
         return MOE_OK, 0
 
 
@@ -155,6 +180,9 @@ class KVCache(_Bound):
         i32 = dict(dtype=torch.int32, device=device)
         return cls(k, torch.empty_like(k), torch.full((n_slots, width), -1, **i32), torch.zeros(n_slots, **i32),
                    torch.zeros(n_pages, **i32))
+
+    def _init_workspace(self, ptr, nbytes, stream):
+        return self._lib.moe_cache_workspace_init(self._ref, ptr, nbytes, stream)
 
     def _workspace(self, stream):
         return self._ws.get(stream, self._bytes, self._dev)

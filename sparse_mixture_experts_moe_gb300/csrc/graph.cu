@@ -69,6 +69,16 @@ moe_status moe_graph_capture_begin(void** capture_stream) {
   return MOE_OK;
 }
 
+unsigned long long moe_stream_capture_id(void* stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &st, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return st == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 moe_status moe_graph_capture_end(void* capture_stream, moe_graph* graph) {
   if (capture_stream == nullptr) return MOE_ERR_INVALID_ARG;
   cudaStream_t cs = (cudaStream_t)capture_stream;

@@ -148,3 +148,7 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         i = torch.zeros(3, dtype=torch.int32)
         p = torch.zeros((1, 4, 2, 16, 64), dtype=torch.bfloat16)
         moe.KVCache(p, p, torch.zeros((3, 2), dtype=torch.int32), i, i)  # refs must have one count a page
+
+
+def test_no_stream_records_without_a_gpu():
+    assert _lib.lib().moe_stream_capture_id(None) == 0

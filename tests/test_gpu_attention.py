@@ -352,3 +352,76 @@ def test_binding_refuses_on_the_gpu():
     with pytest.raises(moe.MoeError):  # a stride that is no multiple of 16 bytes
         x = torch.zeros((8, 4 * 64 + 4), dtype=BF16, device=DEV)
         a.prompt(x[:, :256].unflatten(1, (4, 64)), kv, kv, o)
+
+
+def test_workspace_needs_only_its_header_prepared():
+    c, _ = make_cache([300, 1, 0, 77], 64, 32, 2, 64, BF16)
+    q, slots = tensor((4, 8, 64), 1, BF16, DEV), i32([0, 1, 2, 3], DEV)
+    kv, o = tensor((40, 2, 64), 2, BF16, DEV), i32([0, 40], DEV)
+    qp = tensor((40, 8, 64), 3, BF16, DEV)
+    a = moe.Attention(8, 2, 64, BF16)
+
+    def all_calls():
+        return [a.decode(q, c, slots), a.decode(q, c, slots, shared_len=64), a.prompt(qp, kv, kv, o)]
+
+    first = all_calls()
+    for t, _, _ in a._ws._of.values():
+        t[256:].fill_(255)
+    for x, y in zip(first, all_calls()):
+        assert torch.equal(x, y)
+    assert a.device_status()[0] == moe.MOE_OK
+
+
+def test_recorded_calls_share_one_workspace_of_their_own():
+    c, _ = make_cache([900, 33, 64], 32, 32, 2, 128, BF16)
+    q, slots = tensor((3, 8, 128), 1, BF16, DEV), i32([0, 1, 2], DEV)
+    a = moe.Attention(8, 2, 128, BF16)
+    want = a.decode(q, c, slots)
+    need = a._ws._of[torch.cuda.current_stream().cuda_stream][1]
+    assert a._lib.moe_stream_capture_id(torch.cuda.current_stream().cuda_stream) == 0
+    graphs = []
+    for _ in range(2):
+        outs = [torch.empty_like(want) for _ in range(6)]
+        g, before = torch.cuda.CUDAGraph(), torch.cuda.memory_allocated()
+        with torch.cuda.graph(g):
+            for o in outs:
+                a.decode(q, c, slots, out=o)
+        assert torch.cuda.memory_allocated() - before < 2 * need  # one workspace (and what torch keeps for a graph)
+        graphs.append((g, outs))
+    assert a.device_status()[0] == moe.MOE_OK  # nothing has run yet
+    spaces = {w[2] for w in a._ws._recorded.values()} | {w[2] for w in a._ws._of.values()}
+    assert len(spaces) == 3
+    # both graphs and eager calls at once, on three streams
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        assert torch.equal(a.decode(q, c, slots), want)
+    torch.cuda.synchronize()
+    for _, outs in graphs:
+        assert all(torch.equal(o, want) for o in outs)
+    assert a.device_status()[0] == moe.MOE_OK
+    slots[1] = 99  # no such slot: a recorded call reports it
+    graphs[0][0].replay()
+    assert a.device_status() == (moe.MOE_ERR_DEVICE_CHECK, 1)
+    assert a.device_status()[0] == moe.MOE_OK
+
+
+def test_recordings_one_after_the_other_on_private_streams():
+    q, kv = tensor((70, 4, 64), 1, BF16, DEV), tensor((70, 2, 64), 2, BF16, DEV)
+    o = i32([0, 70], DEV)
+    a = moe.Attention(4, 2, 64, BF16)
+    want, caps = a.prompt(q, kv, kv, o), []
+    for _ in range(3):
+        out = torch.zeros_like(want)
+        with moe.GraphCapture(keep=(q, kv, o, out, a)) as cap:
+            a.prompt(q, kv, kv, o, out=out, stream=cap.stream)
+        caps.append((cap, out))
+    assert len({w[2] for w in a._ws._recorded.values()}) == 3
+    for cap, out in caps:
+        cap.graph.launch()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert a.device_status()[0] == moe.MOE_OK
