@@ -1,305 +1,651 @@
 // Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and heads of more than 128.
 //   out[r] = sum_{j < lim(r)} softmax_j(scale q[r] . k[j]) v[j]
-// over packed prompts (PAGED = false) or, one token a sequence, over the paged cache (PAGED = true).
+// Scores are kept in log2 units (times scale * log2 e), so a weight is one 2^x. Keys past a row's limit are left
+// out of both products by index, not by a zero weight, so that a non-finite value there stays there.
 //
-// One CTA takes ROWS packed rows (see PromptArgs) of one key/value head and walks the keys in tiles of KT,
-// both in shared memory in fp32; the running maximum m and sum l of each row live in registers of the
-// 16 threads that share the row, the output row in the registers of the same 16. Scores are kept in
-// log2 units (times scale * log2 e), so a weight is one 2^x. Keys past a row's limit are left out of
-// both products by index, not by a zero weight, so that a non-finite value there stays there.
-// Bound by the CUDA cores' fp32 rate (prompts) and by their loads of shared memory; decode takes 16 rows
-// instead of 64 and splits the keys over CTAs whose pieces decode_join_kernel adds in a fixed order.
+// attn_tile_kernel: 64 packed rows (see PromptArgs) of one key/value head against tiles of 64 keys, all in shared
+// memory in fp32: packed prompts, and the shared positions of a decode batch (rows: every sequence's heads). 8
+// threads share a row, each with 4 rows x 8 keys of the scores and 4 rows x D / 8 columns of the output in registers.
+// Bound by reads of shared memory: a warp's 16-byte read takes four cycles whatever its lanes share, so an
+// element of the scores costs (4 + 8) * 4 cycles for 32 of arithmetic, one of the output 20 for 16; with 2 rows a thread
+// that was 40 for 16. Rows in shared memory have a length known to the compiler (D rounded up to 32, zeros past D): with
+// D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the place of the
+// keys once the scores are done; two CTAs then fit on an SM and one computes while the other loads.
+// Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s; bf16, 16 heads of 256
+// on 4: 30 TFLOP/s (one CTA an SM).
+//
+// decode_rows_kernel: the positions that a sequence does not share, an HBM stream that meets up to 8 rows, far too
+// few for tiles. Lanes lie along a head's elements; a warp takes 4 keys at a time straight from memory, its rows' products
+// with them are summed over the lanes in one exchange (each step halves the values a lane holds: 31 shuffles for
+// 32 sums), which leaves each lane one score. Keys are split over warps and CTAs, whose pieces join in a fixed order.
+// Bound by latency, each warp loading and computing in turn; the launch bounds are what measured best. fp32, heads of 128,
+// 4096 positions: 32 sequences of 8 heads 187 us (5.7 TB/s), 8 of 32 heads on 8 61 us (4.4 TB/s), 8 of 64 on 8 85 us.
 #include "attn.cuh"
 #include "kernels.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int KT = 32;
-constexpr int kThreads = 256;
-
-__host__ __device__ constexpr size_t simt_smem(int rows, int D) {
-  return sizeof(float) * ((size_t)(rows + 2 * KT) * (D + 4) + (size_t)rows * (KT + 1));
-}
-
 template <typename T>
-__device__ __forceinline__ void load8f(const T* p, float* d);
+__device__ __forceinline__ float4 load4f(const T* p);
 template <>
-__device__ __forceinline__ void load8f<float>(const float* p, float* d) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  reinterpret_cast<float4*>(d)[0] = a;
-  reinterpret_cast<float4*>(d)[1] = b;
+__device__ __forceinline__ float4 load4f<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load4f<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+}
+// 4 elements to shared memory: fp32 asynchronously (waited for with the group), bf16 through registers.
+template <typename T>
+__device__ __forceinline__ void stage4(float* dst, const T* src, bool in);
+template <>
+__device__ __forceinline__ void stage4<float>(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 template <>
-__device__ __forceinline__ void load8f<__nv_bfloat16>(const __nv_bfloat16* p, float* d) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  reinterpret_cast<float4*>(d)[0] = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
-  reinterpret_cast<float4*>(d)[1] = make_float4(bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w));
+__device__ __forceinline__ void stage4<__nv_bfloat16>(float* dst, const __nv_bfloat16* src, bool in) {
+  *reinterpret_cast<float4*>(dst) = in ? load4f(src) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
+template <typename T> __device__ __forceinline__ void store_result(T* p, float x) { *p = from_f32<T>(x); }
 
-template <typename T, int ROWS, bool PAGED>
-__global__ void __launch_bounds__(kThreads)
-attn_simt_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ DecodeArgs da, int n_tiles, int splits) {
-  constexpr int RPT = ROWS / 16;  // rows per thread
+// ------------------------------------------------------------------ tiles
+constexpr int kRows = 64, KT = 64, kThreads = 128;
+constexpr int TX = 8;               // threads of a row
+constexpr int RPT = kRows * TX / kThreads, KPT = KT / TX;
+constexpr int kLdP = KT + 4;
+
+// DP: D rounded up to a multiple of 32; the elements past D are zeros in shared memory.
+constexpr int tile_keys(int DP) { return KT * (DP + 4) > kRows * kLdP ? KT * (DP + 4) : kRows * kLdP; }
+constexpr size_t tile_smem(int DP) { return sizeof(float) * ((size_t)(kRows + KT) * (DP + 4) + tile_keys(DP)); }
+
+struct SharedPart {
+  DecodeArgs d;
+  int splits, per;  // pieces of a row over the shared positions; positions of a piece
+  int pieces;       // of a row altogether
+};
+
+template <typename T, int DP, bool SHARED>
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
+attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ SharedPart sp) {
+  constexpr int NC = DP / (4 * TX);  // groups of 4 columns of a thread
   extern __shared__ __align__(16) float sm[];
-  griddep_launch_dependents();
   griddep_wait();
-  const int H = PAGED ? da.H : pa.H, Hkv = PAGED ? da.c.Hkv : pa.Hkv, D = PAGED ? da.c.D : pa.D;
-  const int G = H / Hkv, hk = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int LD = D + 4;
+  griddep_launch_dependents();  // after the wait: the own positions' kernel relies on it
+  const DecodeArgs& da = sp.d;
+  const int H = SHARED ? da.H : pa.H, Hkv = SHARED ? da.c.Hkv : pa.Hkv, D = SHARED ? da.c.D : pa.D;
+  const int G = H / Hkv, hk = blockIdx.y, tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
+  constexpr int LD = DP + 4, d4 = DP / 4;
   float* Qs = sm;
-  float* Ks = Qs + ROWS * LD;
-  float* Vs = Ks + KT * LD;
-  float* Ps = Vs + KT * LD;
+  float* Ks = Qs + kRows * LD;
+  float* Ps = Ks;  // [kRows][kLdP], once the scores are done
+  float* Vs = Ks + tile_keys(DP);
 
   // ---- which rows, which keys
-  int row0, nrows, j_begin, j_end;  // packed rows row0 .. of the sequence; keys
+  int row0, nrows, j_begin, j_end;
   Seq sq{0, 0, 0, 0};
-  int slot = 0, len = 0, seq;
-  if (PAGED) {
-    seq = blockIdx.x / n_tiles;
-    row0 = (blockIdx.x % n_tiles) * ROWS;
-    nrows = min(ROWS, G - row0);
-    slot = da.slots[seq];
-    if (slot < 0 || slot >= da.c.n_slots) {
-      if (tid == 0) record_error(da.status, MOE_ERR_DEVICE_CHECK, seq);
-      len = 0;
-    } else {
-      len = max(0, min(da.c.lens[slot], da.c.width << da.c.page_shift));
-    }
-    const int per = ((len + splits - 1) / splits + KT - 1) / KT * KT;
-    j_begin = min(len, (int)blockIdx.z * per);
-    j_end = min(len, j_begin + per);
+  const int32_t* pages = nullptr;
+  if (SHARED) {
+    row0 = blockIdx.x * kRows;
+    nrows = min(kRows, da.n * G - row0);
+    j_begin = min(da.shared, (int)blockIdx.z * sp.per);
+    j_end = min(da.shared, j_begin + sp.per);
+    const int s0 = da.slots[0];  // an out-of-range slot or page is recorded by the own part
+    pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
-    seq = find_tile_seq(pa.qo, pa.n, G, ROWS, blockIdx.x);
+    const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
+    const int seq = find_tile_seq(pa.qo, pa.n, G, kRows, slot);
     sq = load_seq(pa, seq);
-    const long long first = (long long)sq.q0 * G / ROWS + seq;
-    const long long r0 = ((long long)blockIdx.x - first) * ROWS;
+    const long long first = (long long)sq.q0 * G / kRows + seq;
+    const long long r0 = ((long long)slot - first) * kRows;
     if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
     row0 = (int)r0;
-    nrows = min(ROWS, sq.nq * G - row0);
+    nrows = min(kRows, sq.nq * G - row0);
     j_begin = 0;
     j_end = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, pa.causal);
   }
-
-  const float c2 = (PAGED ? da.scale : pa.scale) * 1.4426950408889634f;
-  const int d8 = D / 8;
-  for (int i = tid; i < ROWS * d8; i += kThreads) {
-    const int r = i / d8, c = (i % d8) * 8;
-    float t[8];
-    if (r < nrows) {
-      const int R = row0 + r, tok = PAGED ? seq : sq.q0 + R / G, h = hk * G + (PAGED ? R : R % G);
-      const T* src = (const T*)(PAGED ? da.q : pa.q) + (long long)tok * (PAGED ? da.qs : pa.qs) + (long long)h * D + c;
-      load8f<T>(src, t);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) Qs[r * LD + c + e] = t[e];
+  const float c2 = (SHARED ? da.scale : pa.scale) * 1.4426950408889634f;
+  const T* qsrc = (const T*)(SHARED ? da.q : pa.q);
+  const long long qs = SHARED ? da.qs : pa.qs;
+  for (int i = tid; i < kRows * d4; i += kThreads) {
+    const int r = i / d4, c = (i % d4) * 4, R = row0 + min(r, nrows - 1);
+    const T* row = qsrc + (long long)(sq.q0 + R / G) * qs + (long long)(hk * G + R % G) * D;
+    stage4<T>(Qs + r * LD + c, row + min(c, D - 4), r < nrows && c < D);
   }
 
   float m[RPT], l[RPT];
   int lim[RPT];
-  float o[RPT][4][4];
+  uint64_t o[RPT][NC][2];
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
     const int R = ty * RPT + r;
-    lim[r] = R >= nrows ? 0 : (PAGED ? j_end : visible_keys((row0 + R) / G, sq.nq, sq.nk, pa.causal));
+    lim[r] = 0;
+    if (R < nrows && SHARED) {  // a slot shorter than the shared positions sees its own length of them
+      const int s = da.slots[(row0 + R) / G];
+      lim[r] = s < 0 || s >= da.c.n_slots ? 0 : min(j_end, max(0, da.c.lens[s]));
+    } else if (R < nrows) {
+      lim[r] = visible_keys((row0 + R) / G, sq.nq, sq.nk, pa.causal);
+    }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[r][c][e] = 0.f;
+    for (int c = 0; c < NC; ++c) o[r][c][0] = o[r][c][1] = 0ull;
   }
 
-  for (int j0 = j_begin; j0 < j_end; j0 += KT) {
+  const T* kb = (const T*)(SHARED ? da.k : pa.k);
+  const T* vb = (const T*)(SHARED ? da.v : pa.v);
+  // (what is left counts down: positions near 2^31 must not wrap)
+  for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
     __syncthreads();
-    for (int i = tid; i < KT * d8; i += kThreads) {
-      const int r = i / d8, c = (i % d8) * 8, j = j0 + r;
-      float a[8], b[8];
-      if (j < j_end) {
-        long long ok, ov;
-        if (PAGED) {
-          int page = da.c.table[(long long)slot * da.c.width + (j >> da.c.page_shift)];
-          if (page < 0 || page >= da.c.n_pages) {
-            record_error(da.status, MOE_ERR_DEVICE_CHECK, seq);
-            page = 0;
-          }
-          ok = ov = (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D + c;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // K, then V
+      float* dst = half ? Vs : Ks;
+      const T* src = half ? vb : kb;
+      const long long stride = SHARED ? 0 : (half ? pa.vs : pa.ks);
+      for (int i = tid; i < KT * d4; i += kThreads) {
+        const int r = i / d4, c = (i % d4) * 4, j = j0 + min(r, left - 1), ce = min(c, D - 4);
+        long long at;
+        if (SHARED) {
+          int page = pages[j >> da.c.page_shift];
+          page = page < 0 || page >= da.c.n_pages ? 0 : page;
+          at = (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D + ce;
         } else {
-          ok = (long long)(sq.k0 + j) * pa.ks + (long long)hk * D + c;
-          ov = (long long)(sq.k0 + j) * pa.vs + (long long)hk * D + c;
+          at = (long long)(sq.k0 + j) * stride + (long long)hk * D + ce;
         }
-        load8f<T>((const T*)(PAGED ? da.k : pa.k) + ok, a);
-        load8f<T>((const T*)(PAGED ? da.v : pa.v) + ov, b);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;
+        stage4<T>(dst + r * LD + c, src + at, r < left && c < D);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) { Ks[r * LD + c + e] = a[e]; Vs[r * LD + c + e] = b[e]; }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
-    // ---- scores of RPT rows x 2 keys (tx, tx + 16) per thread
-    float s[RPT][2];
+    // ---- scores of rows ty * RPT + r and keys tx + TX * k
+    float sc[RPT][KPT];
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) s[r][0] = s[r][1] = 0.f;
-    for (int d = 0; d < D; d += 4) {
-      const float4 k0 = *reinterpret_cast<const float4*>(Ks + tx * LD + d);
-      const float4 k1 = *reinterpret_cast<const float4*>(Ks + (tx + 16) * LD + d);
+    for (int r = 0; r < RPT; ++r)
 #pragma unroll
-      for (int r = 0; r < RPT; ++r) {
-        const float4 q = *reinterpret_cast<const float4*>(Qs + (ty * RPT + r) * LD + d);
-        s[r][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, s[r][0]))));
-        s[r][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, s[r][1]))));
+      for (int k = 0; k < KPT; ++k) sc[r][k] = 0.f;
+#pragma unroll 2
+    for (int d = 0; d < DP; d += 4) {
+      float4 q[RPT];
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) q[r] = *reinterpret_cast<const float4*>(Qs + (ty * RPT + r) * LD + d);
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        const float4 kk = *reinterpret_cast<const float4*>(Ks + (tx + TX * k) * LD + d);
+#pragma unroll
+        for (int r = 0; r < RPT; ++r)
+          sc[r][k] = fmaf(q[r].w, kk.w, fmaf(q[r].z, kk.z, fmaf(q[r].y, kk.y, fmaf(q[r].x, kk.x, sc[r][k]))));
       }
     }
+    __syncthreads();  // the keys' place is free
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
-      float a = j0 + tx < lim[r] ? s[r][0] * c2 : -INFINITY, b = j0 + tx + 16 < lim[r] ? s[r][1] * c2 : -INFINITY;
-      float mx = fmaxf(a, b);
+      float s[KPT], mx = -INFINITY;
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      for (int k = 0; k < KPT; ++k) {
+        s[k] = tx + TX * k < lim[r] - j0 ? sc[r][k] * c2 : -INFINITY;
+        mx = fmaxf(mx, s[k]);
+      }
+#pragma unroll
+      for (int w = TX / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
       const float mn = fmaxf(m[r], mx), ref = mn == -INFINITY ? 0.f : mn;  // no key yet: every weight is 0
-      a = ex2(a - ref);
-      b = ex2(b - ref);
-      float sum = a + b;
+      float sum = 0.f;
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      for (int k = 0; k < KPT; ++k) {
+        const float p = ex2(s[k] - ref);
+        sum += p;
+        Ps[(ty * RPT + r) * kLdP + tx + TX * k] = p;
+      }
+#pragma unroll
+      for (int w = TX / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       const float al = ex2(m[r] - ref);
       l[r] = l[r] * al + sum;
       m[r] = mn;
+      const uint64_t al2 = f2_pack(al, al);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[r][c][e] *= al;
-      Ps[(ty * RPT + r) * (KT + 1) + tx] = a;
-      Ps[(ty * RPT + r) * (KT + 1) + tx + 16] = b;
+      for (int c = 0; c < NC; ++c) {
+        o[r][c][0] = ffma2(o[r][c][0], al2, 0ull);
+        o[r][c][1] = ffma2(o[r][c][1], al2, 0ull);
+      }
     }
-    __syncwarp();  // a row's weights are written and read by the same half warp
-    // ---- o += p v: each thread its RPT rows x columns tx * 4 + 64 c
-    int kmax = 0;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the values are there (a row's weights are written and read by the same warp)
+    // ---- o += p v: columns 4 tx + 4 TX c
+    int kmin = KT, kmax = 0;  // every row of the thread sees the keys below kmin, none those from kmax on
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) kmax = max(kmax, min(KT, lim[r] - j0));
-    for (int kk = 0; kk < kmax; ++kk) {
+    for (int r = 0; r < RPT; ++r) {
+      const int x = max(0, min(KT, lim[r] - j0));
+      kmin = min(kmin, x);
+      kmax = max(kmax, x);
+    }
+    kmin &= ~3;
+    for (int kk = 0; kk < kmin; kk += 4) {
+      float4 p[RPT];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (tx * 4 + 64 * c < D) {
-          const float4 v = *reinterpret_cast<const float4*>(Vs + kk * LD + tx * 4 + 64 * c);
+      for (int r = 0; r < RPT; ++r) p[r] = *reinterpret_cast<const float4*>(Ps + (ty * RPT + r) * kLdP + kk);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint64_t pp[RPT];
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+          const float x = y == 0 ? p[r].x : y == 1 ? p[r].y : y == 2 ? p[r].z : p[r].w;
+          pp[r] = f2_pack(x, x);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(Vs + (kk + y) * LD + tx * 4 + 4 * TX * c);
 #pragma unroll
           for (int r = 0; r < RPT; ++r) {
-            if (j0 + kk < lim[r]) {
-              const float p = Ps[(ty * RPT + r) * (KT + 1) + kk];
-              o[r][c][0] = fmaf(p, v.x, o[r][c][0]);
-              o[r][c][1] = fmaf(p, v.y, o[r][c][1]);
-              o[r][c][2] = fmaf(p, v.z, o[r][c][2]);
-              o[r][c][3] = fmaf(p, v.w, o[r][c][3]);
-            }
+            o[r][c][0] = ffma2(pp[r], v.x, o[r][c][0]);
+            o[r][c][1] = ffma2(pp[r], v.y, o[r][c][1]);
           }
         }
       }
     }
+    for (int kk = kmin; kk < kmax; ++kk) {
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) {
+        if (kk >= lim[r] - j0) continue;
+        const float x = Ps[(ty * RPT + r) * kLdP + kk];
+        const uint64_t pp = f2_pack(x, x);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(Vs + kk * LD + tx * 4 + 4 * TX * c);
+          o[r][c][0] = ffma2(pp, v.x, o[r][c][0]);
+          o[r][c][1] = ffma2(pp, v.y, o[r][c][1]);
+        }
+      }
+    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const int R = ty * RPT + r;
     if (R >= nrows) continue;
-    const int P = row0 + R, tok = PAGED ? seq : sq.q0 + P / G, h = hk * G + (PAGED ? P : P % G);
-    if (PAGED && splits > 1) {
-      const long long row = (long long)seq * H + h, piece = row * splits + blockIdx.z;
-      float* po = da.part + piece * (D + 2);
-      if (tx == 0) { po[D] = m[r]; po[D + 1] = l[r]; }
+    const int P = row0 + R, tok = sq.q0 + P / G, h = hk * G + P % G;
+    if (SHARED) {
+      float* po = da.part + (((long long)tok * H + h) * sp.pieces + blockIdx.z) * (D + 2);
+      if (tx == 0) *reinterpret_cast<float2*>(po + D) = make_float2(m[r], l[r]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (tx * 4 + 64 * c < D) po[tx * 4 + 64 * c + e] = o[r][c][e];
+      for (int c = 0; c < NC; ++c) {
+        if (tx * 4 + 4 * TX * c >= D) continue;
+        *reinterpret_cast<uint64_t*>(po + tx * 4 + 4 * TX * c) = o[r][c][0];
+        *reinterpret_cast<uint64_t*>(po + tx * 4 + 4 * TX * c + 2) = o[r][c][1];
+      }
       continue;
     }
     const float inv = l[r] == 0.f ? 0.f : 1.0f / l[r];
-    T* dst = (T*)(PAGED ? da.out : pa.out) + (long long)tok * (PAGED ? da.os : pa.os) + (long long)h * D;
+    T* dst = (T*)pa.out + (long long)tok * pa.os + (long long)h * D;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < NC; ++c) {
+      if (tx * 4 + 4 * TX * c >= D) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (tx * 4 + 64 * c < D) dst[tx * 4 + 64 * c + e] = from_f32<T>(o[r][c][e] * inv);
-    float* lse = PAGED ? da.lse : pa.lse;
-    if (lse != nullptr && tx == 0)
-      lse[(long long)tok * H + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
+        store_result<T>(dst + tx * 4 + 4 * TX * c + e, (e & 1 ? f2_hi(o[r][c][e / 2]) : f2_lo(o[r][c][e / 2])) * inv);
+    }
+    if (pa.lse != nullptr && tx == 0)
+      pa.lse[(long long)tok * H + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
   }
 }
 
-// Joins a row's pieces (fixed order): one warp per (sequence, head).
-template <typename T>
-__global__ void __launch_bounds__(128)
-decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int splits) {
+// ------------------------------------------------------------------ few rows
+constexpr int kRowWarps = 4;
+constexpr int NK = 4;  // keys of a warp's step
+// From this many sequences on the shared positions are read once for all by tiles; fewer read them each (4096 shared, fp32
+// heads of 128 on 4: two sequences of 4 heads 26 us by tiles, 16 each; four 22 and 21; eight 22 and 31; four of 32 heads
+// 25 and 28).
+constexpr int kSharedFrom = 4;
+
+// V4: groups of 4 elements of a lane (elements 4 lane + 128 x); GR: rows of a CTA.
+template <typename T, int V4, int GR>
+__global__ void __launch_bounds__(32 * kRowWarps, V4 == 2 ? 3 : GR == 8 ? 4 : 5)
+decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_piece, int splits, int pieces) {
+  constexpr int NV = GR * NK;  // products of a step
+  static_assert(NV == 32 || NV == 16, "one or two lanes a score");
+  __shared__ __align__(16) float2 ps[kRowWarps][NV];  // each weight twice, a packed factor
+  __shared__ float sml[2][kRowWarps][GR];
+  __shared__ __align__(16) float buf[kRowWarps][GR][V4 * 128];
+  // Behind the shared positions' kernel (first_piece > 0) this one need not wait for it: that kernel lets dependents start
+  // only once it has itself waited for everything before it, and only the join reads what it writes.
+  if (first_piece == 0) griddep_wait();
   griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, D = a.c.D;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)a.n * a.H) return;
-  const float* p = a.part + row * splits * (D + 2);
-  float M = -INFINITY;
-  for (int i = 0; i < splits; ++i) M = fmaxf(M, p[(long long)i * (D + 2) + D]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  for (int i = 0; i < splits; ++i) l += ex2(p[(long long)i * (D + 2) + D] - ref) * p[(long long)i * (D + 2) + D + 1];
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const int tok = (int)(row / a.H), h = (int)(row % a.H);
-  T* dst = (T*)a.out + (long long)tok * a.os + (long long)h * D;
-  for (int d = lane; d < D; d += 32) {
-    float o = 0.f;
-    for (int i = 0; i < splits; ++i) {
-      const float w = ex2(p[(long long)i * (D + 2) + D] - ref);
-      if (p[(long long)i * (D + 2) + D + 1] != 0.f) o = fmaf(w, p[(long long)i * (D + 2) + d], o);
-    }
-    dst[d] = from_f32<T>(o * inv);
+  const CacheView& c = a.c;
+  const int G = a.H / c.Hkv, D = c.D, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int seq = blockIdx.x / groups, row0 = (blockIdx.x % groups) * GR, nrows = min(GR, G - row0);
+  const int from = first_piece > 0 ? a.shared : 0;
+  const int slot = a.slots[seq];
+  int len = 0;
+  if (slot < 0 || slot >= c.n_slots) {
+    if (tid == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
+  } else {
+    len = (int)max(0ll, min((long long)c.lens[slot], (long long)c.width << c.page_shift));
   }
+  const int32_t* pages = c.table + (long long)slot * c.width;
+  if (first_piece > 0 && len > 0 && blockIdx.y == 0 && blockIdx.z == 0 && row0 == 0) {
+    // that the slots share what the caller says they share
+    const int s0 = a.slots[0];
+    if (s0 >= 0 && s0 < c.n_slots)
+      for (int p = tid; p < a.shared >> c.page_shift && (p << c.page_shift) < len; p += 32 * kRowWarps) {
+        const int page = pages[p];
+        if (page < 0 || page >= c.n_pages || page != c.table[(long long)s0 * c.width + p])
+          record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
+      }
+  }
+  // this CTA's keys, then this warp's: NK at a time, the warps in turn
+  const int own = max(0, len - from), step = NK * kRowWarps;
+  const int per = (int)(((long long)own + splits - 1) / splits + step - 1) / step * step;
+  const int j_begin = from + (int)min((long long)own, (long long)blockIdx.z * per), j_end = min(from + own, j_begin + per);
+
+  uint64_t q[GR][V4][2], o[GR][V4][2];
+  const T* qp = (const T*)a.q + (long long)seq * a.qs + (long long)(hk * G + row0) * D;
+#pragma unroll
+  for (int r = 0; r < GR; ++r)
+#pragma unroll
+    for (int x = 0; x < V4; ++x) {
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nrows && 4 * lane + 128 * x < D) t = load4f<T>(qp + (long long)r * D + 4 * lane + 128 * x);
+      q[r][x][0] = f2_pack(t.x, t.y);
+      q[r][x][1] = f2_pack(t.z, t.w);
+      o[r][x][0] = o[r][x][1] = 0ull;
+    }
+  const float c2 = a.scale * 1.4426950408889634f;
+  // this lane's score: row my_row, key my_key of the step
+  const int idx = NV == 32 ? lane : lane >> 1, my_row = idx % GR, my_key = idx / GR;
+  float m = -INFINITY, l = 0.f;  // of my_row
+  const T* kb = (const T*)a.k;
+  const T* vb = (const T*)a.v;
+  int page[NK];
+  auto look_up = [&](int j) {
+#pragma unroll
+    for (int k = 0; k < NK; ++k) page[k] = k < j_end - j ? pages[(j + k) >> c.page_shift] : 0;
+  };
+  int left = j_end - j_begin - warp * NK;
+  int j = j_begin + warp * NK;
+  if (left > 0) look_up(j);
+  for (; left > 0; left -= step, j += step) {
+    uint64_t kv[NK][V4][2], vv[NK][V4][2];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      int p = page[k];
+      if (p < 0 || p >= c.n_pages) {
+        if (lane == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
+        p = 0;
+      }
+      const long long at = (((long long)p * c.Hkv + hk) * c.page_size + ((j + k) & (c.page_size - 1))) * D + 4 * lane;
+#pragma unroll
+      for (int x = 0; x < V4; ++x) {
+        const bool in = k < left && 4 * lane + 128 * x < D;
+        const float4 ke = in ? load4f<T>(kb + at + 128 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 ve = in ? load4f<T>(vb + at + 128 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        kv[k][x][0] = f2_pack(ke.x, ke.y);
+        kv[k][x][1] = f2_pack(ke.z, ke.w);
+        vv[k][x][0] = f2_pack(ve.x, ve.y);
+        vv[k][x][1] = f2_pack(ve.z, ve.w);
+      }
+    }
+    if (left > step) look_up(j + step);
+    float v[NV];
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int r = 0; r < GR; ++r) {
+        uint64_t t = 0ull;
+#pragma unroll
+        for (int x = 0; x < V4; ++x) t = ffma2(q[r][x][1], kv[k][x][1], ffma2(q[r][x][0], kv[k][x][0], t));
+        v[k * GR + r] = f2_lo(t) + f2_hi(t);
+      }
+#pragma unroll
+    for (int half = NV / 2, w = 16; half > 0; half >>= 1, w >>= 1) {
+      const bool up = lane & w;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+      }
+    }
+    if (NV == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+    const float s = my_key < left ? v[0] * c2 : -INFINITY;
+    float mx = fmaxf(s, -INFINITY);  // (drops a NaN: the maximum is never NaN)
+#pragma unroll
+    for (int w = 32 / NK; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+    const float al = ex2(m - ref), p = ex2(s - ref);
+    float sum = p;
+#pragma unroll
+    for (int w = 32 / NK; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    l = l * al + sum;
+    if (__any_sync(0xffffffffu, mn > m))
+#pragma unroll
+      for (int r = 0; r < GR; ++r) {
+        const float t = __shfl_sync(0xffffffffu, al, NV == 32 ? r : 2 * r);
+#pragma unroll
+        for (int x = 0; x < V4; ++x) {
+          o[r][x][0] = ffma2(o[r][x][0], f2_pack(t, t), 0ull);
+          o[r][x][1] = ffma2(o[r][x][1], f2_pack(t, t), 0ull);
+        }
+      }
+    m = mn;
+    __syncwarp();
+    ps[warp][idx] = make_float2(p, p);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int r = 0; r < GR; r += 2) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&ps[warp][k * GR + r]);
+#pragma unroll
+        for (int x = 0; x < V4; ++x) {
+          o[r][x][0] = ffma2(w.x, vv[k][x][0], o[r][x][0]);
+          o[r][x][1] = ffma2(w.x, vv[k][x][1], o[r][x][1]);
+          o[r + 1][x][0] = ffma2(w.y, vv[k][x][0], o[r + 1][x][0]);
+          o[r + 1][x][1] = ffma2(w.y, vv[k][x][1], o[r + 1][x][1]);
+        }
+      }
+  }
+  // ---- the warps' parts
+  if (my_key == 0) {
+    sml[0][warp][my_row] = m;
+    sml[1][warp][my_row] = l;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < GR; ++r) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int y = 0; y < kRowWarps; ++y) M = fmaxf(M, sml[0][y][r]);
+    const float w = M == -INFINITY ? 0.f : ex2(sml[0][warp][r] - M);
+#pragma unroll
+    for (int x = 0; x < V4; ++x)
+      *reinterpret_cast<float4*>(&buf[warp][r][4 * lane + 128 * x]) =
+          sml[1][warp][r] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                 : make_float4(f2_lo(o[r][x][0]) * w, f2_hi(o[r][x][0]) * w, f2_lo(o[r][x][1]) * w,
+                                               f2_hi(o[r][x][1]) * w);
+  }
+  __syncthreads();
+  for (int i = tid; i < nrows * (D / 2); i += 32 * kRowWarps) {
+    const int r = i / (D / 2), col = (i % (D / 2)) * 2, h = hk * G + row0 + r;
+    float2 t = make_float2(0.f, 0.f);
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int y = 0; y < kRowWarps; ++y) {
+      t.x += buf[y][r][col];
+      t.y += buf[y][r][col + 1];
+      M = fmaxf(M, sml[0][y][r]);
+    }
+#pragma unroll
+    for (int y = 0; y < kRowWarps; ++y)
+      if (M != -INFINITY) L += sml[1][y][r] * ex2(sml[0][y][r] - M);
+    if (pieces > 1) {
+      float* po = a.part + (((long long)seq * a.H + h) * pieces + first_piece + blockIdx.z) * (D + 2);
+      *reinterpret_cast<float2*>(po + col) = t;
+      if (col == 0) *reinterpret_cast<float2*>(po + D) = make_float2(M, L);
+    } else {
+      const float inv = L == 0.f ? 0.f : 1.0f / L;
+      T* dst = (T*)a.out + (long long)seq * a.os + (long long)h * D + col;
+      store_result<T>(dst, t.x * inv);
+      store_result<T>(dst + 1, t.y * inv);
+      if (a.lse != nullptr && col == 0)
+        a.lse[(long long)seq * a.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+  }
+  if (first_piece > 0) griddep_wait();
+}
+
+// Joins a row's pieces in a fixed order, by WPR warps that take every WPR-th piece, eight on their way at a time: 4 while
+// there are few rows, 1 (four rows a CTA) when the rows alone fill the GPU. A lane holds elements 2 lane + 64 x.
+template <typename T, int WPR>
+__global__ void __launch_bounds__(128)
+decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
+  __shared__ float2 part[WPR][4][32];
+  __shared__ float part_l[WPR];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WPR, D = a.c.D;
+  const long long row = (long long)blockIdx.x * (4 / WPR) + (threadIdx.x >> 5) / WPR;
+  if (row >= (long long)a.n * a.H) return;  // (with WPR = 4 there is a CTA a row)
+  const float* p = a.part + row * pieces * (D + 2);
+  auto ml = [&](int i) { return *reinterpret_cast<const float2*>(p + (long long)i * (D + 2) + D); };
+  float M = -INFINITY, l = 0.f;
+  for (int i = lane; i < pieces; i += 32) M = fmaxf(M, ml(i).x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float2 o[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) o[x] = make_float2(0.f, 0.f);
+  for (int i0 = warp; i0 < pieces; i0 += 32 * WPR) {  // lane: piece i0 + WPR lane
+    const float2 v = i0 + WPR * lane < pieces ? ml(i0 + WPR * lane) : make_float2(-INFINITY, 0.f);
+    const float wl = v.y == 0.f ? 0.f : ex2(v.x - ref);
+    l += wl * v.y;
+    for (int y0 = 0; y0 < 32 && i0 + WPR * y0 < pieces; y0 += 8) {
+      float2 u[8][4];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + WPR * (y0 + y);
+          u[y][x] = i < pieces && 2 * lane + 64 * x < D
+                        ? *reinterpret_cast<const float2*>(p + (long long)i * (D + 2) + 2 * lane + 64 * x) : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xffffffffu, wl, y0 + y);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          o[x].x = fmaf(w, u[y][x].x, o[x].x);
+          o[x].y = fmaf(w, u[y][x].y, o[x].y);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  if (WPR > 1) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) part[warp][x][lane] = o[x];
+    if (lane == 0) part_l[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int y = 1; y < WPR; ++y) {
+      l += part_l[y];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        o[x].x += part[y][x][lane].x;
+        o[x].y += part[y][x][lane].y;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  T* dst = (T*)a.out + (row / a.H) * a.os + (row % a.H) * D;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (2 * lane + 64 * x < D) {
+      store_result<T>(dst + 2 * lane + 64 * x, o[x].x * inv);
+      store_result<T>(dst + 2 * lane + 64 * x + 1, o[x].y * inv);
+    }
   if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
-template <typename T, int ROWS, bool PAGED>
-cudaError_t launch(const PromptArgs& pa, const DecodeArgs& da, dim3 grid, int n_tiles, int splits, cudaStream_t s) {
-  auto kern = attn_simt_kernel<T, ROWS, PAGED>;
+template <typename T, int DP, bool SHARED>
+cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, dim3 grid, cudaStream_t s) {
+  auto kern = attn_tile_kernel<T, DP, SHARED>;
   static std::atomic<int> done{0};
-  const size_t smem = simt_smem(ROWS, PAGED ? da.c.D : pa.D);
-  const cudaError_t e = allow_smem(kern, simt_smem(ROWS, 256), done);
+  const cudaError_t e = allow_smem(kern, tile_smem(DP), done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, grid, dim3(kThreads), smem, s, pa, da, n_tiles, splits);
+  return launch_pdl(kern, grid, dim3(kThreads), tile_smem(DP), s, pa, sp);
+}
+// bf16 comes here with heads of more than 128 only.
+template <bool SHARED>
+cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, int dt, int D, dim3 grid, cudaStream_t s) {
+  if (dt == MOE_DTYPE_BF16)
+    return D <= 192 ? launch_tiles<__nv_bfloat16, 192, SHARED>(pa, sp, grid, s)
+                    : launch_tiles<__nv_bfloat16, 256, SHARED>(pa, sp, grid, s);
+  if (D <= 64) return launch_tiles<float, 64, SHARED>(pa, sp, grid, s);
+  if (D <= 96) return launch_tiles<float, 96, SHARED>(pa, sp, grid, s);
+  if (D <= 128) return launch_tiles<float, 128, SHARED>(pa, sp, grid, s);
+  return D <= 192 ? launch_tiles<float, 192, SHARED>(pa, sp, grid, s) : launch_tiles<float, 256, SHARED>(pa, sp, grid, s);
+}
+
+template <typename T, int V4, int GR>
+cudaError_t launch_rows(const DecodeArgs& a, int first_piece, int splits, cudaStream_t s) {
+  const int groups = (a.H / a.c.Hkv + GR - 1) / GR;
+  const dim3 grid((unsigned)((long long)a.n * groups), (unsigned)a.c.Hkv, (unsigned)splits);
+  return launch_pdl(decode_rows_kernel<T, V4, GR>, grid, dim3(32 * kRowWarps), 0, s, a, groups, first_piece, splits,
+                    first_piece + splits);
+}
+
+template <typename T>
+cudaError_t launch_join(const DecodeArgs& a, int pieces, cudaStream_t s) {
+  const long long rows = (long long)a.n * a.H;
+  if (rows <= 8 * device_sm_count())
+    return launch_pdl(decode_join_simt_kernel<T, 4>, dim3((unsigned)rows), dim3(128), 0, s, a, pieces);
+  return launch_pdl(decode_join_simt_kernel<T, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, pieces);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
-  const long long slots = prompt_tile_slots(a.Tq, a.n, a.H / a.Hkv, 64);
-  const dim3 grid((unsigned)slots, (unsigned)a.Hkv);
-  const DecodeArgs none{};
-  return a.dt == MOE_DTYPE_BF16 ? launch<__nv_bfloat16, 64, false>(a, none, grid, 1, 1, s)
-                                : launch<float, 64, false>(a, none, grid, 1, 1, s);
+  const long long slots = prompt_tile_slots(a.Tq, a.n, a.H / a.Hkv, kRows);
+  const SharedPart none{};
+  return launch_tiles<false>(a, none, a.dt, a.D, dim3((unsigned)slots, (unsigned)a.Hkv), s);
 }
 
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s) {
-  const int G = a.H / a.c.Hkv, tiles = (G + 15) / 16;
-  // enough CTAs to fill the GPU a few times over, at least 8 key tiles each at the longest length
-  const long long ctas = (long long)a.n * tiles * a.c.Hkv, most = (long long)a.c.width * a.c.page_size;
-  long long splits = (4LL * device_sm_count() + ctas - 1) / ctas;
-  const long long cap = (most + 8 * KT - 1) / (8 * KT);
-  splits = splits > cap ? cap : splits;
+  const int G = a.H / a.c.Hkv, D = a.c.D, GR = D <= 128 && G > 4 ? 8 : 4, sms = device_sm_count();
   const long long rows = (long long)a.n * a.H, fit = decode_pieces(rows) / rows;
-  splits = splits > fit ? fit : (splits < 1 ? 1 : splits);
-  splits = splits > 65535 ? 65535 : splits;
-  const dim3 grid((unsigned)((long long)a.n * tiles), (unsigned)a.c.Hkv, (unsigned)splits);
-  const PromptArgs none{};
-  cudaError_t e = a.c.dt == MOE_DTYPE_BF16 ? launch<__nv_bfloat16, 16, true>(none, a, grid, tiles, (int)splits, s)
-                                           : launch<float, 16, true>(none, a, grid, tiles, (int)splits, s);
-  if (e != cudaSuccess || splits == 1) return e;
-  const dim3 jg((unsigned)(((long long)a.n * a.H + 3) / 4));
-  return a.c.dt == MOE_DTYPE_BF16
-             ? launch_pdl(decode_join_simt_kernel<__nv_bfloat16>, jg, dim3(128), 0, s, a, (int)splits)
-             : launch_pdl(decode_join_simt_kernel<float>, jg, dim3(128), 0, s, a, (int)splits);
+  const bool shared = a.shared > 0 && a.n >= kSharedFrom;
+  // own positions: about 8 CTAs an SM, at least 64 positions each at the longest length
+  const long long ctas = (long long)a.n * ((G + GR - 1) / GR) * a.c.Hkv;
+  const long long most = (long long)a.c.width * a.c.page_size - (shared ? a.shared : 0);
+  long long splits = (8LL * sms + ctas - 1) / ctas;
+  const long long cap = (most + 63) / 64;
+  splits = splits > cap ? cap : splits;
+  splits = splits > fit / 2 ? fit / 2 : splits;
+  splits = splits < 1 ? 1 : (splits > 65535 ? 65535 : splits);
+  SharedPart sp{};
+  cudaError_t e = cudaSuccess;
+  if (shared) {
+    const long long tiles = ((long long)a.n * G + kRows - 1) / kRows, tiles_kv = tiles * a.c.Hkv;
+    const int blocks = (a.shared + KT - 1) / KT;
+    long long n = (2LL * sms) / tiles_kv;
+    n = n > fit / 2 ? fit / 2 : n;
+    n = n < 1 ? 1 : (n > blocks ? blocks : n);
+    const int per = (int)((blocks + n - 1) / n);
+    sp.d = a;
+    sp.per = per * KT;
+    sp.splits = (blocks + per - 1) / per;
+    sp.pieces = sp.splits + (int)splits;
+    const PromptArgs none{};
+    e = launch_tiles<true>(none, sp, a.c.dt, D, dim3((unsigned)tiles, (unsigned)a.c.Hkv, (unsigned)sp.splits), s);
+    if (e != cudaSuccess) return e;
+  }
+  const int first = sp.splits, n = (int)splits;
+  if (a.c.dt == MOE_DTYPE_BF16) e = launch_rows<__nv_bfloat16, 2, 4>(a, first, n, s);
+  else if (D > 128) e = launch_rows<float, 2, 4>(a, first, n, s);
+  else e = GR == 4 ? launch_rows<float, 1, 4>(a, first, n, s) : launch_rows<float, 1, 8>(a, first, n, s);
+  if (e != cudaSuccess || first + n == 1) return e;
+  return a.c.dt == MOE_DTYPE_BF16 ? launch_join<__nv_bfloat16>(a, first + n, s) : launch_join<float>(a, first + n, s);
 }
 
 }  // namespace moe
