@@ -61,6 +61,16 @@ def test_prompt_packed_with_past(seed, causal, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 200])
+@pytest.mark.parametrize("nq,nk", [([3, 18, 0, 1], [1100, 700, 50, 2049]), ([16], [4096]), ([1, 1], [1, 300]),
+                                   ([70, 5], [600, 0]), ([64], [1025])])
+def test_prompt_few_rows_many_keys(nq, nk, D, dtype):
+    """Few tiles of rows: their keys are split over CTAs, some of which see none."""
+    run_prompt(nq, nk, 6, 2, D, dtype, seed=D)
+    run_prompt(nq, nk, 6, 2, D, dtype, causal=False, seed=D)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prompt_no_keys_at_all(dtype):
     q = tensor((7, 4, 64), 1, dtype, DEV)
     kv = torch.empty((0, 2, 64), dtype=dtype, device=DEV)
