@@ -409,11 +409,14 @@ moe_status moe_graph_destroy(moe_graph graph);
  *   without it every key. Lengths of 0 are valid.
  * In:  q [Tq, H, D], k, v [Tkv, H_kv, D] (token strides q_stride, k_stride, v_stride).
  * Out: out [Tq, H, D] (token stride out_stride), lse [Tq, H] or NULL.
- * Workspace: at least 256 bytes, prepared with moe_workspace_init (status word).
+ * Workspace: at least 256 bytes, prepared with moe_workspace_init (status word). With
+ *   moe_attention_prompt_workspace_bytes (0 on bad sizes) a bf16 call of few rows over many keys splits the keys
+ *   over the GPU and joins the parts; with less it runs without.
  * Device checks: offsets that decrease or leave [0, Tq] / [0, Tkv] record MOE_ERR_DEVICE_CHECK
  *   (detail = sequence) and that sequence's rows are not computed.
  */
 enum { MOE_ATTN_CAUSAL = 1 };
+size_t moe_attention_prompt_workspace_bytes(int n_seqs, int Tq, int Tkv, int H, int H_kv, int D, moe_dtype dt);
 moe_status moe_attention_prompt(const void* q, const void* k, const void* v, const int32_t* q_offsets,
                                 const int32_t* kv_offsets, int n_seqs, int Tq, int Tkv, int H, int H_kv, int D,
                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride, float scale,

@@ -74,6 +74,7 @@ SIGNATURES = {
     "moe_get_device_status": [_p, _p, _p],
     "moe_status_string": [_i],
     "moe_selftest_wait_timeout": [_p, _sz, _i, _p],
+    "moe_attention_prompt_workspace_bytes": [_i, _i, _i, _i, _i, _i, _i],
     "moe_attention_prompt": [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i64, _i64, _i64, _f, _i, _i, _p, _p, _p,
                              _sz, _p],
     "moe_attention_workspace_bytes": [_i, _i, _i],
@@ -91,7 +92,8 @@ SIGNATURES = {
 }
 _RESTYPES = {"moe_workspace_bytes": ctypes.c_size_t, "moe_status_string": ctypes.c_char_p,
              "moe_qweight_bytes": ctypes.c_size_t, "moe_qscale_bytes": ctypes.c_size_t,
-             "moe_attention_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t,
+             "moe_attention_workspace_bytes": ctypes.c_size_t,
+             "moe_attention_prompt_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t,
              "moe_cache_plan_bytes": ctypes.c_size_t, "moe_stream_capture_id": ctypes.c_ulonglong}
 
 _LIB = None

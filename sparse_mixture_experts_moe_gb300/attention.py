@@ -25,7 +25,7 @@ from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
 
 _HEADER = 256           # bytes of a workspace's header
 _HEADER_USED = 64       # of these: status and counters, the rest stays zero
-_PROMPT_WORKSPACE = _HEADER  # moe_attention_prompt needs no more
+_SPLIT_KEYS = 1024      # moe_attention_prompt uses no more than the header below this many keys
 
 
 class _Cache(ctypes.Structure):
@@ -261,6 +261,7 @@ class Attention(_Bound):
             raise ValueError("Attention: heads must be a multiple of kv_heads, head_dim a multiple of 8 from 8 to 256")
         self.scale = float(scale) if scale is not None else self.head_dim ** -0.5
         super().__init__()
+        self._prompt_bytes = self._lib.moe_attention_prompt_workspace_bytes
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
         self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
@@ -310,7 +311,10 @@ class Attention(_Bound):
             _ints(kv_offsets, "kv_offsets", n + 1, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
-        ws = self._ws.get(s, _PROMPT_WORKSPACE, dev)
+        need = _HEADER
+        if Tk >= _SPLIT_KEYS:
+            need = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
+        ws = self._ws.get(s, need, dev)
         _check(self._prompt(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
             None if kv_offsets is None else kv_offsets.data_ptr(), n, Tq, Tk, self.heads, self.kv_heads, self.head_dim,

@@ -76,7 +76,9 @@ constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
 
 cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);
 // bf16, D <= 128, at least one key.
-cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s);
+// splits: attn_prompt_splits or 1; part: Tq H splits (D + 2) floats where there are several.
+int attn_prompt_splits(int n, int Tq, int Tkv, int H, int Hkv);
+cudaError_t launch_attn_prompt_tc(const PromptArgs& a, int splits, float* part, cudaStream_t s);
 cudaError_t launch_attn_decode_tc(const DecodeArgs& a, const CacheMaps& m, cudaStream_t s);
 // The shared keys of a decode batch: `splits` pieces of every row, part_o [(sequence, head)][splits][D] unnormalised.
 int attn_shared_splits(const DecodeArgs& a);
@@ -140,12 +142,13 @@ __device__ __forceinline__ Seq load_seq(const PromptArgs& a, int i) {
   return s;
 }
 // The same by a warp: 32 places a step, and the four offsets in one load.
-__device__ __forceinline__ int find_tile_seq_warp(const int32_t* qo, int n, int G, int R, long long s) {
+// (slot: 1 where every sequence has a slot of its own besides its tiles, 0 to find a token's sequence.)
+__device__ __forceinline__ int find_tile_seq_warp(const int32_t* qo, int n, int G, int R, long long s, int slot = 1) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;  // the answer is in [lo, lo + len)
   while (len > 1) {
     const int step = (len + 31) / 32, i = lo + lane * step;
-    const bool at = lane * step < len && (long long)qo[i] * G / R + i <= s;
+    const bool at = lane * step < len && (long long)qo[i] * G / R + slot * i <= s;
     const int k = __popc(__ballot_sync(0xffffffffu, at)) - 1;  // (the first place always is, but for bad offsets)
     const int skip = (k < 0 ? 0 : k) * step;
     lo += skip;

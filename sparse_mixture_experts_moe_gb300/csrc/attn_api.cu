@@ -102,12 +102,24 @@ size_t decode_ws_bytes(int n, int H, int D) {
   return align256(kWsHeaderBytes) + align256((size_t)decode_pieces((long long)n * H) * (D + 2) * 4);
 }
 
+size_t prompt_ws_bytes(long long rows, int splits, int D) {
+  return kWsHeaderBytes + (splits > 1 ? align256((size_t)rows * splits * (D + 2) * 4) : 0);
+}
+
 }  // namespace
 }  // namespace moe
 
 using namespace moe;
 
 extern "C" {
+
+size_t moe_attention_prompt_workspace_bytes(int n_seqs, int Tq, int Tkv, int H, int H_kv, int D, moe_dtype dt) {
+  if (!dtype_ok(dt) || !heads_ok(H, H_kv, D) || n_seqs < 0 || Tq < 0 || Tkv < 0 ||
+      (long long)Tq * H + (long long)n_seqs * H_kv >= (1ll << 31))
+    return 0;
+  const bool tc = dt == MOE_DTYPE_BF16 && D <= 128 && Tq > 0;
+  return prompt_ws_bytes((long long)Tq * H, tc ? attn_prompt_splits(n_seqs, Tq, Tkv, H, H_kv) : 1, D);
+}
 
 moe_status moe_attention_prompt(const void* q, const void* k, const void* v, const int32_t* q_offsets,
                                 const int32_t* kv_offsets, int n_seqs, int Tq, int Tkv, int H, int H_kv, int D,
@@ -143,7 +155,10 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
   // The tensor cores take bf16 heads of up to 128 elements (a tile of longer ones does not fit in TMEM).
   if (dt == MOE_DTYPE_BF16 && D <= 128 && Tkv > 0) {
     bind_primary_context();
-    return cuda_status(launch_attn_prompt_tc(a, (cudaStream_t)stream));
+    int splits = attn_prompt_splits(n_seqs, Tq, Tkv, H, H_kv);
+    if (ws_bytes < prompt_ws_bytes((long long)Tq * H, splits, D)) splits = 1;
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes);
+    return cuda_status(launch_attn_prompt_tc(a, splits, part, (cudaStream_t)stream));
   }
   return cuda_status(launch_attn_prompt_simt(a, (cudaStream_t)stream));
 }

@@ -55,6 +55,7 @@ struct __align__(16) Item {
   int key0, n_keys;         // keys of the item
   int lim0, lim1;           // keys that each tile's last row sees (relative to key0)
   int last;                 // no item: the end
+  int split;                // which part of the keys
 };
 constexpr int kItems = 3;   // items published: one worked on, one ahead, one being given back
 constexpr int kItemReaders = 1 + 8 + 2;
@@ -143,16 +144,17 @@ __device__ __forceinline__ void exact_row(const __nv_bfloat16* q, const __nv_bfl
 
 struct SharedArgs {
   DecodeArgs d;
-  int per;        // keys of a split, a multiple of BK
-  int splits;
+  int per;        // keys of a split, a multiple of BK (decode)
+  int splits;     // pieces of a row
   float* part_o;  // [piece][D]
   float2* part_ml;
 };
 
 // SHARED = false: items are tile-pair slots (descending, so that the longest rows of a sequence start first) x key/value
 // heads, n_items of them. SHARED = true: one item a CTA, blockIdx = (key/value head, row pair, split of the shared keys);
-// rows are (sequence, head) pairs, and each row's piece goes to the workspace unnormalised.
-template <int DP, bool SHARED>
+// rows are (sequence, head) pairs, and each row's piece goes to the workspace unnormalised. SPLIT (prompts of few rows):
+// every item's keys in sa.splits parts, an item each, and the rows' pieces likewise.
+template <int DP, bool SHARED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs pa,
@@ -261,18 +263,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const int w = __shfl_sync(0xffffffffu, ahead, 0);
           if (w >= n_items) return;
           ahead = take();
-          const int slot = (n_items - 1 - w) / Hkv;
+          const int parts = SPLIT ? sa.splits : 1, v = w / parts;
+          const int slot = (n_items / parts - 1 - v) / Hkv;
           const int i = find_tile_seq_warp(pa.qo, pa.n, G, 2 * TM, slot);
           const Seq sq = load_seq_warp(pa, i);
           const long long r0 = ((long long)slot - ((long long)sq.q0 * G / (2 * TM) + i)) * (2 * TM);
           if (r0 < 0 || r0 >= (long long)sq.nq * G) continue;  // a slot that no tile fills
-          it.hk = w % Hkv;
+          it.hk = v % Hkv;
           it.row0 = (int)r0;
           it.nrows = min(2 * TM, sq.nq * G - it.row0);
           it.q0 = sq.q0; it.nq = sq.nq; it.k0 = sq.k0; it.nk = sq.nk;
           it.lim0 = visible_keys((it.row0 + min(it.nrows, TM) - 1) / G, sq.nq, sq.nk, pa.causal);
           it.lim1 = it.nrows > TM ? visible_keys((it.row0 + it.nrows - 1) / G, sq.nq, sq.nk, pa.causal) : 0;
           it.n_keys = max(it.lim0, it.lim1);
+          if (SPLIT) {
+            it.split = w % parts;
+            const int per = (blocks(it.n_keys) + parts - 1) / parts * BK;
+            it.key0 = (int)min((long long)it.split * per, (long long)it.n_keys);
+            it.n_keys = min(it.n_keys - it.key0, per);
+            it.lim0 = max(0, min(it.lim0 - it.key0, it.n_keys));
+            it.lim1 = max(0, min(it.lim1 - it.key0, it.n_keys));
+          }
           it.last = 0;
           return;
         }
@@ -528,6 +539,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         lim = slot < 0 || slot >= sa.d.c.n_slots ? 0 : max(0, min(it->n_keys, sa.d.c.lens[slot] - it->key0));
       } else if (valid) {
         lim = visible_keys(tok, it->nq, it->nk, pa.causal);
+        if (SPLIT) lim = max(0, min(lim - it->key0, it->n_keys));
       }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++done) {
@@ -621,8 +633,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc_fence_after();
       }
       if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-        if (SHARED) {
-          const long long piece = ((long long)tok * H + h) * sa.splits + blockIdx.z;
+        if (SHARED || SPLIT) {
+          const long long piece = SHARED ? ((long long)tok * H + h) * sa.splits + blockIdx.z
+                                         : ((long long)(it->q0 + tok) * H + h) * sa.splits + it->split;
           const float* orow = sa.part_o + piece * D;
           const uint32_t stg = sOut + warp * C::kStage;  // 32 elements a step through shared memory, as below
           bool fine = true;
@@ -656,25 +669,37 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             __syncwarp();
           }
           if (valid) sa.part_ml[piece] = make_float2(m * c2, l);
-          uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && lim < it->n_keys);
+          uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && (SPLIT || lim < it->n_keys));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
             const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
             const int limw = __shfl_sync(0xffffffffu, lim, w);
-            const CacheView& cv = sa.d.c;
-            const int32_t* row = cv.table + (long long)sa.d.slots[tw] * cv.width;
             float o[4], mw, lw;
-            exact_row((const __nv_bfloat16*)sa.d.q + (long long)tw * sa.d.qs + (long long)hw * D,
-                      (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v,
-                      [&](int j, long long& ko, long long& vo) {
-                        const int p = it->key0 + j;
-                        int page = row[p >> cv.page_shift];
-                        page = page < 0 || page >= cv.n_pages ? 0 : page;
-                        ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
-                      },
-                      D, limw, c2, o, mw, lw);
-            const long long pw = ((long long)tw * H + hw) * sa.splits + blockIdx.z;
+            long long pw = ((long long)tw * H + hw) * sa.splits + blockIdx.z;
+            if (SPLIT) {
+              pw = ((long long)(it->q0 + tw) * H + hw) * sa.splits + it->split;
+              exact_row((const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                        (const __nv_bfloat16*)pa.k + (long long)(it->k0 + it->key0) * pa.ks + (long long)it->hk * D,
+                        (const __nv_bfloat16*)pa.v + (long long)(it->k0 + it->key0) * pa.vs + (long long)it->hk * D,
+                        [&](int j, long long& ko, long long& vo) {
+                          ko = (long long)j * pa.ks;
+                          vo = (long long)j * pa.vs;
+                        },
+                        D, limw, c2, o, mw, lw);
+            } else {
+              const CacheView& cv = sa.d.c;
+              const int32_t* row = cv.table + (long long)sa.d.slots[tw] * cv.width;
+              exact_row((const __nv_bfloat16*)sa.d.q + (long long)tw * sa.d.qs + (long long)hw * D,
+                        (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v,
+                        [&](int j, long long& ko, long long& vo) {
+                          const int p = it->key0 + j;
+                          int page = row[p >> cv.page_shift];
+                          page = page < 0 || page >= cv.n_pages ? 0 : page;
+                          ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
+                        },
+                        D, limw, c2, o, mw, lw);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (lane * 4 + e < D) sa.part_o[pw * D + lane * 4 + e] = o[e];
@@ -763,6 +788,57 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   }
 }
 
+// A row's pieces in their order, a warp each, eight pieces on their way at a time.
+__global__ void __launch_bounds__(128)
+prompt_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ SharedArgs sa) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (long long)a.Tq * a.H) return;
+  const int tok = (int)(row / a.H), h = (int)(row % a.H);
+  const Seq sq = load_seq_warp(a, find_tile_seq_warp(a.qo, a.n, 1, 1, tok, 0));
+  if (tok < sq.q0 || tok >= sq.q0 + sq.nq) return;  // not a row of a sequence (or of one with bad offsets)
+  const long long p0 = row * sa.splits;
+  float M = -INFINITY, l = 0.f;
+  for (int i = lane; i < sa.splits; i += 32) M = fmaxf(M, sa.part_ml[p0 + i].x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  const float ref = M == -INFINITY ? 0.f : M;
+  const bool on = lane * 4 < a.D;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < sa.splits; i0 += 32) {
+    const float2 v = i0 + lane < sa.splits ? sa.part_ml[p0 + i0 + lane] : make_float2(-INFINITY, 0.f);
+    const float wl = ex2(v.x - ref);
+    l += wl * v.y;
+    for (int y0 = 0; y0 < 32 && i0 + y0 < sa.splits; y0 += 8) {
+      float4 u[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        u[y] = on && i0 + y0 + y < sa.splits
+                   ? reinterpret_cast<const float4*>(sa.part_o + (p0 + i0 + y0 + y) * a.D)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xffffffffu, wl, y0 + y);
+        o.x = fmaf(w, u[y].x, o.x);
+        o.y = fmaf(w, u[y].y, o.y);
+        o.z = fmaf(w, u[y].z, o.z);
+        o.w = fmaf(w, u[y].w, o.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  if (on) {
+    uint2 u;
+    u.x = pack_bf16x2(o.x * inv, o.y * inv);
+    u.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * a.D + lane * 4) = u;
+  }
+  if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
 bool encode3(EncodeTiledFn enc, CUtensorMap* m, const void* p, int D, int heads, int T, long long stride, int box_heads,
              int box_rows) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
@@ -776,11 +852,11 @@ bool encode_q(EncodeTiledFn enc, CUtensorMap* m, const void* p, int D, int H, in
   return !*ok || encode3(enc, m, p, D, H, T, stride, G, TM / G);
 }
 
-template <int DP, bool SHARED>
+template <int DP, bool SHARED, bool SPLIT>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PromptArgs& pa,
                    const SharedArgs& sa, dim3 grid, int n_items, int q_tma, cudaStream_t s) {
   static std::atomic<int> done{0};
-  auto kern = attn_tc_kernel<DP, SHARED>;
+  auto kern = attn_tc_kernel<DP, SHARED, SPLIT>;
   const cudaError_t e = allow_smem(kern, Cfg<DP>::kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), Cfg<DP>::kSmem, s, tq, tk, tv, pa, sa, n_items, q_tma);
@@ -788,7 +864,15 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 
 }  // namespace
 
-cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s) {
+// Few items: each item's keys in as many parts as fill the SMs, four blocks a part at least where the keys are one
+// sequence's.
+int attn_prompt_splits(int n, int Tq, int Tkv, int H, int Hkv) {
+  const long long items = prompt_tile_slots(Tq, n, H / Hkv, 2 * TM) * Hkv;
+  const long long most = Tkv / (4 * BK), fill = items > 0 ? device_sm_count() / items : 1;
+  return (int)(fill < most ? (fill < 1 ? 1 : fill) : (most < 1 ? 1 : most));
+}
+
+cudaError_t launch_attn_prompt_tc(const PromptArgs& a, int splits, float* part, cudaStream_t s) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return cudaErrorNotSupported;
   CUtensorMap tq{}, tk{}, tv{};
@@ -798,11 +882,19 @@ cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s) {
       !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma))
     return cudaErrorInvalidValue;
   const long long slots = prompt_tile_slots(a.Tq, a.n, G, 2 * TM);
-  const SharedArgs none{};
-  const long long items = slots * a.Hkv;
+  SharedArgs sa{};
+  sa.splits = splits;
+  sa.part_o = part;
+  sa.part_ml = reinterpret_cast<float2*>(part + (long long)a.Tq * a.H * splits * a.D);
+  const long long items = slots * a.Hkv * splits;
   const dim3 grid((unsigned)(items < device_sm_count() ? items : device_sm_count()));
-  return a.D <= 64 ? launch<64, false>(tq, tk, tv, a, none, grid, (int)items, q_tma, s)
-                   : launch<128, false>(tq, tk, tv, a, none, grid, (int)items, q_tma, s);
+  if (splits == 1)
+    return a.D <= 64 ? launch<64, false, false>(tq, tk, tv, a, sa, grid, (int)items, q_tma, s)
+                     : launch<128, false, false>(tq, tk, tv, a, sa, grid, (int)items, q_tma, s);
+  const cudaError_t e = a.D <= 64 ? launch<64, false, true>(tq, tk, tv, a, sa, grid, (int)items, q_tma, s)
+                                  : launch<128, false, true>(tq, tk, tv, a, sa, grid, (int)items, q_tma, s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prompt_join_kernel, dim3((unsigned)(((long long)a.Tq * a.H + 3) / 4)), dim3(128), 0, s, a, sa);
 }
 
 // One CTA an SM takes 256 rows of one key/value head, the keys split over the SMs; about a sixth of those (where splits
@@ -833,8 +925,8 @@ cudaError_t launch_attn_shared_tc(const DecodeArgs& a, const CacheMaps& m, int s
   const PromptArgs none{};
   const long long pairs = (a.n * (long long)(a.H / a.c.Hkv) + 2 * TM - 1) / (2 * TM);
   const dim3 grid((unsigned)a.c.Hkv, (unsigned)pairs, (unsigned)splits);
-  return a.c.D <= 64 ? launch<64, true>(tq, m.k128, m.v128, none, sa, grid, 0, q_tma, s)
-                     : launch<128, true>(tq, m.k128, m.v128, none, sa, grid, 0, q_tma, s);
+  return a.c.D <= 64 ? launch<64, true, false>(tq, m.k128, m.v128, none, sa, grid, 0, q_tma, s)
+                     : launch<128, true, false>(tq, m.k128, m.v128, none, sa, grid, 0, q_tma, s);
 }
 
 }  // namespace moe

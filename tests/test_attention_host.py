@@ -152,3 +152,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
 
 def test_no_stream_records_without_a_gpu():
     assert _lib.lib().moe_stream_capture_id(None) == 0
+
+
+def test_prompt_workspace_bytes():
+    f = _lib.lib().moe_attention_prompt_workspace_bytes
+    assert f(0, 0, 0, 8, 2, 64, moe.MOE_DTYPE_BF16) == 256
+    assert f(1, 16, 1000, 8, 2, 64, moe.MOE_DTYPE_BF16) == 256      # few keys
+    assert f(1, 16, 100000, 8, 2, 64, moe.MOE_DTYPE_F32) == 256     # fp32 needs none
+    assert f(1, 16, 100000, 8, 2, 136, moe.MOE_DTYPE_BF16) == 256
+    assert f(1, 16, 100000, 8, 2, 64, moe.MOE_DTYPE_BF16) % 256 == 0
+    for args in [(-1, 16, 16, 8, 2, 64, 0), (1, -1, 16, 8, 2, 64, 0), (1, 16, -1, 8, 2, 64, 0), (1, 16, 16, 7, 2, 64, 0),
+                 (1, 16, 16, 8, 2, 60, 0), (1, 16, 16, 8, 2, 264, 0), (1, 16, 16, 8, 2, 64, 7), (1, 1 << 30, 16, 8, 2, 64, 0),
+                 (1, 16, 16, 8, 0, 64, 0)]:
+        assert f(*args) == 0, args

@@ -139,6 +139,81 @@ def test_prompt_nonfinite_stays_where_it_is_seen(value, D, dtype):
             assert torch.isfinite(hurt).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("-inf")])
+def test_prompt_split_keys_nonfinite(value, dtype):
+    """The same where the keys of few rows are split over CTAs: a position that some rows do not see, in the last part."""
+    nq, nk, H, Hk, D = [8, 20, 1], [2000, 900, 1200], 4, 2, 128
+    Tq, Tk, at = sum(nq), sum(nk), 2000 - 3  # seen by the last three tokens of sequence 0
+    q = tensor((Tq, H, D), 1, dtype, DEV)
+    k, v = tensor((Tk, Hk, D), 2, dtype, DEV), tensor((Tk, Hk, D), 3, dtype, DEV)
+    qo, ko = offsets(nq), offsets(nk)
+    ref = prompt_reference(q, k, v, qo, ko, True, D ** -0.5)
+    a = moe.Attention(H, Hk, D, dtype)
+    keep = [t for t in range(Tq) if not 5 <= t < 8]
+    for bad in ("k", "v"):
+        kk, vv = k.clone(), v.clone()
+        (kk if bad == "k" else vv)[at, 1, 5] = value
+        out = a.prompt(q, kk, vv, i32(qo, DEV), i32(ko, DEV))
+        check(out[keep], None, tuple(x[keep] for x in ref), 2000, D, dtype)
+        check(out[:, :2], None, tuple(x[:, :2] for x in ref), 2000, D, dtype)
+        if bad == "v":
+            assert not torch.isfinite(out[5:8, 2:, 5]).any()
+            hurt = out[5:8, 2:].clone()
+            hurt[..., 5] = 0
+            assert torch.isfinite(hurt).all()
+    assert a.device_status()[0] == moe.MOE_OK
+
+
+def test_prompt_split_keys_bad_offsets():
+    """A sequence with bad offsets is recorded and its rows stay as they were; the others are computed."""
+    q, kv = tensor((24, 4, 64), 1, BF16, DEV), tensor((3000, 2, 64), 2, BF16, DEV)
+    a = moe.Attention(4, 2, 64, BF16)
+    for qo, ko, bad, rows in [([0, 8, 24], [0, 3001, 3000], (0, 1), range(0, 24)), ([0, 8, 25], [0, 1500, 3000], (1,), range(8, 24)),
+                              ([0, 8, 24], [0, 1500, 3004], (1,), range(8, 24))]:
+        out = torch.full((24, 4, 64), 7.0, dtype=BF16, device=DEV)
+        a.prompt(q, kv, kv, i32(qo, DEV), i32(ko, DEV), out=out)
+        st, seq = a.device_status()
+        assert st == moe.MOE_ERR_DEVICE_CHECK and seq in bad  # (of two, whichever is found first)
+        assert (out[list(rows)] == 7).all()
+        good = [t for t in range(24) if t not in rows]
+        if good:
+            ref = prompt_reference(q[good], kv[:1500], kv[:1500], [0, 8], [0, 1500], True, 64 ** -0.5)
+            check(out[good], None, ref, 1500, 64, BF16)
+
+
+def test_prompt_split_keys_with_little_workspace_and_in_a_graph():
+    nq, nk, H, Hk, D = [3, 40], [2500, 1000], 8, 2, 64
+    q, kv = tensor((43, H, D), 1, BF16, DEV), tensor((3500, Hk, D), 2, BF16, DEV)
+    qo, ko = offsets(nq), offsets(nk)
+    ref = prompt_reference(q, kv, kv, qo, ko, True, D ** -0.5)
+    a = moe.Attention(H, Hk, D, BF16)
+    lse = torch.empty((43, H), device=DEV)
+    first = a.prompt(q, kv, kv, i32(qo, DEV), i32(ko, DEV), lse=lse)
+    check(first, lse, ref, 2500, D, BF16)
+    need = a._lib.moe_attention_prompt_workspace_bytes(2, 43, 3500, H, Hk, D, moe.MOE_DTYPE_BF16)
+    assert need > 256
+    # a workspace of the least size: the same numbers without the split
+    ws, out = torch.zeros(need - 1, dtype=torch.uint8, device=DEV), torch.empty_like(first)
+    stream = torch.cuda.current_stream().cuda_stream
+    oq, ok = i32(qo, DEV), i32(ko, DEV)
+    for nbytes in (256, need - 1):
+        out.fill_(0)
+        assert a._lib.moe_attention_prompt(q.data_ptr(), kv.data_ptr(), kv.data_ptr(), oq.data_ptr(), ok.data_ptr(), 2, 43, 3500,
+                                           H, Hk, D, H * D, Hk * D, Hk * D, H * D, D ** -0.5, 1, moe.MOE_DTYPE_BF16,
+                                           out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nbytes, stream) == moe.MOE_OK
+        check(out, lse, ref, 2500, D, BF16)
+    g, o = torch.cuda.CUDAGraph(), torch.zeros_like(first)
+    with torch.cuda.graph(g):
+        a.prompt(q, kv, kv, oq, ok, out=o)
+    for _ in range(2):
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, first)
+    assert a.device_status()[0] == moe.MOE_OK
+
+
 def test_prompt_bad_offsets_are_recorded():
     q, kv = tensor((20, 4, 64), 1, BF16, DEV), tensor((20, 2, 64), 2, BF16, DEV)
     a = moe.Attention(4, 2, 64, BF16)
