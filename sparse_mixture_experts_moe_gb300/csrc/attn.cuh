@@ -10,6 +10,9 @@
 
 namespace moe {
 
+// Words of the workspace's header (see kWsHeaderBytes) besides the status: [6] the decode kernel's counter of runs taken, [7]
+// the prompt kernel's counter of items and [8] its count of finished CTAs. Zero between calls, like the others there.
+
 // Packed rows: the G = H / H_kv query heads that share a key/value head are laid side by side, row
 // r = token * G + g, so that one key/value tile serves all of them and short prompts or single tokens
 // still fill a tile's rows.
