@@ -10,8 +10,9 @@
 
 namespace moe {
 
-// Words of the workspace's header (see kWsHeaderBytes) besides the status: [6] the decode kernel's counter of runs taken, [7]
-// the prompt kernel's counter of items and [8] its count of finished CTAs. Zero between calls, like the others there.
+// Words of the workspace's header (see kWsHeaderBytes) besides the status: [6] the decode kernel's counter of runs
+// taken, [7] the prompt kernel's counter of items and [8] its count of finished CTAs. Zero between calls, like the
+// others there.
 
 // Packed rows: the G = H / H_kv query heads that share a key/value head are laid side by side, row
 // r = token * G + g, so that one key/value tile serves all of them and short prompts or single tokens
@@ -36,15 +37,15 @@ struct CacheView {
   long long layer_elems() const { return (long long)n_pages * Hkv * page_size * D; }
 };
 
-// Copy descriptors of a bf16 cache's pages: a layer's page rows ((page H_kv + head) page_size + row) x D, the layer as
-// the third coordinate; boxes of 64 elements x 16, min(page_size, 64) and min(page_size, 128) rows.
+// Copy descriptors of a bf16 cache's pages: a layer's page rows ((page H_kv + head) page_size + row) x D, the layer
+// as the third coordinate; boxes of 64 elements x 16, min(page_size, 64) and min(page_size, 128) rows.
 struct CacheMaps {
   CUtensorMap k16, v16, k64, v64, k128, v128;
 };
 bool encode_cache_maps(const CacheView& c, CacheMaps* m);
 
-// Sets a kernel's dynamic shared memory limit, once a device: the last device it was set for is remembered (setting it
-// again is harmless, so a race between threads is too).
+// Sets a kernel's dynamic shared memory limit, once a device: the last device it was set for is remembered (setting
+// it again is harmless, so a race between threads is too).
 template <typename Kernel>
 inline cudaError_t allow_smem(Kernel kern, size_t bytes, std::atomic<int>& done) {
   int dev = 0;

@@ -543,8 +543,8 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   if (a.d.shared > 0) griddep_wait();
 }
 
-// A (sequence, head)'s pieces over the shared keys, then over its own, by WPR warps that take every WPR-th piece and add
-// up in a fixed order: 4 while there are few rows, 1 (four rows a CTA) when the rows alone fill the GPU.
+// A (sequence, head)'s pieces over the shared keys, then over its own, by WPR warps that take every WPR-th piece and
+// add up in a fixed order: 4 while there are few rows, 1 (four rows a CTA) when the rows alone fill the GPU.
 template <int WPR>
 __global__ void __launch_bounds__(128)
 decode_join_kernel(const __grid_constant__ OwnArgs a) {

@@ -7,19 +7,21 @@
 // memory in fp32: packed prompts, and the shared positions of a decode batch (rows: every sequence's heads). 8
 // threads share a row, each with 4 rows x 8 keys of the scores and 4 rows x D / 8 columns of the output in registers.
 // Bound by reads of shared memory: a warp's 16-byte read takes four cycles whatever its lanes share, so an
-// element of the scores costs (4 + 8) * 4 cycles for 32 of arithmetic, one of the output 20 for 16; with 2 rows a thread
-// that was 40 for 16. Rows in shared memory have a length known to the compiler (D rounded up to 32, zeros past D): with
+// element of the scores costs (4 + 8) * 4 cycles for 32 of arithmetic, one of the output 20 for 16; with 2 rows a
+// thread that was 40 for 16. Rows in shared memory have a length known to the compiler (D rounded up to 32, zeros
+// past D): with
 // D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the place of the
 // keys once the scores are done; two CTAs then fit on an SM and one computes while the other loads.
-// Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s; bf16, 16 heads of 256
-// on 4: 30 TFLOP/s (one CTA an SM).
+// Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s; bf16, 16 heads of
+// 256 on 4: 30 TFLOP/s (one CTA an SM).
 //
 // decode_rows_kernel: the positions that a sequence does not share, an HBM stream that meets up to 8 rows, far too
-// few for tiles. Lanes lie along a head's elements; a warp takes 4 keys at a time straight from memory, its rows' products
-// with them are summed over the lanes in one exchange (each step halves the values a lane holds: 31 shuffles for
-// 32 sums), which leaves each lane one score. Keys are split over warps and CTAs, whose pieces join in a fixed order.
-// Bound by latency, each warp loading and computing in turn; the launch bounds are what measured best. fp32, heads of 128,
-// 4096 positions: 32 sequences of 8 heads 187 us (5.7 TB/s), 8 of 32 heads on 8 61 us (4.4 TB/s), 8 of 64 on 8 85 us.
+// few for tiles. Lanes lie along a head's elements; a warp takes 4 keys at a time straight from memory, its rows'
+// products with them are summed over the lanes in one exchange (each step halves the values a lane holds: 31
+// shuffles for 32 sums), which leaves each lane one score. Keys are split over warps and CTAs, whose pieces join in
+// a fixed order. Bound by latency, each warp loading and computing in turn; the launch bounds are what measured
+// best. fp32, heads of 128, 4096 positions: 32 sequences of 8 heads 187 us (5.7 TB/s), 8 of 32 heads on 8 61 us (4.4
+// TB/s), 8 of 64 on 8 85 us.
 #include "attn.cuh"
 #include "kernels.cuh"
 
@@ -264,8 +266,8 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
   asm volatile("cp.async.wait_all;" ::: "memory");
 
   if (SPLIT) {
-    // The cluster's CTAs hold parts of the same rows over different keys: they put them in shared memory, and each adds up
-    // every C-th row from all of them, in order.
+    // The cluster's CTAs hold parts of the same rows over different keys: they put them in shared memory, and each
+    // adds up every C-th row from all of them, in order.
     const int C = gridDim.z, rank = (int)cluster_ctarank();
     __syncthreads();
     float* po = Qs;
@@ -353,9 +355,9 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
 // ------------------------------------------------------------------ few rows
 constexpr int kRowWarps = 4;
 constexpr int NK = 4;  // keys of a warp's step
-// From this many sequences on the shared positions are read once for all by tiles; fewer read them each (4096 shared, fp32
-// heads of 128 on 4: two sequences of 4 heads 26 us by tiles, 16 each; four 22 and 21; eight 22 and 31; four of 32 heads
-// 25 and 28).
+// From this many sequences on the shared positions are read once for all by tiles; fewer read them each (4096
+// shared, fp32 heads of 128 on 4: two sequences of 4 heads 26 us by tiles, 16 each; four 22 and 21; eight 22 and 31;
+// four of 32 heads 25 and 28).
 constexpr int kSharedFrom = 4;
 
 // V4: groups of 4 elements of a lane (elements 4 lane + 128 x); GR: rows of a CTA.
@@ -367,8 +369,8 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
   __shared__ __align__(16) float2 ps[kRowWarps][NV];  // each weight twice, a packed factor
   __shared__ float sml[2][kRowWarps][GR];
   __shared__ __align__(16) float buf[kRowWarps][GR][V4 * 128];
-  // Behind the shared positions' kernel (first_piece > 0) this one need not wait for it: that kernel lets dependents start
-  // only once it has itself waited for everything before it, and only the join reads what it writes.
+  // Behind the shared positions' kernel (first_piece > 0) this one need not wait for it: that kernel lets dependents
+  // start only once it has itself waited for everything before it, and only the join reads what it writes.
   if (first_piece == 0) griddep_wait();
   griddep_launch_dependents();
   const CacheView& c = a.c;
@@ -553,8 +555,9 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
   if (first_piece > 0) griddep_wait();
 }
 
-// Joins a row's pieces in a fixed order, by WPR warps that take every WPR-th piece, eight on their way at a time: 4 while
-// there are few rows, 1 (four rows a CTA) when the rows alone fill the GPU. A lane holds elements 2 lane + 64 x.
+// Joins a row's pieces in a fixed order, by WPR warps that take every WPR-th piece, eight on their way at a time: 4
+// while there are few rows, 1 (four rows a CTA) when the rows alone fill the GPU. A lane holds elements 2 lane + 64
+// x.
 template <typename T, int WPR>
 __global__ void __launch_bounds__(128)
 decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
@@ -687,8 +690,8 @@ cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
   const long long slots = prompt_tile_slots(a.Tq, a.n, a.H / a.Hkv, kRows);
   const SharedPart none{};
   // Few tiles: a cluster of CTAs takes the keys of each, at least two tiles of them where the keys are one sequence's
-  // (fp32, 1024 tokens of 8 heads of 128: 183 us without, 116 with two CTAs; 18 tokens of two sequences behind up to 1100
-  // keys: 98 without, 58 with eight).
+  // (fp32, 1024 tokens of 8 heads of 128: 183 us without, 116 with two CTAs; 18 tokens of two sequences behind up to
+  // 1100 keys: 98 without, 58 with eight).
   int C = 1;
   while (C < kMaxCluster && slots * a.Hkv * 2 * C <= 2LL * device_sm_count() && a.Tkv >= 4 * C * KT) C *= 2;
   const dim3 grid((unsigned)slots, (unsigned)a.Hkv, (unsigned)C);

@@ -4,17 +4,17 @@
 // with m a running reference of each row and l the sum of its weights, in one pass over the keys: no score
 // ever leaves the SM.
 //
-// An item is 256 packed rows (two tiles of 128) of one key/value head; the tiles share every key/value block (128 keys),
-// which halves the reads of L2 against one tile an item. One CTA an SM takes items from a counter, the longest rows
-// of a sequence first, and its warps walk the items one behind the other:
+// An item is 256 packed rows (two tiles of 128) of one key/value head; the tiles share every key/value block (128
+// keys), which halves the reads of L2 against one tile an item. One CTA an SM takes items from a counter, the
+// longest rows of a sequence first, and its warps walk the items one behind the other:
 //   warps 0..3, 4..7  softmax of tile 0 / 1: thread = row = TMEM lane. Reads S, takes the maximum, writes P
 //                     (bf16) over S's own columns, sums the weights; at the end divides and stores the rows
 //   warp 8            allocates TMEM; one elected thread issues every MMA: QK with both operands in shared memory, PV
 //                     with P read from TMEM as the A operand
 //   warp 9            finds the items, one ahead, and loads K and V blocks by TMA into a ring (K0 V0 K1 V1 ...)
 //   warps 10, 11      load the Q tiles of the next item as soon as the last QK of this one is done
-// so an item's first loads, its search and its first scores overlap the end of the item before. (With a CTA for each item
-// these cost 9 us an item, as much as six blocks of keys.)
+// so an item's first loads, its search and its first scores overlap the end of the item before. (With a CTA for each
+// item these cost 9 us an item, as much as six blocks of keys.)
 // TMEM (512 columns): S0 S1 (128 fp32 columns each, P in the first 64), O0 O1.
 // The MMAs go PV0(j) QK0(j+1) PV1(j) QK1(j+1): while one tile is in softmax the tensor cores work on the
 // other. QK(j+1) may overwrite P(j) because MMAs of one thread run in issue order.
@@ -29,10 +29,10 @@
 // non-finite value reaches only rows that see it. That costs nothing where everything is finite.
 // All waits are bounded, as in ffn_tc.cu.
 // Measured: one prompt of 16384 tokens, 32 heads of 128 on 8: 1.37 ms, 1.61 PFLOP/s, 85% of the measured matrix rate.
-// What is left: a tile's softmax (reading S, the maximum, 128 powers of two a thread, storing P) takes about as long as the
-// other tile's MMAs, so the tensor pipe waits at each exchange (8192 tokens: tensor pipe 70%, the pipe of the powers 35%,
-// issue 39%). 13 ragged prompts, 8192 tokens together, same heads: 104 us; the masked block of a row, its epilogue and
-// the first scores cost about 3.5 us an item (taking the longest sequences first gains 1 us).
+// What is left: a tile's softmax (reading S, the maximum, 128 powers of two a thread, storing P) takes about as long
+// as the other tile's MMAs, so the tensor pipe waits at each exchange (8192 tokens: tensor pipe 70%, the pipe of the
+// powers 35%, issue 39%). 13 ragged prompts, 8192 tokens together, same heads: 104 us; the masked block of a row,
+// its epilogue and the first scores cost about 3.5 us an item (taking the longest sequences first gains 1 us).
 #include <cuda.h>
 
 #include "attn.cuh"
@@ -151,10 +151,10 @@ struct SharedArgs {
   float2* part_ml;
 };
 
-// SHARED = false: items are tile-pair slots (descending, so that the longest rows of a sequence start first) x key/value
-// heads, n_items of them. SHARED = true: one item a CTA, blockIdx = (key/value head, row pair, split of the shared keys);
-// rows are (sequence, head) pairs, and each row's piece goes to the workspace unnormalised. SPLIT (prompts of few rows):
-// every item's keys in sa.splits parts, an item each, and the rows' pieces likewise.
+// SHARED = false: items are tile-pair slots (descending, so that the longest rows of a sequence start first) x
+// key/value heads, n_items of them. SHARED = true: one item a CTA, blockIdx = (key/value head, row pair, split of
+// the shared keys); rows are (sequence, head) pairs, and each row's piece goes to the workspace unnormalised. SPLIT
+// (prompts of few rows): every item's keys in sa.splits parts, an item each, and the rows' pieces likewise.
 template <int DP, bool SHARED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -203,16 +203,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
-  // Only after TMEM is allocated: a dependent kernel that starts on this SM may allocate some before it waits for this
-  // grid. And only after the wait: the decode's own-key kernel relies on everything before this grid being done.
+  // Only after TMEM is allocated: a dependent kernel that starts on this SM may allocate some before it waits for
+  // this grid. And only after the wait: the decode's own-key kernel relies on everything before this grid being done.
   griddep_launch_dependents();
 
   const int H = SHARED ? sa.d.H : pa.H, Hkv = SHARED ? sa.d.c.Hkv : pa.Hkv, D = SHARED ? sa.d.c.D : pa.D;
   const int G = H / Hkv;
   int* status = SHARED ? sa.d.status : pa.status;
   const uint64_t timeout_ns = SHARED ? sa.d.timeout_ns : pa.timeout_ns;
-  // The items, for every warp but the one that finds them: the next one (nullptr after the last), and giving it back. The
-  // fields are read where they are needed, as the softmax warps have no registers to keep them in.
+  // The items, for every warp but the one that finds them: the next one (nullptr after the last), and giving it
+  // back. The fields are read where they are needed, as the softmax warps have no registers to keep them in.
   int iq = 0;
   uint32_t iphase = 0;
   auto next_item = [&]() -> const Item* {
@@ -315,7 +315,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (SHARED) {
               const int rows = min(sa.d.c.page_size, BK);
               for (int r = 0; r < BK; r += rows) {
-                // past the shared keys the last page again: those columns are masked, their values finite or seen anyway
+                // past the shared keys the last page again: those columns are masked, their values finite or seen
+                // anyway
                 const int p = min((j0 + r) >> sa.d.c.page_shift, pages - 1);
                 int page = table[p];
                 page = page < 0 || page >= sa.d.c.n_pages ? 0 : page;
@@ -336,8 +337,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       };
-      // The next item is taken when this one's last ring of copies is due: early enough for its Q to be on its way in time,
-      // and no earlier, as a long item would keep it from the CTAs that are idle by then.
+      // The next item is taken when this one's last ring of copies is due: early enough for its Q to be on its way
+      // in time, and no earlier, as a long item would keep it from the CTAs that are idle by then.
       Item it, nx;
       find(it);
       bool ok = publish(it);
@@ -362,9 +363,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       __syncwarp();
     } else if (warp > kSoftWarps + 1) {
       // -------------------------------------------------------------- Q tiles, the swizzled K-major operand. Where the
-      // group's heads divide a tile's rows one TMA box is 128 / G tokens of G heads, in the packed rows' order (rows past
-      // the end hold whatever comes next: they see no key and are not stored). Else kLanes lanes copy a row, with zeros
-      // past the rows and past D: 5 us a tile, against 1.5.
+      // group's heads divide a tile's rows one TMA box is 128 / G tokens of G heads, in the packed rows' order (rows
+      // past the end hold whatever comes next: they see no key and are not stored). Else kLanes lanes copy a row,
+      // with zeros past the rows and past D: 5 us a tile, against 1.5.
       constexpr int kLanes = DP / 8, kRowsPer = 32 / kLanes;
       const int t = warp - kSoftWarps - 2;
       uint32_t loads = 0;
@@ -708,7 +709,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
         } else {
           const float inv = l == 0.f ? 0.f : 1.0f / l;
-          // 64 elements a step through shared memory, so that a store covers 4 rows and not 32 (2.2 -> 0.8 us an item)
+          // 64 elements a step through shared memory, so that a store covers 4 rows and not 32 (2.2 -> 0.8 us an
+          // item)
           __nv_bfloat16* orow = (__nv_bfloat16*)pa.out + (long long)(it->q0 + tok) * pa.os + (long long)h * D;
           const uint32_t stg = sOut + warp * C::kStage;
           const uint64_t inv2 = f2_pack(inv, inv);
@@ -866,8 +868,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 }  // namespace
 
 // Few items: each item's keys in as many parts as fill the SMs, four blocks a part at least where the keys are one
-// sequence's. Heads of 128, 32 on 8: 16 tokens with 1024 keys 14 us in two parts, 17 in one; 4096 keys 17 and 52; 32768 44 and
-// 392; 512 tokens behind 4096 41 and 54. 1024 tokens of their own (half the keys masked), 8 heads: 18 and 17.
+// sequence's. Heads of 128, 32 on 8: 16 tokens with 1024 keys 14 us in two parts, 17 in one; 4096 keys 17 and 52;
+// 32768 44 and 392; 512 tokens behind 4096 41 and 54. 1024 tokens of their own (half the keys masked), 8 heads: 18
+// and 17.
 int attn_prompt_splits(int n, int Tq, int Tkv, int H, int Hkv) {
   const long long items = prompt_tile_slots(Tq, n, H / Hkv, 2 * TM) * Hkv;
   const long long most = Tkv / (4 * BK), fill = items > 0 ? device_sm_count() / items : 1;
@@ -899,9 +902,9 @@ cudaError_t launch_attn_prompt_tc(const PromptArgs& a, int splits, float* part, 
   return launch_pdl(prompt_join_kernel, dim3((unsigned)(((long long)a.Tq * a.H + 3) / 4)), dim3(128), 0, s, a, sa);
 }
 
-// One CTA an SM takes 256 rows of one key/value head, the keys split over the SMs; about a sixth of those (where splits
-// can be had) are left to the own keys, which run beside. 64 sequences behind 32768 positions, own keys up to 2048:
-// see launch_attn_decode_tc.
+// One CTA an SM takes 256 rows of one key/value head, the keys split over the SMs; about a sixth of those (where
+// splits can be had) are left to the own keys, which run beside. 64 sequences behind 32768 positions, own keys up to
+// 2048: see launch_attn_decode_tc.
 int attn_shared_splits(const DecodeArgs& a) {
   const long long units = (long long)a.c.Hkv * ((a.n * (long long)(a.H / a.c.Hkv) + 2 * TM - 1) / (2 * TM));
   const int blocks = (a.shared + BK - 1) / BK;
