@@ -22,7 +22,7 @@
 // then stay below 2^8, exact enough for bf16 as only their relative precision counts); the softmax
 // warp that sees it waits for the last PV and scales the 32 rows of O itself. After the first blocks
 // that is rare, so no warps are kept for it.
-// A weight is rounded to bf16 (half a step, 2^-9 of it) because the MMA takes both operands in one type; its
+// A weight is rounded to bf16 (off by at most 2^-8 of it) because the MMA takes both operands in one type; its
 // sum l takes the unrounded value.
 // Keys past a row's limit get weight 0 by index. 0 times a non-finite value in V would still be NaN: a row whose
 // result is not finite is computed again, key by key over the keys it sees (exact_row), so that a
