@@ -28,11 +28,12 @@
 // result is not finite is computed again, key by key over the keys it sees (exact_row), so that a
 // non-finite value reaches only rows that see it. That costs nothing where everything is finite.
 // All waits are bounded, as in ffn_tc.cu.
-// Measured: one prompt of 16384 tokens, 32 heads of 128 on 8: 1.37 ms, 1.61 PFLOP/s, 85% of the measured matrix rate.
-// What is left: a tile's softmax (reading S, the maximum, 128 powers of two a thread, storing P) takes about as long
-// as the other tile's MMAs, so the tensor pipe waits at each exchange (8192 tokens: tensor pipe 70%, the pipe of the
-// powers 35%, issue 39%). 13 ragged prompts, 8192 tokens together, same heads: 104 us; the masked block of a row,
-// its epilogue and the first scores cost about 3.5 us an item (taking the longest sequences first gains 1 us).
+// Measured: one prompt of 16384 tokens, 32 heads of 128 on 8: 1.23 ms in a run of ten (1.79 PFLOP/s, 94% of the matrix
+// rate measured in a burst), 1.35 ms in a loop of seconds (1.63, 94% of the sustained rate). Heads of 64: 1.03 ms,
+// 1.06 PFLOP/s, bound by the powers of two: 256 warp instructions of 8 cycles a scheduler and block of a tile pair are
+// 2048 of 2300 cycles (scores computed one block ahead, so that no softmax waits for an MMA, gained nothing).
+// 13 ragged prompts, 8192 tokens together, heads of 128: 104 us; the masked block of a row, its epilogue and the first
+// scores cost about 3.5 us an item (taking the longest sequences first gains 1 us).
 #include <cuda.h>
 
 #include "attn.cuh"
