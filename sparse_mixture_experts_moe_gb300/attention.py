@@ -71,7 +71,7 @@ class _Bound:
         self._lib = _lib.lib()
         self._i32 = torch.int32
         self._f32 = torch.float32
-        self._empty = torch.empty
+        self._empty, self._empty_like = torch.empty, torch.empty_like
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._ws = _Workspaces(self._lib, self._init_workspace)
@@ -261,6 +261,7 @@ class Attention(_Bound):
             raise ValueError("Attention: heads must be a multiple of kv_heads, head_dim a multiple of 8 from 8 to 256")
         self.scale = float(scale) if scale is not None else self.head_dim ** -0.5
         super().__init__()
+        self._sized, self._sized_bytes = None, 0
         self._prompt_bytes = self._lib.moe_attention_prompt_workspace_bytes
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
         self._key = (self.kv_heads, self.head_dim, self.dtype)
@@ -279,7 +280,7 @@ class Attention(_Bound):
         if out is None:
             if stream is not None:  # a tensor made here belongs to the current stream
                 raise ValueError("moe: pass out with an explicit stream")
-            out = self._empty(q.shape, dtype=self.dtype, device=q.device)
+            out = self._empty_like(q) if q.is_contiguous() else self._empty(q.shape, dtype=self.dtype, device=q.device)
             so = self.heads * self.head_dim
         else:
             to, so = _heads(out, "out", self.heads, self.head_dim, self.dtype, dev)
@@ -313,7 +314,10 @@ class Attention(_Bound):
         s = self._raw_stream(dev) if stream is None else _stream(stream)
         need = _HEADER
         if Tk >= _SPLIT_KEYS:
-            need = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
+            if self._sized != (n, Tq, Tk):  # the layers of a model call with the same sizes
+                self._sized_bytes = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
+                self._sized = (n, Tq, Tk)
+            need = self._sized_bytes
         ws = self._ws.get(s, need, dev)
         _check(self._prompt(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
