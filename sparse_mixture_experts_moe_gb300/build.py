@@ -23,7 +23,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 LIB_SOURCES = ["api.cu", "router.cu", "router_tc.cu", "router_small.cu", "dispatch.cu", "dispatch_noalloc.cu",
                "ffn_simt.cu", "ffn_stream.cu", "ffn_tc.cu", "ffn_tc2.cu", "combine.cu", "graph.cu", "quant.cu",
-               "ffn_tct.cu", "attn_api.cu", "attn_simt.cu", "attn_tc.cu",
+               "ffn_tct.cu", "attn_api.cu", "attn_simt.cu", "attn_mma.cu", "attn_tc.cu",
                "attn_decode.cu", "kvcache.cu"]
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 INPUTGEN_SRC = os.path.join(ROOT, "inputgen", "fill.cu")

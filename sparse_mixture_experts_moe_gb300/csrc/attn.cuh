@@ -78,7 +78,8 @@ struct DecodeArgs {
 // Pieces that a call may have: 4 a row, and enough for every SM to hold several pieces of many rows.
 constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
 
-cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);
+cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);  // fp32
+cudaError_t launch_attn_prompt_mma(const PromptArgs& a, cudaStream_t s);   // bf16, any D
 // bf16, D <= 128, at least one key.
 // splits: attn_prompt_splits or 1; part: Tq H splits (D + 2) floats where there are several.
 int attn_prompt_splits(int n, int Tq, int Tkv, int H, int Hkv);
@@ -181,6 +182,20 @@ __device__ __forceinline__ int visible_keys(int t, int nq, int nk, int causal) {
   if (!causal) return nk;
   const int lim = t + 1 + nk - nq;
   return lim < 0 ? 0 : (lim > nk ? nk : lim);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // try_wait that may sleep for up to 20 us. Without the hint it comes back after some tens of cycles, and warps that

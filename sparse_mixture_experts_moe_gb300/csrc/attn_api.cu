@@ -152,7 +152,7 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
   a.out = out; a.lse = lse;
   a.status = static_cast<int*>(workspace);
   a.timeout_ns = wait_timeout_ns();
-  // The tensor cores take bf16 heads of up to 128 elements (a tile of longer ones does not fit in TMEM).
+  // bf16 heads of up to 128 elements go to tcgen05 (a tile of longer ones does not fit in TMEM); its copies need a key.
   if (dt == MOE_DTYPE_BF16 && D <= 128 && Tkv > 0) {
     bind_primary_context();
     int splits = attn_prompt_splits(n_seqs, Tq, Tkv, H, H_kv);
@@ -160,7 +160,8 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
     float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes);
     return cuda_status(launch_attn_prompt_tc(a, splits, part, (cudaStream_t)stream));
   }
-  return cuda_status(launch_attn_prompt_simt(a, (cudaStream_t)stream));
+  return cuda_status(dt == MOE_DTYPE_BF16 ? launch_attn_prompt_mma(a, (cudaStream_t)stream)
+                                          : launch_attn_prompt_simt(a, (cudaStream_t)stream));
 }
 
 size_t moe_attention_workspace_bytes(int n, int H, int D) {

@@ -1,4 +1,4 @@
-// Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and heads of more than 128.
+// Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and decode with heads of more than 128.
 //   out[r] = sum_{j < lim(r)} softmax_j(scale q[r] . k[j]) v[j]
 // Scores are kept in log2 units (times scale * log2 e), so a weight is one 2^x. Keys past a row's limit are left
 // out of both products by index, not by a zero weight, so that a non-finite value there stays there.
@@ -12,8 +12,7 @@
 // past D): with
 // D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the place of the
 // keys once the scores are done; two CTAs then fit on an SM and one computes while the other loads.
-// Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s; bf16, 16 heads of
-// 256 on 4: 30 TFLOP/s (one CTA an SM).
+// Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s.
 //
 // decode_rows_kernel: the positions that a sequence does not share, an HBM stream that meets up to 8 rows, far too
 // few for tiles. Lanes lie along a head's elements; a warp takes 4 keys at a time straight from memory, its rows'
@@ -68,7 +67,7 @@ struct SharedPart {
 };
 
 // SHARED: rows and keys of a decode call, in pieces. SPLIT: a tile's keys over a cluster (in a kernel without it the
-// code for it would cost registers: 3% of fp32's time, 12% of bf16's with heads of 256).
+// code for it would cost registers and 3% of the time).
 template <typename T, int DP, bool SHARED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ SharedPart sp) {
@@ -655,12 +654,13 @@ cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, dim3 grid, 
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, pa, sp);
 }
-// bf16 comes here with heads of more than 128 only.
+// bf16 comes here with the shared positions of heads of more than 128 only.
 template <bool SHARED, bool SPLIT>
 cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, int dt, int D, dim3 grid, cudaStream_t s) {
-  if (dt == MOE_DTYPE_BF16)
-    return D <= 192 ? launch_tiles<__nv_bfloat16, 192, SHARED, SPLIT>(pa, sp, grid, s)
-                    : launch_tiles<__nv_bfloat16, 256, SHARED, SPLIT>(pa, sp, grid, s);
+  if constexpr (SHARED)
+    if (dt == MOE_DTYPE_BF16)
+      return D <= 192 ? launch_tiles<__nv_bfloat16, 192, SHARED, SPLIT>(pa, sp, grid, s)
+                      : launch_tiles<__nv_bfloat16, 256, SHARED, SPLIT>(pa, sp, grid, s);
   if (D <= 64) return launch_tiles<float, 64, SHARED, SPLIT>(pa, sp, grid, s);
   if (D <= 96) return launch_tiles<float, 96, SHARED, SPLIT>(pa, sp, grid, s);
   if (D <= 128) return launch_tiles<float, 128, SHARED, SPLIT>(pa, sp, grid, s);
