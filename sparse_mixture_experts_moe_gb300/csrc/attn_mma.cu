@@ -8,6 +8,8 @@
 // while its softmax runs, its V while the next scores do, and two CTAs share an SM (96 KB and up to 255 registers each).
 // The scores' accumulators are the second product's A operand as they lie. Weights are rounded to bf16 (off by at most
 // 2^-8 of each) as that operand; l takes them unrounded.
+// Bound by the MMA's operands: each 16 x 16 piece of K or V read from shared memory meets only the warp's 16 rows. 4096
+// tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us.
 // A row whose result is not finite is computed again over the keys that it sees, as in attn_tc.cu: 0 times a
 // non-finite value that the row does not see must not reach it.
 #include "attn.cuh"
@@ -17,6 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 64, KT = 64, kThreads = 128;
+constexpr int kMaxCluster = 8;
 
 template <int DP> constexpr size_t mma_smem() { return (size_t)(kRows + 2 * KT) * DP * 2; }
 
@@ -47,7 +50,8 @@ __device__ __noinline__ void exact_row256(const __nv_bfloat16* q, const __nv_bfl
     for (int e = 0; e < 8; ++e) out[d + e] = __float2bfloat16_rn(o[e] * inv);
 }
 
-template <int DP>
+// SPLIT: a tile's keys over the CTAs of a cluster.
+template <int DP, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_mma_kernel(const __grid_constant__ PromptArgs a) {
   constexpr int NU = DP / 8;  // 16-byte pieces of a row
@@ -63,29 +67,34 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
   if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
   const int row0 = (int)r0, nrows = min(kRows, sq.nq * G - row0);
   const int keys = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, a.causal);
+  int j_begin = 0, j_end = keys;
+  if (SPLIT) {
+    const int per = ((keys - 1) / KT / (int)gridDim.z + 1) * KT;
+    j_begin = (int)min((long long)keys, (long long)blockIdx.z * per);
+    j_end = (int)min((long long)keys, (long long)j_begin + per);
+  }
 
   auto copy = [&](uint32_t dst, const __nv_bfloat16* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
   };
-  // tile j0 of K or V; what is past the keys and past D becomes zeros
-  auto load = [&](uint32_t dst, const void* base, long long stride, int j0) {
+  // the tile of K or V at j0, `left` keys of it; what is past them and past D becomes zeros
+  auto load = [&](uint32_t dst, const void* base, long long stride, int j0, int left) {
     const __nv_bfloat16* src = (const __nv_bfloat16*)base + (long long)(sq.k0 + j0) * stride + (long long)hk * D;
-    const int left = keys - j0;
 #pragma unroll 4
     for (int i = tid; i < KT * NU; i += kThreads) {
       const int r = i / NU, u = i % NU;
       copy(dst + piece<DP>(r, u), src + (long long)min(r, left - 1) * stride + min(u * 8, D - 8), r < left && u * 8 < D);
     }
   };
-  if (keys > 0) {
+  if (j_end > j_begin) {
     for (int i = tid; i < kRows * NU; i += kThreads) {
       const int r = i / NU, u = i % NU, R = row0 + min(r, nrows - 1);
       copy(sQ + piece<DP>(r, u), (const __nv_bfloat16*)a.q + (long long)(sq.q0 + R / G) * a.qs +
                                      (long long)(hk * G + R % G) * D + min(u * 8, D - 8), r < nrows && u * 8 < D);
     }
-    load(sK, a.k, a.ks, 0);
+    load(sK, a.k, a.ks, j_begin, j_end - j_begin);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    load(sV, a.v, a.vs, 0);
+    load(sV, a.v, a.vs, j_begin, j_end - j_begin);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   const float c2 = a.scale * 1.4426950408889634f;
@@ -101,7 +110,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
     const int r = warp * 16 + g + 8 * y;
     lim[y] = r < nrows ? visible_keys((row0 + r) / G, sq.nq, sq.nk, a.causal) : 0;
   }
-  for (int j0 = 0, left = keys; left > 0; j0 += KT, left -= KT) {
+  for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();  // K is there
     float s[KT / 8][4];
@@ -122,7 +131,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
       }
     }
     __syncthreads();  // K is read
-    if (left > KT) load(sK, a.k, a.ks, j0 + KT);
+    if (left > KT) load(sK, a.k, a.ks, j0 + KT, left - KT);
     asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -173,16 +182,91 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
       }
     }
     __syncthreads();  // V is read
-    if (left > KT) load(sV, a.v, a.vs, j0 + KT);
+    if (left > KT) load(sV, a.v, a.vs, j0 + KT, left - KT);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-
-  uint32_t again[2];
+  auto exact = [&](int R) {  // row R of the tile, by a warp
+    const int P = row0 + R, tok = P / G, h = hk * G + P % G;
+    exact_row256((const __nv_bfloat16*)a.q + (long long)(sq.q0 + tok) * a.qs + (long long)h * D,
+                 (const __nv_bfloat16*)a.k + (long long)sq.k0 * a.ks + (long long)hk * D, a.ks,
+                 (const __nv_bfloat16*)a.v + (long long)sq.k0 * a.vs + (long long)hk * D, a.vs, D,
+                 visible_keys(tok, sq.nq, sq.nk, a.causal), c2,
+                 (__nv_bfloat16*)a.out + (long long)(sq.q0 + tok) * a.os + (long long)h * D);
+  };
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+  }
+  if (SPLIT) {
+    // The cluster's CTAs hold parts of the same rows: they put them in shared memory, and each adds up every C-th row
+    // from all of them, in order.
+    constexpr int LD = DP + 4;
+    const int C = gridDim.z, rank = (int)cluster_ctarank();
+    float* po = reinterpret_cast<float*>(smem);
+    float2* ml = reinterpret_cast<float2*>(po + kRows * LD);
+    int* odd = reinterpret_cast<int*>(ml + kRows);
+    static_assert(kRows * (LD * 4 + 8 + 4) <= mma_smem<DP>(), "the parts take the tiles' place");
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int R = warp * 16 + g + 8 * y;
+      if (t4 == 0) ml[R] = make_float2(m[y], l[y]);
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n)
+        *reinterpret_cast<float2*>(po + R * LD + 8 * n + 2 * t4) = make_float2(o[n][2 * y], o[n][2 * y + 1]);
+    }
+    if (tid < kRows) odd[tid] = 0;
+    cluster_sync_all();
+    for (int i = tid; i < kRows / C * (DP / 4); i += kThreads) {
+      const int R = rank + C * (i / (DP / 4)), c = (i % (DP / 4)) * 4;
+      if (R >= nrows || c >= D) continue;
+      float2 v[kMaxCluster];
+      float4 u[kMaxCluster];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int y = 0; y < kMaxCluster; ++y) {
+        if (y >= C) break;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[y].x), "=f"(v[y].y)
+                     : "r"(map_to_cta(smem_u32(ml + R), (uint32_t)y)) : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u[y].x), "=f"(u[y].y), "=f"(u[y].z), "=f"(u[y].w)
+                     : "r"(map_to_cta(smem_u32(po + R * LD + c), (uint32_t)y)) : "memory");
+        M = fmaxf(M, v[y].x);
+      }
+      const float ref = M == -INFINITY ? 0.f : M;
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < kMaxCluster; ++y) {
+        if (y >= C) break;
+        const float w = ex2((v[y].x - ref) * c2);
+        L = fmaf(w, v[y].y, L);
+        t.x = fmaf(w, u[y].x, t.x);
+        t.y = fmaf(w, u[y].y, t.y);
+        t.z = fmaf(w, u[y].z, t.z);
+        t.w = fmaf(w, u[y].w, t.w);
+      }
+      const int P = row0 + R, tok = sq.q0 + P / G, h = hk * G + P % G;
+      const bool none = visible_keys(P / G, sq.nq, sq.nk, a.causal) == 0;
+      const float inv = none || L == 0.f ? 0.f : 1.0f / L;
+      if (none) t = make_float4(0.f, 0.f, 0.f, 0.f);
+      t.x *= inv; t.y *= inv; t.z *= inv; t.w *= inv;
+      if (!(fabsf(t.x) <= 3.0e38f && fabsf(t.y) <= 3.0e38f && fabsf(t.z) <= 3.0e38f && fabsf(t.w) <= 3.0e38f)) odd[R] = 1;
+      *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * D + c) =
+          make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+      if (a.lse != nullptr && c == 0)
+        a.lse[(long long)tok * a.H + h] = none ? -INFINITY : (M * c2 + log2f(L)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+    for (int r = warp; r < kRows / C; r += kThreads / 32)
+      if (odd[rank + C * r] != 0) exact(rank + C * r);
+    cluster_sync_all();  // the others have read this CTA's part
+    return;
+  }
+  uint32_t again[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
     const int r = warp * 16 + g + 8 * y, R = row0 + r, tok = sq.q0 + R / G, h = hk * G + R % G;
     const float inv = l[y] == 0.f ? 0.f : 1.0f / l[y];
     __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * D;
@@ -201,29 +285,45 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
   __syncwarp();
   for (int r = 0; r < 16; ++r) {
     if ((again[r >> 3] >> (4 * (r & 7)) & 15u) == 0) continue;
-    const int R = row0 + warp * 16 + r, tok = R / G, h = hk * G + R % G;
-    exact_row256((const __nv_bfloat16*)a.q + (long long)(sq.q0 + tok) * a.qs + (long long)h * D,
-                 (const __nv_bfloat16*)a.k + (long long)sq.k0 * a.ks + (long long)hk * D, a.ks,
-                 (const __nv_bfloat16*)a.v + (long long)sq.k0 * a.vs + (long long)hk * D, a.vs, D,
-                 visible_keys(tok, sq.nq, sq.nk, a.causal), c2,
-                 (__nv_bfloat16*)a.out + (long long)(sq.q0 + tok) * a.os + (long long)h * D);
+    exact(warp * 16 + r);
   }
 }
 
-template <int DP>
-cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
-  auto kern = attn_mma_kernel<DP>;
+template <int DP, bool SPLIT>
+cudaError_t launch(const PromptArgs& a, dim3 grid, cudaStream_t s) {
+  auto kern = attn_mma_kernel<DP, SPLIT>;
   static std::atomic<int> done{0};
   const cudaError_t e = allow_smem(kern, mma_smem<DP>(), done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)prompt_tile_slots(a.Tq, a.n, a.H / a.Hkv, kRows), (unsigned)a.Hkv);
-  return launch_pdl(kern, grid, dim3(kThreads), mma_smem<DP>(), s, a);
+  if (!SPLIT) return launch_pdl(kern, grid, dim3(kThreads), mma_smem<DP>(), s, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = mma_smem<DP>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = grid.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prompt_mma(const PromptArgs& a, cudaStream_t s) {
-  return a.D <= 192 ? launch<192>(a, s) : launch<256>(a, s);
+  const long long slots = prompt_tile_slots(a.Tq, a.n, a.H / a.Hkv, kRows);
+  // Few tiles: a cluster of CTAs takes the keys of each, at least two tiles of them where the keys are one sequence's
+  // (heads of 256, 16 on 4: 16 tokens behind 8192 keys 64 us, 358 without; 1024 tokens of 4 heads on 4 31 and 53).
+  int C = 1;
+  while (C < kMaxCluster && slots * a.Hkv * 2 * C <= 2LL * device_sm_count() && a.Tkv >= 4 * C * KT) C *= 2;
+  const dim3 grid((unsigned)slots, (unsigned)a.Hkv, (unsigned)C);
+  if (a.D <= 192) return C > 1 ? launch<192, true>(a, grid, s) : launch<192, false>(a, grid, s);
+  return C > 1 ? launch<256, true>(a, grid, s) : launch<256, false>(a, grid, s);
 }
 
 }  // namespace moe

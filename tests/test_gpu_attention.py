@@ -510,3 +510,29 @@ def test_recordings_one_after_the_other_on_private_streams():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert a.device_status()[0] == moe.MOE_OK
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("D", [136, 256])
+@pytest.mark.parametrize("lens", [[50, 150, 60], [50, 150, 60] * 12, [700, 900]])
+def test_prompt_long_heads_nonfinite(lens, D, value):
+    """Heads of more than 128: a non-finite key or value reaches only rows that see it, with and without split keys."""
+    H, Hk, n0, n1 = 4, 2, lens[0], lens[1]
+    T, at = sum(lens), lens[0] + n1 - 60
+    q, k, v = tensor((T, H, D), 1, BF16, DEV), tensor((T, Hk, D), 2, BF16, DEV), tensor((T, Hk, D), 3, BF16, DEV)
+    o = offsets(lens)
+    ref = prompt_reference(q, k, v, o, o, True, D ** -0.5)
+    a = moe.Attention(H, Hk, D, BF16)
+    keep = [t for t in range(T) if not at <= t < n0 + n1]
+    for bad in ("k", "v"):
+        kk, vv = k.clone(), v.clone()
+        (kk if bad == "k" else vv)[at, 1, 5] = value
+        out = a.prompt(q, kk, vv, i32(o, DEV))
+        check(out[keep], None, tuple(x[keep] for x in ref), max(lens), D, BF16)
+        check(out[:, :2], None, tuple(x[:, :2] for x in ref), max(lens), D, BF16)
+        if bad == "v":
+            assert not torch.isfinite(out[at:n0 + n1, 2:, 5]).any()
+            hurt = out[at:n0 + n1, 2:].clone()
+            hurt[..., 5] = 0
+            assert torch.isfinite(hurt).all()
+    assert a.device_status()[0] == moe.MOE_OK
