@@ -72,6 +72,13 @@ struct DecodeArgs {
   uint64_t timeout_ns;
 };
 
+// The shared positions of a decode call that does not take the tcgen05 path, in tiles of 64 rows and 64 keys.
+struct SharedPart {
+  DecodeArgs d;
+  int splits, per;  // pieces of a row over the shared positions; positions of a piece
+  int pieces;       // of a row altogether
+};
+
 // Workspace of one decode call. A piece is the attention of one row over a part of its keys: the sum of
 // the weighted values (D floats), the weights' sum l and the reference m (in log2 units) that the
 // weights 2^(s - m) were taken against. A row's pieces join as out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
@@ -80,6 +87,7 @@ constexpr long long decode_pieces(long long rows) { return 4 * rows + 65536; }
 
 cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s);  // fp32
 cudaError_t launch_attn_prompt_mma(const PromptArgs& a, cudaStream_t s);   // bf16, any D
+cudaError_t launch_attn_shared_mma(const SharedPart& sp, dim3 grid, cudaStream_t s);  // grid: (row tiles, H_kv, splits)
 // bf16, D <= 128, at least one key.
 // splits: attn_prompt_splits or 1; part: Tq H splits (D + 2) floats where there are several.
 int attn_prompt_splits(int n, int Tq, int Tkv, int H, int Hkv);

@@ -1,5 +1,5 @@
-// Prompt attention for bf16 heads of 136 to 256 elements, whose output tile does not fit in TMEM beside two tiles of
-// scores: warp-level MMAs (m16n8k16) with the output in registers.
+// Attention for bf16 heads of 136 to 256 elements, whose output tile does not fit in TMEM beside two tiles of scores:
+// warp-level MMAs (m16n8k16) with the output in registers. Packed prompts, and the shared positions of a decode batch.
 //   S = Q K^T, P = 2^(c S - c m) (c = scale log2 e), O += P V, out = O / l
 // with each row's running maximum m and sum l, in one pass over the keys.
 //
@@ -9,7 +9,8 @@
 // The scores' accumulators are the second product's A operand as they lie. Weights are rounded to bf16 (off by at most
 // 2^-8 of each) as that operand; l takes them unrounded.
 // Bound by the MMA's operands: each 16 x 16 piece of K or V read from shared memory meets only the warp's 16 rows. 4096
-// tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us.
+// tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us. Decode, 64 sequences behind 2048
+// shared positions with 2048 of their own: 157 us (340 with the shared ones on the CUDA cores).
 // A row whose result is not finite is computed again over the keys that it sees, as in attn_tc.cu: 0 times a
 // non-finite value that the row does not see must not reach it.
 #include "attn.cuh"
@@ -26,78 +27,105 @@ template <int DP> constexpr size_t mma_smem() { return (size_t)(kRows + 2 * KT) 
 // Byte offset of 16-byte piece u of row r.
 template <int DP> __device__ __forceinline__ uint32_t piece(int r, int u) { return (uint32_t)(r * DP * 2 + ((u ^ (r & 7)) << 4)); }
 
-// One row again, key by key (a warp; a lane owns 8 consecutive elements).
-__device__ __noinline__ void exact_row256(const __nv_bfloat16* q, const __nv_bfloat16* k, long long ks, const __nv_bfloat16* v,
-                                          long long vs, int D, int lim, float c2, __nv_bfloat16* out) {
+// One row again, key by key (a warp; a lane owns 8 consecutive elements): its sums against the maximum m, in log2
+// units. at(j, ko, vo) gives the element offsets of key j.
+template <typename At>
+__device__ __noinline__ void exact_row256(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v, At at, int D,
+                                          int j0, int lim, float c2, float (&o)[8], float& m, float& l) {
   const int d = (threadIdx.x & 31) * 8;
   const bool on = d < D;
-  float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < lim; ++j) {
+  m = -INFINITY;
+  l = 0.f;
+  for (int e = 0; e < 8; ++e) o[e] = 0.f;
+  for (int j = j0; j < lim; ++j) {
+    long long ko, vo;
+    at(j, ko, vo);
     float s = 0.f;
     if (on)
-      for (int e = 0; e < 8; ++e) s = fmaf(__bfloat162float(q[d + e]), __bfloat162float(k[j * ks + d + e]), s);
+      for (int e = 0; e < 8; ++e) s = fmaf(__bfloat162float(q[d + e]), __bfloat162float(k[ko + d + e]), s);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
     s *= c2;
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), p = ex2(s - ref);
-    l = fmaf(l, a, p);
+    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, x = ex2(m - ref), p = ex2(s - ref);
+    l = fmaf(l, x, p);
     m = mn;
     if (on)
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(p, __bfloat162float(v[j * vs + d + e]), o[e] * a);
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(p, __bfloat162float(v[vo + d + e]), o[e] * x);
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  if (on)
-    for (int e = 0; e < 8; ++e) out[d + e] = __float2bfloat16_rn(o[e] * inv);
 }
 
-// SPLIT: a tile's keys over the CTAs of a cluster.
-template <int DP, bool SPLIT>
+// SPLIT: a tile's keys over the CTAs of a cluster. SHARED: the shared positions of a decode call, as in attn_simt.cu.
+template <int DP, bool SPLIT, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 2)
-attn_mma_kernel(const __grid_constant__ PromptArgs a) {
+attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ SharedPart sp) {
   constexpr int NU = DP / 8;  // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_wait();
-  griddep_launch_dependents();
+  griddep_launch_dependents();  // after the wait: the own positions' kernel relies on it
   const uint32_t sQ = smem_u32(smem), sK = sQ + kRows * DP * 2, sV = sK + KT * DP * 2;
-  const int G = a.H / a.Hkv, D = a.D, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
-  const int seq = find_tile_seq(a.qo, a.n, G, kRows, slot);
-  const Seq sq = load_seq(a, seq);
-  const long long r0 = ((long long)slot - ((long long)sq.q0 * G / kRows + seq)) * kRows;
-  if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
-  const int row0 = (int)r0, nrows = min(kRows, sq.nq * G - row0);
-  const int keys = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, a.causal);
-  int j_begin = 0, j_end = keys;
-  if (SPLIT) {
-    const int per = ((keys - 1) / KT / (int)gridDim.z + 1) * KT;
-    j_begin = (int)min((long long)keys, (long long)blockIdx.z * per);
-    j_end = (int)min((long long)keys, (long long)j_begin + per);
+  const DecodeArgs& da = sp.d;
+  const int H = SHARED ? da.H : a.H, Hkv = SHARED ? da.c.Hkv : a.Hkv, D = SHARED ? da.c.D : a.D;
+  const int G = H / Hkv, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int row0, nrows, j_begin, j_end;
+  Seq sq{0, 0, 0, 0};
+  const int32_t* pages = nullptr;
+  if (SHARED) {
+    row0 = blockIdx.x * kRows;
+    nrows = min(kRows, da.n * G - row0);
+    j_begin = min(da.shared, (int)blockIdx.z * sp.per);
+    j_end = min(da.shared, j_begin + sp.per);
+    const int s0 = da.slots[0];  // an out-of-range slot or page is recorded by the own part
+    pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
+  } else {
+    const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
+    const int seq = find_tile_seq(a.qo, a.n, G, kRows, slot);
+    sq = load_seq(a, seq);
+    const long long r0 = ((long long)slot - ((long long)sq.q0 * G / kRows + seq)) * kRows;
+    if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
+    row0 = (int)r0;
+    nrows = min(kRows, sq.nq * G - row0);
+    j_begin = 0;
+    j_end = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, a.causal);
+    if (SPLIT) {
+      const int keys = j_end, per = ((keys - 1) / KT / (int)gridDim.z + 1) * KT;
+      j_begin = (int)min((long long)keys, (long long)blockIdx.z * per);
+      j_end = (int)min((long long)keys, (long long)j_begin + per);
+    }
   }
+  const __nv_bfloat16 *qb = (const __nv_bfloat16*)(SHARED ? da.q : a.q), *kb = (const __nv_bfloat16*)(SHARED ? da.k : a.k),
+                      *vb = (const __nv_bfloat16*)(SHARED ? da.v : a.v);
+  const long long qs = SHARED ? da.qs : a.qs;
+  // where position j of the keys lies
+  auto paged = [&](int j) {
+    int page = pages[j >> da.c.page_shift];
+    page = page < 0 || page >= da.c.n_pages ? 0 : page;
+    return (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D;
+  };
 
   auto copy = [&](uint32_t dst, const __nv_bfloat16* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
   };
   // the tile of K or V at j0, `left` keys of it; what is past them and past D becomes zeros
-  auto load = [&](uint32_t dst, const void* base, long long stride, int j0, int left) {
-    const __nv_bfloat16* src = (const __nv_bfloat16*)base + (long long)(sq.k0 + j0) * stride + (long long)hk * D;
+  auto load = [&](uint32_t dst, const __nv_bfloat16* base, long long stride, int j0, int left) {
 #pragma unroll 4
     for (int i = tid; i < KT * NU; i += kThreads) {
-      const int r = i / NU, u = i % NU;
-      copy(dst + piece<DP>(r, u), src + (long long)min(r, left - 1) * stride + min(u * 8, D - 8), r < left && u * 8 < D);
+      const int r = i / NU, u = i % NU, j = j0 + min(r, left - 1);
+      const long long at = SHARED ? paged(j) : (long long)(sq.k0 + j) * stride + (long long)hk * D;
+      copy(dst + piece<DP>(r, u), base + at + min(u * 8, D - 8), r < left && u * 8 < D);
     }
   };
   if (j_end > j_begin) {
     for (int i = tid; i < kRows * NU; i += kThreads) {
       const int r = i / NU, u = i % NU, R = row0 + min(r, nrows - 1);
-      copy(sQ + piece<DP>(r, u), (const __nv_bfloat16*)a.q + (long long)(sq.q0 + R / G) * a.qs +
-                                     (long long)(hk * G + R % G) * D + min(u * 8, D - 8), r < nrows && u * 8 < D);
+      const __nv_bfloat16* row = qb + (long long)(sq.q0 + R / G) * qs + (long long)(hk * G + R % G) * D;
+      copy(sQ + piece<DP>(r, u), row + min(u * 8, D - 8), r < nrows && u * 8 < D);
     }
-    load(sK, a.k, a.ks, j_begin, j_end - j_begin);
+    load(sK, kb, a.ks, j_begin, j_end - j_begin);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    load(sV, a.v, a.vs, j_begin, j_end - j_begin);
+    load(sV, vb, a.vs, j_begin, j_end - j_begin);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  const float c2 = a.scale * 1.4426950408889634f;
+  const float c2 = (SHARED ? da.scale : a.scale) * 1.4426950408889634f;
   const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, l8 = lane & 7;
   float o[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   int lim[2];
@@ -108,7 +136,13 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     const int r = warp * 16 + g + 8 * y;
-    lim[y] = r < nrows ? visible_keys((row0 + r) / G, sq.nq, sq.nk, a.causal) : 0;
+    lim[y] = 0;
+    if (r < nrows && SHARED) {  // a slot shorter than the shared positions sees its own length of them
+      const int s = da.slots[(row0 + r) / G];
+      lim[y] = s < 0 || s >= da.c.n_slots ? 0 : min(j_end, max(0, da.c.lens[s]));
+    } else if (r < nrows) {
+      lim[y] = visible_keys((row0 + r) / G, sq.nq, sq.nk, a.causal);
+    }
   }
   for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -131,7 +165,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
       }
     }
     __syncthreads();  // K is read
-    if (left > KT) load(sK, a.k, a.ks, j0 + KT, left - KT);
+    if (left > KT) load(sK, kb, a.ks, j0 + KT, left - KT);
     asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -182,22 +216,61 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
       }
     }
     __syncthreads();  // V is read
-    if (left > KT) load(sV, a.v, a.vs, j0 + KT, left - KT);
+    if (left > KT) load(sV, vb, a.vs, j0 + KT, left - KT);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   auto exact = [&](int R) {  // row R of the tile, by a warp
     const int P = row0 + R, tok = P / G, h = hk * G + P % G;
-    exact_row256((const __nv_bfloat16*)a.q + (long long)(sq.q0 + tok) * a.qs + (long long)h * D,
-                 (const __nv_bfloat16*)a.k + (long long)sq.k0 * a.ks + (long long)hk * D, a.ks,
-                 (const __nv_bfloat16*)a.v + (long long)sq.k0 * a.vs + (long long)hk * D, a.vs, D,
-                 visible_keys(tok, sq.nq, sq.nk, a.causal), c2,
-                 (__nv_bfloat16*)a.out + (long long)(sq.q0 + tok) * a.os + (long long)h * D);
+    float x[8], mx, lx;
+    exact_row256(qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + (long long)sq.k0 * a.ks + (long long)hk * D,
+                 vb + (long long)sq.k0 * a.vs + (long long)hk * D,
+                 [&](int j, long long& ko, long long& vo) {
+                   ko = j * a.ks;
+                   vo = j * a.vs;
+                 },
+                 D, 0, visible_keys(tok, sq.nq, sq.nk, a.causal), c2, x, mx, lx);
+    const float inv = lx == 0.f ? 0.f : 1.0f / lx;
+    __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (long long)(sq.q0 + tok) * a.os + (long long)h * D + lane * 8;
+    if (lane * 8 < D)
+      for (int e = 0; e < 8; ++e) dst[e] = __float2bfloat16_rn(x[e] * inv);
   };
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+  }
+  if (SHARED) {
+    uint32_t again[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int r = warp * 16 + g + 8 * y, P = row0 + min(r, nrows - 1);
+      float* po = da.part + (((long long)(P / G) * H + hk * G + P % G) * sp.pieces + blockIdx.z) * (D + 2);
+      bool fine = true;
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        const int c = 8 * n + 2 * t4;
+        const float x = lim[y] <= j_begin ? 0.f : o[n][2 * y], z = lim[y] <= j_begin ? 0.f : o[n][2 * y + 1];
+        fine = fine && fabsf(x) <= 3.0e38f && fabsf(z) <= 3.0e38f;
+        if (r < nrows && c < D) *reinterpret_cast<float2*>(po + c) = make_float2(x, z);
+      }
+      if (r < nrows && t4 == 0) *reinterpret_cast<float2*>(po + D) = make_float2(m[y] * c2, l[y]);
+      again[y] = __ballot_sync(0xffffffffu, r < nrows && !fine && lim[y] < j_end);
+    }
+    __syncwarp();
+    for (int r = 0; r < 16; ++r) {
+      if ((again[r >> 3] >> (4 * (r & 7)) & 15u) == 0) continue;
+      const int P = row0 + warp * 16 + r, tok = P / G, h = hk * G + P % G;
+      float x[8], mx, lx;
+      exact_row256(qb + (long long)tok * qs + (long long)h * D, kb, vb,
+                   [&](int j, long long& ko, long long& vo) { ko = vo = paged(j); }, D, j_begin,
+                   min(j_end, max(0, da.c.lens[da.slots[tok]])), c2, x, mx, lx);
+      float* po = da.part + (((long long)tok * H + h) * sp.pieces + blockIdx.z) * (D + 2);
+      if (lane * 8 < D)
+        for (int e = 0; e < 8; ++e) po[lane * 8 + e] = x[e];
+      if (lane == 0) *reinterpret_cast<float2*>(po + D) = make_float2(mx, lx);
+    }
+    return;
   }
   if (SPLIT) {
     // The cluster's CTAs hold parts of the same rows: they put them in shared memory, and each adds up every C-th row
@@ -256,7 +329,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
       *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * D + c) =
           make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
       if (a.lse != nullptr && c == 0)
-        a.lse[(long long)tok * a.H + h] = none ? -INFINITY : (M * c2 + log2f(L)) * 0.6931471805599453f;
+        a.lse[(long long)tok * H + h] = none ? -INFINITY : (M * c2 + log2f(L)) * 0.6931471805599453f;
     }
     __syncthreads();
     for (int r = warp; r < kRows / C; r += kThreads / 32)
@@ -279,7 +352,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
       if (r < nrows && c < D) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(x, z);
     }
     if (a.lse != nullptr && r < nrows && t4 == 0)
-      a.lse[(long long)tok * a.H + h] = lim[y] == 0 ? -INFINITY : (m[y] * c2 + log2f(l[y])) * 0.6931471805599453f;
+      a.lse[(long long)tok * H + h] = lim[y] == 0 ? -INFINITY : (m[y] * c2 + log2f(l[y])) * 0.6931471805599453f;
     again[y] = __ballot_sync(0xffffffffu, r < nrows && !fine);
   }
   __syncwarp();
@@ -289,13 +362,13 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a) {
   }
 }
 
-template <int DP, bool SPLIT>
-cudaError_t launch(const PromptArgs& a, dim3 grid, cudaStream_t s) {
-  auto kern = attn_mma_kernel<DP, SPLIT>;
+template <int DP, bool SPLIT, bool SHARED>
+cudaError_t launch(const PromptArgs& a, const SharedPart& sp, dim3 grid, cudaStream_t s) {
+  auto kern = attn_mma_kernel<DP, SPLIT, SHARED>;
   static std::atomic<int> done{0};
   const cudaError_t e = allow_smem(kern, mma_smem<DP>(), done);
   if (e != cudaSuccess) return e;
-  if (!SPLIT) return launch_pdl(kern, grid, dim3(kThreads), mma_smem<DP>(), s, a);
+  if (!SPLIT) return launch_pdl(kern, grid, dim3(kThreads), mma_smem<DP>(), s, a, sp);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
@@ -310,7 +383,7 @@ cudaError_t launch(const PromptArgs& a, dim3 grid, cudaStream_t s) {
   attr[1].val.clusterDim.z = grid.z;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, a, sp);
 }
 
 }  // namespace
@@ -322,8 +395,14 @@ cudaError_t launch_attn_prompt_mma(const PromptArgs& a, cudaStream_t s) {
   int C = 1;
   while (C < kMaxCluster && slots * a.Hkv * 2 * C <= 2LL * device_sm_count() && a.Tkv >= 4 * C * KT) C *= 2;
   const dim3 grid((unsigned)slots, (unsigned)a.Hkv, (unsigned)C);
-  if (a.D <= 192) return C > 1 ? launch<192, true>(a, grid, s) : launch<192, false>(a, grid, s);
-  return C > 1 ? launch<256, true>(a, grid, s) : launch<256, false>(a, grid, s);
+  const SharedPart none{};
+  if (a.D <= 192) return C > 1 ? launch<192, true, false>(a, none, grid, s) : launch<192, false, false>(a, none, grid, s);
+  return C > 1 ? launch<256, true, false>(a, none, grid, s) : launch<256, false, false>(a, none, grid, s);
+}
+
+cudaError_t launch_attn_shared_mma(const SharedPart& sp, dim3 grid, cudaStream_t s) {
+  const PromptArgs none{};
+  return sp.d.c.D <= 192 ? launch<192, false, true>(none, sp, grid, s) : launch<256, false, true>(none, sp, grid, s);
 }
 
 }  // namespace moe

@@ -1,4 +1,5 @@
-// Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and decode with heads of more than 128.
+// Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and the own positions of a decode batch of bf16
+// heads of more than 128 (whose prompts and shared positions attn_mma.cu takes).
 //   out[r] = sum_{j < lim(r)} softmax_j(scale q[r] . k[j]) v[j]
 // Scores are kept in log2 units (times scale * log2 e), so a weight is one 2^x. Keys past a row's limit are left
 // out of both products by index, not by a zero weight, so that a non-finite value there stays there.
@@ -9,8 +10,7 @@
 // Bound by reads of shared memory: a warp's 16-byte read takes four cycles whatever its lanes share, so an
 // element of the scores costs (4 + 8) * 4 cycles for 32 of arithmetic, one of the output 20 for 16; with 2 rows a
 // thread that was 40 for 16. Rows in shared memory have a length known to the compiler (D rounded up to 32, zeros
-// past D): with
-// D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the place of the
+// past D): with D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the place of the
 // keys once the scores are done; two CTAs then fit on an SM and one computes while the other loads.
 // Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s.
 //
@@ -20,7 +20,7 @@
 // shuffles for 32 sums), which leaves each lane one score. Keys are split over warps and CTAs, whose pieces join in
 // a fixed order. Bound by latency, each warp loading and computing in turn; the launch bounds are what measured
 // best. fp32, heads of 128, 4096 positions: 32 sequences of 8 heads 187 us (5.7 TB/s), 8 of 32 heads on 8 61 us (4.4
-// TB/s), 8 of 64 on 8 85 us.
+// TB/s), 8 of 64 on 8 85 us; bf16, heads of 256, 16 on 4: 64 sequences 259 us (4.2 TB/s).
 #include "attn.cuh"
 #include "kernels.cuh"
 
@@ -36,16 +36,12 @@ __device__ __forceinline__ float4 load4f<__nv_bfloat16>(const __nv_bfloat16* p) 
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
 }
-// 4 elements to shared memory: fp32 asynchronously (waited for with the group), bf16 through registers.
+// 4 elements to shared memory, waited for with the group.
 template <typename T>
 __device__ __forceinline__ void stage4(float* dst, const T* src, bool in);
 template <>
 __device__ __forceinline__ void stage4<float>(float* dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-template <>
-__device__ __forceinline__ void stage4<__nv_bfloat16>(float* dst, const __nv_bfloat16* src, bool in) {
-  *reinterpret_cast<float4*>(dst) = in ? load4f(src) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 template <typename T> __device__ __forceinline__ void store_result(T* p, float x) { *p = from_f32<T>(x); }
 
@@ -59,12 +55,6 @@ constexpr int kMaxCluster = 8;
 // DP: D rounded up to a multiple of 32; the elements past D are zeros in shared memory.
 constexpr int tile_keys(int DP) { return KT * (DP + 4) > kRows * kLdP ? KT * (DP + 4) : kRows * kLdP; }
 constexpr size_t tile_smem(int DP) { return sizeof(float) * ((size_t)(kRows + KT) * (DP + 4) + tile_keys(DP)); }
-
-struct SharedPart {
-  DecodeArgs d;
-  int splits, per;  // pieces of a row over the shared positions; positions of a piece
-  int pieces;       // of a row altogether
-};
 
 // SHARED: rows and keys of a decode call, in pieces. SPLIT: a tile's keys over a cluster (in a kernel without it the
 // code for it would cost registers and 3% of the time).
@@ -359,9 +349,10 @@ constexpr int NK = 4;  // keys of a warp's step
 // four of 32 heads 25 and 28).
 constexpr int kSharedFrom = 4;
 
-// V4: groups of 4 elements of a lane (elements 4 lane + 128 x); GR: rows of a CTA.
+// V4: groups of 4 elements of a lane, 16 bytes side by side (fp32: elements 4 lane + 128 x, bf16: 8 lane + 4 x); GR: rows
+// of a CTA.
 template <typename T, int V4, int GR>
-__global__ void __launch_bounds__(32 * kRowWarps, V4 == 2 ? 3 : GR == 8 ? 4 : 5)
+__global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 2 ? 4 : V4 == 2 ? 3 : GR == 8 ? 4 : 5)
 decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_piece, int splits, int pieces) {
   constexpr int NV = GR * NK;  // products of a step
   static_assert(NV == 32 || NV == 16, "one or two lanes a score");
@@ -399,6 +390,9 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
   const int per = (int)(((long long)own + splits - 1) / splits + step - 1) / step * step;
   const int j_begin = from + (int)min((long long)own, (long long)blockIdx.z * per), j_end = min(from + own, j_begin + per);
 
+  constexpr bool kHalf = sizeof(T) == 2;
+  static_assert(!kHalf || V4 == 2, "16 bytes a lane");
+  auto col = [&](int x) { return kHalf ? 8 * lane + 4 * x : 4 * lane + 128 * x; };
   uint64_t q[GR][V4][2], o[GR][V4][2];
   const T* qp = (const T*)a.q + (long long)seq * a.qs + (long long)(hk * G + row0) * D;
 #pragma unroll
@@ -406,7 +400,7 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
 #pragma unroll
     for (int x = 0; x < V4; ++x) {
       float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nrows && 4 * lane + 128 * x < D) t = load4f<T>(qp + (long long)r * D + 4 * lane + 128 * x);
+      if (r < nrows && col(x) < D) t = load4f<T>(qp + (long long)r * D + col(x));
       q[r][x][0] = f2_pack(t.x, t.y);
       q[r][x][1] = f2_pack(t.z, t.w);
       o[r][x][0] = o[r][x][1] = 0ull;
@@ -434,16 +428,30 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
         if (lane == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
         p = 0;
       }
-      const long long at = (((long long)p * c.Hkv + hk) * c.page_size + ((j + k) & (c.page_size - 1))) * D + 4 * lane;
+      const long long at = (((long long)p * c.Hkv + hk) * c.page_size + ((j + k) & (c.page_size - 1))) * D;
+      if constexpr (kHalf) {
+        const bool in = k < left && 8 * lane < D;
+        const uint4 ke = in ? *reinterpret_cast<const uint4*>(kb + at + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 ve = in ? *reinterpret_cast<const uint4*>(vb + at + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+        kv[k][0][0] = f2_pack(bf16lo(ke.x), bf16hi(ke.x));
+        kv[k][0][1] = f2_pack(bf16lo(ke.y), bf16hi(ke.y));
+        kv[k][1][0] = f2_pack(bf16lo(ke.z), bf16hi(ke.z));
+        kv[k][1][1] = f2_pack(bf16lo(ke.w), bf16hi(ke.w));
+        vv[k][0][0] = f2_pack(bf16lo(ve.x), bf16hi(ve.x));
+        vv[k][0][1] = f2_pack(bf16lo(ve.y), bf16hi(ve.y));
+        vv[k][1][0] = f2_pack(bf16lo(ve.z), bf16hi(ve.z));
+        vv[k][1][1] = f2_pack(bf16lo(ve.w), bf16hi(ve.w));
+      } else {
 #pragma unroll
-      for (int x = 0; x < V4; ++x) {
-        const bool in = k < left && 4 * lane + 128 * x < D;
-        const float4 ke = in ? load4f<T>(kb + at + 128 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 ve = in ? load4f<T>(vb + at + 128 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
-        kv[k][x][0] = f2_pack(ke.x, ke.y);
-        kv[k][x][1] = f2_pack(ke.z, ke.w);
-        vv[k][x][0] = f2_pack(ve.x, ve.y);
-        vv[k][x][1] = f2_pack(ve.z, ve.w);
+        for (int x = 0; x < V4; ++x) {
+          const bool in = k < left && col(x) < D;
+          const float4 ke = in ? load4f<T>(kb + at + col(x)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 ve = in ? load4f<T>(vb + at + col(x)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          kv[k][x][0] = f2_pack(ke.x, ke.y);
+          kv[k][x][1] = f2_pack(ke.z, ke.w);
+          vv[k][x][0] = f2_pack(ve.x, ve.y);
+          vv[k][x][1] = f2_pack(ve.z, ve.w);
+        }
       }
     }
     if (left > step) look_up(j + step);
@@ -519,7 +527,7 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
     const float w = M == -INFINITY ? 0.f : ex2(sml[0][warp][r] - M);
 #pragma unroll
     for (int x = 0; x < V4; ++x)
-      *reinterpret_cast<float4*>(&buf[warp][r][4 * lane + 128 * x]) =
+      *reinterpret_cast<float4*>(&buf[warp][r][col(x)]) =
           sml[1][warp][r] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                                  : make_float4(f2_lo(o[r][x][0]) * w, f2_hi(o[r][x][0]) * w, f2_lo(o[r][x][1]) * w,
                                                f2_hi(o[r][x][1]) * w);
@@ -654,13 +662,8 @@ cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, dim3 grid, 
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, pa, sp);
 }
-// bf16 comes here with the shared positions of heads of more than 128 only.
 template <bool SHARED, bool SPLIT>
-cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, int dt, int D, dim3 grid, cudaStream_t s) {
-  if constexpr (SHARED)
-    if (dt == MOE_DTYPE_BF16)
-      return D <= 192 ? launch_tiles<__nv_bfloat16, 192, SHARED, SPLIT>(pa, sp, grid, s)
-                      : launch_tiles<__nv_bfloat16, 256, SHARED, SPLIT>(pa, sp, grid, s);
+cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, int D, dim3 grid, cudaStream_t s) {
   if (D <= 64) return launch_tiles<float, 64, SHARED, SPLIT>(pa, sp, grid, s);
   if (D <= 96) return launch_tiles<float, 96, SHARED, SPLIT>(pa, sp, grid, s);
   if (D <= 128) return launch_tiles<float, 128, SHARED, SPLIT>(pa, sp, grid, s);
@@ -695,7 +698,7 @@ cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
   int C = 1;
   while (C < kMaxCluster && slots * a.Hkv * 2 * C <= 2LL * device_sm_count() && a.Tkv >= 4 * C * KT) C *= 2;
   const dim3 grid((unsigned)slots, (unsigned)a.Hkv, (unsigned)C);
-  return C > 1 ? launch_tiles<false, true>(a, none, a.dt, a.D, grid, s) : launch_tiles<false, false>(a, none, a.dt, a.D, grid, s);
+  return C > 1 ? launch_tiles<false, true>(a, none, a.D, grid, s) : launch_tiles<false, false>(a, none, a.D, grid, s);
 }
 
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s) {
@@ -724,7 +727,8 @@ cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s) {
     sp.splits = (blocks + per - 1) / per;
     sp.pieces = sp.splits + (int)splits;
     const PromptArgs none{};
-    e = launch_tiles<true, false>(none, sp, a.c.dt, D, dim3((unsigned)tiles, (unsigned)a.c.Hkv, (unsigned)sp.splits), s);
+    const dim3 grid((unsigned)tiles, (unsigned)a.c.Hkv, (unsigned)sp.splits);
+    e = a.c.dt == MOE_DTYPE_BF16 ? launch_attn_shared_mma(sp, grid, s) : launch_tiles<true, false>(none, sp, D, grid, s);
     if (e != cudaSuccess) return e;
   }
   const int first = sp.splits, n = (int)splits;

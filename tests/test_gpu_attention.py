@@ -232,7 +232,7 @@ def make_cache(lens, shared, page, Hk, D, dtype, layers=1, seed=0, stale=0.0):
     """A cache whose slots share their first `shared` positions, on shuffled pages; stale: what unused positions hold."""
     r = random.Random(seed)
     up = lambda a: -(-a // page)  # noqa: E731
-    pages = up(shared) + sum(up(a) - shared // page for a in lens) + 3
+    pages = up(shared) + sum(max(0, up(a) - shared // page) for a in lens) + 3
     order = list(range(pages))
     r.shuffle(order)
     head, at = order[:shared // page], shared // page
@@ -535,4 +535,36 @@ def test_prompt_long_heads_nonfinite(lens, D, value):
             hurt = out[at:n0 + n1, 2:].clone()
             hurt[..., 5] = 0
             assert torch.isfinite(hurt).all()
+    assert a.device_status()[0] == moe.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [136, 192, 200, 256])
+def test_decode_long_heads_with_shared_tiles(D, dtype):
+    """Enough sequences that the shared positions go to tiles: rows that fill one and rows that do not, short slots."""
+    run_decode([100, 96, 31, 0, 97, 200], 96, 8, 2, D, dtype, seed=D)
+    run_decode([300 + 3 * i for i in range(20)], 288, 8, 1, D, dtype, page=32, seed=D)
+    run_decode([1100, 1040, 1025, 1300], 1024, 4, 4, D, dtype, page=64, layers=2, layer=1, seed=D)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [128, 192, 256])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_decode_shared_nonfinite_and_short_slots(value, D, dtype):
+    """A non-finite value at a shared position reaches no slot that ends before it."""
+    lens, shared, H, Hk, page = [150, 90, 128, 140, 64], 128, 8, 2, 16
+    c, rows = make_cache(lens, shared, page, Hk, D, dtype)
+    n, at = len(lens), 100
+    q = tensor((n, H, D), 9, dtype, DEV)
+    ref = decode_reference(q, c, rows, lens, 0, D ** -0.5)
+    c.v[0, rows[0][at // page], 1, at % page, 5] = value
+    a = moe.Attention(H, Hk, D, dtype)
+    out = a.decode(q, c, i32(list(range(n)), DEV), shared_len=shared)
+    short = [1, 4]
+    check(out[short], None, tuple(x[short] for x in ref), 150, D, dtype)
+    check(out[:, :4], None, tuple(x[:, :4] for x in ref), 150, D, dtype)
+    seen = out[[0, 2, 3], 4:].clone()
+    assert not torch.isfinite(seen[..., 5]).any()
+    seen[..., 5] = 0
+    assert torch.isfinite(seen).all()
     assert a.device_status()[0] == moe.MOE_OK
