@@ -3,15 +3,15 @@
 //   S = Q K^T, P = 2^(c S - c m) (c = scale log2 e), O += P V, out = O / l
 // with each row's running maximum m and sum l, in one pass over the keys.
 //
-// A CTA takes 64 packed rows (see PromptArgs) of one key/value head, 16 a warp, against tiles of 64 keys. Q, K and V are
-// in shared memory, 16-byte pieces swizzled by their row so that no ldmatrix meets a bank twice; a tile's K is replaced
-// while its softmax runs, its V while the next scores do, and two CTAs share an SM (96 KB and up to 255 registers each).
-// The scores' accumulators are the second product's A operand as they lie. Weights are rounded to bf16 (off by at most
-// 2^-8 of each) as that operand; l takes them unrounded.
+// A CTA takes 64 packed rows (see PromptArgs) of one key/value head, 16 a warp, against tiles of 64 keys. Q, K and V
+// are in shared memory, 16-byte pieces swizzled by their row so that no ldmatrix meets a bank twice; a tile's K is
+// replaced while its softmax runs, its V while the next scores do, and two CTAs share an SM (96 KB and up to 255
+// registers each). The scores' accumulators are the second product's A operand as they lie. Weights are rounded to
+// bf16 (off by at most 2^-8 of each) as that operand; l takes them unrounded.
 // Bound by the MMA's operands: each 16 x 16 piece of K or V read from shared memory meets only the warp's 16 rows. 4096
-// tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us. Decode, 64 sequences behind 2048
-// shared positions with 2048 of their own: 157 us (340 with the shared ones on the CUDA cores).
-// A row whose result is not finite is computed again over the keys that it sees, as in attn_tc.cu: 0 times a
+// tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us. Decode,
+// 64 sequences behind 2048 shared positions with 2048 of their own: 157 us (340 with the shared ones on the CUDA
+// cores). A row whose result is not finite is computed again over the keys that it sees, as in attn_tc.cu: 0 times a
 // non-finite value that the row does not see must not reach it.
 #include "attn.cuh"
 #include "kernels.cuh"

@@ -1,5 +1,5 @@
-// Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and the own positions of a decode batch of bf16
-// heads of more than 128 (whose prompts and shared positions attn_mma.cu takes).
+// Attention on the CUDA cores, fp32 arithmetic throughout: fp32 tensors, and the own positions of a decode batch of
+// bf16 heads of more than 128 (whose prompts and shared positions attn_mma.cu takes).
 //   out[r] = sum_{j < lim(r)} softmax_j(scale q[r] . k[j]) v[j]
 // Scores are kept in log2 units (times scale * log2 e), so a weight is one 2^x. Keys past a row's limit are left
 // out of both products by index, not by a zero weight, so that a non-finite value there stays there.
@@ -10,8 +10,8 @@
 // Bound by reads of shared memory: a warp's 16-byte read takes four cycles whatever its lanes share, so an
 // element of the scores costs (4 + 8) * 4 cycles for 32 of arithmetic, one of the output 20 for 16; with 2 rows a
 // thread that was 40 for 16. Rows in shared memory have a length known to the compiler (D rounded up to 32, zeros
-// past D): with D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the place of the
-// keys once the scores are done; two CTAs then fit on an SM and one computes while the other loads.
+// past D): with D in the addresses and a test of each column the loops took 1.5 times as long. The weights take the
+// place of the keys once the scores are done; two CTAs then fit on an SM and one computes while the other loads.
 // Measured, fp32: 4096 tokens, 32 heads of 128 on 8: 3.04 ms, 45 TFLOP/s; heads of 64: 39 TFLOP/s.
 //
 // decode_rows_kernel: the positions that a sequence does not share, an HBM stream that meets up to 8 rows, far too
@@ -344,13 +344,13 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
 // ------------------------------------------------------------------ few rows
 constexpr int kRowWarps = 4;
 constexpr int NK = 4;  // keys of a warp's step
-// From this many sequences on the shared positions are read once for all by tiles; fewer read them each (4096
-// shared, fp32 heads of 128 on 4: two sequences of 4 heads 26 us by tiles, 16 each; four 22 and 21; eight 22 and 31;
-// four of 32 heads 25 and 28).
-constexpr int kSharedFrom = 4;
+// From this many sequences on the shared positions are read once for all by tiles; fewer read them each. 4096 shared, 4
+// key/value heads, in a graph: fp32 heads of 128, 4 sequences 21 us by tiles, 18 each, 8 sequences 21 and 26; bf16
+// heads of 256, 2 sequences 16 and 15, 3 sequences 16 and 20.
+constexpr int kSharedFromF32 = 6, kSharedFromBf16 = 3;
 
-// V4: groups of 4 elements of a lane, 16 bytes side by side (fp32: elements 4 lane + 128 x, bf16: 8 lane + 4 x); GR: rows
-// of a CTA.
+// V4: groups of 4 elements of a lane, 16 bytes side by side (fp32: elements 4 lane + 128 x, bf16: 8 lane + 4 x); GR:
+// rows of a CTA.
 template <typename T, int V4, int GR>
 __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 2 ? 4 : V4 == 2 ? 3 : GR == 8 ? 4 : 5)
 decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_piece, int splits, int pieces) {
@@ -704,7 +704,7 @@ cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s) {
   const int G = a.H / a.c.Hkv, D = a.c.D, GR = D <= 128 && G > 4 ? 8 : 4, sms = device_sm_count();
   const long long rows = (long long)a.n * a.H, fit = decode_pieces(rows) / rows;
-  const bool shared = a.shared > 0 && a.n >= kSharedFrom;
+  const bool shared = a.shared > 0 && a.n >= (a.c.dt == MOE_DTYPE_BF16 ? kSharedFromBf16 : kSharedFromF32);
   // own positions: about 8 CTAs an SM, at least 64 positions each at the longest length
   const long long ctas = (long long)a.n * ((G + GR - 1) / GR) * a.c.Hkv;
   const long long most = (long long)a.c.width * a.c.page_size - (shared ? a.shared : 0);

@@ -544,7 +544,7 @@ def test_decode_long_heads_with_shared_tiles(D, dtype):
     """Enough sequences that the shared positions go to tiles: rows that fill one and rows that do not, short slots."""
     run_decode([100, 96, 31, 0, 97, 200], 96, 8, 2, D, dtype, seed=D)
     run_decode([300 + 3 * i for i in range(20)], 288, 8, 1, D, dtype, page=32, seed=D)
-    run_decode([1100, 1040, 1025, 1300], 1024, 4, 4, D, dtype, page=64, layers=2, layer=1, seed=D)
+    run_decode([1100, 1040, 1025, 1300, 1024, 1030, 1100], 1024, 4, 4, D, dtype, page=64, layers=2, layer=1, seed=D)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -552,7 +552,7 @@ def test_decode_long_heads_with_shared_tiles(D, dtype):
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_decode_shared_nonfinite_and_short_slots(value, D, dtype):
     """A non-finite value at a shared position reaches no slot that ends before it."""
-    lens, shared, H, Hk, page = [150, 90, 128, 140, 64], 128, 8, 2, 16
+    lens, shared, H, Hk, page = [150, 90, 128, 140, 64, 128, 150], 128, 8, 2, 16
     c, rows = make_cache(lens, shared, page, Hk, D, dtype)
     n, at = len(lens), 100
     q = tensor((n, H, D), 9, dtype, DEV)
@@ -563,7 +563,7 @@ def test_decode_shared_nonfinite_and_short_slots(value, D, dtype):
     short = [1, 4]
     check(out[short], None, tuple(x[short] for x in ref), 150, D, dtype)
     check(out[:, :4], None, tuple(x[:, :4] for x in ref), 150, D, dtype)
-    seen = out[[0, 2, 3], 4:].clone()
+    seen = out[[0, 2, 3, 5, 6], 4:].clone()
     assert not torch.isfinite(seen[..., 5]).any()
     seen[..., 5] = 0
     assert torch.isfinite(seen).all()
