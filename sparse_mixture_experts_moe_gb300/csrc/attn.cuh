@@ -60,6 +60,7 @@ struct DecodeArgs {
   const void* q;
   long long qs, os;
   const int32_t* slots;
+  const int32_t* lead;  // the call's first slot, whose pages hold the shared positions (slots may begin at a slice)
   int n, H, shared;
   float scale;
   CacheView c;

@@ -310,7 +310,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   } else {
     // that the slots share what the caller says they share
     if (a.d.shared > 0) {
-      const int s0 = a.d.slots[0], pages = a.d.shared >> c.page_shift;
+      const int s0 = a.d.lead[0], pages = a.d.shared >> c.page_shift;
       if (s0 >= 0 && s0 < c.n_slots)
         for (long long x = (long long)blockIdx.x * (32 * kWarps) + tid; x < (long long)n * pages;
              x += (long long)gridDim.x * (32 * kWarps)) {

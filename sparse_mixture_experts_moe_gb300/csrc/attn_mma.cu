@@ -74,7 +74,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     nrows = min(kRows, da.n * G - row0);
     j_begin = min(da.shared, (int)blockIdx.z * sp.per);
     j_end = min(da.shared, j_begin + sp.per);
-    const int s0 = da.slots[0];  // an out-of-range slot or page is recorded by the own part
+    const int s0 = da.lead[0];  // an out-of-range slot or page is recorded by the own part
     pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
     const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first

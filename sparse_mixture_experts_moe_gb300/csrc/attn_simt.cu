@@ -83,7 +83,7 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     nrows = min(kRows, da.n * G - row0);
     j_begin = min(da.shared, (int)blockIdx.z * sp.per);
     j_end = min(da.shared, j_begin + sp.per);
-    const int s0 = da.slots[0];  // an out-of-range slot or page is recorded by the own part
+    const int s0 = da.lead[0];  // an out-of-range slot or page is recorded by the own part
     pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
     const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
@@ -377,7 +377,7 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
   const int32_t* pages = c.table + (long long)slot * c.width;
   if (first_piece > 0 && len > 0 && blockIdx.y == 0 && blockIdx.z == 0 && row0 == 0) {
     // that the slots share what the caller says they share
-    const int s0 = a.slots[0];
+    const int s0 = a.lead[0];
     if (s0 >= 0 && s0 < c.n_slots)
       for (int p = tid; p < a.shared >> c.page_shift && (p << c.page_shift) < len; p += 32 * kRowWarps) {
         const int page = pages[p];

@@ -236,7 +236,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const int32_t* table = nullptr;
       int pages = 0;
       if (SHARED) {
-        int slot = sa.d.slots[0];  // an out-of-range slot or page is recorded by the own part
+        int slot = sa.d.lead[0];  // an out-of-range slot or page is recorded by the own part
         slot = slot < 0 || slot >= sa.d.c.n_slots ? 0 : slot;
         table = sa.d.c.table + (long long)slot * sa.d.c.width;
         pages = sa.d.shared >> sa.d.c.page_shift;
