@@ -62,6 +62,7 @@ struct DecodeArgs {
   const int32_t* slots;
   const int32_t* lead;  // the call's first slot, whose pages hold the shared positions (slots may begin at a slice)
   int n, H, shared;
+  int first;  // number in the call of row 0, for errors
   float scale;
   CacheView c;
   const void *k, *v;  // the layer's pages
@@ -123,6 +124,27 @@ cudaError_t launch_cache_write(const CacheView& c, const CacheWs& w, int layer, 
                                long long ks, long long vs, cudaStream_t s);
 
 // ------------------------------------------------------------------ device helpers
+// That slots [i0, i1) hold the pages of the call's first slot in columns [p0, p1) of the shared positions, as far as
+// they reach, and that the first slot has them at all; `me` of `all` threads. A row that does not is recorded. (Slots out
+// of range, and lengths, are recorded where the rows' own positions are read.)
+__device__ __forceinline__ void check_shared(const DecodeArgs& a, int i0, int i1, int p0, int p1, int me, int all) {
+  const CacheView& c = a.c;
+  const int s0 = a.lead[0], np = p1 - p0;
+  if (s0 < 0 || s0 >= c.n_slots) return;
+  const int32_t* lead = c.table + (long long)s0 * c.width;
+  const int held = c.lens[s0];
+  for (long long x = me; x < (long long)(i1 - i0) * np; x += all) {
+    const int i = i0 + (int)(x / np), p = p0 + (int)(x % np), s = a.slots[i];
+    if ((p << c.page_shift) >= held) {
+      if (a.first + i == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, 0);
+      continue;
+    }
+    if (s < 0 || s >= c.n_slots || (p << c.page_shift) >= c.lens[s]) continue;
+    const int page = c.table[(long long)s * c.width + p];
+    if (page < 0 || page >= c.n_pages || page != lead[p]) record_error(a.status, MOE_ERR_DEVICE_CHECK, a.first + i);
+  }
+}
+
 // A tile slot of packed prompts: with R rows a tile, sequence i (L_i tokens) owns the slots
 // floor(q_offsets[i] G / R) + i up to the next sequence's first, which are never fewer than its
 // ceil(L_i G / R) tiles. So tile slots are found from the offsets alone, with no scan over the

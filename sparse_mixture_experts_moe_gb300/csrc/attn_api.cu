@@ -186,7 +186,7 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   if (q == nullptr || slots == nullptr || out == nullptr || !aligned16(q) || !aligned16(out))
     return MOE_ERR_INVALID_ARG;
   DecodeArgs a;
-  a.q = q; a.qs = q_stride; a.os = out_stride; a.slots = slots; a.lead = slots; a.n = n; a.H = H; a.shared = shared_len;
+  a.q = q; a.qs = q_stride; a.os = out_stride; a.slots = slots; a.lead = slots; a.first = 0; a.n = n; a.H = H; a.shared = shared_len;
   a.scale = scale;
   a.c = view_of(cache);
   const size_t off = (size_t)layer * a.c.layer_elems() * elem_bytes(cache->dt);

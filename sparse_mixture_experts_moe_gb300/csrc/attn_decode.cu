@@ -65,7 +65,6 @@ struct OwnArgs {
   const float* sh_o;      // [(sequence, head)][splits][D]
   const float2* sh_ml;
   int splits;      // pieces of a row over the shared keys
-  int first;       // sequence number of the slice's first row (for errors)
   int* next_run;   // nullable: runs are taken from this counter (zero before the call; the join sets it back)
   int n_runs;      // runs that the units are cut into (at most); without the counter one a CTA
   int min_run;     // units of a run, at least
@@ -148,7 +147,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (s >= 0 && s < c.n_slots) len = c.lens[s];
     const bool bad = s < 0 || s >= c.n_slots || len < 0 || (long long)len > ((long long)c.width << c.page_shift);
     if (bad) {
-      if (blockIdx.x == 0) record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + i);
+      if (blockIdx.x == 0) record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.d.first + i);
       len = 0;
     }
     const int nb = len > a.d.shared ? (len - a.d.shared + kUnit - 1) / kUnit + kEnd : 0;
@@ -282,7 +281,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               const int nr = rows - r >= box ? box : kKeys;  // whole boxes, then 16 rows at a time
               if (r > 0) page = row_pages[(key + r) >> c.page_shift];
               if (page < 0 || page >= c.n_pages) {
-                record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + cur);
+                record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.d.first + cur);
                 page = 0;
               }
               const int row = (page * c.Hkv + cu.hr / a.RG) * c.page_size + ((key + r) & (c.page_size - 1));
@@ -308,19 +307,6 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     // lane that loads.
     __syncwarp();
   } else {
-    // that the slots share what the caller says they share
-    if (a.d.shared > 0) {
-      const int s0 = a.d.lead[0], pages = a.d.shared >> c.page_shift;
-      if (s0 >= 0 && s0 < c.n_slots)
-        for (long long x = (long long)blockIdx.x * (32 * kWarps) + tid; x < (long long)n * pages;
-             x += (long long)gridDim.x * (32 * kWarps)) {
-          const int i = (int)(x / pages), p = (int)(x % pages), s = a.d.slots[i];
-          if (s < 0 || s >= c.n_slots || (p << c.page_shift) >= c.lens[s]) continue;
-          const int page = c.table[(long long)s * c.width + p];
-          if (page < 0 || page >= c.n_pages || page != c.table[(long long)s0 * c.width + p])
-            record_error(a.d.status, MOE_ERR_DEVICE_CHECK, a.first + i);
-        }
-    }
     const float c2 = a.d.scale * 1.4426950408889634f, thr = 8.0f / c2;
     const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, group = warp >> 2;
     const int mi = lane >> 3, l8 = lane & 7;
@@ -676,8 +662,8 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, const CacheMaps& m, cud
     d.slots = all.slots + first;
     if (all.lse != nullptr) d.lse = all.lse + (long long)first * all.H;
     OwnArgs o;
+    d.first = first;
     o.d = d;
-    o.first = first;
     o.splits = 0;
     o.R = R;
     o.RG = RG;

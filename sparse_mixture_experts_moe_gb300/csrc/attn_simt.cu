@@ -375,16 +375,8 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
     len = (int)max(0ll, min((long long)c.lens[slot], (long long)c.width << c.page_shift));
   }
   const int32_t* pages = c.table + (long long)slot * c.width;
-  if (first_piece > 0 && len > 0 && blockIdx.y == 0 && blockIdx.z == 0 && row0 == 0) {
-    // that the slots share what the caller says they share
-    const int s0 = a.lead[0];
-    if (s0 >= 0 && s0 < c.n_slots)
-      for (int p = tid; p < a.shared >> c.page_shift && (p << c.page_shift) < len; p += 32 * kRowWarps) {
-        const int page = pages[p];
-        if (page < 0 || page >= c.n_pages || page != c.table[(long long)s0 * c.width + p])
-          record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
-      }
-  }
+  if (a.shared > 0 && blockIdx.y == 0 && blockIdx.z == 0 && row0 == 0)
+    check_shared(a, seq, seq + 1, 0, a.shared >> c.page_shift, tid, 32 * kRowWarps);
   // this CTA's keys, then this warp's: NK at a time, the warps in turn
   const int own = max(0, len - from), step = NK * kRowWarps;
   const int per = (int)(((long long)own + splits - 1) / splits + step - 1) / step * step;

@@ -65,3 +65,58 @@ def test_decode_slice_that_begins_with_a_bad_slot(bad):
     at = [i for i in range(n) if i != 2048]
     ref = decode_reference(q[at], c, [rows[slots[i]] for i in at], [lens[slots[i]] for i in at], 0, 32 ** -0.5)
     check(out[at], lse[at], ref, max(lens), 32, BF16)
+
+
+# --------------------------------------------------------------------------- slots that do not share what the call says
+
+def other_page(c, slot, column):
+    """The slot's page of that column becomes another valid page."""
+    c.table[slot, column] = (c.table[slot, column] + 1) % c.n_pages
+
+
+@pytest.mark.parametrize("n,pages,row", [(64, 512, 63), (64, 512, 5), (64, 512, 32), (3, 700, 2), (70, 9, 40)])
+@pytest.mark.parametrize("H,Hk,D", [(8, 1, 64), (16, 8, 128), (12, 2, 64)])
+def test_decode_other_pages_are_recorded(n, pages, row, H, Hk, D):
+    """Wherever they lie, and however few positions the sequences have of their own."""
+    lens = [16 * pages + (i == 1) for i in range(n)]
+    c, rows = make_cache(lens, 16 * pages, 16, Hk, D, BF16)
+    for column in (0, pages // 2, pages - 1):
+        was = c.table.clone()
+        other_page(c, row, column)
+        out, lse, q, st = decode(c, H, D, BF16, range(n), 16 * pages)
+        assert st == (BAD, row), column
+        c.table.copy_(was)
+        if column == 0:  # the other rows are right
+            right(out, lse, q, c, rows, lens, [i for i in (1, n - 1) if i != row], D, BF16)
+    assert decode(c, H, D, BF16, range(n), 16 * pages)[3] == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 256), (BF16, 136), (BF16, 256), (BF16, 64)])
+@pytest.mark.parametrize("n", [2, 3, 5, 6, 9])
+def test_decode_other_pages_are_recorded_for_few_sequences(n, dtype, D):
+    """Also where each sequence reads the shared positions for itself."""
+    lens = [64] * n
+    c, rows = make_cache(lens, 64, 16, 2, D, dtype)
+    for row, column in ((1, 0), (n - 1, 3)):
+        was = c.table.clone()
+        other_page(c, row, column)
+        assert decode(c, 4, D, dtype, range(n), 64)[3] == (BAD, row)
+        c.table.copy_(was)
+
+
+@pytest.mark.parametrize("n,dtype,D", [(7, BF16, 64), (2, BF16, 64), (7, F32, 64), (2, F32, 64), (7, BF16, 256), (2, BF16, 256)])
+def test_decode_a_first_slot_without_the_prefix_is_recorded(n, dtype, D):
+    lens = [40] + [70] * (n - 1)
+    c, rows = make_cache(lens, 64, 16, 2, D, dtype)
+    trim(c, lens)
+    assert decode(c, 4, D, dtype, range(n), 64)[3] == (BAD, 0)
+
+
+@pytest.mark.parametrize("value", [-1, 1 << 20])
+@pytest.mark.parametrize("n,dtype,D", [(7, BF16, 64), (2, BF16, 64), (7, F32, 64), (2, F32, 64), (7, BF16, 256), (2, BF16, 256)])
+def test_decode_shared_pages_out_of_range_are_recorded(n, dtype, D, value):
+    lens = [64] * n
+    c, rows = make_cache(lens, 64, 16, 2, D, dtype)
+    c.table[:, 2] = value  # the same in every slot
+    st, row = decode(c, 4, D, dtype, range(n), 64)[3]
+    assert st == BAD and 0 <= row < n
