@@ -90,11 +90,11 @@ bool cache_call_ok(const moe_kv_cache* c, const void* ws, size_t ws_bytes) {
 struct CachePlan {
   CacheMaps maps;
   const void *k, *v;
-  int n_layers, n_pages, page_size, H_kv, D;
+  int n_layers, n_pages, page_size, H_kv, D, dt;
 };
 bool plan_holds(const CachePlan& p, const moe_kv_cache* c) {
   return p.k == c->k && p.v == c->v && p.n_layers == c->n_layers && p.n_pages == c->n_pages &&
-         p.page_size == c->page_size && p.H_kv == c->H_kv && p.D == c->D;
+         p.page_size == c->page_size && p.H_kv == c->H_kv && p.D == c->D && p.dt == c->dt;
 }
 bool planned(const moe_kv_cache* c) { return c->dt == MOE_DTYPE_BF16 && c->D <= 128; }
 
@@ -197,15 +197,14 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   a.status = static_cast<int*>(workspace);
   a.timeout_ns = wait_timeout_ns();
   a.layer = layer;
+  CachePlan p;
+  if (cache->plan != nullptr) {
+    std::memcpy(&p, cache->plan, sizeof(p));
+    if (!plan_holds(p, cache)) return MOE_ERR_INVALID_ARG;
+  }
   if (planned(cache)) {
     bind_primary_context();
-    CachePlan p;
-    if (cache->plan != nullptr) {
-      std::memcpy(&p, cache->plan, sizeof(p));
-      if (!plan_holds(p, cache)) return MOE_ERR_INVALID_ARG;
-    } else {
-      if (!encode_cache_maps(a.c, &p.maps)) return MOE_ERR_CUDA;
-    }
+    if (cache->plan == nullptr && !encode_cache_maps(a.c, &p.maps)) return MOE_ERR_CUDA;
     return cuda_status(launch_attn_decode_tc(a, p.maps, (cudaStream_t)stream));
   }
   return cuda_status(launch_attn_decode_simt(a, (cudaStream_t)stream));
@@ -218,7 +217,7 @@ moe_status moe_cache_plan(const moe_kv_cache* cache, void* plan, size_t bytes) {
   CachePlan p{};
   p.k = cache->k; p.v = cache->v;
   p.n_layers = cache->n_layers; p.n_pages = cache->n_pages; p.page_size = cache->page_size;
-  p.H_kv = cache->H_kv; p.D = cache->D;
+  p.H_kv = cache->H_kv; p.D = cache->D; p.dt = cache->dt;
   if (planned(cache)) {  // other caches take the CUDA cores, which need no descriptors
     bind_primary_context();
     if (!encode_cache_maps(view_of(cache), &p.maps)) return MOE_ERR_CUDA;
