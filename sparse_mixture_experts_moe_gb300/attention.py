@@ -85,26 +85,28 @@ class _Bound:
 
 
 class _Workspaces:
-    """Prepared workspaces, one for each stream that calls arrive on, so that calls on different streams never
-    share scratch memory, and one for each graph recording (and stream of it): the graph prepares it at its
+    """Prepared workspaces, one for each stream (of each device) that calls arrive on, so that calls on different streams
+    never share scratch memory, and one for each graph recording (and stream of it): the graph prepares it at its
     first use, and nothing else uses it, however late and on whatever stream the graph runs. (A recording on a stream that
     calls have used before takes that stream's: its replays are to be ordered with further calls there.) Each is
     kept for good: work in flight may use one that a larger one replaced."""
 
     def __init__(self, lib, init):
         self._lib, self._init = lib, init
-        self._of = {}        # stream -> (tensor, bytes, address)
-        self._recorded = {}  # (stream, recording) -> the same
+        self._of = {}        # stream -> (tensor, bytes, address); (stream, device) on others than the first device,
+                             # as the default stream has one handle for all of them
+        self._recorded = {}  # (stream, recording, device) -> the same
         self._old = []
 
     def get(self, stream, nbytes, dev):
-        ws = self._of.get(stream)
+        ws = self._of.get(stream if dev == 0 else (stream, dev))
         return ws if ws is not None and ws[1] >= nbytes else self._make(stream, nbytes, dev)
 
     def _make(self, stream, nbytes, dev):
         import torch
         recording = self._lib.moe_stream_capture_id(stream)
-        of, key = (self._recorded, (stream, recording)) if recording else (self._of, stream)
+        of, key = ((self._recorded, (stream, recording, dev)) if recording
+                   else (self._of, stream if dev == 0 else (stream, dev)))
         ws = of.get(key)
         if ws is not None:
             if ws[1] >= nbytes:
@@ -115,24 +117,27 @@ class _Workspaces:
         if current.cuda_stream != (stream or 0):
             current.synchronize()  # what used this memory before, on the stream that it was allocated for
         ws = of[key] = (t, nbytes, t.data_ptr())
-        _check(self._init(ws[2], nbytes, stream), "workspace_init")
+        with torch.cuda.device(dev):
+            _check(self._init(ws[2], nbytes, stream), "workspace_init")
         return ws
 
     def status(self):
         """(status, detail) of the first device-side error of any of them; clears it."""
         import torch
-        for stream, ws in self._of.items():
-            st, detail = _lib.get_device_status(ws[0], stream)
+        for key, ws in self._of.items():
+            with torch.cuda.device(ws[0].device):
+                st, detail = _lib.get_device_status(ws[0], key[0] if type(key) is tuple else key)
             if st != MOE_OK:
                 return st, detail
-        if self._recorded:
-            torch.cuda.synchronize(next(iter(self._recorded.values()))[0].device)
+        for dev in {ws[0].device for ws in self._recorded.values()}:
+            torch.cuda.synchronize(dev)
         for ws in self._recorded.values():
             # a graph that has not run yet has not prepared its workspace: the header's unused words tell
-            if not ws[0][_HEADER_USED:_HEADER].any():
-                st, detail = _lib.get_device_status(ws[0])
-                if st != MOE_OK:
-                    return st, detail
+            with torch.cuda.device(ws[0].device):
+                if not ws[0][_HEADER_USED:_HEADER].any():
+                    st, detail = _lib.get_device_status(ws[0])
+                    if st != MOE_OK:
+                        return st, detail
         return MOE_OK, 0
 
 
@@ -314,9 +319,9 @@ class Attention(_Bound):
         s = self._raw_stream(dev) if stream is None else _stream(stream)
         need = _HEADER
         if Tk >= _SPLIT_KEYS:
-            if self._sized != (n, Tq, Tk):  # the layers of a model call with the same sizes
+            if self._sized != (n, Tq, Tk, dev):  # the layers of a model call with the same sizes
                 self._sized_bytes = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
-                self._sized = (n, Tq, Tk)
+                self._sized = (n, Tq, Tk, dev)
             need = self._sized_bytes
         ws = self._ws.get(s, need, dev)
         _check(self._prompt(

@@ -1,0 +1,103 @@
+"""Which workspace a call of Attention or KVCache gets. Needs no GPU: memory, streams and the library are stand-ins."""
+import contextlib
+
+import pytest
+import torch
+
+import sparse_mixture_experts_moe_gb300 as moe
+from sparse_mixture_experts_moe_gb300 import _lib
+from sparse_mixture_experts_moe_gb300.attention import _Workspaces
+
+
+class Memory:
+    """A device tensor's place: `live` counts the ones that somebody still holds."""
+    live, made = 0, 0
+
+    def __init__(self, nbytes, device):
+        Memory.live += 1
+        Memory.made += 1
+        self.nbytes, self.device = nbytes, device
+        self.address = Memory.made << 40
+        self.header = [0] * 256  # the header's bytes
+
+    def __del__(self):
+        Memory.live -= 1
+
+    def data_ptr(self):
+        return self.address
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+    def synchronize(self):
+        pass
+
+    def wait_stream(self, other):
+        pass
+
+
+class Lib:
+    """The library's calls that workspaces make."""
+
+    def __init__(self):
+        self.recording = {}  # stream -> number of the recording
+        self.prepared = []
+
+    def moe_stream_capture_id(self, stream):
+        return self.recording.get(stream, 0)
+
+    def init(self, ptr, nbytes, stream):
+        self.prepared.append((ptr, nbytes, stream))
+        return moe.MOE_OK
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """A workspace pool on stand-ins, with the library and the devices that were selected."""
+    lib, selected = Lib(), [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        selected.append(torch.device("cuda", d).index if isinstance(d, int) else d.index)
+        yield
+        selected.pop()
+
+    monkeypatch.setattr(torch, "empty", lambda n, dtype=None, device=None: Memory(n, device))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream(0))
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    pool = _Workspaces(lib, lib.init)
+    return pool, lib, selected
+
+
+def test_a_stream_keeps_its_workspace(world):
+    pool, lib, _ = world
+    a = pool.get(0, 1000, 0)
+    assert pool.get(0, 1000, 0) == a and pool.get(0, 500, 0) == a
+    b = pool.get(7, 1000, 0)
+    assert b[2] != a[2] and pool.get(7, 800, 0) == b
+    assert [p[0] for p in lib.prepared] == [a[2], b[2]]
+
+
+def test_devices_do_not_share_workspaces(world):
+    """The default stream has the same handle on every device."""
+    pool, lib, _ = world
+    a, b = pool.get(0, 1000, 0), pool.get(0, 1000, 1)
+    assert a[2] != b[2] and (a[0].device.index, b[0].device.index) == (0, 1)
+    assert pool.get(0, 1000, 0) == a and pool.get(0, 1000, 1) == b
+    lib.recording[9] = 5
+    c, d = pool.get(9, 1000, 0), pool.get(9, 1000, 1)
+    assert len({x[2] for x in (a, b, c, d)}) == 4
+
+
+def test_workspaces_are_prepared_and_read_on_their_device(world, monkeypatch):
+    pool, lib, selected = world
+    where = []
+    monkeypatch.setattr(pool, "_init", lambda *a: where.append(("init", selected[-1])) or moe.MOE_OK)
+    monkeypatch.setattr(_lib, "get_device_status", lambda ws, stream=None: where.append((ws.device.index, selected[-1])) or (moe.MOE_OK, 0))
+    for dev in (0, 1, 3):
+        pool.get(0, 1000, dev)
+    assert pool.status() == (moe.MOE_OK, 0)
+    assert where == [("init", 0), ("init", 1), ("init", 3), (0, 0), (1, 1), (3, 3)]
