@@ -9,11 +9,11 @@
     out = attn.decode(q, cache, slots, layer=l, shared_len=n)   # one token a sequence
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
-Everything is enqueued on the current stream, or on `stream`; nothing synchronises, except that the first call
-on a `stream` other than the current one (and one that needs a larger workspace) waits for the current one. Calls can
-be recorded into a graph (torch.cuda.graph, GraphCapture). Index tensors (offsets,
-slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the work is
-done by the library's kernels.
+The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
+synchronises, except that the first call on a `stream` other than the current one (and one that needs a larger
+workspace) waits for the current one. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture). Index
+tensors (offsets, slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the
+work is done by the library's kernels.
 """
 from __future__ import annotations
 
@@ -74,10 +74,17 @@ class _Bound:
         self._empty, self._empty_like = torch.empty, torch.empty_like
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._current_device = torch._C._cuda_getDevice
         self._ws = _Workspaces(self._lib, self._init_workspace)
 
     def _init_workspace(self, ptr, nbytes, stream):
         return self._lib.moe_workspace_init(ptr, nbytes, stream)
+
+    def _stream_on(self, dev, stream):
+        """The stream's handle for a call on tensors of CUDA device `dev`. Kernels run on the current device."""
+        if self._current_device() != dev:
+            raise ValueError(f"moe: the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
+        return self._raw_stream(dev) if stream is None else _stream(stream)
 
     def device_status(self):
         """(status, detail) of the first device-side error since the last call; synchronises."""
@@ -194,14 +201,14 @@ class KVCache(_Bound):
 
     def clear(self, stream=None):
         """Empties every slot and frees every page."""
-        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        s = self._stream_on(self._dev, stream)
         _check(self._lib.moe_cache_clear(self._ref, s), "moe_cache_clear")
 
     def resize(self, slots, new_lens, stream=None):
         """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
         n = _ints(slots, "slots", None, self._dev, self._i32)
         _ints(new_lens, "new_lens", n, self._dev, self._i32)
-        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        s = self._stream_on(self._dev, stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_resize")
@@ -216,7 +223,7 @@ class KVCache(_Bound):
         n = _ints(slots, "slots", None, self._dev, self._i32)
         _ints(offsets, "offsets", n + 1, self._dev, self._i32)
         _ints(pos, "pos", n, self._dev, self._i32)
-        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        s = self._stream_on(self._dev, stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
                                          k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
@@ -225,7 +232,7 @@ class KVCache(_Bound):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
         n = _ints(src, "src", None, self._dev, self._i32)
         _ints(dst, "dst", n, self._dev, self._i32)
-        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        s = self._stream_on(self._dev, stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
 
@@ -237,7 +244,7 @@ class KVCache(_Bound):
                 raise ValueError("moe: pass n_live with an explicit stream")
             n_live = self._empty(1, dtype=self._i32, device=self.device)
         _ints(n_live, "n_live", 1, self._dev, self._i32)
-        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        s = self._stream_on(self._dev, stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
         return n_live
@@ -246,7 +253,7 @@ class KVCache(_Bound):
         """Page dst[i] gets page src[i]'s contents in every layer."""
         n = _ints(src, "src", None, self._dev, self._i32)
         _ints(dst, "dst", n, self._dev, self._i32)
-        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        s = self._stream_on(self._dev, stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_copy_pages")
@@ -316,7 +323,7 @@ class Attention(_Bound):
         if kv_offsets is not None:
             _ints(kv_offsets, "kv_offsets", n + 1, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
-        s = self._raw_stream(dev) if stream is None else _stream(stream)
+        s = self._stream_on(dev, stream)
         need = _HEADER
         if Tk >= _SPLIT_KEYS:
             if self._sized != (n, Tq, Tk, dev):  # the layers of a model call with the same sizes
@@ -342,7 +349,7 @@ class Attention(_Bound):
         n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
         _ints(slots, "slots", n, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
-        s = self._raw_stream(dev) if stream is None else _stream(stream)
+        s = self._stream_on(dev, stream)
         ws = self._workspace(s, n, dev)
         _check(self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
                             out.data_ptr(), None if lse is None else lse.data_ptr(), ws[2], ws[1], s),

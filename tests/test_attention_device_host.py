@@ -1,0 +1,96 @@
+"""Calls on tensors of a device that is not the current one, whose kernels would run on another device than the memory
+they are given. Needs no GPU: tensors are stand-ins, and the library's calls are counted, not made."""
+import pytest
+import torch
+
+import sparse_mixture_experts_moe_gb300 as moe
+
+
+class Fake:
+    """What the binding looks at of a dense tensor on cuda:`dev`."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, dev):
+        self.shape, self.dtype, self.device, self._dev = torch.Size(shape), dtype, torch.device("cuda", dev), dev
+
+    def get_device(self):
+        return self._dev
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        s = [1]
+        for n in reversed(self.shape[1:]):
+            s.insert(0, s[0] * n)
+        return tuple(s)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names of the library's kernels that were called; the current device is 0."""
+    called = []
+
+    class Space:
+        def get(self, stream, nbytes, dev, *more):
+            return None, 1 << 40, 1 << 21
+
+    def watch(obj):
+        obj._raw_stream = lambda dev: 0
+        obj._current_device = lambda: 0
+        obj._ws = Space()
+
+        class Lib:
+            def __getattr__(self, name):
+                return (lambda *a: 256) if name.endswith("_bytes") else (lambda *a: called.append(name) or moe.MOE_OK)
+        obj._lib = Lib()
+        for name in ("_prompt", "_decode"):
+            if hasattr(obj, name):
+                setattr(obj, name, lambda *a, name=name: called.append(name) or moe.MOE_OK)
+        return obj
+    return called, watch
+
+
+def cache_on(dev, watch):
+    i = torch.int32
+    kv = Fake((1, 4, 2, 16, 64), torch.float32, dev)
+    return watch(moe.KVCache(kv, kv, Fake((3, 2), i, dev), Fake((3,), i, dev), Fake((4,), i, dev)))
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+def test_attention_calls(calls, dev):
+    called, watch = calls
+    a = watch(moe.Attention(4, 2, 64, torch.float32))
+    c = cache_on(dev, watch)
+    q, kv, i = Fake((3, 4, 64), torch.float32, dev), Fake((3, 2, 64), torch.float32, dev), lambda n: Fake((n,), torch.int32, dev)
+    todo = [lambda: a.prompt(q, kv, kv, i(2), out=q), lambda: a.prompt(q, kv, kv, i(2), out=q, stream=5),
+            lambda: a.decode(q, c, i(3), out=q), lambda: a.decode(q, c, i(3), out=q, stream=5)]
+    for call in todo:
+        if dev == 0:
+            call()
+        else:
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    assert called == (["_prompt", "_prompt", "_decode", "_decode"] if dev == 0 else [])
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+def test_cache_calls(calls, dev):
+    called, watch = calls
+    c = cache_on(dev, watch)
+    kv, i = Fake((3, 2, 64), torch.float32, dev), lambda n: Fake((n,), torch.int32, dev)
+    todo = [c.clear, lambda: c.resize(i(2), i(2)), lambda: c.write(kv, kv, i(2), i(3), i(2)), lambda: c.fork(i(2), i(2)),
+            lambda: c.compact(i(1)), lambda: c.copy_pages(i(2), i(2)), lambda: c.resize(i(2), i(2), stream=5)]
+    for call in todo:
+        if dev == 0:
+            call()
+        else:
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    assert len(called) == (len(todo) if dev == 0 else 0)
