@@ -316,12 +316,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (SHARED) {
               const int rows = min(sa.d.c.page_size, BK);
               for (int r = 0; r < BK; r += rows) {
-                // past the shared keys the last page again: those columns are masked, their values finite or seen
-                // anyway
-                const int p = min((j0 + r) >> sa.d.c.page_shift, pages - 1);
-                int page = table[p];
+                // past the shared keys a box of rows that do not exist: those columns are masked, and the copy fills them
+                // with zeros (weight 0 times a value that is not finite would be NaN)
+                const int p = (j0 + r) >> sa.d.c.page_shift;
+                int page = table[min(p, pages - 1)];
                 page = page < 0 || page >= sa.d.c.n_pages ? 0 : page;
-                const int g = (page * Hkv + it.hk) * sa.d.c.page_size + ((j0 + r) & (sa.d.c.page_size - 1));
+                const int g = p < pages ? (page * Hkv + it.hk) * sa.d.c.page_size + ((j0 + r) & (sa.d.c.page_size - 1)) : -BK;
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c)
                   tma_load_3d(dst + c * (BK * 128) + r * 128, tm, 64 * c, g, sa.d.layer, bar(FULL + stage));

@@ -120,3 +120,21 @@ def test_decode_shared_pages_out_of_range_are_recorded(n, dtype, D, value):
     c.table[:, 2] = value  # the same in every slot
     st, row = decode(c, 4, D, dtype, range(n), 64)[3]
     assert st == BAD and 0 <= row < n
+
+
+# ------------------------------------------------------------------------------------------------- non-finite values
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("page,pages", [(16, 9), (32, 1), (64, 3), (256, 1)])
+def test_decode_infinite_shared_value_stays_infinite(page, pages, value):
+    """An infinite value at the end of the shared positions, which are no whole number of blocks: rows that see it get
+    that infinity, not a NaN."""
+    shared, n, D = page * pages, 5, 64
+    lens = [shared + i for i in range(n)]
+    c, rows = make_cache(lens, shared, page, 2, D, BF16)
+    for at in (shared - 1, shared - page):
+        c.v[0, rows[0][at // page], 1, at % page, 5] = value
+    out, lse, q, st = decode(c, 8, D, BF16, range(n), shared)
+    assert st == (moe.MOE_OK, 0)
+    assert (out[:, 4:, 5] == value).all()
+    assert torch.isfinite(out[:, :4]).all() and torch.isfinite(out[:, 4:, 6:]).all()
