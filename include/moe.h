@@ -399,7 +399,8 @@ moe_status moe_graph_destroy(moe_graph graph);
  *   multiple of 16; anything else is MOE_ERR_INVALID_ARG.
  * A row that sees no key has out = 0 and lse = -inf. lse (nullable) is the natural logarithm of the sum
  *   of the exponentials of the scaled scores, fp32.
- * A non-finite key or value reaches only the rows that see its position.
+ * A non-finite key or value reaches only the rows that see its position. A value's column of such a row is then not
+ *   finite (an infinity or NaN); a score that is not finite may make the whole row NaN.
  *
  * moe_attention_prompt — attention over packed prompts. Sequence i has the query tokens
  *   q_offsets[i] .. q_offsets[i+1]-1 and the keys kv_offsets[i] .. kv_offsets[i+1]-1 (int32 device

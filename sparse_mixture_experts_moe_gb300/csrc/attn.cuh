@@ -81,6 +81,10 @@ struct SharedPart {
   int pieces;       // of a row altogether
 };
 
+// What the other warps' waits allow a softmax warp of attn_tc.cu that replaces columns of its 32 rows (replace_unseen):
+// 0.4 us a key and row, where 0.1 was measured.
+constexpr uint64_t replace_time(long long keys) { return (uint64_t)keys * 32 * 400; }
+
 // Workspace of one decode call. A piece is the attention of one row over a part of its keys: the sum of
 // the weighted values (D floats), the weights' sum l and the reference m (in log2 units) that the
 // weights 2^(s - m) were taken against. A row's pieces join as out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
@@ -262,11 +266,120 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     }
   }
 }
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // the hardware 2^x, ~2 ulp; 2^-inf = 0
   return y;
+}
+
+// ------------------------------------------------------------------ rows that an unseen value made NaN
+// A tile of the tensor cores multiplies the values of columns that a row does not see by a weight of 0, which makes NaN
+// of a value that is not finite. The columns d of the head that this can touch are known: those with such a value in
+// V[lim .. end) (the row sees lim keys, the tile's products took end). Their results are replaced, by a warp:
+//   - where the row sees values that are not finite in d too, by what these add up to with weights above 0
+//     (NaN, or an infinity),
+//   - else by sum_j 2^(c q.k_j - c m) v_j[d] with the row's own m, every key computed again.
+// Everything else the row already has is right. So the keys are only computed again for rows near the first such value of a column,
+// and the two scans of V go on from row to row. (With every row that was not finite computed again over all its keys, one
+// infinity made 8192 tokens of 32 heads of 128 take 200 ms instead of 0.4. One near the end takes 25 ms now, 120 then.)
+// A lane has columns 8 lane .. 8 lane + 7. at(j, ko, vo): the element offsets of key j.
+struct Unseen {
+  int from, upto;   // V has been looked through in [from, end) and in [0, upto)
+  int last[8];      // the last key of the first stretch whose value is not finite
+  uint32_t seen;    // of the second: a bit a column, 8 of NaN, 8 of +inf, 8 of -inf
+  __device__ __forceinline__ explicit Unseen(int end) : from(end), upto(0), seen(0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) last[e] = -1;
+  }
+};
+__device__ __forceinline__ bool not_finite2(uint32_t x) {
+  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
+// found(e, bits, j) for every value in [a, b) that is not finite; more(): goes on
+template <typename At, typename Found, typename More>
+__device__ __forceinline__ int scan_values(const __nv_bfloat16* v, At at, int D, int a, int b, Found found, More more) {
+  const int d = (int)(threadIdx.x & 31) * 8;
+  int j = a;
+  while (j < b && more()) {
+    uint4 u[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      long long ko, vo;
+      at(j + min(y, b - 1 - j), ko, vo);
+      u[y] = d < D ? *reinterpret_cast<const uint4*>(v + vo + d) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      if (!not_finite2(u[y].x) && !not_finite2(u[y].y) && !not_finite2(u[y].z) && !not_finite2(u[y].w)) continue;
+      const uint32_t w[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t h = w[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+        if ((h & 0x7F80u) == 0x7F80u) found(e, h, j + min(y, b - 1 - j));
+      }
+    }
+    j += min(8, b - j);
+  }
+  return j;
+}
+// The columns of a row to replace (a bit each) and their sums, not yet divided. mc: m times scale * log2 e, 0 for -inf.
+template <typename At>
+__device__ __forceinline__ uint32_t replace_unseen(Unseen& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                                   const __nv_bfloat16* v, At at, int D, int lim, float c2, float mc,
+                                                   float (&o)[8]) {
+  if (lim < s.from) {
+    scan_values(v, at, D, lim, s.from, [&](int e, uint32_t, int j) { s.last[e] = max(s.last[e], j); }, [] { return true; });
+    s.from = lim;
+  }
+  uint32_t cols = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) cols |= (s.last[e] >= lim ? 1u : 0u) << e;
+  if (!__any_sync(0xffffffffu, cols != 0)) return 0;
+  if (s.upto > lim) {  // (rows in another order than their limits)
+    s.upto = 0;
+    s.seen = 0;
+  }
+  s.upto = scan_values(
+      v, at, D, s.upto, lim,
+      [&](int e, uint32_t h, int) { s.seen |= (1u << e) << ((h & 0x7FFFu) > 0x7F80u ? 0 : (h & 0x8000u) ? 16 : 8); },
+      [&] { return __any_sync(0xffffffffu, (cols & ~s.seen) != 0) != 0; });
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.f;
+  const uint32_t odd = (s.seen | s.seen >> 8 | s.seen >> 16) & 0xFFu;
+  if (__any_sync(0xffffffffu, (cols & ~odd) != 0)) {
+    const int lane = (int)(threadIdx.x & 31), d = lane * 8;
+    for (int j0 = 0; j0 < lim; j0 += min(32, lim - j0)) {
+      long long ko, vo;
+      at(j0 + min(lane, lim - 1 - j0), ko, vo);
+      float x = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(q + c), b = *reinterpret_cast<const uint4*>(k + ko + c);
+        x = fmaf(bf16lo(a.x), bf16lo(b.x), x); x = fmaf(bf16hi(a.x), bf16hi(b.x), x);
+        x = fmaf(bf16lo(a.y), bf16lo(b.y), x); x = fmaf(bf16hi(a.y), bf16hi(b.y), x);
+        x = fmaf(bf16lo(a.z), bf16lo(b.z), x); x = fmaf(bf16hi(a.z), bf16hi(b.z), x);
+        x = fmaf(bf16lo(a.w), bf16lo(b.w), x); x = fmaf(bf16hi(a.w), bf16hi(b.w), x);
+      }
+      const float p = lane < lim - j0 ? ex2(fmaf(x, c2, -mc)) : 0.f;
+#pragma unroll 8
+      for (int y = 0; y < 32; ++y) {
+        const float py = __shfl_sync(0xffffffffu, p, y);
+        const long long vy = __shfl_sync(0xffffffffu, vo, y);
+        const uint4 u = d < D ? *reinterpret_cast<const uint4*>(v + vy + d) : make_uint4(0u, 0u, 0u, 0u);
+        o[0] = fmaf(py, bf16lo(u.x), o[0]); o[1] = fmaf(py, bf16hi(u.x), o[1]);
+        o[2] = fmaf(py, bf16lo(u.y), o[2]); o[3] = fmaf(py, bf16hi(u.y), o[3]);
+        o[4] = fmaf(py, bf16lo(u.z), o[4]); o[5] = fmaf(py, bf16hi(u.z), o[5]);
+        o[6] = fmaf(py, bf16lo(u.w), o[6]); o[7] = fmaf(py, bf16hi(u.w), o[7]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if ((odd >> e & 1u) == 0) continue;
+    const bool nan = s.seen >> e & 1u, up = s.seen >> (8 + e) & 1u, down = s.seen >> (16 + e) & 1u;
+    o[e] = nan || (up && down) ? __int_as_float(0x7FFFFFFF) : up ? INFINITY : -INFINITY;
+  }
+  return cols;
 }
 
 }  // namespace moe

@@ -151,7 +151,7 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
   a.dt = dt;
   a.out = out; a.lse = lse;
   a.status = static_cast<int*>(workspace);
-  a.timeout_ns = wait_timeout_ns();
+  a.timeout_ns = wait_timeout_ns() + replace_time(Tkv);
   // bf16 heads of up to 128 elements go to tcgen05 (a tile of longer ones does not fit in TMEM); its copies need a key.
   if (dt == MOE_DTYPE_BF16 && D <= 128 && Tkv > 0) {
     bind_primary_context();
@@ -195,7 +195,7 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   a.out = out; a.lse = lse;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(kWsHeaderBytes));
   a.status = static_cast<int*>(workspace);
-  a.timeout_ns = wait_timeout_ns();
+  a.timeout_ns = wait_timeout_ns() + replace_time(shared_len);
   a.layer = layer;
   CachePlan p;
   if (cache->plan != nullptr) {

@@ -11,8 +11,8 @@
 // Bound by the MMA's operands: each 16 x 16 piece of K or V read from shared memory meets only the warp's 16 rows. 4096
 // tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us. Decode,
 // 64 sequences behind 2048 shared positions with 2048 of their own: 157 us (340 with the shared ones on the CUDA
-// cores). A row whose result is not finite is computed again over the keys that it sees, as in attn_tc.cu: 0 times a
-// non-finite value that the row does not see must not reach it.
+// cores). Columns of a row that a non-finite value at a position which it does not see can have touched are replaced, as
+// in attn_tc.cu: 0 times that value must not reach it.
 #include "attn.cuh"
 #include "kernels.cuh"
 
@@ -27,31 +27,11 @@ template <int DP> constexpr size_t mma_smem() { return (size_t)(kRows + 2 * KT) 
 // Byte offset of 16-byte piece u of row r.
 template <int DP> __device__ __forceinline__ uint32_t piece(int r, int u) { return (uint32_t)(r * DP * 2 + ((u ^ (r & 7)) << 4)); }
 
-// One row again, key by key (a warp; a lane owns 8 consecutive elements): its sums against the maximum m, in log2
-// units. at(j, ko, vo) gives the element offsets of key j.
+// (a call, as its registers would be the kernel's)
 template <typename At>
-__device__ __noinline__ void exact_row256(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v, At at, int D,
-                                          int j0, int lim, float c2, float (&o)[8], float& m, float& l) {
-  const int d = (threadIdx.x & 31) * 8;
-  const bool on = d < D;
-  m = -INFINITY;
-  l = 0.f;
-  for (int e = 0; e < 8; ++e) o[e] = 0.f;
-  for (int j = j0; j < lim; ++j) {
-    long long ko, vo;
-    at(j, ko, vo);
-    float s = 0.f;
-    if (on)
-      for (int e = 0; e < 8; ++e) s = fmaf(__bfloat162float(q[d + e]), __bfloat162float(k[ko + d + e]), s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= c2;
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, x = ex2(m - ref), p = ex2(s - ref);
-    l = fmaf(l, x, p);
-    m = mn;
-    if (on)
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(p, __bfloat162float(v[vo + d + e]), o[e] * x);
-  }
+__device__ __noinline__ uint32_t replace_row(Unseen& s, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                             At at, int D, int lim, float c2, float mc, float (&o)[8]) {
+  return replace_unseen(s, q, k, v, at, D, lim, c2, mc, o);
 }
 
 // SPLIT: a tile's keys over the CTAs of a cluster. SHARED: the shared positions of a decode call, as in attn_simt.cu.
@@ -66,7 +46,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   const DecodeArgs& da = sp.d;
   const int H = SHARED ? da.H : a.H, Hkv = SHARED ? da.c.Hkv : a.Hkv, D = SHARED ? da.c.D : a.D;
   const int G = H / Hkv, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int row0, nrows, j_begin, j_end;
+  int row0, nrows, j_begin, j_end, tile_end = 0;
   Seq sq{0, 0, 0, 0};
   const int32_t* pages = nullptr;
   if (SHARED) {
@@ -85,9 +65,9 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     row0 = (int)r0;
     nrows = min(kRows, sq.nq * G - row0);
     j_begin = 0;
-    j_end = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, a.causal);
+    j_end = tile_end = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, a.causal);
     if (SPLIT) {
-      const int keys = j_end, per = ((keys - 1) / KT / (int)gridDim.z + 1) * KT;
+      const int keys = tile_end, per = ((keys - 1) / KT / (int)gridDim.z + 1) * KT;
       j_begin = (int)min((long long)keys, (long long)blockIdx.z * per);
       j_end = (int)min((long long)keys, (long long)j_begin + per);
     }
@@ -220,21 +200,27 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  auto exact = [&](int R) {  // row R of the tile, by a warp
+  Unseen unseen(SHARED || !SPLIT ? j_end : tile_end);
+  auto replace = [&](int R, float mr, float lr) {  // in row R of the tile, by a warp
     const int P = row0 + R, tok = P / G, h = hk * G + P % G;
-    float x[8], mx, lx;
-    exact_row256(qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + (long long)sq.k0 * a.ks + (long long)hk * D,
-                 vb + (long long)sq.k0 * a.vs + (long long)hk * D,
-                 [&](int j, long long& ko, long long& vo) {
-                   ko = j * a.ks;
-                   vo = j * a.vs;
-                 },
-                 D, 0, visible_keys(tok, sq.nq, sq.nk, a.causal), c2, x, mx, lx);
-    const float inv = lx == 0.f ? 0.f : 1.0f / lx;
+    float x[8];
+    const uint32_t cols = replace_row(
+        unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + (long long)sq.k0 * a.ks + (long long)hk * D,
+        vb + (long long)sq.k0 * a.vs + (long long)hk * D,
+        [&](int j, long long& ko, long long& vo) {
+          ko = j * a.ks;
+          vo = j * a.vs;
+        },
+        D, visible_keys(tok, sq.nq, sq.nk, a.causal), c2, mr == -INFINITY ? 0.f : mr * c2, x);
+    const float inv = lr == 0.f ? 0.f : 1.0f / lr;
     __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (long long)(sq.q0 + tok) * a.os + (long long)h * D + lane * 8;
-    if (lane * 8 < D)
-      for (int e = 0; e < 8; ++e) dst[e] = __float2bfloat16_rn(x[e] * inv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (cols >> e & 1u) dst[e] = __float2bfloat16_rn(x[e] * inv);
   };
+  // m and l of row r of the warp's 16
+  auto row_m = [&](int r) { return __shfl_sync(0xffffffffu, r < 8 ? m[0] : m[1], 4 * (r & 7)); };
+  auto row_l = [&](int r) { return __shfl_sync(0xffffffffu, r < 8 ? l[0] : l[1], 4 * (r & 7)); };
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
@@ -255,20 +241,24 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
         if (r < nrows && c < D) *reinterpret_cast<float2*>(po + c) = make_float2(x, z);
       }
       if (r < nrows && t4 == 0) *reinterpret_cast<float2*>(po + D) = make_float2(m[y] * c2, l[y]);
-      again[y] = __ballot_sync(0xffffffffu, r < nrows && !fine && lim[y] < j_end);
+      again[y] = __ballot_sync(0xffffffffu, r < nrows && !fine && fabsf(l[y]) <= 3.0e38f);
     }
     __syncwarp();
+    Unseen pieces_unseen(j_end - j_begin);
     for (int r = 0; r < 16; ++r) {
       if ((again[r >> 3] >> (4 * (r & 7)) & 15u) == 0) continue;
       const int P = row0 + warp * 16 + r, tok = P / G, h = hk * G + P % G;
-      float x[8], mx, lx;
-      exact_row256(qb + (long long)tok * qs + (long long)h * D, kb, vb,
-                   [&](int j, long long& ko, long long& vo) { ko = vo = paged(j); }, D, j_begin,
-                   min(j_end, max(0, da.c.lens[da.slots[tok]])), c2, x, mx, lx);
+      float x[8];
+      const float mr = row_m(r);
+      const int j0 = j_begin;  // (the keys counted from the piece's first)
+      const uint32_t cols = replace_row(
+          pieces_unseen, qb + (long long)tok * qs + (long long)h * D, kb, vb,
+          [&](int j, long long& ko, long long& vo) { ko = vo = paged(j0 + j); }, D,
+          max(0, min(j_end, max(0, da.c.lens[da.slots[tok]])) - j0), c2, mr == -INFINITY ? 0.f : mr * c2, x);
       float* po = da.part + (((long long)tok * H + h) * sp.pieces + blockIdx.z) * (D + 2);
-      if (lane * 8 < D)
-        for (int e = 0; e < 8; ++e) po[lane * 8 + e] = x[e];
-      if (lane == 0) *reinterpret_cast<float2*>(po + D) = make_float2(mx, lx);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (cols >> e & 1u) po[lane * 8 + e] = x[e];
     }
     return;
   }
@@ -279,8 +269,9 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     const int C = gridDim.z, rank = (int)cluster_ctarank();
     float* po = reinterpret_cast<float*>(smem);
     float2* ml = reinterpret_cast<float2*>(po + kRows * LD);
-    int* odd = reinterpret_cast<int*>(ml + kRows);
-    static_assert(kRows * (LD * 4 + 8 + 4) <= mma_smem<DP>(), "the parts take the tiles' place");
+    float2* joined = ml + kRows;  // a row's m and l
+    int* odd = reinterpret_cast<int*>(joined + kRows);
+    static_assert(kRows * (LD * 4 + 8 + 8 + 4) <= mma_smem<DP>(), "the parts take the tiles' place");
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -328,12 +319,16 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       if (!(fabsf(t.x) <= 3.0e38f && fabsf(t.y) <= 3.0e38f && fabsf(t.z) <= 3.0e38f && fabsf(t.w) <= 3.0e38f)) odd[R] = 1;
       *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * D + c) =
           make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+      if (c == 0) joined[R] = make_float2(M, L);
       if (a.lse != nullptr && c == 0)
         a.lse[(long long)tok * H + h] = none ? -INFINITY : (M * c2 + log2f(L)) * 0.6931471805599453f;
     }
     __syncthreads();
-    for (int r = warp; r < kRows / C; r += kThreads / 32)
-      if (odd[rank + C * r] != 0) exact(rank + C * r);
+    // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
+    for (int r = warp; r < kRows / C; r += kThreads / 32) {
+      const int R = rank + C * r;
+      if (odd[R] != 0 && fabsf(joined[R].y) <= 3.0e38f) replace(R, joined[R].x, joined[R].y);
+    }
     cluster_sync_all();  // the others have read this CTA's part
     return;
   }
@@ -353,12 +348,13 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     }
     if (a.lse != nullptr && r < nrows && t4 == 0)
       a.lse[(long long)tok * H + h] = lim[y] == 0 ? -INFINITY : (m[y] * c2 + log2f(l[y])) * 0.6931471805599453f;
-    again[y] = __ballot_sync(0xffffffffu, r < nrows && !fine);
+    again[y] = __ballot_sync(0xffffffffu, r < nrows && !fine && fabsf(l[y]) <= 3.0e38f);
   }
   __syncwarp();
   for (int r = 0; r < 16; ++r) {
     if ((again[r >> 3] >> (4 * (r & 7)) & 15u) == 0) continue;
-    exact(warp * 16 + r);
+    const float mr = row_m(r), lr = row_l(r);
+    replace(warp * 16 + r, mr, lr);
   }
 }
 

@@ -24,10 +24,10 @@
 // that is rare, so no warps are kept for it.
 // A weight is rounded to bf16 (off by at most 2^-8 of it) because the MMA takes both operands in one type; its
 // sum l takes the unrounded value.
-// Keys past a row's limit get weight 0 by index. 0 times a non-finite value in V would still be NaN: a row whose
-// result is not finite is computed again, key by key over the keys it sees (exact_row), so that a
-// non-finite value reaches only rows that see it. That costs nothing where everything is finite.
-// All waits are bounded, as in ffn_tc.cu.
+// Keys past a row's limit get weight 0 by index. 0 times a non-finite value in V would still be NaN: the columns of a row
+// that such a value can have touched are replaced (replace_unseen), so that a non-finite value reaches only rows that
+// see it. That costs nothing where everything is finite.
+// All waits are bounded, as in ffn_tc.cu, with time for rows that are replaced (replace_time).
 // Measured: one prompt of 16384 tokens, 32 heads of 128 on 8: 1.23 ms in a run of ten (1.79 PFLOP/s, 94% of the matrix
 // rate measured in a burst), 1.35 ms in a loop of seconds (1.63, 94% of the sustained rate). Heads of 64: 1.03 ms,
 // 1.06 PFLOP/s, bound by the powers of two: 256 warp instructions of 8 cycles a scheduler and block of a tile pair are
@@ -108,40 +108,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok));
   return ok != 0;
-}
-
-// One row again, key by key (a warp; lane owns 4 consecutive elements): only keys below lim take part.
-// at(j, k, v) gives key j's element offsets.
-template <typename At>
-__device__ __forceinline__ void exact_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v, At at,
-                                          int D, int lim, float c2, float (&o)[4], float& m, float& l) {
-  const int d = (int)(threadIdx.x & 31) * 4;
-  const bool on = d < D;
-  float qv[4] = {0.f, 0.f, 0.f, 0.f};
-  if (on)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) qv[e] = __bfloat162float(q[d + e]);
-  m = -INFINITY;
-  l = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = 0.f;
-  for (int j = 0; j < lim; ++j) {
-    float s = 0.f;
-    long long ko, vo;
-    at(j, ko, vo);
-    if (on)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(qv[e], __bfloat162float(k[ko + d + e]), s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= c2;
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), p = ex2(s - ref);
-    l = fmaf(l, a, p);
-    m = mn;
-    if (on)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = fmaf(p, __bfloat162float(v[vo + d + e]), o[e] * a);
-  }
 }
 
 struct SharedArgs {
@@ -316,12 +282,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (SHARED) {
               const int rows = min(sa.d.c.page_size, BK);
               for (int r = 0; r < BK; r += rows) {
-                // past the shared keys a box of rows that do not exist: those columns are masked, and the copy fills them
-                // with zeros (weight 0 times a value that is not finite would be NaN)
-                const int p = (j0 + r) >> sa.d.c.page_shift;
-                int page = table[min(p, pages - 1)];
+                // past the shared keys the last page again: those columns are masked (and looked through for values that
+                // are not finite like any that a row does not see)
+                const int p = min((j0 + r) >> sa.d.c.page_shift, pages - 1);
+                int page = table[p];
                 page = page < 0 || page >= sa.d.c.n_pages ? 0 : page;
-                const int g = p < pages ? (page * Hkv + it.hk) * sa.d.c.page_size + ((j0 + r) & (sa.d.c.page_size - 1)) : -BK;
+                const int g = (page * Hkv + it.hk) * sa.d.c.page_size + ((j0 + r) & (sa.d.c.page_size - 1));
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c)
                   tma_load_3d(dst + c * (BK * 128) + r * 128, tm, 64 * c, g, sa.d.layer, bar(FULL + stage));
@@ -680,41 +646,47 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             __syncwarp();
           }
           if (valid) sa.part_ml[piece] = make_float2(m * c2, l);
-          uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && (SPLIT || lim < it->n_keys));
+          // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
+          uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && fabsf(l) <= 3.0e38f);
+          Unseen unseen(SHARED ? n * BK : min(n * BK, pa.Tkv - it->k0 - it->key0));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
             const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
             const int limw = __shfl_sync(0xffffffffu, lim, w);
-            float o[4], mw, lw;
-            long long pw = ((long long)tw * H + hw) * sa.splits + blockIdx.z;
+            const float mw = __shfl_sync(0xffffffffu, m, w), mcw = mw == -INFINITY ? 0.f : mw * c2;
+            float o[8];
+            long long pw;
+            uint32_t cols;
             if (SPLIT) {
               pw = ((long long)(it->q0 + tw) * H + hw) * sa.splits + it->split;
-              exact_row((const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
-                        (const __nv_bfloat16*)pa.k + (long long)(it->k0 + it->key0) * pa.ks + (long long)it->hk * D,
-                        (const __nv_bfloat16*)pa.v + (long long)(it->k0 + it->key0) * pa.vs + (long long)it->hk * D,
-                        [&](int j, long long& ko, long long& vo) {
-                          ko = (long long)j * pa.ks;
-                          vo = (long long)j * pa.vs;
-                        },
-                        D, limw, c2, o, mw, lw);
+              cols = replace_unseen(unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                                    (const __nv_bfloat16*)pa.k + (long long)(it->k0 + it->key0) * pa.ks + (long long)it->hk * D,
+                                    (const __nv_bfloat16*)pa.v + (long long)(it->k0 + it->key0) * pa.vs + (long long)it->hk * D,
+                                    [&](int j, long long& ko, long long& vo) {
+                                      ko = (long long)j * pa.ks;
+                                      vo = (long long)j * pa.vs;
+                                    },
+                                    D, limw, c2, mcw, o);
             } else {
+              // (the pages are the first slot's, which the other slots share, and past them the last one, as loaded)
               const CacheView& cv = sa.d.c;
-              const int32_t* row = cv.table + (long long)sa.d.slots[tw] * cv.width;
-              exact_row((const __nv_bfloat16*)sa.d.q + (long long)tw * sa.d.qs + (long long)hw * D,
-                        (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v,
-                        [&](int j, long long& ko, long long& vo) {
-                          const int p = it->key0 + j;
-                          int page = row[p >> cv.page_shift];
-                          page = page < 0 || page >= cv.n_pages ? 0 : page;
-                          ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
-                        },
-                        D, limw, c2, o, mw, lw);
+              const int s0 = sa.d.lead[0], last = (sa.d.shared >> cv.page_shift) - 1;
+              const int32_t* row = cv.table + (long long)(s0 < 0 || s0 >= cv.n_slots ? 0 : s0) * cv.width;
+              pw = ((long long)tw * H + hw) * sa.splits + blockIdx.z;
+              cols = replace_unseen(unseen, (const __nv_bfloat16*)sa.d.q + (long long)tw * sa.d.qs + (long long)hw * D,
+                                    (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v,
+                                    [&](int j, long long& ko, long long& vo) {
+                                      const int p = it->key0 + j;
+                                      int page = row[min(p >> cv.page_shift, last)];
+                                      page = page < 0 || page >= cv.n_pages ? 0 : page;
+                                      ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
+                                    },
+                                    D, limw, c2, mcw, o);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (lane * 4 + e < D) sa.part_o[pw * D + lane * 4 + e] = o[e];
-            if (lane == 0) sa.part_ml[pw] = make_float2(mw, lw);
+            for (int e = 0; e < 8; ++e)
+              if (cols >> e & 1u) sa.part_o[pw * D + lane * 8 + e] = o[e];
           }
         } else {
           const float inv = l == 0.f ? 0.f : 1.0f / l;
@@ -765,26 +737,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
           if (valid && pa.lse != nullptr)
             pa.lse[(long long)(it->q0 + tok) * H + h] = lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
-          uint32_t again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f));
+          // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
+          uint32_t again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
+          Unseen unseen(min(n * BK, pa.Tkv - it->k0));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
             const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
             const int limw = __shfl_sync(0xffffffffu, lim, w);
-            float o[4], mw, lw;
-            exact_row((const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
-                      (const __nv_bfloat16*)pa.k + (long long)it->k0 * pa.ks + (long long)it->hk * D,
-                      (const __nv_bfloat16*)pa.v + (long long)it->k0 * pa.vs + (long long)it->hk * D,
-                      [&](int j, long long& ko, long long& vo) {
-                        ko = (long long)j * pa.ks;
-                        vo = (long long)j * pa.vs;
-                      },
-                      D, limw, c2, o, mw, lw);
-            const float iw = lw == 0.f ? 0.f : 1.0f / lw;
+            const float mw = __shfl_sync(0xffffffffu, m, w), iw = __shfl_sync(0xffffffffu, inv, w);
+            float o[8];
+            const uint32_t cols = replace_unseen(
+                unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                (const __nv_bfloat16*)pa.k + (long long)it->k0 * pa.ks + (long long)it->hk * D,
+                (const __nv_bfloat16*)pa.v + (long long)it->k0 * pa.vs + (long long)it->hk * D,
+                [&](int j, long long& ko, long long& vo) {
+                  ko = (long long)j * pa.ks;
+                  vo = (long long)j * pa.vs;
+                },
+                D, limw, c2, mw == -INFINITY ? 0.f : mw * c2, o);
             __nv_bfloat16* dw = (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (lane * 4 + e < D) dw[lane * 4 + e] = __float2bfloat16_rn(o[e] * iw);
+            for (int e = 0; e < 8; ++e)
+              if (cols >> e & 1u) dw[lane * 8 + e] = __float2bfloat16_rn(o[e] * iw);
           }
         }
       }

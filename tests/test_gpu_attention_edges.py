@@ -138,3 +138,56 @@ def test_decode_infinite_shared_value_stays_infinite(page, pages, value):
     assert st == (moe.MOE_OK, 0)
     assert (out[:, 4:, 5] == value).all()
     assert torch.isfinite(out[:, :4]).all() and torch.isfinite(out[:, 4:, 6:]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 200, 256])
+@pytest.mark.parametrize("nq,nk", [([700], [700]), ([40, 300], [900, 300]), ([9, 2], [2500, 64])])
+def test_prompt_values_that_are_not_finite_in_many_columns(nq, nk, D):
+    """Infinities and NaN at many positions and columns: what a row does not see leaves its columns as they are, and what it
+    does see makes them what the formula says."""
+    H, Hk = 4, 2
+    q, k, v = (tensor((sum(x), h, D), s, BF16, DEV) for x, h, s in ((nq, H, 1), (nk, Hk, 2), (nk, Hk, 3)))
+    qo, ko = offsets(nq), offsets(nk)
+    ref = prompt_reference(q, k, v, qo, ko, True, D ** -0.5)
+    hurt = v.clone()
+    n = nk[0]
+    for at, col, value in ((n - 1, 7, "inf"), (n - 1, 8, "nan"), (n - 2, 7, "-inf"), (n - 5, 0, "nan"), (n - 9, 31, "inf"),
+                           (n // 2, D - 1, "-inf"), (n // 2 + 3, D - 2, "inf"), (3, 5, "inf"), (n - 3, 5, "nan")):
+        hurt[at, 1, col] = float(value)
+    a = moe.Attention(H, Hk, D, BF16)
+    out = a.prompt(q, k, hurt, i32(qo, DEV), i32(ko, DEV))
+    assert a.device_status() == (moe.MOE_OK, 0)
+    check(out[:, :2], None, tuple(x[:, :2] for x in ref), max(nk), D, BF16)  # the other key/value head
+    check(out[nq[0]:], None, tuple(x[nq[0]:] for x in ref), max(nk), D, BF16)  # the other sequences
+    got, bad = f64(out[:, 2:]), f64(hurt[:, 1])
+    for t in range(nq[0]):
+        seen = bad[:t + 1 + nk[0] - nq[0]]
+        odd = ~np.isfinite(seen).all(0)
+        for h in range(2):
+            # (a weight of 0 times an infinity is NaN where all the row's keys were multiplied at once)
+            assert not np.isfinite(got[t, h, odd]).any()
+            assert np.isfinite(got[t, h, ~odd]).all(), (t, h)
+    fine = np.isfinite(got)
+    keep = np.where(fine, got, ref[0][:, 2:])  # the finite ones are right
+    check(torch.from_numpy(keep), None, tuple(x[:, 2:] for x in ref), max(nk), D, BF16)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("where", ["first", "late", "column", "all"])
+def test_prompt_with_non_finite_values_takes_no_waits_to_their_limit(where, D, monkeypatch):
+    """Rows that are not finite are not all computed again: a call with waits of at most 20 ms ends without an error."""
+    monkeypatch.setenv("MOE_WAIT_TIMEOUT_MS", "20")
+    T, H, Hk = 6000, 8, 2
+    x = tensor((T, H + 2 * Hk, D), 1, BF16, DEV)
+    q, k, v = x[:, :H], x[:, H:H + Hk], x[:, H + Hk:]
+    at = {"first": (0, 5), "late": (T - 70, 5), "column": (slice(None), 5), "all": (slice(None), slice(None))}[where]
+    v[at[0], 1, at[1]] = float("inf")
+    a = moe.Attention(H, Hk, D, BF16)
+    out = a.prompt(q, k, v, i32([0, T], DEV))
+    assert a.device_status() == (moe.MOE_OK, 0)
+    assert torch.isfinite(out[:, :4]).all()
+    first = {"late": T - 70}.get(where, 0)
+    assert not torch.isfinite(out[first:, 4:, 5]).any() and torch.isfinite(out[:first, 4:]).all()
+    if where != "all":
+        out[:, 4:, 5] = 0
+        assert torch.isfinite(out).all()
