@@ -128,23 +128,19 @@ cudaError_t launch_cache_write(const CacheView& c, const CacheWs& w, int layer, 
                                long long ks, long long vs, cudaStream_t s);
 
 // ------------------------------------------------------------------ device helpers
-// That slots [i0, i1) hold the pages of the call's first slot in columns [p0, p1) of the shared positions, as far as
-// they reach, and that the first slot has them at all; `me` of `all` threads. A row that does not is recorded. (Slots out
-// of range, and lengths, are recorded where the rows' own positions are read.)
-__device__ __forceinline__ void check_shared(const DecodeArgs& a, int i0, int i1, int p0, int p1, int me, int all) {
+// That slot slots[i] holds the pages of the call's first slot at the shared positions, as far as it reaches, and that
+// the first slot has them all; by threads `me` of `all`. A row that does not is recorded.
+__device__ __forceinline__ void check_shared(const DecodeArgs& a, int i, int me, int all) {
   const CacheView& c = a.c;
-  const int s0 = a.lead[0], np = p1 - p0;
+  const int s0 = a.lead[0], s = a.slots[i], pages = a.shared >> c.page_shift;
   if (s0 < 0 || s0 >= c.n_slots) return;
-  const int32_t* lead = c.table + (long long)s0 * c.width;
-  const int held = c.lens[s0];
-  for (long long x = me; x < (long long)(i1 - i0) * np; x += all) {
-    const int i = i0 + (int)(x / np), p = p0 + (int)(x % np), s = a.slots[i];
-    if ((p << c.page_shift) >= held) {
-      if (a.first + i == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, 0);
-      continue;
-    }
-    if (s < 0 || s >= c.n_slots || (p << c.page_shift) >= c.lens[s]) continue;
-    const int page = c.table[(long long)s * c.width + p];
+  auto held_by = [&](int x) { return (int)(((long long)c.lens[x] + c.page_size - 1) >> c.page_shift); };
+  const int held = held_by(s0);
+  if (held < pages && a.first + i == 0 && me == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, 0);
+  const int end = min(pages, min(held, s < 0 || s >= c.n_slots ? 0 : held_by(s)));
+  const int32_t *lead = c.table + (long long)s0 * c.width, *row = c.table + (long long)s * c.width;
+  for (int p = me; p < end; p += all) {
+    const int page = row[p];
     if (page < 0 || page >= c.n_pages || page != lead[p]) record_error(a.status, MOE_ERR_DEVICE_CHECK, a.first + i);
   }
 }

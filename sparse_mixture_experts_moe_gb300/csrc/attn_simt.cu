@@ -376,7 +376,7 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
   }
   const int32_t* pages = c.table + (long long)slot * c.width;
   if (a.shared > 0 && blockIdx.y == 0 && blockIdx.z == 0 && row0 == 0)
-    check_shared(a, seq, seq + 1, 0, a.shared >> c.page_shift, tid, 32 * kRowWarps);
+    check_shared(a, seq, tid, 32 * kRowWarps);
   // this CTA's keys, then this warp's: NK at a time, the warps in turn
   const int own = max(0, len - from), step = NK * kRowWarps;
   const int per = (int)(((long long)own + splits - 1) / splits + step - 1) / step * step;

@@ -336,12 +336,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       constexpr int kLanes = DP / 8, kRowsPer = 32 / kLanes;
       const int t = warp - kSoftWarps - 2;
       uint32_t loads = 0;
-      // With its Q on the way, the warp looks whether the tile's sequences share this item's pages; the items of the other
-      // heads, which have the same rows and keys, take every Hkv-th of them.
-      auto check = [&](const Item& it) {
-        const int r0 = it.row0 + t * TM, r1 = it.row0 + min(it.nrows, (t + 1) * TM) - 1, sh = sa.d.c.page_shift;
-        check_shared(sa.d, r0 / G, r1 / G + 1, it.key0 >> sh, ((it.key0 + it.n_keys - 1) >> sh) + 1, it.hk * 32 + lane, Hkv * 32);
-      };
       while (const Item* ip = next_item()) {
         const Item it = *ip;
         item_done();
@@ -356,7 +350,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               tma_load_3d(sQ + t * C::kTileBytes + c * (TM * 128), &tmQ, 64 * c, it.hk * G, it.q0 + (it.row0 + t * TM) / G,
                           bar(QFULL + t));
           }
-          if (SHARED) check(it);
           continue;
         }
         const int nrow_t = min(TM, it.nrows - t * TM);
@@ -379,7 +372,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(QFULL + t));
-        if (SHARED) check(it);
       }
       if (loads > 0) mbar_wait_bounded(bar(QFULL + t), (loads - 1) & 1u, timeout_ns);  // copies in flight
     } else {
