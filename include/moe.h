@@ -495,9 +495,9 @@ moe_status moe_cache_write(const moe_kv_cache* cache, int layer, const int32_t* 
  *   first slot holds at least shared_len positions.
  * In:  q [n, H, D] (token stride q_stride), slots [n].  Out: out [n, H, D] (out_stride), lse [n, H] or NULL.
  * Workspace: moe_attention_workspace_bytes(n, H, D) bytes, prepared with moe_workspace_init.
- * Device checks: a slot or page out of range, a slot with other pages in the shared part than the first one's, or a
- *   first slot that is shorter than it, records MOE_ERR_DEVICE_CHECK (detail = row). An out-of-range slot's row is 0;
- *   a row with other pages there may attend either. */
+ * Device checks: a slot, length or page out of range, a slot with other pages in the shared part than the first one's, or a
+ *   first slot that is shorter than it, records MOE_ERR_DEVICE_CHECK (detail = row). A row whose slot or
+ *   length is out of range is 0; a row with other pages there may attend either. */
 size_t moe_attention_workspace_bytes(int n, int H, int D);
 moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
                                 int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,

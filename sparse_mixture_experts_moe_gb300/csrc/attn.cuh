@@ -69,7 +69,7 @@ struct DecodeArgs {
   int layer;
   void* out;
   float* lse;
-  float* part;  // partial results, see PartView
+  float* part;  // partial results: attn_simt.cu has [row][piece][D + 2], attn_decode.cu arrays of their own for o and ml
   int* status;
   uint64_t timeout_ns;
 };
@@ -128,16 +128,22 @@ cudaError_t launch_cache_write(const CacheView& c, const CacheWs& w, int layer, 
                                long long ks, long long vs, cudaStream_t s);
 
 // ------------------------------------------------------------------ device helpers
+// Positions that a slot holds: none if the slot or its length is out of range (recorded where the rows' own positions are
+// read).
+__device__ __forceinline__ int slot_len(const CacheView& c, int s) {
+  if (s < 0 || s >= c.n_slots) return 0;
+  const int len = c.lens[s];
+  return len < 0 || (long long)len > (long long)c.width << c.page_shift ? 0 : len;
+}
 // That slot slots[i] holds the pages of the call's first slot at the shared positions, as far as it reaches, and that
 // the first slot has them all; by threads `me` of `all`. A row that does not is recorded.
 __device__ __forceinline__ void check_shared(const DecodeArgs& a, int i, int me, int all) {
   const CacheView& c = a.c;
   const int s0 = a.lead[0], s = a.slots[i], pages = a.shared >> c.page_shift;
   if (s0 < 0 || s0 >= c.n_slots) return;
-  auto held_by = [&](int x) { return (int)(((long long)c.lens[x] + c.page_size - 1) >> c.page_shift); };
-  const int held = held_by(s0);
+  const int held = (slot_len(c, s0) + c.page_size - 1) >> c.page_shift;
   if (held < pages && a.first + i == 0 && me == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, 0);
-  const int end = min(pages, min(held, s < 0 || s >= c.n_slots ? 0 : held_by(s)));
+  const int end = min(pages, min(held, (slot_len(c, s) + c.page_size - 1) >> c.page_shift));
   const int32_t *lead = c.table + (long long)s0 * c.width, *row = c.table + (long long)s * c.width;
   for (int p = me; p < end; p += all) {
     const int page = row[p];

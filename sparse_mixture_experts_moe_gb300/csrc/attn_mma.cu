@@ -118,8 +118,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     const int r = warp * 16 + g + 8 * y;
     lim[y] = 0;
     if (r < nrows && SHARED) {  // a slot shorter than the shared positions sees its own length of them
-      const int s = da.slots[(row0 + r) / G];
-      lim[y] = s < 0 || s >= da.c.n_slots ? 0 : min(j_end, max(0, da.c.lens[s]));
+      lim[y] = min(j_end, slot_len(da.c, da.slots[(row0 + r) / G]));
     } else if (r < nrows) {
       lim[y] = visible_keys((row0 + r) / G, sq.nq, sq.nk, a.causal);
     }
@@ -254,7 +253,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       const uint32_t cols = replace_row(
           pieces_unseen, qb + (long long)tok * qs + (long long)h * D, kb, vb,
           [&](int j, long long& ko, long long& vo) { ko = vo = paged(j0 + j); }, D,
-          max(0, min(j_end, max(0, da.c.lens[da.slots[tok]])) - j0), c2, mr == -INFINITY ? 0.f : mr * c2, x);
+          max(0, min(j_end, slot_len(da.c, da.slots[tok])) - j0), c2, mr == -INFINITY ? 0.f : mr * c2, x);
       float* po = da.part + (((long long)tok * H + h) * sp.pieces + blockIdx.z) * (D + 2);
 #pragma unroll
       for (int e = 0; e < 8; ++e)

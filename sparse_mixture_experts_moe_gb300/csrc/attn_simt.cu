@@ -118,8 +118,7 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     const int R = ty * RPT + r;
     lim[r] = 0;
     if (R < nrows && SHARED) {  // a slot shorter than the shared positions sees its own length of them
-      const int s = da.slots[(row0 + R) / G];
-      lim[r] = s < 0 || s >= da.c.n_slots ? 0 : min(j_end, max(0, da.c.lens[s]));
+      lim[r] = min(j_end, slot_len(da.c, da.slots[(row0 + R) / G]));
     } else if (R < nrows) {
       lim[r] = visible_keys((row0 + R) / G, sq.nq, sq.nk, pa.causal);
     }
@@ -367,13 +366,9 @@ decode_rows_kernel(const __grid_constant__ DecodeArgs a, int groups, int first_p
   const int G = a.H / c.Hkv, D = c.D, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = blockIdx.x / groups, row0 = (blockIdx.x % groups) * GR, nrows = min(GR, G - row0);
   const int from = first_piece > 0 ? a.shared : 0;
-  const int slot = a.slots[seq];
-  int len = 0;
-  if (slot < 0 || slot >= c.n_slots) {
-    if (tid == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
-  } else {
-    len = (int)max(0ll, min((long long)c.lens[slot], (long long)c.width << c.page_shift));
-  }
+  const int slot = a.slots[seq], len = slot_len(c, slot);
+  if (tid == 0 && len == 0 && (slot < 0 || slot >= c.n_slots || c.lens[slot] != 0))
+    record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
   const int32_t* pages = c.table + (long long)slot * c.width;
   if (a.shared > 0 && blockIdx.y == 0 && blockIdx.z == 0 && row0 == 0)
     check_shared(a, seq, tid, 32 * kRowWarps);

@@ -504,8 +504,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const int tok = valid ? R / G : 0, h = it->hk * G + (valid ? R % G : 0);
       int lim = 0;
       if (valid && SHARED) {  // a slot shorter than the shared keys sees its own length of them
-        const int slot = sa.d.slots[tok];
-        lim = slot < 0 || slot >= sa.d.c.n_slots ? 0 : max(0, min(it->n_keys, sa.d.c.lens[slot] - it->key0));
+        lim = max(0, min(it->n_keys, slot_len(sa.d.c, sa.d.slots[tok]) - it->key0));
       } else if (valid) {
         lim = visible_keys(tok, it->nq, it->nk, pa.causal);
         if (SPLIT) lim = max(0, min(lim - it->key0, it->n_keys));

@@ -122,6 +122,23 @@ def test_decode_shared_pages_out_of_range_are_recorded(n, dtype, D, value):
     assert st == BAD and 0 <= row < n
 
 
+# ---------------------------------------------------------------------------------------------- lengths out of range
+
+@pytest.mark.parametrize("length", [-5, 1 << 30, None])
+@pytest.mark.parametrize("shared", [0, 32])
+@pytest.mark.parametrize("n,dtype,D", [(7, BF16, 64), (2, BF16, 128), (7, F32, 64), (2, F32, 64), (3, F32, 256), (7, BF16, 256),
+                                       (2, BF16, 256)])
+def test_decode_bad_lengths_are_recorded(n, dtype, D, shared, length):
+    """On every path a length outside [0, width * page size] is an error, and its row one that sees nothing."""
+    lens = [60] * n
+    c, rows = make_cache(lens, 32, 16, 2, D, dtype)
+    c.lens[1] = c.width * 16 + 1 if length is None else length
+    out, lse, q, st = decode(c, 4, D, dtype, range(n), shared)
+    assert st == (BAD, 1)
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+    right(out, lse, q, c, rows, lens, [i for i in range(n) if i != 1], D, dtype)
+
+
 # ------------------------------------------------------------------------------------------------- non-finite values
 
 @pytest.mark.parametrize("value", [float("inf"), float("-inf")])
