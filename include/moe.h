@@ -393,7 +393,8 @@ moe_status moe_graph_destroy(moe_graph graph);
  *   csdn/6a462027 §4.3 (a block is attention, then the MoE FFN); csdn/6a919c0d §3.3 (a paged cache).
  * H query heads share H_kv key/value heads (H % H_kv == 0): query head h reads key/value head
  *   h / (H / H_kv). Heads of D elements, D % 8 == 0, 8 <= D <= 256; q, k, v and out are `dt` (bf16 or
- *   fp32); scores, softmax statistics and sums are fp32. `scale` (> 0, finite) multiplies the scores.
+ *   fp32); scores, softmax statistics and sums are fp32. `scale` (> 0, finite also times log2 e) multiplies
+ *   the scores.
  * Token strides are in elements: token t of q is at q + t * q_stride, its heads [H][D] dense, so q, k
  *   and v may be slices of one fused projection. Every pointer and every token stride in bytes is a
  *   multiple of 16; anything else is MOE_ERR_INVALID_ARG.

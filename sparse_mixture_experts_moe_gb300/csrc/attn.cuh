@@ -268,6 +268,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     }
   }
 }
+// A running reference rises with a score that is this much above it: 8 in log2 units (weights then stay below 2^8). Finite,
+// as -inf plus it is to be -inf (c2, the scale times log2 e, may be next to 0).
+__device__ __forceinline__ float rescale_above(float c2) { return fminf(8.0f / c2, 3.0e38f); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // the hardware 2^x, ~2 ulp; 2^-inf = 0

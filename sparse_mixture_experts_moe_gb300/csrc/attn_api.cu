@@ -18,7 +18,7 @@ bool dtype_ok(int dt) { return dt == MOE_DTYPE_F32 || dt == MOE_DTYPE_BF16; }
 bool heads_ok(int H, int Hkv, int D) {
   return H >= 1 && Hkv >= 1 && H <= 65535 && H % Hkv == 0 && D >= 8 && D <= 256 && D % 8 == 0;
 }
-bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }
+bool scale_ok(float s) { return s > 0.f && std::isfinite(s * 1.4426950408889634f); }  // (as the kernels take it)
 // Rows of `inner` dense elements every `stride` elements, each row 16-byte aligned; strides below 2^40.
 bool stride_ok(int64_t stride, long long inner, int dt) {
   return stride >= inner && stride < (1ll << 40) && stride * elem_bytes(dt) % 16 == 0;

@@ -307,7 +307,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     // lane that loads.
     __syncwarp();
   } else {
-    const float c2 = a.d.scale * 1.4426950408889634f, thr = 8.0f / c2;
+    const float c2 = a.d.scale * 1.4426950408889634f, thr = rescale_above(c2);
     const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, group = warp >> 2;
     const int mi = lane >> 3, l8 = lane & 7;
     uint32_t q[KS][NT][2], qn[KS][NT][2];

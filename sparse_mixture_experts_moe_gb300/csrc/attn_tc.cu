@@ -49,7 +49,6 @@ constexpr int TM = 128;       // rows per tile
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr int kMaxSmem = 232448;
-constexpr float kRescale = 8.0f;  // log2 units
 
 struct __align__(16) Item {
   int hk, row0, nrows;      // key/value head; packed rows row0 .. of the sequence (or batch)
@@ -489,7 +488,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const int t = warp >> 2, r = tid & 127;  // tile, row of it
     const int q4 = warp & 3;                 // TMEM lanes 32 q4 ..
     const float c2 = (SHARED ? sa.d.scale : pa.scale) * 1.4426950408889634f;
-    const float thr = kRescale / c2;
+    const float thr = rescale_above(c2);
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const uint32_t tS = tmem + lanes + t * BK, tO = tmem + lanes + 256 + t * DP;
     uint32_t done = 0;  // blocks of all items so far: their barriers' phases

@@ -208,3 +208,26 @@ def test_prompt_with_non_finite_values_takes_no_waits_to_their_limit(where, D, m
     if where != "all":
         out[:, 4:, 5] = 0
         assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------------------------------------------------------- scales
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-38, 3e-39, 1e-44])
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 200), (F32, 64)])
+def test_scales_near_zero(scale, dtype, D):
+    """All weights are the same: a mean, and the logarithm of the number of keys."""
+    scale = float(np.float32(scale))
+    lens = [200, 70, 65, 64, 300, 64, 128]
+    c, rows = make_cache(lens, 64, 16, 2, D, dtype)
+    q = tensor((7, 4, D), 3, dtype, DEV)
+    a = moe.Attention(4, 2, D, dtype, scale=scale)
+    for shared in (0, 64):
+        lse = torch.empty((7, 4), device=DEV)
+        out = a.decode(q, c, i32(range(7), DEV), shared_len=shared, lse=lse)
+        check(out, lse, decode_reference(q, c, rows, lens, 0, scale), 300, D, dtype)
+    for nq, nk in (([150, 3], [150, 3]), ([7], [2500])):
+        q, k, v = (tensor((sum(x), h, D), s, dtype, DEV) for x, h, s in ((nq, 4, 1), (nk, 2, 2), (nk, 2, 3)))
+        lse = torch.empty((sum(nq), 4), device=DEV)
+        out = a.prompt(q, k, v, i32(offsets(nq), DEV), i32(offsets(nk), DEV), lse=lse)
+        check(out, lse, prompt_reference(q, k, v, offsets(nq), offsets(nk), True, scale), max(nk), D, dtype)
+    assert a.device_status() == (moe.MOE_OK, 0)
