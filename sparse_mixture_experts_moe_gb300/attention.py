@@ -103,7 +103,7 @@ class _Workspaces:
         self._of = {}        # stream -> (tensor, bytes, address); (stream, device) on others than the first device,
                              # as the default stream has one handle for all of them
         self._recorded = {}  # (stream, recording, device) -> the same
-        self._old = []
+        self._old = []       # (key, the same): replaced by larger ones; calls in flight and graphs may use them
 
     def get(self, stream, nbytes, dev):
         ws = self._of.get(stream if dev == 0 else (stream, dev))
@@ -118,7 +118,7 @@ class _Workspaces:
         if ws is not None:
             if ws[1] >= nbytes:
                 return ws
-            self._old.append(ws)
+            self._old.append((key, ws))
         t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
         current = torch.cuda.current_stream(dev)
         if current.cuda_stream != (stream or 0):
@@ -131,14 +131,18 @@ class _Workspaces:
     def status(self):
         """(status, detail) of the first device-side error of any of them; clears it."""
         import torch
-        for key, ws in self._of.items():
+        recorded = []
+        for key, ws in [*self._old, *self._of.items(), *self._recorded.items()]:
+            if type(key) is tuple and len(key) == 3:
+                recorded.append(ws)
+                continue
             with torch.cuda.device(ws[0].device):
                 st, detail = _lib.get_device_status(ws[0], key[0] if type(key) is tuple else key)
             if st != MOE_OK:
                 return st, detail
-        for dev in {ws[0].device for ws in self._recorded.values()}:
+        for dev in {ws[0].device for ws in recorded}:
             torch.cuda.synchronize(dev)
-        for ws in self._recorded.values():
+        for ws in recorded:
             # a graph that has not run yet has not prepared its workspace: the header's unused words tell
             with torch.cuda.device(ws[0].device):
                 if not ws[0][_HEADER_USED:_HEADER].any():

@@ -26,6 +26,20 @@ class Memory:
     def data_ptr(self):
         return self.address
 
+    def __getitem__(self, part):
+        return Part(self, part)
+
+
+class Part:
+    def __init__(self, memory, part):
+        self.memory, self.part = memory, part
+
+    def any(self):
+        return any(self.memory.header[self.part])
+
+    def copy_(self, other):
+        self.memory.header[self.part] = other.memory.header[other.part]
+
 
 class Stream:
     def __init__(self, handle):
@@ -53,6 +67,13 @@ class Lib:
         return moe.MOE_OK
 
 
+def read_status(ws, stream=None):
+    """moe_get_device_status on a stand-in: the header's first two places, cleared."""
+    got = tuple(ws.header[:2])
+    ws.header[:2] = [0, 0]
+    return got
+
+
 @pytest.fixture
 def world(monkeypatch):
     """A workspace pool on stand-ins, with the library and the devices that were selected."""
@@ -68,6 +89,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream(0))
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    monkeypatch.setattr(_lib, "get_device_status", read_status)
     pool = _Workspaces(lib, lib.init)
     return pool, lib, selected
 
@@ -101,3 +123,30 @@ def test_workspaces_are_prepared_and_read_on_their_device(world, monkeypatch):
         pool.get(0, 1000, dev)
     assert pool.status() == (moe.MOE_OK, 0)
     assert where == [("init", 0), ("init", 1), ("init", 3), (0, 0), (1, 1), (3, 3)]
+
+
+BAD = moe.MOE_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("stream", [0, 7])
+def test_an_error_is_not_lost_when_a_workspace_grows(world, stream):
+    pool, lib, _ = world
+    pool.get(stream, 1000, 0)[0].header[:2] = [BAD, 5]
+    pool.get(stream, 2000, 0)
+    pool.get(stream, 9000, 0)
+    assert pool.status() == (BAD, 5)
+    assert pool.status() == (moe.MOE_OK, 0)
+
+
+def test_errors_of_all_workspaces_of_a_recording_are_read(world):
+    """A graph goes on using the smaller workspace that its first calls recorded."""
+    pool, lib, _ = world
+    lib.recording[3] = 11
+    small = pool.get(3, 1000, 0)
+    large = pool.get(3, 5000, 0)
+    assert small[2] != large[2]
+    lib.recording.clear()
+    for ws, row in ((small, 4), (large, 6), (small, 8)):
+        ws[0].header[:2] = [BAD, row]
+        assert pool.status() == (BAD, row)
+        assert pool.status() == (moe.MOE_OK, 0)
