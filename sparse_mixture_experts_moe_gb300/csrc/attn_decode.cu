@@ -331,6 +331,10 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             qn[k][t][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
           }
     };
+    // A run's first unit goes to the group whose turn it is, which depends on the runs that the CTA had before: `flip` says
+    // whether that is the second one. Parts are added up with the first unit's group first, so that the sums do not depend
+    // on which CTA takes a run.
+    int flip = 0;
     int rq = 0, run = 0, run_no = 0;
     uint32_t rphase = 0;
     // the next run with anything in it, at cu; false after the last
@@ -453,11 +457,15 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
       const Cursor was = cu;
       const int was_run = run_no;
+      const int part = quarter + 4 * (group ^ flip);  // this warp's place among the eight parts
       run -= advance(cu, P, n, HR);
       if (run > 0 && cu.i == was.i && cu.hr == was.hr) continue;
       // ---- the segment (or the run) ends: the eight warps' parts become one piece, while the next rows are on their way
       fresh = true;
-      if (run <= 0) more = next_run();
+      if (run <= 0) {
+        more = next_run();
+        flip = (x + 1) & 1;
+      }
       if (more) fetch(cu);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -466,8 +474,8 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], w);
           if (g == 0) {
-            sm_m[warp * C::kRows + 8 * t + 2 * t4 + r] = m[t][r];
-            sm_l[warp * C::kRows + 8 * t + 2 * t4 + r] = l[t][r];
+            sm_m[part * C::kRows + 8 * t + 2 * t4 + r] = m[t][r];
+            sm_l[part * C::kRows + 8 * t + 2 * t4 + r] = l[t][r];
           }
         }
       consumers_sync();
@@ -480,7 +488,7 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
           for (int y = 0; y < kWarps; ++y) M = fmaxf(M, sm_m[y * C::kRows + row]);
           const float w = M == -INFINITY ? 0.f : ex2((m[t][r] - M) * c2);
-          float* d = buf + (warp * C::kRows + row) * C::kLd + g;
+          float* d = buf + (part * C::kRows + row) * C::kLd + g;
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             d[16 * k] = o[k][t][r] * w;

@@ -231,3 +231,26 @@ def test_scales_near_zero(scale, dtype, D):
         out = a.prompt(q, k, v, i32(offsets(nq), DEV), i32(offsets(nk), DEV), lse=lse)
         check(out, lse, prompt_reference(q, k, v, offsets(nq), offsets(nk), True, scale), max(nk), D, dtype)
     assert a.device_status() == (moe.MOE_OK, 0)
+
+
+# --------------------------------------------------------------------------------------------- the same, every time
+
+@pytest.mark.parametrize("H,Hk,D", [(8, 2, 64), (16, 2, 128)])
+def test_decode_repeats_itself_beside_other_work(H, Hk, D):
+    """Bit for bit, whichever CTAs find an SM first: sums do not depend on who takes what."""
+    lens = [32 + 5 + 23 * i for i in range(64)]
+    c, _ = make_cache(lens, 32, 16, Hk, D, BF16)
+    q, slots = tensor((64, H, D), 1, BF16, DEV), i32(range(64), DEV)
+    a, b = moe.Attention(H, Hk, D, BF16), moe.Attention(8, 8, 64, BF16)
+    want = a.decode(q, c, slots, shared_len=32)
+    x = [tensor((t, 24, 64), 2, BF16, DEV) for t in (130, 700, 1500, 2900)]
+    o = [i32([0, t], DEV) for t in (130, 700, 1500, 2900)]
+    outs = [torch.empty_like(want) for _ in range(400)]
+    other, y = torch.cuda.Stream(), [torch.empty((len(z), 8, 64), dtype=BF16, device=DEV) for z in x]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        j = i % 4
+        b.prompt(x[j][:, :8], x[j][:, 8:16], x[j][:, 16:], o[j], out=y[j], stream=other)
+        a.decode(q, c, slots, shared_len=32, out=out)
+    torch.cuda.synchronize()
+    assert sum(not torch.equal(out, want) for out in outs) == 0
