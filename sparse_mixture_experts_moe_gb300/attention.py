@@ -10,13 +10,13 @@
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
 The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
-synchronises, except that the first call on a `stream` other than the current one (and one that needs a larger
-workspace) waits for the current one. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture). Index
-tensors (offsets, slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the
-work is done by the library's kernels.
+synchronises (a recording's first call on a stream other than the current one waits for the current one). Calls can be
+recorded into a graph (torch.cuda.graph, GraphCapture). Index tensors (offsets, slots, lengths, positions) are int32 CUDA
+tensors. Arguments are marshalled and checked here; the work is done by the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import _lib
@@ -95,15 +95,15 @@ class _Workspaces:
     """Prepared workspaces, one for each stream (of each device) that calls arrive on, so that calls on different streams
     never share scratch memory, and one for each graph recording (and stream of it): the graph prepares it at its
     first use, and nothing else uses it, however late and on whatever stream the graph runs. (A recording on a stream that
-    calls have used before takes that stream's: its replays are to be ordered with further calls there.) Each is
-    kept for good: work in flight may use one that a larger one replaced."""
+    calls have used before takes that stream's: its replays are to be ordered with further calls there.) A
+    recording's are kept for good; a stream's is given back when a larger one replaces it."""
 
     def __init__(self, lib, init):
         self._lib, self._init = lib, init
         self._of = {}        # stream -> (tensor, bytes, address); (stream, device) on others than the first device,
                              # as the default stream has one handle for all of them
         self._recorded = {}  # (stream, recording, device) -> the same
-        self._old = []       # (key, the same): replaced by larger ones; calls in flight and graphs may use them
+        self._old = []       # (key, the same): of recordings, replaced by larger ones; their graphs use both
 
     def get(self, stream, nbytes, dev):
         ws = self._of.get(stream if dev == 0 else (stream, dev))
@@ -112,9 +112,31 @@ class _Workspaces:
     def _make(self, stream, nbytes, dev):
         import torch
         recording = self._lib.moe_stream_capture_id(stream)
-        of, key = ((self._recorded, (stream, recording, dev)) if recording
-                   else (self._of, stream if dev == 0 else (stream, dev)))
-        ws = of.get(key)
+        if recording:
+            return self._make_recorded(stream, recording, nbytes, dev)
+        key = stream if dev == 0 else (stream, dev)
+        old = self._of.get(key)
+        if old is not None:
+            if old[1] >= nbytes:
+                return old
+            nbytes = max(nbytes, old[1] * 3 // 2)  # a batch that grows one by one
+        current = torch.cuda.current_stream(dev).cuda_stream == (stream or 0)
+        # Memory of the stream's own: what was enqueued there is done with it before the next call that gets it runs, so the
+        # workspace that this one replaces can be given back at once.
+        with contextlib.nullcontext() if current else torch.cuda.stream(torch.cuda.ExternalStream(stream or 0, device=dev)):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+            ws = (t, nbytes, t.data_ptr())
+            with torch.cuda.device(dev):
+                _check(self._init(ws[2], nbytes, stream), "workspace_init")
+            if old is not None:  # an error that nobody has read yet
+                t[:_HEADER].copy_(old[0][:_HEADER])
+        self._of[key] = ws
+        return ws
+
+    def _make_recorded(self, stream, recording, nbytes, dev):
+        import torch
+        key = (stream, recording, dev)
+        ws = self._recorded.get(key)
         if ws is not None:
             if ws[1] >= nbytes:
                 return ws
@@ -123,7 +145,7 @@ class _Workspaces:
         current = torch.cuda.current_stream(dev)
         if current.cuda_stream != (stream or 0):
             current.synchronize()  # what used this memory before, on the stream that it was allocated for
-        ws = of[key] = (t, nbytes, t.data_ptr())
+        ws = self._recorded[key] = (t, nbytes, t.data_ptr())
         with torch.cuda.device(dev):
             _check(self._init(ws[2], nbytes, stream), "workspace_init")
         return ws
@@ -131,15 +153,12 @@ class _Workspaces:
     def status(self):
         """(status, detail) of the first device-side error of any of them; clears it."""
         import torch
-        recorded = []
-        for key, ws in [*self._old, *self._of.items(), *self._recorded.items()]:
-            if type(key) is tuple and len(key) == 3:
-                recorded.append(ws)
-                continue
+        for key, ws in self._of.items():
             with torch.cuda.device(ws[0].device):
                 st, detail = _lib.get_device_status(ws[0], key[0] if type(key) is tuple else key)
             if st != MOE_OK:
                 return st, detail
+        recorded = [ws for _, ws in self._old] + list(self._recorded.values())
         for dev in {ws[0].device for ws in recorded}:
             torch.cuda.synchronize(dev)
         for ws in recorded:

@@ -89,6 +89,8 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream(0))
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(_lib, "get_device_status", read_status)
     pool = _Workspaces(lib, lib.init)
     return pool, lib, selected
@@ -150,3 +152,14 @@ def test_errors_of_all_workspaces_of_a_recording_are_read(world):
         ws[0].header[:2] = [BAD, row]
         assert pool.status() == (BAD, row)
         assert pool.status() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("stream", [0, 7])
+def test_replaced_workspaces_are_given_back(world, stream):
+    """A batch that grows by one sequence at a time keeps one workspace, and seldom makes a new one."""
+    pool, lib, _ = world
+    live, made = Memory.live, Memory.made
+    for n in range(1, 257):
+        assert pool.get(stream, 1000 + 100 * n, 0)[1] >= 1000 + 100 * n
+    assert Memory.live - live == 1
+    assert Memory.made - made <= 10

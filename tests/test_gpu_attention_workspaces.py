@@ -30,3 +30,22 @@ def test_an_error_is_not_lost_when_the_workspace_grows(own_stream):
         call(list(range(n)))
     assert a.device_status() == (BAD, 1)
     assert a.device_status() == (OK, 0)
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_a_growing_batch_keeps_one_workspace(own_stream):
+    a, c, q = setup(n=64, shared=32)
+    s = torch.cuda.Stream() if own_stream else None
+    want = a.decode(q, c, i32(range(64), DEV), shared_len=32)
+    a = moe.Attention(8, 2, 64, BF16)
+    out = torch.empty_like(q)
+    slots = [i32(range(n), DEV) for n in range(65)]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for n in range(1, 65):
+        a.decode(q[:n], c, slots[n], shared_len=32, out=out[:n], stream=s)
+    torch.cuda.synchronize()
+    need = a._lib.moe_attention_workspace_bytes(64, 8, 64)
+    assert torch.cuda.memory_allocated() - before <= 1.5 * need + 512
+    assert torch.equal(out, want)
+    assert a.device_status() == (OK, 0)
