@@ -375,7 +375,12 @@ moe_status moe_forward_q(const void* x, const void* w_r, const float* b_r, const
  *      capture, instantiates what was recorded into *graph and destroys the stream (always, also
  *      on error). Use it for moe_forward_q or for a sequence of the separate entry points.
  * moe_stream_capture_id: a number for the recording that `stream` is part of (this library's or any other
- *      of the process), 0 outside one. Calls recorded into one graph can share a workspace of that graph's own. */
+ *      of the process), 0 outside one. Calls recorded into one graph can share a workspace of that graph's own.
+ * moe_capture_watch: how long such a workspace is needed. *ended (host memory, 0) becomes 1 once the graph that is being
+ *      recorded on `stream`, every executable graph made of it and their launches are gone. moe_capture_watch_free
+ *      gives it back, at any time.
+ * moe_private_stream / moe_thread_capture_mode: a stream on which a workspace can be prepared while another records, and
+ *      the calling thread's cudaStreamCaptureMode (returns the one before), with which it may allocate there meanwhile. */
 typedef struct moe_graph_s* moe_graph;
 moe_status moe_graph_capture_begin(void** capture_stream);
 moe_status moe_forward_graph_create(const void* x, const void* w_r, const float* b_r, const void* w1,
@@ -385,6 +390,10 @@ moe_status moe_forward_graph_create(const void* x, const void* w_r, const float*
                                     void* workspace, size_t ws_bytes, moe_graph* graph);
 moe_status moe_graph_capture_end(void* capture_stream, moe_graph* graph);
 unsigned long long moe_stream_capture_id(void* stream);
+moe_status moe_capture_watch(void* stream, int** ended);
+moe_status moe_capture_watch_free(int* ended);
+moe_status moe_private_stream(void** stream);
+int moe_thread_capture_mode(int mode);
 moe_status moe_graph_launch(moe_graph graph, void* stream);
 moe_status moe_graph_destroy(moe_graph graph);
 

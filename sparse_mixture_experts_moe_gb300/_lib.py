@@ -60,6 +60,10 @@ SIGNATURES = {
     "moe_graph_capture_begin": [_p],
     "moe_graph_capture_end": [_p, _p],
     "moe_stream_capture_id": [_p],
+    "moe_capture_watch": [_p, _p],
+    "moe_capture_watch_free": [_p],
+    "moe_private_stream": [_p],
+    "moe_thread_capture_mode": [_i],
     "moe_qweight_bytes": [_i, _i, _i, _i],
     "moe_qscale_bytes": [_i, _i, _i],
     "moe_quantize_weights": [_p, _i, _i, _i, _i, _i, _p, _p, _p],

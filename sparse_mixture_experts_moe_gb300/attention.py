@@ -10,9 +10,9 @@
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
 The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
-synchronises (a recording's first call on a stream other than the current one waits for the current one). Calls can be
-recorded into a graph (torch.cuda.graph, GraphCapture). Index tensors (offsets, slots, lengths, positions) are int32 CUDA
-tensors. Arguments are marshalled and checked here; the work is done by the library's kernels.
+synchronises. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture), which keeps the workspace that they use;
+an error that a replay records stays until device_status() reads it. Index tensors (offsets, slots, lengths, positions)
+are int32 CUDA tensors. Arguments are marshalled and checked here; the work is done by the library's kernels.
 """
 from __future__ import annotations
 
@@ -24,7 +24,7 @@ from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
 
 
 _HEADER = 256           # bytes of a workspace's header
-_HEADER_USED = 64       # of these: status and counters, the rest stays zero
+_RELAXED = 2            # cudaStreamCaptureModeRelaxed
 _SPLIT_KEYS = 1024      # moe_attention_prompt uses no more than the header below this many keys
 
 
@@ -91,19 +91,56 @@ class _Bound:
         return self._ws.status()
 
 
+class _Recorded:
+    """A workspace that recorded calls use, and whether their graph is gone."""
+
+    def __init__(self, lib, stream, key, ws):
+        self._lib, self.key, self.ws = lib, key, ws
+        self._ended = ctypes.POINTER(ctypes.c_int)()
+        lib.moe_capture_watch(stream, ctypes.byref(self._ended))  # (without a watch: kept for good)
+
+    def gone(self):
+        return bool(self._ended) and self._ended[0] != 0
+
+    def __del__(self):
+        if self._ended:
+            self._lib.moe_capture_watch_free(self._ended)
+
+
+_in_graphs = set()     # _Recorded of all objects: a graph may outlive the Attention or KVCache whose calls it recorded
+_private_streams = {}  # device -> a stream on which recordings' workspaces are allocated and prepared
+
+
+def _private_stream(lib, dev):
+    s = _private_streams.get(dev)
+    if s is None:
+        p = ctypes.c_void_p()
+        _check(lib.moe_private_stream(ctypes.byref(p)), "moe_private_stream")
+        s = _private_streams[dev] = p.value
+    return s
+
+
+def _size_class(n):
+    """The next power of two, or three quarters of one: few sizes, so that a workspace that a graph leaves fits another."""
+    p = 1 << max(n - 1, 1).bit_length()
+    return p * 3 // 4 if n <= p * 3 // 4 else p
+
+
 class _Workspaces:
     """Prepared workspaces, one for each stream (of each device) that calls arrive on, so that calls on different streams
-    never share scratch memory, and one for each graph recording (and stream of it): the graph prepares it at its
-    first use, and nothing else uses it, however late and on whatever stream the graph runs. (A recording on a stream that
-    calls have used before takes that stream's: its replays are to be ordered with further calls there.) A
-    recording's are kept for good; a stream's is given back when a larger one replaces it."""
+    never share scratch memory, and one for each graph recording (and stream of it), which nothing else uses while the
+    graph lives, however late and on whatever stream it runs. It is prepared beside the recording, once, so an error that a
+    replay records stays until it is read; when the graph is gone another recording gets it. (A recording on a stream that
+    calls have used before takes that stream's: its replays are to be ordered with further calls there.) A stream's is
+    given back when a larger one replaces it."""
 
     def __init__(self, lib, init):
         self._lib, self._init = lib, init
         self._of = {}        # stream -> (tensor, bytes, address); (stream, device) on others than the first device,
                              # as the default stream has one handle for all of them
         self._recorded = {}  # (stream, recording, device) -> the same
-        self._old = []       # (key, the same): of recordings, replaced by larger ones; their graphs use both
+        self._graphs = []    # _Recorded: of these, and those that larger ones replaced, which their graph uses too
+        self._idle = []      # (device, the same): their graph is gone
 
     def get(self, stream, nbytes, dev):
         ws = self._of.get(stream if dev == 0 else (stream, dev))
@@ -137,18 +174,40 @@ class _Workspaces:
         import torch
         key = (stream, recording, dev)
         ws = self._recorded.get(key)
-        if ws is not None:
-            if ws[1] >= nbytes:
-                return ws
-            self._old.append((key, ws))
-        t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-        current = torch.cuda.current_stream(dev)
-        if current.cuda_stream != (stream or 0):
-            current.synchronize()  # what used this memory before, on the stream that it was allocated for
-        ws = self._recorded[key] = (t, nbytes, t.data_ptr())
-        with torch.cuda.device(dev):
-            _check(self._init(ws[2], nbytes, stream), "workspace_init")
+        if ws is not None and ws[1] >= nbytes:
+            return ws
+        self._sweep()
+        fit = min((w for w in self._idle if w[0] == dev and w[1][1] >= nbytes), key=lambda w: w[1][1], default=None)
+        if fit is not None:
+            self._idle.remove(fit)
+            ws = fit[1]
+        else:
+            # not the recording's memory, which its graph may use for other things before and after these calls
+            nbytes, private = _size_class(nbytes), _private_stream(self._lib, dev)
+            beside = torch.cuda.ExternalStream(private, device=dev)
+            mode = self._lib.moe_thread_capture_mode(_RELAXED)  # this thread's other calls are to allocate and wait
+            try:
+                with torch.cuda.device(dev), torch.cuda.stream(beside):
+                    t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+                    ws = (t, nbytes, t.data_ptr())
+                    _check(self._init(ws[2], nbytes, private), "workspace_init")
+                    beside.synchronize()
+            finally:
+                self._lib.moe_thread_capture_mode(mode)
+        held = _Recorded(self._lib, stream, key, ws)
+        self._graphs.append(held)
+        _in_graphs.add(held)
+        self._recorded[key] = ws
         return ws
+
+    def _sweep(self):
+        """Takes back what graphs that are gone have used."""
+        _in_graphs.difference_update([r for r in _in_graphs if r.gone()])
+        for r in [r for r in self._graphs if r.gone()]:
+            self._graphs.remove(r)
+            if self._recorded.get(r.key) is r.ws:
+                del self._recorded[r.key]
+            self._idle.append((r.key[2], r.ws))
 
     def status(self):
         """(status, detail) of the first device-side error of any of them; clears it."""
@@ -158,16 +217,14 @@ class _Workspaces:
                 st, detail = _lib.get_device_status(ws[0], key[0] if type(key) is tuple else key)
             if st != MOE_OK:
                 return st, detail
-        recorded = [ws for _, ws in self._old] + list(self._recorded.values())
+        recorded = [r.ws for r in self._graphs] + [w[1] for w in self._idle]
         for dev in {ws[0].device for ws in recorded}:
             torch.cuda.synchronize(dev)
         for ws in recorded:
-            # a graph that has not run yet has not prepared its workspace: the header's unused words tell
             with torch.cuda.device(ws[0].device):
-                if not ws[0][_HEADER_USED:_HEADER].any():
-                    st, detail = _lib.get_device_status(ws[0])
-                    if st != MOE_OK:
-                        return st, detail
+                st, detail = _lib.get_device_status(ws[0])
+            if st != MOE_OK:
+                return st, detail
         return MOE_OK, 0
 
 

@@ -1,11 +1,13 @@
 """Which workspace a call of Attention or KVCache gets. Needs no GPU: memory, streams and the library are stand-ins."""
 import contextlib
+import ctypes
+import gc
 
 import pytest
 import torch
 
 import sparse_mixture_experts_moe_gb300 as moe
-from sparse_mixture_experts_moe_gb300 import _lib
+from sparse_mixture_experts_moe_gb300 import _lib, attention
 from sparse_mixture_experts_moe_gb300.attention import _Workspaces
 
 
@@ -58,11 +60,36 @@ class Lib:
     def __init__(self):
         self.recording = {}  # stream -> number of the recording
         self.prepared = []
+        self.watches, self.freed, self.mode = {}, 0, 0
 
     def moe_stream_capture_id(self, stream):
         return self.recording.get(stream, 0)
 
+    def moe_capture_watch(self, stream, ended):
+        flag = ctypes.c_int(0)
+        self.watches.setdefault(self.recording[stream], []).append(flag)
+        ended._obj.contents = flag
+        return moe.MOE_OK
+
+    def moe_capture_watch_free(self, ended):
+        self.freed += 1
+        return moe.MOE_OK
+
+    def moe_private_stream(self, stream):
+        stream._obj.value = 0xABC0
+        return moe.MOE_OK
+
+    def moe_thread_capture_mode(self, mode):
+        self.mode, was = mode, self.mode
+        return was
+
+    def gone(self, recording):
+        """The recording's graph is destroyed."""
+        for flag in self.watches.pop(recording):
+            flag.value = 1
+
     def init(self, ptr, nbytes, stream):
+        assert self.mode == (2 if stream == 0xABC0 else 0)
         self.prepared.append((ptr, nbytes, stream))
         return moe.MOE_OK
 
@@ -92,6 +119,8 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(_lib, "get_device_status", read_status)
+    monkeypatch.setattr(attention, "_private_streams", {})
+    monkeypatch.setattr(attention, "_in_graphs", set())
     pool = _Workspaces(lib, lib.init)
     return pool, lib, selected
 
@@ -163,3 +192,62 @@ def test_replaced_workspaces_are_given_back(world, stream):
         assert pool.get(stream, 1000 + 100 * n, 0)[1] >= 1000 + 100 * n
     assert Memory.live - live == 1
     assert Memory.made - made <= 10
+
+
+def test_recordings_whose_graph_is_gone_leave_their_workspace_to_the_next(world):
+    pool, lib, _ = world
+    live = Memory.live
+    for n in range(1, 200):
+        lib.recording[3] = n
+        assert pool.get(3, 1000 + n, 0)[1] >= 1000 + n
+        lib.recording.clear()
+        lib.gone(n)
+    assert Memory.live - live <= 2 and len(pool._recorded) <= 1
+    assert lib.freed >= 190
+
+
+def test_living_graphs_share_no_workspace(world):
+    pool, lib, _ = world
+    seen = set()
+    for n in range(1, 9):
+        lib.recording[3] = n
+        a, b = pool.get(3, 1000, 0), pool.get(3, 1000, 0)
+        assert a is b
+        lib.recording[4] = n  # another stream of the same recording
+        seen |= {a[2], pool.get(4, 1000, 0)[2]}
+        lib.recording.clear()
+    assert len(seen) == 16
+    lib.gone(5)
+    lib.recording[3] = 20
+    assert pool.get(3, 1000, 0)[2] in seen
+    lib.recording.clear()
+    assert len({w[2] for w in pool._recorded.values()}) == len(pool._recorded) == 15
+
+
+def test_an_error_of_a_graph_that_is_gone_is_read(world):
+    pool, lib, _ = world
+    lib.recording[3] = 1
+    pool.get(3, 1000, 0)[0].header[:2] = [BAD, 9]
+    lib.recording.clear()
+    lib.gone(1)
+    lib.recording[3] = 2
+    pool.get(3, 1000, 0)
+    lib.recording.clear()
+    assert pool.status() == (BAD, 9) and pool.status() == (moe.MOE_OK, 0)
+
+
+def test_a_graph_keeps_its_workspace_when_the_object_is_gone(world):
+    pool, lib, _ = world
+    live = Memory.live
+    other = _Workspaces(lib, lib.init)
+    lib.recording[3] = 1
+    other.get(3, 1000, 0)
+    lib.recording.clear()
+    del other
+    gc.collect()
+    assert Memory.live - live == 1
+    lib.gone(1)
+    lib.recording[3] = 2
+    pool.get(3, 1000, 0)  # any other recording finds that it is over
+    gc.collect()
+    assert Memory.live - live == 1
