@@ -60,8 +60,6 @@ SIGNATURES = {
     "moe_graph_capture_begin": [_p],
     "moe_graph_capture_end": [_p, _p],
     "moe_stream_capture_id": [_p],
-    "moe_capture_watch": [_p, _p],
-    "moe_capture_watch_free": [_p],
     "moe_private_stream": [_p],
     "moe_thread_capture_mode": [_i],
     "moe_qweight_bytes": [_i, _i, _i, _i],
@@ -81,8 +79,11 @@ SIGNATURES = {
     "moe_attention_prompt_workspace_bytes": [_i, _i, _i, _i, _i, _i, _i],
     "moe_attention_prompt": [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i64, _i64, _i64, _f, _i, _i, _p, _p, _p,
                              _sz, _p],
+    "moe_attention_prompt_ex": [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i64, _i64, _i64, _f, _i, _i, _p, _p, _p,
+                                _sz, _p, _sz, _p],
     "moe_attention_workspace_bytes": [_i, _i, _i],
     "moe_attention_decode": [_p, _i, _p, _p, _i, _i, _i64, _i64, _i, _f, _p, _p, _p, _sz, _p],
+    "moe_attention_decode_ex": [_p, _i, _p, _p, _i, _i, _i64, _i64, _i, _f, _p, _p, _p, _sz, _p, _sz, _p],
     "moe_cache_plan_bytes": [],
     "moe_cache_plan": [_p, _p, _sz],
     "moe_cache_workspace_bytes": [_p],
@@ -412,18 +413,33 @@ class GraphCapture:
     (moe_graph_capture_begin / _end); `cap.graph` then replays them with launch(). Keep the
     tensors those calls used alive while the graph is in use (pass them as keep=...)."""
 
+    _now = {}  # recording -> the capture
+
     def __init__(self, keep=()):
-        self._keep = tuple(keep)
+        self._keep = list(keep)
         self.stream = None
         self.graph = None
+        self.scratch = {}  # stream -> memory that recorded calls use one after the other
 
     def __enter__(self):
         cs = ctypes.c_void_p()
         _check(lib().moe_graph_capture_begin(ctypes.byref(cs)), "moe_graph_capture_begin")
         self.stream = cs.value
+        self._recording = lib().moe_stream_capture_id(cs)
+        GraphCapture._now[self._recording] = self
         return self
 
+    @classmethod
+    def of(cls, recording):
+        """The capture that makes a recording, if one of these does."""
+        return cls._now.get(recording)
+
+    def hold(self, t):
+        """Keeps a tensor alive as long as the graph."""
+        self._keep.append(t)
+
     def __exit__(self, exc_type, exc, tb):
+        GraphCapture._now.pop(self._recording, None)
         h = ctypes.c_void_p()
         rc = lib().moe_graph_capture_end(self.stream, ctypes.byref(h))
         if exc_type is None:

@@ -10,9 +10,10 @@
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
 The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
-synchronises. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture), which keeps the workspace that they use;
-an error that a replay records stays until device_status() reads it. Index tensors (offsets, slots, lengths, positions)
-are int32 CUDA tensors. Arguments are marshalled and checked here; the work is done by the library's kernels.
+synchronises. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture); an error that a replay records stays
+until device_status() reads it. Calls on one KVCache must not overlap in time, on whatever streams they are. Index tensors
+(offsets, slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the work is done
+by the library's kernels.
 """
 from __future__ import annotations
 
@@ -75,72 +76,118 @@ class _Bound:
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._current_device = torch._C._cuda_getDevice
-        self._ws = _Workspaces(self._lib, self._init_workspace)
+        self._ws = self._spaces(self._lib, self._init_workspace)
 
-    def _init_workspace(self, ptr, nbytes, stream):
-        return self._lib.moe_workspace_init(ptr, nbytes, stream)
-
-    def _stream_on(self, dev, stream):
-        """The stream's handle for a call on tensors of CUDA device `dev`. Kernels run on the current device."""
-        if self._current_device() != dev:
-            raise ValueError(f"moe: the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
-        return self._raw_stream(dev) if stream is None else _stream(stream)
+    def _elsewhere(self, dev):
+        raise ValueError(f"moe: the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
 
     def device_status(self):
         """(status, detail) of the first device-side error since the last call; synchronises."""
         return self._ws.status()
 
 
-class _Recorded:
-    """A workspace that recorded calls use, and whether their graph is gone."""
-
-    def __init__(self, lib, stream, key, ws):
-        self._lib, self.key, self.ws = lib, key, ws
-        self._ended = ctypes.POINTER(ctypes.c_int)()
-        lib.moe_capture_watch(stream, ctypes.byref(self._ended))  # (without a watch: kept for good)
-
-    def gone(self):
-        return bool(self._ended) and self._ended[0] != 0
-
-    def __del__(self):
-        if self._ended:
-            self._lib.moe_capture_watch_free(self._ended)
-
-
-_in_graphs = set()     # _Recorded of all objects: a graph may outlive the Attention or KVCache whose calls it recorded
-_private_streams = {}  # device -> a stream on which recordings' workspaces are allocated and prepared
+_private_streams = {}  # device -> a stream that nothing but the functions here uses
+_kept = []             # memory that graphs may use, whatever becomes of the object whose calls they recorded
+_pooled_recording = (0, False)
 
 
 def _private_stream(lib, dev):
+    import torch
     s = _private_streams.get(dev)
     if s is None:
         p = ctypes.c_void_p()
         _check(lib.moe_private_stream(ctypes.byref(p)), "moe_private_stream")
-        s = _private_streams[dev] = p.value
+        s = _private_streams[dev] = torch.cuda.ExternalStream(p.value, device=dev)
     return s
 
 
-def _size_class(n):
-    """The next power of two, or three quarters of one: few sizes, so that a workspace that a graph leaves fits another."""
-    p = 1 << max(n - 1, 1).bit_length()
-    return p * 3 // 4 if n <= p * 3 // 4 else p
+@contextlib.contextmanager
+def _beside(lib, dev):
+    """A stream to allocate and prepare memory on while another stream of this thread is recording; waits for it."""
+    import torch
+    with torch.cuda.device(dev):
+        s = _private_stream(lib, dev)
+        mode = lib.moe_thread_capture_mode(_RELAXED)  # else allocating and waiting would break the recording off
+        try:
+            with torch.cuda.stream(s):
+                yield s.cuda_stream
+                s.synchronize()
+        finally:
+            lib.moe_thread_capture_mode(mode)
+
+
+def _on(stream, dev):
+    """`stream` as the current one, so that memory allocated meanwhile is that stream's."""
+    import torch
+    if torch.cuda.current_stream(dev).cuda_stream == (stream or 0):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream or 0, device=dev))
+
+
+def _bytes(n, dev):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+
+
+def _graph_owns(t):
+    """Whether a tensor is memory of a graph's own (of torch's graphs), which no other program part gets."""
+    import torch
+    at = t.data_ptr()
+    return any(s["address"] <= at < s["address"] + s["total_size"] and tuple(s.get("segment_pool_id", (0, 0))) != (0, 0)
+               for s in torch.cuda.memory_snapshot())
+
+
+def _scratch(lib, stream, recording, nbytes, dev):
+    """Scratch memory of a recorded call. Only the call itself uses it, so the graph may use it for other things too, but
+    nothing else may while the graph lives: it is the graph's own memory if torch records the graph, and kept with the
+    graph if GraphCapture does. Of other recordings nobody knows when the graph is gone."""
+    global _pooled_recording
+    if nbytes == 0:
+        return None
+    capture = _lib.GraphCapture.of(recording)
+    if capture is None:
+        if _pooled_recording[0] != recording:
+            with _on(stream, dev):
+                _pooled_recording = (recording, _graph_owns(_bytes(1, dev)))
+        if _pooled_recording[1]:
+            with _on(stream, dev):
+                return _bytes(nbytes, dev)
+    t = capture.scratch.get(stream) if capture is not None else None
+    if t is None or t.numel() < nbytes:
+        with _beside(lib, dev):
+            t = _bytes(nbytes, dev)
+        if capture is not None:
+            capture.scratch[stream] = t
+            capture.hold(t)
+        else:
+            _kept.append(t)
+    return t
+
+
+def _failed(headers, n):
+    """Which of a tensor's first n headers hold an error."""
+    import torch
+    words = headers.view(torch.int32)[:n * _HEADER // 4:_HEADER // 4].tolist()
+    return [i for i, w in enumerate(words) if w != MOE_OK]
 
 
 class _Workspaces:
     """Prepared workspaces, one for each stream (of each device) that calls arrive on, so that calls on different streams
-    never share scratch memory, and one for each graph recording (and stream of it), which nothing else uses while the
-    graph lives, however late and on whatever stream it runs. It is prepared beside the recording, once, so an error that a
-    replay records stays until it is read; when the graph is gone another recording gets it. (A recording on a stream that
-    calls have used before takes that stream's: its replays are to be ordered with further calls there.) A stream's is
-    given back when a larger one replaces it."""
+    never share scratch memory. A stream's is given back when a larger one replaces it. Calls that are recorded get a
+    header of their own for each recording (and stream of it), and scratch memory that is the graph's (_scratch), so that
+    nothing else uses either while the graph lives, however late and on whatever stream it runs. Headers are prepared
+    beside the recording, once, and kept for good, 256 bytes each: an error that a replay records stays until it is read.
+    (A recording on a stream that calls have used before takes that stream's: its replays are to be ordered with further
+    calls there.)"""
+
+    _HEADERS = 64  # of one piece of memory
 
     def __init__(self, lib, init):
         self._lib, self._init = lib, init
         self._of = {}        # stream -> (tensor, bytes, address); (stream, device) on others than the first device,
                              # as the default stream has one handle for all of them
-        self._recorded = {}  # (stream, recording, device) -> the same
-        self._graphs = []    # _Recorded: of these, and those that larger ones replaced, which their graph uses too
-        self._idle = []      # (device, the same): their graph is gone
+        self._recorded = {}  # (stream, recording, device) -> the same, a header
+        self._headers = {}   # device -> [(tensor, how many of its headers are taken)]
 
     def get(self, stream, nbytes, dev):
         ws = self._of.get(stream if dev == 0 else (stream, dev))
@@ -157,11 +204,10 @@ class _Workspaces:
             if old[1] >= nbytes:
                 return old
             nbytes = max(nbytes, old[1] * 3 // 2)  # a batch that grows one by one
-        current = torch.cuda.current_stream(dev).cuda_stream == (stream or 0)
         # Memory of the stream's own: what was enqueued there is done with it before the next call that gets it runs, so the
         # workspace that this one replaces can be given back at once.
-        with contextlib.nullcontext() if current else torch.cuda.stream(torch.cuda.ExternalStream(stream or 0, device=dev)):
-            t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+        with _on(stream, dev):
+            t = _bytes(nbytes, dev)
             ws = (t, nbytes, t.data_ptr())
             with torch.cuda.device(dev):
                 _check(self._init(ws[2], nbytes, stream), "workspace_init")
@@ -171,43 +217,22 @@ class _Workspaces:
         return ws
 
     def _make_recorded(self, stream, recording, nbytes, dev):
-        import torch
+        """(header's tensor, bytes, address, scratch memory's address, bytes, tensor)"""
         key = (stream, recording, dev)
-        ws = self._recorded.get(key)
-        if ws is not None and ws[1] >= nbytes:
-            return ws
-        self._sweep()
-        fit = min((w for w in self._idle if w[0] == dev and w[1][1] >= nbytes), key=lambda w: w[1][1], default=None)
-        if fit is not None:
-            self._idle.remove(fit)
-            ws = fit[1]
-        else:
-            # not the recording's memory, which its graph may use for other things before and after these calls
-            nbytes, private = _size_class(nbytes), _private_stream(self._lib, dev)
-            beside = torch.cuda.ExternalStream(private, device=dev)
-            mode = self._lib.moe_thread_capture_mode(_RELAXED)  # this thread's other calls are to allocate and wait
-            try:
-                with torch.cuda.device(dev), torch.cuda.stream(beside):
-                    t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-                    ws = (t, nbytes, t.data_ptr())
-                    _check(self._init(ws[2], nbytes, private), "workspace_init")
-                    beside.synchronize()
-            finally:
-                self._lib.moe_thread_capture_mode(mode)
-        held = _Recorded(self._lib, stream, key, ws)
-        self._graphs.append(held)
-        _in_graphs.add(held)
-        self._recorded[key] = ws
-        return ws
-
-    def _sweep(self):
-        """Takes back what graphs that are gone have used."""
-        _in_graphs.difference_update([r for r in _in_graphs if r.gone()])
-        for r in [r for r in self._graphs if r.gone()]:
-            self._graphs.remove(r)
-            if self._recorded.get(r.key) is r.ws:
-                del self._recorded[r.key]
-            self._idle.append((r.key[2], r.ws))
+        head = self._recorded.get(key)
+        if head is None:
+            rows = self._headers.setdefault(dev, [])
+            with _beside(self._lib, dev) as s:
+                if not rows or rows[-1][1] == self._HEADERS:
+                    rows.append((_bytes(self._HEADERS * _HEADER, dev), 0))
+                    _kept.append(rows[-1][0])
+                t, n = rows[-1]
+                at = t.data_ptr() + n * _HEADER
+                _check(self._init(at, _HEADER, s), "workspace_init")
+            rows[-1] = (t, n + 1)
+            head = self._recorded[key] = (t, _HEADER, at)
+        t = _scratch(self._lib, stream, recording, nbytes - _HEADER, dev)
+        return (*head, None, 0, None) if t is None else (*head, t.data_ptr(), t.numel(), t)
 
     def status(self):
         """(status, detail) of the first device-side error of any of them; clears it."""
@@ -217,15 +242,46 @@ class _Workspaces:
                 st, detail = _lib.get_device_status(ws[0], key[0] if type(key) is tuple else key)
             if st != MOE_OK:
                 return st, detail
-        recorded = [r.ws for r in self._graphs] + [w[1] for w in self._idle]
-        for dev in {ws[0].device for ws in recorded}:
-            torch.cuda.synchronize(dev)
-        for ws in recorded:
-            with torch.cuda.device(ws[0].device):
-                st, detail = _lib.get_device_status(ws[0])
-            if st != MOE_OK:
-                return st, detail
+        for dev, rows in self._headers.items():
+            with torch.cuda.device(dev):
+                torch.cuda.synchronize()
+                for t, n in rows:
+                    for i in _failed(t, n):
+                        return _lib.get_device_status(t[i * _HEADER:(i + 1) * _HEADER])
         return MOE_OK, 0
+
+
+class _CacheWorkspace:
+    """The workspace of a KVCache: one for all streams and graphs, as calls on one cache do not overlap in time. A graph of
+    such calls needs it as it needs the cache's tensors."""
+
+    def __init__(self, lib, init):
+        self._lib, self._init, self._ws = lib, init, None
+
+    def get(self, stream, nbytes, dev):
+        return self._ws or self._make(stream, nbytes, dev)
+
+    def _make(self, stream, nbytes, dev):
+        import torch
+        if self._lib.moe_stream_capture_id(stream):
+            with _beside(self._lib, dev) as s:
+                t = _bytes(nbytes, dev)
+                _check(self._init(t.data_ptr(), nbytes, s), "workspace_init")
+        else:
+            with _on(stream, dev), torch.cuda.device(dev):
+                t = _bytes(nbytes, dev)
+                _check(self._init(t.data_ptr(), nbytes, stream), "workspace_init")
+        self._ws = (t, nbytes, t.data_ptr())
+        return self._ws
+
+    def status(self):
+        """(status, detail) of the first device-side error; clears it."""
+        import torch
+        if self._ws is None:
+            return MOE_OK, 0
+        with torch.cuda.device(self._ws[0].device):
+            torch.cuda.synchronize()
+            return _lib.get_device_status(self._ws[0])
 
 
 class KVCache(_Bound):
@@ -273,6 +329,8 @@ class KVCache(_Bound):
         return cls(k, torch.empty_like(k), torch.full((n_slots, width), -1, **i32), torch.zeros(n_slots, **i32),
                    torch.zeros(n_pages, **i32))
 
+    _spaces = _CacheWorkspace
+
     def _init_workspace(self, ptr, nbytes, stream):
         return self._lib.moe_cache_workspace_init(self._ref, ptr, nbytes, stream)
 
@@ -281,14 +339,18 @@ class KVCache(_Bound):
 
     def clear(self, stream=None):
         """Empties every slot and frees every page."""
-        s = self._stream_on(self._dev, stream)
+        if self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         _check(self._lib.moe_cache_clear(self._ref, s), "moe_cache_clear")
 
     def resize(self, slots, new_lens, stream=None):
         """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
         n = _ints(slots, "slots", None, self._dev, self._i32)
         _ints(new_lens, "new_lens", n, self._dev, self._i32)
-        s = self._stream_on(self._dev, stream)
+        if self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_resize")
@@ -303,7 +365,9 @@ class KVCache(_Bound):
         n = _ints(slots, "slots", None, self._dev, self._i32)
         _ints(offsets, "offsets", n + 1, self._dev, self._i32)
         _ints(pos, "pos", n, self._dev, self._i32)
-        s = self._stream_on(self._dev, stream)
+        if self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
                                          k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
@@ -312,7 +376,9 @@ class KVCache(_Bound):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
         n = _ints(src, "src", None, self._dev, self._i32)
         _ints(dst, "dst", n, self._dev, self._i32)
-        s = self._stream_on(self._dev, stream)
+        if self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
 
@@ -324,7 +390,9 @@ class KVCache(_Bound):
                 raise ValueError("moe: pass n_live with an explicit stream")
             n_live = self._empty(1, dtype=self._i32, device=self.device)
         _ints(n_live, "n_live", 1, self._dev, self._i32)
-        s = self._stream_on(self._dev, stream)
+        if self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
         return n_live
@@ -333,7 +401,9 @@ class KVCache(_Bound):
         """Page dst[i] gets page src[i]'s contents in every layer."""
         n = _ints(src, "src", None, self._dev, self._i32)
         _ints(dst, "dst", n, self._dev, self._i32)
-        s = self._stream_on(self._dev, stream)
+        if self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         ws = self._workspace(s)
         _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
                "moe_cache_copy_pages")
@@ -356,8 +426,14 @@ class Attention(_Bound):
         self._sized, self._sized_bytes = None, 0
         self._prompt_bytes = self._lib.moe_attention_prompt_workspace_bytes
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
+        self._prompt_ex, self._decode_ex = self._lib.moe_attention_prompt_ex, self._lib.moe_attention_decode_ex
         self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
+
+    _spaces = _Workspaces
+
+    def _init_workspace(self, ptr, nbytes, stream):
+        return self._lib.moe_workspace_init(ptr, nbytes, stream)
 
     def _workspace(self, stream, n, dev):
         need = self._need.get(n)
@@ -403,7 +479,9 @@ class Attention(_Bound):
         if kv_offsets is not None:
             _ints(kv_offsets, "kv_offsets", n + 1, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
-        s = self._stream_on(dev, stream)
+        if self._current_device() != dev:  # kernels run on the current device
+            self._elsewhere(dev)
+        s = self._raw_stream(dev) if stream is None else _stream(stream)
         need = _HEADER
         if Tk >= _SPLIT_KEYS:
             if self._sized != (n, Tq, Tk, dev):  # the layers of a model call with the same sizes
@@ -411,11 +489,18 @@ class Attention(_Bound):
                 self._sized = (n, Tq, Tk, dev)
             need = self._sized_bytes
         ws = self._ws.get(s, need, dev)
-        _check(self._prompt(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
-            None if kv_offsets is None else kv_offsets.data_ptr(), n, Tq, Tk, self.heads, self.kv_heads, self.head_dim,
-            qs, ks, vs, so, self.scale, _lib.ATTN_CAUSAL if causal else 0, self.dt, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), ws[2], ws[1], s), "moe_attention_prompt")
+        lse_at = None if lse is None else lse.data_ptr()
+        flags = _lib.ATTN_CAUSAL if causal else 0
+        ko = None if kv_offsets is None else kv_offsets.data_ptr()
+        if len(ws) == 3:
+            rc = self._prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
+                              self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(), lse_at,
+                              ws[2], ws[1], s)
+        else:
+            rc = self._prompt_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
+                                 self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(),
+                                 lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        _check(rc, "moe_attention_prompt")
         return out
 
     def decode(self, q, cache, slots, layer=0, shared_len=0, out=None, lse=None, stream=None):
@@ -429,9 +514,16 @@ class Attention(_Bound):
         n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
         _ints(slots, "slots", n, dev, self._i32)
         out, so = self._out(q, out, lse, stream, dev)
-        s = self._stream_on(dev, stream)
+        if self._current_device() != dev:  # kernels run on the current device
+            self._elsewhere(dev)
+        s = self._raw_stream(dev) if stream is None else _stream(stream)
         ws = self._workspace(s, n, dev)
-        _check(self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
-                            out.data_ptr(), None if lse is None else lse.data_ptr(), ws[2], ws[1], s),
-               "moe_attention_decode")
+        lse_at = None if lse is None else lse.data_ptr()
+        if len(ws) == 3:
+            rc = self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
+                              out.data_ptr(), lse_at, ws[2], ws[1], s)
+        else:
+            rc = self._decode_ex(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len,
+                                 self.scale, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        _check(rc, "moe_attention_decode")
         return out

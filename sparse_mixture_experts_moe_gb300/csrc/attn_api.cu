@@ -26,6 +26,17 @@ bool stride_ok(int64_t stride, long long inner, int dt) {
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return ws != nullptr && aligned16(ws) && have >= need;
 }
+// The scratch memory of an attention call: apart, or the workspace from its header on.
+struct Scratch {
+  float* at;
+  size_t bytes;
+};
+bool scratch_of(void* ws, size_t ws_bytes, void* scratch, size_t scratch_bytes, Scratch* s) {
+  if (!workspace_ok(ws, ws_bytes, kWsHeaderBytes) || !aligned16(scratch) || (scratch == nullptr && scratch_bytes != 0)) return false;
+  s->at = static_cast<float*>(scratch != nullptr ? scratch : static_cast<uint8_t*>(ws) + kWsHeaderBytes);
+  s->bytes = scratch != nullptr ? scratch_bytes : ws_bytes - kWsHeaderBytes;
+  return true;
+}
 
 bool cache_sizes_ok(const moe_kv_cache* c) {
   if (c == nullptr || !dtype_ok(c->dt) || !heads_ok(c->H_kv, c->H_kv, c->D)) return false;
@@ -99,7 +110,7 @@ bool plan_holds(const CachePlan& p, const moe_kv_cache* c) {
 bool planned(const moe_kv_cache* c) { return c->dt == MOE_DTYPE_BF16 && c->D <= 128; }
 
 size_t decode_ws_bytes(int n, int H, int D) {
-  return align256(kWsHeaderBytes) + align256((size_t)decode_pieces((long long)n * H) * (D + 2) * 4);
+  return kWsHeaderBytes + align256((size_t)decode_pieces((long long)n * H) * (D + 2) * 4);
 }
 
 size_t prompt_ws_bytes(long long rows, int splits, int D) {
@@ -126,6 +137,15 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride, float scale,
                                 int flags, moe_dtype dt, void* out, float* lse, void* workspace, size_t ws_bytes,
                                 void* stream) {
+  return moe_attention_prompt_ex(q, k, v, q_offsets, kv_offsets, n_seqs, Tq, Tkv, H, H_kv, D, q_stride, k_stride, v_stride,
+                                 out_stride, scale, flags, dt, out, lse, workspace, ws_bytes, nullptr, 0, stream);
+}
+
+moe_status moe_attention_prompt_ex(const void* q, const void* k, const void* v, const int32_t* q_offsets,
+                                   const int32_t* kv_offsets, int n_seqs, int Tq, int Tkv, int H, int H_kv, int D,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                                   float scale, int flags, moe_dtype dt, void* out, float* lse, void* workspace,
+                                   size_t ws_bytes, void* scratch, size_t scratch_bytes, void* stream) {
   if (!dtype_ok(dt) || !heads_ok(H, H_kv, D) || !scale_ok(scale) || (flags & ~MOE_ATTN_CAUSAL) != 0)
     return MOE_ERR_INVALID_ARG;
   if (n_seqs < 0 || Tq < 0 || Tkv < 0 || (Tq > 0 && n_seqs == 0)) return MOE_ERR_INVALID_ARG;
@@ -135,7 +155,8 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
   if (!stride_ok(q_stride, (long long)H * D, dt) || !stride_ok(out_stride, (long long)H * D, dt) ||
       !stride_ok(k_stride, (long long)H_kv * D, dt) || !stride_ok(v_stride, (long long)H_kv * D, dt))
     return MOE_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, ws_bytes, kWsHeaderBytes)) return MOE_ERR_INVALID_ARG;
+  Scratch room;
+  if (!scratch_of(workspace, ws_bytes, scratch, scratch_bytes, &room)) return MOE_ERR_INVALID_ARG;
   if (Tq == 0) return MOE_OK;
   if (q == nullptr || out == nullptr || q_offsets == nullptr || (Tkv > 0 && (k == nullptr || v == nullptr)))
     return MOE_ERR_INVALID_ARG;
@@ -156,9 +177,8 @@ moe_status moe_attention_prompt(const void* q, const void* k, const void* v, con
   if (dt == MOE_DTYPE_BF16 && D <= 128 && Tkv > 0) {
     bind_primary_context();
     int splits = attn_prompt_splits(n_seqs, Tq, Tkv, H, H_kv);
-    if (ws_bytes < prompt_ws_bytes((long long)Tq * H, splits, D)) splits = 1;
-    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes);
-    return cuda_status(launch_attn_prompt_tc(a, splits, part, (cudaStream_t)stream));
+    if (room.bytes < prompt_ws_bytes((long long)Tq * H, splits, D) - kWsHeaderBytes) splits = 1;
+    return cuda_status(launch_attn_prompt_tc(a, splits, room.at, (cudaStream_t)stream));
   }
   return cuda_status(dt == MOE_DTYPE_BF16 ? launch_attn_prompt_mma(a, (cudaStream_t)stream)
                                           : launch_attn_prompt_simt(a, (cudaStream_t)stream));
@@ -172,6 +192,14 @@ size_t moe_attention_workspace_bytes(int n, int H, int D) {
 moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
                                 int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,
                                 float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return moe_attention_decode_ex(cache, layer, q, slots, n, H, q_stride, out_stride, shared_len, scale, out, lse, workspace,
+                                 ws_bytes, nullptr, 0, stream);
+}
+
+moe_status moe_attention_decode_ex(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
+                                   int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,
+                                   float* lse, void* workspace, size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                   void* stream) {
   if (!cache_ok(cache) || layer < 0 || layer >= cache->n_layers || n < 0) return MOE_ERR_INVALID_ARG;
   if (!heads_ok(H, cache->H_kv, cache->D) || !scale_ok(scale) || (long long)n * H >= (1ll << 31))
     return MOE_ERR_INVALID_ARG;
@@ -181,7 +209,10 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   if (!stride_ok(q_stride, (long long)H * cache->D, cache->dt) ||
       !stride_ok(out_stride, (long long)H * cache->D, cache->dt))
     return MOE_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, ws_bytes, decode_ws_bytes(n, H, cache->D))) return MOE_ERR_INVALID_ARG;
+  Scratch room;
+  if (!scratch_of(workspace, ws_bytes, scratch, scratch_bytes, &room) ||
+      room.bytes < decode_ws_bytes(n, H, cache->D) - kWsHeaderBytes)
+    return MOE_ERR_INVALID_ARG;
   if (n == 0) return MOE_OK;
   if (q == nullptr || slots == nullptr || out == nullptr || !aligned16(q) || !aligned16(out))
     return MOE_ERR_INVALID_ARG;
@@ -193,7 +224,7 @@ moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void
   a.k = static_cast<const uint8_t*>(cache->k) + off;
   a.v = static_cast<const uint8_t*>(cache->v) + off;
   a.out = out; a.lse = lse;
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(kWsHeaderBytes));
+  a.part = room.at;
   a.status = static_cast<int*>(workspace);
   a.timeout_ns = wait_timeout_ns() + replace_time(shared_len);
   a.layer = layer;

@@ -3,9 +3,7 @@
 // small batch is no longer bound by the host's per-kernel launch cost.
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <new>
-#include <type_traits>
 
 #include "moe.h"
 
@@ -13,25 +11,6 @@ struct moe_graph_s {
   cudaGraph_t graph = nullptr;
   cudaGraphExec_t exec = nullptr;
 };
-
-namespace {
-
-// Two hold it: the graph (through a CUDA user object) and the caller.
-struct Watch {
-  int ended = 0;  // first: the caller's pointer is the watch's
-  std::atomic<int> holders{2};
-};
-static_assert(std::is_standard_layout<Watch>::value, "a pointer to its first member is one to it");
-void drop(Watch* w) {
-  if (w->holders.fetch_sub(1) == 1) delete w;
-}
-void CUDART_CB graph_gone(void* p) {
-  Watch* w = static_cast<Watch*>(p);
-  __atomic_store_n(&w->ended, 1, __ATOMIC_RELEASE);
-  drop(w);
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -98,40 +77,6 @@ unsigned long long moe_stream_capture_id(void* stream) {
     return 0;
   }
   return st == cudaStreamCaptureStatusActive ? id : 0;
-}
-
-moe_status moe_capture_watch(void* stream, int** ended) {
-  if (ended == nullptr) return MOE_ERR_INVALID_ARG;
-  *ended = nullptr;
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  unsigned long long id = 0;
-  cudaGraph_t graph = nullptr;
-  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &st, &id, &graph) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  if (st != cudaStreamCaptureStatusActive) return MOE_ERR_INVALID_ARG;
-  Watch* w = new (std::nothrow) Watch;
-  if (w == nullptr) return MOE_ERR_CUDA;
-  cudaUserObject_t object = nullptr;
-  if (cudaUserObjectCreate(&object, w, graph_gone, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
-    delete w;
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
-    cudaUserObjectRelease(object, 1);  // (graph_gone drops the graph's hold)
-    drop(w);
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  *ended = &w->ended;
-  return MOE_OK;
-}
-
-moe_status moe_capture_watch_free(int* ended) {
-  if (ended != nullptr) drop(reinterpret_cast<Watch*>(ended));
-  return MOE_OK;
 }
 
 moe_status moe_private_stream(void** stream) {

@@ -11,6 +11,9 @@ from sparse_mixture_experts_moe_gb300 import _lib, attention
 from sparse_mixture_experts_moe_gb300.attention import _Workspaces
 
 
+BAD = moe.MOE_ERR_DEVICE_CHECK
+
+
 class Memory:
     """A device tensor's place: `live` counts the ones that somebody still holds."""
     live, made = 0, 0
@@ -20,7 +23,7 @@ class Memory:
         Memory.made += 1
         self.nbytes, self.device = nbytes, device
         self.address = Memory.made << 40
-        self.header = [0] * 256  # the header's bytes
+        self.header = [0] * max(256, min(nbytes, 1 << 16))  # the bytes of its headers
 
     def __del__(self):
         Memory.live -= 1
@@ -28,16 +31,16 @@ class Memory:
     def data_ptr(self):
         return self.address
 
+    def numel(self):
+        return self.nbytes
+
     def __getitem__(self, part):
         return Part(self, part)
 
 
 class Part:
     def __init__(self, memory, part):
-        self.memory, self.part = memory, part
-
-    def any(self):
-        return any(self.memory.header[self.part])
+        self.memory, self.part, self.device = memory, part, memory.device
 
     def copy_(self, other):
         self.memory.header[self.part] = other.memory.header[other.part]
@@ -50,9 +53,6 @@ class Stream:
     def synchronize(self):
         pass
 
-    def wait_stream(self, other):
-        pass
-
 
 class Lib:
     """The library's calls that workspaces make."""
@@ -60,20 +60,10 @@ class Lib:
     def __init__(self):
         self.recording = {}  # stream -> number of the recording
         self.prepared = []
-        self.watches, self.freed, self.mode = {}, 0, 0
+        self.mode, self.torch_records = 0, True
 
     def moe_stream_capture_id(self, stream):
         return self.recording.get(stream, 0)
-
-    def moe_capture_watch(self, stream, ended):
-        flag = ctypes.c_int(0)
-        self.watches.setdefault(self.recording[stream], []).append(flag)
-        ended._obj.contents = flag
-        return moe.MOE_OK
-
-    def moe_capture_watch_free(self, ended):
-        self.freed += 1
-        return moe.MOE_OK
 
     def moe_private_stream(self, stream):
         stream._obj.value = 0xABC0
@@ -83,11 +73,6 @@ class Lib:
         self.mode, was = mode, self.mode
         return was
 
-    def gone(self, recording):
-        """The recording's graph is destroyed."""
-        for flag in self.watches.pop(recording):
-            flag.value = 1
-
     def init(self, ptr, nbytes, stream):
         assert self.mode == (2 if stream == 0xABC0 else 0)
         self.prepared.append((ptr, nbytes, stream))
@@ -96,9 +81,20 @@ class Lib:
 
 def read_status(ws, stream=None):
     """moe_get_device_status on a stand-in: the header's first two places, cleared."""
-    got = tuple(ws.header[:2])
-    ws.header[:2] = [0, 0]
+    memory, at = (ws.memory, ws.part.start) if isinstance(ws, Part) else (ws, 0)
+    got = tuple(memory.header[at:at + 2])
+    memory.header[at:at + 2] = [0, 0]
     return got
+
+
+def failed(memory, n):
+    return [i for i in range(n) if memory.header[256 * i] != 0]
+
+
+def fail(ws, row):
+    """What a call on a workspace (or a recorded call on its header) leaves behind."""
+    at = ws[2] - ws[0].address
+    ws[0].header[at:at + 2] = [BAD, row]
 
 
 @pytest.fixture
@@ -120,7 +116,10 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(_lib, "get_device_status", read_status)
     monkeypatch.setattr(attention, "_private_streams", {})
-    monkeypatch.setattr(attention, "_in_graphs", set())
+    monkeypatch.setattr(attention, "_kept", [])
+    monkeypatch.setattr(attention, "_failed", failed)
+    monkeypatch.setattr(attention, "_pooled_recording", (0, False))
+    monkeypatch.setattr(attention, "_graph_owns", lambda t: lib.torch_records)
     pool = _Workspaces(lib, lib.init)
     return pool, lib, selected
 
@@ -156,13 +155,10 @@ def test_workspaces_are_prepared_and_read_on_their_device(world, monkeypatch):
     assert where == [("init", 0), ("init", 1), ("init", 3), (0, 0), (1, 1), (3, 3)]
 
 
-BAD = moe.MOE_ERR_DEVICE_CHECK
-
-
 @pytest.mark.parametrize("stream", [0, 7])
 def test_an_error_is_not_lost_when_a_workspace_grows(world, stream):
     pool, lib, _ = world
-    pool.get(stream, 1000, 0)[0].header[:2] = [BAD, 5]
+    fail(pool.get(stream, 1000, 0), 5)
     pool.get(stream, 2000, 0)
     pool.get(stream, 9000, 0)
     assert pool.status() == (BAD, 5)
@@ -173,12 +169,10 @@ def test_errors_of_all_workspaces_of_a_recording_are_read(world):
     """A graph goes on using the smaller workspace that its first calls recorded."""
     pool, lib, _ = world
     lib.recording[3] = 11
-    small = pool.get(3, 1000, 0)
-    large = pool.get(3, 5000, 0)
-    assert small[2] != large[2]
+    small, large = pool.get(3, 1000, 0), pool.get(3, 5000, 0)
     lib.recording.clear()
     for ws, row in ((small, 4), (large, 6), (small, 8)):
-        ws[0].header[:2] = [BAD, row]
+        fail(ws, row)
         assert pool.status() == (BAD, row)
         assert pool.status() == (moe.MOE_OK, 0)
 
@@ -194,60 +188,69 @@ def test_replaced_workspaces_are_given_back(world, stream):
     assert Memory.made - made <= 10
 
 
-def test_recordings_whose_graph_is_gone_leave_their_workspace_to_the_next(world):
+@pytest.mark.parametrize("torch_records", [True, False])
+def test_living_graphs_share_nothing(world, torch_records):
+    pool, lib, _ = world
+    lib.torch_records = torch_records
+    seen, scratch = set(), []
+    for n in range(1, 101):  # more than one piece of headers
+        lib.recording.update({3: n, 4: n})  # two streams of a recording
+        for s in (3, 4):
+            ws = pool.get(s, 1000, 0)
+            assert ws[1] == 256 and ws[4] >= 744 and pool.get(s, 500, 0)[2] == ws[2]
+            seen.add(ws[2])
+            scratch.append(ws[5])
+    lib.recording.clear()
+    assert len(seen) == len(pool._recorded) == 200
+    assert len({t.address for t in scratch}) == 200
+
+
+def test_what_torchs_graphs_use_is_theirs_alone(world):
+    """Scratch memory of the graph's own is not held beyond the call."""
     pool, lib, _ = world
     live = Memory.live
-    for n in range(1, 200):
+    for n in range(1, 129):
         lib.recording[3] = n
-        assert pool.get(3, 1000 + n, 0)[1] >= 1000 + n
-        lib.recording.clear()
-        lib.gone(n)
-    assert Memory.live - live <= 2 and len(pool._recorded) <= 1
-    assert lib.freed >= 190
+        pool.get(3, 1 << 20, 0)
+    assert Memory.live - live == 2  # the headers
 
 
-def test_living_graphs_share_no_workspace(world):
+def test_what_other_recordings_use_is_kept(world):
     pool, lib, _ = world
-    seen = set()
-    for n in range(1, 9):
-        lib.recording[3] = n
-        a, b = pool.get(3, 1000, 0), pool.get(3, 1000, 0)
-        assert a is b
-        lib.recording[4] = n  # another stream of the same recording
-        seen |= {a[2], pool.get(4, 1000, 0)[2]}
-        lib.recording.clear()
-    assert len(seen) == 16
-    lib.gone(5)
-    lib.recording[3] = 20
-    assert pool.get(3, 1000, 0)[2] in seen
-    lib.recording.clear()
-    assert len({w[2] for w in pool._recorded.values()}) == len(pool._recorded) == 15
-
-
-def test_an_error_of_a_graph_that_is_gone_is_read(world):
-    pool, lib, _ = world
+    lib.torch_records = False
+    live = Memory.live
     lib.recording[3] = 1
-    pool.get(3, 1000, 0)[0].header[:2] = [BAD, 9]
-    lib.recording.clear()
-    lib.gone(1)
-    lib.recording[3] = 2
-    pool.get(3, 1000, 0)
-    lib.recording.clear()
-    assert pool.status() == (BAD, 9) and pool.status() == (moe.MOE_OK, 0)
+    at = pool.get(3, 1 << 20, 0)[3]
+    del pool
+    gc.collect()
+    assert Memory.live - live == 2 and at in [t.address for t in attention._kept]
 
 
-def test_a_graph_keeps_its_workspace_when_the_object_is_gone(world):
+def test_what_a_capture_uses_is_kept_with_its_graph(world):
     pool, lib, _ = world
     live = Memory.live
-    other = _Workspaces(lib, lib.init)
-    lib.recording[3] = 1
-    other.get(3, 1000, 0)
-    lib.recording.clear()
-    del other
+    capture = _lib.GraphCapture()
+    _lib.GraphCapture._now[77] = capture
+    try:
+        lib.recording[3] = 77
+        a, b, c = (pool.get(3, n, 0) for n in (5000, 4000, 9000))
+        assert a[3] == b[3] and c[3] != a[3]
+    finally:
+        del _lib.GraphCapture._now[77]
+    assert {id(t) for t in capture._keep} == {id(a[5]), id(c[5])}
+    del a, b, c, capture
     gc.collect()
-    assert Memory.live - live == 1
-    lib.gone(1)
-    lib.recording[3] = 2
-    pool.get(3, 1000, 0)  # any other recording finds that it is over
-    gc.collect()
-    assert Memory.live - live == 1
+    assert Memory.live - live == 1  # the headers
+
+
+def test_a_cache_has_one_workspace(world):
+    _, lib, _ = world
+    pool = attention._CacheWorkspace(lib, lib.init)
+    a = pool.get(0, 3000, 0)
+    lib.recording[5] = 9
+    assert pool.get(7, 3000, 0) is a and pool.get(5, 3000, 0) is a and len(lib.prepared) == 1
+    fail(a, 3)
+    assert pool.status() == (BAD, 3) and pool.status() == (moe.MOE_OK, 0)
+    other = attention._CacheWorkspace(lib, lib.init)
+    b = other.get(5, 3000, 0)  # made while recording: prepared beside it
+    assert lib.prepared[-1][2] == 0xABC0 and other.get(0, 3000, 0) is b
