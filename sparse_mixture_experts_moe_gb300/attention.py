@@ -176,9 +176,8 @@ class _Workspaces:
     never share scratch memory. A stream's is given back when a larger one replaces it. Calls that are recorded get a
     header of their own for each recording (and stream of it), and scratch memory that is the graph's (_scratch), so that
     nothing else uses either while the graph lives, however late and on whatever stream it runs. Headers are prepared
-    beside the recording, once, and kept for good, 256 bytes each: an error that a replay records stays until it is read.
-    (A recording on a stream that calls have used before takes that stream's: its replays are to be ordered with further
-    calls there.)"""
+    beside the recording, once, and kept for good, 256 bytes each: an error that a replay records stays until it is
+    read."""
 
     _HEADERS = 64  # of one piece of memory
 
@@ -189,20 +188,20 @@ class _Workspaces:
         self._recorded = {}  # (stream, recording, device) -> the same, a header
         self._headers = {}   # device -> [(tensor, how many of its headers are taken)]
 
-    def get(self, stream, nbytes, dev):
+    def get(self, stream, nbytes, dev, recording=None):
+        """recording: the number of the recording that the call is part of, 0 for none (None: the library is asked)."""
+        if recording is None:
+            recording = self._lib.moe_stream_capture_id(stream)
+        if recording:
+            return self._make_recorded(stream, recording, nbytes, dev)
         ws = self._of.get(stream if dev == 0 else (stream, dev))
         return ws if ws is not None and ws[1] >= nbytes else self._make(stream, nbytes, dev)
 
     def _make(self, stream, nbytes, dev):
         import torch
-        recording = self._lib.moe_stream_capture_id(stream)
-        if recording:
-            return self._make_recorded(stream, recording, nbytes, dev)
         key = stream if dev == 0 else (stream, dev)
         old = self._of.get(key)
         if old is not None:
-            if old[1] >= nbytes:
-                return old
             nbytes = max(nbytes, old[1] * 3 // 2)  # a batch that grows one by one
         # Memory of the stream's own: what was enqueued there is done with it before the next call that gets it runs, so the
         # workspace that this one replaces can be given back at once.
@@ -427,6 +426,7 @@ class Attention(_Bound):
         self._prompt_bytes = self._lib.moe_attention_prompt_workspace_bytes
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
         self._prompt_ex, self._decode_ex = self._lib.moe_attention_prompt_ex, self._lib.moe_attention_decode_ex
+        self._capturing, self._recording = torch._C._cuda_isCurrentStreamCapturing, self._lib.moe_stream_capture_id
         self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
 
@@ -435,14 +435,14 @@ class Attention(_Bound):
     def _init_workspace(self, ptr, nbytes, stream):
         return self._lib.moe_workspace_init(ptr, nbytes, stream)
 
-    def _workspace(self, stream, n, dev):
+    def _workspace(self, stream, n, dev, recording):
         need = self._need.get(n)
         if need is None:
             need = int(self._lib.moe_attention_workspace_bytes(n, self.heads, self.head_dim))
             if need == 0:
                 raise MoeError(MOE_ERR_INVALID_ARG, "moe_attention_workspace_bytes")
             self._need[n] = need
-        return self._ws.get(stream, need, dev)
+        return self._ws.get(stream, need, dev, recording)
 
     def _out(self, q, out, lse, stream, dev):
         if out is None:
@@ -488,7 +488,7 @@ class Attention(_Bound):
                 self._sized_bytes = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
                 self._sized = (n, Tq, Tk, dev)
             need = self._sized_bytes
-        ws = self._ws.get(s, need, dev)
+        ws = self._ws.get(s, need, dev, self._recording(s) if stream is not None or self._capturing() else 0)
         lse_at = None if lse is None else lse.data_ptr()
         flags = _lib.ATTN_CAUSAL if causal else 0
         ko = None if kv_offsets is None else kv_offsets.data_ptr()
@@ -517,7 +517,8 @@ class Attention(_Bound):
         if self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
-        ws = self._workspace(s, n, dev)
+        # (the current stream is asked faster than any other)
+        ws = self._workspace(s, n, dev, self._recording(s) if stream is not None or self._capturing() else 0)
         lse_at = None if lse is None else lse.data_ptr()
         if len(ws) == 3:
             rc = self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,

@@ -44,6 +44,7 @@ def calls(monkeypatch):
     def watch(obj):
         obj._raw_stream = lambda dev: 0
         obj._current_device = lambda: 0
+        obj._capturing, obj._recording = (lambda: False), (lambda handle: 0)
         obj._ws = Space()
 
         class Lib:
@@ -94,3 +95,18 @@ def test_cache_calls(calls, dev):
             with pytest.raises(ValueError, match="current device"):
                 call()
     assert len(called) == (len(todo) if dev == 0 else 0)
+
+
+@pytest.mark.parametrize("stream", [None, 9])
+def test_calls_say_whether_they_are_recorded(calls, stream):
+    called, watch = calls
+    a = watch(moe.Attention(4, 2, 64, torch.float32))
+    c = cache_on(0, watch)
+    asked = []
+    a._ws.get = lambda *args: asked.append(args[3]) or (None, 1 << 40, 1 << 21)
+    q, kv, i = Fake((3, 4, 64), torch.float32, 0), Fake((3, 2, 64), torch.float32, 0), lambda n: Fake((n,), torch.int32, 0)
+    for now in (0, 41):
+        a._capturing, a._recording = (lambda: now != 0), (lambda handle: now)
+        a.prompt(q, kv, kv, i(2), out=q, stream=stream)
+        a.decode(q, c, i(3), out=q, stream=stream)
+    assert asked == [0, 0, 41, 41]

@@ -254,3 +254,17 @@ def test_a_cache_has_one_workspace(world):
     other = attention._CacheWorkspace(lib, lib.init)
     b = other.get(5, 3000, 0)  # made while recording: prepared beside it
     assert lib.prepared[-1][2] == 0xABC0 and other.get(0, 3000, 0) is b
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+def test_a_recording_on_a_used_stream_shares_nothing_with_it(world, dev):
+    """The graph may run on any stream, and beside further calls on this one."""
+    pool, lib, _ = world
+    eager = pool.get(6, 1000, dev)
+    lib.recording[6] = 5
+    first = pool.get(6, 1000, dev, 5)
+    lib.recording[6] = 8
+    second = pool.get(6, 1000, dev, 8)
+    assert len({eager[2], first[2], second[2]}) == 3
+    lib.recording.clear()
+    assert pool.get(6, 1000, dev, 0) is eager

@@ -165,6 +165,35 @@ def test_graphs_of_one_attention_run_at_the_same_time():
     assert a.device_status() == (OK, 0)
 
 
+def test_recordings_on_a_used_stream_run_beside_it():
+    """Two graphs recorded on a stream that calls have used, replayed on other streams while calls go on there."""
+    a, c, q = setup(n=40)
+    slots = i32(range(40), DEV)
+    want = a.decode(q, c, slots, shared_len=64)
+    used = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(used):
+        a.decode(q, c, slots, shared_len=64)
+    graphs = []
+    for _ in range(2):
+        g, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=used):
+            a.decode(q, c, slots, shared_len=64, out=out)
+        graphs.append((g, out, torch.cuda.Stream()))
+    assert len({w[2] for w in a._ws._recorded.values()} | {w[2] for w in a._ws._of.values()}) == 4
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for g, _, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(used):
+            again = a.decode(q, c, slots, shared_len=64)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for _, o, _ in graphs) and torch.equal(again, want)
+    assert a.device_status() == (OK, 0)
+
+
 def test_scratch_memory_apart():
     """moe_attention_decode_ex with scratch memory elsewhere, that holds anything: the same result; too little is refused."""
     a, c, q = setup()
