@@ -12,13 +12,14 @@
 The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
 synchronises. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture); an error that a replay records stays
 until device_status() reads it. Calls on one KVCache must not overlap in time, on whatever streams they are. Index tensors
-(offsets, slots, lengths, positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the work is done
-by the library's kernels.
+(offsets, slots, lengths, positions) are int32 CUDA tensors. Threads may share an Attention; they enqueue their calls one
+after the other. Arguments are marshalled and checked here; the work is done by the library's kernels.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
 
 from . import _lib
 from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
@@ -76,6 +77,8 @@ class _Bound:
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._current_device = torch._C._cuda_getDevice
+        # Calls enqueue several kernels that use one workspace; threads take turns.
+        self._lock = threading.Lock()
         self._ws = self._spaces(self._lib, self._init_workspace)
 
     def _elsewhere(self, dev):
@@ -83,7 +86,8 @@ class _Bound:
 
     def device_status(self):
         """(status, detail) of the first device-side error since the last call; synchronises."""
-        return self._ws.status()
+        with self._lock:
+            return self._ws.status()
 
 
 _private_streams = {}  # device -> a stream that nothing but the functions here uses
@@ -146,11 +150,11 @@ def _scratch(lib, stream, recording, nbytes, dev):
         return None
     capture = _lib.GraphCapture.of(recording)
     if capture is None:
-        if _pooled_recording[0] != recording:
-            with _on(stream, dev):
-                _pooled_recording = (recording, _graph_owns(_bytes(1, dev)))
-        if _pooled_recording[1]:
-            with _on(stream, dev):
+        pooled = _pooled_recording
+        with _on(stream, dev):
+            if pooled[0] != recording:
+                pooled = _pooled_recording = (recording, _graph_owns(_bytes(1, dev)))
+            if pooled[1]:
                 return _bytes(nbytes, dev)
     t = capture.scratch.get(stream) if capture is not None else None
     if t is None or t.numel() < nbytes:
@@ -341,7 +345,8 @@ class KVCache(_Bound):
         if self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
-        _check(self._lib.moe_cache_clear(self._ref, s), "moe_cache_clear")
+        with self._lock:
+            _check(self._lib.moe_cache_clear(self._ref, s), "moe_cache_clear")
 
     def resize(self, slots, new_lens, stream=None):
         """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
@@ -350,9 +355,10 @@ class KVCache(_Bound):
         if self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
-        ws = self._workspace(s)
-        _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
-               "moe_cache_resize")
+        with self._lock:
+            ws = self._workspace(s)
+            _check(self._lib.moe_cache_resize(self._ref, slots.data_ptr(), new_lens.data_ptr(), n, ws[2], ws[1], s),
+                   "moe_cache_resize")
 
     def write(self, k, v, slots, offsets, pos, layer=0, stream=None):
         """Tokens offsets[i] .. offsets[i+1]-1 of k, v [total, kv_heads, head_dim] become positions pos[i], pos[i]+1,
@@ -367,9 +373,10 @@ class KVCache(_Bound):
         if self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
-        ws = self._workspace(s)
-        _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
-                                         k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
+        with self._lock:
+            ws = self._workspace(s)
+            _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
+                                             k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
@@ -378,8 +385,9 @@ class KVCache(_Bound):
         if self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
-        ws = self._workspace(s)
-        _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
+        with self._lock:
+            ws = self._workspace(s)
+            _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
 
     def compact(self, n_live=None, stream=None):
         """Moves the pages in use to the pool's lowest page numbers; returns their number, a one-entry int32
@@ -392,8 +400,9 @@ class KVCache(_Bound):
         if self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
-        ws = self._workspace(s)
-        _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
+        with self._lock:
+            ws = self._workspace(s)
+            _check(self._lib.moe_cache_compact(self._ref, n_live.data_ptr(), ws[2], ws[1], s), "moe_cache_compact")
         return n_live
 
     def copy_pages(self, src, dst, stream=None):
@@ -403,9 +412,10 @@ class KVCache(_Bound):
         if self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
-        ws = self._workspace(s)
-        _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
-               "moe_cache_copy_pages")
+        with self._lock:
+            ws = self._workspace(s)
+            _check(self._lib.moe_cache_copy_pages(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
+                   "moe_cache_copy_pages")
 
 
 class Attention(_Bound):
@@ -482,24 +492,25 @@ class Attention(_Bound):
         if self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
-        need = _HEADER
-        if Tk >= _SPLIT_KEYS:
-            if self._sized != (n, Tq, Tk, dev):  # the layers of a model call with the same sizes
-                self._sized_bytes = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
-                self._sized = (n, Tq, Tk, dev)
-            need = self._sized_bytes
-        ws = self._ws.get(s, need, dev, self._recording(s) if stream is not None or self._capturing() else 0)
-        lse_at = None if lse is None else lse.data_ptr()
-        flags = _lib.ATTN_CAUSAL if causal else 0
-        ko = None if kv_offsets is None else kv_offsets.data_ptr()
-        if len(ws) == 3:
-            rc = self._prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
-                              self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(), lse_at,
-                              ws[2], ws[1], s)
-        else:
-            rc = self._prompt_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
-                                 self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(),
-                                 lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        with self._lock:
+            need = _HEADER
+            if Tk >= _SPLIT_KEYS:
+                if self._sized != (n, Tq, Tk, dev):  # the layers of a model call with the same sizes
+                    self._sized_bytes = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
+                    self._sized = (n, Tq, Tk, dev)
+                need = self._sized_bytes
+            ws = self._ws.get(s, need, dev, self._recording(s) if stream is not None or self._capturing() else 0)
+            lse_at = None if lse is None else lse.data_ptr()
+            flags = _lib.ATTN_CAUSAL if causal else 0
+            ko = None if kv_offsets is None else kv_offsets.data_ptr()
+            if len(ws) == 3:
+                rc = self._prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
+                                  self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(), lse_at,
+                                  ws[2], ws[1], s)
+            else:
+                rc = self._prompt_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
+                                     self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(),
+                                     lse_at, ws[2], ws[1], ws[3], ws[4], s)
         _check(rc, "moe_attention_prompt")
         return out
 
@@ -517,14 +528,15 @@ class Attention(_Bound):
         if self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
-        # (the current stream is asked faster than any other)
-        ws = self._workspace(s, n, dev, self._recording(s) if stream is not None or self._capturing() else 0)
-        lse_at = None if lse is None else lse.data_ptr()
-        if len(ws) == 3:
-            rc = self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
-                              out.data_ptr(), lse_at, ws[2], ws[1], s)
-        else:
-            rc = self._decode_ex(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len,
-                                 self.scale, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        with self._lock:
+            # (the current stream is asked faster than any other)
+            ws = self._workspace(s, n, dev, self._recording(s) if stream is not None or self._capturing() else 0)
+            lse_at = None if lse is None else lse.data_ptr()
+            if len(ws) == 3:
+                rc = self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
+                                  out.data_ptr(), lse_at, ws[2], ws[1], s)
+            else:
+                rc = self._decode_ex(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len,
+                                     self.scale, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
         _check(rc, "moe_attention_decode")
         return out

@@ -1,5 +1,8 @@
 """Calls on tensors of a device that is not the current one, whose kernels would run on another device than the memory
 they are given. Needs no GPU: tensors are stand-ins, and the library's calls are counted, not made."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -110,3 +113,47 @@ def test_calls_say_whether_they_are_recorded(calls, stream):
         a.prompt(q, kv, kv, i(2), out=q, stream=stream)
         a.decode(q, c, i(3), out=q, stream=stream)
     assert asked == [0, 0, 41, 41]
+
+
+def test_threads_that_use_one_object_take_turns(calls):
+    """A call enqueues several kernels, and the library's calls run without the interpreter's lock: the kernels of two calls
+    must not mix, as they use one workspace."""
+    called, watch = calls
+    a = watch(moe.Attention(4, 2, 64, torch.float32))
+    c = cache_on(0, watch)
+    busy, mixed = set(), []
+
+    def library(owner):
+        def call(*args):
+            if owner in busy:
+                mixed.append(owner)
+            busy.add(owner)
+            time.sleep(0.002)
+            busy.discard(owner)
+            return moe.MOE_OK
+        return call
+
+    class Lib:
+        def __getattr__(self, name):
+            return (lambda *x: 256) if name.endswith("_bytes") else library("cache")
+    a._prompt = a._decode = library("attention")
+    c._lib = Lib()
+    q, kv, i = Fake((3, 4, 64), torch.float32, 0), Fake((3, 2, 64), torch.float32, 0), lambda n: Fake((n,), torch.int32, 0)
+    todo = [lambda: a.prompt(q, kv, kv, i(2), out=q), lambda: a.decode(q, c, i(3), out=q), lambda: c.resize(i(2), i(2)),
+            lambda: c.write(kv, kv, i(2), i(3), i(2)), lambda: c.fork(i(2), i(2)), lambda: c.compact(i(1)),
+            lambda: c.copy_pages(i(2), i(2)), c.clear]
+    failed = []
+
+    def run(k):
+        try:
+            for n in range(40):
+                todo[(n + k) % len(todo)]()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in (0, 1, 3, 5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and not mixed

@@ -1,4 +1,6 @@
 """Workspaces of Attention on the GPU: what a larger one, a graph or a second thread does to them."""
+import threading
+
 import pytest
 import torch
 
@@ -224,3 +226,29 @@ def test_cache_calls_in_graphs_recorded_again_and_again():
         assert c.lens.tolist() == [40 + n, 0, 0, 17 + 20 * n, 0, 0]
         assert int((c.refs > 0).sum()) == -(-(40 + n) // 16) + -(-(17 + 20 * n) // 16)
         assert c.device_status() == (OK, 0)
+
+
+def test_two_threads_use_one_attention_on_one_stream():
+    a, c, q = setup(n=24, H=16, Hk=2, D=128)
+    rows = [i32(range(n), DEV) for n in (24, 7)]
+    want = [a.decode(q[:len(r)], c, r, shared_len=64) for r in rows]
+    torch.cuda.synchronize()
+    outs, failed = [[], []], []
+
+    def run(k):
+        try:
+            for _ in range(300):
+                outs[k].append(a.decode(q[:len(rows[k])], c, rows[k], shared_len=64))
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for k in (0, 1):
+        assert sum(not torch.equal(o, want[k]) for o in outs[k]) == 0
+    assert a.device_status() == (OK, 0)
