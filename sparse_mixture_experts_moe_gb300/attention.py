@@ -10,10 +10,10 @@
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
 The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
-synchronises. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture); an error that a replay records stays
-until device_status() reads it. Calls on one KVCache must not overlap in time, on whatever streams they are. Index tensors
-(offsets, slots, lengths, positions) are int32 CUDA tensors. Threads may share an Attention; they enqueue their calls one
-after the other. Arguments are marshalled and checked here; the work is done by the library's kernels.
+synchronises. Calls can be recorded into a graph (torch.cuda.graph, GraphCapture); an error that a replay records
+stays until device_status() reads it. Calls on one KVCache must not overlap in time, on whatever streams they are.
+Threads may share an Attention; they enqueue their calls one after the other. Index tensors (offsets, slots, lengths,
+positions) are int32 CUDA tensors. Arguments are marshalled and checked here; the work is done by the library's kernels.
 """
 from __future__ import annotations
 
@@ -76,7 +76,7 @@ class _Bound:
         self._empty, self._empty_like = torch.empty, torch.empty_like
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
-        self._current_device = torch._C._cuda_getDevice
+        self._current_device, self._many = torch._C._cuda_getDevice, torch.cuda.device_count() > 1
         # Calls enqueue several kernels that use one workspace; threads take turns.
         self._lock = threading.Lock()
         self._ws = self._spaces(self._lib, self._init_workspace)
@@ -142,9 +142,9 @@ def _graph_owns(t):
 
 
 def _scratch(lib, stream, recording, nbytes, dev):
-    """Scratch memory of a recorded call. Only the call itself uses it, so the graph may use it for other things too, but
-    nothing else may while the graph lives: it is the graph's own memory if torch records the graph, and kept with the
-    graph if GraphCapture does. Of other recordings nobody knows when the graph is gone."""
+    """Scratch memory of a recorded call. Only the call itself uses it, so the graph may use it for other things too,
+    but nothing else may while the graph lives: it is the graph's own memory if torch records the graph, and kept with
+    the graph if GraphCapture does. Of other recordings nobody knows when the graph is gone."""
     global _pooled_recording
     if nbytes == 0:
         return None
@@ -176,12 +176,12 @@ def _failed(headers, n):
 
 
 class _Workspaces:
-    """Prepared workspaces, one for each stream (of each device) that calls arrive on, so that calls on different streams
-    never share scratch memory. A stream's is given back when a larger one replaces it. Calls that are recorded get a
-    header of their own for each recording (and stream of it), and scratch memory that is the graph's (_scratch), so that
-    nothing else uses either while the graph lives, however late and on whatever stream it runs. Headers are prepared
-    beside the recording, once, and kept for good, 256 bytes each: an error that a replay records stays until it is
-    read."""
+    """Prepared workspaces, one for each stream (of each device) that calls arrive on, so that calls on different
+    streams never share scratch memory. A stream's is given back when a larger one replaces it. Calls that are recorded
+    get a header of their own for each recording (and stream of it), and scratch memory that is the graph's (_scratch),
+    so that nothing else uses either while the graph lives, however late and on whatever stream it runs. Headers are
+    prepared beside the recording, once, and kept for good, 256 bytes each: an error that a replay records stays until
+    it is read."""
 
     _HEADERS = 64  # of one piece of memory
 
@@ -207,8 +207,8 @@ class _Workspaces:
         old = self._of.get(key)
         if old is not None:
             nbytes = max(nbytes, old[1] * 3 // 2)  # a batch that grows one by one
-        # Memory of the stream's own: what was enqueued there is done with it before the next call that gets it runs, so the
-        # workspace that this one replaces can be given back at once.
+        # Memory of the stream's own: what was enqueued there is done with it before the next call that gets it runs, so
+        # the workspace that this one replaces can be given back at once.
         with _on(stream, dev):
             t = _bytes(nbytes, dev)
             ws = (t, nbytes, t.data_ptr())
@@ -255,8 +255,8 @@ class _Workspaces:
 
 
 class _CacheWorkspace:
-    """The workspace of a KVCache: one for all streams and graphs, as calls on one cache do not overlap in time. A graph of
-    such calls needs it as it needs the cache's tensors."""
+    """The workspace of a KVCache: one for all streams and graphs, as calls on one cache do not overlap in time. A graph
+    of such calls needs it as it needs the cache's tensors."""
 
     def __init__(self, lib, init):
         self._lib, self._init, self._ws = lib, init, None
@@ -342,7 +342,7 @@ class KVCache(_Bound):
 
     def clear(self, stream=None):
         """Empties every slot and frees every page."""
-        if self._current_device() != self._dev:  # kernels run on the current device
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
@@ -352,7 +352,7 @@ class KVCache(_Bound):
         """Slot slots[i] gets length new_lens[i]: pages are released (0 frees the slot) or allocated."""
         n = _ints(slots, "slots", None, self._dev, self._i32)
         _ints(new_lens, "new_lens", n, self._dev, self._i32)
-        if self._current_device() != self._dev:  # kernels run on the current device
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
@@ -370,24 +370,25 @@ class KVCache(_Bound):
         n = _ints(slots, "slots", None, self._dev, self._i32)
         _ints(offsets, "offsets", n + 1, self._dev, self._i32)
         _ints(pos, "pos", n, self._dev, self._i32)
-        if self._current_device() != self._dev:  # kernels run on the current device
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
             ws = self._workspace(s)
-            _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
-                                             k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
+            _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n,
+                                             total, k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
         n = _ints(src, "src", None, self._dev, self._i32)
         _ints(dst, "dst", n, self._dev, self._i32)
-        if self._current_device() != self._dev:  # kernels run on the current device
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
             ws = self._workspace(s)
-            _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s), "moe_cache_fork")
+            _check(self._lib.moe_cache_fork(self._ref, src.data_ptr(), dst.data_ptr(), n, ws[2], ws[1], s),
+                   "moe_cache_fork")
 
     def compact(self, n_live=None, stream=None):
         """Moves the pages in use to the pool's lowest page numbers; returns their number, a one-entry int32
@@ -397,7 +398,7 @@ class KVCache(_Bound):
                 raise ValueError("moe: pass n_live with an explicit stream")
             n_live = self._empty(1, dtype=self._i32, device=self.device)
         _ints(n_live, "n_live", 1, self._dev, self._i32)
-        if self._current_device() != self._dev:  # kernels run on the current device
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
@@ -409,7 +410,7 @@ class KVCache(_Bound):
         """Page dst[i] gets page src[i]'s contents in every layer."""
         n = _ints(src, "src", None, self._dev, self._i32)
         _ints(dst, "dst", n, self._dev, self._i32)
-        if self._current_device() != self._dev:  # kernels run on the current device
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
@@ -439,27 +440,26 @@ class Attention(_Bound):
         self._capturing, self._recording = torch._C._cuda_isCurrentStreamCapturing, self._lib.moe_stream_capture_id
         self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
+        self._of = self._ws._of
 
     _spaces = _Workspaces
 
     def _init_workspace(self, ptr, nbytes, stream):
         return self._lib.moe_workspace_init(ptr, nbytes, stream)
 
-    def _workspace(self, stream, n, dev, recording):
-        need = self._need.get(n)
-        if need is None:
-            need = int(self._lib.moe_attention_workspace_bytes(n, self.heads, self.head_dim))
-            if need == 0:
-                raise MoeError(MOE_ERR_INVALID_ARG, "moe_attention_workspace_bytes")
-            self._need[n] = need
-        return self._ws.get(stream, need, dev, recording)
+    def _size(self, n):
+        need = int(self._lib.moe_attention_workspace_bytes(n, self.heads, self.head_dim))
+        if need == 0:
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_attention_workspace_bytes")
+        self._need[n] = need
+        return need
 
-    def _out(self, q, out, lse, stream, dev):
+    def _out(self, q, qs, out, lse, stream, dev):
         if out is None:
             if stream is not None:  # a tensor made here belongs to the current stream
                 raise ValueError("moe: pass out with an explicit stream")
-            out = self._empty_like(q) if q.is_contiguous() else self._empty(q.shape, dtype=self.dtype, device=q.device)
             so = self.heads * self.head_dim
+            out = self._empty_like(q) if qs == so else self._empty(q.shape, dtype=self.dtype, device=q.device)
         else:
             to, so = _heads(out, "out", self.heads, self.head_dim, self.dtype, dev)
             if to != q.shape[0]:
@@ -488,8 +488,8 @@ class Attention(_Bound):
             raise ValueError("moe: q_offsets has one entry more than there are sequences")
         if kv_offsets is not None:
             _ints(kv_offsets, "kv_offsets", n + 1, dev, self._i32)
-        out, so = self._out(q, out, lse, stream, dev)
-        if self._current_device() != dev:  # kernels run on the current device
+        out, so = self._out(q, qs, out, lse, stream, dev)
+        if self._many and self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
         with self._lock:
@@ -499,19 +499,23 @@ class Attention(_Bound):
                     self._sized_bytes = self._prompt_bytes(n, Tq, Tk, self.heads, self.kv_heads, self.head_dim, self.dt)
                     self._sized = (n, Tq, Tk, dev)
                 need = self._sized_bytes
-            ws = self._ws.get(s, need, dev, self._recording(s) if stream is not None or self._capturing() else 0)
+            rec = self._recording(s) if stream is not None or self._capturing() else 0
+            ws = None if rec or dev else self._of.get(s)  # the usual case of _Workspaces.get
+            if ws is None or ws[1] < need:
+                ws = self._ws.get(s, need, dev, rec)
             lse_at = None if lse is None else lse.data_ptr()
             flags = _lib.ATTN_CAUSAL if causal else 0
             ko = None if kv_offsets is None else kv_offsets.data_ptr()
             if len(ws) == 3:
-                rc = self._prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
-                                  self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(), lse_at,
-                                  ws[2], ws[1], s)
+                rc = self._prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk,
+                                  self.heads, self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt,
+                                  out.data_ptr(), lse_at, ws[2], ws[1], s)
             else:
-                rc = self._prompt_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk, self.heads,
-                                     self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt, out.data_ptr(),
-                                     lse_at, ws[2], ws[1], ws[3], ws[4], s)
-        _check(rc, "moe_attention_prompt")
+                rc = self._prompt_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), ko, n, Tq, Tk,
+                                     self.heads, self.kv_heads, self.head_dim, qs, ks, vs, so, self.scale, flags, self.dt,
+                                     out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        if rc != MOE_OK:
+            raise MoeError(rc, "moe_attention_prompt")
         return out
 
     def decode(self, q, cache, slots, layer=0, shared_len=0, out=None, lse=None, stream=None):
@@ -524,19 +528,24 @@ class Attention(_Bound):
                              f"attention {self.kv_heads} of {self.head_dim} in {self.dtype}")
         n, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
         _ints(slots, "slots", n, dev, self._i32)
-        out, so = self._out(q, out, lse, stream, dev)
-        if self._current_device() != dev:  # kernels run on the current device
+        out, so = self._out(q, qs, out, lse, stream, dev)
+        if self._many and self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
         with self._lock:
             # (the current stream is asked faster than any other)
-            ws = self._workspace(s, n, dev, self._recording(s) if stream is not None or self._capturing() else 0)
+            rec = self._recording(s) if stream is not None or self._capturing() else 0
+            need = self._need.get(n) or self._size(n)
+            ws = None if rec or dev else self._of.get(s)  # the usual case of _Workspaces.get
+            if ws is None or ws[1] < need:
+                ws = self._ws.get(s, need, dev, rec)
             lse_at = None if lse is None else lse.data_ptr()
             if len(ws) == 3:
-                rc = self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len, self.scale,
-                                  out.data_ptr(), lse_at, ws[2], ws[1], s)
+                rc = self._decode(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len,
+                                  self.scale, out.data_ptr(), lse_at, ws[2], ws[1], s)
             else:
-                rc = self._decode_ex(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so, shared_len,
-                                     self.scale, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
-        _check(rc, "moe_attention_decode")
+                rc = self._decode_ex(cache._ref, layer, q.data_ptr(), slots.data_ptr(), n, self.heads, qs, so,
+                                     shared_len, self.scale, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        if rc != MOE_OK:
+            raise MoeError(rc, "moe_attention_decode")
         return out

@@ -46,9 +46,9 @@ def calls(monkeypatch):
 
     def watch(obj):
         obj._raw_stream = lambda dev: 0
-        obj._current_device = lambda: 0
+        obj._current_device, obj._many = (lambda: 0), True
         obj._capturing, obj._recording = (lambda: False), (lambda handle: 0)
-        obj._ws = Space()
+        obj._ws, obj._of = Space(), {}
 
         class Lib:
             def __getattr__(self, name):
