@@ -413,7 +413,7 @@ moe_status moe_graph_destroy(moe_graph graph);
  *   same as q_offsets, Tkv = Tq). With MOE_ATTN_CAUSAL query token t of L_q sees the first
  *   t + 1 + L_kv - L_q keys (clipped to [0, L_kv]): the queries are the last L_q of L_kv positions;
  *   without it every key. Lengths of 0 are valid.
- * In:  q [Tq, H, D], k, v [Tkv, H_kv, D] (token strides q_stride, k_stride, v_stride).
+ * In:  q [Tq, H, D], k, v [Tkv, H_kv, D], Tkv <= 2^31 - 256 (token strides q_stride, k_stride, v_stride).
  * Out: out [Tq, H, D] (token stride out_stride), lse [Tq, H] or NULL.
  * Workspace: at least 256 bytes, prepared with moe_workspace_init (status word). With
  *   moe_attention_prompt_workspace_bytes (0 on bad sizes) a bf16 call of few rows over many keys splits the keys
@@ -452,7 +452,7 @@ typedef struct {
   int32_t* lens;   /* [n_slots] positions held */
   int32_t* refs;   /* [n_pages] */
   int n_layers, n_pages, page_size; /* page_size 16, 32, 64, 128 or 256 */
-  int n_slots, table_width, H_kv, D;
+  int n_slots, table_width, H_kv, D; /* table_width * page_size <= 2^31 - 256 */
   moe_dtype dt;
   const void* plan; /* NULL, or host memory that moe_cache_plan wrote for this cache */
 } moe_kv_cache;

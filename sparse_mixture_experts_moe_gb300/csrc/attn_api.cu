@@ -38,12 +38,14 @@ bool scratch_of(void* ws, size_t ws_bytes, void* scratch, size_t scratch_bytes, 
   return true;
 }
 
+// Keys of a sequence, so that a block's end is still a 32-bit position.
+constexpr long long kMostKeys = (1ll << 31) - 256;
 bool cache_sizes_ok(const moe_kv_cache* c) {
   if (c == nullptr || !dtype_ok(c->dt) || !heads_ok(c->H_kv, c->H_kv, c->D)) return false;
   if (c->n_layers < 1 || c->n_layers > 4096 || c->n_pages < 1 || c->n_pages >= (1 << 30)) return false;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return false;
   if (c->n_slots < 1 || c->n_slots >= (1 << 30) || c->table_width < 1 || (long long)c->n_slots * c->table_width >= (1ll << 31)) return false;
-  if ((long long)c->table_width * c->page_size >= (1ll << 31)) return false;
+  if ((long long)c->table_width * c->page_size > kMostKeys) return false;
   // the rows of a layer are numbered with 32 bits
   return (long long)c->n_pages * c->H_kv * c->page_size < (1ll << 31);
 }
@@ -149,7 +151,7 @@ moe_status moe_attention_prompt_ex(const void* q, const void* k, const void* v, 
   if (!dtype_ok(dt) || !heads_ok(H, H_kv, D) || !scale_ok(scale) || (flags & ~MOE_ATTN_CAUSAL) != 0)
     return MOE_ERR_INVALID_ARG;
   if (n_seqs < 0 || Tq < 0 || Tkv < 0 || (Tq > 0 && n_seqs == 0)) return MOE_ERR_INVALID_ARG;
-  if (kv_offsets == nullptr && Tkv != Tq) return MOE_ERR_INVALID_ARG;
+  if ((kv_offsets == nullptr && Tkv != Tq) || Tkv > kMostKeys) return MOE_ERR_INVALID_ARG;
   // rows and work items are numbered with 32 bits
   if ((long long)Tq * H + (long long)n_seqs * H_kv >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
   if (!stride_ok(q_stride, (long long)H * D, dt) || !stride_ok(out_stride, (long long)H * D, dt) ||

@@ -24,6 +24,8 @@
 // Piece (segment s, run c) has number s + c: going along the units, s or c grows by one from piece to piece.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "attn.cuh"
 #include "kernels.cuh"
 
@@ -666,9 +668,13 @@ cudaError_t launch_attn_decode_tc(const DecodeArgs& all, const CacheMaps& m, cud
   const int G = all.H / all.c.Hkv, NT = G <= 8 ? 1 : 2, RG = (G + 8 * NT - 1) / (8 * NT), HR = all.c.Hkv * RG;
   const int R = G < 8 * NT ? G : 8 * NT, D = all.c.D;
   const int ctas = device_sm_count();
-  for (int first = 0; first < all.n; first += kSlice) {
+  // A slice's units are counted in 32 bits, and its shared part's row pairs are a grid's y.
+  const long long longest = (long long)all.c.width * all.c.page_size;
+  const long long fit = std::min((1ll << 36) / longest, 65535ll * 256 / G);
+  const int slice = (int)std::max(1ll, std::min((long long)kSlice, fit));
+  for (int first = 0; first < all.n; first += slice) {
     DecodeArgs d = all;
-    d.n = all.n - first < kSlice ? all.n - first : kSlice;
+    d.n = std::min(slice, all.n - first);
     d.q = (const __nv_bfloat16*)all.q + (long long)first * all.qs;
     d.out = (__nv_bfloat16*)all.out + (long long)first * all.os;
     d.slots = all.slots + first;

@@ -254,3 +254,21 @@ def test_decode_repeats_itself_beside_other_work(H, Hk, D):
         a.decode(q, c, slots, shared_len=32, out=out)
     torch.cuda.synchronize()
     assert sum(not torch.equal(out, want) for out in outs) == 0
+
+
+# ---------------------------------------------------------------------------------------------------- wide tables
+
+@pytest.mark.parametrize("shared", [0, 256])
+def test_decode_with_tables_for_very_long_sequences(shared):
+    """A table that could hold 2^30 positions a slot: slices are smaller, so that their counts stay below 2^32."""
+    n, page = 100, 256
+    lens = [shared + 3 * i for i in range(n)]
+    lens[64] = 0
+    c, rows = make_cache(lens, shared, page, 1, 8, BF16)
+    table = torch.full((n, 1 << 22), -1, dtype=torch.int32, device=DEV)
+    table[:, :c.width] = c.table
+    wide = moe.KVCache(c.k, c.v, table, c.lens, c.refs)
+    trim(wide, lens)
+    out, lse, q, st = decode(wide, 2, 8, BF16, range(n), shared)
+    assert st == (moe.MOE_OK, 0)
+    right(out, lse, q, c, rows, lens, list(range(n)), 8, BF16)
