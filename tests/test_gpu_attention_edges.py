@@ -272,3 +272,59 @@ def test_decode_with_tables_for_very_long_sequences(shared):
     out, lse, q, st = decode(wide, 2, 8, BF16, range(n), shared)
     assert st == (moe.MOE_OK, 0)
     right(out, lse, q, c, rows, lens, list(range(n)), 8, BF16)
+
+
+# ------------------------------------------------------------------------------ every key, one by one, in long sequences
+
+def spikes(n, D, at, dtype):
+    """n keys of which key j alone has a large product with query i where at[i] = j; values that tell keys apart."""
+    g = torch.Generator().manual_seed(n)
+    k = torch.randn((n, 1, D), generator=g)
+    k = (8 * k / k.norm(dim=-1, keepdim=True)).to(dtype)
+    v = torch.randn((n, 1, D), generator=g).to(dtype)
+    return k, v, (4 * k[at, 0].float()).to(dtype)
+
+
+# q . k is 256 for a query's own key and at most 256 cos of their angle for the others; with scale 1 the own key's weight is
+# then 1 - n e^-(256 (1 - cos)). Among these directions the cosine stays below 0.61, so the others weigh less than 1e-40
+# together: the result is the own key's value, exactly, and lse the own score, up to the D + 8 roundings of a sum of 256.
+
+@pytest.mark.parametrize("D", [64, 128, 200])
+@pytest.mark.parametrize("n,causal", [(3000, False), (3000, True), (700, False)])
+def test_prompt_finds_every_key(n, causal, D):
+    """Each query's result is one key's value, and every key is the one of some query: none is lost or taken twice."""
+    at = torch.arange(n) if causal else torch.randperm(n, generator=torch.Generator().manual_seed(1))
+    for dtype in (BF16, F32):
+        k, v, q = (x.to(DEV) for x in spikes(n, D, at, dtype))
+        a = moe.Attention(1, 1, D, dtype, scale=1.0)
+        lse = torch.empty((n, 1), device=DEV)
+        out = a.prompt(q.unsqueeze(1), k, v, i32([0, n], DEV), causal=causal, lse=lse)
+        assert torch.equal(out[:, 0], v[at.to(DEV), 0])
+        want = (q.double() * k[at.to(DEV), 0].double()).sum(-1)
+        assert ((lse[:, 0].double() - want).abs() <= (D + 8) * 2.0 ** -24 * want + 2.0 ** -20).all()
+        few = a.prompt(q[-40:].unsqueeze(1), k, v, i32([0, 40], DEV), i32([0, n], DEV), causal=causal)  # split keys
+        assert torch.equal(few[:, 0], v[at[-40:].to(DEV), 0])
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (200, BF16), (64, F32), (200, F32)])
+@pytest.mark.parametrize("page,shared", [(16, 0), (64, 0), (16, 1264), (128, 1152)])
+def test_decode_finds_every_key(page, shared, D, dtype):
+    """Key after key of sequences of 1500 positions, through the pages, shared and own."""
+    n, seqs = 1500, 60
+    at = torch.arange(n)
+    k, v, q = (x.to(DEV) for x in spikes(n, D, at, dtype))
+    c, rows = make_cache([n] * seqs, shared, page, 1, D, dtype)
+    for i, r in enumerate(rows):
+        where = i32(r, DEV).long()
+        for pool, x in ((c.k, k), (c.v, v)):
+            full = torch.zeros((len(r) * page, D), dtype=dtype, device=DEV)
+            full[:n] = x[:, 0]
+            pool[0, where, 0] = full.view(len(r), page, D)
+    a, slots = moe.Attention(1, 1, D, dtype, scale=1.0), i32(range(seqs), DEV)
+    lse = torch.empty((seqs, 1), device=DEV)
+    for first in range(0, n, seqs):
+        out = a.decode(q[first:first + seqs].unsqueeze(1), c, slots, shared_len=shared, lse=lse)
+        assert torch.equal(out[:, 0], v[first:first + seqs, 0]), first
+        want = (q[first:first + seqs].double() * k[first:first + seqs, 0].double()).sum(-1)
+        assert ((lse[:, 0].double() - want).abs() <= (D + 8) * 2.0 ** -24 * want + 2.0 ** -20).all()
+    assert a.device_status() == (moe.MOE_OK, 0)
