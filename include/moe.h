@@ -402,8 +402,8 @@ moe_status moe_graph_destroy(moe_graph graph);
  * Token strides are in elements: token t of q is at q + t * q_stride, its heads [H][D] dense, so q, k
  *   and v may be slices of one fused projection. Every pointer and every token stride in bytes is a
  *   multiple of 16; anything else is MOE_ERR_INVALID_ARG.
- * A row that sees no key has out = 0 and lse = -inf. lse (nullable) is the natural logarithm of the sum
- *   of the exponentials of the scaled scores, fp32.
+ * A row that sees no key, or whose scores are all -inf, has out = 0 and lse = -inf. lse (nullable) is the natural
+ *   logarithm of the sum of the exponentials of the scaled scores, fp32.
  * A non-finite key or value reaches only the rows that see its position. A value's column of such a row is then not
  *   finite (an infinity or NaN); a score that is not finite may make the whole row NaN.
  *

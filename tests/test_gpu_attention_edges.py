@@ -328,3 +328,33 @@ def test_decode_finds_every_key(page, shared, D, dtype):
         want = (q[first:first + seqs].double() * k[first:first + seqs, 0].double()).sum(-1)
         assert ((lse[:, 0].double() - want).abs() <= (D + 8) * 2.0 ** -24 * want + 2.0 ** -20).all()
     assert a.device_status() == (moe.MOE_OK, 0)
+
+
+# ------------------------------------------------------------------------------------------- scores that are all -inf
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 200), (F32, 64)])
+def test_rows_whose_scores_are_all_minus_infinity_are_rows_that_see_nothing(dtype, D):
+    T, H, Hk = 1500, 4, 2
+    q = tensor((T, H, D), 1, dtype, DEV)
+    q[..., 3] = 1.0
+    k, v = tensor((T, Hk, D), 2, dtype, DEV), tensor((T, Hk, D), 3, dtype, DEV)
+    k[:70, 1, 3] = float("-inf")  # (all that the first 70 rows see of this key/value head)
+    a = moe.Attention(H, Hk, D, dtype)
+    for tq in (T, 16):  # (16 rows: split keys)
+        lo = T - tq
+        qo, ko = i32([0, tq], DEV), i32([0, T], DEV)
+        kk = k if tq == T else torch.cat([k[:70]] * (T // 70 + 1))[:T]
+        lse = torch.zeros((tq, H), device=DEV)
+        out = a.prompt(q[lo:].contiguous(), kk, v, qo, ko, lse=lse)
+        none = 70 if tq == T else tq
+        assert (out[:none, 2:] == 0).all() and torch.isneginf(lse[:none, 2:]).all()
+        assert torch.isfinite(out).all() and torch.isfinite(lse[:, :2]).all() and torch.isfinite(lse[none:]).all()
+    c, rows = make_cache([64, 70, 150], 64, 16, Hk, D, dtype)
+    for p in rows[0][:4]:
+        c.k[0, p, 1, :, 3] = float("-inf")
+    for shared in (0, 64):
+        lse = torch.zeros((3, H), device=DEV)
+        out = a.decode(q[:3], c, i32(range(3), DEV), shared_len=shared, lse=lse)
+        assert (out[0, 2:] == 0).all() and torch.isneginf(lse[0, 2:]).all()
+        assert torch.isfinite(out).all() and torch.isfinite(lse[1:]).all() and torch.isfinite(lse[:, :2]).all()
+    assert a.device_status() == (moe.MOE_OK, 0)
