@@ -364,21 +364,7 @@ cudaError_t launch(const PromptArgs& a, const SharedPart& sp, dim3 grid, cudaStr
   const cudaError_t e = allow_smem(kern, mma_smem<DP>(), done);
   if (e != cudaSuccess) return e;
   if (!SPLIT) return launch_pdl(kern, grid, dim3(kThreads), mma_smem<DP>(), s, a, sp);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = mma_smem<DP>();
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = grid.z;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, sp);
+  return launch_clusters(kern, grid, dim3(kThreads), dim3(1, 1, grid.z), mma_smem<DP>(), s, a, sp);
 }
 
 }  // namespace

@@ -37,10 +37,7 @@ __device__ __forceinline__ float4 load4f<__nv_bfloat16>(const __nv_bfloat16* p) 
   return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
 }
 // 4 elements to shared memory, waited for with the group.
-template <typename T>
-__device__ __forceinline__ void stage4(float* dst, const T* src, bool in);
-template <>
-__device__ __forceinline__ void stage4<float>(float* dst, const float* src, bool in) {
+__device__ __forceinline__ void stage4(float* dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 template <typename T> __device__ __forceinline__ void store_result(T* p, float x) { *p = from_f32<T>(x); }
@@ -58,7 +55,7 @@ constexpr size_t tile_smem(int DP) { return sizeof(float) * ((size_t)(kRows + KT
 
 // SHARED: rows and keys of a decode call, in pieces. SPLIT: a tile's keys over a cluster (in a kernel without it the
 // code for it would cost registers and 3% of the time).
-template <typename T, int DP, bool SHARED, bool SPLIT>
+template <int DP, bool SHARED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ SharedPart sp) {
   constexpr int NC = DP / (4 * TX);  // groups of 4 columns of a thread
@@ -100,12 +97,12 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     j_end = (int)min((long long)keys, (long long)j_begin + per);
   }
   const float c2 = (SHARED ? da.scale : pa.scale) * 1.4426950408889634f;
-  const T* qsrc = (const T*)(SHARED ? da.q : pa.q);
+  const float* qsrc = (const float*)(SHARED ? da.q : pa.q);
   const long long qs = SHARED ? da.qs : pa.qs;
   for (int i = tid; i < kRows * d4; i += kThreads) {
     const int r = i / d4, c = (i % d4) * 4, R = row0 + min(r, nrows - 1);
-    const T* row = qsrc + (long long)(sq.q0 + R / G) * qs + (long long)(hk * G + R % G) * D;
-    stage4<T>(Qs + r * LD + c, row + min(c, D - 4), r < nrows && c < D);
+    const float* row = qsrc + (long long)(sq.q0 + R / G) * qs + (long long)(hk * G + R % G) * D;
+    stage4(Qs + r * LD + c, row + min(c, D - 4), r < nrows && c < D);
   }
 
   float m[RPT], l[RPT];
@@ -126,15 +123,15 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     for (int c = 0; c < NC; ++c) o[r][c][0] = o[r][c][1] = 0ull;
   }
 
-  const T* kb = (const T*)(SHARED ? da.k : pa.k);
-  const T* vb = (const T*)(SHARED ? da.v : pa.v);
+  const float* kb = (const float*)(SHARED ? da.k : pa.k);
+  const float* vb = (const float*)(SHARED ? da.v : pa.v);
   // (what is left counts down: positions near 2^31 must not wrap)
   for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
     __syncthreads();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // K, then V
       float* dst = half ? Vs : Ks;
-      const T* src = half ? vb : kb;
+      const float* src = half ? vb : kb;
       const long long stride = SHARED ? 0 : (half ? pa.vs : pa.ks);
       for (int i = tid; i < KT * d4; i += kThreads) {
         const int r = i / d4, c = (i % d4) * 4, j = j0 + min(r, left - 1), ce = min(c, D - 4);
@@ -146,7 +143,7 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
         } else {
           at = (long long)(sq.k0 + j) * stride + (long long)hk * D + ce;
         }
-        stage4<T>(dst + r * LD + c, src + at, r < left && c < D);
+        stage4(dst + r * LD + c, src + at, r < left && c < D);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
@@ -299,11 +296,11 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
       }
       const float inv = L == 0.f ? 0.f : 1.0f / L;
       const int P = row0 + R, tok = sq.q0 + P / G, h = hk * G + P % G;
-      T* dst = (T*)pa.out + (long long)tok * pa.os + (long long)h * D + c;
-      store_result<T>(dst, t.x * inv);
-      store_result<T>(dst + 1, t.y * inv);
-      store_result<T>(dst + 2, t.z * inv);
-      store_result<T>(dst + 3, t.w * inv);
+      float* dst = (float*)pa.out + (long long)tok * pa.os + (long long)h * D + c;
+      store_result(dst, t.x * inv);
+      store_result(dst + 1, t.y * inv);
+      store_result(dst + 2, t.z * inv);
+      store_result(dst + 3, t.w * inv);
       if (pa.lse != nullptr && c == 0)
         pa.lse[(long long)tok * H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
@@ -327,13 +324,13 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
       continue;
     }
     const float inv = l[r] == 0.f ? 0.f : 1.0f / l[r];
-    T* dst = (T*)pa.out + (long long)tok * pa.os + (long long)h * D;
+    float* dst = (float*)pa.out + (long long)tok * pa.os + (long long)h * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (tx * 4 + 4 * TX * c >= D) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        store_result<T>(dst + tx * 4 + 4 * TX * c + e, (e & 1 ? f2_hi(o[r][c][e / 2]) : f2_lo(o[r][c][e / 2])) * inv);
+        store_result(dst + tx * 4 + 4 * TX * c + e, (e & 1 ? f2_hi(o[r][c][e / 2]) : f2_lo(o[r][c][e / 2])) * inv);
     }
     if (pa.lse != nullptr && tx == 0)
       pa.lse[(long long)tok * H + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
@@ -626,36 +623,22 @@ decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
   if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
-template <typename T, int DP, bool SHARED, bool SPLIT>
+template <int DP, bool SHARED, bool SPLIT>
 cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, dim3 grid, cudaStream_t s) {
-  auto kern = attn_tile_kernel<T, DP, SHARED, SPLIT>;
+  auto kern = attn_tile_kernel<DP, SHARED, SPLIT>;
   static std::atomic<int> done{0};
   const cudaError_t e = allow_smem(kern, tile_smem(DP), done);
   if (e != cudaSuccess) return e;
   if (!SPLIT) return launch_pdl(kern, grid, dim3(kThreads), tile_smem(DP), s, pa, sp);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = tile_smem(DP);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = grid.z;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, pa, sp);
+  return launch_clusters(kern, grid, dim3(kThreads), dim3(1, 1, grid.z), tile_smem(DP), s, pa, sp);
 }
 template <bool SHARED, bool SPLIT>
 cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, int D, dim3 grid, cudaStream_t s) {
-  if (D <= 64) return launch_tiles<float, 64, SHARED, SPLIT>(pa, sp, grid, s);
-  if (D <= 96) return launch_tiles<float, 96, SHARED, SPLIT>(pa, sp, grid, s);
-  if (D <= 128) return launch_tiles<float, 128, SHARED, SPLIT>(pa, sp, grid, s);
-  return D <= 192 ? launch_tiles<float, 192, SHARED, SPLIT>(pa, sp, grid, s)
-                  : launch_tiles<float, 256, SHARED, SPLIT>(pa, sp, grid, s);
+  if (D <= 64) return launch_tiles<64, SHARED, SPLIT>(pa, sp, grid, s);
+  if (D <= 96) return launch_tiles<96, SHARED, SPLIT>(pa, sp, grid, s);
+  if (D <= 128) return launch_tiles<128, SHARED, SPLIT>(pa, sp, grid, s);
+  return D <= 192 ? launch_tiles<192, SHARED, SPLIT>(pa, sp, grid, s)
+                  : launch_tiles<256, SHARED, SPLIT>(pa, sp, grid, s);
 }
 
 template <typename T, int V4, int GR>

@@ -526,25 +526,6 @@ inline long long page_vectors(const CacheView& c) {
   return (long long)c.Hkv * c.page_size * c.D * (c.dt == MOE_DTYPE_BF16 ? 2 : 4) / 16;
 }
 
-// Launch of one cluster of `ctas` CTAs, with programmatic stream serialisation.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), int ctas, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTB);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 constexpr int kCluster = 8;
 // From here on a cluster works on the tables: entries of a resize, table cells of a fork (64 forks of 250 pages: 15
 // to 21 against 17 to 24 us), pages of a pool.
@@ -560,21 +541,24 @@ cudaError_t copy_list(const CacheView& c, const CacheWs& w, const int32_t* src, 
 
 cudaError_t launch_cache_resize(const CacheView& c, const CacheWs& w, const int32_t* slots, const int32_t* new_lens, int n,
                                 cudaStream_t s) {
-  return launch_cluster(n > kWideEntries ? cache_resize_kernel<true> : cache_resize_kernel<false>, kCluster, s, c, w, slots,
-                        new_lens, n, page_vectors(c));
+  return launch_clusters(n > kWideEntries ? cache_resize_kernel<true> : cache_resize_kernel<false>, dim3(kCluster),
+                         dim3(kTB), dim3(kCluster), 0, s, c, w, slots, new_lens, n, page_vectors(c));
 }
 
 cudaError_t launch_cache_fork(const CacheView& c, const CacheWs& w, const int32_t* src, const int32_t* dst, int n,
                               cudaStream_t s) {
   const bool wide = (long long)n * c.width > kWideCells;
-  const cudaError_t e = wide ? launch_cluster(cache_fork_kernel<true>, kCluster, s, c, w, src, dst, n)
+  const cudaError_t e = wide ? launch_clusters(cache_fork_kernel<true>, dim3(kCluster), dim3(kTB), dim3(kCluster), 0, s, c,
+                                               w, src, dst, n)
                              : launch_pdl(cache_fork_kernel<false>, dim3(1), dim3(kTB), 0, s, c, w, src, dst, n);
   return e != cudaSuccess ? e : copy_list(c, w, nullptr, nullptr, 0, 0, s);
 }
 
 cudaError_t launch_cache_compact(const CacheView& c, const CacheWs& w, int32_t* n_live, cudaStream_t s) {
-  const cudaError_t e = c.n_pages > kWidePages ? launch_cluster(cache_compact_kernel<true>, kCluster, s, c, w, n_live)
-                                               : launch_pdl(cache_compact_kernel<false>, dim3(1), dim3(kTB), 0, s, c, w, n_live);
+  const cudaError_t e = c.n_pages > kWidePages
+                            ? launch_clusters(cache_compact_kernel<true>, dim3(kCluster), dim3(kTB), dim3(kCluster), 0, s,
+                                              c, w, n_live)
+                            : launch_pdl(cache_compact_kernel<false>, dim3(1), dim3(kTB), 0, s, c, w, n_live);
   return e != cudaSuccess ? e : copy_list(c, w, nullptr, nullptr, 0, 1, s);
 }
 
