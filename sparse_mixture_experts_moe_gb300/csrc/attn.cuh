@@ -103,8 +103,8 @@ struct SharedPart {
 };
 
 // What the other warps' waits allow a softmax warp of attn_tc.cu that replaces columns of its 32 rows (replace_unseen):
-// 0.4 us a key and row, where 0.1 was measured.
-constexpr uint64_t replace_time(long long keys) { return (uint64_t)keys * 32 * 400; }
+// 0.4 us a key and row, where 0.1 was measured, and 20 s at most.
+constexpr uint64_t replace_time(long long keys) { return keys < 1562500 ? (uint64_t)keys * 32 * 400 : 20000000000ull; }
 
 // Workspace of one decode call. A piece is the attention of one row over a part of its keys: the sum of
 // the weighted values (D floats), the weights' sum l and the reference m (in log2 units) that the
