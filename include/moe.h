@@ -376,8 +376,9 @@ moe_status moe_forward_q(const void* x, const void* w_r, const float* b_r, const
  *      on error). Use it for moe_forward_q or for a sequence of the separate entry points.
  * moe_stream_capture_id: a number for the recording that `stream` is part of (this library's or any other
  *      of the process), 0 outside one. Calls recorded into one graph can share a workspace of that graph's own.
- * moe_private_stream / moe_thread_capture_mode: a stream on which a workspace can be prepared while another records, and
- *      the calling thread's cudaStreamCaptureMode (returns the one before), with which it may allocate there meanwhile. */
+ * moe_private_stream / moe_thread_capture_mode: a stream on which a workspace can be prepared while another
+ *      records, and the calling thread's cudaStreamCaptureMode (returns the one before), with which it may allocate
+ *      there meanwhile. */
 typedef struct moe_graph_s* moe_graph;
 moe_status moe_graph_capture_begin(void** capture_stream);
 moe_status moe_forward_graph_create(const void* x, const void* w_r, const float* b_r, const void* w1,
@@ -418,10 +419,10 @@ moe_status moe_graph_destroy(moe_graph graph);
  * Workspace: at least 256 bytes, prepared with moe_workspace_init (status word). With
  *   moe_attention_prompt_workspace_bytes (0 on bad sizes) a bf16 call of few rows over many keys splits the keys
  *   over the GPU and joins the parts; with less it runs without.
- *   moe_attention_prompt_ex takes scratch memory apart from the workspace's first 256 bytes, which keep state between calls
- *   and must not be shared by calls that may run at the same time: scratch_bytes at `scratch` (NULL: the rest of the
- *   workspace), at least what moe_attention_prompt_workspace_bytes says less 256. Its contents do not matter, so a graph
- *   may use the memory for other things before and after the call.
+ *   moe_attention_prompt_ex takes scratch memory apart from the workspace's first 256 bytes, which keep state between
+ *   calls and must not be shared by calls that may run at the same time: scratch_bytes at `scratch` (NULL: the rest of
+ *   the workspace); moe_attention_prompt_workspace_bytes less 256 are enough. Its contents do not matter, so a graph may
+ *   use the memory for other things before and after the call.
  * Device checks: offsets that decrease or leave [0, Tq] / [0, Tkv] record MOE_ERR_DEVICE_CHECK
  *   (detail = sequence) and that sequence's rows are not computed.
  */
@@ -508,17 +509,17 @@ moe_status moe_cache_write(const moe_kv_cache* cache, int layer, const int32_t* 
  *   keys are read once for the whole batch, the rest once per sequence, and the parts are joined. The
  *   first slot holds at least shared_len positions.
  * In:  q [n, H, D] (token stride q_stride), slots [n].  Out: out [n, H, D] (out_stride), lse [n, H] or NULL.
- * Workspace: moe_attention_workspace_bytes(n, H, D) bytes, prepared with moe_workspace_init. moe_attention_decode_ex: as
- *   moe_attention_prompt_ex, moe_attention_workspace_bytes less 256 of scratch.
- * Device checks: a slot, length or page out of range, a slot with other pages in the shared part than the first one's, or a
- *   first slot that is shorter than it, records MOE_ERR_DEVICE_CHECK (detail = row). A row whose slot or
+ * Workspace: moe_attention_workspace_bytes(n, H, D) bytes, prepared with moe_workspace_init.
+ *   moe_attention_decode_ex: scratch memory apart, as in moe_attention_prompt_ex, moe_attention_workspace_bytes less 256.
+ * Device checks: a slot, length or page out of range, a slot with other pages in the shared part than the first
+ *   one's, or a first slot that is shorter than it, records MOE_ERR_DEVICE_CHECK (detail = row). A row whose slot or
  *   length is out of range is 0; a row with other pages there may attend either. */
 size_t moe_attention_workspace_bytes(int n, int H, int D);
 moe_status moe_attention_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
                                 int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,
                                 float* lse, void* workspace, size_t ws_bytes, void* stream);
-moe_status moe_attention_decode_ex(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n, int H,
-                                   int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,
+moe_status moe_attention_decode_ex(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots, int n,
+                                   int H, int64_t q_stride, int64_t out_stride, int shared_len, float scale, void* out,
                                    float* lse, void* workspace, size_t ws_bytes, void* scratch, size_t scratch_bytes,
                                    void* stream);
 

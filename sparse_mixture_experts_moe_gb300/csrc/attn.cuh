@@ -90,7 +90,7 @@ struct DecodeArgs {
   int layer;
   void* out;
   float* lse;
-  float* part;  // partial results: attn_simt.cu has [row][piece][D + 2], attn_decode.cu arrays of their own for o and ml
+  float* part;  // partial results: attn_simt.cu has [row][piece][D + 2], attn_decode.cu arrays for o and ml apart
   int* status;
   uint64_t timeout_ns;
 };
@@ -149,8 +149,8 @@ cudaError_t launch_cache_write(const CacheView& c, const CacheWs& w, int layer, 
                                long long ks, long long vs, cudaStream_t s);
 
 // ------------------------------------------------------------------ device helpers
-// Positions that a slot holds: none if the slot or its length is out of range (recorded where the rows' own positions are
-// read).
+// Positions that a slot holds: none if the slot or its length is out of range (recorded where the rows' own positions
+// are read).
 __device__ __forceinline__ int slot_len(const CacheView& c, int s) {
   if (s < 0 || s >= c.n_slots) return 0;
   const int len = c.lens[s];
@@ -289,8 +289,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     }
   }
 }
-// A running reference rises with a score that is this much above it: 8 in log2 units (weights then stay below 2^8). Finite,
-// as -inf plus it is to be -inf (c2, the scale times log2 e, may be next to 0).
+// A running reference rises with a score that is this much above it: 8 in log2 units (weights then stay below 2^8).
+// Finite, as -inf plus it is to be -inf (c2, the scale times log2 e, may be next to 0).
 __device__ __forceinline__ float rescale_above(float c2) { return fminf(8.0f / c2, 3.0e38f); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -305,9 +305,10 @@ __device__ __forceinline__ float ex2(float x) {
 //   - where the row sees values that are not finite in d too, by what these add up to with weights above 0
 //     (NaN, or an infinity),
 //   - else by sum_j 2^(c q.k_j - c m) v_j[d] with the row's own m, every key computed again.
-// Everything else the row already has is right. So the keys are only computed again for rows near the first such value of a column,
-// and the two scans of V go on from row to row. (With every row that was not finite computed again over all its keys, one
-// infinity made 8192 tokens of 32 heads of 128 take 200 ms instead of 0.4. One near the end takes 25 ms now, 120 then.)
+// Everything else the row already has is right. So the keys are only computed again for rows near the first such value
+// of a column, and the two scans of V go on from row to row. (With every row that was not finite computed again over
+// all its keys, one infinity made 8192 tokens of 32 heads of 128 take 200 ms instead of 0.4. One near the end takes 25
+// ms now, 120 then.)
 // A lane has columns 8 lane .. 8 lane + 7. at(j, ko, vo): the element offsets of key j.
 struct Unseen {
   int from, upto;   // V has been looked through in [from, end) and in [0, upto)

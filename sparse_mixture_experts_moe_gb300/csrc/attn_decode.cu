@@ -1,6 +1,6 @@
 // Decode attention over the paged cache (bf16, heads of up to 128 elements): one query token a sequence.
 // Three launches: the shared prefix on the tensor cores (attn_tc.cu, all sequences' rows against each key block
-// once), each sequence's own keys (here), and the join of the pieces.
+// once), each sequence's own keys (here), and the join of the pieces, which also checks that the prefix is shared.
 //
 // Own keys are an HBM stream: every key and value is read once and meets the G rows of its head group, far
 // too few to fill a 128-row tile. The products are m16n8k16 MMAs with the keys on the long side,
@@ -333,9 +333,9 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             qn[k][t][e] = row < nr && col < D ? *reinterpret_cast<const uint32_t*>(qp + row * D + col) : 0u;
           }
     };
-    // A run's first unit goes to the group whose turn it is, which depends on the runs that the CTA had before: `flip` says
-    // whether that is the second one. Parts are added up with the first unit's group first, so that the sums do not depend
-    // on which CTA takes a run.
+    // A run's first unit goes to the group whose turn it is, which depends on the runs that the CTA had before: `flip`
+    // says whether that is the second one. Parts are added up with the first unit's group first, so that the sums do not
+    // depend on which CTA takes a run.
     int flip = 0;
     int rq = 0, run = 0, run_no = 0;
     uint32_t rphase = 0;

@@ -11,8 +11,8 @@
 // Bound by the MMA's operands: each 16 x 16 piece of K or V read from shared memory meets only the warp's 16 rows. 4096
 // tokens, 16 heads of 256 on 4: 471 us, 292 TFLOP/s (16384: 335; on the CUDA cores 4565 us); of 192: 398 us. Decode,
 // 64 sequences behind 2048 shared positions with 2048 of their own: 157 us (340 with the shared ones on the CUDA
-// cores). Columns of a row that a non-finite value at a position which it does not see can have touched are replaced, as
-// in attn_tc.cu: 0 times that value must not reach it.
+// cores). Columns of a row that a non-finite value at a position which it does not see can have touched are replaced,
+// as in attn_tc.cu: 0 times that value must not reach it.
 #include "attn.cuh"
 #include "kernels.cuh"
 

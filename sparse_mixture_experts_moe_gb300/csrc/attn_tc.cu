@@ -18,20 +18,20 @@
 // TMEM (512 columns): S0 S1 (128 fp32 columns each, P in the first 64), O0 O1.
 // The MMAs go PV0(j) QK0(j+1) PV1(j) QK1(j+1): while one tile is in softmax the tensor cores work on the
 // other. QK(j+1) may overwrite P(j) because MMAs of one thread run in issue order.
-// O is only rescaled when a row's maximum rises by more than 8 in log2 units above the reference m (weights
-// then stay below 2^8, exact enough for bf16 as only their relative precision counts); the softmax
+// O is only rescaled when a row's maximum rises by more than 8 in log2 units above the reference m (rescale_above;
+// weights then stay below 2^8, exact enough for bf16 as only their relative precision counts); the softmax
 // warp that sees it waits for the last PV and scales the 32 rows of O itself. After the first blocks
 // that is rare, so no warps are kept for it.
 // A weight is rounded to bf16 (off by at most 2^-8 of it) because the MMA takes both operands in one type; its
 // sum l takes the unrounded value.
-// Keys past a row's limit get weight 0 by index. 0 times a non-finite value in V would still be NaN: the columns of a row
-// that such a value can have touched are replaced (replace_unseen), so that a non-finite value reaches only rows that
-// see it. That costs nothing where everything is finite.
+// Keys past a row's limit get weight 0 by index. 0 times a non-finite value in V would still be NaN: the columns of a
+// row that such a value can have touched are replaced (replace_unseen), so that a non-finite value reaches only rows
+// that see it. That costs nothing where everything is finite.
 // All waits are bounded, as in ffn_tc.cu, with time for rows that are replaced (replace_time).
-// Measured: one prompt of 16384 tokens, 32 heads of 128 on 8: 1.23 ms in a run of ten (1.79 PFLOP/s, 94% of the matrix
-// rate measured in a burst), 1.35 ms in a loop of seconds (1.63, 94% of the sustained rate). Heads of 64: 1.03 ms,
-// 1.06 PFLOP/s, bound by the powers of two: 256 warp instructions of 8 cycles a scheduler and block of a tile pair are
-// 2048 of 2300 cycles (scores computed one block ahead, so that no softmax waits for an MMA, gained nothing).
+// Measured: one prompt of 16384 tokens, 32 heads of 128 on 8: 1.24 ms in a run of ten (1.77 PFLOP/s, 93% of the matrix
+// rate measured in a burst), 1.37 ms in a loop of seconds (1.61, 93% of the sustained rate). Heads of 64: 1.00 ms,
+// 1.10 PFLOP/s, bound by the powers of two: 256 warp instructions of 8 cycles a scheduler and block of a tile pair are
+// 2048 of some 2200 cycles (scores computed one block ahead, so that no softmax waits for an MMA, gained nothing).
 // 13 ragged prompts, 8192 tokens together, heads of 128: 104 us; the masked block of a row, its epilogue and the first
 // scores cost about 3.5 us an item (taking the longest sequences first gains 1 us).
 #include <cuda.h>
@@ -281,8 +281,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (SHARED) {
               const int rows = min(sa.d.c.page_size, BK);
               for (int r = 0; r < BK; r += rows) {
-                // past the shared keys the last page again: those columns are masked (and looked through for values that
-                // are not finite like any that a row does not see)
+                // past the shared keys the last page again: those columns are masked (and looked through for values
+                // that are not finite like any that a row does not see)
                 const int p = min((j0 + r) >> sa.d.c.page_shift, pages - 1);
                 int page = table[p];
                 page = page < 0 || page >= sa.d.c.n_pages ? 0 : page;
