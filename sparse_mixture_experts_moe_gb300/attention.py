@@ -137,8 +137,12 @@ def _graph_owns(t):
     """Whether a tensor is memory of a graph's own (of torch's graphs), which no other program part gets."""
     import torch
     at = t.data_ptr()
+    try:
+        segments = torch.cuda.memory_snapshot()
+    except RuntimeError:  # an allocator that keeps no such record
+        return False
     return any(s["address"] <= at < s["address"] + s["total_size"] and tuple(s.get("segment_pool_id", (0, 0))) != (0, 0)
-               for s in torch.cuda.memory_snapshot())
+               for s in segments)
 
 
 def _scratch(lib, stream, recording, nbytes, dev):

@@ -268,3 +268,17 @@ def test_a_recording_on_a_used_stream_shares_nothing_with_it(world, dev):
     assert len({eager[2], first[2], second[2]}) == 3
     lib.recording.clear()
     assert pool.get(6, 1000, dev, 0) is eager
+
+
+@pytest.mark.parametrize("pool,owned", [((0, 0), False), ((0, 7), True), ((3, 0), True), (None, False)])
+def test_whose_memory_it_is(monkeypatch, pool, owned):
+    """Only memory of a graph's own pool is left to the graph; an allocator that cannot say has none."""
+    t = Memory(64, None)
+
+    def snapshot():
+        if pool is None:
+            raise RuntimeError("no record")
+        return [dict(address=t.address - 4096, total_size=4096, segment_pool_id=(9, 9)),
+                dict(address=t.address - 512, total_size=2048, segment_pool_id=pool)]
+    monkeypatch.setattr(torch.cuda, "memory_snapshot", snapshot)
+    assert attention._graph_owns(t) is owned
