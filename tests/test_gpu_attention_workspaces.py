@@ -252,3 +252,20 @@ def test_two_threads_use_one_attention_on_one_stream():
     for k in (0, 1):
         assert sum(not torch.equal(o, want[k]) for o in outs[k]) == 0
     assert a.device_status() == (OK, 0)
+
+
+def test_calls_on_the_default_stream_while_another_is_current():
+    a, c, q = setup()
+    slots, out = i32(range(12), DEV), torch.zeros_like(q)
+    want = moe.Attention(8, 2, 64, BF16).decode(q, c, slots, shared_len=64)
+    grown = i32([40] * 3, DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for n in (2, 12):
+            a.decode(q[:n], c, slots[:n], shared_len=64, out=out[:n], stream=torch.cuda.default_stream())
+        fresh = moe.KVCache.create(1, 20, 16, 3, 64, 2, 32, BF16, DEV)
+        torch.cuda.synchronize()
+        fresh.resize(i32([0, 1, 2], DEV), grown, stream=torch.cuda.default_stream())
+        torch.cuda.synchronize()
+    assert torch.equal(out, want) and fresh.lens.tolist() == [40] * 3
+    assert a.device_status() == (OK, 0) and fresh.device_status() == (OK, 0)
