@@ -523,6 +523,73 @@ moe_status moe_attention_decode_ex(const moe_kv_cache* cache, int layer, const v
                                    float* lse, void* workspace, size_t ws_bytes, void* scratch, size_t scratch_bytes,
                                    void* stream);
 
+/* moe_attention_chunk — a chunk of new tokens of each of n sequences over the cache: pieces of prompts, drafted tokens and
+ *   single ones, mixed as they come. Sequence i has the query tokens q_offsets[i] .. q_offsets[i+1]-1 (int32 device array
+ *   [n + 1], q_offsets[0] = 0, non-decreasing, last entry at most Tq) and attends the lens[slots[i]] positions of its
+ *   slot, the chunk's own included, once written. With MOE_ATTN_CAUSAL the queries are the slot's last positions: query
+ *   token t of L sees the first lens - L + t + 1 positions (none where that is not above 0); without it every position.
+ *   Two sequences may name one slot. Chunks of 0 tokens are valid; rows of q from q_offsets[n] on are left alone.
+ * In:  q [Tq, H, D] (token stride q_stride), slots [n].  Out: out [Tq, H, D] (out_stride), lse [Tq, H] or NULL.
+ * Workspace: moe_attention_chunk_workspace_bytes(cache, n, Tq, H) bytes (0 on bad sizes), prepared with
+ *   moe_workspace_init. moe_attention_chunk_ex: scratch memory apart, as in moe_attention_prompt_ex.
+ * Device checks: offsets that decrease or leave [0, Tq], a slot, a length or a page out of range record
+ *   MOE_ERR_DEVICE_CHECK (detail = sequence). With such offsets that sequence's rows are not computed, with such a slot or
+ *   length they see nothing; page 0 stands in for such a page. */
+size_t moe_attention_chunk_workspace_bytes(const moe_kv_cache* cache, int n, int Tq, int H);
+moe_status moe_attention_chunk(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots,
+                               const int32_t* q_offsets, int n, int Tq, int H, int64_t q_stride, int64_t out_stride,
+                               float scale, int flags, void* out, float* lse, void* workspace, size_t ws_bytes,
+                               void* stream);
+moe_status moe_attention_chunk_ex(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots,
+                                  const int32_t* q_offsets, int n, int Tq, int H, int64_t q_stride, int64_t out_stride,
+                                  float scale, int flags, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                  void* scratch, size_t scratch_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Rotary positions and norms of heads, for queries and keys on their way to attention or into the cache.
+ * Pair p of the first R elements of a head turns by the angle position * f_p:
+ *   (x_a, x_b) -> (x_a c - x_b s, x_b c + x_a s),  c, s = magnitude * cos, sin(position * f_p)
+ *   with (a, b) = (p, p + R/2) (MOE_ROTARY_HALF) or (2p, 2p + 1) (MOE_ROTARY_INTERLEAVED). Elements from R on stay.
+ * With norm weights w [D] (`dt`, 16-byte aligned; NULL: no norm) a head is first x / sqrt(mean x^2 + eps) * w, over
+ *   all D elements. Everything is fp32 up to one rounding to `dt`; the angles are exact to 2^-31 of a circle at any int32
+ *   position (negative ones turn back).
+ *
+ * moe_rotary: host memory that the caller owns and the calls read.
+ * moe_rotary_init: f_p = base^(-2p / R), base > 1, changed for contexts longer than the trained original_len positions:
+ *   MOE_ROTARY_UNSCALED; MOE_ROTARY_LINEAR: f / factor; MOE_ROTARY_BASE: base * factor^(R / (R - 2)) in place of base
+ *   (R != 2); MOE_ROTARY_TURNS: with n = original_len f / 2 pi turns over the trained length, f (s + (1 - s) / factor),
+ *   s = (n - low) / (high - low) cut to [0, 1]; MOE_ROTARY_PAIRS: f (1 - r + r / factor), where r rises from 0 to 1 over the
+ *   pairs from the one that makes `high` turns (rounded down, at least 0) to the one that makes `low` (rounded up, at most
+ *   R - 1). factor >= 1, 0 < low < high. magnitude 0: 0.1 ln factor + 1 with MOE_ROTARY_PAIRS, else 1.
+ * moe_rotary_set: the same from R / 2 frequencies in radians a position.
+ * moe_rotary_apply: q [T, H, D] and k [T, H_kv, D] (NULL with H_kv = 0) of the tokens at positions[T] (int32, device) to
+ *   q_out and k_out, which may be q and k themselves (with the same strides), and may not overlap them otherwise. Token
+ *   strides in elements, as for attention.
+ * moe_cache_append: moe_cache_write whose keys are normed (k_weight) and turned by their positions in the slot on the way;
+ *   r NULL: not turned. With H > 0 the same tokens' queries q [total, H, D] are normed (q_weight) and turned into q_out in
+ *   the same pass. Device checks as in moe_cache_write; a token that is skipped has no q_out either.
+ * Errors: MOE_ERR_INVALID_ARG on sizes out of range (D as for attention, R even, 0 <= R <= D), non-finite numbers, NULL
+ *   or misaligned pointers, strides as for attention. */
+enum { MOE_ROTARY_HALF = 0, MOE_ROTARY_INTERLEAVED = 1 };
+enum { MOE_ROTARY_UNSCALED = 0, MOE_ROTARY_LINEAR = 1, MOE_ROTARY_BASE = 2, MOE_ROTARY_TURNS = 3, MOE_ROTARY_PAIRS = 4 };
+typedef struct {
+  int D, R, layout;
+  float magnitude;
+  uint64_t turns[128]; /* f_p in 2^-64 of a circle, modulo whole circles */
+} moe_rotary;
+moe_status moe_rotary_init(moe_rotary* r, int D, int R, int layout, double base, int scaling, double factor,
+                           int original_len, double low, double high, double magnitude);
+moe_status moe_rotary_set(moe_rotary* r, int D, int R, int layout, const double* radians, double magnitude);
+moe_status moe_rotary_apply(const moe_rotary* r, const void* q, int64_t q_stride, int H, const void* k, int64_t k_stride,
+                            int H_kv, const int32_t* positions, int T, moe_dtype dt, const void* q_weight,
+                            const void* k_weight, float eps, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, void* stream);
+moe_status moe_cache_append(const moe_kv_cache* cache, int layer, const int32_t* slots, const int32_t* offsets,
+                            const int32_t* pos, int n, int total, const moe_rotary* r, const void* k_new, const void* v_new,
+                            int64_t k_stride, int64_t v_stride, const void* k_weight, const void* q, int64_t q_stride, int H,
+                            const void* q_weight, float eps, void* q_out, int64_t q_out_stride, void* workspace,
+                            size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,8 +6,9 @@ The layer runs in hand-written CUDA kernels behind the C ABI of include/moe.h
     layer = MoELayer(w_r, w1, w2, k=2)          # weights: CUDA tensors, bf16 or fp32
     out = layer(x)                              # x: [T, d] CUDA tensor
 
-Around it, for a decoder block: Attention (packed prompts, and one token a sequence over a paged cache)
-and KVCache (the cache's pages: growing, writing, forking, compacting), in attention.py.
+Around it, for a decoder block: Attention (packed prompts; one token, or a chunk of new ones, a sequence over a paged
+cache) and KVCache (the cache's pages: growing, writing, appending, forking, compacting), in attention.py, and Rotary
+(positions and norms of queries and keys), in rotary.py.
 
 Weights layout: w_r [d, E], w1 [E, d, d_ff], w2 [E, d_ff, d], optional fp32 router bias b_r [E].
 """
@@ -26,6 +27,7 @@ from ._lib import (  # noqa: F401
     get_device_status, status_string, selftest_wait_timeout, lib,
 )
 from .attention import Attention, KVCache  # noqa: F401
+from .rotary import Rotary  # noqa: F401
 
 
 class MoELayer:

@@ -33,6 +33,7 @@ _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _i64 = ctypes.c_int64
 _f = ctypes.c_float
+_d = ctypes.c_double
 
 # name -> argument types (all return int moe_status unless listed in _RESTYPES)
 SIGNATURES = {
@@ -84,6 +85,14 @@ SIGNATURES = {
     "moe_attention_workspace_bytes": [_i, _i, _i],
     "moe_attention_decode": [_p, _i, _p, _p, _i, _i, _i64, _i64, _i, _f, _p, _p, _p, _sz, _p],
     "moe_attention_decode_ex": [_p, _i, _p, _p, _i, _i, _i64, _i64, _i, _f, _p, _p, _p, _sz, _p, _sz, _p],
+    "moe_attention_chunk_workspace_bytes": [_p, _i, _i, _i],
+    "moe_attention_chunk": [_p, _i, _p, _p, _p, _i, _i, _i, _i64, _i64, _f, _i, _p, _p, _p, _sz, _p],
+    "moe_attention_chunk_ex": [_p, _i, _p, _p, _p, _i, _i, _i, _i64, _i64, _f, _i, _p, _p, _p, _sz, _p, _sz, _p],
+    "moe_rotary_init": [_p, _i, _i, _i, _d, _i, _d, _i, _d, _d, _d],
+    "moe_rotary_set": [_p, _i, _i, _i, _p, _d],
+    "moe_rotary_apply": [_p, _p, _i64, _i, _p, _i64, _i, _p, _i, _i, _p, _p, _f, _p, _i64, _p, _i64, _p],
+    "moe_cache_append": [_p, _i, _p, _p, _p, _i, _i, _p, _p, _p, _i64, _i64, _p, _p, _i64, _i, _p, _f, _p, _i64, _p, _sz,
+                         _p],
     "moe_cache_plan_bytes": [],
     "moe_cache_plan": [_p, _p, _sz],
     "moe_cache_workspace_bytes": [_p],
@@ -98,7 +107,8 @@ SIGNATURES = {
 _RESTYPES = {"moe_workspace_bytes": ctypes.c_size_t, "moe_status_string": ctypes.c_char_p,
              "moe_qweight_bytes": ctypes.c_size_t, "moe_qscale_bytes": ctypes.c_size_t,
              "moe_attention_workspace_bytes": ctypes.c_size_t,
-             "moe_attention_prompt_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t,
+             "moe_attention_prompt_workspace_bytes": ctypes.c_size_t,
+             "moe_attention_chunk_workspace_bytes": ctypes.c_size_t, "moe_cache_workspace_bytes": ctypes.c_size_t,
              "moe_cache_plan_bytes": ctypes.c_size_t, "moe_stream_capture_id": ctypes.c_ulonglong}
 
 _LIB = None

@@ -6,7 +6,9 @@
                            dtype=torch.bfloat16, device="cuda")
     cache.resize(slots, new_lens)                     # pages for the new positions (0 frees a slot)
     cache.write(k, v, slots, offsets, pos, layer=l)   # their keys and values, once per layer
+    q = cache.append(k, v, slots, offsets, pos, rope, layer=l, q=q)  # the same, keys and queries turned on the way (Rotary)
     out = attn.decode(q, cache, slots, layer=l, shared_len=n)   # one token a sequence
+    out = attn.chunk(q, cache, slots, offsets, layer=l)         # any number of new tokens of each sequence
     cache.fork(src, dst)                              # samples of one sequence share its full pages
 
 The tensors are on the current device. Everything is enqueued on the current stream, or on `stream`; nothing
@@ -23,6 +25,7 @@ import threading
 
 from . import _lib
 from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
+from .rotary import Rotary, _alone, _tokens, _weight
 
 
 _HEADER = 256           # bytes of a workspace's header
@@ -382,6 +385,55 @@ class KVCache(_Bound):
             _check(self._lib.moe_cache_write(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n,
                                              total, k.data_ptr(), v.data_ptr(), ks, vs, ws[2], ws[1], s), "moe_cache_write")
 
+    def append(self, k, v, slots, offsets, pos, rotary=None, layer=0, q=None, q_weight=None, k_weight=None, eps=1e-6,
+               q_out=None, stream=None):
+        """write() whose keys are normed (where there is k_weight [head_dim]) and turned by their positions (where there is a
+        Rotary) on the way. With q [total, heads, head_dim], the queries of the same tokens, these are normed (q_weight) and
+        turned in the same pass, into q_out if given (it may be q itself); returns them, else None. Norm: x / sqrt(mean x^2 +
+        eps) * weight."""
+        total, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, self._dev)
+        tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, self._dev)
+        if tv != total:
+            raise ValueError(f"moe: k has {total} tokens, v has {tv}")
+        n = _ints(slots, "slots", None, self._dev, self._i32)
+        _ints(offsets, "offsets", n + 1, self._dev, self._i32)
+        _ints(pos, "pos", n, self._dev, self._i32)
+        if rotary is not None and (not isinstance(rotary, Rotary) or rotary.head_dim != self.head_dim):
+            raise ValueError(f"moe: rotary must be a Rotary of head_dim {self.head_dim}")
+        wk, wq = (_weight(w, name, self.head_dim, self.dtype, self._dev) for w, name in ((k_weight, "k_weight"), (q_weight, "q_weight")))
+        H = qs = qso = 0
+        q_at = qo_at = None
+        if q is None:
+            if q_weight is not None or q_out is not None:
+                raise ValueError("moe: q_weight and q_out need q")
+        else:
+            tq, H, qs = _tokens(q, "q", self.head_dim, self.dtype, self._dev)
+            if tq != total or H == 0:
+                raise ValueError(f"moe: k has {total} tokens, q {tq} with {H} heads")
+            if q_out is None:
+                if stream is not None:  # a tensor made here belongs to the current stream
+                    raise ValueError("moe: pass q_out with an explicit stream")
+                q_out, qso = self._empty((total, H, self.head_dim), dtype=self.dtype, device=self.device), H * self.head_dim
+            else:
+                to, _, qso = _tokens(q_out, "q_out", self.head_dim, self.dtype, self._dev, H)
+                if to != total:
+                    raise ValueError(f"moe: expected q_out {tuple(q.shape)}, got {tuple(q_out.shape)}")
+                if total > 0:
+                    for x in (q, k, v):
+                        _alone(q_out, x, "q_out")
+            q_at, qo_at = q.data_ptr(), q_out.data_ptr()
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
+        s = self._raw_stream(self._dev) if stream is None else _stream(stream)
+        with self._lock:
+            ws = self._workspace(s)
+            rc = self._lib.moe_cache_append(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
+                                            None if rotary is None else rotary._ref, k.data_ptr(), v.data_ptr(), ks, vs, wk, q_at,
+                                            qs, H, wq, float(eps), qo_at, qso, ws[2], ws[1], s)
+        if rc != MOE_OK:
+            raise MoeError(rc, "moe_cache_append")
+        return q_out
+
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
         n = _ints(src, "src", None, self._dev, self._i32)
@@ -441,6 +493,8 @@ class Attention(_Bound):
         self._prompt_bytes = self._lib.moe_attention_prompt_workspace_bytes
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
         self._prompt_ex, self._decode_ex = self._lib.moe_attention_prompt_ex, self._lib.moe_attention_decode_ex
+        self._chunk, self._chunk_ex = self._lib.moe_attention_chunk, self._lib.moe_attention_chunk_ex
+        self._chunk_sized, self._chunk_bytes = None, 0
         self._capturing, self._recording = torch._C._cuda_isCurrentStreamCapturing, self._lib.moe_stream_capture_id
         self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
@@ -552,4 +606,43 @@ class Attention(_Bound):
                                      shared_len, self.scale, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
         if rc != MOE_OK:
             raise MoeError(rc, "moe_attention_decode")
+        return out
+
+    def chunk(self, q, cache, slots, q_offsets, layer=0, causal=True, out=None, lse=None, stream=None):
+        """New tokens of each sequence, pieces of prompts, drafted tokens and single ones mixed: q [Tq, heads, head_dim] packed;
+        those of sequence i, q_offsets[i] .. q_offsets[i+1]-1, attend the positions of slot slots[i] of the cache, their own
+        included, once written. causal: they are the slot's last positions, and each sees those up to its own."""
+        dev = cache._dev
+        if cache._key != self._key:
+            raise ValueError(f"moe: the cache holds {cache.kv_heads} heads of {cache.head_dim} in {cache.dtype}, the "
+                             f"attention {self.kv_heads} of {self.head_dim} in {self.dtype}")
+        Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
+        n = _ints(slots, "slots", None, dev, self._i32)
+        _ints(q_offsets, "q_offsets", n + 1, dev, self._i32)
+        out, so = self._out(q, qs, out, lse, stream, dev)
+        if self._many and self._current_device() != dev:  # kernels run on the current device
+            self._elsewhere(dev)
+        s = self._raw_stream(dev) if stream is None else _stream(stream)
+        with self._lock:
+            sizes = (n, Tq, cache.width, cache.page_size, dev)
+            if self._chunk_sized != sizes:  # the layers of a model call with the same sizes
+                need = int(self._lib.moe_attention_chunk_workspace_bytes(cache._ref, n, Tq, self.heads))
+                if need == 0:
+                    raise MoeError(MOE_ERR_INVALID_ARG, "moe_attention_chunk_workspace_bytes")
+                self._chunk_sized, self._chunk_bytes = sizes, need
+            need = self._chunk_bytes
+            rec = self._recording(s) if stream is not None or self._capturing() else 0
+            ws = None if rec or dev else self._of.get(s)  # the usual case of _Workspaces.get
+            if ws is None or ws[1] < need:
+                ws = self._ws.get(s, need, dev, rec)
+            lse_at = None if lse is None else lse.data_ptr()
+            flags = _lib.ATTN_CAUSAL if causal else 0
+            if len(ws) == 3:
+                rc = self._chunk(cache._ref, layer, q.data_ptr(), slots.data_ptr(), q_offsets.data_ptr(), n, Tq, self.heads, qs,
+                                 so, self.scale, flags, out.data_ptr(), lse_at, ws[2], ws[1], s)
+            else:
+                rc = self._chunk_ex(cache._ref, layer, q.data_ptr(), slots.data_ptr(), q_offsets.data_ptr(), n, Tq, self.heads,
+                                    qs, so, self.scale, flags, out.data_ptr(), lse_at, ws[2], ws[1], ws[3], ws[4], s)
+        if rc != MOE_OK:
+            raise MoeError(rc, "moe_attention_chunk")
         return out

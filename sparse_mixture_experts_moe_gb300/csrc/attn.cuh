@@ -102,6 +102,12 @@ struct SharedPart {
   int pieces;       // of a row altogether
 };
 
+// A chunk call's run of items (attn_tc.cu): the one that begins in it and goes on in others, up to run `end`. nrows =
+// 0: none.
+struct ChunkRun {
+  int hk, q0, row0, nrows, end;
+};
+
 // What the other warps' waits allow a softmax warp of attn_tc.cu that replaces columns of its 32 rows (replace_unseen):
 // 0.4 us a key and row, where 0.1 was measured, and 20 s at most.
 constexpr uint64_t replace_time(long long keys) { return keys < 1562500 ? (uint64_t)keys * 32 * 400 : 20000000000ull; }
@@ -125,6 +131,15 @@ int attn_shared_splits(const DecodeArgs& a);
 cudaError_t launch_attn_shared_tc(const DecodeArgs& a, const CacheMaps& m, int splits, float* part_o, float2* part_ml,
                                   cudaStream_t s);
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
+// A chunk of new tokens over the cache: queries and offsets of a, the cache, slots and layer of d. bf16, D <= 128: runs,
+// one an SM, and part, 2 pieces an SM of chunk_piece_rows rows of D + 2 floats.
+int chunk_piece_rows(int Tq, int G);
+cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, ChunkRun* runs, float* part,
+                                 cudaStream_t s);
+// The other types and heads: rows in `pieces` parts, d.part [Tq H][pieces][D + 2].
+int chunk_tile_pieces(const CacheView& c, int n, int Tq, int H);
+cudaError_t launch_attn_chunk_tiles(const PromptArgs& a, const DecodeArgs& d, int pieces, cudaStream_t s);
+cudaError_t launch_attn_chunk_mma(const PromptArgs& a, const SharedPart& sp, dim3 grid, cudaStream_t s);
 
 struct CacheWs {
   int* status;       // workspace header
@@ -147,6 +162,29 @@ cudaError_t launch_cache_copy(const CacheView& c, const CacheWs& w, const int32_
 cudaError_t launch_cache_write(const CacheView& c, const CacheWs& w, int layer, const int32_t* slots,
                                const int32_t* offsets, const int32_t* pos, int n, int total, const void* k, const void* v,
                                long long ks, long long vs, cudaStream_t s);
+
+// Queries and keys turned by their positions (rotary.cu); append: keys and values into the cache's pages.
+struct RotaryArgs {
+  moe_rotary rot;
+  const void *q, *k, *v;
+  long long qs, ks, vs;  // token strides in elements
+  const void *qw, *kw;   // norm weights (nullptr: no norm)
+  float eps;
+  void *qo, *ko;
+  long long qos, kos;
+  const int32_t* positions;
+  int T, H, Hkv, D;
+  int lpr_shift, parts;  // log2 of LPR; warps of a token
+  // append: token t's place comes from the cache's tables
+  CacheView c;
+  void *kp, *vp;  // the layer's pages
+  const int32_t *slots, *offsets, *pos;
+  int n;
+  int* status;
+};
+
+cudaError_t launch_rotary(RotaryArgs& a, int dt, cudaStream_t s);
+cudaError_t launch_cache_append(RotaryArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------------ device helpers
 // Positions that a slot holds: none if the slot or its length is out of range (recorded where the rows' own positions
@@ -201,6 +239,24 @@ __device__ __forceinline__ Seq load_seq(const PromptArgs& a, int i) {
     record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
     s.nq = 0;
     s.nk = 0;
+  }
+  return s;
+}
+// Sequence i of a chunk call: its keys are the positions of its slot (k0). A slot or length out of range is recorded, and
+// its rows see nothing.
+__device__ __forceinline__ Seq load_chunk_seq(const PromptArgs& a, const DecodeArgs& d, int i) {
+  Seq s;
+  s.q0 = a.qo[i];
+  const int q1 = a.qo[i + 1];
+  s.nq = q1 - s.q0;
+  s.k0 = d.slots[i];
+  s.nk = slot_len(d.c, s.k0);
+  if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq) {
+    record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
+    s.nq = 0;
+    s.nk = 0;
+  } else if (s.nk == 0 && s.nq > 0 && (s.k0 < 0 || s.k0 >= d.c.n_slots || d.c.lens[s.k0] != 0)) {
+    record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
   }
   return s;
 }

@@ -119,6 +119,39 @@ size_t prompt_ws_bytes(long long rows, int splits, int D) {
   return kWsHeaderBytes + (splits > 1 ? align256((size_t)rows * splits * (D + 2) * 4) : 0);
 }
 
+// A chunk call's scratch memory: the runs and their pieces, or every row's pieces.
+struct ChunkScratch {
+  size_t bytes;
+  int pieces;
+};
+size_t chunk_runs_bytes() { return align256(sizeof(ChunkRun) * (size_t)device_sm_count()); }
+ChunkScratch chunk_scratch(const CacheView& c, int n, int Tq, int H) {
+  if (c.dt == MOE_DTYPE_BF16 && c.D <= 128)
+    return {chunk_runs_bytes() + align256((size_t)2 * device_sm_count() * chunk_piece_rows(Tq, H / c.Hkv) * (c.D + 2) * 4), 0};
+  const int pieces = chunk_tile_pieces(c, n, Tq, H);
+  return {pieces > 1 ? align256((size_t)Tq * H * pieces * (c.D + 2) * 4) : 0, pieces};
+}
+// rows and work items are numbered with 32 bits
+bool chunk_sizes_ok(const moe_kv_cache* c, int n, int Tq, int H) {
+  return heads_ok(H, c->H_kv, c->D) && n >= 0 && Tq >= 0 && (long long)Tq * H + (long long)n * c->H_kv < (1ll << 31);
+}
+
+bool rotary_ok(const moe_rotary* r) {
+  return r != nullptr && heads_ok(1, 1, r->D) && r->R >= 0 && r->R <= r->D && r->R % 2 == 0 &&
+         (r->layout == MOE_ROTARY_HALF || r->layout == MOE_ROTARY_INTERLEAVED) && std::isfinite(r->magnitude);
+}
+bool eps_ok(float eps) { return eps >= 0.f && std::isfinite(eps); }
+bool rotary_sizes_ok(const moe_rotary* r, int D, int R, int layout) {
+  return r != nullptr && heads_ok(1, 1, D) && R >= 0 && R <= D && R % 2 == 0 &&
+         (layout == MOE_ROTARY_HALF || layout == MOE_ROTARY_INTERLEAVED);
+}
+// `radians` a position as a fraction of a circle, in 2^-64; whole turns drop out.
+uint64_t turn_of(double radians) {
+  double x = radians / 6.283185307179586476925286766559;
+  x -= std::floor(x);  // [0, 1), or 1 for a tiny negative one
+  return x >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(x, 64));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -243,6 +276,63 @@ moe_status moe_attention_decode_ex(const moe_kv_cache* cache, int layer, const v
   return cuda_status(launch_attn_decode_simt(a, (cudaStream_t)stream));
 }
 
+size_t moe_attention_chunk_workspace_bytes(const moe_kv_cache* cache, int n, int Tq, int H) {
+  if (!cache_sizes_ok(cache) || !chunk_sizes_ok(cache, n, Tq, H)) return 0;
+  return kWsHeaderBytes + chunk_scratch(view_of(cache), n, Tq, H).bytes;
+}
+
+moe_status moe_attention_chunk(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots,
+                               const int32_t* q_offsets, int n, int Tq, int H, int64_t q_stride, int64_t out_stride, float scale,
+                               int flags, void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return moe_attention_chunk_ex(cache, layer, q, slots, q_offsets, n, Tq, H, q_stride, out_stride, scale, flags, out, lse,
+                                workspace, ws_bytes, nullptr, 0, stream);
+}
+
+moe_status moe_attention_chunk_ex(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots,
+                                  const int32_t* q_offsets, int n, int Tq, int H, int64_t q_stride, int64_t out_stride,
+                                  float scale, int flags, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                  void* scratch, size_t scratch_bytes, void* stream) {
+  if (!cache_ok(cache) || layer < 0 || layer >= cache->n_layers || !chunk_sizes_ok(cache, n, Tq, H) || !scale_ok(scale) ||
+      (flags & ~MOE_ATTN_CAUSAL) != 0 || (Tq > 0 && n == 0))
+    return MOE_ERR_INVALID_ARG;
+  if (!stride_ok(q_stride, (long long)H * cache->D, cache->dt) || !stride_ok(out_stride, (long long)H * cache->D, cache->dt))
+    return MOE_ERR_INVALID_ARG;
+  const CacheView c = view_of(cache);
+  const ChunkScratch need = chunk_scratch(c, n, Tq, H);
+  Scratch room;
+  if (!scratch_of(workspace, ws_bytes, scratch, scratch_bytes, &room) || room.bytes < need.bytes) return MOE_ERR_INVALID_ARG;
+  if (Tq == 0) return MOE_OK;
+  if (q == nullptr || slots == nullptr || q_offsets == nullptr || out == nullptr || !aligned16(q) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  DecodeArgs d{};
+  d.slots = slots; d.n = n; d.H = H; d.c = c; d.layer = layer; d.scale = scale;
+  const size_t off = (size_t)layer * c.layer_elems() * elem_bytes(cache->dt);
+  d.k = static_cast<const uint8_t*>(cache->k) + off;
+  d.v = static_cast<const uint8_t*>(cache->v) + off;
+  d.part = room.at;
+  PromptArgs a{};
+  a.q = q; a.qo = q_offsets;
+  a.n = n; a.Tq = Tq; a.H = H; a.Hkv = cache->H_kv; a.D = cache->D;
+  a.qs = q_stride; a.os = out_stride;
+  a.scale = scale;
+  a.causal = (flags & MOE_ATTN_CAUSAL) != 0;
+  a.dt = cache->dt;
+  a.out = out; a.lse = lse;
+  a.status = static_cast<int*>(workspace);
+  a.timeout_ns = wait_timeout_ns() + replace_time((long long)c.width * c.page_size);
+  CachePlan p;
+  if (cache->plan != nullptr) {
+    std::memcpy(&p, cache->plan, sizeof(p));
+    if (!plan_holds(p, cache)) return MOE_ERR_INVALID_ARG;
+  }
+  if (!planned(cache)) return cuda_status(launch_attn_chunk_tiles(a, d, need.pieces, (cudaStream_t)stream));
+  bind_primary_context();
+  if (cache->plan == nullptr && !encode_cache_maps(c, &p.maps)) return MOE_ERR_CUDA;
+  ChunkRun* runs = reinterpret_cast<ChunkRun*>(room.at);
+  float* part = room.at + chunk_runs_bytes() / 4;
+  return cuda_status(launch_attn_chunk_tc(a, d, p.maps, runs, part, (cudaStream_t)stream));
+}
+
 size_t moe_cache_plan_bytes(void) { return sizeof(CachePlan); }
 
 moe_status moe_cache_plan(const moe_kv_cache* cache, void* plan, size_t bytes) {
@@ -321,6 +411,114 @@ moe_status moe_cache_write(const moe_kv_cache* cache, int layer, const int32_t* 
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_cache_write(view_of(cache), cache_ws(cache, workspace), layer, slots, offsets, pos, n, total,
                                         k_new, v_new, k_stride, v_stride, (cudaStream_t)stream));
+}
+
+moe_status moe_rotary_set(moe_rotary* r, int D, int R, int layout, const double* radians, double magnitude) {
+  if (!rotary_sizes_ok(r, D, R, layout) || (R > 0 && radians == nullptr) || !std::isfinite((float)magnitude))
+    return MOE_ERR_INVALID_ARG;
+  for (int p = 0; p < R / 2; ++p)
+    if (!std::isfinite(radians[p])) return MOE_ERR_INVALID_ARG;
+  moe_rotary t{};
+  t.D = D; t.R = R; t.layout = layout;
+  t.magnitude = (float)magnitude;
+  for (int p = 0; p < R / 2; ++p) t.turns[p] = turn_of(radians[p]);
+  *r = t;
+  return MOE_OK;
+}
+
+moe_status moe_rotary_init(moe_rotary* r, int D, int R, int layout, double base, int scaling, double factor,
+                           int original_len, double low, double high, double magnitude) {
+  constexpr double kCircle = 6.283185307179586476925286766559;
+  if (!rotary_sizes_ok(r, D, R, layout) || !(base > 1.0) || !std::isfinite(base) || !std::isfinite((float)magnitude))
+    return MOE_ERR_INVALID_ARG;
+  if (scaling < MOE_ROTARY_UNSCALED || scaling > MOE_ROTARY_PAIRS) return MOE_ERR_INVALID_ARG;
+  if (scaling != MOE_ROTARY_UNSCALED && (!(factor >= 1.0) || !std::isfinite(factor))) return MOE_ERR_INVALID_ARG;
+  if (scaling == MOE_ROTARY_BASE && R == 2) return MOE_ERR_INVALID_ARG;
+  if ((scaling == MOE_ROTARY_TURNS || scaling == MOE_ROTARY_PAIRS) &&
+      (original_len < 1 || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
+    return MOE_ERR_INVALID_ARG;
+  if (scaling == MOE_ROTARY_BASE && R > 2) base *= std::pow(factor, (double)R / (R - 2));
+  // the pairs that make `turns` turns over the trained length lie here
+  auto pair_of = [&](double turns) { return R * std::log(original_len / (kCircle * turns)) / (2.0 * std::log(base)); };
+  double first = 0.0, last = 0.0;
+  if (scaling == MOE_ROTARY_PAIRS) {
+    first = std::fmax(0.0, std::floor(pair_of(high)));
+    last = std::fmin(R - 1.0, std::ceil(pair_of(low)));
+  }
+  double f[128];
+  for (int p = 0; p < R / 2; ++p) {
+    f[p] = std::pow(base, -2.0 * p / R);
+    double kept = 1.0;  // how much of the frequency is not divided by the factor
+    if (scaling == MOE_ROTARY_LINEAR) {
+      kept = 0.0;
+    } else if (scaling == MOE_ROTARY_TURNS) {
+      kept = (original_len * f[p] / kCircle - low) / (high - low);
+    } else if (scaling == MOE_ROTARY_PAIRS) {
+      kept = p <= first ? 1.0 : p >= last ? 0.0 : (last - p) / (last - first);
+    }
+    kept = kept < 0.0 ? 0.0 : (kept > 1.0 ? 1.0 : kept);
+    f[p] = scaling == MOE_ROTARY_UNSCALED || scaling == MOE_ROTARY_BASE ? f[p] : f[p] * (kept + (1.0 - kept) / factor);
+  }
+  if (magnitude == 0.0) magnitude = scaling == MOE_ROTARY_PAIRS ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return moe_rotary_set(r, D, R, layout, f, magnitude);
+}
+
+moe_status moe_rotary_apply(const moe_rotary* r, const void* q, int64_t q_stride, int H, const void* k, int64_t k_stride,
+                            int H_kv, const int32_t* positions, int T, moe_dtype dt, const void* q_weight,
+                            const void* k_weight, float eps, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, void* stream) {
+  if (!rotary_ok(r) || !dtype_ok(dt) || T < 0 || H < 1 || H > 65535 || H_kv < 0 || H_kv > 65535 || !eps_ok(eps))
+    return MOE_ERR_INVALID_ARG;
+  const long long inner = (long long)H * r->D, inner_kv = (long long)H_kv * r->D;
+  if (!stride_ok(q_stride, inner, dt) || !stride_ok(q_out_stride, inner, dt)) return MOE_ERR_INVALID_ARG;
+  if (H_kv > 0 && (!stride_ok(k_stride, inner_kv, dt) || !stride_ok(k_out_stride, inner_kv, dt))) return MOE_ERR_INVALID_ARG;
+  if (H_kv == 0 && (k != nullptr || k_out != nullptr || k_weight != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (q == nullptr || q_out == nullptr || positions == nullptr || !aligned16(q) || !aligned16(q_out)) return MOE_ERR_INVALID_ARG;
+  if (H_kv > 0 && (k == nullptr || k_out == nullptr || !aligned16(k) || !aligned16(k_out))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return MOE_ERR_INVALID_ARG;
+  RotaryArgs a{};
+  a.rot = *r;
+  a.q = q; a.k = k; a.qs = q_stride; a.ks = k_stride;
+  a.qw = q_weight; a.kw = k_weight; a.eps = eps;
+  a.qo = q_out; a.ko = k_out; a.qos = q_out_stride; a.kos = k_out_stride;
+  a.positions = positions;
+  a.T = T; a.H = H; a.Hkv = H_kv; a.D = r->D;
+  return cuda_status(launch_rotary(a, dt, (cudaStream_t)stream));
+}
+
+moe_status moe_cache_append(const moe_kv_cache* cache, int layer, const int32_t* slots, const int32_t* offsets,
+                            const int32_t* pos, int n, int total, const moe_rotary* r, const void* k_new, const void* v_new,
+                            int64_t k_stride, int64_t v_stride, const void* k_weight, const void* q, int64_t q_stride, int H,
+                            const void* q_weight, float eps, void* q_out, int64_t q_out_stride, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  if (!cache_call_ok(cache, workspace, ws_bytes) || layer < 0 || layer >= cache->n_layers) return MOE_ERR_INVALID_ARG;
+  if (n < 0 || n > cache->n_slots || total < 0 || (total > 0 && n == 0) || !eps_ok(eps)) return MOE_ERR_INVALID_ARG;
+  if (r != nullptr && (!rotary_ok(r) || r->D != cache->D)) return MOE_ERR_INVALID_ARG;
+  const long long inner = (long long)cache->H_kv * cache->D, inner_q = (long long)H * cache->D;
+  if (!stride_ok(k_stride, inner, cache->dt) || !stride_ok(v_stride, inner, cache->dt)) return MOE_ERR_INVALID_ARG;
+  if (H < 0 || H > 65535 || (H == 0 && (q != nullptr || q_out != nullptr || q_weight != nullptr))) return MOE_ERR_INVALID_ARG;
+  if (H > 0 && (!stride_ok(q_stride, inner_q, cache->dt) || !stride_ok(q_out_stride, inner_q, cache->dt)))
+    return MOE_ERR_INVALID_ARG;
+  if (total == 0) return MOE_OK;
+  if (slots == nullptr || offsets == nullptr || pos == nullptr || k_new == nullptr || v_new == nullptr ||
+      !aligned16(k_new) || !aligned16(v_new))
+    return MOE_ERR_INVALID_ARG;
+  if (H > 0 && (q == nullptr || q_out == nullptr || !aligned16(q) || !aligned16(q_out))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return MOE_ERR_INVALID_ARG;
+  RotaryArgs a{};
+  if (r != nullptr) a.rot = *r;
+  a.q = q; a.k = k_new; a.v = v_new; a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
+  a.qw = q_weight; a.kw = k_weight; a.eps = eps;
+  a.qo = q_out; a.qos = q_out_stride;
+  a.T = total; a.H = H; a.Hkv = cache->H_kv; a.D = cache->D;
+  a.c = view_of(cache);
+  const size_t off = (size_t)layer * a.c.layer_elems() * elem_bytes(cache->dt);
+  a.kp = static_cast<uint8_t*>(cache->k) + off;
+  a.vp = static_cast<uint8_t*>(cache->v) + off;
+  a.slots = slots; a.offsets = offsets; a.pos = pos; a.n = n;
+  a.status = static_cast<int*>(workspace);
+  return cuda_status(launch_cache_append(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -35,7 +35,8 @@ __device__ __noinline__ uint32_t replace_row(Unseen& s, const __nv_bfloat16* q, 
 }
 
 // SPLIT: a tile's keys over the CTAs of a cluster. SHARED: the shared positions of a decode call, as in attn_simt.cu.
-template <int DP, bool SPLIT, bool SHARED>
+// PAGED: a chunk's rows over its slots' positions in the cache, in blockIdx.z pieces where there are several.
+template <int DP, bool SPLIT, bool SHARED, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ SharedPart sp) {
   constexpr int NU = DP / 8;  // 16-byte pieces of a row
@@ -46,7 +47,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   const DecodeArgs& da = sp.d;
   const int H = SHARED ? da.H : a.H, Hkv = SHARED ? da.c.Hkv : a.Hkv, D = SHARED ? da.c.D : a.D;
   const int G = H / Hkv, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int row0, nrows, j_begin, j_end, tile_end = 0;
+  int row0, nrows, j_begin, j_end, tile_end = 0, seq = 0;
   Seq sq{0, 0, 0, 0};
   const int32_t* pages = nullptr;
   if (SHARED) {
@@ -58,27 +59,31 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
     const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
-    const int seq = find_tile_seq(a.qo, a.n, G, kRows, slot);
-    sq = load_seq(a, seq);
+    seq = find_tile_seq(a.qo, a.n, G, kRows, slot);
+    sq = PAGED ? load_chunk_seq(a, da, seq) : load_seq(a, seq);
     const long long r0 = ((long long)slot - ((long long)sq.q0 * G / kRows + seq)) * kRows;
     if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
     row0 = (int)r0;
     nrows = min(kRows, sq.nq * G - row0);
     j_begin = 0;
     j_end = tile_end = visible_keys((row0 + nrows - 1) / G, sq.nq, sq.nk, a.causal);
-    if (SPLIT) {
+    if (PAGED) pages = da.c.table + (long long)sq.k0 * da.c.width;
+    if (SPLIT || PAGED) {
       const int keys = tile_end, per = ((keys - 1) / KT / (int)gridDim.z + 1) * KT;
       j_begin = (int)min((long long)keys, (long long)blockIdx.z * per);
       j_end = (int)min((long long)keys, (long long)j_begin + per);
     }
   }
-  const __nv_bfloat16 *qb = (const __nv_bfloat16*)(SHARED ? da.q : a.q), *kb = (const __nv_bfloat16*)(SHARED ? da.k : a.k),
-                      *vb = (const __nv_bfloat16*)(SHARED ? da.v : a.v);
+  const __nv_bfloat16 *qb = (const __nv_bfloat16*)(SHARED ? da.q : a.q), *kb = (const __nv_bfloat16*)(SHARED || PAGED ? da.k : a.k),
+                      *vb = (const __nv_bfloat16*)(SHARED || PAGED ? da.v : a.v);
   const long long qs = SHARED ? da.qs : a.qs;
   // where position j of the keys lies
   auto paged = [&](int j) {
     int page = pages[j >> da.c.page_shift];
-    page = page < 0 || page >= da.c.n_pages ? 0 : page;
+    if (page < 0 || page >= da.c.n_pages) {
+      if (PAGED) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
+      page = 0;
+    }
     return (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D;
   };
 
@@ -90,7 +95,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
 #pragma unroll 4
     for (int i = tid; i < KT * NU; i += kThreads) {
       const int r = i / NU, u = i % NU, j = j0 + min(r, left - 1);
-      const long long at = SHARED ? paged(j) : (long long)(sq.k0 + j) * stride + (long long)hk * D;
+      const long long at = SHARED || PAGED ? paged(j) : (long long)(sq.k0 + j) * stride + (long long)hk * D;
       copy(dst + piece<DP>(r, u), base + at + min(u * 8, D - 8), r < left && u * 8 < D);
     }
   };
@@ -203,12 +208,13 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   auto replace = [&](int R, float mr, float lr) {  // in row R of the tile, by a warp
     const int P = row0 + R, tok = P / G, h = hk * G + P % G;
     float x[8];
+    const long long k0 = PAGED ? 0 : (long long)sq.k0 * a.ks + (long long)hk * D;
+    const long long v0 = PAGED ? 0 : (long long)sq.k0 * a.vs + (long long)hk * D;
     const uint32_t cols = replace_row(
-        unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + (long long)sq.k0 * a.ks + (long long)hk * D,
-        vb + (long long)sq.k0 * a.vs + (long long)hk * D,
+        unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + k0, vb + v0,
         [&](int j, long long& ko, long long& vo) {
-          ko = j * a.ks;
-          vo = j * a.vs;
+          ko = PAGED ? paged(j) : j * a.ks;
+          vo = PAGED ? ko : j * a.vs;
         },
         D, visible_keys(tok, sq.nq, sq.nk, a.causal), c2, mr == -INFINITY ? 0.f : mr * c2, x);
     const float inv = lr == 0.f ? 0.f : 1.0f / lr;
@@ -225,12 +231,14 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
   }
-  if (SHARED) {
+  if (SHARED || (PAGED && gridDim.z > 1)) {
+    // the row's piece
+    auto part = [&](int P) { return da.part + (((long long)(sq.q0 + P / G) * H + hk * G + P % G) * sp.pieces + blockIdx.z) * (D + 2); };
     uint32_t again[2];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       const int r = warp * 16 + g + 8 * y, P = row0 + min(r, nrows - 1);
-      float* po = da.part + (((long long)(P / G) * H + hk * G + P % G) * sp.pieces + blockIdx.z) * (D + 2);
+      float* po = part(P);
       bool fine = true;
 #pragma unroll
       for (int n = 0; n < DP / 8; ++n) {
@@ -251,10 +259,11 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       const float mr = row_m(r);
       const int j0 = j_begin;  // (the keys counted from the piece's first)
       const uint32_t cols = replace_row(
-          pieces_unseen, qb + (long long)tok * qs + (long long)h * D, kb, vb,
+          pieces_unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb, vb,
           [&](int j, long long& ko, long long& vo) { ko = vo = paged(j0 + j); }, D,
-          max(0, min(j_end, slot_len(da.c, da.slots[tok])) - j0), c2, mr == -INFINITY ? 0.f : mr * c2, x);
-      float* po = da.part + (((long long)tok * H + h) * sp.pieces + blockIdx.z) * (D + 2);
+          max(0, min(j_end, PAGED ? visible_keys(tok, sq.nq, sq.nk, a.causal) : slot_len(da.c, da.slots[tok])) - j0), c2,
+          mr == -INFINITY ? 0.f : mr * c2, x);
+      float* po = part(P);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (cols >> e & 1u) po[lane * 8 + e] = x[e];
@@ -357,9 +366,9 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   }
 }
 
-template <int DP, bool SPLIT, bool SHARED>
+template <int DP, bool SPLIT, bool SHARED, bool PAGED = false>
 cudaError_t launch(const PromptArgs& a, const SharedPart& sp, dim3 grid, cudaStream_t s) {
-  auto kern = attn_mma_kernel<DP, SPLIT, SHARED>;
+  auto kern = attn_mma_kernel<DP, SPLIT, SHARED, PAGED>;
   static std::atomic<int> done{0};
   const cudaError_t e = allow_smem(kern, mma_smem<DP>(), done);
   if (e != cudaSuccess) return e;
@@ -379,6 +388,10 @@ cudaError_t launch_attn_prompt_mma(const PromptArgs& a, cudaStream_t s) {
   const SharedPart none{};
   if (a.D <= 192) return C > 1 ? launch<192, true, false>(a, none, grid, s) : launch<192, false, false>(a, none, grid, s);
   return C > 1 ? launch<256, true, false>(a, none, grid, s) : launch<256, false, false>(a, none, grid, s);
+}
+
+cudaError_t launch_attn_chunk_mma(const PromptArgs& a, const SharedPart& sp, dim3 grid, cudaStream_t s) {
+  return a.D <= 192 ? launch<192, false, false, true>(a, sp, grid, s) : launch<256, false, false, true>(a, sp, grid, s);
 }
 
 cudaError_t launch_attn_shared_mma(const SharedPart& sp, dim3 grid, cudaStream_t s) {

@@ -55,7 +55,8 @@ constexpr size_t tile_smem(int DP) { return sizeof(float) * ((size_t)(kRows + KT
 
 // SHARED: rows and keys of a decode call, in pieces. SPLIT: a tile's keys over a cluster (in a kernel without it the
 // code for it would cost registers and 3% of the time).
-template <int DP, bool SHARED, bool SPLIT>
+// PAGED: a chunk's rows over its slots' positions in the cache, in blockIdx.z pieces where there are several.
+template <int DP, bool SHARED, bool SPLIT, bool PAGED>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ SharedPart sp) {
   constexpr int NC = DP / (4 * TX);  // groups of 4 columns of a thread
@@ -72,7 +73,7 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
   float* Vs = Ks + tile_keys(DP);
 
   // ---- which rows, which keys
-  int row0, nrows, j_begin, j_end;
+  int row0, nrows, j_begin, j_end, seq = 0;
   Seq sq{0, 0, 0, 0};
   const int32_t* pages = nullptr;
   if (SHARED) {
@@ -84,8 +85,9 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
     const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
-    const int seq = find_tile_seq(pa.qo, pa.n, G, kRows, slot);
-    sq = load_seq(pa, seq);
+    seq = find_tile_seq(pa.qo, pa.n, G, kRows, slot);
+    sq = PAGED ? load_chunk_seq(pa, da, seq) : load_seq(pa, seq);
+    if (PAGED) pages = da.c.table + (long long)sq.k0 * da.c.width;
     const long long first = (long long)sq.q0 * G / kRows + seq;
     const long long r0 = ((long long)slot - first) * kRows;
     if (r0 < 0 || r0 >= (long long)sq.nq * G) return;
@@ -123,8 +125,8 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     for (int c = 0; c < NC; ++c) o[r][c][0] = o[r][c][1] = 0ull;
   }
 
-  const float* kb = (const float*)(SHARED ? da.k : pa.k);
-  const float* vb = (const float*)(SHARED ? da.v : pa.v);
+  const float* kb = (const float*)(SHARED || PAGED ? da.k : pa.k);
+  const float* vb = (const float*)(SHARED || PAGED ? da.v : pa.v);
   // (what is left counts down: positions near 2^31 must not wrap)
   for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
     __syncthreads();
@@ -132,13 +134,16 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     for (int half = 0; half < 2; ++half) {  // K, then V
       float* dst = half ? Vs : Ks;
       const float* src = half ? vb : kb;
-      const long long stride = SHARED ? 0 : (half ? pa.vs : pa.ks);
+      const long long stride = SHARED || PAGED ? 0 : (half ? pa.vs : pa.ks);
       for (int i = tid; i < KT * d4; i += kThreads) {
         const int r = i / d4, c = (i % d4) * 4, j = j0 + min(r, left - 1), ce = min(c, D - 4);
         long long at;
-        if (SHARED) {
+        if (SHARED || PAGED) {
           int page = pages[j >> da.c.page_shift];
-          page = page < 0 || page >= da.c.n_pages ? 0 : page;
+          if (page < 0 || page >= da.c.n_pages) {
+            if (PAGED) record_error(pa.status, MOE_ERR_DEVICE_CHECK, seq);
+            page = 0;
+          }
           at = (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D + ce;
         } else {
           at = (long long)(sq.k0 + j) * stride + (long long)hk * D + ce;
@@ -312,7 +317,7 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     const int R = ty * RPT + r;
     if (R >= nrows) continue;
     const int P = row0 + R, tok = sq.q0 + P / G, h = hk * G + P % G;
-    if (SHARED) {
+    if (SHARED || (PAGED && gridDim.z > 1)) {
       float* po = da.part + (((long long)tok * H + h) * sp.pieces + blockIdx.z) * (D + 2);
       if (tx == 0) *reinterpret_cast<float2*>(po + D) = make_float2(m[r], l[r]);
 #pragma unroll
@@ -623,22 +628,82 @@ decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
   if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int DP, bool SHARED, bool SPLIT>
+// A chunk's rows, whose keys were taken in `pieces` parts: a warp a row, the parts in their order. A lane holds elements
+// 4 lane + 128 x. A row of no sequence (or of one with bad offsets) stays as it is.
+template <typename T>
+__global__ void __launch_bounds__(128)
+chunk_rows_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ DecodeArgs d, int pieces) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, D = a.D;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (long long)a.Tq * a.H) return;
+  const int tok = (int)(row / a.H), h = (int)(row % a.H);
+  const Seq sq = load_chunk_seq(a, d, find_tile_seq_warp(a.qo, a.n, 1, 1, tok, 0));
+  if (tok < sq.q0 || tok >= sq.q0 + sq.nq) return;
+  const float* p = d.part + row * pieces * (D + 2);
+  auto ml = [&](int i) { return *reinterpret_cast<const float2*>(p + (long long)i * (D + 2) + D); };
+  float M = -INFINITY, l = 0.f;
+  for (int i = lane; i < pieces; i += 32) M = fmaxf(M, ml(i).x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float2 o[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) o[x] = make_float2(0.f, 0.f);
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
+    const float2 v = i0 + lane < pieces ? ml(i0 + lane) : make_float2(-INFINITY, 0.f);
+    const float wl = v.y == 0.f ? 0.f : ex2(v.x - ref);
+    l += wl * v.y;
+    for (int y0 = 0; y0 < 32 && i0 + y0 < pieces; y0 += 4) {
+      float2 u[4][4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          u[y][x] = i0 + y0 + y < pieces && 2 * lane + 64 * x < D
+                        ? *reinterpret_cast<const float2*>(p + (long long)(i0 + y0 + y) * (D + 2) + 2 * lane + 64 * x)
+                        : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float w = __shfl_sync(0xffffffffu, wl, y0 + y);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          o[x].x = fmaf(w, u[y][x].x, o[x].x);
+          o[x].y = fmaf(w, u[y][x].y, o[x].y);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  T* dst = (T*)a.out + (long long)tok * a.os + (long long)h * D;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (2 * lane + 64 * x < D) {
+      store_result<T>(dst + 2 * lane + 64 * x, o[x].x * inv);
+      store_result<T>(dst + 2 * lane + 64 * x + 1, o[x].y * inv);
+    }
+  if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int DP, bool SHARED, bool SPLIT, bool PAGED>
 cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, dim3 grid, cudaStream_t s) {
-  auto kern = attn_tile_kernel<DP, SHARED, SPLIT>;
+  auto kern = attn_tile_kernel<DP, SHARED, SPLIT, PAGED>;
   static std::atomic<int> done{0};
   const cudaError_t e = allow_smem(kern, tile_smem(DP), done);
   if (e != cudaSuccess) return e;
   if (!SPLIT) return launch_pdl(kern, grid, dim3(kThreads), tile_smem(DP), s, pa, sp);
   return launch_clusters(kern, grid, dim3(kThreads), dim3(1, 1, grid.z), tile_smem(DP), s, pa, sp);
 }
-template <bool SHARED, bool SPLIT>
+template <bool SHARED, bool SPLIT, bool PAGED = false>
 cudaError_t launch_tiles(const PromptArgs& pa, const SharedPart& sp, int D, dim3 grid, cudaStream_t s) {
-  if (D <= 64) return launch_tiles<64, SHARED, SPLIT>(pa, sp, grid, s);
-  if (D <= 96) return launch_tiles<96, SHARED, SPLIT>(pa, sp, grid, s);
-  if (D <= 128) return launch_tiles<128, SHARED, SPLIT>(pa, sp, grid, s);
-  return D <= 192 ? launch_tiles<192, SHARED, SPLIT>(pa, sp, grid, s)
-                  : launch_tiles<256, SHARED, SPLIT>(pa, sp, grid, s);
+  if (D <= 64) return launch_tiles<64, SHARED, SPLIT, PAGED>(pa, sp, grid, s);
+  if (D <= 96) return launch_tiles<96, SHARED, SPLIT, PAGED>(pa, sp, grid, s);
+  if (D <= 128) return launch_tiles<128, SHARED, SPLIT, PAGED>(pa, sp, grid, s);
+  return D <= 192 ? launch_tiles<192, SHARED, SPLIT, PAGED>(pa, sp, grid, s)
+                  : launch_tiles<256, SHARED, SPLIT, PAGED>(pa, sp, grid, s);
 }
 
 template <typename T, int V4, int GR>
@@ -669,6 +734,30 @@ cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
   while (C < kMaxCluster && slots * a.Hkv * 2 * C <= 2LL * device_sm_count() && a.Tkv >= 4 * C * KT) C *= 2;
   const dim3 grid((unsigned)slots, (unsigned)a.Hkv, (unsigned)C);
   return C > 1 ? launch_tiles<false, true>(a, none, a.D, grid, s) : launch_tiles<false, false>(a, none, a.D, grid, s);
+}
+
+// Few tiles: a row's keys in pieces, about 8 CTAs an SM altogether, at least two tiles of keys each at the longest
+// length that the cache may hold.
+int chunk_tile_pieces(const CacheView& c, int n, int Tq, int H) {
+  const long long ctas = prompt_tile_slots(Tq, n, H / c.Hkv, kRows) * c.Hkv, rows = (long long)Tq * H;
+  const long long most = (long long)c.width * c.page_size / (2 * KT), fit = rows > 0 ? decode_pieces(rows) / rows : 1;
+  long long p = 8LL * device_sm_count() / (ctas > 0 ? ctas : 1);
+  p = p > most ? most : p;
+  p = p > fit ? fit : p;
+  return (int)(p < 1 ? 1 : p);
+}
+
+cudaError_t launch_attn_chunk_tiles(const PromptArgs& a, const DecodeArgs& d, int pieces, cudaStream_t s) {
+  SharedPart sp{};
+  sp.d = d;
+  sp.pieces = pieces;
+  const dim3 grid((unsigned)prompt_tile_slots(a.Tq, a.n, a.H / a.Hkv, kRows), (unsigned)a.Hkv, (unsigned)pieces);
+  const cudaError_t e = a.dt == MOE_DTYPE_BF16 ? launch_attn_chunk_mma(a, sp, grid, s)
+                                               : launch_tiles<false, false, true>(a, sp, a.D, grid, s);
+  if (e != cudaSuccess || pieces == 1) return e;
+  const dim3 rows((unsigned)(((long long)a.Tq * a.H + 3) / 4));
+  return a.dt == MOE_DTYPE_BF16 ? launch_pdl(chunk_rows_join_kernel<__nv_bfloat16>, rows, dim3(128), 0, s, a, d, pieces)
+                                : launch_pdl(chunk_rows_join_kernel<float>, rows, dim3(128), 0, s, a, d, pieces);
 }
 
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s) {

@@ -56,7 +56,8 @@ struct __align__(16) Item {
   int key0, n_keys;         // keys of the item
   int lim0, lim1;           // keys that each tile's last row sees (relative to key0)
   int last;                 // no item: the end
-  int split;                // which part of the keys
+  int seq;                  // (of a chunk, for errors)
+  int split;                // which part of the keys; of a chunk: the piece that takes the results (-1: the output)
 };
 constexpr int kItems = 3;   // items published: one worked on, one ahead, one being given back
 constexpr int kItemReaders = 1 + 8 + 2;
@@ -66,7 +67,7 @@ template <int DP> struct Cfg {
   static constexpr int kTileBytes = TM * DP * 2;   // a Q tile, and a K or V block
   static constexpr int kStages = DP == 128 ? 4 : 8;
   static constexpr int kStage = 32 * 128;  // bytes of a softmax warp's output staging: 32 rows x 64 bf16 elements
-  static constexpr int kBars = 2 * kStages + 5 * 2 + 1 + 2 * kItems;
+  static constexpr int kBars = 2 * kStages + 5 * 2 + 1 + 2 * kItems + 1;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 + kItems * sizeof(Item);
 };
 static_assert(Cfg<128>::kSmem <= kMaxSmem && Cfg<64>::kSmem <= kMaxSmem, "shared memory");
@@ -115,13 +116,70 @@ struct SharedArgs {
   int splits;     // pieces of a row
   float* part_o;  // [piece][D]
   float2* part_ml;
+  ChunkRun* runs;  // of a chunk call, one a CTA
+  int piece_rows;  // and the rows of a piece
+};
+
+// ------------------------------------------------------------------ chunks over the paged cache
+// How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head; the items lie in a
+// row (heads outside, tile slots inside), each as long as its cost: kOneTile or kTwoTiles a block of keys, and kItem for
+// Q, the first scores and the results. The row is cut into equally long runs, one a CTA, whatever items the
+// cuts fall into: a decoding sequence of 100,000 keys beside a hundred short ones then takes as many CTAs as it needs.
+// A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
+// several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order. A
+// run has at most two such items, its first and its last, so that 2 pieces a CTA are enough however long the keys.
+constexpr int kOneTile = 2, kTwoTiles = 3, kItem = 3, kShortest = 12;
+
+struct ChunkItem {
+  int seq, row0, nrows, q0, nq, nk, slot;
+  int lim0, lim1, n_blocks;
+  int cost;  // of a block
+  __device__ __forceinline__ long long length() const { return nrows > 0 ? kItem + (long long)n_blocks * cost : 0; }
+};
+// What fills tile slot s (nrows = 0: nothing).
+__device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const SharedArgs& sa, int s, int i) {
+  const int G = pa.H / pa.Hkv;
+  ChunkItem it{};
+  it.seq = i;
+  const int q0 = pa.qo[i], q1 = pa.qo[i + 1];
+  it.slot = sa.d.slots[i];
+  if (q0 < 0 || q1 < q0 || q1 > pa.Tq) {
+    record_error(pa.status, MOE_ERR_DEVICE_CHECK, i);
+    return it;
+  }
+  it.q0 = q0;
+  it.nq = q1 - q0;
+  const long long r0 = ((long long)s - ((long long)q0 * G / (2 * TM) + i)) * (2 * TM);
+  if (r0 < 0 || r0 >= (long long)it.nq * G) return it;
+  it.nk = slot_len(sa.d.c, it.slot);
+  if (it.nk == 0 && (it.slot < 0 || it.slot >= sa.d.c.n_slots || sa.d.c.lens[it.slot] != 0))
+    record_error(pa.status, MOE_ERR_DEVICE_CHECK, i);
+  it.row0 = (int)r0;
+  it.nrows = min(2 * TM, it.nq * G - it.row0);
+  it.lim0 = visible_keys((it.row0 + min(it.nrows, TM) - 1) / G, it.nq, it.nk, pa.causal);
+  it.lim1 = it.nrows > TM ? visible_keys((it.row0 + it.nrows - 1) / G, it.nq, it.nk, pa.causal) : 0;
+  it.n_blocks = (max(it.lim0, it.lim1) + BK - 1) / BK;
+  it.cost = it.nrows > TM ? kTwoTiles : kOneTile;
+  return it;
+}
+// The runs: how many, their beginnings, and the run that place x lies in.
+struct Runs {
+  long long all;
+  int n;
+  __device__ __forceinline__ Runs(long long total, int ctas) : all(total) {
+    const long long most = total / kShortest;
+    n = (int)(most < 1 ? 1 : (most < ctas ? most : ctas));
+  }
+  __device__ __forceinline__ long long begin(int c) const { return all * c / n; }
+  __device__ __forceinline__ int of(long long x) const { return (int)(((x + 1) * n - 1) / all); }
 };
 
 // SHARED = false: items are tile-pair slots (descending, so that the longest rows of a sequence start first) x
 // key/value heads, n_items of them. SHARED = true: one item a CTA, blockIdx = (key/value head, row pair, split of
 // the shared keys); rows are (sequence, head) pairs, and each row's piece goes to the workspace unnormalised. SPLIT
-// (prompts of few rows): every item's keys in sa.splits parts, an item each, and the rows' pieces likewise.
-template <int DP, bool SHARED, bool SPLIT>
+// (prompts of few rows): every item's keys in sa.splits parts, an item each, and the rows' pieces likewise. PAGED: the
+// keys are a cache's, and each CTA takes a run of the items (above), n_items the number of tile slots.
+template <int DP, bool SHARED, bool SPLIT, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs pa,
@@ -139,7 +197,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 2,
-                ODONE = PFULL + 2, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems;
+                ODONE = PFULL + 2, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
+                TAIL = IEMPTY + kItems;
 
   // (the shuffle tells the compiler that the warp number is the same in all lanes)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -154,6 +213,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
     for (int i = 0; i < kItems; ++i) { mbar_init(bar(IFULL + i), 1); mbar_init(bar(IEMPTY + i), kItemReaders); }
     mbar_init(bar(DONE), 1);
+    mbar_init(bar(TAIL), 1);
     fence_mbar_init();
     *abort_flag = 0;
     if (q_tma) tma_prefetch_desc(&tmQ);
@@ -192,6 +252,54 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   };
   auto blocks = [](int keys) { return (keys + BK - 1) / BK; };
 
+  // This CTA's run: a scan over the lengths of all tile slots, each thread with some of them in a row. The results stay
+  // in the output staging until the first item is published.
+  long long* plan = reinterpret_cast<long long*>(gbase + (2 + C::kStages) * C::kTileBytes);
+  if (PAGED) {
+    const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
+    auto item = [&](int s) { return chunk_item(pa, sa, s, find_tile_seq(pa.qo, pa.n, G, 2 * TM, s)); };
+    long long sum = 0;
+    for (int s = s0; s < s1; ++s) sum += item(s).length();
+    long long upto = sum;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, w);
+      if (lane >= w) upto += x;
+    }
+    if (lane == 31) plan[4 + warp] = upto;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) upto += total;
+      total += plan[4 + w];
+    }
+    if (total > 0) {
+      const Runs runs(total * pa.Hkv, gridDim.x);
+      if ((int)blockIdx.x < runs.n) {
+        const long long begin = runs.begin(blockIdx.x), at = begin % total;
+        if (at >= upto - sum && at < upto) {  // one thread
+          long long x = upto - sum;
+          int s = s0;
+          for (long long len = item(s).length(); x + len <= at; len = item(s).length()) {
+            x += len;
+            ++s;
+          }
+          plan[1] = s;
+          plan[2] = begin - at + x;  // where item (head, slot s) begins
+          plan[3] = begin / total;   // the head
+        }
+      }
+    }
+    if (tid == 0) {
+      plan[0] = total;
+      ChunkRun none;
+      none.nrows = 0;
+      sa.runs[blockIdx.x] = none;
+    }
+    __syncthreads();
+  }
+
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kSoftWarps + 1) {
@@ -200,6 +308,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       uint32_t phase = 0, filled = 0, fill_phase = 0;
       const int32_t* table = nullptr;
       int pages = 0;
+      // PAGED: the run's place, and the pages of 32 x page_size positions from table column 32 `window` on and of the
+      // next ones, a page a lane
+      const Runs runs(PAGED ? plan[0] * Hkv : 0, gridDim.x);
+      long long x = PAGED ? plan[2] : 0;
+      int at_slot = PAGED ? (int)plan[1] : 0, at_head = PAGED ? (int)plan[3] : 0;
+      int window_slot = -1, window = 0, page_now = 0, page_next = 0;
+      const bool idle = PAGED && (plan[0] == 0 || (int)blockIdx.x >= runs.n);
+      const long long run_begin = idle ? 0 : runs.begin(blockIdx.x), run_end = idle ? 0 : runs.begin(blockIdx.x + 1);
+      bool tail = false;  // the last block of values loaded needs its end cleared
+      int tail_stage = 0, tail_keys = 0;
+      uint32_t tail_phase = 0;
       if (SHARED) {
         int slot = sa.d.lead[0];  // an out-of-range slot or page is recorded by the own part
         slot = slot < 0 || slot >= sa.d.c.n_slots ? 0 : slot;
@@ -208,7 +327,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       int* counter = status + 7;  // items taken; status[8]: CTAs that are done with it
       auto take = [&]() { return lane == 0 ? atomicAdd(counter, 1) : 0; };
-      int ahead = SHARED ? 0 : take();  // the next item's number (lane 0), asked for early
+      int ahead = SHARED || PAGED ? 0 : take();  // the next item's number (lane 0), asked for early
       // The next item with rows, by the whole warp (last: none).
       auto find = [&](Item& it) {
         it = Item{};
@@ -223,6 +342,45 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             it.lim0 = it.n_keys;
             it.lim1 = it.nrows > TM ? it.n_keys : 0;
             it.last = 0;
+          }
+          return;
+        }
+        if (PAGED) {
+          while (!idle && x < run_end) {
+            const ChunkItem ci = chunk_item(pa, sa, at_slot, find_tile_seq_warp(pa.qo, pa.n, G, 2 * TM, at_slot));
+            const long long begin = x;
+            const int head = at_head;
+            x += ci.length();
+            if (++at_slot == n_items) {
+              at_slot = 0;
+              ++at_head;
+            }
+            if (ci.nrows == 0) continue;  // a slot that no tile fills
+            // the blocks whose beginnings lie in the run: block j at begin + j cost
+            const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
+            auto first_from = [&](long long p) {
+              return p <= begin ? 0 : (int)min((long long)all, (p - begin + ci.cost - 1) / ci.cost);
+            };
+            const int b0 = first_from(run_begin), b1 = first_from(run_end);
+            if (b0 >= b1) continue;
+            it.hk = head;
+            it.seq = ci.seq;
+            it.row0 = ci.row0;
+            it.nrows = ci.nrows;
+            it.q0 = ci.q0; it.nq = ci.nq; it.k0 = ci.slot; it.nk = ci.nk;
+            it.key0 = b0 * BK;
+            it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
+            it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
+            it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
+            it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
+            it.last = 0;
+            if (b0 == 0 && b1 < all && lane == 0) {
+              ChunkRun r;
+              r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
+              r.end = runs.of(begin + (long long)(all - 1) * ci.cost);
+              sa.runs[blockIdx.x] = r;
+            }
+            return;
           }
           return;
         }
@@ -255,7 +413,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           return;
         }
       };
+      // What pages hold past a sequence's end is anyone's: the last block's values there become zeros once they
+      // have arrived, as 0 times a leftover that is not finite would be NaN. This is done when the next item's first copies
+      // are on their way (they need no stage that waits for it).
+      auto clear_tail = [&]() {
+        if (!PAGED || !tail) return true;
+        if (!warp_wait(bar(TAIL), tail_phase, timeout_ns, abort_flag, status, 51)) return false;
+        tail = false;
+        tail_phase ^= 1u;
+        const uint32_t dst = sKV + tail_stage * C::kTileBytes;
+        for (int i = lane; i < (BK - tail_keys) * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + c * (BK * 128) + tail_keys * 128 + i * 16), "r"(0)
+                         : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(FULL + tail_stage));
+        return true;
+      };
       auto publish = [&](const Item& it) {
+        if (!clear_tail()) return false;
         bool ok = true;
         if (lane == 0) {
           ok = wait_or_abort(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51);
@@ -270,6 +448,53 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // copies u = begin .. end - 1 of an item (K and V of block u / 2)
       auto load = [&](const Item& it, int begin, int end) {
         bool ok = true;
+        if (PAGED) {
+          const CacheView& cv = sa.d.c;
+          const int32_t* row = cv.table + (long long)it.k0 * cv.width;
+          const int box = min(cv.page_size, BK), box_shift = min(cv.page_shift, 7);
+          for (int u = begin; u < end && ok; ++u) {
+            const int j0 = it.key0 + (u >> 1) * BK, held = min(BK, it.nk - j0);
+            const bool cut = (u & 1) && held < BK;
+            if ((u >= begin + 2 || cut) && !clear_tail()) return false;
+            // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
+            const int col = j0 >> cv.page_shift;
+            if (window_slot != it.k0 || window != col >> 5) {
+              auto read = [&](int w) { return (long long)w * 32 + lane < cv.width ? row[w * 32 + lane] : 0; };
+              page_now = window_slot == it.k0 && window + 1 == col >> 5 ? page_next : read(col >> 5);
+              window_slot = it.k0;
+              window = col >> 5;
+              page_next = read(window + 1);
+            }
+            int page = __shfl_sync(0xffffffffu, page_now, (col + lane) & 31);
+            const bool mine = lane << box_shift < held;  // a copy a lane
+            if (page < 0 || page >= cv.n_pages) {
+              if (mine) record_error(status, MOE_ERR_DEVICE_CHECK, it.seq);
+              page = 0;
+            }
+            if (lane == 0) ok = wait_or_abort(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!ok) break;
+            const uint32_t dst = sKV + stage * C::kTileBytes, b = cut ? bar(TAIL) : bar(FULL + stage);
+            if (lane == 0)
+              mbar_arrive_expect_tx(b, (uint32_t)(((held + box - 1) >> box_shift << box_shift) * C::kChunks * 128));
+            __syncwarp();
+            if (mine) {
+              const int g = (page * Hkv + it.hk) * cv.page_size + (j0 & (cv.page_size - 1));
+#pragma unroll
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(dst + c * (BK * 128) + (lane << box_shift) * 128, (u & 1) ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
+            }
+            if (cut) {
+              tail = true;
+              tail_stage = stage;
+              tail_keys = held;
+            }
+            filled |= 1u << stage;
+            fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+          }
+          return ok;
+        }
         if (lane == 0) {
           for (int u = begin; u < end; ++u) {
             const CUtensorMap* tm = (u & 1) ? &tmV : &tmK;
@@ -315,8 +540,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         ok = ok && publish(nx) && load(it, first, end);
         it = nx;
       }
+      if (PAGED && !clear_tail() && lane == 0) {  // (given up: the copies are waited for all the same)
+        mbar_wait_bounded(bar(TAIL), tail_phase, timeout_ns);
+        mbar_arrive(bar(FULL + tail_stage));
+      }
       if (lane == 0) {
-        if (!SHARED) {  // the CTA that is done last sets the counters back: nobody takes items any more
+        if (!SHARED && !PAGED) {  // the CTA that is done last sets the counters back: nobody takes items any more
           __threadfence();
           if (atomicAdd(counter + 1, 1) == (int)gridDim.x - 1) {
             atomicExch(counter, 0);
@@ -506,7 +735,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         lim = max(0, min(it->n_keys, slot_len(sa.d.c, sa.d.slots[tok]) - it->key0));
       } else if (valid) {
         lim = visible_keys(tok, it->nq, it->nk, pa.causal);
-        if (SPLIT) lim = max(0, min(lim - it->key0, it->n_keys));
+        if (SPLIT || PAGED) lim = max(0, min(lim - it->key0, it->n_keys));
       }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++done) {
@@ -600,9 +829,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc_fence_after();
       }
       if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-        if (SHARED || SPLIT) {
+        // where a chunk's keys lie: key j of the item
+        const int32_t* row = PAGED ? sa.d.c.table + (long long)it->k0 * sa.d.c.width : nullptr;
+        auto paged = [&](int j, long long& ko, long long& vo) {
+          const CacheView& cv = sa.d.c;
+          const int p = it->key0 + j;
+          int page = row[p >> cv.page_shift];
+          page = page < 0 || page >= cv.n_pages ? 0 : page;
+          ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
+        };
+        if (SHARED || SPLIT || (PAGED && it->split >= 0)) {
           const long long piece = SHARED ? ((long long)tok * H + h) * sa.splits + blockIdx.z
-                                         : ((long long)(it->q0 + tok) * H + h) * sa.splits + it->split;
+                                  : PAGED ? (long long)it->split * sa.piece_rows + t * TM + r
+                                          : ((long long)(it->q0 + tok) * H + h) * sa.splits + it->split;
           const float* orow = sa.part_o + piece * D;
           const uint32_t stg = sOut + warp * C::kStage;  // 32 elements a step through shared memory, as below
           bool fine = true;
@@ -638,7 +877,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (valid) sa.part_ml[piece] = make_float2(m * c2, l);
           // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
           uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && fabsf(l) <= 3.0e38f);
-          Unseen unseen(SHARED ? n * BK : min(n * BK, pa.Tkv - it->k0 - it->key0));
+          Unseen unseen(SHARED ? n * BK : PAGED ? min(n * BK, it->nk - it->key0) : min(n * BK, pa.Tkv - it->k0 - it->key0));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
@@ -648,7 +887,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             float o[8];
             long long pw;
             uint32_t cols;
-            if (SPLIT) {
+            if (PAGED) {
+              pw = (long long)it->split * sa.piece_rows + t * TM + 32 * q4 + w;
+              cols = replace_unseen(unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                                    (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v, paged, D, limw, c2, mcw, o);
+            } else if (SPLIT) {
               pw = ((long long)(it->q0 + tw) * H + hw) * sa.splits + it->split;
               cols = replace_unseen(unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
                                     (const __nv_bfloat16*)pa.k + (long long)(it->k0 + it->key0) * pa.ks + (long long)it->hk * D,
@@ -729,23 +972,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             pa.lse[(long long)(it->q0 + tok) * H + h] = lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
           // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
           uint32_t again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
-          Unseen unseen(min(n * BK, pa.Tkv - it->k0));
+          Unseen unseen(min(n * BK, PAGED ? it->nk : pa.Tkv - it->k0));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
             const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
             const int limw = __shfl_sync(0xffffffffu, lim, w);
             const float mw = __shfl_sync(0xffffffffu, m, w), iw = __shfl_sync(0xffffffffu, inv, w);
+            const __nv_bfloat16* qw = (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D;
+            const float mcw = mw == -INFINITY ? 0.f : mw * c2;
             float o[8];
-            const uint32_t cols = replace_unseen(
-                unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
-                (const __nv_bfloat16*)pa.k + (long long)it->k0 * pa.ks + (long long)it->hk * D,
-                (const __nv_bfloat16*)pa.v + (long long)it->k0 * pa.vs + (long long)it->hk * D,
-                [&](int j, long long& ko, long long& vo) {
-                  ko = (long long)j * pa.ks;
-                  vo = (long long)j * pa.vs;
-                },
-                D, limw, c2, mw == -INFINITY ? 0.f : mw * c2, o);
+            uint32_t cols;
+            if (PAGED) {
+              cols = replace_unseen(unseen, qw, (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v, paged, D, limw, c2,
+                                    mcw, o);
+            } else {
+              cols = replace_unseen(
+                  unseen, qw, (const __nv_bfloat16*)pa.k + (long long)it->k0 * pa.ks + (long long)it->hk * D,
+                  (const __nv_bfloat16*)pa.v + (long long)it->k0 * pa.vs + (long long)it->hk * D,
+                  [&](int j, long long& ko, long long& vo) {
+                    ko = (long long)j * pa.ks;
+                    vo = (long long)j * pa.vs;
+                  },
+                  D, limw, c2, mcw, o);
+            }
             __nv_bfloat16* dw = (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -816,6 +1066,58 @@ prompt_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
   if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
+// The rows that several runs share, by the run that such an item begins in (blockIdx.x): a warp a row, its pieces in
+// their order, eight on their way at a time.
+__global__ void __launch_bounds__(256)
+chunk_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ SharedArgs sa) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), c0 = blockIdx.x;
+  const ChunkRun run = sa.runs[c0];
+  if (r >= run.nrows) return;
+  const int G = a.H / a.Hkv, R = run.row0 + r, tok = run.q0 + R / G, h = run.hk * G + R % G, n = run.end - c0 + 1;
+  // run c0 has its last item's piece, the others their first's
+  auto row = [&](int i) { return (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * sa.piece_rows + r; };
+  float M = -INFINITY, l = 0.f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, sa.part_ml[row(i)].x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  const float ref = M == -INFINITY ? 0.f : M;
+  const bool on = lane * 4 < a.D;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float2 v = i0 + lane < n ? sa.part_ml[row(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    const float wl = ex2(v.x - ref);
+    l += wl * v.y;
+    for (int y0 = 0; y0 < 32 && i0 + y0 < n; y0 += 8) {
+      float4 u[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        u[y] = on && i0 + y0 + y < n ? reinterpret_cast<const float4*>(sa.part_o + row(i0 + y0 + y) * a.D)[lane]
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xffffffffu, wl, y0 + y);
+        o.x = fmaf(w, u[y].x, o.x);
+        o.y = fmaf(w, u[y].y, o.y);
+        o.z = fmaf(w, u[y].z, o.z);
+        o.w = fmaf(w, u[y].w, o.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  if (on) {
+    uint2 u;
+    u.x = pack_bf16x2(o.x * inv, o.y * inv);
+    u.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * a.D + lane * 4) = u;
+  }
+  if (a.lse != nullptr && lane == 0)
+    a.lse[(long long)tok * a.H + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
 bool encode3(EncodeTiledFn enc, CUtensorMap* m, const void* p, int D, int heads, int T, long long stride, int box_heads,
              int box_rows) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
@@ -829,11 +1131,11 @@ bool encode_q(EncodeTiledFn enc, CUtensorMap* m, const void* p, int D, int H, in
   return !*ok || encode3(enc, m, p, D, H, T, stride, G, TM / G);
 }
 
-template <int DP, bool SHARED, bool SPLIT>
+template <int DP, bool SHARED, bool SPLIT, bool PAGED = false>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PromptArgs& pa,
                    const SharedArgs& sa, dim3 grid, int n_items, int q_tma, cudaStream_t s) {
   static std::atomic<int> done{0};
-  auto kern = attn_tc_kernel<DP, SHARED, SPLIT>;
+  auto kern = attn_tc_kernel<DP, SHARED, SPLIT, PAGED>;
   const cudaError_t e = allow_smem(kern, Cfg<DP>::kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), Cfg<DP>::kSmem, s, tq, tk, tv, pa, sa, n_items, q_tma);
@@ -906,6 +1208,30 @@ cudaError_t launch_attn_shared_tc(const DecodeArgs& a, const CacheMaps& m, int s
   const dim3 grid((unsigned)a.c.Hkv, (unsigned)pairs, (unsigned)splits);
   return a.c.D <= 64 ? launch<64, true, false>(tq, m.k128, m.v128, none, sa, grid, 0, q_tma, s)
                      : launch<128, true, false>(tq, m.k128, m.v128, none, sa, grid, 0, q_tma, s);
+}
+
+int chunk_piece_rows(int Tq, int G) {
+  return (long long)Tq * G < 2 * TM ? Tq * G : 2 * TM;
+}
+
+cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, ChunkRun* runs, float* part,
+                                 cudaStream_t s) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  CUtensorMap tq{};
+  const int G = a.H / a.Hkv;
+  int q_tma = 0;
+  if (enc == nullptr || !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma)) return cudaErrorInvalidValue;
+  const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM), ctas = device_sm_count();
+  SharedArgs sa{};
+  sa.d = d;
+  sa.runs = runs;
+  sa.piece_rows = chunk_piece_rows(a.Tq, G);
+  sa.part_o = part;
+  sa.part_ml = reinterpret_cast<float2*>(part + 2LL * ctas * sa.piece_rows * a.D);
+  const cudaError_t e = a.D <= 64 ? launch<64, false, false, true>(tq, m.k128, m.v128, a, sa, dim3(ctas), slots, q_tma, s)
+                                  : launch<128, false, false, true>(tq, m.k128, m.v128, a, sa, dim3(ctas), slots, q_tma, s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((sa.piece_rows + 7) / 8)), dim3(256), 0, s, a, sa);
 }
 
 }  // namespace moe
