@@ -302,23 +302,100 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == kSoftWarps + 1) {
+    if (PAGED && warp == kSoftWarps + 1) {
+      // -------------------------------------------------------------- K and V of a chunk's items (warp 10 finds them)
+      int stage = 0;
+      uint32_t phase = 0, filled = 0, fill_phase = 0;
+      // the pages of 32 x page_size positions from table column 32 `window` on and of the next ones, a page a lane
+      int window_slot = -1, window = 0, page_now = 0, page_next = 0;
+      bool tail = false;  // the last block of values loaded needs its end cleared
+      int tail_stage = 0, tail_keys = 0;
+      uint32_t tail_phase = 0;
+      // What pages hold past a sequence's end is anyone's: the last block's values there become zeros once they
+      // have arrived, as 0 times a leftover that is not finite would be NaN. This is done when the next item's first copies
+      // are on their way (they need no stage that waits for it).
+      auto clear_tail = [&]() {
+        if (!tail) return true;
+        if (!warp_wait(bar(TAIL), tail_phase, timeout_ns, abort_flag, status, 51)) return false;
+        tail = false;
+        tail_phase ^= 1u;
+        const uint32_t dst = sKV + tail_stage * C::kTileBytes;
+        for (int i = lane; i < (BK - tail_keys) * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + c * (BK * 128) + tail_keys * 128 + i * 16), "r"(0)
+                         : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(FULL + tail_stage));
+        return true;
+      };
+      const CacheView& cv = sa.d.c;
+      const int box = min(cv.page_size, BK), box_shift = min(cv.page_shift, 7);
+      bool ok = true;
+      while (ok) {
+        if (tail && !__all_sync(0xffffffffu, mbar_try_wait(bar(IFULL + iq), iphase)) && !clear_tail()) break;
+        const Item* ip = next_item();
+        if (ip == nullptr) break;
+        const int key0 = ip->key0, held_all = ip->nk, slot = ip->k0, hk = ip->hk, seq = ip->seq, end = 2 * blocks(ip->n_keys);
+        item_done();
+        const int32_t* row = cv.table + (long long)slot * cv.width;
+        for (int u = 0; u < end && ok; ++u) {
+          const int j0 = key0 + (u >> 1) * BK, held = min(BK, held_all - j0);
+          const bool cut = (u & 1) && held < BK;
+          if ((u >= 2 || cut) && !(ok = clear_tail())) break;
+          // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
+          const int col = j0 >> cv.page_shift;
+          if (window_slot != slot || window != col >> 5) {
+            auto read = [&](int w) { return (long long)w * 32 + lane < cv.width ? row[w * 32 + lane] : 0; };
+            page_now = window_slot == slot && window + 1 == col >> 5 ? page_next : read(col >> 5);
+            window_slot = slot;
+            window = col >> 5;
+            page_next = read(window + 1);
+          }
+          int page = __shfl_sync(0xffffffffu, page_now, (col + lane) & 31);
+          const bool mine = lane << box_shift < held;  // a copy a lane
+          if (page < 0 || page >= cv.n_pages) {
+            if (mine) record_error(status, MOE_ERR_DEVICE_CHECK, seq);
+            page = 0;
+          }
+          if (lane == 0) ok = wait_or_abort(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+          const uint32_t dst = sKV + stage * C::kTileBytes, b = cut ? bar(TAIL) : bar(FULL + stage);
+          if (lane == 0)
+            mbar_arrive_expect_tx(b, (uint32_t)(((held + box - 1) >> box_shift << box_shift) * C::kChunks * 128));
+          __syncwarp();
+          if (mine) {
+            const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(dst + c * (BK * 128) + (lane << box_shift) * 128, (u & 1) ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
+          }
+          if (cut) {
+            tail = true;
+            tail_stage = stage;
+            tail_keys = held;
+          }
+          filled |= 1u << stage;
+          fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!clear_tail() && lane == 0) {  // (given up: the copies are waited for all the same)
+        mbar_wait_bounded(bar(TAIL), tail_phase, timeout_ns);
+        mbar_arrive(bar(FULL + tail_stage));
+      }
+      if (lane == 0)
+        for (int s = 0; s < C::kStages; ++s)
+          if (filled & (1u << s)) mbar_wait_bounded(bar(FULL + s), (fill_phase >> s) & 1u, timeout_ns);
+      __syncwarp();
+    } else if (warp == kSoftWarps + 1) {
       // -------------------------------------------------------------- items, K and V
       int stage = 0;
       uint32_t phase = 0, filled = 0, fill_phase = 0;
       const int32_t* table = nullptr;
       int pages = 0;
-      // PAGED: the run's place, and the pages of 32 x page_size positions from table column 32 `window` on and of the
-      // next ones, a page a lane
-      const Runs runs(PAGED ? plan[0] * Hkv : 0, gridDim.x);
-      long long x = PAGED ? plan[2] : 0;
-      int at_slot = PAGED ? (int)plan[1] : 0, at_head = PAGED ? (int)plan[3] : 0;
-      int window_slot = -1, window = 0, page_now = 0, page_next = 0;
-      const bool idle = PAGED && (plan[0] == 0 || (int)blockIdx.x >= runs.n);
-      const long long run_begin = idle ? 0 : runs.begin(blockIdx.x), run_end = idle ? 0 : runs.begin(blockIdx.x + 1);
-      bool tail = false;  // the last block of values loaded needs its end cleared
-      int tail_stage = 0, tail_keys = 0;
-      uint32_t tail_phase = 0;
       if (SHARED) {
         int slot = sa.d.lead[0];  // an out-of-range slot or page is recorded by the own part
         slot = slot < 0 || slot >= sa.d.c.n_slots ? 0 : slot;
@@ -327,7 +404,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       int* counter = status + 7;  // items taken; status[8]: CTAs that are done with it
       auto take = [&]() { return lane == 0 ? atomicAdd(counter, 1) : 0; };
-      int ahead = SHARED || PAGED ? 0 : take();  // the next item's number (lane 0), asked for early
+      int ahead = SHARED ? 0 : take();  // the next item's number (lane 0), asked for early
       // The next item with rows, by the whole warp (last: none).
       auto find = [&](Item& it) {
         it = Item{};
@@ -342,45 +419,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             it.lim0 = it.n_keys;
             it.lim1 = it.nrows > TM ? it.n_keys : 0;
             it.last = 0;
-          }
-          return;
-        }
-        if (PAGED) {
-          while (!idle && x < run_end) {
-            const ChunkItem ci = chunk_item(pa, sa, at_slot, find_tile_seq_warp(pa.qo, pa.n, G, 2 * TM, at_slot));
-            const long long begin = x;
-            const int head = at_head;
-            x += ci.length();
-            if (++at_slot == n_items) {
-              at_slot = 0;
-              ++at_head;
-            }
-            if (ci.nrows == 0) continue;  // a slot that no tile fills
-            // the blocks whose beginnings lie in the run: block j at begin + j cost
-            const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
-            auto first_from = [&](long long p) {
-              return p <= begin ? 0 : (int)min((long long)all, (p - begin + ci.cost - 1) / ci.cost);
-            };
-            const int b0 = first_from(run_begin), b1 = first_from(run_end);
-            if (b0 >= b1) continue;
-            it.hk = head;
-            it.seq = ci.seq;
-            it.row0 = ci.row0;
-            it.nrows = ci.nrows;
-            it.q0 = ci.q0; it.nq = ci.nq; it.k0 = ci.slot; it.nk = ci.nk;
-            it.key0 = b0 * BK;
-            it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
-            it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
-            it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
-            it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
-            it.last = 0;
-            if (b0 == 0 && b1 < all && lane == 0) {
-              ChunkRun r;
-              r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
-              r.end = runs.of(begin + (long long)(all - 1) * ci.cost);
-              sa.runs[blockIdx.x] = r;
-            }
-            return;
           }
           return;
         }
@@ -413,27 +451,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           return;
         }
       };
-      // What pages hold past a sequence's end is anyone's: the last block's values there become zeros once they
-      // have arrived, as 0 times a leftover that is not finite would be NaN. This is done when the next item's first copies
-      // are on their way (they need no stage that waits for it).
-      auto clear_tail = [&]() {
-        if (!PAGED || !tail) return true;
-        if (!warp_wait(bar(TAIL), tail_phase, timeout_ns, abort_flag, status, 51)) return false;
-        tail = false;
-        tail_phase ^= 1u;
-        const uint32_t dst = sKV + tail_stage * C::kTileBytes;
-        for (int i = lane; i < (BK - tail_keys) * 8; i += 32)
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + c * (BK * 128) + tail_keys * 128 + i * 16), "r"(0)
-                         : "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FULL + tail_stage));
-        return true;
-      };
       auto publish = [&](const Item& it) {
-        if (!clear_tail()) return false;
         bool ok = true;
         if (lane == 0) {
           ok = wait_or_abort(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51);
@@ -448,53 +466,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // copies u = begin .. end - 1 of an item (K and V of block u / 2)
       auto load = [&](const Item& it, int begin, int end) {
         bool ok = true;
-        if (PAGED) {
-          const CacheView& cv = sa.d.c;
-          const int32_t* row = cv.table + (long long)it.k0 * cv.width;
-          const int box = min(cv.page_size, BK), box_shift = min(cv.page_shift, 7);
-          for (int u = begin; u < end && ok; ++u) {
-            const int j0 = it.key0 + (u >> 1) * BK, held = min(BK, it.nk - j0);
-            const bool cut = (u & 1) && held < BK;
-            if ((u >= begin + 2 || cut) && !clear_tail()) return false;
-            // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
-            const int col = j0 >> cv.page_shift;
-            if (window_slot != it.k0 || window != col >> 5) {
-              auto read = [&](int w) { return (long long)w * 32 + lane < cv.width ? row[w * 32 + lane] : 0; };
-              page_now = window_slot == it.k0 && window + 1 == col >> 5 ? page_next : read(col >> 5);
-              window_slot = it.k0;
-              window = col >> 5;
-              page_next = read(window + 1);
-            }
-            int page = __shfl_sync(0xffffffffu, page_now, (col + lane) & 31);
-            const bool mine = lane << box_shift < held;  // a copy a lane
-            if (page < 0 || page >= cv.n_pages) {
-              if (mine) record_error(status, MOE_ERR_DEVICE_CHECK, it.seq);
-              page = 0;
-            }
-            if (lane == 0) ok = wait_or_abort(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-            if (!ok) break;
-            const uint32_t dst = sKV + stage * C::kTileBytes, b = cut ? bar(TAIL) : bar(FULL + stage);
-            if (lane == 0)
-              mbar_arrive_expect_tx(b, (uint32_t)(((held + box - 1) >> box_shift << box_shift) * C::kChunks * 128));
-            __syncwarp();
-            if (mine) {
-              const int g = (page * Hkv + it.hk) * cv.page_size + (j0 & (cv.page_size - 1));
-#pragma unroll
-              for (int c = 0; c < C::kChunks; ++c)
-                tma_load_3d(dst + c * (BK * 128) + (lane << box_shift) * 128, (u & 1) ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
-            }
-            if (cut) {
-              tail = true;
-              tail_stage = stage;
-              tail_keys = held;
-            }
-            filled |= 1u << stage;
-            fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
-            if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-          }
-          return ok;
-        }
         if (lane == 0) {
           for (int u = begin; u < end; ++u) {
             const CUtensorMap* tm = (u & 1) ? &tmV : &tmK;
@@ -540,12 +511,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         ok = ok && publish(nx) && load(it, first, end);
         it = nx;
       }
-      if (PAGED && !clear_tail() && lane == 0) {  // (given up: the copies are waited for all the same)
-        mbar_wait_bounded(bar(TAIL), tail_phase, timeout_ns);
-        mbar_arrive(bar(FULL + tail_stage));
-      }
       if (lane == 0) {
-        if (!SHARED && !PAGED) {  // the CTA that is done last sets the counters back: nobody takes items any more
+        if (!SHARED) {  // the CTA that is done last sets the counters back: nobody takes items any more
           __threadfence();
           if (atomicAdd(counter + 1, 1) == (int)gridDim.x - 1) {
             atomicExch(counter, 0);
@@ -564,9 +531,96 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       constexpr int kLanes = DP / 8, kRowsPer = 32 / kLanes;
       const int t = warp - kSoftWarps - 2;
       uint32_t loads = 0;
-      while (const Item* ip = next_item()) {
-        const Item it = *ip;
-        item_done();
+      // PAGED: the first of these warps walks the CTA's run and publishes its items, one ahead of the Q tiles it loads
+      const bool finder = PAGED && t == 0;
+      const Runs runs(finder ? plan[0] * Hkv : 0, gridDim.x);
+      long long x = finder ? plan[2] : 0, late_x = 0;
+      int at_slot = finder ? (int)plan[1] : 0, at_head = finder ? (int)plan[3] : 0, late_slot = -1, late_head = 0;
+      const bool idle = !finder || plan[0] == 0 || (int)blockIdx.x >= runs.n;
+      const long long run_begin = idle ? 0 : runs.begin(blockIdx.x), run_end = idle ? 0 : runs.begin(blockIdx.x + 1);
+      auto find = [&](Item& it) {
+        it = Item{};
+        it.last = 1;
+        while (!idle && (x < run_end || late_slot >= 0)) {
+          const bool late = x >= run_end;
+          const int s = late ? late_slot : at_slot, head = late ? late_head : at_head;
+          const ChunkItem ci = chunk_item(pa, sa, s, find_tile_seq_warp(pa.qo, pa.n, G, 2 * TM, s));
+          const long long begin = late ? late_x : x;
+          if (late) {
+            late_slot = -1;
+          } else {
+            x += ci.length();
+            if (++at_slot == n_items) {
+              at_slot = 0;
+              ++at_head;
+            }
+          }
+          if (ci.nrows == 0) continue;  // a slot that no tile fills
+          // The end of an item that began in another run comes last: the whole items of all runs then begin with their
+          // first keys at about the same time, and L2 serves those that share a head.
+          if (!late && begin < run_begin) {
+            late_slot = s;
+            late_head = head;
+            late_x = begin;
+            continue;
+          }
+          // the blocks whose beginnings lie in the run: block j at begin + j cost
+          const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
+          auto first_from = [&](long long p) {
+            return p <= begin ? 0 : (int)min((long long)all, (p - begin + ci.cost - 1) / ci.cost);
+          };
+          const int b0 = first_from(run_begin), b1 = first_from(run_end);
+          if (b0 >= b1) continue;
+          it.hk = head;
+          it.seq = ci.seq;
+          it.row0 = ci.row0;
+          it.nrows = ci.nrows;
+          it.q0 = ci.q0; it.nq = ci.nq; it.k0 = ci.slot; it.nk = ci.nk;
+          it.key0 = b0 * BK;
+          it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
+          it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
+          it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
+          it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
+          it.last = 0;
+          if (b0 == 0 && b1 < all && lane == 0) {
+            ChunkRun r;
+            r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
+            r.end = runs.of(begin + (long long)(all - 1) * ci.cost);
+            sa.runs[blockIdx.x] = r;
+          }
+          return;
+        }
+      };
+      auto publish = [&](const Item& it) {
+        bool ok = true;
+        if (lane == 0) {
+          ok = wait_or_abort(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51);
+          if (ok) {
+            items[iq] = it;
+            mbar_arrive(bar(IFULL + iq));
+          }
+        }
+        if (++iq == kItems) { iq = 0; iphase ^= 1u; }
+        return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      };
+      Item ahead;
+      if (finder) {
+        find(ahead);
+        publish(ahead);
+      }
+      while (true) {
+        Item it;
+        if (finder) {
+          it = ahead;
+          if (it.last) break;
+          find(ahead);
+          if (!publish(ahead)) break;
+        } else {
+          const Item* ip = next_item();
+          if (ip == nullptr) break;
+          it = *ip;
+          item_done();
+        }
         if ((t ? it.lim1 : it.lim0) == 0) continue;
         if (!warp_wait(bar(QEMPTY + t), (loads & 1u) ^ 1u, timeout_ns, abort_flag, status, 55)) break;
         ++loads;
@@ -829,18 +883,66 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc_fence_after();
       }
       if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-        // where a chunk's keys lie: key j of the item
-        const int32_t* row = PAGED ? sa.d.c.table + (long long)it->k0 * sa.d.c.width : nullptr;
-        auto paged = [&](int j, long long& ko, long long& vo) {
-          const CacheView& cv = sa.d.c;
-          const int p = it->key0 + j;
-          int page = row[p >> cv.page_shift];
-          page = page < 0 || page >= cv.n_pages ? 0 : page;
-          ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
-        };
-        if (SHARED || SPLIT || (PAGED && it->split >= 0)) {
+        uint32_t again;  // rows whose results are looked at again (replace_unseen)
+        if (PAGED) {
+          // a piece: the sums in fp32; a whole item: the results in bf16. 32 elements a step through shared memory, as below
+          const bool part = it->split >= 0;
+          const long long at = part ? ((long long)it->split * sa.piece_rows + t * TM + r) * D : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
+          uint8_t* orow = part ? reinterpret_cast<uint8_t*>(sa.part_o + at) : (uint8_t*)pa.out + 2 * at;
+          const float f = part ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+          const uint32_t stg = sOut + warp * C::kStage;
+          const uint64_t f2 = f2_pack(f, f);
+          uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_ld_32x32b_x32(tO + 32 * c, o);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              uint64_t v = ffma2(((uint64_t)o[i + 1] << 32) | o[i], f2, 0ull);
+              v = lim == 0 ? 0ull : v;
+              odd = ffma2(v, 0ull, odd);
+              o[i] = (uint32_t)v;
+              o[i + 1] = (uint32_t)(v >> 32);
+            }
+            if (part) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)),
+                             "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                             : "memory");
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 64 + ((i ^ (lane >> 1 & 3)) * 16)),
+                             "r"(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]))),
+                             "r"(pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]))),
+                             "r"(pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]))),
+                             "r"(pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])))
+                             : "memory");
+            }
+            __syncwarp();
+            const int us = part ? 3 : 2;  // log2 of the 16-byte stores of a row
+            for (int i = 0; i < 1 << us; ++i) {
+              const int u = lane & ((1 << us) - 1), rr = (i << (5 - us)) + (lane >> us);
+              uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + (c << (4 + us)) + 16 * u;
+              uint4 x;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(stg + (rr << (4 + us)) + ((u ^ (part ? rr & 7 : rr >> 1 & 3)) * 16)) : "memory");
+              if (32 * q4 + rr < nrow_t && 32 * c + (32 >> us) * u < D) *reinterpret_cast<uint4*>(dst) = x;
+            }
+            __syncwarp();
+          }
+          if (valid && part) sa.part_ml[(long long)it->split * sa.piece_rows + t * TM + r] = make_float2(m * c2, l);
+          if (valid && !part && pa.lse != nullptr)
+            pa.lse[(long long)(it->q0 + tok) * H + h] = lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
+          // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
+          again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
+        } else if (SHARED || SPLIT) {
           const long long piece = SHARED ? ((long long)tok * H + h) * sa.splits + blockIdx.z
-                                  : PAGED ? (long long)it->split * sa.piece_rows + t * TM + r
                                           : ((long long)(it->q0 + tok) * H + h) * sa.splits + it->split;
           const float* orow = sa.part_o + piece * D;
           const uint32_t stg = sOut + warp * C::kStage;  // 32 elements a step through shared memory, as below
@@ -876,8 +978,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
           if (valid) sa.part_ml[piece] = make_float2(m * c2, l);
           // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
-          uint32_t again = __ballot_sync(0xffffffffu, valid && !fine && fabsf(l) <= 3.0e38f);
-          Unseen unseen(SHARED ? n * BK : PAGED ? min(n * BK, it->nk - it->key0) : min(n * BK, pa.Tkv - it->k0 - it->key0));
+          again = __ballot_sync(0xffffffffu, valid && !fine && fabsf(l) <= 3.0e38f);
+          Unseen unseen(SHARED ? n * BK : min(n * BK, pa.Tkv - it->k0 - it->key0));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
@@ -887,11 +989,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             float o[8];
             long long pw;
             uint32_t cols;
-            if (PAGED) {
-              pw = (long long)it->split * sa.piece_rows + t * TM + 32 * q4 + w;
-              cols = replace_unseen(unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
-                                    (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v, paged, D, limw, c2, mcw, o);
-            } else if (SPLIT) {
+            if (SPLIT) {
               pw = ((long long)(it->q0 + tw) * H + hw) * sa.splits + it->split;
               cols = replace_unseen(unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
                                     (const __nv_bfloat16*)pa.k + (long long)(it->k0 + it->key0) * pa.ks + (long long)it->hk * D,
@@ -971,35 +1069,57 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (valid && pa.lse != nullptr)
             pa.lse[(long long)(it->q0 + tok) * H + h] = lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
           // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
-          uint32_t again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
-          Unseen unseen(min(n * BK, PAGED ? it->nk : pa.Tkv - it->k0));
+          again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
+          Unseen unseen(min(n * BK, pa.Tkv - it->k0));
           while (again != 0) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
             const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
             const int limw = __shfl_sync(0xffffffffu, lim, w);
             const float mw = __shfl_sync(0xffffffffu, m, w), iw = __shfl_sync(0xffffffffu, inv, w);
-            const __nv_bfloat16* qw = (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D;
-            const float mcw = mw == -INFINITY ? 0.f : mw * c2;
             float o[8];
-            uint32_t cols;
-            if (PAGED) {
-              cols = replace_unseen(unseen, qw, (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v, paged, D, limw, c2,
-                                    mcw, o);
-            } else {
-              cols = replace_unseen(
-                  unseen, qw, (const __nv_bfloat16*)pa.k + (long long)it->k0 * pa.ks + (long long)it->hk * D,
-                  (const __nv_bfloat16*)pa.v + (long long)it->k0 * pa.vs + (long long)it->hk * D,
-                  [&](int j, long long& ko, long long& vo) {
-                    ko = (long long)j * pa.ks;
-                    vo = (long long)j * pa.vs;
-                  },
-                  D, limw, c2, mcw, o);
-            }
+            const uint32_t cols = replace_unseen(
+                unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                (const __nv_bfloat16*)pa.k + (long long)it->k0 * pa.ks + (long long)it->hk * D,
+                (const __nv_bfloat16*)pa.v + (long long)it->k0 * pa.vs + (long long)it->hk * D,
+                [&](int j, long long& ko, long long& vo) {
+                  ko = (long long)j * pa.ks;
+                  vo = (long long)j * pa.vs;
+                },
+                D, limw, c2, mw == -INFINITY ? 0.f : mw * c2, o);
             __nv_bfloat16* dw = (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (cols >> e & 1u) dw[lane * 8 + e] = __float2bfloat16_rn(o[e] * iw);
+          }
+        }
+        if (PAGED && again != 0) {
+          Unseen unseen(min(n * BK, it->nk - it->key0));
+          while (again != 0) {
+            const int w = __ffs(again) - 1;
+            again &= again - 1;
+            const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
+            const float mw = __shfl_sync(0xffffffffu, m, w), lw = __shfl_sync(0xffffffffu, l, w);
+            float o[8];
+            const uint32_t cols = replace_unseen(
+                unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                (const __nv_bfloat16*)sa.d.k, (const __nv_bfloat16*)sa.d.v,
+                [&](int j, long long& ko, long long& vo) {  // where key j of the item lies
+                  const CacheView& cv = sa.d.c;
+                  const int p = it->key0 + j;
+                  int page = cv.table[(long long)it->k0 * cv.width + (p >> cv.page_shift)];
+                  page = page < 0 || page >= cv.n_pages ? 0 : page;
+                  ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
+                },
+                D, __shfl_sync(0xffffffffu, lim, w), c2, mw == -INFINITY ? 0.f : mw * c2, o);
+            float* po = sa.part_o + ((long long)it->split * sa.piece_rows + t * TM + 32 * q4 + w) * D + lane * 8;
+            __nv_bfloat16* dw = (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D + lane * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (cols >> e & 1u) {
+                if (it->split >= 0) po[e] = o[e];
+                else dw[e] = __float2bfloat16_rn(o[e] * (lw == 0.f ? 0.f : 1.0f / lw));
+              }
           }
         }
       }
