@@ -36,6 +36,8 @@
 // scores cost about 3.5 us an item (taking the longest sequences first gains 1 us).
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "attn.cuh"
 #include "kernels.cuh"
 
@@ -57,6 +59,7 @@ struct __align__(16) Item {
   int lim0, lim1;           // keys that each tile's last row sees (relative to key0)
   int last;                 // no item: the end
   int seq;                  // (of a chunk, for errors)
+  int dual;                 // (of a chunk) one tile of rows: both softmax groups take it, with half of each block's keys
   int split;                // which part of the keys; of a chunk: the piece that takes the results (-1: the output)
 };
 constexpr int kItems = 3;   // items published: one worked on, one ahead, one being given back
@@ -67,8 +70,9 @@ template <int DP> struct Cfg {
   static constexpr int kTileBytes = TM * DP * 2;   // a Q tile, and a K or V block
   static constexpr int kStages = DP == 128 ? 4 : 8;
   static constexpr int kStage = 32 * 128;  // bytes of a softmax warp's output staging: 32 rows x 64 bf16 elements
-  static constexpr int kBars = 2 * kStages + 5 * 2 + 1 + 2 * kItems + 1;
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 + kItems * sizeof(Item);
+  static constexpr int kBars = 2 * kStages + 5 * 2 + 1 + 2 * kItems + 1 + 8;
+  static constexpr size_t kSmem =
+      1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 + kItems * sizeof(Item) + 4 * 32 * 8;
 };
 static_assert(Cfg<128>::kSmem <= kMaxSmem && Cfg<64>::kSmem <= kMaxSmem, "shared memory");
 
@@ -198,7 +202,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 2,
                 ODONE = PFULL + 2, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
-                TAIL = IEMPTY + kItems;
+                TAIL = IEMPTY + kItems, GIVEN = TAIL + 1, TAKEN = GIVEN + 4;
+  float2* given_ml = reinterpret_cast<float2*>(gbase + C::kSmem - 1024 - 4 * 32 * 8);  // [warp of tile 1][row]
 
   // (the shuffle tells the compiler that the warp number is the same in all lanes)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -214,6 +219,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int i = 0; i < kItems; ++i) { mbar_init(bar(IFULL + i), 1); mbar_init(bar(IEMPTY + i), kItemReaders); }
     mbar_init(bar(DONE), 1);
     mbar_init(bar(TAIL), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(GIVEN + i), 1);
     fence_mbar_init();
     *abort_flag = 0;
     if (q_tma) tma_prefetch_desc(&tmQ);
@@ -309,11 +315,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // the pages of 32 x page_size positions from table column 32 `window` on and of the next ones, a page a lane
       int window_slot = -1, window = 0, page_now = 0, page_next = 0;
       bool tail = false;  // the last block of values loaded needs its end cleared
-      int tail_stage = 0, tail_keys = 0;
+      int tail_stage = 0, tail_keys = 0, behind = 0;
       uint32_t tail_phase = 0;
       // What pages hold past a sequence's end is anyone's: the last block's values there become zeros once they
-      // have arrived, as 0 times a leftover that is not finite would be NaN. This is done when the next item's first copies
-      // are on their way (they need no stage that waits for it).
+      // have arrived, as 0 times a leftover that is not finite would be NaN. This is done when the two copies behind them
+      // are on their way: their stages wait for nothing that comes after the block before.
       auto clear_tail = [&]() {
         if (!tail) return true;
         if (!warp_wait(bar(TAIL), tail_phase, timeout_ns, abort_flag, status, 51)) return false;
@@ -342,8 +348,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const int32_t* row = cv.table + (long long)slot * cv.width;
         for (int u = 0; u < end && ok; ++u) {
           const int j0 = key0 + (u >> 1) * BK, held = min(BK, held_all - j0);
-          const bool cut = (u & 1) && held < BK;
-          if ((u >= 2 || cut) && !(ok = clear_tail())) break;
+          const bool is_v = u & 1, cut = is_v && held < BK;
+          if (tail && (++behind > 2 || cut) && !(ok = clear_tail())) break;
           // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
           const int col = j0 >> cv.page_shift;
           if (window_slot != slot || window != col >> 5) {
@@ -370,10 +376,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(dst + c * (BK * 128) + (lane << box_shift) * 128, (u & 1) ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
+              tma_load_3d(dst + c * (BK * 128) + (lane << box_shift) * 128, is_v ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
           }
           if (cut) {
             tail = true;
+            behind = 0;
             tail_stage = stage;
             tail_keys = held;
           }
@@ -580,6 +587,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
           it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
           it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
+          it.dual = ci.nrows <= TM;
+          if (it.dual) it.lim1 = it.lim0;
           it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
           it.last = 0;
           if (b0 == 0 && b1 < all && lane == 0) {
@@ -629,16 +638,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_arrive_expect_tx(bar(QFULL + t), C::kTileBytes);
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(sQ + t * C::kTileBytes + c * (TM * 128), &tmQ, 64 * c, it.hk * G, it.q0 + (it.row0 + t * TM) / G,
-                          bar(QFULL + t));
+              tma_load_3d(sQ + t * C::kTileBytes + c * (TM * 128), &tmQ, 64 * c, it.hk * G,
+                          it.q0 + (it.row0 + (PAGED && it.dual ? 0 : t * TM)) / G, bar(QFULL + t));
           }
           continue;
         }
-        const int nrow_t = min(TM, it.nrows - t * TM);
+        const int first = PAGED && it.dual ? 0 : t * TM, nrow_t = min(TM, it.nrows - first);
         const __nv_bfloat16* q = (const __nv_bfloat16*)(SHARED ? sa.d.q : pa.q) + (long long)(SHARED ? 0 : it.q0) * (SHARED ? sa.d.qs : pa.qs);
 #pragma unroll
         for (int k = 0; k < TM / 32; ++k) {
-          const int R = it.row0 + t * TM + 32 * k + lane, tok = R / G;  // (rows past the end are not read)
+          const int R = it.row0 + first + 32 * k + lane, tok = R / G;  // (rows past the end are not read)
           const __nv_bfloat16* row = q + (long long)tok * (SHARED ? sa.d.qs : pa.qs) + (long long)(it.hk * G + R - tok * G) * D;
 #pragma unroll 4
           for (int i = 0; i < 32 / kRowsPer; ++i) {
@@ -664,7 +673,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const bool leader = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc_qk = make_idesc_bf16_f32(TM, BK, false);
+      constexpr uint32_t idesc_half = make_idesc_bf16_f32(TM, BK / 2, false);
       constexpr uint32_t idesc_pv = make_idesc_bf16_f32(TM, DP, true);
+      bool dual = false;  // tile t has keys t BK / 2 .. of each block (the same rows)
       int stage = 0;
       uint32_t phase = 0;
       auto wait = [&](int b, uint32_t ph) {
@@ -687,21 +698,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       };
       auto qk = [&](int t, int st) {
         const uint64_t a = make_smem_desc_sw128(sQ + t * C::kTileBytes, 16, 1024);
-        const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes, 16, 1024);
+        const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes + (PAGED && dual ? t * (BK / 2) * 128 : 0), 16, 1024);
+        const uint32_t idesc = PAGED && dual ? idesc_half : idesc_qk;
         if (!leader) return;
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk / 4) * (TM * 128) + (kk % 4) * 32) >> 4);
-          tc_mma_f16(tm + t * BK, a + off, b + off, idesc_qk, kk != 0);
+          tc_mma_f16(tm + t * BK, a + off, b + off, idesc, kk != 0);
         }
         tc_commit(bar(SFULL + t));
       };
       auto pv = [&](int t, int st, bool acc) {
-        const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes, BK * 128, 1024);
+        const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes + (PAGED && dual ? t * (BK / 2) * 128 : 0), BK * 128, 1024);
+        const int steps = PAGED && dual ? BK / 32 : BK / 16;
         if (!leader) return;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+          if (!PAGED || kk < steps) tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
                         acc || kk != 0);
         tc_commit(bar(ODONE + t));
       };
@@ -713,6 +726,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (it == nullptr) break;
         const int n0 = __shfl_sync(0xffffffffu, blocks(it->lim0), 0), n1 = __shfl_sync(0xffffffffu, blocks(it->lim1), 0);
         const int nn = max(n0, n1);
+        dual = PAGED && __shfl_sync(0xffffffffu, it->dual, 0) != 0;
         item_done();
         if (nn == 0) continue;
         ok = wait(FULL + stage, phase);
@@ -775,15 +789,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const uint32_t tS = tmem + lanes + t * BK, tO = tmem + lanes + 256 + t * DP;
     uint32_t done = 0;  // blocks of all items so far: their barriers' phases
+    uint32_t given = 0;  // exchanges with the other tile's warp
     bool ok = true;
     while (ok) {
       const Item* it = next_item();
       if (it == nullptr) break;
-      const int nrow_t = min(TM, it->nrows - t * TM);  // rows of this tile (<= 0: none)
+      // Where the thread's row lies. (A chunk's is found again after the loop, which has no registers to keep it in.)
+      bool dual, valid;
+      int tile0, nrow_t, tok, h;
+      auto place = [&]() {
+        int g = G;
+        if (PAGED) asm volatile("" : "+r"(g));
+        dual = PAGED && it->dual;
+        tile0 = dual ? 0 : t * TM;               // the tile's first row of the item's
+        nrow_t = min(TM, it->nrows - tile0);     // rows of this tile (<= 0: none)
+        const int R = it->row0 + tile0 + r;
+        valid = r < nrow_t;
+        tok = valid ? R / g : 0;
+        h = it->hk * g + (valid ? R % g : 0);
+      };
+      place();
       const int n = blocks(t ? it->lim1 : it->lim0);
-      const int R = it->row0 + t * TM + r;
-      const bool valid = r < nrow_t;
-      const int tok = valid ? R / G : 0, h = it->hk * G + (valid ? R % G : 0);
       int lim = 0;
       if (valid && SHARED) {  // a slot shorter than the shared keys sees its own length of them
         lim = max(0, min(it->n_keys, slot_len(sa.d.c, sa.d.slots[tok]) - it->key0));
@@ -792,18 +818,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (SPLIT || PAGED) lim = max(0, min(lim - it->key0, it->n_keys));
       }
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++done) {
+      // Block j, of which the tile has COLS keys: 128, or half of them.
+      auto block = [&](auto cols, int j) {
+        constexpr int NC = decltype(cols)::value / 32;
         ok = warp_wait(bar(SFULL + t), done & 1, timeout_ns, abort_flag, status, 53);
-        if (!ok) break;
+        if (!ok) return;
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[NC][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32 * c, s[c]);
+        for (int c = 0; c < NC; ++c) tmem_ld_32x32b_x32(tS + 32 * c, s[c]);
         tmem_ld_wait();
-        const int left = lim - j * BK;  // columns that this row sees
-        if (__any_sync(0xffffffffu, left < BK)) {
+        const int left = lim - j * BK - (NC < 4 ? t * (BK / 2) : 0);  // columns that this row sees
+        if (__any_sync(0xffffffffu, left < 32 * NC)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * c + i >= left) s[c][i] = 0xff800000u;  // -inf
@@ -811,14 +839,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // four chains of three-input maxima (max drops a NaN score: the maximum is never NaN)
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < 16 * NC; ++i)
           mx4[i & 3] = max3(mx4[i & 3], __uint_as_float(s[i >> 4][2 * (i & 15)]), __uint_as_float(s[i >> 4][2 * (i & 15) + 1]));
         const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
         if (__any_sync(0xffffffffu, mx > m + thr)) {
           const bool up = mx > m + thr;
           if (j > 0) {
             ok = warp_wait(bar(ODONE + t), (done - 1) & 1, timeout_ns, abort_flag, status, 53);
-            if (!ok) break;
+            if (!ok) return;
             tc_fence_after();
             const float a = up ? ex2((m - mx) * c2) : 1.0f;
             l *= a;
@@ -840,7 +868,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // before, so that nothing waits for a power of two just asked for
         uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < NC / 2; ++h) {
           uint32_t p[32];
 #pragma unroll
           for (int b = 0; b < 5; ++b) {
@@ -876,22 +904,60 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (lane == 0) mbar_arrive(bar(PFULL + t));
         const uint64_t sum = fadd2(sum0, sum1);
         l += f2_lo(sum) + f2_hi(sum);
+      };
+      for (int j = 0; j < n && ok; ++j) {
+        if (PAGED && it->dual) block(std::integral_constant<int, BK / 2>{}, j);
+        else block(std::integral_constant<int, BK>{}, j);
+        done += ok ? 1 : 0;
       }
       // ---- the rows' results
       if (ok && n > 0) {
         ok = warp_wait(bar(ODONE + t), (done - 1) & 1, timeout_ns, abort_flag, status, 53);
         tc_fence_after();
       }
+      if (PAGED) place();
       if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-        uint32_t again;  // rows whose results are looked at again (replace_unseen)
-        if (PAGED) {
+        uint32_t again = 0;  // rows whose results are looked at again (replace_unseen)
+        if (PAGED && dual && t == 1) {
+          // the other half of the keys of tile 0's rows: m, l and the sums to the warp there, 32 elements a step
+          const uint32_t stg = sOut + warp * C::kStage;
+          given_ml[32 * q4 + lane] = make_float2(m, l);
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c, ++given) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + 32 * c, o);  // (not this item's where there was no block: not used then)
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = m == -INFINITY ? 0u : o[i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)),
+                           "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                           : "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(GIVEN + q4));
+            ok = ok && warp_wait(bar(TAKEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+          }
+        } else if (PAGED) {
           // a piece: the sums in fp32; a whole item: the results in bf16. 32 elements a step through shared memory, as below
           const bool part = it->split >= 0;
-          const long long at = part ? ((long long)it->split * sa.piece_rows + t * TM + r) * D : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
+          const long long at = part ? ((long long)it->split * sa.piece_rows + tile0 + r) * D : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
           uint8_t* orow = part ? reinterpret_cast<uint8_t*>(sa.part_o + at) : (uint8_t*)pa.out + 2 * at;
+          float f1 = 0.f, f0 = 1.f;  // factors of tile 1's sums and of this tile's
+          if (dual) {
+            ok = warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+            const float2 x = given_ml[32 * q4 + lane];
+            const float top = fmaxf(m, x.x);
+            f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2);
+            f1 = x.x == -INFINITY ? 0.f : ex2((x.x - top) * c2);
+            l = l * f0 + x.y * f1;
+            m = top;
+          }
           const float f = part ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+          f0 *= f;
+          f1 *= f;
           const uint32_t stg = sOut + warp * C::kStage;
-          const uint64_t f2 = f2_pack(f, f);
+          const uint64_t f2 = f2_pack(f0, f0), g2 = f2_pack(f1, f1);
           uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
 #pragma unroll
           for (int c = 0; c < DP / 32; ++c) {
@@ -900,13 +966,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               tmem_ld_32x32b_x32(tO + 32 * c, o);
               tmem_ld_wait();
             }
+            if (dual && c > 0) ok = ok && warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              uint64_t v = ffma2(((uint64_t)o[i + 1] << 32) | o[i], f2, 0ull);
-              v = lim == 0 ? 0ull : v;
-              odd = ffma2(v, 0ull, odd);
-              o[i] = (uint32_t)v;
-              o[i + 1] = (uint32_t)(v >> 32);
+            for (int i = 0; i < 8; ++i) {
+              uint64_t v0 = ffma2(((uint64_t)o[4 * i + 1] << 32) | o[4 * i], f2, 0ull);
+              uint64_t v1 = ffma2(((uint64_t)o[4 * i + 3] << 32) | o[4 * i + 2], f2, 0ull);
+              if (dual) {
+                uint64_t x0, x1;
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x0), "=l"(x1)
+                             : "r"(stg + 4 * C::kStage + lane * 128 + ((i ^ (lane & 7)) * 16)) : "memory");
+                v0 = ffma2(x0, g2, v0);
+                v1 = ffma2(x1, g2, v1);
+              }
+              if (lim == 0) v0 = v1 = 0ull;
+              odd = ffma2(v0, 0ull, odd);
+              odd = ffma2(v1, 0ull, odd);
+              o[4 * i] = (uint32_t)v0;
+              o[4 * i + 1] = (uint32_t)(v0 >> 32);
+              o[4 * i + 2] = (uint32_t)v1;
+              o[4 * i + 3] = (uint32_t)(v1 >> 32);
+            }
+            if (dual) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(TAKEN + q4));
+              ++given;
             }
             if (part) {
 #pragma unroll
@@ -936,7 +1019,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             __syncwarp();
           }
-          if (valid && part) sa.part_ml[(long long)it->split * sa.piece_rows + t * TM + r] = make_float2(m * c2, l);
+          if (valid && part) sa.part_ml[(long long)it->split * sa.piece_rows + tile0 + r] = make_float2(m * c2, l);
           if (valid && !part && pa.lse != nullptr)
             pa.lse[(long long)(it->q0 + tok) * H + h] = lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
           // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
@@ -1112,7 +1195,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                   ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
                 },
                 D, __shfl_sync(0xffffffffu, lim, w), c2, mw == -INFINITY ? 0.f : mw * c2, o);
-            float* po = sa.part_o + ((long long)it->split * sa.piece_rows + t * TM + 32 * q4 + w) * D + lane * 8;
+            float* po = sa.part_o + ((long long)it->split * sa.piece_rows + tile0 + 32 * q4 + w) * D + lane * 8;
             __nv_bfloat16* dw = (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D + lane * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e)

@@ -121,6 +121,14 @@ def test_many_sequences(dtype):
     run_chunk(nq, [a + r.choice([0, 1, 40]) for a in nq], 4, 1, 64, dtype, page=16, seed=5)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [(77, 128), (50, 128, 128), (200, 128, 256, 1), (129, 127, 128)])
+def test_short_sequences_behind_cut_blocks(lens, D):
+    """Many items of one or two blocks for each CTA, whole blocks behind ones that the sequence's end cuts."""
+    nk = [lens[i % len(lens)] for i in range(700)]
+    run_chunk([1] * 700, nk, 8, 4, D, BF16, page=64, seed=2)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_slots_in_any_order_and_twice(dtype):
     """Slots named in another order than the table's, some not at all, one by two sequences."""
