@@ -174,7 +174,7 @@ struct RotaryArgs {
   long long qos, kos;
   const int32_t* positions;
   int T, H, Hkv, D;
-  int lpr_shift, parts;  // log2 of LPR; warps of a token
+  int lpr_shift, groups;  // log2 of the lanes of a row; units of a token (rotary.cu)
   // append: token t's place comes from the cache's tables
   CacheView c;
   void *kp, *vp;  // the layer's pages

@@ -132,7 +132,7 @@ struct SharedArgs {
 // A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
 // several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order. A
 // run has at most two such items, its first and its last, so that 2 pieces a CTA are enough however long the keys.
-constexpr int kOneTile = 2, kTwoTiles = 3, kItem = 3, kShortest = 12;
+constexpr int kOneTile = 4, kTwoTiles = 4, kItem = 16, kShortest = 16;
 
 struct ChunkItem {
   int seq, row0, nrows, q0, nq, nk, slot;

@@ -11,16 +11,19 @@
 //
 // LPR lanes share a row (a head of a token), so that a warp has 32 / LPR rows under way; a lane holds NC pairs of chunks
 // of VEC elements. In the half layout those are elements p .. p + VEC - 1 and R/2 + p ..: both parts of its pairs, so no
-// rotation crosses lanes. (VEC is 16 bytes, or what divides R / 2 where that is less.) A warp takes a token, or with few
-// tokens some of its rows, and computes its lanes' sines and cosines once for all of them; a group of kUnroll rows
-// is loaded at once.
+// rotation crosses lanes. (VEC is 16 bytes, or what divides R / 2 where that is less.)
+//
+// The rows of all tokens lie in a row, kUnroll * 32 / LPR at a time (a unit), and each warp takes a run of them: it computes
+// its lanes' sines and cosines once a token and looks for the token's place in the cache only where the sequence or the page
+// changes. A lane copies its chunks of the next kStages units into shared memory while it works on the oldest, and reads
+// back what it copied itself, so no barrier is needed.
 #include "attn.cuh"
 #include "kernels.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kUnroll = 4, kThreads = 256;
+constexpr int kUnroll = 2, kStages = 4, kThreads = 256, kWarps = kThreads / 32, kBlocks = 2;
 
 template <int BYTES> struct Raw;  // a chunk as it lies in memory
 template <> struct Raw<16> { using T = uint4; };
@@ -57,45 +60,75 @@ __device__ __forceinline__ void cos_sin(uint64_t turn, float& c, float& s) {
   if (quad & 2u) s = -s;         // 2 and 3
 }
 
-// Where token t goes: its position, and the page and row (append). false: nowhere, which is recorded.
-__device__ __forceinline__ bool find_place(const RotaryArgs& a, int t, bool first, int& position, int& page) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, len = a.n;
-  while (len > 1) {
-    const int step = (len + 31) / 32;
-    const bool at = lane * step < len && a.offsets[lo + lane * step] <= t;
-    const int m = __popc(__ballot_sync(0xffffffffu, at)) - 1, skip = (m < 0 ? 0 : m) * step;
-    lo += skip;
-    len = len - skip < step ? len - skip : step;
+// Where the tokens of a run go: the sequence and the page of the last one, and its position and page.
+struct Place {
+  int o0 = 0, o1 = 0, slot = 0, p0 = 0, held = 0;  // the sequence's tokens, slot, first position and the slot's length
+  int col = -1, page = 0;                          // the table's column and what is there (-1: no page to write to)
+  int position = 0;
+  __device__ __forceinline__ bool find(const RotaryArgs& a, int t) {
+    const CacheView& c = a.c;
+    if (t < o0 || t >= o1) {  // (no sequence yet, or the next one)
+      const int lane = threadIdx.x & 31;
+      int lo = 0, len = a.n;
+      while (len > 1) {
+        const int step = (len + 31) / 32;
+        const bool at = lane * step < len && a.offsets[lo + lane * step] <= t;
+        const int m = __popc(__ballot_sync(0xffffffffu, at)) - 1, skip = (m < 0 ? 0 : m) * step;
+        lo += skip;
+        len = len - skip < step ? len - skip : step;
+      }
+      slot = a.slots[lo];
+      o0 = a.offsets[lo];
+      o1 = a.offsets[lo + 1];
+      p0 = a.pos[lo];
+      held = slot >= 0 && slot < c.n_slots && p0 >= 0 ? c.lens[slot] : 0;
+      col = -1;
+      if (t < o0 || t >= o1) return false;
+    }
+    const long long p = (long long)p0 + (t - o0);
+    if (p < 0 || p >= held || (p >> c.page_shift) >= c.width) return false;
+    position = (int)p;
+    if (col != position >> c.page_shift) {
+      col = position >> c.page_shift;
+      page = c.table[(long long)slot * c.width + col];
+      if (page < 0 || page >= c.n_pages || c.refs[page] != 1) page = -1;
+    }
+    return page >= 0;
   }
-  const CacheView& c = a.c;
-  const int s = a.slots[lo], o0 = a.offsets[lo], o1 = a.offsets[lo + 1], p0 = a.pos[lo];
-  bool ok = s >= 0 && s < c.n_slots && t >= o0 && t < o1 && p0 >= 0;
-  const long long p = (long long)p0 + ((long long)t - o0);
-  if (ok && (p >> c.page_shift) < c.width) {
-    const int held = c.lens[s];
-    page = c.table[(long long)s * c.width + (p >> c.page_shift)];
-    ok = p < held && page >= 0 && page < c.n_pages && c.refs[page] == 1;
-  } else {
-    ok = false;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  } else if constexpr (BYTES >= 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+  } else {  // (copies have 4 bytes at least)
+    const unsigned short x = *static_cast<const unsigned short*>(src);
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(x) : "memory");
   }
-  position = (int)p;
-  if (!ok && first && lane == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, t);
-  return ok;
 }
 
+template <int CHUNK, int NC> constexpr int warp_smem() { return kStages * kUnroll * NC * 2 * 32 * CHUNK; }
+
 template <typename T, int VEC, int NC, bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBlocks)
 rotary_kernel(const __grid_constant__ RotaryArgs a) {
   using C = Chunk<T, VEC>;
+  using R4 = typename C::R;
+  constexpr int CB = VEC * (int)sizeof(T);
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint64_t* turns = reinterpret_cast<uint64_t*>(smem);  // [R / 2]
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, lpr = 1 << a.lpr_shift, me = lane & (lpr - 1), rpw = 32 >> a.lpr_shift;
   const int D = a.D, R = a.rot.R;
+  for (int i = threadIdx.x; i < R / 2; i += kThreads) turns[i] = a.rot.turns[i];
+  __syncthreads();
+  const int lane = threadIdx.x & 31, lpr = 1 << a.lpr_shift, me = lane & (lpr - 1), rpw = 32 >> a.lpr_shift;
+  uint8_t* mine = smem + 1024 + (threadIdx.x >> 5) * warp_smem<CB, NC>() + lane * CB;  // chunk i of a stage: + i 32 CB
   // this lane's chunks: elements, whether they exist, and the first of their pairs
   int at[NC][2], pair[NC][2];
   bool in[NC][2];
-  uint64_t turn[NC][VEC];
 #pragma unroll
   for (int y = 0; y < NC; ++y) {
     const int s = me + y * lpr, turning = R / (2 * VEC);
@@ -115,120 +148,150 @@ rotary_kernel(const __grid_constant__ RotaryArgs a) {
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) in[y][x] = at[y][x] < D;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int p = INTERLEAVED ? pair[y][2 * i / VEC] + i % (VEC / 2 > 0 ? VEC / 2 : 1) : pair[y][0] + i;
-      turn[y][i] = p < R / 2 ? a.rot.turns[p] : 0ull;
-    }
   }
   typename C::U qw[NC][2], kw[NC][2];
 #pragma unroll
   for (int y = 0; y < NC; ++y)
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      if (a.qw != nullptr && in[y][x]) qw[y][x].r = *reinterpret_cast<const typename C::R*>((const T*)a.qw + at[y][x]);
-      if (a.kw != nullptr && in[y][x]) kw[y][x].r = *reinterpret_cast<const typename C::R*>((const T*)a.kw + at[y][x]);
+      if (a.qw != nullptr && in[y][x]) qw[y][x].r = *reinterpret_cast<const R4*>((const T*)a.qw + at[y][x]);
+      if (a.kw != nullptr && in[y][x]) kw[y][x].r = *reinterpret_cast<const R4*>((const T*)a.kw + at[y][x]);
     }
-  const int rows = a.H + (APPEND ? 2 : 1) * a.Hkv;
-  const int groups = (rows + rpw * kUnroll - 1) / (rpw * kUnroll);  // of rows that are under way at once
-  const long long warps = (long long)gridDim.x * (kThreads / 32), units = (long long)a.T * a.parts;
-  for (long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < units; w += warps) {
-    const int t = (int)(w / a.parts), part = (int)(w - (long long)t * a.parts);
-    int position, page = 0;
-    if (APPEND) {
-      if (!find_place(a, t, part == 0, position, page)) continue;
-    } else {
-      position = a.positions[t];
-    }
-    float c[NC][VEC], s[NC][VEC];
-#pragma unroll
-    for (int y = 0; y < NC; ++y)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        cos_sin((uint64_t)(long long)position * turn[y][i], c[y][i], s[y][i]);
-        c[y][i] *= a.rot.magnitude;
-        s[y][i] *= a.rot.magnitude;
-      }
-    for (int g = part; g < groups; g += a.parts) {
-      typename C::U u[kUnroll][NC][2];
-      const int r0 = g * rpw * kUnroll + (lane >> a.lpr_shift);
+  const int rows = a.H + (APPEND ? 2 : 1) * a.Hkv, groups = a.groups;
+  const long long warps = (long long)gridDim.x * kWarps, w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long units = (long long)a.T * groups, u0 = units * w / warps, u1 = units * (w + 1) / warps;
+  // the unit whose copies are asked for next
+  long long next = u0;
+  int nt = (int)(u0 / groups), ng = (int)(u0 - (long long)nt * groups);
+  auto ask = [&](int stage) {
+    if (next < u1) {
 #pragma unroll
       for (int z = 0; z < kUnroll; ++z) {
-        const int r = r0 + z * rpw;
-        const T* src = r < a.H ? (const T*)a.q + t * a.qs + (long long)r * D
-                     : r < a.H + a.Hkv ? (const T*)a.k + t * a.ks + (long long)(r - a.H) * D
-                                       : (const T*)a.v + t * a.vs + (long long)(r - a.H - a.Hkv) * D;
+        const int r = (ng * kUnroll + z) * rpw + (lane >> a.lpr_shift);
+        const T* src = r < a.H ? (const T*)a.q + nt * a.qs + (long long)r * D
+                     : r < a.H + a.Hkv ? (const T*)a.k + nt * a.ks + (long long)(r - a.H) * D
+                                       : (const T*)a.v + nt * a.vs + (long long)(r - a.H - a.Hkv) * D;
 #pragma unroll
         for (int y = 0; y < NC; ++y)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (r < rows && in[y][x]) u[z][y][x].r = __ldcs(reinterpret_cast<const typename C::R*>(src + at[y][x]));
+            if (r < rows && in[y][x])
+              copy_chunk<CB>(smem_u32(mine + (((stage * kUnroll + z) * NC + y) * 2 + x) * 32 * CB), src + at[y][x]);
+      }
+      ++next;
+      if (++ng == groups) {
+        ng = 0;
+        ++nt;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) ask(st);
+  int t = (int)(u0 / groups), g = (int)(u0 - (long long)t * groups), position = 0, ahead = 0;
+  if (!APPEND && u0 < u1) ahead = a.positions[t];
+  bool fresh = true, ok = true;  // a token's first unit here; it has a place
+  Place place;
+  float c[NC][VEC], s[NC][VEC];
+  int stage = 0;
+  for (long long u = u0; u < u1; ++u) {
+    if (fresh) {
+      fresh = false;
+      if (APPEND) {
+        ok = place.find(a, t);
+        position = place.position;
+        if (!ok && g == 0 && lane == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, t);
+      } else {
+        position = ahead;
+        if (t + 1 < a.T) ahead = a.positions[t + 1];
       }
 #pragma unroll
-      for (int z = 0; z < kUnroll; ++z) {
-        const int r = r0 + z * rpw;
-        const bool is_q = r < a.H, is_v = r >= a.H + a.Hkv;
-        float f[NC][2][VEC];
+      for (int y = 0; y < NC; ++y)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const int p = INTERLEAVED ? pair[y][2 * i / VEC] + i % (VEC / 2 > 0 ? VEC / 2 : 1) : pair[y][0] + i;
+          cos_sin((uint64_t)(long long)position * (p < R / 2 ? turns[p] : 0ull), c[y][i], s[y][i]);
+          c[y][i] *= a.rot.magnitude;
+          s[y][i] *= a.rot.magnitude;
+        }
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+    for (int z = 0; z < kUnroll; ++z) {
+      const int r = (g * kUnroll + z) * rpw + (lane >> a.lpr_shift);
+      const bool is_q = r < a.H, is_v = r >= a.H + a.Hkv;
+      typename C::U u4[NC][2];
+#pragma unroll
+      for (int y = 0; y < NC; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          u4[y][x].r = *reinterpret_cast<const R4*>(mine + (((stage * kUnroll + z) * NC + y) * 2 + x) * 32 * CB);
+      float f[NC][2][VEC];
+#pragma unroll
+      for (int y = 0; y < NC; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) f[y][x][i] = to_f32<T>(u4[y][x].e[i]);
+      if (a.qw != nullptr || a.kw != nullptr) {
+        float sum = 0.f;
 #pragma unroll
         for (int y = 0; y < NC; ++y)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
+            if (r < rows && in[y][x])
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f[y][x][i] = to_f32<T>(u[z][y][x].e[i]);
-        if (a.qw != nullptr || a.kw != nullptr) {
-          float sum = 0.f;
+              for (int i = 0; i < VEC; ++i) sum = fmaf(f[y][x][i], f[y][x][i], sum);
+        for (int m = lpr >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const float inv = rsqrtf(sum / (float)D + a.eps);
+        if ((is_q ? a.qw : a.kw) != nullptr)
 #pragma unroll
           for (int y = 0; y < NC; ++y)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              if (r < rows && in[y][x])
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sum = fmaf(f[y][x][i], f[y][x][i], sum);
-          for (int m = lpr >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-          const float inv = rsqrtf(sum / (float)D + a.eps);
-          if ((is_q ? a.qw : a.kw) != nullptr)
+              for (int i = 0; i < VEC; ++i) f[y][x][i] = f[y][x][i] * inv * to_f32<T>(is_q ? qw[y][x].e[i] : kw[y][x].e[i]);
+      }
+      if (r >= rows || !ok) continue;
+      T* dst;
+      if (is_q) dst = (T*)a.qo + t * a.qos + (long long)r * D;
+      else if (!APPEND) dst = (T*)a.ko + t * a.kos + (long long)(r - a.H) * D;
+      else dst = (T*)(is_v ? a.vp : a.kp) +
+                 (((long long)place.page * a.Hkv + (is_v ? r - a.H - a.Hkv : r - a.H)) * a.c.page_size + (position & (a.c.page_size - 1))) * D;
 #pragma unroll
-            for (int y = 0; y < NC; ++y)
+      for (int y = 0; y < NC; ++y) {
+        if (!APPEND || !is_v) {
+          if (INTERLEAVED) {
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                  f[y][x][i] *= inv * to_f32<T>(is_q ? qw[y][x].e[i] : kw[y][x].e[i]);
-        }
-        if (r >= rows) continue;
-        T* dst;
-        if (is_q) dst = (T*)a.qo + t * a.qos + (long long)r * D;
-        else if (!APPEND) dst = (T*)a.ko + t * a.kos + (long long)(r - a.H) * D;
-        else dst = (T*)(is_v ? a.vp : a.kp) +
-                   (((long long)page * a.Hkv + (is_v ? r - a.H - a.Hkv : r - a.H)) * a.c.page_size + (position & (a.c.page_size - 1))) * D;
-#pragma unroll
-        for (int y = 0; y < NC; ++y) {
-          if (!APPEND || !is_v) {
-            if (INTERLEAVED) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int i = 0; i < VEC / 2; ++i) {
-                  const float p = f[y][x][2 * i], q = f[y][x][2 * i + 1], cc = c[y][x * (VEC / 2) + i], ss = s[y][x * (VEC / 2) + i];
-                  const bool on = pair[y][x] + i < R / 2;
-                  u[z][y][x].e[2 * i] = from_f32<T>(on ? fmaf(p, cc, -q * ss) : p);
-                  u[z][y][x].e[2 * i + 1] = from_f32<T>(on ? fmaf(q, cc, p * ss) : q);
-                }
-            } else {
-              const bool on = pair[y][0] < R / 2;
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                const float p = f[y][0][i], q = f[y][1][i];
-                u[z][y][0].e[i] = from_f32<T>(on ? fmaf(p, c[y][i], -q * s[y][i]) : p);
-                u[z][y][1].e[i] = from_f32<T>(on ? fmaf(q, c[y][i], p * s[y][i]) : q);
+              for (int i = 0; i < VEC / 2; ++i) {
+                const float p = f[y][x][2 * i], q = f[y][x][2 * i + 1], cc = c[y][x * (VEC / 2) + i], ss = s[y][x * (VEC / 2) + i];
+                const bool on = pair[y][x] + i < R / 2;
+                u4[y][x].e[2 * i] = from_f32<T>(on ? fmaf(p, cc, -q * ss) : p);
+                u4[y][x].e[2 * i + 1] = from_f32<T>(on ? fmaf(q, cc, p * ss) : q);
               }
+          } else {
+            const bool on = pair[y][0] < R / 2;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const float p = f[y][0][i], q = f[y][1][i];
+              u4[y][0].e[i] = from_f32<T>(on ? fmaf(p, c[y][i], -q * s[y][i]) : p);
+              u4[y][1].e[i] = from_f32<T>(on ? fmaf(q, c[y][i], p * s[y][i]) : q);
             }
           }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (in[y][x]) *reinterpret_cast<typename C::R*>(dst + at[y][x]) = u[z][y][x].r;
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (in[y][x]) *reinterpret_cast<R4*>(dst + at[y][x]) = u4[y][x].r;
       }
+    }
+    ask(stage);
+    if (++stage == kStages) stage = 0;
+    if (++g == groups) {
+      g = 0;
+      ++t;
+      fresh = true;
     }
   }
 }
@@ -240,15 +303,15 @@ cudaError_t launch(RotaryArgs& a, cudaStream_t s) {
   a.lpr_shift = 0;
   while ((NC << a.lpr_shift) < slots) ++a.lpr_shift;
   const int rows = a.H + (APPEND ? 2 : 1) * a.Hkv, at_once = (32 >> a.lpr_shift) * kUnroll;
-  const int groups = (rows + at_once - 1) / at_once, wpb = kThreads / 32;
-  // Few tokens: their rows over several warps, up to 16 warps an SM.
-  const long long fill = 16LL * device_sm_count();
-  long long parts = (fill + a.T - 1) / a.T;
-  a.parts = (int)(parts > groups ? groups : parts);
-  long long blocks = ((long long)a.T * a.parts + wpb - 1) / wpb;
-  const long long most = 8LL * device_sm_count();
-  blocks = blocks > most ? most : blocks;
-  return launch_pdl(rotary_kernel<T, VEC, NC, INTERLEAVED, APPEND>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+  a.groups = (rows + at_once - 1) / at_once;
+  const long long units = (long long)a.T * a.groups, most = (long long)kBlocks * device_sm_count();
+  const long long blocks = (units + kWarps - 1) / kWarps;
+  auto kern = rotary_kernel<T, VEC, NC, INTERLEAVED, APPEND>;
+  constexpr size_t bytes = 1024 + kWarps * warp_smem<VEC * (int)sizeof(T), NC>();
+  static std::atomic<int> done{0};
+  const cudaError_t e = allow_smem(kern, bytes, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), bytes, s, a);
 }
 
 template <bool APPEND>
