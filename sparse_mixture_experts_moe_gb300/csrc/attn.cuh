@@ -169,7 +169,7 @@ struct RotaryArgs {
   const void *q, *k, *v;
   long long qs, ks, vs;  // token strides in elements
   const void *qw, *kw;   // norm weights (nullptr: no norm)
-  float eps;
+  float eps, inv_d;      // inv_d: 1 / D
   void *qo, *ko;
   long long qos, kos;
   const int32_t* positions;

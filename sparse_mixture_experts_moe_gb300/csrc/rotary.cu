@@ -23,7 +23,7 @@
 namespace moe {
 namespace {
 
-constexpr int kUnroll = 2, kStages = 4, kThreads = 256, kWarps = kThreads / 32, kBlocks = 2;
+constexpr int kUnroll = 1, kStages = 6, kThreads = 256, kWarps = kThreads / 32, kBlocks = 2;
 
 template <int BYTES> struct Raw;  // a chunk as it lies in memory
 template <> struct Raw<16> { using T = uint4; };
@@ -109,23 +109,37 @@ __device__ __forceinline__ void copy_chunk(uint32_t dst, const void* src) {
   }
 }
 
-template <int CHUNK, int NC> constexpr int warp_smem() { return kStages * kUnroll * NC * 2 * 32 * CHUNK; }
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
-template <typename T, int VEC, int NC, bool INTERLEAVED, bool APPEND>
+template <int CHUNK, int NC> constexpr int warp_smem() { return kStages * kUnroll * NC * 2 * 32 * CHUNK; }
+constexpr int kTables = 128 * 8 + 2 * 256 * 4;  // the pairs' frequencies, and both norms' weights in fp32
+
+// WHOLE: every element turns. NORM: there are weights.
+template <typename T, int VEC, int NC, bool INTERLEAVED, bool APPEND, bool WHOLE, bool NORM>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 rotary_kernel(const __grid_constant__ RotaryArgs a) {
   using C = Chunk<T, VEC>;
   using R4 = typename C::R;
-  constexpr int CB = VEC * (int)sizeof(T);
+  constexpr int CB = VEC * (int)sizeof(T), V2 = VEC / 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint64_t* turns = reinterpret_cast<uint64_t*>(smem);  // [R / 2]
+  uint64_t* turns = reinterpret_cast<uint64_t*>(smem);           // [R / 2]
+  float* weights = reinterpret_cast<float*>(smem + 128 * 8);      // of queries [D] and keys (256 on)
   griddep_launch_dependents();
   griddep_wait();
   const int D = a.D, R = a.rot.R;
   for (int i = threadIdx.x; i < R / 2; i += kThreads) turns[i] = a.rot.turns[i];
+  if (NORM)
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+      weights[i] = a.qw != nullptr ? to_f32<T>(((const T*)a.qw)[i]) : 1.f;
+      weights[256 + i] = a.kw != nullptr ? to_f32<T>(((const T*)a.kw)[i]) : 1.f;
+    }
   __syncthreads();
   const int lane = threadIdx.x & 31, lpr = 1 << a.lpr_shift, me = lane & (lpr - 1), rpw = 32 >> a.lpr_shift;
-  uint8_t* mine = smem + 1024 + (threadIdx.x >> 5) * warp_smem<CB, NC>() + lane * CB;  // chunk i of a stage: + i 32 CB
+  uint8_t* mine = smem + kTables + (threadIdx.x >> 5) * warp_smem<CB, NC>() + lane * CB;  // chunk i of a stage: + i 32 CB
   // this lane's chunks: elements, whether they exist, and the first of their pairs
   int at[NC][2], pair[NC][2];
   bool in[NC][2];
@@ -149,28 +163,25 @@ rotary_kernel(const __grid_constant__ RotaryArgs a) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) in[y][x] = at[y][x] < D;
   }
-  typename C::U qw[NC][2], kw[NC][2];
-#pragma unroll
-  for (int y = 0; y < NC; ++y)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (a.qw != nullptr && in[y][x]) qw[y][x].r = *reinterpret_cast<const R4*>((const T*)a.qw + at[y][x]);
-      if (a.kw != nullptr && in[y][x]) kw[y][x].r = *reinterpret_cast<const R4*>((const T*)a.kw + at[y][x]);
-    }
-  const int rows = a.H + (APPEND ? 2 : 1) * a.Hkv, groups = a.groups;
+  const int H = a.H, Hk = H + a.Hkv, rows = H + (APPEND ? 2 : 1) * a.Hkv, groups = a.groups;
   const long long warps = (long long)gridDim.x * kWarps, w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const long long units = (long long)a.T * groups, u0 = units * w / warps, u1 = units * (w + 1) / warps;
-  // the unit whose copies are asked for next
-  long long next = u0;
-  int nt = (int)(u0 / groups), ng = (int)(u0 - (long long)nt * groups);
+  const int step = kUnroll * rpw, row_in = lane >> a.lpr_shift;
+  // Row r of a token's queries, keys and values (and results) is at its array's base + r D, the bases moved back by the rows
+  // before. The unit whose copies are asked for next: its first row, and the bases of its token.
+  long long left = u1 - u0;
+  int t = (int)(u0 / groups), g = (int)(u0 - (long long)t * groups);
+  int ng = g;
+  const T* nq = (const T*)a.q + t * a.qs;
+  const T* nk = (const T*)a.k + t * a.ks - (long long)H * D;
+  const T* nv = (const T*)a.v + t * a.vs - (long long)Hk * D;
   auto ask = [&](int stage) {
-    if (next < u1) {
+    if (left > 0) {
+      --left;
 #pragma unroll
       for (int z = 0; z < kUnroll; ++z) {
-        const int r = (ng * kUnroll + z) * rpw + (lane >> a.lpr_shift);
-        const T* src = r < a.H ? (const T*)a.q + nt * a.qs + (long long)r * D
-                     : r < a.H + a.Hkv ? (const T*)a.k + nt * a.ks + (long long)(r - a.H) * D
-                                       : (const T*)a.v + nt * a.vs + (long long)(r - a.H - a.Hkv) * D;
+        const int r = ng * step + z * rpw + row_in;
+        const T* src = (r < H ? nq : !APPEND || r < Hk ? nk : nv) + r * D;
 #pragma unroll
         for (int y = 0; y < NC; ++y)
 #pragma unroll
@@ -178,108 +189,153 @@ rotary_kernel(const __grid_constant__ RotaryArgs a) {
             if (r < rows && in[y][x])
               copy_chunk<CB>(smem_u32(mine + (((stage * kUnroll + z) * NC + y) * 2 + x) * 32 * CB), src + at[y][x]);
       }
-      ++next;
       if (++ng == groups) {
         ng = 0;
-        ++nt;
+        nq += a.qs;
+        nk += a.ks;
+        if (APPEND) nv += a.vs;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int st = 0; st < kStages; ++st) ask(st);
-  int t = (int)(u0 / groups), g = (int)(u0 - (long long)t * groups), position = 0, ahead = 0;
+  int position = 0, ahead = 0;
   if (!APPEND && u0 < u1) ahead = a.positions[t];
   bool fresh = true, ok = true;  // a token's first unit here; it has a place
   Place place;
-  float c[NC][VEC], s[NC][VEC];
+  // cosines and sines: of pairs i, i + 1 side by side (half), or of pair i twice, the sine as (-s, s) (interleaved)
+  uint64_t c2[NC][INTERLEAVED ? VEC : V2 > 0 ? V2 : 1], s2[NC][INTERLEAVED ? VEC : V2 > 0 ? V2 : 1];
+  T *dq = nullptr, *dk = nullptr, *dv = nullptr;  // where the results' rows begin
+  const int kv_row = APPEND ? a.c.page_size * D : D;
   int stage = 0;
   for (long long u = u0; u < u1; ++u) {
     if (fresh) {
       fresh = false;
+      dq = (T*)a.qo + t * a.qos;
       if (APPEND) {
         ok = place.find(a, t);
         position = place.position;
         if (!ok && g == 0 && lane == 0) record_error(a.status, MOE_ERR_DEVICE_CHECK, t);
+        const long long first = ((long long)place.page * a.Hkv * a.c.page_size + (position & (a.c.page_size - 1))) * D;
+        dk = (T*)a.kp + first - (long long)H * kv_row;
+        dv = (T*)a.vp + first - (long long)Hk * kv_row;
       } else {
         position = ahead;
         if (t + 1 < a.T) ahead = a.positions[t + 1];
+        dk = (T*)a.ko + t * a.kos - (long long)H * D;
       }
 #pragma unroll
-      for (int y = 0; y < NC; ++y)
+      for (int y = 0; y < NC; ++y) {
+        float c[VEC], s[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const int p = INTERLEAVED ? pair[y][2 * i / VEC] + i % (VEC / 2 > 0 ? VEC / 2 : 1) : pair[y][0] + i;
-          cos_sin((uint64_t)(long long)position * (p < R / 2 ? turns[p] : 0ull), c[y][i], s[y][i]);
-          c[y][i] *= a.rot.magnitude;
-          s[y][i] *= a.rot.magnitude;
+          const int p = INTERLEAVED ? pair[y][2 * i / VEC] + i % (V2 > 0 ? V2 : 1) : pair[y][0] + i;
+          cos_sin((uint64_t)(long long)position * (p < R / 2 ? turns[p] : 0ull), c[i], s[i]);
+          c[i] *= a.rot.magnitude;
+          s[i] *= a.rot.magnitude;
         }
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            c2[y][i] = f2_pack(c[i], c[i]);
+            s2[y][i] = f2_pack(-s[i], s[i]);
+          }
+        } else if constexpr (VEC > 1) {
+#pragma unroll
+          for (int i = 0; i < V2; ++i) {
+            c2[y][i] = f2_pack(c[2 * i], c[2 * i + 1]);
+            s2[y][i] = f2_pack(s[2 * i], s[2 * i + 1]);
+          }
+        } else {
+          c2[y][0] = f2_pack(c[0], c[0]);
+          s2[y][0] = f2_pack(s[0], s[0]);
+        }
+      }
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 #pragma unroll
     for (int z = 0; z < kUnroll; ++z) {
-      const int r = (g * kUnroll + z) * rpw + (lane >> a.lpr_shift);
-      const bool is_q = r < a.H, is_v = r >= a.H + a.Hkv;
+      const int r = g * step + z * rpw + row_in;
+      const bool is_q = r < H, is_v = APPEND && r >= Hk;
       typename C::U u4[NC][2];
 #pragma unroll
       for (int y = 0; y < NC; ++y)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           u4[y][x].r = *reinterpret_cast<const R4*>(mine + (((stage * kUnroll + z) * NC + y) * 2 + x) * 32 * CB);
-      float f[NC][2][VEC];
+      // elements 2 i, 2 i + 1 of a chunk in one register pair (a chunk of one: twice)
+      constexpr int N2 = V2 > 0 ? V2 : 1;
+      uint64_t f[NC][2][N2];
 #pragma unroll
       for (int y = 0; y < NC; ++y)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) f[y][x][i] = to_f32<T>(u4[y][x].e[i]);
-      if (a.qw != nullptr || a.kw != nullptr) {
-        float sum = 0.f;
+          for (int i = 0; i < N2; ++i)
+            f[y][x][i] = f2_pack(to_f32<T>(u4[y][x].e[VEC > 1 ? 2 * i : 0]), to_f32<T>(u4[y][x].e[VEC > 1 ? 2 * i + 1 : 0]));
+      if (NORM) {
+        uint64_t sum2 = 0ull;
 #pragma unroll
         for (int y = 0; y < NC; ++y)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             if (r < rows && in[y][x])
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) sum = fmaf(f[y][x][i], f[y][x][i], sum);
+              for (int i = 0; i < N2; ++i) sum2 = ffma2(f[y][x][i], f[y][x][i], sum2);
+        float sum = VEC > 1 ? f2_lo(sum2) + f2_hi(sum2) : f2_lo(sum2);
         for (int m = lpr >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const float inv = rsqrtf(sum / (float)D + a.eps);
-        if ((is_q ? a.qw : a.kw) != nullptr)
+        const float inv = (is_q ? a.qw : a.kw) != nullptr ? rsqrtf(fmaf(sum, a.inv_d, a.eps)) : 1.f;
+        const uint64_t inv2 = f2_pack(inv, inv);
+        const float* wt = weights + (is_q ? 0 : 256);
 #pragma unroll
-          for (int y = 0; y < NC; ++y)
+        for (int y = 0; y < NC; ++y)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) f[y][x][i] = f[y][x][i] * inv * to_f32<T>(is_q ? qw[y][x].e[i] : kw[y][x].e[i]);
+            for (int i = 0; i < N2; ++i) {
+              // (past the head's end what is read is not used)
+              const uint64_t w2 = VEC > 1 ? *reinterpret_cast<const uint64_t*>(wt + (in[y][x] ? at[y][x] : 0) + 2 * i)
+                                          : f2_pack(wt[in[y][x] ? at[y][x] : 0], 0.f);
+              f[y][x][i] = fmul2(fmul2(f[y][x][i], inv2), w2);
+            }
       }
       if (r >= rows || !ok) continue;
-      T* dst;
-      if (is_q) dst = (T*)a.qo + t * a.qos + (long long)r * D;
-      else if (!APPEND) dst = (T*)a.ko + t * a.kos + (long long)(r - a.H) * D;
-      else dst = (T*)(is_v ? a.vp : a.kp) +
-                 (((long long)place.page * a.Hkv + (is_v ? r - a.H - a.Hkv : r - a.H)) * a.c.page_size + (position & (a.c.page_size - 1))) * D;
+      T* dst = is_q ? dq + r * D : (is_v ? dv : dk) + (APPEND ? (long long)r * kv_row : (long long)(r * D));
 #pragma unroll
       for (int y = 0; y < NC; ++y) {
-        if (!APPEND || !is_v) {
-          if (INTERLEAVED) {
+        if (!is_v) {
+          uint64_t o[2][N2];
+          if constexpr (INTERLEAVED) {
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int i = 0; i < VEC / 2; ++i) {
-                const float p = f[y][x][2 * i], q = f[y][x][2 * i + 1], cc = c[y][x * (VEC / 2) + i], ss = s[y][x * (VEC / 2) + i];
-                const bool on = pair[y][x] + i < R / 2;
-                u4[y][x].e[2 * i] = from_f32<T>(on ? fmaf(p, cc, -q * ss) : p);
-                u4[y][x].e[2 * i + 1] = from_f32<T>(on ? fmaf(q, cc, p * ss) : q);
+              for (int i = 0; i < N2; ++i) {
+                const uint64_t v = f[y][x][i], swapped = f2_pack(f2_hi(v), f2_lo(v));
+                const uint64_t turned = ffma2(v, c2[y][x * V2 + i], fmul2(swapped, s2[y][x * V2 + i]));
+                o[x][i] = WHOLE || pair[y][x] + i < R / 2 ? turned : v;
               }
           } else {
-            const bool on = pair[y][0] < R / 2;
+            const bool on = WHOLE || pair[y][0] < R / 2;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const float p = f[y][0][i], q = f[y][1][i];
-              u4[y][0].e[i] = from_f32<T>(on ? fmaf(p, c[y][i], -q * s[y][i]) : p);
-              u4[y][1].e[i] = from_f32<T>(on ? fmaf(q, c[y][i], p * s[y][i]) : q);
+            for (int i = 0; i < N2; ++i) {
+              const uint64_t p = f[y][0][i], q = f[y][1][i], qs = fmul2(q, s2[y][i]);
+              const uint64_t minus = qs ^ 0x8000000080000000ull;
+              o[0][i] = on ? ffma2(p, c2[y][i], minus) : p;
+              o[1][i] = on ? ffma2(p, s2[y][i], fmul2(q, c2[y][i])) : q;
             }
           }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              if constexpr (sizeof(T) == 2 && VEC > 1) {
+                reinterpret_cast<uint32_t*>(&u4[y][x])[i] = pack_bf16x2(f2_lo(o[x][i]), f2_hi(o[x][i]));
+              } else {
+                u4[y][x].e[VEC > 1 ? 2 * i : 0] = from_f32<T>(f2_lo(o[x][i]));
+                if (VEC > 1) u4[y][x].e[VEC > 1 ? 2 * i + 1 : 0] = from_f32<T>(f2_hi(o[x][i]));
+              }
+            }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -296,7 +352,7 @@ rotary_kernel(const __grid_constant__ RotaryArgs a) {
   }
 }
 
-template <typename T, int VEC, int NC, bool INTERLEAVED, bool APPEND>
+template <typename T, int VEC, int NC, bool INTERLEAVED, bool APPEND, bool WHOLE, bool NORM>
 cudaError_t launch(RotaryArgs& a, cudaStream_t s) {
   const int R = a.rot.R, chunks = a.D / VEC;
   const int slots = INTERLEAVED ? (chunks + 1) / 2 : R / (2 * VEC) + ((a.D - R) / VEC + 1) / 2;
@@ -304,30 +360,39 @@ cudaError_t launch(RotaryArgs& a, cudaStream_t s) {
   while ((NC << a.lpr_shift) < slots) ++a.lpr_shift;
   const int rows = a.H + (APPEND ? 2 : 1) * a.Hkv, at_once = (32 >> a.lpr_shift) * kUnroll;
   a.groups = (rows + at_once - 1) / at_once;
+  a.inv_d = 1.f / (float)a.D;
   const long long units = (long long)a.T * a.groups, most = (long long)kBlocks * device_sm_count();
   const long long blocks = (units + kWarps - 1) / kWarps;
-  auto kern = rotary_kernel<T, VEC, NC, INTERLEAVED, APPEND>;
-  constexpr size_t bytes = 1024 + kWarps * warp_smem<VEC * (int)sizeof(T), NC>();
+  auto kern = rotary_kernel<T, VEC, NC, INTERLEAVED, APPEND, WHOLE, NORM>;
+  constexpr size_t bytes = kTables + kWarps * warp_smem<VEC * (int)sizeof(T), NC>();
   static std::atomic<int> done{0};
   const cudaError_t e = allow_smem(kern, bytes, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), bytes, s, a);
 }
 
+template <typename T, int VEC, int NC, bool INTERLEAVED, bool APPEND, bool WHOLE = false>
+cudaError_t launch_norm(RotaryArgs& a, cudaStream_t s) {
+  return a.qw != nullptr || a.kw != nullptr ? launch<T, VEC, NC, INTERLEAVED, APPEND, WHOLE, true>(a, s)
+                                            : launch<T, VEC, NC, INTERLEAVED, APPEND, WHOLE, false>(a, s);
+}
+
+template <bool APPEND, typename T>
+cudaError_t launch_type(RotaryArgs& a, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int half = a.rot.R / 2;
+  const bool whole = a.rot.R == a.D;
+  if (a.rot.layout == MOE_ROTARY_INTERLEAVED)
+    return whole ? launch_norm<T, V, 1, true, APPEND, true>(a, s) : launch_norm<T, V, 1, true, APPEND>(a, s);
+  if (half % V == 0) return whole ? launch_norm<T, V, 1, false, APPEND, true>(a, s) : launch_norm<T, V, 1, false, APPEND>(a, s);
+  if (V > 4 && half % 4 == 0) return launch_norm<T, 4, 1, false, APPEND>(a, s);
+  if (half % 2 == 0) return launch_norm<T, 2, 2, false, APPEND>(a, s);
+  return launch_norm<T, 1, 4, false, APPEND>(a, s);
+}
+
 template <bool APPEND>
 cudaError_t launch(RotaryArgs& a, int dt, cudaStream_t s) {
-  const int half = a.rot.R / 2;
-  if (dt == MOE_DTYPE_BF16) {
-    if (a.rot.layout == MOE_ROTARY_INTERLEAVED) return launch<__nv_bfloat16, 8, 1, true, APPEND>(a, s);
-    if (half % 8 == 0) return launch<__nv_bfloat16, 8, 1, false, APPEND>(a, s);
-    if (half % 4 == 0) return launch<__nv_bfloat16, 4, 1, false, APPEND>(a, s);
-    if (half % 2 == 0) return launch<__nv_bfloat16, 2, 2, false, APPEND>(a, s);
-    return launch<__nv_bfloat16, 1, 4, false, APPEND>(a, s);
-  }
-  if (a.rot.layout == MOE_ROTARY_INTERLEAVED) return launch<float, 4, 1, true, APPEND>(a, s);
-  if (half % 4 == 0) return launch<float, 4, 1, false, APPEND>(a, s);
-  if (half % 2 == 0) return launch<float, 2, 2, false, APPEND>(a, s);
-  return launch<float, 1, 4, false, APPEND>(a, s);
+  return dt == MOE_DTYPE_BF16 ? launch_type<APPEND, __nv_bfloat16>(a, s) : launch_type<APPEND, float>(a, s);
 }
 
 }  // namespace
