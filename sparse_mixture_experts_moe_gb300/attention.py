@@ -25,7 +25,7 @@ import threading
 
 from . import _lib
 from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
-from .rotary import Rotary, _alone, _tokens, _weight
+from .rotary import Rotary, _check_overlap, _result, _tokens, _weight
 
 
 _HEADER = 256           # bytes of a workspace's header
@@ -328,6 +328,7 @@ class KVCache(_Bound):
         self._plan = ctypes.create_string_buffer(n)
         _check(self._lib.moe_cache_plan(self._ref, ctypes.addressof(self._plan), n), "moe_cache_plan")
         self._c.plan = ctypes.addressof(self._plan)
+        self._append, self._last_append = self._lib.moe_cache_append, (None, None)
 
     @classmethod
     def create(cls, n_layers, n_pages, page_size, n_slots, max_len, kv_heads, head_dim, dtype, device="cuda"):
@@ -391,48 +392,68 @@ class KVCache(_Bound):
         Rotary) on the way. With q [total, heads, head_dim], the queries of the same tokens, these are normed (q_weight) and
         turned in the same pass, into q_out if given (it may be q itself); returns them, else None. Norm: x / sqrt(mean x^2 +
         eps) * weight."""
-        total, ks = _heads(k, "k", self.kv_heads, self.head_dim, self.dtype, self._dev)
-        tv, vs = _heads(v, "v", self.kv_heads, self.head_dim, self.dtype, self._dev)
-        if tv != total:
-            raise ValueError(f"moe: k has {total} tokens, v has {tv}")
-        n = _ints(slots, "slots", None, self._dev, self._i32)
-        _ints(offsets, "offsets", n + 1, self._dev, self._i32)
-        _ints(pos, "pos", n, self._dev, self._i32)
-        if rotary is not None and (not isinstance(rotary, Rotary) or rotary.head_dim != self.head_dim):
-            raise ValueError(f"moe: rotary must be a Rotary of head_dim {self.head_dim}")
-        wk, wq = (_weight(w, name, self.head_dim, self.dtype, self._dev) for w, name in ((k_weight, "k_weight"), (q_weight, "q_weight")))
-        H = qs = qso = 0
-        q_at = qo_at = None
-        if q is None:
-            if q_weight is not None or q_out is not None:
-                raise ValueError("moe: q_weight and q_out need q")
+        # What the tensors look like decides everything but their addresses: a call like the last one is not checked again.
+        look = (k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(), v.dtype, v.get_device(),
+                slots.shape, slots.dtype, slots.get_device(), slots.is_contiguous(),
+                offsets.shape, offsets.dtype, offsets.get_device(), offsets.is_contiguous(),
+                pos.shape, pos.dtype, pos.get_device(), pos.is_contiguous(),
+                q if q is None else (q.shape, q.stride(), q.dtype, q.get_device()),
+                q_weight if q_weight is None else (q_weight.shape, q_weight.dtype, q_weight.get_device(), q_weight.is_contiguous()),
+                k_weight if k_weight is None else (k_weight.shape, k_weight.dtype, k_weight.get_device(), k_weight.is_contiguous()))
+        last = self._last_append
+        if last[0] != look:
+            last = self._last_append = (look, self._checked_append(k, v, slots, offsets, pos, q, q_weight, k_weight))
+        n, total, ks, vs, H, qs, q_shape = last[1]
+        if rotary is None:
+            turn = None
         else:
-            tq, H, qs = _tokens(q, "q", self.head_dim, self.dtype, self._dev)
-            if tq != total or H == 0:
-                raise ValueError(f"moe: k has {total} tokens, q {tq} with {H} heads")
-            if q_out is None:
-                if stream is not None:  # a tensor made here belongs to the current stream
-                    raise ValueError("moe: pass q_out with an explicit stream")
-                q_out, qso = self._empty((total, H, self.head_dim), dtype=self.dtype, device=self.device), H * self.head_dim
-            else:
-                to, _, qso = _tokens(q_out, "q_out", self.head_dim, self.dtype, self._dev, H)
-                if to != total:
-                    raise ValueError(f"moe: expected q_out {tuple(q.shape)}, got {tuple(q_out.shape)}")
-                if total > 0:
-                    for x in (q, k, v):
-                        _alone(q_out, x, "q_out")
-            q_at, qo_at = q.data_ptr(), q_out.data_ptr()
+            if not isinstance(rotary, Rotary) or rotary.head_dim != self.head_dim:
+                raise ValueError(f"moe: rotary must be a Rotary of head_dim {self.head_dim}")
+            turn = rotary._ref
+        qso = H * self.head_dim
+        if q_out is not None:
+            if q is None:
+                raise ValueError("moe: q_out needs q")
+            qso = _result(q_out, "q_out", total, H, self.head_dim, self.dtype, self._dev)
+            if total > 0:
+                _check_overlap((("q_out", q_out),), (q, k, v))
+        elif q is not None:
+            if stream is not None:  # a tensor made here belongs to the current stream
+                raise ValueError("moe: pass q_out with an explicit stream")
+            q_out = self._empty(q_shape, dtype=self.dtype, device=self.device)
         if self._many and self._current_device() != self._dev:  # kernels run on the current device
             self._elsewhere(self._dev)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
             ws = self._workspace(s)
-            rc = self._lib.moe_cache_append(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total,
-                                            None if rotary is None else rotary._ref, k.data_ptr(), v.data_ptr(), ks, vs, wk, q_at,
-                                            qs, H, wq, float(eps), qo_at, qso, ws[2], ws[1], s)
+            rc = self._append(self._ref, layer, slots.data_ptr(), offsets.data_ptr(), pos.data_ptr(), n, total, turn,
+                              k.data_ptr(), v.data_ptr(), ks, vs, k_weight if k_weight is None else k_weight.data_ptr(),
+                              q if q is None else q.data_ptr(), qs, H, q_weight if q_weight is None else q_weight.data_ptr(), eps,
+                              q if q is None else q_out.data_ptr(), qso, ws[2], ws[1], s)
         if rc != MOE_OK:
             raise MoeError(rc, "moe_cache_append")
         return q_out
+
+    def _checked_append(self, k, v, slots, offsets, pos, q, q_weight, k_weight):
+        D, dtype, dev = self.head_dim, self.dtype, self._dev
+        total, ks = _heads(k, "k", self.kv_heads, D, dtype, dev)
+        tv, vs = _heads(v, "v", self.kv_heads, D, dtype, dev)
+        if tv != total:
+            raise ValueError(f"moe: k has {total} tokens, v has {tv}")
+        n = _ints(slots, "slots", None, dev, self._i32)
+        _ints(offsets, "offsets", n + 1, dev, self._i32)
+        _ints(pos, "pos", n, dev, self._i32)
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _weight(w, name, D, dtype, dev)
+        if q is None:
+            if q_weight is not None:
+                raise ValueError("moe: q_weight needs q")
+            return n, total, ks, vs, 0, 0, None
+        tq, H, qs = _tokens(q, "q", D, dtype, dev)
+        if tq != total or H == 0:
+            raise ValueError(f"moe: k has {total} tokens, q {tq} with {H} heads")
+        return n, total, ks, vs, H, qs, (total, H, D)
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
@@ -494,7 +515,7 @@ class Attention(_Bound):
         self._prompt, self._decode = self._lib.moe_attention_prompt, self._lib.moe_attention_decode
         self._prompt_ex, self._decode_ex = self._lib.moe_attention_prompt_ex, self._lib.moe_attention_decode_ex
         self._chunk, self._chunk_ex = self._lib.moe_attention_chunk, self._lib.moe_attention_chunk_ex
-        self._chunk_sized, self._chunk_bytes = None, 0
+        self._chunk_sized, self._chunk_bytes, self._last_chunk = None, 0, (None, None)
         self._capturing, self._recording = torch._C._cuda_isCurrentStreamCapturing, self._lib.moe_stream_capture_id
         self._key = (self.kv_heads, self.head_dim, self.dtype)
         self._need = {}
@@ -616,10 +637,20 @@ class Attention(_Bound):
         if cache._key != self._key:
             raise ValueError(f"moe: the cache holds {cache.kv_heads} heads of {cache.head_dim} in {cache.dtype}, the "
                              f"attention {self.kv_heads} of {self.head_dim} in {self.dtype}")
-        Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
-        n = _ints(slots, "slots", None, dev, self._i32)
-        _ints(q_offsets, "q_offsets", n + 1, dev, self._i32)
-        out, so = self._out(q, qs, out, lse, stream, dev)
+        # What the tensors look like decides everything but their addresses: a call like the last one is not checked again.
+        look = (q.shape, q.stride(), q.dtype, q.get_device(), slots.shape, slots.dtype, slots.get_device(), slots.is_contiguous(),
+                q_offsets.shape, q_offsets.dtype, q_offsets.get_device(), q_offsets.is_contiguous(), dev)
+        last = self._last_chunk
+        if last[0] != look:
+            Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
+            n = _ints(slots, "slots", None, dev, self._i32)
+            _ints(q_offsets, "q_offsets", n + 1, dev, self._i32)
+            last = self._last_chunk = (look, (n, Tq, qs, (Tq, self.heads, self.head_dim)))
+        n, Tq, qs, shape = last[1]
+        if out is None and lse is None and stream is None:
+            out, so = self._empty(shape, dtype=self.dtype, device=q.device), self.heads * self.head_dim
+        else:
+            out, so = self._out(q, qs, out, lse, stream, dev)
         if self._many and self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)

@@ -710,11 +710,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       };
       auto pv = [&](int t, int st, bool acc) {
         const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes + (PAGED && dual ? t * (BK / 2) * 128 : 0), BK * 128, 1024);
-        const int steps = PAGED && dual ? BK / 32 : BK / 16;
         if (!leader) return;
+        if (PAGED && dual) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                          acc || kk != 0);
+          tc_commit(bar(ODONE + t));
+          return;
+        }
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          if (!PAGED || kk < steps) tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+          tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
                         acc || kk != 0);
         tc_commit(bar(ODONE + t));
       };
@@ -905,8 +912,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const uint64_t sum = fadd2(sum0, sum1);
         l += f2_lo(sum) + f2_hi(sum);
       };
+      const bool halves = dual;
       for (int j = 0; j < n && ok; ++j) {
-        if (PAGED && it->dual) block(std::integral_constant<int, BK / 2>{}, j);
+        if (PAGED && halves) block(std::integral_constant<int, BK / 2>{}, j);
         else block(std::integral_constant<int, BK>{}, j);
         done += ok ? 1 : 0;
       }

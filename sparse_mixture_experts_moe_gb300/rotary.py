@@ -25,44 +25,70 @@ class _Rotary(ctypes.Structure):
                 ("turns", ctypes.c_uint64 * 128)]
 
 
-def _tokens(t, name, dim, dtype, dev, heads=None):
+# The checks below run on every call, where a decode step's kernel takes a few microseconds: each looks at a tensor's
+# attributes once and formats a message only when it refuses.
+def _tokens(t, name, dim, dtype, dev):
     """Checks a [T, heads, dim] tensor on CUDA device `dev` whose heads are dense within a token; returns (T, heads, token
     stride)."""
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads) or t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError(f"moe: expected {name} [T, {'heads' if heads is None else heads}, {dim}] in {dtype} on cuda:{dev}, got "
-                         f"{tuple(shape)} in {t.dtype} on {t.device}")
+    if t.dim() != 3 or t.dtype is not dtype or t.get_device() != dev:
+        _not_tokens(t, name, dim, dtype, dev)
+    T, n, d = t.shape
     st, sh, sd = t.stride()
-    T, n = shape[0], shape[1]
-    if T > 0 and (sd != 1 or (sh != dim and n > 1)):
-        raise ValueError(f"moe: {name} must have dense heads within a token (strides {t.stride()})")
+    if d != dim or ((sd != 1 or (sh != dim and n > 1)) and T > 0):
+        _not_tokens(t, name, dim, dtype, dev)
     return T, n, (st if T > 1 else n * dim)  # (a single token's stride means nothing)
 
 
+def _not_tokens(t, name, dim, dtype, dev):
+    raise ValueError(f"moe: expected {name} [T, heads, {dim}] in {dtype} on cuda:{dev}, heads dense within a token, got "
+                     f"{tuple(t.shape)} in {t.dtype} on {t.device} (strides {t.stride()})")
+
+
+def _result(t, name, T, heads, dim, dtype, dev):
+    """Checks an output [T, heads, dim]; returns its token stride."""
+    n, h, stride = _tokens(t, name, dim, dtype, dev)
+    if n != T or h != heads:
+        raise ValueError(f"moe: expected {name} [{T}, {heads}, {dim}], got {tuple(t.shape)}")
+    return stride
+
+
 def _weight(w, name, dim, dtype, dev):
-    """Address of a norm's weights, None without."""
-    if w is None:
-        return None
+    """Address of a norm's weights."""
     if w.dim() != 1 or w.shape[0] != dim or w.dtype is not dtype or w.get_device() != dev or not w.is_contiguous():
         raise ValueError(f"moe: {name} must be a contiguous [{dim}] tensor in {dtype} on cuda:{dev}")
     return w.data_ptr()
 
 
-def _alone(out, x, name):
-    """Refuses an output that shares memory with an input which is not the very same tensor: a warp may write there before
-    another has read it."""
-    a, b = out.data_ptr(), x.data_ptr()
-    if a == b and (out.stride(0) == x.stride(0) or x.shape[0] < 2):
-        return
-    end_a = a + ((out.shape[0] - 1) * out.stride(0) + out.shape[1] * out.shape[2]) * out.element_size()
-    end_b = b + ((x.shape[0] - 1) * x.stride(0) + x.shape[1] * x.shape[2]) * x.element_size()
-    if a >= end_b or b >= end_a:
-        return
-    # slices of one fused tensor: the same token stride, and apart within a token
-    row, size = x.stride(0) * x.element_size(), out.element_size() * out.shape[2]
-    off = (a - b) % row if out.stride(0) == x.stride(0) else 0
-    if not (out.stride(0) == x.stride(0) and off >= x.shape[1] * size and off + out.shape[1] * size <= row):
-        raise ValueError(f"moe: {name} overlaps an input without being that input")
+def _apart(a, b):
+    """Whether two [T, heads, dim] tensors share no element: their extents do not meet, or they are different heads of one
+    fused tensor."""
+    size = a.element_size()
+    at, bt = a.data_ptr(), b.data_ptr()
+    end = [p + ((x.shape[0] - 1) * x.stride(0) + x.shape[1] * x.shape[2]) * size for p, x in ((at, a), (bt, b))]
+    if at >= end[1] or bt >= end[0]:
+        return True
+    row = a.stride(0) * size
+    if a.stride(0) != b.stride(0) or a.shape[0] < 2 or b.shape[0] < 2:
+        return False
+    off = (bt - at) % row  # of b's heads behind a's in a token's row
+    return off >= a.shape[1] * a.shape[2] * size and off + b.shape[1] * b.shape[2] * size <= row
+
+
+def _check_overlap(outs, inputs):
+    """Refuses outputs that share memory with each other, or with an input that is not the very same tensor: a warp might write
+    there before another has read it."""
+    outs = [(name, o) for name, o in outs if o is not None]
+    for i, (name, o) in enumerate(outs):
+        for x, theirs in zip(inputs, ("out", "k_out", "")):
+            if x is None:
+                continue
+            same = (name == theirs or name == "q_out" and theirs == "out") and o.data_ptr() == x.data_ptr() and (
+                o.stride(0) == x.stride(0) or o.shape[0] < 2)
+            if not same and not _apart(o, x):
+                raise ValueError(f"moe: {name} overlaps an input without being that input")
+        for other, p in outs[i + 1:]:
+            if not _apart(o, p):
+                raise ValueError(f"moe: {name} and {other} overlap")
 
 
 class Rotary:
@@ -114,6 +140,8 @@ class Rotary:
         self._i32 = torch.int32
         self._dtypes = {torch.bfloat16: _lib.MOE_DTYPE_BF16, torch.float32: _lib.MOE_DTYPE_F32}
         self._empty = torch.empty
+        self._call = self._lib.moe_rotary_apply
+        self._last = (None, None)
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._current_device, self._many = torch._C._cuda_getDevice, torch.cuda.device_count() > 1
 
@@ -126,60 +154,79 @@ class Rotary:
         """The pairs' frequencies, radians a position (below a whole turn)."""
         return [self._c.turns[p] * 2.0 ** -64 * 6.283185307179586 for p in range(self.rotary_dim // 2)]
 
-    def _out(self, x, out, n, name, T, dtype, dev, stream):
-        if out is None:
-            if stream is not None:  # a tensor made here belongs to the current stream
-                raise ValueError(f"moe: pass {name} with an explicit stream")
-            return self._empty((T, n, self.head_dim), dtype=dtype, device=x.device), n * self.head_dim
-        to, _, so = _tokens(out, name, self.head_dim, dtype, dev, n)
-        if to != T:
-            raise ValueError(f"moe: expected {name} {tuple(x.shape)}, got {tuple(out.shape)}")
-        return out, so
-
     def apply(self, q, positions, k=None, q_weight=None, k_weight=None, eps=1e-6, out=None, k_out=None, stream=None):
         """q [T, heads, head_dim] and k [T, kv_heads, head_dim] (optional) of the tokens at positions [T] (int32, any sign).
         With q_weight / k_weight [head_dim] (their type) each head is first x / sqrt(mean x^2 + eps) * weight. Returns q's
         result, or (q's, k's) where there is k; out and k_out may be q and k themselves."""
-        dev = q.get_device()
-        if dev < 0:
-            raise ValueError(f"moe: q must be a CUDA tensor (got one on {q.device})")
-        dtype = q.dtype
-        dt = self._dtypes.get(dtype)
-        if dt is None:
-            raise TypeError(f"unsupported dtype {dtype}")
-        T, H, qs = _tokens(q, "q", self.head_dim, dtype, dev)
-        if positions.dtype is not self._i32 or positions.get_device() != dev or positions.shape != (T,) or not positions.is_contiguous():
-            raise ValueError(f"moe: positions must be a contiguous int32 tensor [{T}] on cuda:{dev}")
-        wq, wk = _weight(q_weight, "q_weight", self.head_dim, dtype, dev), _weight(k_weight, "k_weight", self.head_dim, dtype, dev)
-        if H == 0:
-            raise ValueError("moe: q has no heads")
-        given, k_given = out, k_out
-        if k is None:
-            if k_out is not None or k_weight is not None:
-                raise ValueError("moe: k_out and k_weight need k")
-            Hk, ks, kso, k_at, ko_at = 0, 0, 0, None, None
+        # What the tensors look like decides everything but their addresses: a call like the last one is not checked again.
+        look = (q.shape, q.stride(), q.dtype, q.get_device(), positions.shape, positions.dtype, positions.get_device(),
+                positions.is_contiguous(),
+                k if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
+                q_weight if q_weight is None else (q_weight.shape, q_weight.dtype, q_weight.get_device(), q_weight.is_contiguous()),
+                k_weight if k_weight is None else (k_weight.shape, k_weight.dtype, k_weight.get_device(), k_weight.is_contiguous()))
+        last = self._last
+        if last[0] != look:
+            last = self._last = (look, self._checked(q, positions, k, q_weight, k_weight))
+        dev, dtype, dt, T, H, qs, Hk, ks, q_shape, k_shape = last[1]
+        if out is None and k_out is None:
+            if stream is not None:  # tensors made here belong to the current stream
+                raise ValueError("moe: pass out (and k_out) with an explicit stream")
+            out, qso = self._empty(q_shape, dtype=dtype, device=q.device), H * self.head_dim
+            if k is not None:
+                k_out = self._empty(k_shape, dtype=dtype, device=q.device)
+            kso = Hk * self.head_dim
         else:
-            Tk, Hk, ks = _tokens(k, "k", self.head_dim, dtype, dev)
-            if Tk != T or Hk == 0:
-                raise ValueError(f"moe: q has {T} tokens, k {Tk} with {Hk} heads")
-            k_out, kso = self._out(k, k_out, Hk, "k_out", T, dtype, dev, stream)
-            k_at, ko_at = k.data_ptr(), k_out.data_ptr()
-        out, qso = self._out(q, out, H, "out", T, dtype, dev, stream)
-        if T > 0:
-            for o, name in ((given, "out"), (k_given, "k_out")):
-                if o is not None:
-                    for x in (q, k):
-                        if x is not None:
-                            _alone(o, x, name)
-            if given is not None and k_given is not None:
-                _alone(given, k_given, "out")
-                if given.data_ptr() == k_given.data_ptr():
-                    raise ValueError("moe: out and k_out are the same memory")
+            out, qso, k_out, kso = self._outs(q, k, out, k_out, last[1], stream)
         if self._many and self._current_device() != dev:  # kernels run on the current device
             raise ValueError(f"moe: the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
-        s = self._raw_stream(dev) if stream is None else _stream(stream)
-        rc = self._lib.moe_rotary_apply(self._ref, q.data_ptr(), qs, H, k_at, ks, Hk, positions.data_ptr(), T, dt, wq, wk,
-                                        float(eps), out.data_ptr(), qso, ko_at, kso, s)
+        rc = self._call(self._ref, q.data_ptr(), qs, H, k if k is None else k.data_ptr(), ks, Hk, positions.data_ptr(), T, dt,
+                        q_weight if q_weight is None else q_weight.data_ptr(), k_weight if k_weight is None else k_weight.data_ptr(),
+                        eps, out.data_ptr(), qso, k if k is None else k_out.data_ptr(), kso,
+                        self._raw_stream(dev) if stream is None else _stream(stream))
         if rc != MOE_OK:
             raise MoeError(rc, "moe_rotary_apply")
         return out if k is None else (out, k_out)
+
+    def _checked(self, q, positions, k, q_weight, k_weight):
+        dev, dtype, D = q.get_device(), q.dtype, self.head_dim
+        if dev < 0:
+            raise ValueError(f"moe: q must be a CUDA tensor (got one on {q.device})")
+        dt = self._dtypes.get(dtype)
+        if dt is None:
+            raise TypeError(f"unsupported dtype {dtype}")
+        T, H, qs = _tokens(q, "q", D, dtype, dev)
+        if H == 0:
+            raise ValueError("moe: q has no heads")
+        if (positions.dtype is not self._i32 or positions.get_device() != dev or positions.shape != (T,)
+                or not positions.is_contiguous()):
+            raise ValueError(f"moe: positions must be a contiguous int32 tensor [{T}] on cuda:{dev}")
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _weight(w, name, D, dtype, dev)
+        if k is None:
+            if k_weight is not None:
+                raise ValueError("moe: k_weight needs k")
+            Hk = ks = 0
+        else:
+            Tk, Hk, ks = _tokens(k, "k", D, dtype, dev)
+            if Tk != T or Hk == 0:
+                raise ValueError(f"moe: q has {T} tokens, k {Tk} with {Hk} heads")
+        return dev, dtype, dt, T, H, qs, Hk, ks, (T, H, D), (T, Hk, D)
+
+    def _outs(self, q, k, out, k_out, call, stream):
+        """Outputs of which the caller gave one or both, and their token strides."""
+        dev, dtype, _, T, H, _, Hk, _, q_shape, k_shape = call
+        if stream is not None and (out is None or (k is not None and k_out is None)):
+            raise ValueError("moe: pass out (and k_out) with an explicit stream")
+        if k is None and k_out is not None:
+            raise ValueError("moe: k_out needs k")
+        if out is None:
+            out = self._empty(q_shape, dtype=dtype, device=q.device)
+        qso, kso = _result(out, "out", T, H, self.head_dim, dtype, dev), 0
+        if k is not None:
+            if k_out is None:
+                k_out = self._empty(k_shape, dtype=dtype, device=q.device)
+            kso = _result(k_out, "k_out", T, Hk, self.head_dim, dtype, dev)
+        if T > 0:
+            _check_overlap((("out", out), ("k_out", k_out)), (q, k))
+        return out, qso, k_out, kso
