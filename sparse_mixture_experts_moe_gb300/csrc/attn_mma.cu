@@ -41,6 +41,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ SharedPart sp) {
   constexpr int NU = DP / 8;  // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
+  // PAGED: where the rows of the tile being loaded and of the one after it lie (found once, not for every 16 bytes)
+  __shared__ long long row_at[PAGED ? 2 : 1][KT];
   griddep_wait();
   griddep_launch_dependents();  // after the wait: the own positions' kernel relies on it
   const uint32_t sQ = smem_u32(smem), sK = sQ + kRows * DP * 2, sV = sK + KT * DP * 2;
@@ -87,15 +89,19 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     return (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D;
   };
 
+  auto find_rows = [&](int j0, int left, int to) {
+    if (tid < KT) row_at[to][tid] = tid < left ? paged(j0 + tid) : 0;
+  };
   auto copy = [&](uint32_t dst, const __nv_bfloat16* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
   };
   // the tile of K or V at j0, `left` keys of it; what is past them and past D becomes zeros
-  auto load = [&](uint32_t dst, const __nv_bfloat16* base, long long stride, int j0, int left) {
+  auto load = [&](uint32_t dst, const __nv_bfloat16* base, long long stride, int j0, int left, int from = 0) {
 #pragma unroll 4
     for (int i = tid; i < KT * NU; i += kThreads) {
       const int r = i / NU, u = i % NU, j = j0 + min(r, left - 1);
-      const long long at = SHARED || PAGED ? paged(j) : (long long)(sq.k0 + j) * stride + (long long)hk * D;
+      const long long at = PAGED ? row_at[from][min(r, left - 1)]
+                         : SHARED ? paged(j) : (long long)(sq.k0 + j) * stride + (long long)hk * D;
       copy(dst + piece<DP>(r, u), base + at + min(u * 8, D - 8), r < left && u * 8 < D);
     }
   };
@@ -104,6 +110,10 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       const int r = i / NU, u = i % NU, R = row0 + min(r, nrows - 1);
       const __nv_bfloat16* row = qb + (long long)(sq.q0 + R / G) * qs + (long long)(hk * G + R % G) * D;
       copy(sQ + piece<DP>(r, u), row + min(u * 8, D - 8), r < nrows && u * 8 < D);
+    }
+    if (PAGED) {
+      find_rows(j_begin, j_end - j_begin, 0);
+      __syncthreads();
     }
     load(sK, kb, a.ks, j_begin, j_end - j_begin);
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -128,7 +138,9 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       lim[y] = visible_keys((row0 + r) / G, sq.nq, sq.nk, a.causal);
     }
   }
-  for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
+  int rows_of = 0;  // PAGED: the half of row_at that has this tile's
+  for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT, rows_of ^= 1) {
+    if (PAGED) find_rows(j0 + KT, left - KT, rows_of ^ 1);  // (the barriers below come before its use)
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();  // K is there
     float s[KT / 8][4];
@@ -149,7 +161,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       }
     }
     __syncthreads();  // K is read
-    if (left > KT) load(sK, kb, a.ks, j0 + KT, left - KT);
+    if (left > KT) load(sK, kb, a.ks, j0 + KT, left - KT, rows_of ^ 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -200,7 +212,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       }
     }
     __syncthreads();  // V is read
-    if (left > KT) load(sV, vb, a.vs, j0 + KT, left - KT);
+    if (left > KT) load(sV, vb, a.vs, j0 + KT, left - KT, rows_of ^ 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");

@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ SharedPart sp) {
   constexpr int NC = DP / (4 * TX);  // groups of 4 columns of a thread
   extern __shared__ __align__(16) float sm[];
+  __shared__ long long row_at[PAGED ? KT : 1];  // PAGED: where the tile's rows lie (found once, not for every 16 bytes)
   griddep_wait();
   griddep_launch_dependents();  // after the wait: the own positions' kernel relies on it
   const DecodeArgs& da = sp.d;
@@ -129,6 +130,15 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
   const float* vb = (const float*)(SHARED || PAGED ? da.v : pa.v);
   // (what is left counts down: positions near 2^31 must not wrap)
   for (int j0 = j_begin, left = j_end - j_begin; left > 0; j0 += KT, left -= KT) {
+    if (PAGED && tid < KT && tid < left) {  // (the tile before is past its loads)
+      const int j = j0 + tid;
+      int page = pages[j >> da.c.page_shift];
+      if (page < 0 || page >= da.c.n_pages) {
+        record_error(pa.status, MOE_ERR_DEVICE_CHECK, seq);
+        page = 0;
+      }
+      row_at[tid] = (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D;
+    }
     __syncthreads();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // K, then V
@@ -138,12 +148,11 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
       for (int i = tid; i < KT * d4; i += kThreads) {
         const int r = i / d4, c = (i % d4) * 4, j = j0 + min(r, left - 1), ce = min(c, D - 4);
         long long at;
-        if (SHARED || PAGED) {
+        if (PAGED) {
+          at = row_at[min(r, left - 1)] + ce;
+        } else if (SHARED) {
           int page = pages[j >> da.c.page_shift];
-          if (page < 0 || page >= da.c.n_pages) {
-            if (PAGED) record_error(pa.status, MOE_ERR_DEVICE_CHECK, seq);
-            page = 0;
-          }
+          page = page < 0 || page >= da.c.n_pages ? 0 : page;
           at = (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D + ce;
         } else {
           at = (long long)(sq.k0 + j) * stride + (long long)hk * D + ce;
@@ -736,12 +745,13 @@ cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
   return C > 1 ? launch_tiles<false, true>(a, none, a.D, grid, s) : launch_tiles<false, false>(a, none, a.D, grid, s);
 }
 
-// Few tiles: a row's keys in pieces, about 8 CTAs an SM altogether, at least two tiles of keys each at the longest
-// length that the cache may hold.
+// Few tiles: a row's keys in pieces, about kPieceCtas CTAs an SM altogether, at least kPieceTiles tiles of keys each at the
+// longest length that the cache may hold.
+constexpr int kPieceCtas = 8, kPieceTiles = 1;
 int chunk_tile_pieces(const CacheView& c, int n, int Tq, int H) {
   const long long ctas = prompt_tile_slots(Tq, n, H / c.Hkv, kRows) * c.Hkv, rows = (long long)Tq * H;
-  const long long most = (long long)c.width * c.page_size / (2 * KT), fit = rows > 0 ? decode_pieces(rows) / rows : 1;
-  long long p = 8LL * device_sm_count() / (ctas > 0 ? ctas : 1);
+  const long long most = ((long long)c.width * c.page_size + kPieceTiles * KT - 1) / (kPieceTiles * KT), fit = rows > 0 ? decode_pieces(rows) / rows : 1;
+  long long p = (long long)kPieceCtas * device_sm_count() / (ctas > 0 ? ctas : 1);
   p = p > most ? most : p;
   p = p > fit ? fit : p;
   return (int)(p < 1 ? 1 : p);
