@@ -70,7 +70,7 @@ template <int DP> struct Cfg {
   static constexpr int kTileBytes = TM * DP * 2;   // a Q tile, and a K or V block
   static constexpr int kStages = DP == 128 ? 4 : 8;
   static constexpr int kStage = 32 * 128;  // bytes of a softmax warp's output staging: 32 rows x 64 bf16 elements
-  static constexpr int kBars = 2 * kStages + 5 * 2 + 1 + 2 * kItems + 1 + 8;
+  static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
   static constexpr size_t kSmem =
       1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 + kItems * sizeof(Item) + 4 * 32 * 8;
 };
@@ -200,8 +200,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 2,
-                ODONE = PFULL + 2, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
+  constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 4,
+                ODONE = PFULL + 4, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
                 TAIL = IEMPTY + kItems, GIVEN = TAIL + 1, TAKEN = GIVEN + 4;
   float2* given_ml = reinterpret_cast<float2*>(gbase + C::kSmem - 1024 - 4 * 32 * 8);  // [warp of tile 1][row]
 
@@ -211,8 +211,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int s = 0; s < C::kStages; ++s) { mbar_init(bar(FULL + s), 1); mbar_init(bar(EMPTY + s), 1); }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(QFULL + t), 1);
-      mbar_init(bar(SFULL + t), 1);
-      mbar_init(bar(PFULL + t), 4);
+      for (int b = 0; b < 4; b += 2) {  // (the second of each is for halves of blocks)
+        mbar_init(bar(SFULL + b + t), 1);
+        mbar_init(bar(PFULL + b + t), 4);
+      }
       mbar_init(bar(ODONE + t), 1);
       mbar_init(bar(QEMPTY + t), 1);
     }
@@ -338,55 +340,63 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       };
       const CacheView& cv = sa.d.c;
       const int box = min(cv.page_size, BK), box_shift = min(cv.page_shift, 7);
+      const bool leader = elect_one();
       bool ok = true;
       while (ok) {
         if (tail && !__all_sync(0xffffffffu, mbar_try_wait(bar(IFULL + iq), iphase)) && !clear_tail()) break;
         const Item* ip = next_item();
         if (ip == nullptr) break;
-        const int key0 = ip->key0, held_all = ip->nk, slot = ip->k0, hk = ip->hk, seq = ip->seq, end = 2 * blocks(ip->n_keys);
+        const int slot = ip->k0, hk = ip->hk, n = blocks(ip->n_keys);
+        int j0 = ip->key0, rest = ip->nk - j0;  // the block's first position, and what the sequence holds from there on
+        const int seq = ip->seq;
         item_done();
         const int32_t* row = cv.table + (long long)slot * cv.width;
-        for (int u = 0; u < end && ok; ++u) {
-          const int j0 = key0 + (u >> 1) * BK, held = min(BK, held_all - j0);
-          const bool is_v = u & 1, cut = is_v && held < BK;
-          if (tail && (++behind > 2 || cut) && !(ok = clear_tail())) break;
+        // The whole warp walks the copies and one elected thread issues them: what they are given stays in uniform registers.
+        for (int j = 0; j < n && ok; ++j, j0 += BK, rest -= BK) {
           // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
           const int col = j0 >> cv.page_shift;
           if (window_slot != slot || window != col >> 5) {
-            auto read = [&](int w) { return (long long)w * 32 + lane < cv.width ? row[w * 32 + lane] : 0; };
+            auto read = [&](int w) {
+              int page = w * 32 + lane < cv.width ? row[w * 32 + lane] : 0;
+              if (page < 0 || page >= cv.n_pages) page = -1;
+              return page;
+            };
             page_now = window_slot == slot && window + 1 == col >> 5 ? page_next : read(col >> 5);
             window_slot = slot;
             window = col >> 5;
             page_next = read(window + 1);
           }
-          int page = __shfl_sync(0xffffffffu, page_now, (col + lane) & 31);
-          const bool mine = lane << box_shift < held;  // a copy a lane
-          if (page < 0 || page >= cv.n_pages) {
-            if (mine) record_error(status, MOE_ERR_DEVICE_CHECK, seq);
-            page = 0;
+          const int held = min(BK, rest), boxes = (held + box - 1) >> box_shift;
+          if (__any_sync(0xffffffffu, page_now < 0 && ((lane - col) & 31) < boxes)) {
+            if (lane == 0) record_error(status, MOE_ERR_DEVICE_CHECK, seq);
           }
-          if (lane == 0) ok = wait_or_abort(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-          if (!ok) break;
-          const uint32_t dst = sKV + stage * C::kTileBytes, b = cut ? bar(TAIL) : bar(FULL + stage);
-          if (lane == 0)
-            mbar_arrive_expect_tx(b, (uint32_t)(((held + box - 1) >> box_shift << box_shift) * C::kChunks * 128));
-          __syncwarp();
-          if (mine) {
-            const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
 #pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(dst + c * (BK * 128) + (lane << box_shift) * 128, is_v ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
+          for (int v = 0; v < 2; ++v) {  // K, then V
+            const bool cut = v == 1 && held < BK;
+            if (tail && (++behind > 2 || cut) && !(ok = clear_tail())) break;
+            ok = warp_wait(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
+            if (!ok) break;
+            const uint32_t b = cut ? bar(TAIL) : bar(FULL + stage);
+            uint32_t dst = sKV + stage * C::kTileBytes;
+            if (leader) mbar_arrive_expect_tx(b, (uint32_t)((boxes << box_shift) * C::kChunks * 128));
+            for (int i = 0; i < boxes; ++i, dst += 128 << box_shift) {
+              const int page = max(0, __shfl_sync(0xffffffffu, page_now, (col + i) & 31));
+              const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
+              if (leader) {
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c) tma_load_3d(dst + c * (BK * 128), v ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
+              }
+            }
+            if (cut) {
+              tail = true;
+              behind = 0;
+              tail_stage = stage;
+              tail_keys = held;
+            }
+            filled |= 1u << stage;
+            fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
           }
-          if (cut) {
-            tail = true;
-            behind = 0;
-            tail_stage = stage;
-            tail_keys = held;
-          }
-          filled |= 1u << stage;
-          fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
       }
       if (!clear_tail() && lane == 0) {  // (given up: the copies are waited for all the same)
@@ -696,7 +706,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc_fence_after();
         return true;
       };
-      auto qk = [&](int t, int st) {
+      auto qk = [&](int t, int st, int b2 = 0) {  // (b2: which half of the tile's columns, by halves of blocks)
         const uint64_t a = make_smem_desc_sw128(sQ + t * C::kTileBytes, 16, 1024);
         const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes + (PAGED && dual ? t * (BK / 2) * 128 : 0), 16, 1024);
         const uint32_t idesc = PAGED && dual ? idesc_half : idesc_qk;
@@ -704,17 +714,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk / 4) * (TM * 128) + (kk % 4) * 32) >> 4);
-          tc_mma_f16(tm + t * BK, a + off, b + off, idesc, kk != 0);
+          tc_mma_f16(tm + t * BK + b2 * (BK / 2), a + off, b + off, idesc, kk != 0);
         }
-        tc_commit(bar(SFULL + t));
+        tc_commit(bar(SFULL + 2 * b2 + t));
       };
-      auto pv = [&](int t, int st, bool acc) {
+      auto pv = [&](int t, int st, bool acc, int b2 = 0) {
         const uint64_t b = make_smem_desc_sw128(sKV + st * C::kTileBytes + (PAGED && dual ? t * (BK / 2) * 128 : 0), BK * 128, 1024);
         if (!leader) return;
         if (PAGED && dual) {
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+            tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + b2 * (BK / 2) + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
                           acc || kk != 0);
           tc_commit(bar(ODONE + t));
           return;
@@ -727,6 +737,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       };
       auto next = [&]() { if (++stage == C::kStages) { stage = 0; phase ^= 1u; } };
       uint32_t pp0 = 0, pp1 = 0, qp0 = 0, qp1 = 0;  // phases of the tiles' P and Q barriers
+      uint32_t pp0b = 0, pp1b = 0;                  // and of the second P barriers
       bool ok = true;
       while (ok) {
         const Item* it = next_item();
@@ -736,6 +747,67 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         dual = PAGED && __shfl_sync(0xffffffffu, it->dual, 0) != 0;
         item_done();
         if (nn == 0) continue;
+        if (dual) {
+          // Both halves' scores are computed two blocks ahead: they take half of the tile's columns each time, so block
+          // j + 1 need not wait for the softmax of block j. Copy i of the item (K0 V0 K1 V1 ..) is in this stage:
+          auto copy_at = [&](int i, int& st, uint32_t& ph) {
+            const int x = stage + i;
+            st = x & (C::kStages - 1);
+            ph = phase ^ ((uint32_t)(x / C::kStages) & 1u);
+          };
+          int st, ks;
+          uint32_t ph, kp;
+          for (int j = 0; j < 2 && j < nn && ok; ++j) {
+            copy_at(2 * j, st, ph);
+            ok = wait(FULL + st, ph);
+            if (ok && j == 0) {
+              ok = wait(QFULL, qp0) && wait(QFULL + 1, qp1);
+              qp0 ^= 1u;
+              qp1 ^= 1u;
+            }
+            if (!ok) break;
+            qk(0, st, j);
+            qk(1, st, j);
+            if (leader) {
+              tc_commit(bar(EMPTY + st));
+              if (j + 1 == nn) {
+                tc_commit(bar(QEMPTY));
+                tc_commit(bar(QEMPTY + 1));
+              }
+            }
+          }
+          for (int j = 0; j < nn && ok; ++j) {
+            const int b2 = j & 1;
+            const bool more = j + 2 < nn;
+            copy_at(2 * j + 1, st, ph);
+            ok = wait3(FULL + st, ph, FULL + st, ph, PFULL + 2 * b2, b2 ? pp0b : pp0);
+            if (!ok) break;
+            pv(0, st, j > 0, b2);
+            ok = wait(PFULL + 2 * b2 + 1, b2 ? pp1b : pp1);
+            if (!ok) break;
+            pv(1, st, j > 0, b2);
+            if (leader) tc_commit(bar(EMPTY + st));
+            if (more) {
+              copy_at(2 * j + 4, ks, kp);
+              ok = wait(FULL + ks, kp);
+              if (!ok) break;
+              qk(0, ks, b2);
+              qk(1, ks, b2);
+            }
+            if (b2) { pp0b ^= 1u; pp1b ^= 1u; } else { pp0 ^= 1u; pp1 ^= 1u; }
+            if (leader) {
+              if (more) tc_commit(bar(EMPTY + ks));
+              if (more && j + 3 == nn) {
+                tc_commit(bar(QEMPTY));
+                tc_commit(bar(QEMPTY + 1));
+              }
+            }
+          }
+          copy_at(2 * nn, st, ph);
+          stage = st;
+          phase = ph;
+          continue;
+        }
         ok = wait(FULL + stage, phase);
         if (ok && n0 > 0) {
           ok = wait(QFULL, qp0);
@@ -795,7 +867,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const float thr = rescale_above(c2);
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const uint32_t tS = tmem + lanes + t * BK, tO = tmem + lanes + 256 + t * DP;
-    uint32_t done = 0;  // blocks of all items so far: their barriers' phases
+    uint32_t done = 0;  // blocks of all items so far: the phase of the last PV's barrier
+    uint32_t seen = 0;  // phases of the scores' barriers, a bit each
     uint32_t given = 0;  // exchanges with the other tile's warp
     bool ok = true;
     while (ok) {
@@ -828,12 +901,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // Block j, of which the tile has COLS keys: 128, or half of them.
       auto block = [&](auto cols, int j) {
         constexpr int NC = decltype(cols)::value / 32;
-        ok = warp_wait(bar(SFULL + t), done & 1, timeout_ns, abort_flag, status, 53);
+        const int b2 = NC < 4 ? j & 1 : 0;  // by halves, blocks alternate between the halves of the tile's columns
+        const uint32_t tB = tS + b2 * (BK / 2);
+        ok = warp_wait(bar(SFULL + 2 * b2 + t), seen >> b2 & 1u, timeout_ns, abort_flag, status, 53);
         if (!ok) return;
+        seen ^= 1u << b2;
         tc_fence_after();
         uint32_t s[NC][32];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) tmem_ld_32x32b_x32(tS + 32 * c, s[c]);
+        for (int c = 0; c < NC; ++c) tmem_ld_32x32b_x32(tB + 32 * c, s[c]);
         tmem_ld_wait();
         const int left = lim - j * BK - (NC < 4 ? t * (BK / 2) : 0);  // columns that this row sees
         if (__any_sync(0xffffffffu, left < 32 * NC)) {
@@ -903,12 +979,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               }
             }
           }
-          tmem_st_32x32b_x32(tS + 32 * h, p);
+          tmem_st_32x32b_x32(tB + 32 * h, p);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PFULL + t));
+        if (NC < 4 && j > 0 && j == n - 1) {
+          // Once this block's weights are given the barrier may go on by two phases, whose parities would look alike, so the
+          // PV before (in flight for one softmax by now) is waited for first.
+          ok = warp_wait(bar(ODONE + t), (done - 1) & 1, timeout_ns, abort_flag, status, 53);
+          if (!ok) return;
+        }
+        if (lane == 0) mbar_arrive(bar(PFULL + 2 * b2 + t));
         const uint64_t sum = fadd2(sum0, sum1);
         l += f2_lo(sum) + f2_hi(sum);
       };
