@@ -72,7 +72,7 @@ template <int DP> struct Cfg {
   static constexpr int kStage = 32 * 128;  // bytes of a softmax warp's output staging: 32 rows x 64 bf16 elements
   static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
   static constexpr size_t kSmem =
-      1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 + kItems * sizeof(Item) + 4 * 32 * 8;
+      1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 + (kItems + 1) * sizeof(Item) + 4 * 32 * 8;
 };
 static_assert(Cfg<128>::kSmem <= kMaxSmem && Cfg<64>::kSmem <= kMaxSmem, "shared memory");
 
@@ -126,19 +126,18 @@ struct SharedArgs {
 
 // ------------------------------------------------------------------ chunks over the paged cache
 // How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head; the items lie in a
-// row (heads outside, tile slots inside), each as long as its cost: kOneTile or kTwoTiles a block of keys, and kItem for
-// Q, the first scores and the results. The row is cut into equally long runs, one a CTA, whatever items the
+// row (heads outside, tile slots inside), each as long as its cost: kBlock a block of keys, and kItem for Q, the first scores
+// and the results. The row is cut into equally long runs, one a CTA, whatever items the
 // cuts fall into: a decoding sequence of 100,000 keys beside a hundred short ones then takes as many CTAs as it needs.
 // A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
 // several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order. A
 // run has at most two such items, its first and its last, so that 2 pieces a CTA are enough however long the keys.
-constexpr int kOneTile = 4, kTwoTiles = 4, kItem = 16, kShortest = 16;
+constexpr int kBlock = 4, kItem = 16, kShortest = 16;
 
 struct ChunkItem {
   int seq, row0, nrows, q0, nq, nk, slot;
   int lim0, lim1, n_blocks;
-  int cost;  // of a block
-  __device__ __forceinline__ long long length() const { return nrows > 0 ? kItem + (long long)n_blocks * cost : 0; }
+  __device__ __forceinline__ long long length() const { return nrows > 0 ? kItem + (long long)n_blocks * kBlock : 0; }
 };
 // What fills tile slot s (nrows = 0: nothing).
 __device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const SharedArgs& sa, int s, int i) {
@@ -163,7 +162,6 @@ __device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const Shar
   it.lim0 = visible_keys((it.row0 + min(it.nrows, TM) - 1) / G, it.nq, it.nk, pa.causal);
   it.lim1 = it.nrows > TM ? visible_keys((it.row0 + it.nrows - 1) / G, it.nq, it.nk, pa.causal) : 0;
   it.n_blocks = (max(it.lim0, it.lim1) + BK - 1) / BK;
-  it.cost = it.nrows > TM ? kTwoTiles : kOneTile;
   return it;
 }
 // The runs: how many, their beginnings, and the run that place x lies in.
@@ -196,7 +194,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
   const uint32_t sOut = sKV + C::kStages * C::kTileBytes;  // [softmax warp][32 rows][64]
   Item* items = reinterpret_cast<Item*>(gbase + (2 + C::kStages) * C::kTileBytes + 8 * C::kStage);  // [kItems]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kItems);
+  Item* late_item = items + kItems;  // (of a chunk)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kItems + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -289,10 +288,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (at >= upto - sum && at < upto) {  // one thread
           long long x = upto - sum;
           int s = s0;
-          for (long long len = item(s).length(); x + len <= at; len = item(s).length()) {
-            x += len;
-            ++s;
-          }
+          if (s1 - s0 > 1)
+            for (long long len = item(s).length(); x + len <= at; len = item(s).length()) {
+              x += len;
+              ++s;
+            }
           plan[1] = s;
           plan[2] = begin - at + x;  // where item (head, slot s) begins
           plan[3] = begin / total;   // the head
@@ -548,92 +548,118 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       constexpr int kLanes = DP / 8, kRowsPer = 32 / kLanes;
       const int t = warp - kSoftWarps - 2;
       uint32_t loads = 0;
-      // PAGED: the first of these warps walks the CTA's run and publishes its items, one ahead of the Q tiles it loads
+      // PAGED: the first of these warps walks the CTA's run and publishes its items, one ahead of the Q tiles it loads. It
+      // looks at 32 tile slots at once, one a lane (the next of an item after the other cost 9 us an item).
       const bool finder = PAGED && t == 0;
       const Runs runs(finder ? plan[0] * Hkv : 0, gridDim.x);
-      long long x = finder ? plan[2] : 0, late_x = 0;
-      int at_slot = finder ? (int)plan[1] : 0, at_head = finder ? (int)plan[3] : 0, late_slot = -1, late_head = 0;
-      const bool idle = !finder || plan[0] == 0 || (int)blockIdx.x >= runs.n;
-      const long long run_begin = idle ? 0 : runs.begin(blockIdx.x), run_end = idle ? 0 : runs.begin(blockIdx.x + 1);
-      auto find = [&](Item& it) {
-        it = Item{};
-        it.last = 1;
-        while (!idle && (x < run_end || late_slot >= 0)) {
-          const bool late = x >= run_end;
-          const int s = late ? late_slot : at_slot, head = late ? late_head : at_head;
-          const ChunkItem ci = chunk_item(pa, sa, s, find_tile_seq_warp(pa.qo, pa.n, G, 2 * TM, s));
-          const long long begin = late ? late_x : x;
-          if (late) {
-            late_slot = -1;
-          } else {
-            x += ci.length();
-            if (++at_slot == n_items) {
-              at_slot = 0;
-              ++at_head;
-            }
-          }
-          if (ci.nrows == 0) continue;  // a slot that no tile fills
-          // The end of an item that began in another run comes last: the whole items of all runs then begin with their
-          // first keys at about the same time, and L2 serves those that share a head.
-          if (!late && begin < run_begin) {
-            late_slot = s;
-            late_head = head;
-            late_x = begin;
-            continue;
-          }
-          // the blocks whose beginnings lie in the run: block j at begin + j cost
-          const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
-          auto first_from = [&](long long p) {
-            return p <= begin ? 0 : (int)min((long long)all, (p - begin + ci.cost - 1) / ci.cost);
-          };
-          const int b0 = first_from(run_begin), b1 = first_from(run_end);
-          if (b0 >= b1) continue;
-          it.hk = head;
-          it.seq = ci.seq;
-          it.row0 = ci.row0;
-          it.nrows = ci.nrows;
-          it.q0 = ci.q0; it.nq = ci.nq; it.k0 = ci.slot; it.nk = ci.nk;
-          it.key0 = b0 * BK;
-          it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
-          it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
-          it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
-          it.dual = ci.nrows <= TM;
-          if (it.dual) it.lim1 = it.lim0;
-          it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
-          it.last = 0;
-          if (b0 == 0 && b1 < all && lane == 0) {
-            ChunkRun r;
-            r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
-            r.end = runs.of(begin + (long long)(all - 1) * ci.cost);
-            sa.runs[blockIdx.x] = r;
-          }
-          return;
+      const long long run_begin = finder && (int)blockIdx.x < runs.n ? runs.begin(blockIdx.x) : 0;
+      const long long run_end = finder && (int)blockIdx.x < runs.n ? runs.begin(blockIdx.x + 1) : 0;
+      ChunkItem ci{};
+      int base = finder ? (int)plan[1] & ~31 : 0, head = finder ? (int)plan[3] : 0, loaded = -1;
+      long long x = 0, before = 0, length = 0;  // the place of the 32 slots from `base` on in this head, of the lane's item among them, of all
+      int b0 = 0, b1 = 0;
+      uint32_t todo = 0;  // the lanes whose items have blocks in the run and are not published yet
+      bool late = false;
+      auto load_slots = [&]() {
+        const int s = base + lane;
+        ci = s < n_items ? chunk_item(pa, sa, s, find_tile_seq(pa.qo, pa.n, G, 2 * TM, s)) : ChunkItem{};
+        loaded = base;
+        const long long len = ci.length();
+        before = len;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, before, w);
+          if (lane >= w) before += y;
         }
+        length = __shfl_sync(0xffffffffu, before, 31);
+        before -= len;
       };
-      auto publish = [&](const Item& it) {
-        bool ok = true;
-        if (lane == 0) {
-          ok = wait_or_abort(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51);
-          if (ok) {
-            items[iq] = it;
-            mbar_arrive(bar(IFULL + iq));
-          }
+      auto my_item = [&]() {
+        const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
+        Item it{};
+        it.hk = head;
+        it.seq = ci.seq;
+        it.row0 = ci.row0;
+        it.nrows = ci.nrows;
+        it.q0 = ci.q0; it.nq = ci.nq; it.k0 = ci.slot; it.nk = ci.nk;
+        it.key0 = b0 * BK;
+        it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
+        it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
+        it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
+        it.dual = ci.nrows <= TM;
+        if (it.dual) it.lim1 = it.lim0;
+        it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
+        if (b0 == 0 && b1 < all) {
+          ChunkRun r;
+          r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
+          r.end = runs.of(x + before + (long long)(all - 1) * kBlock);
+          sa.runs[blockIdx.x] = r;
         }
-        if (++iq == kItems) { iq = 0; iphase ^= 1u; }
-        return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        return it;
       };
-      Item ahead;
-      if (finder) {
-        find(ahead);
-        publish(ahead);
+      // The blocks of the slots' items that lie in the run: block j begins at x + before + j kBlock.
+      auto look = [&]() {
+        if (loaded != base) load_slots();
+        const int all = max(1, ci.n_blocks);
+        auto first_from = [&](long long p) {
+          p -= x + before;
+          return p <= 0 ? 0 : (int)min((long long)all, (p + kBlock - 1) / kBlock);
+        };
+        b0 = first_from(run_begin);
+        b1 = first_from(run_end);
+        const bool in = ci.nrows > 0 && b0 < b1;
+        // The end of an item that began in another run comes last: the whole items of all runs then begin with their first
+        // keys at about the same time, and L2 serves those that share a head.
+        const bool is_late = in && x + before < run_begin;
+        if (is_late) *late_item = my_item();
+        __syncwarp();
+        late = late || __any_sync(0xffffffffu, is_late);
+        todo = __ballot_sync(0xffffffffu, in && !is_late);
+      };
+      bool ended = run_begin == run_end;
+      if (!ended) {
+        load_slots();
+        x = plan[2] - __shfl_sync(0xffffffffu, before, (int)plan[1] & 31);
+        look();
       }
+      // Publishes the run's next item, or its end.
+      auto advance = [&]() {
+        while (todo == 0 && !ended) {
+          x += length;
+          base += 32;
+          if (base >= n_items) {
+            base = 0;
+            ++head;
+          }
+          if (x >= run_end) ended = true;
+          else look();
+        }
+        if (!warp_wait(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51)) return false;
+        int from = 0;
+        if (todo != 0) {
+          from = __ffs(todo) - 1;
+          todo &= todo - 1;
+          if (lane == from) items[iq] = my_item();
+        } else if (late) {
+          late = false;
+          if (lane == 0) items[iq] = *late_item;
+        } else if (lane == 0) {
+          items[iq] = Item{};
+          items[iq].last = 1;
+        }
+        __syncwarp();
+        if (lane == from) mbar_arrive(bar(IFULL + iq));
+        if (++iq == kItems) { iq = 0; iphase ^= 1u; }
+        return true;
+      };
+      int mine = 0;  // the place of the finder's own next item
+      if (finder && !advance()) ended = true;
       while (true) {
         Item it;
         if (finder) {
-          it = ahead;
-          if (it.last) break;
-          find(ahead);
-          if (!publish(ahead)) break;
+          it = items[mine];
+          if (it.last || !advance()) break;
+          if (++mine == kItems) mine = 0;
         } else {
           const Item* ip = next_item();
           if (ip == nullptr) break;
