@@ -1124,15 +1124,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                              : "memory");
             }
             __syncwarp();
-            const int us = part ? 3 : 2;  // log2 of the 16-byte stores of a row
-            for (int i = 0; i < 1 << us; ++i) {
-              const int u = lane & ((1 << us) - 1), rr = (i << (5 - us)) + (lane >> us);
-              uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + (c << (4 + us)) + 16 * u;
-              uint4 x;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                           : "r"(stg + (rr << (4 + us)) + ((u ^ (part ? rr & 7 : rr >> 1 & 3)) * 16)) : "memory");
-              if (32 * q4 + rr < nrow_t && 32 * c + (32 >> us) * u < D) *reinterpret_cast<uint4*>(dst) = x;
-            }
+            // 2^us stores of 16 bytes a row
+            auto store = [&](auto shift) {
+              constexpr int us = decltype(shift)::value;
+#pragma unroll
+              for (int i = 0; i < 1 << us; ++i) {
+                const int u = lane & ((1 << us) - 1), rr = (i << (5 - us)) + (lane >> us);
+                uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + (c << (4 + us)) + 16 * u;
+                uint4 x;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                             : "r"(stg + (rr << (4 + us)) + ((u ^ (us == 3 ? rr & 7 : rr >> 1 & 3)) * 16)) : "memory");
+                if (32 * q4 + rr < nrow_t && 32 * c + (32 >> us) * u < D) *reinterpret_cast<uint4*>(dst) = x;
+              }
+            };
+            if (part) store(std::integral_constant<int, 3>{});
+            else store(std::integral_constant<int, 2>{});
             __syncwarp();
           }
           if (valid && part) sa.part_ml[(long long)it->split * sa.piece_rows + tile0 + r] = make_float2(m * c2, l);
