@@ -134,6 +134,8 @@ struct SharedArgs {
 // run has at most two such items, its first and its last, so that 2 pieces a CTA are enough however long the keys.
 constexpr int kBlock = 4, kItem = 16, kShortest = 16;
 
+// Length of an item of so many keys.
+__device__ __forceinline__ long long chunk_length(int keys) { return kItem + (long long)((keys + BK - 1) / BK) * kBlock; }
 struct ChunkItem {
   int seq, row0, nrows, q0, nq, nk, slot;
   int lim0, lim1, n_blocks;
@@ -264,9 +266,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   long long* plan = reinterpret_cast<long long*>(gbase + (2 + C::kStages) * C::kTileBytes);
   if (PAGED) {
     const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
-    auto item = [&](int s) { return chunk_item(pa, sa, s, find_tile_seq(pa.qo, pa.n, G, 2 * TM, s)); };
+    // f(slot, length) for the slots of [s0, s1) that a tile fills, as long as it returns true. The sequences lie in the slots'
+    // order, so what is read of them is read ahead, four at a time.
+    auto walk = [&](auto f) {
+      int s = s0, i = find_tile_seq(pa.qo, pa.n, G, 2 * TM, s0);
+      while (s < s1 && i < pa.n) {
+        int q[5], len[4];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) q[k] = pa.qo[min(i + k, pa.n)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) len[k] = slot_len(sa.d.c, sa.d.slots[min(i + k, pa.n - 1)]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i + k >= pa.n || q[k] < 0 || q[k + 1] < q[k] || q[k + 1] > pa.Tq) continue;
+          const long long first = (long long)q[k] * G / (2 * TM) + i + k, rows = (long long)(q[k + 1] - q[k]) * G;
+          const long long end = min((long long)s1, first + (rows + 2 * TM - 1) / (2 * TM));
+          for (s = max(s, (int)min(first, (long long)s1)); s < end; ++s) {
+            const int row0 = (int)(s - first) * 2 * TM, nrows = min(2 * TM, (int)rows - row0), nq = q[k + 1] - q[k];
+            const int lim0 = visible_keys((row0 + min(nrows, TM) - 1) / G, nq, len[k], pa.causal);
+            const int lim1 = nrows > TM ? visible_keys((row0 + nrows - 1) / G, nq, len[k], pa.causal) : 0;
+            if (!f(s, chunk_length(max(lim0, lim1)))) return;
+          }
+        }
+        i += 4;
+      }
+    };
     long long sum = 0;
-    for (int s = s0; s < s1; ++s) sum += item(s).length();
+    if (s0 < s1) walk([&](int, long long len) { sum += len; return true; });
     long long upto = sum;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -287,15 +313,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const long long begin = runs.begin(blockIdx.x), at = begin % total;
         if (at >= upto - sum && at < upto) {  // one thread
           long long x = upto - sum;
-          int s = s0;
-          if (s1 - s0 > 1)
-            for (long long len = item(s).length(); x + len <= at; len = item(s).length()) {
-              x += len;
-              ++s;
-            }
-          plan[1] = s;
-          plan[2] = begin - at + x;  // where item (head, slot s) begins
-          plan[3] = begin / total;   // the head
+          walk([&](int s, long long len) {
+            plan[1] = s;
+            plan[2] = begin - at + x;  // where item (head, slot s) begins
+            x += len;
+            return x <= at;
+          });
+          plan[3] = begin / total;  // the head
         }
       }
     }
@@ -1075,7 +1099,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const uint32_t stg = sOut + warp * C::kStage;
           const uint64_t f2 = f2_pack(f0, f0), g2 = f2_pack(f1, f1);
           uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
-#pragma unroll
+#pragma unroll 1  // (run once an item: what is not in the instruction cache costs more than the loop)
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
             if (n > 0) {
