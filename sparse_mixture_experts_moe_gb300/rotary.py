@@ -64,11 +64,11 @@ def _apart(a, b):
     fused tensor."""
     size = a.element_size()
     at, bt = a.data_ptr(), b.data_ptr()
-    end = [p + ((x.shape[0] - 1) * x.stride(0) + x.shape[1] * x.shape[2]) * size for p, x in ((at, a), (bt, b))]
+    end = [p + ((x.shape[0] - 1) * x.stride()[0] + x.shape[1] * x.shape[2]) * size for p, x in ((at, a), (bt, b))]
     if at >= end[1] or bt >= end[0]:
         return True
-    row = a.stride(0) * size
-    if a.stride(0) != b.stride(0) or a.shape[0] < 2 or b.shape[0] < 2:
+    row = a.stride()[0] * size
+    if a.stride()[0] != b.stride()[0] or a.shape[0] < 2 or b.shape[0] < 2:
         return False
     off = (bt - at) % row  # of b's heads behind a's in a token's row
     return off >= a.shape[1] * a.shape[2] * size and off + b.shape[1] * b.shape[2] * size <= row
@@ -83,7 +83,7 @@ def _check_overlap(outs, inputs):
             if x is None:
                 continue
             same = (name == theirs or name == "q_out" and theirs == "out") and o.data_ptr() == x.data_ptr() and (
-                o.stride(0) == x.stride(0) or o.shape[0] < 2)
+                o.stride()[0] == x.stride()[0] or o.shape[0] < 2)
             if not same and not _apart(o, x):
                 raise ValueError(f"moe: {name} overlaps an input without being that input")
         for other, p in outs[i + 1:]:
@@ -109,6 +109,7 @@ class Rotary:
             raise ValueError(f"Rotary: layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
         if scaling not in _SCALINGS:
             raise ValueError(f"Rotary: scaling must be None, 'linear', 'base', 'turns' or 'pairs', got {scaling!r}")
+        self._made = (head_dim, rotary_dim, base, layout, scaling, factor, original_len, low, high, magnitude, frequencies)
         self.head_dim = int(head_dim)
         self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
         self.layout, self.scaling = layout, scaling
@@ -120,7 +121,8 @@ class Rotary:
         if frequencies is not None:
             if scaling is not None:
                 raise ValueError("Rotary: frequencies are taken as they are: scaling must be None")
-            f = [float(x) for x in frequencies]
+            f = frequencies = [float(x) for x in frequencies]
+            self._made = self._made[:-1] + (f,)
             if len(f) != self.rotary_dim // 2:
                 raise ValueError(f"Rotary: expected {self.rotary_dim // 2} frequencies, got {len(f)}")
             f = (ctypes.c_double * max(1, len(f)))(*f)
@@ -144,6 +146,9 @@ class Rotary:
         self._last = (None, None)
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._current_device, self._many = torch._C._cuda_getDevice, torch.cuda.device_count() > 1
+
+    def __reduce__(self):  # copies and pickles are made anew: they have a table of their own
+        return Rotary, self._made
 
     @property
     def magnitude(self):
