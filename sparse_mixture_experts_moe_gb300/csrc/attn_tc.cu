@@ -940,7 +940,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       };
       place();
       const int n = blocks(t ? it->lim1 : it->lim0);
-      int lim = 0;
+      // (What a row past the tile's end makes of whatever lies there is dropped, so a chunk's are not masked: a tile of a single
+      // token's heads would go through the masking below in every block.)
+      int lim = PAGED && !valid ? 0x7fffffff : 0;
       if (valid && SHARED) {  // a slot shorter than the shared keys sees its own length of them
         lim = max(0, min(it->n_keys, slot_len(sa.d.c, sa.d.slots[tok]) - it->key0));
       } else if (valid) {
