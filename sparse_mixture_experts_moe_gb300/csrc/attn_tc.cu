@@ -1101,71 +1101,77 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const uint32_t stg = sOut + warp * C::kStage;
           const uint64_t f2 = f2_pack(f0, f0), g2 = f2_pack(f1, f1);
           uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
-#pragma unroll 1  // (run once an item: what is not in the instruction cache costs more than the loop)
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t o[32];
-            if (n > 0) {
-              tmem_ld_32x32b_x32(tO + 32 * c, o);
-              tmem_ld_wait();
-            }
-            if (dual && c > 0) ok = ok && warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+          // A row's 128 bytes (32 sums or 64 results) from shared memory to `to`, of which the first `elems` exist
+          auto store = [&](uint32_t to, int elems, int per) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              uint64_t v0 = ffma2(((uint64_t)o[4 * i + 1] << 32) | o[4 * i], f2, 0ull);
-              uint64_t v1 = ffma2(((uint64_t)o[4 * i + 3] << 32) | o[4 * i + 2], f2, 0ull);
+              const int u = lane & 7, rr = 4 * i + (lane >> 3);
+              uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + to + 16 * u;
+              uint4 x;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(stg + rr * 128 + ((u ^ (rr & 7)) * 16)) : "memory");
+              if (32 * q4 + rr < nrow_t && per * u < elems) *reinterpret_cast<uint4*>(dst) = x;
+            }
+          };
+#pragma unroll 1  // (run once an item: what is not in the instruction cache costs more than the loop)
+          for (int c = 0; c < DP / 64; ++c) {
+            uint32_t o2[2][32];
+            tmem_ld_32x32b_x32(tO + 64 * c, o2[0]);  // (not this item's where there was no block: lim is 0 then)
+            tmem_ld_32x32b_x32(tO + 64 * c + 32, o2[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint32_t(&o)[32] = o2[b];
+              if (dual && c + b > 0) ok = ok && warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint64_t v0 = ffma2(((uint64_t)o[4 * i + 1] << 32) | o[4 * i], f2, 0ull);
+                uint64_t v1 = ffma2(((uint64_t)o[4 * i + 3] << 32) | o[4 * i + 2], f2, 0ull);
+                if (dual) {
+                  uint64_t x0, x1;
+                  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x0), "=l"(x1)
+                               : "r"(stg + 4 * C::kStage + lane * 128 + ((i ^ (lane & 7)) * 16)) : "memory");
+                  v0 = ffma2(x0, g2, v0);
+                  v1 = ffma2(x1, g2, v1);
+                }
+                if (lim == 0) v0 = v1 = 0ull;
+                odd = ffma2(v0, 0ull, odd);
+                odd = ffma2(v1, 0ull, odd);
+                o[4 * i] = (uint32_t)v0;
+                o[4 * i + 1] = (uint32_t)(v0 >> 32);
+                o[4 * i + 2] = (uint32_t)v1;
+                o[4 * i + 3] = (uint32_t)(v1 >> 32);
+              }
               if (dual) {
-                uint64_t x0, x1;
-                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x0), "=l"(x1)
-                             : "r"(stg + 4 * C::kStage + lane * 128 + ((i ^ (lane & 7)) * 16)) : "memory");
-                v0 = ffma2(x0, g2, v0);
-                v1 = ffma2(x1, g2, v1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(TAKEN + q4));
+                ++given;
               }
-              if (lim == 0) v0 = v1 = 0ull;
-              odd = ffma2(v0, 0ull, odd);
-              odd = ffma2(v1, 0ull, odd);
-              o[4 * i] = (uint32_t)v0;
-              o[4 * i + 1] = (uint32_t)(v0 >> 32);
-              o[4 * i + 2] = (uint32_t)v1;
-              o[4 * i + 3] = (uint32_t)(v1 >> 32);
+              if (part) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)),
+                               "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                               : "memory");
+                __syncwarp();
+                store((2 * c + b) * 128, D - 64 * c - 32 * b, 4);
+                __syncwarp();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + (((4 * b + i) ^ (lane & 7)) * 16)),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]))),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]))),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]))),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])))
+                               : "memory");
+              }
             }
-            if (dual) {
+            if (!part) {
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(TAKEN + q4));
-              ++given;
+              store(c * 128, D - 64 * c, 8);
+              __syncwarp();
             }
-            if (part) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)),
-                             "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
-                             : "memory");
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 64 + ((i ^ (lane >> 1 & 3)) * 16)),
-                             "r"(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]))),
-                             "r"(pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]))),
-                             "r"(pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]))),
-                             "r"(pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])))
-                             : "memory");
-            }
-            __syncwarp();
-            // 2^us stores of 16 bytes a row
-            auto store = [&](auto shift) {
-              constexpr int us = decltype(shift)::value;
-#pragma unroll
-              for (int i = 0; i < 1 << us; ++i) {
-                const int u = lane & ((1 << us) - 1), rr = (i << (5 - us)) + (lane >> us);
-                uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + (c << (4 + us)) + 16 * u;
-                uint4 x;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                             : "r"(stg + (rr << (4 + us)) + ((u ^ (us == 3 ? rr & 7 : rr >> 1 & 3)) * 16)) : "memory");
-                if (32 * q4 + rr < nrow_t && 32 * c + (32 >> us) * u < D) *reinterpret_cast<uint4*>(dst) = x;
-              }
-            };
-            if (part) store(std::integral_constant<int, 3>{});
-            else store(std::integral_constant<int, 2>{});
-            __syncwarp();
           }
           if (valid && part) sa.part_ml[(long long)it->split * sa.piece_rows + tile0 + r] = make_float2(m * c2, l);
           if (valid && !part && pa.lse != nullptr)
