@@ -1585,7 +1585,10 @@ cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const
   const int G = a.H / a.Hkv;
   int q_tma = 0;
   if (enc == nullptr || !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma)) return cudaErrorInvalidValue;
-  const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM), ctas = device_sm_count();
+  const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM);
+  // one CTA an SM, as far as the longest sequences that the cache may hold make as many runs
+  const long long runs_most = a.Hkv * (long long)slots * (kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kBlock) / kShortest;
+  const int ctas = (int)(runs_most < 1 ? 1 : (runs_most < device_sm_count() ? runs_most : device_sm_count()));
   SharedArgs sa{};
   sa.d = d;
   sa.runs = runs;
