@@ -1,14 +1,15 @@
 """A decoder of attention and MoE blocks: several samples continue one prompt.
 
-    python examples/decoder_block.py [--layers 2] [--prompt 1024] [--samples 8] [--steps 32] [--dtype bf16]
+    python examples/decoder_block.py [--layers 2] [--prompt 1024] [--piece 400] [--samples 8] [--steps 32] [--dtype bf16]
 
-The prompt's keys and values go into a paged cache once (Attention.prompt, KVCache.resize and .write). Each
-sample is a fork of the prompt's slot: it shares the prompt's full pages and has its own last page. A step appends one
-token of every sample (resize, write) and attends the cache (Attention.decode), which reads the shared pages
-once for all samples; MoELayer is the feed-forward part. At the end half of the samples are dropped and the pool is
-compacted. The prompt path over the whole sequences gives the same numbers, which main() checks.
+The prompt is admitted in pieces of --piece tokens: the piece's keys are normed and turned by their positions on the way
+into a paged cache, its queries in the same pass (KVCache.resize and .append, Rotary), and it attends everything admitted so
+far (Attention.chunk). Each sample is a fork of the prompt's slot: it shares the prompt's full pages and has its own last
+page. A step appends one token of every sample and attends the cache (Attention.decode), which reads the shared pages once
+for all samples; MoELayer is the feed-forward part. At the end half of the samples are dropped and the pool is compacted. The
+whole sequences without a cache (Rotary.apply, Attention.prompt) give the same numbers, which main() checks.
 
-Weights and inputs are random; the dense projections and norms are plain torch.
+Weights and inputs are random; the dense projections and the blocks' norms are plain torch.
 """
 from __future__ import annotations
 
@@ -34,14 +35,16 @@ def rms_norm(x):
 class Block:
     """x + attention, then + MoE. d = heads * head_dim."""
 
-    def __init__(self, layer, d, heads, kv_heads, experts, d_ff, dtype, device, gen):
-        self.layer, self.heads, self.kv_heads, self.head_dim = layer, heads, kv_heads, d // heads
+    def __init__(self, layer, d, heads, kv_heads, experts, d_ff, rope, dtype, device, gen):
+        self.layer, self.heads, self.kv_heads, self.head_dim, self.rope = layer, heads, kv_heads, d // heads, rope
 
         def weight(*shape):
             return (torch.randn(shape, generator=gen, device=device) * shape[-2] ** -0.5).to(dtype)
 
         self.w_qkv = weight(d, (heads + 2 * kv_heads) * self.head_dim)
         self.w_o = weight(d, d)
+        self.norms = {name: (1 + 0.1 * torch.randn(self.head_dim, generator=gen, device=device)).to(dtype)
+                      for name in ("q_weight", "k_weight")}  # of each head's queries and keys
         self.attn = moe.Attention(heads, kv_heads, self.head_dim, dtype)
         self.ffn = moe.MoELayer(weight(d, experts), weight(experts, d, d_ff), weight(experts, d_ff, d), k=2)
 
@@ -54,17 +57,24 @@ class Block:
         x = x + a.reshape(x.shape) @ self.w_o
         return x + self.ffn(rms_norm(x))
 
-    def prompt(self, x, offsets, cache=None, slots=None, pos=None):
-        """Whole packed prompts; their keys and values go into the cache, if one is given."""
+    def prompt(self, x, offsets, positions):
+        """Whole packed prompts, without a cache."""
         q, k, v = self._qkv(x)
-        if cache is not None:
-            cache.write(k, v, slots, offsets, pos, layer=self.layer)
+        q, k = self.rope.apply(q, positions, k, **self.norms)
         return self._rest(x, self.attn.prompt(q, k, v, offsets))
+
+    def _append(self, x, offsets, cache, slots, pos):
+        q, k, v = self._qkv(x)
+        return cache.append(k, v, slots, offsets, pos, self.rope, layer=self.layer, q=q, **self.norms)
+
+    def piece(self, x, offsets, cache, slots, pos):
+        """The next tokens of each slot, however many."""
+        q = self._append(x, offsets, cache, slots, pos)
+        return self._rest(x, self.attn.chunk(q, cache, slots, offsets, layer=self.layer))
 
     def step(self, x, offsets, cache, slots, pos, shared_len):
         """One more token of each slot."""
-        q, k, v = self._qkv(x)
-        cache.write(k, v, slots, offsets, pos, layer=self.layer)
+        q = self._append(x, offsets, cache, slots, pos)
         return self._rest(x, self.attn.decode(q, cache, slots, layer=self.layer, shared_len=shared_len))
 
 
@@ -73,7 +83,8 @@ class Decoder:
                  seed=0):
         gen = torch.Generator(device=device).manual_seed(seed)
         self.d, self.dtype, self.device, self.kv_heads, self.head_dim = d, dtype, device, kv_heads, d // heads
-        self.blocks = [Block(i, d, heads, kv_heads, experts, d_ff, dtype, device, gen) for i in range(layers)]
+        rope = moe.Rotary(self.head_dim)
+        self.blocks = [Block(i, d, heads, kv_heads, experts, d_ff, rope, dtype, device, gen) for i in range(layers)]
 
     def cache(self, n_pages, page_size, n_slots, max_len):
         return moe.KVCache.create(len(self.blocks), n_pages, page_size, n_slots, max_len, self.kv_heads, self.head_dim,
@@ -82,14 +93,20 @@ class Decoder:
     def ints(self, values):
         return torch.tensor(values, dtype=torch.int32, device=self.device)
 
-    def prompt(self, x, lengths, cache=None, slots=None):
+    def prompt(self, x, lengths):
         offsets = self.ints([sum(lengths[:i]) for i in range(len(lengths) + 1)])
-        pos = None
-        if cache is not None:
-            cache.resize(slots, self.ints(lengths))
-            pos = torch.zeros_like(slots)
+        positions = torch.cat([torch.arange(n, dtype=torch.int32, device=self.device) for n in lengths])
         for b in self.blocks:
-            x = b.prompt(x, offsets, cache, slots, pos)
+            x = b.prompt(x, offsets, positions)
+        return x
+
+    def piece(self, x, lengths, cache, slots):
+        """The next lengths[i] tokens of each slot."""
+        offsets = self.ints([sum(lengths[:i]) for i in range(len(lengths) + 1)])
+        pos = cache.lens[slots]
+        cache.resize(slots, pos + self.ints(lengths))
+        for b in self.blocks:
+            x = b.piece(x, offsets, cache, slots, pos)
         return x
 
     def step(self, x, cache, slots, shared_len=0):
@@ -109,16 +126,17 @@ class Decoder:
                 raise moe.MoeError(status, f"device status ({detail})")
 
 
-def generate(dec, prompt, tokens, page_size=64):
-    """prompt [P, d]; tokens [steps, samples, d], the embeddings that each sample goes on with. Returns the outputs
-    [steps, samples, d] and the cache."""
+def generate(dec, prompt, tokens, piece=400, page_size=64):
+    """prompt [P, d], admitted `piece` tokens at a time; tokens [steps, samples, d], the embeddings that each sample goes
+    on with. Returns the outputs [steps, samples, d] and the cache."""
     steps, n, _ = tokens.shape
     length = len(prompt) + steps
     full = len(prompt) // page_size            # pages that every sample shares
     own = -(-length // page_size) - full
     cache = dec.cache(full + 1 + n * own, page_size, n + 1, length)
     first, samples = dec.ints([n]), dec.ints(list(range(n)))
-    dec.prompt(prompt, [len(prompt)], cache, first)
+    for x in prompt.split(piece):
+        dec.piece(x, [len(x)], cache, first)
     cache.fork(first.expand(n).contiguous(), samples)
     cache.resize(first, torch.zeros_like(first))  # the samples hold its pages now
     out = torch.stack([dec.step(tokens[t], cache, samples, shared_len=full * page_size) for t in range(steps)])
@@ -129,6 +147,7 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--prompt", type=int, default=1024)
+    ap.add_argument("--piece", type=int, default=400, help="tokens of the prompt admitted at a time")
     ap.add_argument("--samples", type=int, default=8)
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--dtype", choices=["bf16", "f32"], default="bf16")
@@ -140,10 +159,10 @@ def main():
     prompt = torch.randn(args.prompt, dec.d, generator=gen, device="cuda").to(dtype)
     tokens = torch.randn(args.steps, args.samples, dec.d, generator=gen, device="cuda").to(dtype)
 
-    generate(dec, prompt, tokens)  # warm-up: workspaces
+    generate(dec, prompt, tokens, args.piece)  # warm-up: workspaces
     torch.cuda.synchronize()
     t0 = time.perf_counter()
-    out, cache = generate(dec, prompt, tokens)
+    out, cache = generate(dec, prompt, tokens, args.piece)
     torch.cuda.synchronize()
     ms = 1e3 * (time.perf_counter() - t0)
     dec.check(cache)
