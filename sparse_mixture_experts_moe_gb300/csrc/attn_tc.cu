@@ -86,6 +86,21 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
       ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// A TMA copy with an L2 eviction priority (a policy from createpolicy).
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy(bool first) {
+  uint64_t a, b;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(a));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(b));
+  return first ? a : b;
+}
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -373,6 +388,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const int slot = ip->k0, hk = ip->hk, n = blocks(ip->n_keys);
         int j0 = ip->key0, rest = ip->nk - j0;  // the block's first position, and what the sequence holds from there on
         const int seq = ip->seq;
+        // Keys that one item alone reads leave L2 first: they would push out those that the tile pairs of a longer chunk share.
+        const uint64_t policy = l2_policy((long long)ip->nq * G <= 2 * TM);
         item_done();
         const int32_t* row = cv.table + (long long)slot * cv.width;
         // The whole warp walks the copies and one elected thread issues them: what they are given stays in uniform registers.
@@ -408,7 +425,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
               if (leader) {
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c) tma_load_3d(dst + c * (BK * 128), v ? &tmV : &tmK, 64 * c, g, sa.d.layer, b);
+                for (int c = 0; c < C::kChunks; ++c) tma_load_3d_hint(dst + c * (BK * 128), v ? &tmV : &tmK, 64 * c, g, sa.d.layer, b, policy);
               }
             }
             if (cut) {
