@@ -82,10 +82,10 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   // where position j of the keys lies
   auto paged = [&](int j) {
     int page = pages[j >> da.c.page_shift];
-    if (page < 0 || page >= da.c.n_pages) {
-      if (PAGED) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
-      page = 0;
+    if constexpr (PAGED) {
+      if (page < 0 || page >= da.c.n_pages) record_error(a.status, MOE_ERR_DEVICE_CHECK, seq);
     }
+    page = page < 0 || page >= da.c.n_pages ? 0 : page;
     return (((long long)page * Hkv + hk) * da.c.page_size + (j & (da.c.page_size - 1))) * D;
   };
 
@@ -220,15 +220,22 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   auto replace = [&](int R, float mr, float lr) {  // in row R of the tile, by a warp
     const int P = row0 + R, tok = P / G, h = hk * G + P % G;
     float x[8];
-    const long long k0 = PAGED ? 0 : (long long)sq.k0 * a.ks + (long long)hk * D;
-    const long long v0 = PAGED ? 0 : (long long)sq.k0 * a.vs + (long long)hk * D;
-    const uint32_t cols = replace_row(
-        unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + k0, vb + v0,
-        [&](int j, long long& ko, long long& vo) {
-          ko = PAGED ? paged(j) : j * a.ks;
-          vo = PAGED ? ko : j * a.vs;
-        },
-        D, visible_keys(tok, sq.nq, sq.nk, a.causal), c2, mr == -INFINITY ? 0.f : mr * c2, x);
+    uint32_t cols;
+    if constexpr (PAGED) {
+      cols = replace_row(
+          unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb, vb,
+          [&](int j, long long& ko, long long& vo) { ko = vo = paged(j); }, D, visible_keys(tok, sq.nq, sq.nk, a.causal), c2,
+          mr == -INFINITY ? 0.f : mr * c2, x);
+    } else {
+      cols = replace_row(
+          unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb + (long long)sq.k0 * a.ks + (long long)hk * D,
+          vb + (long long)sq.k0 * a.vs + (long long)hk * D,
+          [&](int j, long long& ko, long long& vo) {
+            ko = j * a.ks;
+            vo = j * a.vs;
+          },
+          D, visible_keys(tok, sq.nq, sq.nk, a.causal), c2, mr == -INFINITY ? 0.f : mr * c2, x);
+    }
     const float inv = lr == 0.f ? 0.f : 1.0f / lr;
     __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (long long)(sq.q0 + tok) * a.os + (long long)h * D + lane * 8;
 #pragma unroll
@@ -245,7 +252,9 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
   }
   if (SHARED || (PAGED && gridDim.z > 1)) {
     // the row's piece
-    auto part = [&](int P) { return da.part + (((long long)(sq.q0 + P / G) * H + hk * G + P % G) * sp.pieces + blockIdx.z) * (D + 2); };
+    auto part = [&](int P) {
+      return da.part + (((long long)((PAGED ? sq.q0 : 0) + P / G) * H + hk * G + P % G) * sp.pieces + blockIdx.z) * (D + 2);
+    };
     uint32_t again[2];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -271,7 +280,7 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
       const float mr = row_m(r);
       const int j0 = j_begin;  // (the keys counted from the piece's first)
       const uint32_t cols = replace_row(
-          pieces_unseen, qb + (long long)(sq.q0 + tok) * qs + (long long)h * D, kb, vb,
+          pieces_unseen, qb + (long long)((PAGED ? sq.q0 : 0) + tok) * qs + (long long)h * D, kb, vb,
           [&](int j, long long& ko, long long& vo) { ko = vo = paged(j0 + j); }, D,
           max(0, min(j_end, PAGED ? visible_keys(tok, sq.nq, sq.nk, a.causal) : slot_len(da.c, da.slots[tok])) - j0), c2,
           mr == -INFINITY ? 0.f : mr * c2, x);
