@@ -102,14 +102,14 @@ struct SharedPart {
   int pieces;       // of a row altogether
 };
 
-// A chunk call's run of items (attn_tc.cu): the one that begins in it and goes on in others, up to run `end`. nrows =
+// A chunk call's run of items (attn_chunk.cu): the one that begins in it and goes on in others, up to run `end`. nrows =
 // 0: none.
 struct ChunkRun {
   int hk, q0, row0, nrows, end;
 };
 
-// What the other warps' waits allow a softmax warp of attn_tc.cu that replaces columns of its 32 rows (replace_unseen):
-// 0.4 us a key and row, where 0.1 was measured, and 20 s at most.
+// What the other warps' waits allow a softmax warp of attn_tc.cu or attn_chunk.cu that replaces columns of its 32 rows
+// (replace_unseen): 0.4 us a key and row, where 0.1 was measured, and 20 s at most.
 constexpr uint64_t replace_time(long long keys) { return keys < 1562500 ? (uint64_t)keys * 32 * 400 : 20000000000ull; }
 
 // Workspace of one decode call. A piece is the attention of one row over a part of its keys: the sum of

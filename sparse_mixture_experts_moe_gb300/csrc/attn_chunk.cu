@@ -1,0 +1,1149 @@
+// Chunks: the new tokens of each sequence against everything that its slot of the paged cache holds, theirs included
+// (bf16, heads of up to 128 elements, on the 5th-generation tensor cores). A prompt's piece, a draft of a few tokens and
+// single tokens lie in one call.
+//   S = Q K^T (scores), P = 2^(c S - c m) (weights, c = scale log2 e), O += P V, out = O / l
+// in one pass over the keys, as for packed prompts (attn_tc.cu), whose item, MMA order and rescaling these are: 256
+// packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 2^8, weights rounded
+// to bf16 for the MMA and their sum not. What is different here:
+// - Work is shared out by keys, not by items (below): one sequence of 100,000 keys beside a hundred short ones still takes
+//   every SM.
+// - Keys and values come from pages, by one TMA box a page and 64 elements (pages of 128 positions and up: a block of 128),
+//   and no byte past a sequence's last page is read. Values past its end become zeros in shared memory.
+// - An item of one tile (a decoding sequence's heads, a short draft) would leave one softmax group and half of the MMA's
+//   rhythm idle: both groups take the same rows then, each half of every block's keys, with scores two blocks ahead, and add
+//   up at the end. Single tokens of 64 sequences behind 8192 positions: 196 us, 5.8 TB/s.
+// Warps of a CTA (one an SM):
+//   0..3, 4..7  softmax of tile 0 / 1 (or of the halves of the keys); thread = row = TMEM lane
+//   8           allocates TMEM; one elected thread issues every MMA
+//   9           pages, K and V by TMA into a ring (K0 V0 K1 V1 ..)
+//   10          finds the run's items, one ahead, and loads tile 0's Q
+//   11          loads tile 1's Q
+// All waits are bounded; a wait that runs out records an error, and the CTA ends after its copies and MMAs have.
+// A CTA per item, as many as there are, would need a second kernel or a counter for the parts of long items; with the
+// runs, a launch of one CTA an SM ends within a block or two of the others wherever the lengths lie.
+// Measured (32 heads of 128 on 8): 4096 tokens behind 12288: 1.20 ms in a run of ten (1.60 PFLOP/s of 1.92 measured
+// for a dense product in a burst); 8 sequences' chunks of 500 tokens and 56 single tokens behind up to 32768: 0.80 ms, where
+// reading the keys and values once takes 0.39: the chunks' tile pairs (0.4 ms of MMAs) and the single tokens' reads lie in
+// different runs, of which each takes its time; 64 drafts of 4 tokens behind up to 16384: 358 us, 6.4 TB/s; 16 sequences
+// of 4 tokens behind 300: 15.7 us, four waits on memory one behind the other (lengths, pages, keys, pieces).
+#include "attn_tc.cuh"
+
+namespace moe {
+namespace {
+
+struct __align__(16) Item {
+  int hk, row0, nrows;      // key/value head; packed rows row0 .. of the sequence
+  int q0, nq, k0, nk;       // the sequence: first token and tokens, slot and positions held
+  int key0, n_keys;         // keys of the item
+  int lim0, lim1;           // keys that each tile's last row sees (relative to key0)
+  int last;                 // no item: the end
+  int seq;                  // (for errors)
+  int dual;                 // one tile of rows: both softmax groups take it, with half of each block's keys
+  int split;                // the piece that takes the results (-1: the output)
+};
+constexpr int kItems = 3;   // items published: one worked on, one ahead, one being given back
+constexpr int kItemReaders = 1 + 8 + 2;
+
+template <int DP> struct Cfg {
+  static constexpr int kChunks = DP / 64;          // 64-element (128-byte) swizzle columns of a row
+  static constexpr int kTileBytes = TM * DP * 2;   // a Q tile, and a K or V block
+  static constexpr int kStages = DP == 128 ? 4 : 8;
+  static constexpr int kStage = 32 * 128;  // bytes of a softmax warp's output staging: 32 rows x 64 bf16 elements
+  static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 +
+                                  (kItems + 1) * sizeof(Item) + 4 * 32 * 8;
+};
+static_assert(Cfg<128>::kSmem <= kMaxSmem && Cfg<64>::kSmem <= kMaxSmem, "shared memory");
+
+// A TMA copy with an L2 eviction priority (a policy from createpolicy).
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy(bool first) {
+  uint64_t a, b;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(a));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(b));
+  return first ? a : b;
+}
+
+struct ChunkArgs {
+  DecodeArgs d;
+  ChunkRun* runs;  // [CTA] the item that begins in each run and goes on in the next ones
+  int piece_rows;  // rows of a piece
+  float* part_o;   // [piece][piece_rows][D]
+  float2* part_ml;
+};
+
+// How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head; the items lie in a
+// row (heads outside, tile slots inside), each as long as its cost: kBlock a block of keys, and kItem for Q, the first
+// scores and the results (an item's fixed part took as long as four blocks). The row is cut into equally long runs, one
+// a CTA, whatever items the cuts fall into; runs are not shorter than kShortest.
+// A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
+// several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order, so
+// that results do not depend on which CTA is done first. A run has at most two such items, its first and its last: 2
+// pieces a CTA are enough however long the keys.
+constexpr int kBlock = 4, kItem = 16, kShortest = 16;
+
+// Length of an item of so many keys.
+__device__ __forceinline__ long long chunk_length(int keys) {
+  return kItem + (long long)((keys + BK - 1) / BK) * kBlock;
+}
+
+struct ChunkItem {
+  int seq, row0, nrows, q0, nq, nk, slot;
+  int lim0, lim1, n_blocks;
+  __device__ __forceinline__ long long length() const { return nrows > 0 ? kItem + (long long)n_blocks * kBlock : 0; }
+};
+// What fills tile slot s (nrows = 0: nothing).
+__device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const ChunkArgs& ca, int s, int i) {
+  const int G = pa.H / pa.Hkv;
+  ChunkItem it{};
+  it.seq = i;
+  const int q0 = pa.qo[i], q1 = pa.qo[i + 1];
+  it.slot = ca.d.slots[i];
+  if (q0 < 0 || q1 < q0 || q1 > pa.Tq) {
+    record_error(pa.status, MOE_ERR_DEVICE_CHECK, i);
+    return it;
+  }
+  it.q0 = q0;
+  it.nq = q1 - q0;
+  const long long r0 = ((long long)s - ((long long)q0 * G / (2 * TM) + i)) * (2 * TM);
+  if (r0 < 0 || r0 >= (long long)it.nq * G) return it;
+  it.nk = slot_len(ca.d.c, it.slot);
+  if (it.nk == 0 && (it.slot < 0 || it.slot >= ca.d.c.n_slots || ca.d.c.lens[it.slot] != 0))
+    record_error(pa.status, MOE_ERR_DEVICE_CHECK, i);
+  it.row0 = (int)r0;
+  it.nrows = min(2 * TM, it.nq * G - it.row0);
+  it.lim0 = visible_keys((it.row0 + min(it.nrows, TM) - 1) / G, it.nq, it.nk, pa.causal);
+  it.lim1 = it.nrows > TM ? visible_keys((it.row0 + it.nrows - 1) / G, it.nq, it.nk, pa.causal) : 0;
+  it.n_blocks = (max(it.lim0, it.lim1) + BK - 1) / BK;
+  return it;
+}
+// The runs: how many, their beginnings, and the run that place x lies in.
+struct Runs {
+  long long all;
+  int n;
+  __device__ __forceinline__ Runs(long long total, int ctas) : all(total) {
+    const long long most = total / kShortest;
+    n = (int)(most < 1 ? 1 : (most < ctas ? most : ctas));
+  }
+  __device__ __forceinline__ long long begin(int c) const { return all * c / n; }
+  __device__ __forceinline__ int of(long long x) const { return (int)(((x + 1) * n - 1) / all); }
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs pa,
+               const __grid_constant__ ChunkArgs ca, int n_items, int q_tma) {
+  using C = Cfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
+  const uint32_t sOut = sKV + C::kStages * C::kTileBytes;  // [softmax warp][32 rows][64]
+  Item* items = reinterpret_cast<Item*>(gbase + (2 + C::kStages) * C::kTileBytes + 8 * C::kStage);  // [kItems]
+  Item* late_item = items + kItems;  // (of a chunk)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kItems + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 4,
+                ODONE = PFULL + 4, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
+                TAIL = IEMPTY + kItems, GIVEN = TAIL + 1, TAKEN = GIVEN + 4;
+  float2* given_ml = reinterpret_cast<float2*>(gbase + C::kSmem - 1024 - 4 * 32 * 8);  // [warp of tile 1][row]
+
+  // (the shuffle tells the compiler that the warp number is the same in all lanes)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(bar(FULL + s), 1); mbar_init(bar(EMPTY + s), 1); }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(QFULL + t), 1);
+      for (int b = 0; b < 4; b += 2) {  // (the second of each is for halves of blocks)
+        mbar_init(bar(SFULL + b + t), 1);
+        mbar_init(bar(PFULL + b + t), 4);
+      }
+      mbar_init(bar(ODONE + t), 1);
+      mbar_init(bar(QEMPTY + t), 1);
+    }
+    for (int i = 0; i < kItems; ++i) { mbar_init(bar(IFULL + i), 1); mbar_init(bar(IEMPTY + i), kItemReaders); }
+    mbar_init(bar(DONE), 1);
+    mbar_init(bar(TAIL), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(GIVEN + i), 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+    if (q_tma) tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == kSoftWarps) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  // Only after TMEM is allocated: a dependent kernel that starts on this SM may allocate some before it waits for
+  // this grid. And only after the wait: the decode's own-key kernel relies on everything before this grid being done.
+  griddep_launch_dependents();
+
+  const int H = pa.H, Hkv = pa.Hkv, D = pa.D, G = H / Hkv;
+  int* status = pa.status;
+  const uint64_t timeout_ns = pa.timeout_ns;
+  // The items, for every warp but the one that finds them: the next one (nullptr after the last), and giving it
+  // back. The fields are read where they are needed, as the softmax warps have no registers to keep them in.
+  int iq = 0;
+  uint32_t iphase = 0;
+  auto next_item = [&]() -> const Item* {
+    if (!warp_wait(bar(IFULL + iq), iphase, timeout_ns, abort_flag, status, 54)) return nullptr;
+    return items[iq].last ? nullptr : items + iq;
+  };
+  auto item_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(IEMPTY + iq));
+    if (++iq == kItems) { iq = 0; iphase ^= 1u; }
+  };
+  auto blocks = [](int keys) { return (keys + BK - 1) / BK; };
+
+  // This CTA's run: a scan over the lengths of all tile slots, each thread with some of them in a row. The results stay
+  // in the output staging until the first item is published.
+  long long* plan = reinterpret_cast<long long*>(gbase + (2 + C::kStages) * C::kTileBytes);
+  const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
+  // f(slot, length) for the slots of [s0, s1) that a tile fills, as long as it returns true. The sequences lie in the
+  // slots' order, so what is read of them is read ahead, four at a time.
+  auto walk = [&](auto f) {
+    int s = s0, i = find_tile_seq(pa.qo, pa.n, G, 2 * TM, s0);
+    while (s < s1 && i < pa.n) {
+      int q[5], len[4];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) q[k] = pa.qo[min(i + k, pa.n)];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) len[k] = slot_len(ca.d.c, ca.d.slots[min(i + k, pa.n - 1)]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i + k >= pa.n || q[k] < 0 || q[k + 1] < q[k] || q[k + 1] > pa.Tq) continue;
+        const long long first = (long long)q[k] * G / (2 * TM) + i + k, rows = (long long)(q[k + 1] - q[k]) * G;
+        const long long end = min((long long)s1, first + (rows + 2 * TM - 1) / (2 * TM));
+        for (s = max(s, (int)min(first, (long long)s1)); s < end; ++s) {
+          const int row0 = (int)(s - first) * 2 * TM, nrows = min(2 * TM, (int)rows - row0), nq = q[k + 1] - q[k];
+          const int lim0 = visible_keys((row0 + min(nrows, TM) - 1) / G, nq, len[k], pa.causal);
+          const int lim1 = nrows > TM ? visible_keys((row0 + nrows - 1) / G, nq, len[k], pa.causal) : 0;
+          if (!f(s, chunk_length(max(lim0, lim1)))) return;
+        }
+      }
+      i += 4;
+    }
+  };
+  long long sum = 0;
+  if (s0 < s1) walk([&](int, long long len) { sum += len; return true; });
+  long long upto = sum;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, w);
+    if (lane >= w) upto += x;
+  }
+  if (lane == 31) plan[4 + warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) upto += total;
+    total += plan[4 + w];
+  }
+  if (total > 0) {
+    const Runs runs(total * pa.Hkv, gridDim.x);
+    if ((int)blockIdx.x < runs.n) {
+      const long long begin = runs.begin(blockIdx.x), at = begin % total;
+      if (at >= upto - sum && at < upto) {  // one thread
+        long long x = upto - sum;
+        walk([&](int s, long long len) {
+          plan[1] = s;
+          plan[2] = begin - at + x;  // where item (head, slot s) begins
+          x += len;
+          return x <= at;
+        });
+        plan[3] = begin / total;  // the head
+      }
+    }
+  }
+  if (tid == 0) {
+    plan[0] = total;
+    ChunkRun none;
+    none.nrows = 0;
+    ca.runs[blockIdx.x] = none;
+  }
+  __syncthreads();
+
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == kSoftWarps + 1) {
+      // -------------------------------------------------------------- K and V (warp 10 finds the items)
+      int stage = 0;
+      uint32_t phase = 0, filled = 0, fill_phase = 0;
+      // the pages of 32 x page_size positions from table column 32 `window` on and of the next ones, a page a lane
+      int window_slot = -1, window = 0, page_now = 0, page_next = 0;
+      bool tail = false;  // the last block of values loaded needs its end cleared
+      int tail_stage = 0, tail_keys = 0, behind = 0;
+      uint32_t tail_phase = 0;
+      // What pages hold past a sequence's end is anyone's: the last block's values there become zeros once they have
+      // arrived, as 0 times a leftover that is not finite would be NaN. This is done when the two copies behind them are
+      // on their way: their stages wait for nothing that comes after the block before.
+      auto clear_tail = [&]() {
+        if (!tail) return true;
+        if (!warp_wait(bar(TAIL), tail_phase, timeout_ns, abort_flag, status, 51)) return false;
+        tail = false;
+        tail_phase ^= 1u;
+        const uint32_t dst = sKV + tail_stage * C::kTileBytes;
+        for (int i = lane; i < (BK - tail_keys) * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                         ::"r"(dst + c * (BK * 128) + tail_keys * 128 + i * 16), "r"(0) : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(FULL + tail_stage));
+        return true;
+      };
+      const CacheView& cv = ca.d.c;
+      const int box = min(cv.page_size, BK), box_shift = min(cv.page_shift, 7);
+      const bool leader = elect_one();
+      bool ok = true;
+      while (ok) {
+        if (tail && !__all_sync(0xffffffffu, mbar_try_wait(bar(IFULL + iq), iphase)) && !clear_tail()) break;
+        const Item* ip = next_item();
+        if (ip == nullptr) break;
+        const int slot = ip->k0, hk = ip->hk, n = blocks(ip->n_keys);
+        int j0 = ip->key0, rest = ip->nk - j0;  // the block's first position, and what the sequence holds from there on
+        const int seq = ip->seq;
+        // Keys that one item alone reads leave L2 first: they would push out those that the tile pairs of a longer
+        // chunk share (64 single tokens behind 8192: 203 -> 196 us).
+        const uint64_t policy = l2_policy((long long)ip->nq * G <= 2 * TM);
+        item_done();
+        const int32_t* row = cv.table + (long long)slot * cv.width;
+        // The whole warp walks the copies and one elected thread issues them: what they are given stays in uniform
+        // registers.
+        for (int j = 0; j < n && ok; ++j, j0 += BK, rest -= BK) {
+          // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
+          const int col = j0 >> cv.page_shift;
+          if (window_slot != slot || window != col >> 5) {
+            auto read = [&](int w) {
+              int page = w * 32 + lane < cv.width ? row[w * 32 + lane] : 0;
+              if (page < 0 || page >= cv.n_pages) page = -1;
+              return page;
+            };
+            page_now = window_slot == slot && window + 1 == col >> 5 ? page_next : read(col >> 5);
+            window_slot = slot;
+            window = col >> 5;
+            page_next = read(window + 1);
+          }
+          const int held = min(BK, rest), boxes = (held + box - 1) >> box_shift;
+          if (__any_sync(0xffffffffu, page_now < 0 && ((lane - col) & 31) < boxes)) {
+            if (lane == 0) record_error(status, MOE_ERR_DEVICE_CHECK, seq);
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {  // K, then V
+            const bool cut = v == 1 && held < BK;
+            if (tail && (++behind > 2 || cut) && !(ok = clear_tail())) break;
+            ok = warp_wait(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
+            if (!ok) break;
+            const uint32_t b = cut ? bar(TAIL) : bar(FULL + stage);
+            uint32_t dst = sKV + stage * C::kTileBytes;
+            if (leader) mbar_arrive_expect_tx(b, (uint32_t)((boxes << box_shift) * C::kChunks * 128));
+            for (int i = 0; i < boxes; ++i, dst += 128 << box_shift) {
+              const int page = max(0, __shfl_sync(0xffffffffu, page_now, (col + i) & 31));
+              const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
+              if (leader) {
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+                  tma_load_3d_hint(dst + c * (BK * 128), v ? &tmV : &tmK, 64 * c, g, ca.d.layer, b, policy);
+              }
+            }
+            if (cut) {
+              tail = true;
+              behind = 0;
+              tail_stage = stage;
+              tail_keys = held;
+            }
+            filled |= 1u << stage;
+            fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+          }
+        }
+      }
+      if (!clear_tail() && lane == 0) {  // (given up: the copies are waited for all the same)
+        mbar_wait_bounded(bar(TAIL), tail_phase, timeout_ns);
+        mbar_arrive(bar(FULL + tail_stage));
+      }
+      if (lane == 0)
+        for (int s = 0; s < C::kStages; ++s)
+          if (filled & (1u << s)) mbar_wait_bounded(bar(FULL + s), (fill_phase >> s) & 1u, timeout_ns);
+      __syncwarp();
+    } else if (warp > kSoftWarps + 1) {
+      // -------------------------------------------------------------- Q tiles, the swizzled K-major operand. Where the
+      // group's heads divide a tile's rows one TMA box is 128 / G tokens of G heads, in the packed rows' order (rows
+      // past the end hold whatever comes next: they see no key and are not stored). Else kLanes lanes copy a row,
+      // with zeros past the rows and past D: 5 us a tile, against 1.5.
+      constexpr int kLanes = DP / 8, kRowsPer = 32 / kLanes;
+      const int t = warp - kSoftWarps - 2;
+      uint32_t loads = 0;
+      // The first of these warps walks the CTA's run and publishes its items, one ahead of the Q tiles it loads. It
+      // looks at 32 tile slots at once, one a lane (the next of an item after the other cost 9 us an item).
+      const bool finder = t == 0;
+      const Runs runs(finder ? plan[0] * Hkv : 0, gridDim.x);
+      const long long run_begin = finder && (int)blockIdx.x < runs.n ? runs.begin(blockIdx.x) : 0;
+      const long long run_end = finder && (int)blockIdx.x < runs.n ? runs.begin(blockIdx.x + 1) : 0;
+      ChunkItem ci{};
+      int base = finder ? (int)plan[1] & ~31 : 0, head = finder ? (int)plan[3] : 0, loaded = -1;
+      // the place of the 32 slots from `base` on in this head, of the lane's item among them, the length of all
+      long long x = 0, before = 0, length = 0;
+      int b0 = 0, b1 = 0;
+      uint32_t todo = 0;  // the lanes whose items have blocks in the run and are not published yet
+      bool late = false;
+      auto load_slots = [&]() {
+        const int s = base + lane;
+        ci = s < n_items ? chunk_item(pa, ca, s, find_tile_seq(pa.qo, pa.n, G, 2 * TM, s)) : ChunkItem{};
+        loaded = base;
+        const long long len = ci.length();
+        before = len;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, before, w);
+          if (lane >= w) before += y;
+        }
+        length = __shfl_sync(0xffffffffu, before, 31);
+        before -= len;
+      };
+      auto my_item = [&]() {
+        const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
+        Item it{};
+        it.hk = head;
+        it.seq = ci.seq;
+        it.row0 = ci.row0;
+        it.nrows = ci.nrows;
+        it.q0 = ci.q0; it.nq = ci.nq; it.k0 = ci.slot; it.nk = ci.nk;
+        it.key0 = b0 * BK;
+        it.n_keys = min((b1 - b0) * BK, max(ci.lim0, ci.lim1) - it.key0);
+        it.lim0 = max(0, min(ci.lim0 - it.key0, it.n_keys));
+        it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
+        it.dual = ci.nrows <= TM;
+        if (it.dual) it.lim1 = it.lim0;
+        it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
+        if (b0 == 0 && b1 < all) {
+          ChunkRun r;
+          r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
+          r.end = runs.of(x + before + (long long)(all - 1) * kBlock);
+          ca.runs[blockIdx.x] = r;
+        }
+        return it;
+      };
+      // The blocks of the slots' items that lie in the run: block j begins at x + before + j kBlock.
+      auto look = [&]() {
+        if (loaded != base) load_slots();
+        const int all = max(1, ci.n_blocks);
+        auto first_from = [&](long long p) {
+          p -= x + before;
+          return p <= 0 ? 0 : (int)min((long long)all, (p + kBlock - 1) / kBlock);
+        };
+        b0 = first_from(run_begin);
+        b1 = first_from(run_end);
+        const bool in = ci.nrows > 0 && b0 < b1;
+        // The end of an item that began in another run comes last: the whole items of all runs then begin with their
+        // first keys at about the same time, and L2 serves those that share a head.
+        const bool is_late = in && x + before < run_begin;
+        if (is_late) *late_item = my_item();
+        __syncwarp();
+        late = late || __any_sync(0xffffffffu, is_late);
+        todo = __ballot_sync(0xffffffffu, in && !is_late);
+      };
+      bool ended = run_begin == run_end;
+      if (!ended) {
+        load_slots();
+        x = plan[2] - __shfl_sync(0xffffffffu, before, (int)plan[1] & 31);
+        look();
+      }
+      // Publishes the run's next item, or its end.
+      auto advance = [&]() {
+        while (todo == 0 && !ended) {
+          x += length;
+          base += 32;
+          if (base >= n_items) {
+            base = 0;
+            ++head;
+          }
+          if (x >= run_end) ended = true;
+          else look();
+        }
+        if (!warp_wait(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51)) return false;
+        int from = 0;
+        if (todo != 0) {
+          from = __ffs(todo) - 1;
+          todo &= todo - 1;
+          if (lane == from) items[iq] = my_item();
+        } else if (late) {
+          late = false;
+          if (lane == 0) items[iq] = *late_item;
+        } else if (lane == 0) {
+          items[iq] = Item{};
+          items[iq].last = 1;
+        }
+        __syncwarp();
+        if (lane == from) mbar_arrive(bar(IFULL + iq));
+        if (++iq == kItems) { iq = 0; iphase ^= 1u; }
+        return true;
+      };
+      int mine = 0;  // the place of the finder's own next item
+      if (finder && !advance()) ended = true;
+      while (true) {
+        Item it;
+        if (finder) {
+          it = items[mine];
+          if (it.last || !advance()) break;
+          if (++mine == kItems) mine = 0;
+        } else {
+          const Item* ip = next_item();
+          if (ip == nullptr) break;
+          it = *ip;
+          item_done();
+        }
+        if ((t ? it.lim1 : it.lim0) == 0) continue;
+        if (!warp_wait(bar(QEMPTY + t), (loads & 1u) ^ 1u, timeout_ns, abort_flag, status, 55)) break;
+        ++loads;
+        if (q_tma) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(QFULL + t), C::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(sQ + t * C::kTileBytes + c * (TM * 128), &tmQ, 64 * c, it.hk * G,
+                          it.q0 + (it.row0 + (it.dual ? 0 : t * TM)) / G, bar(QFULL + t));
+          }
+          continue;
+        }
+        const int first = it.dual ? 0 : t * TM, nrow_t = min(TM, it.nrows - first);
+        const __nv_bfloat16* q = (const __nv_bfloat16*)pa.q + (long long)it.q0 * pa.qs;
+#pragma unroll
+        for (int k = 0; k < TM / 32; ++k) {
+          const int R = it.row0 + first + 32 * k + lane, tok = R / G;  // (rows past the end are not read)
+          const __nv_bfloat16* row = q + (long long)tok * pa.qs + (long long)(it.hk * G + R - tok * G) * D;
+#pragma unroll 4
+          for (int i = 0; i < 32 / kRowsPer; ++i) {
+            const int rr = i * kRowsPer + lane / kLanes, u = lane % kLanes, rt = 32 * k + rr;
+            const __nv_bfloat16* src = (const __nv_bfloat16*)__shfl_sync(0xffffffffu, (unsigned long long)row, rr);
+            const bool in = rt < nrow_t && u * 8 < D;
+            const uint32_t dst = sQ + t * C::kTileBytes + (u / 8) * (TM * 128) + rt * 128 + (((u & 7) ^ (rt & 7)) * 16);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(dst), "l"(in ? src + u * 8 : q), "r"(in ? 16 : 0) : "memory");
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(QFULL + t));
+      }
+      if (loads > 0) mbar_wait_bounded(bar(QFULL + t), (loads - 1) & 1u, timeout_ns);  // copies in flight
+    } else {
+      // -------------------------------------------------------------- MMAs
+      // The whole warp walks the loop and one elected thread issues: descriptors and addresses then stay in uniform
+      // registers. Inside a one-lane branch every MMA first moved its operands there, which took as long as
+      // the MMA itself (about 70 of 64 cycles).
+      const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      constexpr uint32_t idesc_qk = make_idesc_bf16_f32(TM, BK, false);
+      constexpr uint32_t idesc_half = make_idesc_bf16_f32(TM, BK / 2, false);
+      constexpr uint32_t idesc_pv = make_idesc_bf16_f32(TM, DP, true);
+      bool dual = false;  // tile t has keys t BK / 2 .. of each block (the same rows)
+      int stage = 0;
+      uint32_t phase = 0;
+      auto wait = [&](int b, uint32_t ph) {
+        const bool ok = warp_wait(bar(b), ph, timeout_ns, abort_flag, status, 52);
+        tc_fence_after();
+        return ok;
+      };
+      // three barriers at once: the tests go out together, as each takes about 100 cycles to answer (and waits in the
+      // warp's queue behind the MMAs issued before it)
+      auto wait3 = [&](int b0, uint32_t p0, int b1, uint32_t p1, int b2, uint32_t p2) {
+        const bool r0 = mbar_try_wait_long(bar(b0), p0), r1 = mbar_try_wait_long(bar(b1), p1),
+                   r2 = mbar_try_wait_long(bar(b2), p2);
+        if (!__builtin_expect(__all_sync(0xffffffffu, r0 && r1 && r2), 1)) {
+          if (!warp_wait(bar(b0), p0, timeout_ns, abort_flag, status, 52)) return false;
+          if (!warp_wait(bar(b1), p1, timeout_ns, abort_flag, status, 52)) return false;
+          if (!warp_wait(bar(b2), p2, timeout_ns, abort_flag, status, 52)) return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      auto keys_of = [&](int t, int st) { return sKV + st * C::kTileBytes + (dual ? t * (BK / 2) * 128 : 0); };
+      auto qk = [&](int t, int st, int b2 = 0) {  // (b2: which half of the tile's columns, by halves of blocks)
+        const uint64_t a = make_smem_desc_sw128(sQ + t * C::kTileBytes, 16, 1024);
+        const uint64_t b = make_smem_desc_sw128(keys_of(t, st), 16, 1024);
+        const uint32_t idesc = dual ? idesc_half : idesc_qk;
+        if (!leader) return;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk / 4) * (TM * 128) + (kk % 4) * 32) >> 4);
+          tc_mma_f16(tm + t * BK + b2 * (BK / 2), a + off, b + off, idesc, kk != 0);
+        }
+        tc_commit(bar(SFULL + 2 * b2 + t));
+      };
+      auto pv = [&](int t, int st, bool acc, int b2 = 0) {
+        const uint64_t b = make_smem_desc_sw128(keys_of(t, st), BK * 128, 1024);
+        if (!leader) return;
+        if (dual) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + b2 * (BK / 2) + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4),
+                          idesc_pv, acc || kk != 0);
+          tc_commit(bar(ODONE + t));
+          return;
+        }
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_f16_ta(tm + 256 + t * DP, tm + t * BK + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                        acc || kk != 0);
+        tc_commit(bar(ODONE + t));
+      };
+      auto next = [&]() { if (++stage == C::kStages) { stage = 0; phase ^= 1u; } };
+      uint32_t pp0 = 0, pp1 = 0, qp0 = 0, qp1 = 0;  // phases of the tiles' P and Q barriers
+      uint32_t pp0b = 0, pp1b = 0;                  // and of the second P barriers
+      bool ok = true;
+      while (ok) {
+        const Item* it = next_item();
+        if (it == nullptr) break;
+        const int n0 = __shfl_sync(0xffffffffu, blocks(it->lim0), 0);
+        const int n1 = __shfl_sync(0xffffffffu, blocks(it->lim1), 0);
+        const int nn = max(n0, n1);
+        dual = __shfl_sync(0xffffffffu, it->dual, 0) != 0;
+        item_done();
+        if (nn == 0) continue;
+        if (dual) {
+          // Both halves' scores are computed two blocks ahead: they take half of the tile's columns each time, so block
+          // j + 1 need not wait for the softmax of block j. Copy i of the item (K0 V0 K1 V1 ..) is in this stage:
+          auto copy_at = [&](int i, int& st, uint32_t& ph) {
+            const int x = stage + i;
+            st = x & (C::kStages - 1);
+            ph = phase ^ ((uint32_t)(x / C::kStages) & 1u);
+          };
+          int st, ks;
+          uint32_t ph, kp;
+          for (int j = 0; j < 2 && j < nn && ok; ++j) {
+            copy_at(2 * j, st, ph);
+            ok = wait(FULL + st, ph);
+            if (ok && j == 0) {
+              ok = wait(QFULL, qp0) && wait(QFULL + 1, qp1);
+              qp0 ^= 1u;
+              qp1 ^= 1u;
+            }
+            if (!ok) break;
+            qk(0, st, j);
+            qk(1, st, j);
+            if (leader) {
+              tc_commit(bar(EMPTY + st));
+              if (j + 1 == nn) {
+                tc_commit(bar(QEMPTY));
+                tc_commit(bar(QEMPTY + 1));
+              }
+            }
+          }
+          for (int j = 0; j < nn && ok; ++j) {
+            const int b2 = j & 1;
+            const bool more = j + 2 < nn;
+            copy_at(2 * j + 1, st, ph);
+            ok = wait3(FULL + st, ph, FULL + st, ph, PFULL + 2 * b2, b2 ? pp0b : pp0);
+            if (!ok) break;
+            pv(0, st, j > 0, b2);
+            ok = wait(PFULL + 2 * b2 + 1, b2 ? pp1b : pp1);
+            if (!ok) break;
+            pv(1, st, j > 0, b2);
+            if (leader) tc_commit(bar(EMPTY + st));
+            if (more) {
+              copy_at(2 * j + 4, ks, kp);
+              ok = wait(FULL + ks, kp);
+              if (!ok) break;
+              qk(0, ks, b2);
+              qk(1, ks, b2);
+            }
+            if (b2) { pp0b ^= 1u; pp1b ^= 1u; } else { pp0 ^= 1u; pp1 ^= 1u; }
+            if (leader) {
+              if (more) tc_commit(bar(EMPTY + ks));
+              if (more && j + 3 == nn) {
+                tc_commit(bar(QEMPTY));
+                tc_commit(bar(QEMPTY + 1));
+              }
+            }
+          }
+          copy_at(2 * nn, st, ph);
+          stage = st;
+          phase = ph;
+          continue;
+        }
+        ok = wait(FULL + stage, phase);
+        if (ok && n0 > 0) {
+          ok = wait(QFULL, qp0);
+          qp0 ^= 1u;
+          if (ok) qk(0, stage);
+          if (leader && n0 == 1) tc_commit(bar(QEMPTY));
+        }
+        if (ok && n1 > 0) {
+          ok = wait(QFULL + 1, qp1);
+          qp1 ^= 1u;
+          if (ok) qk(1, stage);
+          if (leader && n1 == 1) tc_commit(bar(QEMPTY + 1));
+        }
+        if (leader) tc_commit(bar(EMPTY + stage));
+        next();
+        for (int j = 0; j < nn && ok; ++j) {
+          const int vs = stage;
+          const uint32_t vp = phase;
+          next();
+          const int ks = stage;
+          const uint32_t kp = phase;
+          if (j + 1 < nn) next();
+          // V(j), K(j+1) and the first tile's P(j)
+          const bool more = j + 1 < nn;
+          const int pb = PFULL + (j < n0 ? 0 : 1);
+          ok = wait3(FULL + vs, vp, more ? FULL + ks : FULL + vs, more ? kp : vp, pb, j < n0 ? pp0 : pp1);
+          if (!ok) break;
+          if (j < n0) {
+            pp0 ^= 1u;
+            pv(0, vs, j > 0);
+            if (j + 1 < n0) qk(0, ks);
+            if (leader && j + 2 == n0) tc_commit(bar(QEMPTY));
+            if (j < n1) ok = wait(PFULL + 1, pp1);
+          }
+          if (ok && j < n1) {
+            pp1 ^= 1u;
+            pv(1, vs, j > 0);
+            if (j + 1 < n1) qk(1, ks);
+            if (leader && j + 2 == n1) tc_commit(bar(QEMPTY + 1));
+          }
+          if (leader) {
+            tc_commit(bar(EMPTY + vs));
+            if (j + 1 < nn) tc_commit(bar(EMPTY + ks));
+          }
+        }
+      }
+      // every MMA has completed before TMEM and shared memory go away
+      if (leader) tc_commit(bar(DONE));
+      mbar_wait_bounded(bar(DONE), 0, timeout_ns);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int t = warp >> 2, r = tid & 127;  // tile, row of it
+    const int q4 = warp & 3;                 // TMEM lanes 32 q4 ..
+    const float c2 = pa.scale * 1.4426950408889634f;
+    const float thr = rescale_above(c2);
+    const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+    const uint32_t tS = tmem + lanes + t * BK, tO = tmem + lanes + 256 + t * DP;
+    uint32_t done = 0;  // blocks of all items so far: the phase of the last PV's barrier
+    uint32_t seen = 0;  // phases of the scores' barriers, a bit each
+    uint32_t given = 0;  // exchanges with the other tile's warp
+    bool ok = true;
+    while (ok) {
+      const Item* it = next_item();
+      if (it == nullptr) break;
+      // Where the thread's row lies. (It is found again after the loop, which has no registers to keep it in.)
+      bool dual, valid;
+      int tile0, nrow_t, tok, h;
+      auto place = [&]() {
+        int g = G;
+        asm volatile("" : "+r"(g));
+        dual = it->dual;
+        tile0 = dual ? 0 : t * TM;               // the tile's first row of the item's
+        nrow_t = min(TM, it->nrows - tile0);     // rows of this tile (<= 0: none)
+        const int R = it->row0 + tile0 + r;
+        valid = r < nrow_t;
+        tok = valid ? R / g : 0;
+        h = it->hk * g + (valid ? R % g : 0);
+      };
+      place();
+      const int n = blocks(t ? it->lim1 : it->lim0);
+      // (What a row past the tile's end makes of whatever lies there is dropped, so these are not masked: a tile of a
+      // single token's heads would go through the masking below in every block, 1.15 us a block against 0.95.)
+      int lim = 0x7fffffff;
+      if (valid) lim = max(0, min(visible_keys(tok, it->nq, it->nk, pa.causal) - it->key0, it->n_keys));
+      float m = -INFINITY, l = 0.f;
+      // Block j, of which the tile has COLS keys: 128, or half of them.
+      auto block = [&](auto cols, int j) {
+        constexpr int NC = decltype(cols)::value / 32;
+        const int b2 = NC < 4 ? j & 1 : 0;  // by halves, blocks alternate between the halves of the tile's columns
+        const uint32_t tB = tS + b2 * (BK / 2);
+        ok = warp_wait(bar(SFULL + 2 * b2 + t), seen >> b2 & 1u, timeout_ns, abort_flag, status, 53);
+        if (!ok) return;
+        seen ^= 1u << b2;
+        tc_fence_after();
+        uint32_t s[NC][32];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) tmem_ld_32x32b_x32(tB + 32 * c, s[c]);
+        tmem_ld_wait();
+        const int left = lim - j * BK - (NC < 4 ? t * (BK / 2) : 0);  // columns that this row sees
+        if (__any_sync(0xffffffffu, left < 32 * NC)) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= left) s[c][i] = 0xff800000u;  // -inf
+        }
+        // four chains of three-input maxima (max drops a NaN score: the maximum is never NaN)
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 16 * NC; ++i) {
+          const uint32_t* v = &s[i >> 4][2 * (i & 15)];
+          mx4[i & 3] = max3(mx4[i & 3], __uint_as_float(v[0]), __uint_as_float(v[1]));
+        }
+        const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+        if (__any_sync(0xffffffffu, mx > m + thr)) {
+          const bool up = mx > m + thr;
+          if (j > 0) {
+            ok = warp_wait(bar(ODONE + t), (done - 1) & 1, timeout_ns, abort_flag, status, 53);
+            if (!ok) return;
+            tc_fence_after();
+            const float a = up ? ex2((m - mx) * c2) : 1.0f;
+            l *= a;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tO + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st_32x32b_x32(tO + 32 * c, o);
+            }
+          }
+          if (up) m = mx;
+        }
+        const float mc = m == -INFINITY ? 0.f : -m * c2;
+        const uint64_t c2p = f2_pack(c2, c2), mcp = f2_pack(mc, mc);
+        // in batches of 16: the arguments and powers of one batch are issued before the sums and packing of the one
+        // before, so that nothing waits for a power of two just asked for
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int h = 0; h < NC / 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int b = 0; b < 5; ++b) {
+            if (b < 4) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint32_t* v = &s[2 * h + (b >> 1)][16 * (b & 1) + 2 * i];
+                const uint64_t x = ffma2(((uint64_t)v[1] << 32) | v[0], c2p, mcp);
+                v[0] = (uint32_t)x;
+                v[1] = (uint32_t)(x >> 32);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                uint32_t& v = s[2 * h + (b >> 1)][16 * (b & 1) + i];
+                v = __float_as_uint(ex2(__uint_as_float(v)));
+              }
+            }
+            if (b > 0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t* v = &s[2 * h + ((b - 1) >> 1)][16 * ((b - 1) & 1) + 2 * i];
+                const uint64_t x = ((uint64_t)v[1] << 32) | v[0];
+                if (i & 1) sum1 = fadd2(sum1, x); else sum0 = fadd2(sum0, x);
+                p[8 * (b - 1) + i] = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              }
+            }
+          }
+          tmem_st_32x32b_x32(tB + 32 * h, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (NC < 4 && j > 0 && j == n - 1) {
+          // Once this block's weights are given the barrier may go on by two phases, whose parities would look alike, so
+          // the PV before (in flight for one softmax by now) is waited for first.
+          ok = warp_wait(bar(ODONE + t), (done - 1) & 1, timeout_ns, abort_flag, status, 53);
+          if (!ok) return;
+        }
+        if (lane == 0) mbar_arrive(bar(PFULL + 2 * b2 + t));
+        const uint64_t sum = fadd2(sum0, sum1);
+        l += f2_lo(sum) + f2_hi(sum);
+      };
+      const bool halves = dual;
+      for (int j = 0; j < n && ok; ++j) {
+        if (halves) block(std::integral_constant<int, BK / 2>{}, j);
+        else block(std::integral_constant<int, BK>{}, j);
+        done += ok ? 1 : 0;
+      }
+      // ---- the rows' results
+      if (ok && n > 0) {
+        ok = warp_wait(bar(ODONE + t), (done - 1) & 1, timeout_ns, abort_flag, status, 53);
+        tc_fence_after();
+      }
+      place();
+      if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
+        uint32_t again = 0;  // rows whose results are looked at again (replace_unseen)
+        if (dual && t == 1) {
+          // the other half of the keys of tile 0's rows: m, l and the sums to the warp there, 32 elements a step
+          const uint32_t stg = sOut + warp * C::kStage;
+          given_ml[32 * q4 + lane] = make_float2(m, l);
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c, ++given) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + 32 * c, o);  // (not this item's where there was no block: not used then)
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = m == -INFINITY ? 0u : o[i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)),
+                           "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                           : "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(GIVEN + q4));
+            ok = ok && warp_wait(bar(TAKEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+          }
+        } else {
+          // a piece: the sums in fp32; a whole item: the results in bf16. 32 or 64 elements a step through shared memory,
+          // so that a store covers whole rows
+          const bool part = it->split >= 0;
+          const long long at = part ? ((long long)it->split * ca.piece_rows + tile0 + r) * D
+                                    : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
+          uint8_t* orow = part ? reinterpret_cast<uint8_t*>(ca.part_o + at) : (uint8_t*)pa.out + 2 * at;
+          float f1 = 0.f, f0 = 1.f;  // factors of tile 1's sums and of this tile's
+          if (dual) {
+            ok = warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+            const float2 x = given_ml[32 * q4 + lane];
+            const float top = fmaxf(m, x.x);
+            f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2);
+            f1 = x.x == -INFINITY ? 0.f : ex2((x.x - top) * c2);
+            l = l * f0 + x.y * f1;
+            m = top;
+          }
+          const float f = part ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+          f0 *= f;
+          f1 *= f;
+          const uint32_t stg = sOut + warp * C::kStage;
+          const uint64_t f2 = f2_pack(f0, f0), g2 = f2_pack(f1, f1);
+          uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
+          // A row's 128 bytes (32 sums or 64 results) from shared memory to `to`, of which the first `elems` exist
+          auto store = [&](uint32_t to, int elems, int per) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int u = lane & 7, rr = 4 * i + (lane >> 3);
+              uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + to + 16 * u;
+              uint4 x;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(stg + rr * 128 + ((u ^ (rr & 7)) * 16)) : "memory");
+              if (32 * q4 + rr < nrow_t && per * u < elems) *reinterpret_cast<uint4*>(dst) = x;
+            }
+          };
+#pragma unroll 1  // (run once an item: what is not in the instruction cache costs more than the loop)
+          for (int c = 0; c < DP / 64; ++c) {
+            uint32_t o2[2][32];
+            tmem_ld_32x32b_x32(tO + 64 * c, o2[0]);  // (not this item's where there was no block: lim is 0 then)
+            tmem_ld_32x32b_x32(tO + 64 * c + 32, o2[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint32_t(&o)[32] = o2[b];
+              if (dual && c + b > 0)
+                ok = ok && warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint64_t v0 = ffma2(((uint64_t)o[4 * i + 1] << 32) | o[4 * i], f2, 0ull);
+                uint64_t v1 = ffma2(((uint64_t)o[4 * i + 3] << 32) | o[4 * i + 2], f2, 0ull);
+                if (dual) {
+                  uint64_t x0, x1;
+                  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x0), "=l"(x1)
+                               : "r"(stg + 4 * C::kStage + lane * 128 + ((i ^ (lane & 7)) * 16)) : "memory");
+                  v0 = ffma2(x0, g2, v0);
+                  v1 = ffma2(x1, g2, v1);
+                }
+                if (lim == 0) v0 = v1 = 0ull;
+                odd = ffma2(v0, 0ull, odd);
+                odd = ffma2(v1, 0ull, odd);
+                o[4 * i] = (uint32_t)v0;
+                o[4 * i + 1] = (uint32_t)(v0 >> 32);
+                o[4 * i + 2] = (uint32_t)v1;
+                o[4 * i + 3] = (uint32_t)(v1 >> 32);
+              }
+              if (dual) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(TAKEN + q4));
+                ++given;
+              }
+              if (part) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                               ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)), "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                               : "memory");
+                __syncwarp();
+                store((2 * c + b) * 128, D - 64 * c - 32 * b, 4);
+                __syncwarp();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                               ::"r"(stg + lane * 128 + (((4 * b + i) ^ (lane & 7)) * 16)),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]))),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]))),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]))),
+                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])))
+                               : "memory");
+              }
+            }
+            if (!part) {
+              __syncwarp();
+              store(c * 128, D - 64 * c, 8);
+              __syncwarp();
+            }
+          }
+          if (valid && part) ca.part_ml[(long long)it->split * ca.piece_rows + tile0 + r] = make_float2(m * c2, l);
+          if (valid && !part && pa.lse != nullptr)
+            pa.lse[(long long)(it->q0 + tok) * H + h] =
+                lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
+          // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
+          again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
+        }
+        if (again != 0) {
+          Unseen unseen(min(n * BK, it->nk - it->key0));
+          while (again != 0) {
+            const int w = __ffs(again) - 1;
+            again &= again - 1;
+            const int tw = __shfl_sync(0xffffffffu, tok, w), hw = __shfl_sync(0xffffffffu, h, w);
+            const float mw = __shfl_sync(0xffffffffu, m, w), lw = __shfl_sync(0xffffffffu, l, w);
+            float o[8];
+            const uint32_t cols = replace_unseen(
+                unseen, (const __nv_bfloat16*)pa.q + (long long)(it->q0 + tw) * pa.qs + (long long)hw * D,
+                (const __nv_bfloat16*)ca.d.k, (const __nv_bfloat16*)ca.d.v,
+                [&](int j, long long& ko, long long& vo) {  // where key j of the item lies
+                  const CacheView& cv = ca.d.c;
+                  const int p = it->key0 + j;
+                  int page = cv.table[(long long)it->k0 * cv.width + (p >> cv.page_shift)];
+                  page = page < 0 || page >= cv.n_pages ? 0 : page;
+                  ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
+                },
+                D, __shfl_sync(0xffffffffu, lim, w), c2, mw == -INFINITY ? 0.f : mw * c2, o);
+            float* po = ca.part_o + ((long long)it->split * ca.piece_rows + tile0 + 32 * q4 + w) * D + lane * 8;
+            __nv_bfloat16* dw =
+                (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D + lane * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (cols >> e & 1u) {
+                if (it->split >= 0) po[e] = o[e];
+                else dw[e] = __float2bfloat16_rn(o[e] * (lw == 0.f ? 0.f : 1.0f / lw));
+              }
+          }
+        }
+      }
+      tc_fence_before();
+      item_done();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The rows that several runs share, by the run that such an item begins in (blockIdx.x): a warp a row, its pieces in
+// their order, eight on their way at a time.
+__global__ void __launch_bounds__(256)
+chunk_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ ChunkArgs ca) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), c0 = blockIdx.x;
+  const ChunkRun run = ca.runs[c0];
+  if (r >= run.nrows) return;
+  const int G = a.H / a.Hkv, R = run.row0 + r, tok = run.q0 + R / G, h = run.hk * G + R % G, n = run.end - c0 + 1;
+  // run c0 has its last item's piece, the others their first's
+  auto row = [&](int i) { return (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * ca.piece_rows + r; };
+  float M = -INFINITY, l = 0.f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ca.part_ml[row(i)].x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  const float ref = M == -INFINITY ? 0.f : M;
+  const bool on = lane * 4 < a.D;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float2 v = i0 + lane < n ? ca.part_ml[row(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    const float wl = ex2(v.x - ref);
+    l += wl * v.y;
+    for (int y0 = 0; y0 < 32 && i0 + y0 < n; y0 += 8) {
+      float4 u[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        u[y] = on && i0 + y0 + y < n ? reinterpret_cast<const float4*>(ca.part_o + row(i0 + y0 + y) * a.D)[lane]
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xffffffffu, wl, y0 + y);
+        o.x = fmaf(w, u[y].x, o.x);
+        o.y = fmaf(w, u[y].y, o.y);
+        o.z = fmaf(w, u[y].z, o.z);
+        o.w = fmaf(w, u[y].w, o.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  if (on) {
+    uint2 u;
+    u.x = pack_bf16x2(o.x * inv, o.y * inv);
+    u.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * a.D + lane * 4) = u;
+  }
+  if (a.lse != nullptr && lane == 0)
+    a.lse[(long long)tok * a.H + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int DP>
+cudaError_t launch(const CUtensorMap& tq, const CacheMaps& m, const PromptArgs& pa, const ChunkArgs& ca, int ctas,
+                   int slots, int q_tma, cudaStream_t s) {
+  static std::atomic<int> done{0};
+  auto kern = attn_chunk_kernel<DP>;
+  const cudaError_t e = allow_smem(kern, Cfg<DP>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  // Not as a programmatic dependent: its CTAs would then take the SMs in the order in which the kernel before leaves
+  // them, and CTAs with neighbouring runs, which read the same keys, would lie anywhere on the two dies. 64 sequences of
+  // single tokens and chunks back to back: 1045 us so, 865 us in the usual order.
+  kern<<<dim3(ctas), dim3(kThreads), Cfg<DP>::kSmem, s>>>(tq, m.k128, m.v128, pa, ca, slots, q_tma);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int chunk_piece_rows(int Tq, int G) {
+  return (long long)Tq * G < 2 * TM ? Tq * G : 2 * TM;
+}
+
+cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, ChunkRun* runs,
+                                 float* part, cudaStream_t s) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  CUtensorMap tq{};
+  const int G = a.H / a.Hkv;
+  int q_tma = 0;
+  if (enc == nullptr || !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma)) return cudaErrorInvalidValue;
+  const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM);
+  // one CTA an SM, as far as the longest sequences that the cache may hold make as many runs
+  const long long longest = kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kBlock;
+  const long long runs_most = a.Hkv * (long long)slots * longest / kShortest;
+  const int ctas = (int)(runs_most < 1 ? 1 : (runs_most < device_sm_count() ? runs_most : device_sm_count()));
+  ChunkArgs ca{};
+  ca.d = d;
+  ca.runs = runs;
+  ca.piece_rows = chunk_piece_rows(a.Tq, G);
+  ca.part_o = part;
+  ca.part_ml = reinterpret_cast<float2*>(part + 2LL * ctas * ca.piece_rows * a.D);
+  const cudaError_t e = a.D <= 64 ? launch<64>(tq, m, a, ca, ctas, slots, q_tma, s)
+                                  : launch<128>(tq, m, a, ca, ctas, slots, q_tma, s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((ca.piece_rows + 7) / 8)), dim3(256), 0, s, a,
+                    ca);
+}
+
+}  // namespace moe
