@@ -87,17 +87,18 @@ struct ChunkArgs {
 // several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order, so
 // that results do not depend on which CTA is done first. A run has at most two such items, its first and its last: 2
 // pieces a CTA are enough however long the keys.
-constexpr int kBlock = 4, kItem = 16, kShortest = 16;
+constexpr int kOne = 4, kTwo = 4, kItem = 16, kShortest = 16;
 
-// Length of an item of so many keys.
-__device__ __forceinline__ long long chunk_length(int keys) {
-  return kItem + (long long)((keys + BK - 1) / BK) * kBlock;
+// Length of a block of an item with so many rows, and of an item with so many blocks.
+__device__ __forceinline__ int block_length(int rows) { return rows <= TM ? kOne : kTwo; }
+__device__ __forceinline__ long long item_length(int rows, int blocks) {
+  return kItem + (long long)blocks * block_length(rows);
 }
 
 struct ChunkItem {
   int seq, row0, nrows, q0, nq, nk, slot;
   int lim0, lim1, n_blocks;
-  __device__ __forceinline__ long long length() const { return nrows > 0 ? kItem + (long long)n_blocks * kBlock : 0; }
+  __device__ __forceinline__ long long length() const { return nrows > 0 ? item_length(nrows, n_blocks) : 0; }
 };
 // What fills tile slot s (nrows = 0: nothing).
 __device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const ChunkArgs& ca, int s, int i) {
@@ -236,7 +237,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           const int row0 = (int)(s - first) * 2 * TM, nrows = min(2 * TM, (int)rows - row0), nq = q[k + 1] - q[k];
           const int lim0 = visible_keys((row0 + min(nrows, TM) - 1) / G, nq, len[k], pa.causal);
           const int lim1 = nrows > TM ? visible_keys((row0 + nrows - 1) / G, nq, len[k], pa.causal) : 0;
-          if (!f(s, chunk_length(max(lim0, lim1)))) return;
+          if (!f(s, item_length(nrows, blocks(max(lim0, lim1))))) return;
         }
       }
       i += 4;
@@ -326,30 +327,40 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // Keys that one item alone reads leave L2 first: they would push out those that the tile pairs of a longer
         // chunk share (64 single tokens behind 8192: 203 -> 196 us).
         const uint64_t policy = l2_policy((long long)ip->nq * G <= 2 * TM);
+        // Copies lie in the ring in the order in which the MMAs take them: K0 V0 K1 V1 .., and where the scores are computed
+        // two blocks ahead K0 K1 V0 K2 V1 .. (each copy then has two blocks' time to arrive).
+        const int lag = ip->dual;
         item_done();
         const int32_t* row = cv.table + (long long)slot * cv.width;
         // The whole warp walks the copies and one elected thread issues them: what they are given stays in uniform
         // registers.
-        for (int j = 0; j < n && ok; ++j, j0 += BK, rest -= BK) {
-          // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
-          const int col = j0 >> cv.page_shift;
-          if (window_slot != slot || window != col >> 5) {
-            auto read = [&](int w) {
-              int page = w * 32 + lane < cv.width ? row[w * 32 + lane] : 0;
-              if (page < 0 || page >= cv.n_pages) page = -1;
-              return page;
-            };
-            page_now = window_slot == slot && window + 1 == col >> 5 ? page_next : read(col >> 5);
-            window_slot = slot;
-            window = col >> 5;
-            page_next = read(window + 1);
+        for (int j = 0; j < n + lag && ok; ++j, j0 += BK, rest -= BK) {
+          int page_v = page_now;
+          if (j < n) {
+            // the pages (the 32 of a window begin at a multiple of 32, so that no block lies in two)
+            const int col = j0 >> cv.page_shift;
+            if (window_slot != slot || window != col >> 5) {
+              auto read = [&](int w) {
+                int page = w * 32 + lane < cv.width ? row[w * 32 + lane] : 0;
+                if (page < 0 || page >= cv.n_pages) page = -1;
+                return page;
+              };
+              page_now = window_slot == slot && window + 1 == col >> 5 ? page_next : read(col >> 5);
+              window_slot = slot;
+              window = col >> 5;
+              page_next = read(window + 1);
+            }
+            const int boxes = (min(BK, rest) + box - 1) >> box_shift;
+            if (__any_sync(0xffffffffu, page_now < 0 && ((lane - col) & 31) < boxes)) {
+              if (lane == 0) record_error(status, MOE_ERR_DEVICE_CHECK, seq);
+            }
           }
-          const int held = min(BK, rest), boxes = (held + box - 1) >> box_shift;
-          if (__any_sync(0xffffffffu, page_now < 0 && ((lane - col) & 31) < boxes)) {
-            if (lane == 0) record_error(status, MOE_ERR_DEVICE_CHECK, seq);
-          }
+          if (lag == 0) page_v = page_now;
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {  // K, then V
+          for (int v = 0; v < 2; ++v) {  // K of block j, then V of block j - lag
+            if (v ? j < lag : j >= n) continue;
+            const int back = v ? lag * BK : 0, p0 = j0 - back, held = min(BK, rest + back);
+            const int col = p0 >> cv.page_shift, boxes = (held + box - 1) >> box_shift;
             const bool cut = v == 1 && held < BK;
             if (tail && (++behind > 2 || cut) && !(ok = clear_tail())) break;
             ok = warp_wait(bar(EMPTY + stage), phase ^ 1u, timeout_ns, abort_flag, status, 51);
@@ -358,8 +369,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             uint32_t dst = sKV + stage * C::kTileBytes;
             if (leader) mbar_arrive_expect_tx(b, (uint32_t)((boxes << box_shift) * C::kChunks * 128));
             for (int i = 0; i < boxes; ++i, dst += 128 << box_shift) {
-              const int page = max(0, __shfl_sync(0xffffffffu, page_now, (col + i) & 31));
-              const int g = (page * Hkv + hk) * cv.page_size + (j0 & (cv.page_size - 1));
+              const int page = max(0, __shfl_sync(0xffffffffu, v ? page_v : page_now, (col + i) & 31));
+              const int g = (page * Hkv + hk) * cv.page_size + (p0 & (cv.page_size - 1));
               if (leader) {
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c)
@@ -439,18 +450,18 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (b0 == 0 && b1 < all) {
           ChunkRun r;
           r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
-          r.end = runs.of(x + before + (long long)(all - 1) * kBlock);
+          r.end = runs.of(x + before + (long long)(all - 1) * block_length(ci.nrows));
           ca.runs[blockIdx.x] = r;
         }
         return it;
       };
-      // The blocks of the slots' items that lie in the run: block j begins at x + before + j kBlock.
+      // The blocks of the slots' items that lie in the run: block j begins at x + before + j times a block's length.
       auto look = [&]() {
         if (loaded != base) load_slots();
-        const int all = max(1, ci.n_blocks);
+        const int all = max(1, ci.n_blocks), len = block_length(ci.nrows);
         auto first_from = [&](long long p) {
           p -= x + before;
-          return p <= 0 ? 0 : (int)min((long long)all, (p + kBlock - 1) / kBlock);
+          return p <= 0 ? 0 : (int)min((long long)all, (p + len - 1) / len);
         };
         b0 = first_from(run_begin);
         b1 = first_from(run_end);
@@ -624,7 +635,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (nn == 0) continue;
         if (dual) {
           // Both halves' scores are computed two blocks ahead: they take half of the tile's columns each time, so block
-          // j + 1 need not wait for the softmax of block j. Copy i of the item (K0 V0 K1 V1 ..) is in this stage:
+          // j + 1 need not wait for the softmax of block j. Copy i of the item (K0 K1 V0 K2 V1 ..) is in this stage:
           auto copy_at = [&](int i, int& st, uint32_t& ph) {
             const int x = stage + i;
             st = x & (C::kStages - 1);
@@ -633,7 +644,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           int st, ks;
           uint32_t ph, kp;
           for (int j = 0; j < 2 && j < nn && ok; ++j) {
-            copy_at(2 * j, st, ph);
+            copy_at(j, st, ph);
             ok = wait(FULL + st, ph);
             if (ok && j == 0) {
               ok = wait(QFULL, qp0) && wait(QFULL + 1, qp1);
@@ -654,7 +665,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int j = 0; j < nn && ok; ++j) {
             const int b2 = j & 1;
             const bool more = j + 2 < nn;
-            copy_at(2 * j + 1, st, ph);
+            copy_at(j + 1 < nn ? 2 * j + 2 : 2 * j + 1, st, ph);
             ok = wait3(FULL + st, ph, FULL + st, ph, PFULL + 2 * b2, b2 ? pp0b : pp0);
             if (!ok) break;
             pv(0, st, j > 0, b2);
@@ -663,7 +674,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             pv(1, st, j > 0, b2);
             if (leader) tc_commit(bar(EMPTY + st));
             if (more) {
-              copy_at(2 * j + 4, ks, kp);
+              copy_at(2 * j + 3, ks, kp);
               ok = wait(FULL + ks, kp);
               if (!ok) break;
               qk(0, ks, b2);
@@ -1130,7 +1141,7 @@ cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const
   if (enc == nullptr || !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma)) return cudaErrorInvalidValue;
   const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM);
   // one CTA an SM, as far as the longest sequences that the cache may hold make as many runs
-  const long long longest = kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kBlock;
+  const long long longest = kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kTwo;
   const long long runs_most = a.Hkv * (long long)slots * longest / kShortest;
   const int ctas = (int)(runs_most < 1 ? 1 : (runs_most < device_sm_count() ? runs_most : device_sm_count()));
   ChunkArgs ca{};
