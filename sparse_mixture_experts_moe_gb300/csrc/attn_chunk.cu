@@ -47,11 +47,12 @@ constexpr int kItemReaders = 1 + 8 + 2;
 template <int DP> struct Cfg {
   static constexpr int kChunks = DP / 64;          // 64-element (128-byte) swizzle columns of a row
   static constexpr int kTileBytes = TM * DP * 2;   // a Q tile, and a K or V block
-  static constexpr int kStages = DP == 128 ? 4 : 8;
-  static constexpr int kStage = 32 * 128;  // bytes of a softmax warp's output staging: 32 rows x 64 bf16 elements
+  static constexpr int kStages = DP == 128 ? 5 : 10;
   static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kStage + 8 * kBars + 16 +
-                                  (kItems + 1) * sizeof(Item) + 4 * 32 * 8;
+  static constexpr int kPlan = 4 + kThreads / 32;
+  // tiles and ring, (m, l) of the rows of both tiles, items, the plan, barriers, and the TMEM address beside the abort flag
+  static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + 2 * TM * 8 + (kItems + 1) * sizeof(Item) +
+                                  8 * kPlan + 8 * kBars + 16;
 };
 static_assert(Cfg<128>::kSmem <= kMaxSmem && Cfg<64>::kSmem <= kMaxSmem, "shared memory");
 
@@ -69,6 +70,12 @@ __device__ __forceinline__ uint64_t l2_policy(bool first) {
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(a));
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(b));
   return first ? a : b;
+}
+
+// Eight words to a multiple of 32 bytes.
+__device__ __forceinline__ void store_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
 
 struct ChunkArgs {
@@ -143,22 +150,23 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs pa,
                const __grid_constant__ ChunkArgs ca, int n_items, int q_tma) {
   using C = Cfg<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
-  const uint32_t sOut = sKV + C::kStages * C::kTileBytes;  // [softmax warp][32 rows][64]
-  Item* items = reinterpret_cast<Item*>(gbase + (2 + C::kStages) * C::kTileBytes + 8 * C::kStage);  // [kItems]
-  Item* late_item = items + kItems;  // (of a chunk)
-  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kItems + 1);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // (an address that the compiler does not know: it would keep dozens of sums with it in registers)
+  uint32_t sQ = smem_u32(smem_raw);
+  asm volatile("" : "+r"(sQ));
+  uint8_t* smem = smem_raw + (sQ - smem_u32(smem_raw));
+  const uint32_t sKV = sQ + 2 * C::kTileBytes;
+  float2* given_ml = reinterpret_cast<float2*>(smem + (2 + C::kStages) * C::kTileBytes);  // [tile][row]
+  Item* items = reinterpret_cast<Item*>(given_ml + 2 * TM);                                // [kItems]
+  Item* late_item = items + kItems;
+  long long* plan = reinterpret_cast<long long*>(items + kItems + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(plan + C::kPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 4,
                 ODONE = PFULL + 4, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
                 TAIL = IEMPTY + kItems, GIVEN = TAIL + 1, TAKEN = GIVEN + 4;
-  float2* given_ml = reinterpret_cast<float2*>(gbase + C::kSmem - 1024 - 4 * 32 * 8);  // [warp of tile 1][row]
 
   // (the shuffle tells the compiler that the warp number is the same in all lanes)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -176,7 +184,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     for (int i = 0; i < kItems; ++i) { mbar_init(bar(IFULL + i), 1); mbar_init(bar(IEMPTY + i), kItemReaders); }
     mbar_init(bar(DONE), 1);
     mbar_init(bar(TAIL), 1);
-    for (int i = 0; i < 8; ++i) mbar_init(bar(GIVEN + i), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(GIVEN + i), 2);
     fence_mbar_init();
     *abort_flag = 0;
     if (q_tma) tma_prefetch_desc(&tmQ);
@@ -214,9 +222,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   };
   auto blocks = [](int keys) { return (keys + BK - 1) / BK; };
 
-  // This CTA's run: a scan over the lengths of all tile slots, each thread with some of them in a row. The results stay
-  // in the output staging until the first item is published.
-  long long* plan = reinterpret_cast<long long*>(gbase + (2 + C::kStages) * C::kTileBytes);
+  // This CTA's run: a scan over the lengths of all tile slots, each thread with some of them in a row.
   const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
   // f(slot, length) for the slots of [s0, s1) that a tile fills, as long as it returns true. The sequences lie in the
   // slots' order, so what is read of them is read ahead, four at a time.
@@ -284,7 +290,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   __syncthreads();
 
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kSoftWarps + 1) {
       // -------------------------------------------------------------- K and V (warp 10 finds the items)
       int stage = 0;
@@ -635,63 +641,52 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (nn == 0) continue;
         if (dual) {
           // Both halves' scores are computed two blocks ahead: they take half of the tile's columns each time, so block
-          // j + 1 need not wait for the softmax of block j. Copy i of the item (K0 K1 V0 K2 V1 ..) is in this stage:
-          auto copy_at = [&](int i, int& st, uint32_t& ph) {
-            const int x = stage + i;
-            st = x & (C::kStages - 1);
-            ph = phase ^ ((uint32_t)(x / C::kStages) & 1u);
-          };
-          int st, ks;
-          uint32_t ph, kp;
+          // j + 1 need not wait for the softmax of block j.
           for (int j = 0; j < 2 && j < nn && ok; ++j) {
-            copy_at(j, st, ph);
-            ok = wait(FULL + st, ph);
+            ok = wait(FULL + stage, phase);
             if (ok && j == 0) {
               ok = wait(QFULL, qp0) && wait(QFULL + 1, qp1);
               qp0 ^= 1u;
               qp1 ^= 1u;
             }
             if (!ok) break;
-            qk(0, st, j);
-            qk(1, st, j);
+            qk(0, stage, j);
+            qk(1, stage, j);
             if (leader) {
-              tc_commit(bar(EMPTY + st));
+              tc_commit(bar(EMPTY + stage));
               if (j + 1 == nn) {
                 tc_commit(bar(QEMPTY));
                 tc_commit(bar(QEMPTY + 1));
               }
             }
+            next();
           }
           for (int j = 0; j < nn && ok; ++j) {
             const int b2 = j & 1;
-            const bool more = j + 2 < nn;
-            copy_at(j + 1 < nn ? 2 * j + 2 : 2 * j + 1, st, ph);
-            ok = wait3(FULL + st, ph, FULL + st, ph, PFULL + 2 * b2, b2 ? pp0b : pp0);
+            ok = wait3(FULL + stage, phase, FULL + stage, phase, PFULL + 2 * b2, b2 ? pp0b : pp0);
             if (!ok) break;
-            pv(0, st, j > 0, b2);
+            pv(0, stage, j > 0, b2);
             ok = wait(PFULL + 2 * b2 + 1, b2 ? pp1b : pp1);
             if (!ok) break;
-            pv(1, st, j > 0, b2);
-            if (leader) tc_commit(bar(EMPTY + st));
-            if (more) {
-              copy_at(2 * j + 3, ks, kp);
-              ok = wait(FULL + ks, kp);
-              if (!ok) break;
-              qk(0, ks, b2);
-              qk(1, ks, b2);
-            }
+            pv(1, stage, j > 0, b2);
+            if (leader) tc_commit(bar(EMPTY + stage));
+            next();
             if (b2) { pp0b ^= 1u; pp1b ^= 1u; } else { pp0 ^= 1u; pp1 ^= 1u; }
-            if (leader) {
-              if (more) tc_commit(bar(EMPTY + ks));
-              if (more && j + 3 == nn) {
-                tc_commit(bar(QEMPTY));
-                tc_commit(bar(QEMPTY + 1));
+            if (j + 2 < nn) {
+              ok = wait(FULL + stage, phase);
+              if (!ok) break;
+              qk(0, stage, b2);
+              qk(1, stage, b2);
+              if (leader) {
+                tc_commit(bar(EMPTY + stage));
+                if (j + 3 == nn) {
+                  tc_commit(bar(QEMPTY));
+                  tc_commit(bar(QEMPTY + 1));
+                }
               }
+              next();
             }
           }
-          copy_at(2 * nn, st, ph);
-          stage = st;
-          phase = ph;
           continue;
         }
         ok = wait(FULL + stage, phase);
@@ -731,13 +726,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (ok && j < n1) {
             pp1 ^= 1u;
             pv(1, vs, j > 0);
+            if (leader) tc_commit(bar(EMPTY + vs));  // (before QK: the block that takes its place has 1/4 longer to come)
             if (j + 1 < n1) qk(1, ks);
             if (leader && j + 2 == n1) tc_commit(bar(QEMPTY + 1));
-          }
-          if (leader) {
+          } else if (ok && leader) {
             tc_commit(bar(EMPTY + vs));
-            if (j + 1 < nn) tc_commit(bar(EMPTY + ks));
           }
+          if (leader && j + 1 < nn) tc_commit(bar(EMPTY + ks));
         }
       }
       // every MMA has completed before TMEM and shared memory go away
@@ -746,7 +741,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int t = warp >> 2, r = tid & 127;  // tile, row of it
     const int q4 = warp & 3;                 // TMEM lanes 32 q4 ..
     const float c2 = pa.scale * 1.4426950408889634f;
@@ -892,131 +887,97 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       place();
       if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-        uint32_t again = 0;  // rows whose results are looked at again (replace_unseen)
-        if (dual && t == 1) {
-          // the other half of the keys of tile 0's rows: m, l and the sums to the warp there, 32 elements a step
-          const uint32_t stg = sOut + warp * C::kStage;
-          given_ml[32 * q4 + lane] = make_float2(m, l);
-#pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c, ++given) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tO + 32 * c, o);  // (not this item's where there was no block: not used then)
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = m == -INFINITY ? 0u : o[i];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)),
-                           "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
-                           : "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(GIVEN + q4));
-            ok = ok && warp_wait(bar(TAKEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
-          }
-        } else {
-          // a piece: the sums in fp32; a whole item: the results in bf16. 32 or 64 elements a step through shared memory,
-          // so that a store covers whole rows
-          const bool part = it->split >= 0;
-          const long long at = part ? ((long long)it->split * ca.piece_rows + tile0 + r) * D
-                                    : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
-          uint8_t* orow = part ? reinterpret_cast<uint8_t*>(ca.part_o + at) : (uint8_t*)pa.out + 2 * at;
-          float f1 = 0.f, f0 = 1.f;  // factors of tile 1's sums and of this tile's
-          if (dual) {
-            ok = warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
-            const float2 x = given_ml[32 * q4 + lane];
-            const float top = fmaxf(m, x.x);
-            f0 = m == -INFINITY ? 0.f : ex2((m - top) * c2);
-            f1 = x.x == -INFINITY ? 0.f : ex2((x.x - top) * c2);
-            l = l * f0 + x.y * f1;
-            m = top;
-          }
-          const float f = part ? 1.f : l == 0.f ? 0.f : 1.0f / l;
-          f0 *= f;
-          f1 *= f;
-          const uint32_t stg = sOut + warp * C::kStage;
-          const uint64_t f2 = f2_pack(f0, f0), g2 = f2_pack(f1, f1);
-          uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
-          // A row's 128 bytes (32 sums or 64 results) from shared memory to `to`, of which the first `elems` exist
-          auto store = [&](uint32_t to, int elems, int per) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int u = lane & 7, rr = 4 * i + (lane >> 3);
-              uint8_t* dst = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)orow, rr) + to + 16 * u;
-              uint4 x;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                           : "r"(stg + rr * 128 + ((u ^ (rr & 7)) * 16)) : "memory");
-              if (32 * q4 + rr < nrow_t && per * u < elems) *reinterpret_cast<uint4*>(dst) = x;
-            }
-          };
-#pragma unroll 1  // (run once an item: what is not in the instruction cache costs more than the loop)
-          for (int c = 0; c < DP / 64; ++c) {
-            uint32_t o2[2][32];
-            tmem_ld_32x32b_x32(tO + 64 * c, o2[0]);  // (not this item's where there was no block: lim is 0 then)
-            tmem_ld_32x32b_x32(tO + 64 * c + 32, o2[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              uint32_t(&o)[32] = o2[b];
-              if (dual && c + b > 0)
-                ok = ok && warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                uint64_t v0 = ffma2(((uint64_t)o[4 * i + 1] << 32) | o[4 * i], f2, 0ull);
-                uint64_t v1 = ffma2(((uint64_t)o[4 * i + 3] << 32) | o[4 * i + 2], f2, 0ull);
-                if (dual) {
-                  uint64_t x0, x1;
-                  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x0), "=l"(x1)
-                               : "r"(stg + 4 * C::kStage + lane * 128 + ((i ^ (lane & 7)) * 16)) : "memory");
-                  v0 = ffma2(x0, g2, v0);
-                  v1 = ffma2(x1, g2, v1);
-                }
-                if (lim == 0) v0 = v1 = 0ull;
-                odd = ffma2(v0, 0ull, odd);
-                odd = ffma2(v1, 0ull, odd);
-                o[4 * i] = (uint32_t)v0;
-                o[4 * i + 1] = (uint32_t)(v0 >> 32);
-                o[4 * i + 2] = (uint32_t)v1;
-                o[4 * i + 3] = (uint32_t)(v1 >> 32);
-              }
-              if (dual) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(TAKEN + q4));
-                ++given;
-              }
-              if (part) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                               ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) * 16)), "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
-                               : "memory");
-                __syncwarp();
-                store((2 * c + b) * 128, D - 64 * c - 32 * b, 4);
-                __syncwarp();
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                               ::"r"(stg + lane * 128 + (((4 * b + i) ^ (lane & 7)) * 16)),
-                               "r"(pack_bf16x2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]))),
-                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]))),
-                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]))),
-                               "r"(pack_bf16x2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])))
-                               : "memory");
-              }
-            }
-            if (!part) {
-              __syncwarp();
-              store(c * 128, D - 64 * c, 8);
-              __syncwarp();
-            }
-          }
-          if (valid && part) ca.part_ml[(long long)it->split * ca.piece_rows + tile0 + r] = make_float2(m * c2, l);
-          if (valid && !part && pa.lse != nullptr)
-            pa.lse[(long long)(it->q0 + tok) * H + h] =
-                lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
-          // (a row whose weights' sum is not finite sees a score that is not, and is NaN as a whole)
-          again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
+        const bool part = it->split >= 0;  // a piece: the sums in fp32; a whole item: the results in bf16
+        float f0 = 1.f, f1 = 0.f;          // factors of a tile's sums; of tile 0's and tile 1's
+        if (dual) {
+          // The tiles are the halves of the keys: each of the two warps that share TMEM lanes adds up half of the columns.
+          given_ml[tid] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(GIVEN + q4));
+          ok = warp_wait(bar(GIVEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+          tc_fence_after();
+          const float2 a = given_ml[r], b = given_ml[TM + r];
+          m = fmaxf(a.x, b.x);
+          f0 = a.x == -INFINITY ? 0.f : ex2((a.x - m) * c2);
+          f1 = b.x == -INFINITY ? 0.f : ex2((b.x - m) * c2);
+          l = a.y * f0 + b.y * f1;
         }
+        const float f = part ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+        const uint64_t f0p = f2_pack(f0 * f, f0 * f), f1p = f2_pack(f1 * f, f1 * f);
+        const long long at = part ? ((long long)it->split * ca.piece_rows + tile0 + r) * D
+                                  : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
+        uint8_t* orow = part ? reinterpret_cast<uint8_t*>(ca.part_o + at) : (uint8_t*)pa.out + 2 * at;
+        // 32 bytes a store: whole sectors, though each lane stores to a row of its own
+        const bool wide = part || (((uint32_t)(uintptr_t)pa.out | (uint32_t)pa.os * 2 | (uint32_t)D * 2) & 31) == 0;
+        uint64_t odd = 0ull;  // (times 0 and added up, only a value that is not finite leaves something else than 0)
+        // 32 columns from `col` on
+        auto emit = [&](uint32_t(&o)[32], int col) {
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (valid && col + 8 * i < D) store_32(orow + 4 * (col + 8 * i), o + 8 * i);
+            return;
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          if (wide) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (valid && col + 16 * i < D) store_32(orow + 2 * (col + 16 * i), p + 8 * i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (valid && col + 8 * i < D)
+                *reinterpret_cast<uint4*>(orow + 2 * (col + 8 * i)) =
+                    make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+          }
+        };
+        // (64 columns of a tile or 32 of two a step; what is not in the instruction cache costs more than the loop)
+        const uint32_t tA = tmem + lanes + 256 + (dual ? 0 : t * DP), tB = dual ? tA + DP : tA + 32;
+        const int step = dual ? 32 : 64, col1 = dual ? (t + 1) * (DP / 2) : DP;
+#pragma unroll 1
+        for (int col = dual ? t * (DP / 2) : 0; col < col1; col += step) {
+          uint32_t o[32], x[32];
+          tmem_ld_32x32b_x32(tA + col, o);  // (not this item's where there was no block: lim is 0 then)
+          tmem_ld_32x32b_x32(tB + col, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint64_t v = ffma2(((uint64_t)o[2 * i + 1] << 32) | o[2 * i], f0p, 0ull);
+            uint64_t w = ((uint64_t)x[2 * i + 1] << 32) | x[2 * i];
+            if (dual) {
+              v = ffma2(w, f1p, v);
+            } else {
+              w = ffma2(w, f0p, 0ull);
+            }
+            if (lim == 0) v = w = 0ull;
+            odd = ffma2(v, 0ull, odd);
+            if (!dual) odd = ffma2(w, 0ull, odd);
+            o[2 * i] = (uint32_t)v;
+            o[2 * i + 1] = (uint32_t)(v >> 32);
+            x[2 * i] = (uint32_t)w;
+            x[2 * i + 1] = (uint32_t)(w >> 32);
+          }
+          emit(o, col);
+          if (!dual) emit(x, col + 32);
+        }
+        if (dual) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(TAKEN + q4));
+          ok = ok && warp_wait(bar(TAKEN + q4), given & 1, timeout_ns, abort_flag, status, 56);
+          ++given;
+        }
+        const bool first = !dual || t == 0;
+        if (valid && first && part) ca.part_ml[(long long)it->split * ca.piece_rows + tile0 + r] = make_float2(m * c2, l);
+        if (valid && first && !part && pa.lse != nullptr)
+          pa.lse[(long long)(it->q0 + tok) * H + h] =
+              lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
+        // Rows whose results are looked at again. (One whose weights' sum is not finite sees a score that is not, and is NaN
+        // as a whole.)
+        uint32_t again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
         if (again != 0) {
           Unseen unseen(min(n * BK, it->nk - it->key0));
           while (again != 0) {
@@ -1041,8 +1002,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D + lane * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (cols >> e & 1u) {
-                if (it->split >= 0) po[e] = o[e];
+              if ((cols >> e & 1u) && (!dual || lane / (DP / 16) == t)) {  // (its own columns)
+                if (part) po[e] = o[e];
                 else dw[e] = __float2bfloat16_rn(o[e] * (lw == 0.f ? 0.f : 1.0f / lw));
               }
           }
