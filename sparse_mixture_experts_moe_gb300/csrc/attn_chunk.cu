@@ -87,14 +87,15 @@ struct ChunkArgs {
 };
 
 // How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head; the items lie in a
-// row (heads outside, tile slots inside), each as long as its cost: kBlock a block of keys, and kItem for Q, the first
-// scores and the results (an item's fixed part took as long as four blocks). The row is cut into equally long runs, one
-// a CTA, whatever items the cuts fall into; runs are not shorter than kShortest.
+// row (heads outside, tile slots inside), each as long as its cost: kOne a block of keys of an item of one tile, kTwo one
+// of two tiles, and kItem for Q, the first scores and the results: measured 1.06, 1.45 and 6 us among mixed items
+// (eight batches of chunks and single tokens, geometric mean: 471 us so, 484 with one length for all blocks). The row is
+// cut into equally long runs, one a CTA, whatever items the cuts fall into; runs are not shorter than kShortest.
 // A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
 // several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order, so
 // that results do not depend on which CTA is done first. A run has at most two such items, its first and its last: 2
 // pieces a CTA are enough however long the keys.
-constexpr int kOne = 4, kTwo = 4, kItem = 16, kShortest = 16;
+constexpr int kOne = 5, kTwo = 7, kItem = 28, kShortest = 16;
 
 // Length of a block of an item with so many rows, and of an item with so many blocks.
 __device__ __forceinline__ int block_length(int rows) { return rows <= TM ? kOne : kTwo; }
@@ -1021,56 +1022,88 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   }
 }
 
-// The rows that several runs share, by the run that such an item begins in (blockIdx.x): a warp a row, its pieces in
-// their order, eight on their way at a time.
-__global__ void __launch_bounds__(256)
-chunk_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ ChunkArgs ca) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), c0 = blockIdx.x;
-  const ChunkRun run = ca.runs[c0];
-  if (r >= run.nrows) return;
-  const int G = a.H / a.Hkv, R = run.row0 + r, tok = run.q0 + R / G, h = run.hk * G + R % G, n = run.end - c0 + 1;
+// Rows r0 .. r0 + ROWS - 1 of a shared item by a warp: n pieces each, in order, NP of them on their way at a time. Its
+// lanes lie in ROWS parts, one a row, to weight the pieces.
+template <int ROWS, int NP>
+__device__ __forceinline__ void join_rows(const PromptArgs& a, const ChunkArgs& ca, const ChunkRun& run, int c0, int n,
+                                          int r0) {
+  constexpr int P = 32 / ROWS;
+  const int lane = threadIdx.x & 31, k = lane / P, y0 = lane % P, rows = min(ROWS, run.nrows - r0);
   // run c0 has its last item's piece, the others their first's
-  auto row = [&](int i) { return (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * ca.piece_rows + r; };
+  auto at = [&](int i, int r) { return (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * ca.piece_rows + r0 + r; };
+  auto ml = [&](int i) { return i < n && k < rows ? ca.part_ml[at(i, k)] : make_float2(-INFINITY, 0.f); };
   float M = -INFINITY, l = 0.f;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, ca.part_ml[row(i)].x);
+  for (int i = y0; i < n; i += P) M = fmaxf(M, ml(i).x);
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  for (int w = P / 2; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
   const float ref = M == -INFINITY ? 0.f : M;
   const bool on = lane * 4 < a.D;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const float2 v = i0 + lane < n ? ca.part_ml[row(i0 + lane)] : make_float2(-INFINITY, 0.f);
+  float4 o[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += P) {
+    const float2 v = ml(i0 + y0);
     const float wl = ex2(v.x - ref);
     l += wl * v.y;
-    for (int y0 = 0; y0 < 32 && i0 + y0 < n; y0 += 8) {
-      float4 u[8];
+    for (int y = 0; y < P && i0 + y < n; y += NP) {
+      float4 u[NP][ROWS];
 #pragma unroll
-      for (int y = 0; y < 8; ++y)
-        u[y] = on && i0 + y0 + y < n ? reinterpret_cast<const float4*>(ca.part_o + row(i0 + y0 + y) * a.D)[lane]
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int b = 0; b < NP; ++b)
 #pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const float w = __shfl_sync(0xffffffffu, wl, y0 + y);
-        o.x = fmaf(w, u[y].x, o.x);
-        o.y = fmaf(w, u[y].y, o.y);
-        o.z = fmaf(w, u[y].z, o.z);
-        o.w = fmaf(w, u[y].w, o.w);
-      }
+        for (int r = 0; r < ROWS; ++r)
+          u[b][r] = on && r < rows && i0 + y + b < n
+                        ? reinterpret_cast<const float4*>(ca.part_o + at(i0 + y + b, r) * a.D)[lane]
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int b = 0; b < NP; ++b)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const float w = __shfl_sync(0xffffffffu, wl, P * r + y + b);
+          o[r].x = fmaf(w, u[b][r].x, o[r].x);
+          o[r].y = fmaf(w, u[b][r].y, o[r].y);
+          o[r].z = fmaf(w, u[b][r].z, o[r].z);
+          o[r].w = fmaf(w, u[b][r].w, o[r].w);
+        }
     }
   }
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  for (int w = P / 2; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  if (on) {
+  const int G = a.H / a.Hkv, R0 = run.row0 + r0;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const float f = __shfl_sync(0xffffffffu, inv, P * r);
+    if (r >= rows || !on) continue;
+    const int tok = run.q0 + (R0 + r) / G, h = run.hk * G + (R0 + r) % G;
     uint2 u;
-    u.x = pack_bf16x2(o.x * inv, o.y * inv);
-    u.y = pack_bf16x2(o.z * inv, o.w * inv);
+    u.x = pack_bf16x2(o[r].x * f, o[r].y * f);
+    u.y = pack_bf16x2(o[r].z * f, o[r].w * f);
     *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + (long long)tok * a.os + (long long)h * a.D + lane * 4) = u;
   }
-  if (a.lse != nullptr && lane == 0)
+  if (a.lse != nullptr && y0 == 0 && k < rows) {
+    const int tok = run.q0 + (R0 + k) / G, h = run.hk * G + (R0 + k) % G;
     a.lse[(long long)tok * a.H + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// The rows that several runs share, by the run that such an item begins in (blockIdx.x), 32 a CTA. Two or three pieces,
+// as most have: a warp takes four rows, whose loads go out together (a warp a row: 130 us a call of 4 sequences' 2048
+// tokens behind 8192, 122 so). Many, of a long sequence's few rows: a warp a row (one token behind 4096, 8 rows a head:
+// 20 us a call, 29 with four rows a warp).
+constexpr int kJoinRows = 32;
+
+__global__ void __launch_bounds__(256, 4)
+chunk_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ ChunkArgs ca) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, first = blockIdx.y * kJoinRows;
+  const ChunkRun run = ca.runs[c0];
+  const int n = run.end - c0 + 1, end = min(run.nrows, first + kJoinRows);
+  if (n <= 4) {
+    if (first + 4 * warp < end) join_rows<4, 2>(a, ca, run, c0, n, first + 4 * warp);
+  } else {
+    for (int r = first + warp; r < end; r += 8) join_rows<1, 8>(a, ca, run, c0, n, r);
+  }
 }
 
 template <int DP>
@@ -1114,8 +1147,8 @@ cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const
   const cudaError_t e = a.D <= 64 ? launch<64>(tq, m, a, ca, ctas, slots, q_tma, s)
                                   : launch<128>(tq, m, a, ca, ctas, slots, q_tma, s);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((ca.piece_rows + 7) / 8)), dim3(256), 0, s, a,
-                    ca);
+  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((ca.piece_rows + kJoinRows - 1) / kJoinRows)),
+                    dim3(256), 0, s, a, ca);
 }
 
 }  // namespace moe
