@@ -131,11 +131,10 @@ int attn_shared_splits(const DecodeArgs& a);
 cudaError_t launch_attn_shared_tc(const DecodeArgs& a, const CacheMaps& m, int splits, float* part_o, float2* part_ml,
                                   cudaStream_t s);
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
-// A chunk of new tokens over the cache: queries and offsets of a, the cache, slots and layer of d. bf16, D <= 128: runs,
-// one an SM, and part, 2 pieces an SM of chunk_piece_rows rows of D + 2 floats.
-int chunk_piece_rows(int Tq, int G);
-cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, ChunkRun* runs, float* part,
-                                 cudaStream_t s);
+// A chunk of new tokens over the cache: queries and offsets of a, the cache, slots and layer of d. bf16, D <= 128: scratch
+// of chunk_tc_bytes.
+size_t chunk_tc_bytes(int Tq, int G, int D);
+cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, void* scratch, cudaStream_t s);
 // The other types and heads: rows in `pieces` parts, d.part [Tq H][pieces][D + 2].
 int chunk_tile_pieces(const CacheView& c, int n, int Tq, int H);
 cudaError_t launch_attn_chunk_tiles(const PromptArgs& a, const DecodeArgs& d, int pieces, cudaStream_t s);

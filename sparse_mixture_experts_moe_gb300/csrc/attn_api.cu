@@ -124,10 +124,9 @@ struct ChunkScratch {
   size_t bytes;
   int pieces;
 };
-size_t chunk_runs_bytes() { return align256(sizeof(ChunkRun) * (size_t)device_sm_count()); }
 ChunkScratch chunk_scratch(const CacheView& c, int n, int Tq, int H) {
   if (c.dt == MOE_DTYPE_BF16 && c.D <= 128)
-    return {chunk_runs_bytes() + align256((size_t)2 * device_sm_count() * chunk_piece_rows(Tq, H / c.Hkv) * (c.D + 2) * 4), 0};
+    return {align256(chunk_tc_bytes(Tq, H / c.Hkv, c.D)), 0};
   const int pieces = chunk_tile_pieces(c, n, Tq, H);
   return {pieces > 1 ? align256((size_t)Tq * H * pieces * (c.D + 2) * 4) : 0, pieces};
 }
@@ -328,9 +327,7 @@ moe_status moe_attention_chunk_ex(const moe_kv_cache* cache, int layer, const vo
   if (!planned(cache)) return cuda_status(launch_attn_chunk_tiles(a, d, need.pieces, (cudaStream_t)stream));
   bind_primary_context();
   if (cache->plan == nullptr && !encode_cache_maps(c, &p.maps)) return MOE_ERR_CUDA;
-  ChunkRun* runs = reinterpret_cast<ChunkRun*>(room.at);
-  float* part = room.at + chunk_runs_bytes() / 4;
-  return cuda_status(launch_attn_chunk_tc(a, d, p.maps, runs, part, (cudaStream_t)stream));
+  return cuda_status(launch_attn_chunk_tc(a, d, p.maps, room.at, (cudaStream_t)stream));
 }
 
 size_t moe_cache_plan_bytes(void) { return sizeof(CachePlan); }

@@ -39,17 +39,24 @@ struct __align__(16) Item {
   int last;                 // no item: the end
   int seq;                  // (for errors)
   int dual;                 // one tile of rows: both softmax groups take it, with half of each block's keys
-  int split;                // the piece that takes the results (-1: the output)
+  int piece;                // the first row of the piece that takes the results (-1: the output)
 };
 constexpr int kItems = 3;   // items published: one worked on, one ahead, one being given back
 constexpr int kItemReaders = 1 + 8 + 2;
+
+// What a CTA has of a kind: the length of all items of a head, its run's number, beginning and end, and the slot, place
+// and head of the item that the run begins in.
+struct Plan {
+  long long all, begin, end, x;
+  int run, slot, head, unused;
+};
 
 template <int DP> struct Cfg {
   static constexpr int kChunks = DP / 64;          // 64-element (128-byte) swizzle columns of a row
   static constexpr int kTileBytes = TM * DP * 2;   // a Q tile, and a K or V block
   static constexpr int kStages = DP == 128 ? 5 : 10;
   static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
-  static constexpr int kPlan = 4 + kThreads / 32;
+  static constexpr int kPlan = 2 * (sizeof(Plan) / 8 + kThreads / 32);
   // tiles and ring, (m, l) of the rows of both tiles, items, the plan, barriers, and the TMEM address beside the abort flag
   static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + 2 * TM * 8 + (kItems + 1) * sizeof(Item) +
                                   8 * kPlan + 8 * kBars + 16;
@@ -80,33 +87,39 @@ __device__ __forceinline__ void store_32(void* p, const uint32_t* v) {
 
 struct ChunkArgs {
   DecodeArgs d;
-  ChunkRun* runs;  // [CTA] the item that begins in each run and goes on in the next ones
-  int piece_rows;  // rows of a piece
-  float* part_o;   // [piece][piece_rows][D]
+  ChunkRun* runs;  // [kind][run] the item that begins in each run and goes on in the next ones
+  int rows[2];     // rows of a piece, by kind
+  int ctas;
+  float* part_o;   // [kind][2 runs][rows][D]
   float2* part_ml;
+  // The pieces' rows before run c's: of its first item, which began in another run, or of its last.
+  __device__ __forceinline__ int piece(int kind, int c, bool last) const {
+    return (kind ? 2 * ctas * rows[0] : 0) + (2 * c + (last ? 1 : 0)) * rows[kind];
+  }
 };
 
-// How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head; the items lie in a
-// row (heads outside, tile slots inside), each as long as its cost: kOne a block of keys of an item of one tile, kTwo one
-// of two tiles, and kItem for Q, the first scores and the results: measured 1.06, 1.45 and 6 us among mixed items
-// (eight batches of chunks and single tokens, geometric mean: 471 us so, 484 with one length for all blocks). The row is
-// cut into equally long runs, one a CTA, whatever items the cuts fall into; runs are not shorter than kShortest.
+// How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head. There are two kinds:
+// those of two tiles (0) and those of one (1). The items of a kind lie in a row (heads outside, tile slots inside), each
+// as long as its cost: kBlock a block of keys, and kItem for Q, the first scores and the results (measured, us: 1.45 a
+// block and 6 of two tiles, 1.06 and 5.5 of one). The row is cut into equally long runs, one a CTA, whatever items the
+// cuts fall into; runs are not shorter than kShortest. So each CTA has a run of either kind, if there are enough: the
+// tensor cores bound the one and the memory the other, and CTAs that hold more of one kind than others would end at
+// another time than these (with one row for both kinds, whose costs depend on what else is running: 800 us for 8 chunks
+// and 56 single tokens, 695 so). Half of the CTAs begin with one kind and half with the other.
 // A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
 // several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order, so
 // that results do not depend on which CTA is done first. A run has at most two such items, its first and its last: 2
-// pieces a CTA are enough however long the keys.
-constexpr int kOne = 5, kTwo = 7, kItem = 28, kShortest = 16;
+// pieces a run are enough however long the keys.
+constexpr int kBlock = 4, kItem = 16, kShortest = 16, kBoth = 1200;
 
-// Length of a block of an item with so many rows, and of an item with so many blocks.
-__device__ __forceinline__ int block_length(int rows) { return rows <= TM ? kOne : kTwo; }
-__device__ __forceinline__ long long item_length(int rows, int blocks) {
-  return kItem + (long long)blocks * block_length(rows);
-}
+__device__ __forceinline__ int item_kind(int rows) { return rows <= TM ? 1 : 0; }
+// Length of an item of so many blocks.
+__device__ __forceinline__ long long item_length(int blocks) { return kItem + (long long)blocks * kBlock; }
 
 struct ChunkItem {
   int seq, row0, nrows, q0, nq, nk, slot;
   int lim0, lim1, n_blocks;
-  __device__ __forceinline__ long long length() const { return nrows > 0 ? item_length(nrows, n_blocks) : 0; }
+  __device__ __forceinline__ long long length() const { return nrows > 0 ? item_length(n_blocks) : 0; }
 };
 // What fills tile slot s (nrows = 0: nothing).
 __device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const ChunkArgs& ca, int s, int i) {
@@ -115,17 +128,12 @@ __device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const Chun
   it.seq = i;
   const int q0 = pa.qo[i], q1 = pa.qo[i + 1];
   it.slot = ca.d.slots[i];
-  if (q0 < 0 || q1 < q0 || q1 > pa.Tq) {
-    record_error(pa.status, MOE_ERR_DEVICE_CHECK, i);
-    return it;
-  }
+  if (q0 < 0 || q1 < q0 || q1 > pa.Tq) return it;
   it.q0 = q0;
   it.nq = q1 - q0;
   const long long r0 = ((long long)s - ((long long)q0 * G / (2 * TM) + i)) * (2 * TM);
   if (r0 < 0 || r0 >= (long long)it.nq * G) return it;
   it.nk = slot_len(ca.d.c, it.slot);
-  if (it.nk == 0 && (it.slot < 0 || it.slot >= ca.d.c.n_slots || ca.d.c.lens[it.slot] != 0))
-    record_error(pa.status, MOE_ERR_DEVICE_CHECK, i);
   it.row0 = (int)r0;
   it.nrows = min(2 * TM, it.nq * G - it.row0);
   it.lim0 = visible_keys((it.row0 + min(it.nrows, TM) - 1) / G, it.nq, it.nk, pa.causal);
@@ -133,17 +141,29 @@ __device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const Chun
   it.n_blocks = (max(it.lim0, it.lim1) + BK - 1) / BK;
   return it;
 }
-// The runs: how many, their beginnings, and the run that place x lies in.
+// The runs of a kind: how many, their beginnings, and the run that place x lies in. t0, t1: the lengths of the two rows.
 struct Runs {
   long long all;
   int n;
-  __device__ __forceinline__ Runs(long long total, int ctas) : all(total) {
-    const long long most = total / kShortest;
-    n = (int)(most < 1 ? 1 : (most < ctas ? most : ctas));
+  __device__ __forceinline__ Runs(int kind, long long t0, long long t1, int ctas) : all(kind ? t1 : t0) {
+    long long most = ctas;
+    if (t0 > 0 && t1 > 0 && ctas > 1 && 4 * t0 + 3 * t1 < 4LL * kBoth * ctas) {  // (a block of one tile takes 3/4 as long)
+      const long long ones = min(ctas - 1LL, max(1LL, ctas * (3 * t1) / (4 * t0 + 3 * t1)));
+      most = kind ? ones : ctas - ones;
+    }
+    most = min(most, all / kShortest);
+    n = most < 1 ? 1 : (int)most;
   }
   __device__ __forceinline__ long long begin(int c) const { return all * c / n; }
   __device__ __forceinline__ int of(long long x) const { return (int)(((x + 1) * n - 1) / all); }
 };
+// Which run of a kind a CTA takes: those of kind 1 go on where those of kind 0 end, so that a short call's lie in CTAs of
+// their own.
+__device__ __forceinline__ int run_of(int kind, const Runs& runs0) {
+  if (kind == 0) return blockIdx.x;
+  const int c = (int)blockIdx.x - (runs0.all > 0 ? runs0.n % (int)gridDim.x : 0);
+  return c < 0 ? c + gridDim.x : c;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -160,8 +180,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   float2* given_ml = reinterpret_cast<float2*>(smem + (2 + C::kStages) * C::kTileBytes);  // [tile][row]
   Item* items = reinterpret_cast<Item*>(given_ml + 2 * TM);                                // [kItems]
   Item* late_item = items + kItems;
-  long long* plan = reinterpret_cast<long long*>(items + kItems + 1);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(plan + C::kPlan);
+  Plan* plan = reinterpret_cast<Plan*>(items + kItems + 1);     // [kind]
+  long long* warp_sums = reinterpret_cast<long long*>(plan + 2);  // [kind][warp]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(warp_sums + 2 * (kThreads / 32));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -223,75 +244,103 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   };
   auto blocks = [](int keys) { return (keys + BK - 1) / BK; };
 
-  // This CTA's run: a scan over the lengths of all tile slots, each thread with some of them in a row.
-  const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
-  // f(slot, length) for the slots of [s0, s1) that a tile fills, as long as it returns true. The sequences lie in the
-  // slots' order, so what is read of them is read ahead, four at a time.
-  auto walk = [&](auto f) {
-    int s = s0, i = find_tile_seq(pa.qo, pa.n, G, 2 * TM, s0);
-    while (s < s1 && i < pa.n) {
-      int q[5], len[4];
+  // This CTA's runs: a scan over the lengths of all tile slots, each thread with some of them in a row.
+  {
+    const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
+    // f(slot, kind, length) for the slots of [s0, s1) that a tile fills, as long as it returns true. The sequences lie in
+    // the slots' order, so what is read of them is read ahead, four at a time.
+    auto walk = [&](auto f) {
+      int s = s0, i = find_tile_seq(pa.qo, pa.n, G, 2 * TM, s0);
+      while (s < s1 && i < pa.n) {
+        int q[5], len[4];
 #pragma unroll
-      for (int k = 0; k < 5; ++k) q[k] = pa.qo[min(i + k, pa.n)];
+        for (int k = 0; k < 5; ++k) q[k] = pa.qo[min(i + k, pa.n)];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) len[k] = slot_len(ca.d.c, ca.d.slots[min(i + k, pa.n - 1)]);
+        for (int k = 0; k < 4; ++k) len[k] = slot_len(ca.d.c, ca.d.slots[min(i + k, pa.n - 1)]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (i + k >= pa.n || q[k] < 0 || q[k + 1] < q[k] || q[k + 1] > pa.Tq) continue;
-        const long long first = (long long)q[k] * G / (2 * TM) + i + k, rows = (long long)(q[k + 1] - q[k]) * G;
-        const long long end = min((long long)s1, first + (rows + 2 * TM - 1) / (2 * TM));
-        for (s = max(s, (int)min(first, (long long)s1)); s < end; ++s) {
-          const int row0 = (int)(s - first) * 2 * TM, nrows = min(2 * TM, (int)rows - row0), nq = q[k + 1] - q[k];
-          const int lim0 = visible_keys((row0 + min(nrows, TM) - 1) / G, nq, len[k], pa.causal);
-          const int lim1 = nrows > TM ? visible_keys((row0 + nrows - 1) / G, nq, len[k], pa.causal) : 0;
-          if (!f(s, item_length(nrows, blocks(max(lim0, lim1))))) return;
+        for (int k = 0; k < 4; ++k) {
+          if (i + k >= pa.n || q[k] < 0 || q[k + 1] < q[k] || q[k + 1] > pa.Tq) continue;
+          const long long first = (long long)q[k] * G / (2 * TM) + i + k, rows = (long long)(q[k + 1] - q[k]) * G;
+          const long long end = min((long long)s1, first + (rows + 2 * TM - 1) / (2 * TM));
+          for (s = max(s, (int)min(first, (long long)s1)); s < end; ++s) {
+            const int row0 = (int)(s - first) * 2 * TM, nrows = min(2 * TM, (int)rows - row0), nq = q[k + 1] - q[k];
+            const int lim0 = visible_keys((row0 + min(nrows, TM) - 1) / G, nq, len[k], pa.causal);
+            const int lim1 = nrows > TM ? visible_keys((row0 + nrows - 1) / G, nq, len[k], pa.causal) : 0;
+            if (!f(s, item_kind(nrows), item_length(blocks(max(lim0, lim1))))) return;
+          }
+        }
+        i += 4;
+      }
+    };
+    long long sum[2] = {0, 0}, upto[2];
+    if (s0 < s1) walk([&](int, int kind, long long len) { sum[0] += kind ? 0 : len; sum[1] += kind ? len : 0; return true; });
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      upto[kind] = sum[kind];
+#pragma unroll
+      for (int w = 1; w < 32; w <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto[kind], w);
+        if (lane >= w) upto[kind] += x;
+      }
+      if (lane == 31) warp_sums[kind * (kThreads / 32) + warp] = upto[kind];
+    }
+    __syncthreads();
+    long long total[2] = {0, 0};
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) upto[kind] += total[kind];
+        total[kind] += warp_sums[kind * (kThreads / 32) + w];
+      }
+    const Runs runs0(0, total[0] * Hkv, total[1] * Hkv, gridDim.x);
+    long long at[2], x[2];  // the run's beginning in its head; the item's after the ones looked through
+    bool here[2];           // it lies in one of this thread's slots
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const long long all = total[kind];
+      const int c = run_of(kind, runs0);
+      long long begin = 0, end = 0;
+      here[kind] = false;
+      if (all > 0) {
+        const Runs runs(kind, total[0] * Hkv, total[1] * Hkv, gridDim.x);
+        if (c < runs.n) {
+          begin = runs.begin(c);
+          end = runs.begin(c + 1);
+          const int head = (int)(begin / all);
+          at[kind] = begin - head * all;
+          x[kind] = upto[kind] - sum[kind];
+          here[kind] = at[kind] >= x[kind] && at[kind] < upto[kind];
+          if (here[kind]) plan[kind].head = head;
         }
       }
-      i += 4;
-    }
-  };
-  long long sum = 0;
-  if (s0 < s1) walk([&](int, long long len) { sum += len; return true; });
-  long long upto = sum;
-#pragma unroll
-  for (int w = 1; w < 32; w <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, w);
-    if (lane >= w) upto += x;
-  }
-  if (lane == 31) plan[4 + warp] = upto;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) upto += total;
-    total += plan[4 + w];
-  }
-  if (total > 0) {
-    const Runs runs(total * pa.Hkv, gridDim.x);
-    if ((int)blockIdx.x < runs.n) {
-      const long long begin = runs.begin(blockIdx.x), at = begin % total;
-      if (at >= upto - sum && at < upto) {  // one thread
-        long long x = upto - sum;
-        walk([&](int s, long long len) {
-          plan[1] = s;
-          plan[2] = begin - at + x;  // where item (head, slot s) begins
-          x += len;
-          return x <= at;
-        });
-        plan[3] = begin / total;  // the head
+      if (tid == 0) {
+        plan[kind].all = all;
+        plan[kind].run = c;
+        plan[kind].begin = begin;
+        plan[kind].end = end;
+        ChunkRun none;
+        none.nrows = 0;
+        ca.runs[kind * gridDim.x + c] = none;
       }
     }
+    if (here[0] || here[1])
+      walk([&](int s, int k, long long len) {
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind)
+          if (k == kind && here[kind]) {
+            plan[kind].slot = s;
+            plan[kind].x = x[kind] - at[kind];  // where item (head, slot s) begins, from the run's beginning on
+            x[kind] += len;
+            here[kind] = x[kind] <= at[kind];
+          }
+        return here[0] || here[1];
+      });
+    __syncthreads();
   }
-  if (tid == 0) {
-    plan[0] = total;
-    ChunkRun none;
-    none.nrows = 0;
-    ca.runs[blockIdx.x] = none;
-  }
-  __syncthreads();
 
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kSoftWarps + 1) {
       // -------------------------------------------------------------- K and V (warp 10 finds the items)
       int stage = 0;
@@ -412,22 +461,22 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       constexpr int kLanes = DP / 8, kRowsPer = 32 / kLanes;
       const int t = warp - kSoftWarps - 2;
       uint32_t loads = 0;
-      // The first of these warps walks the CTA's run and publishes its items, one ahead of the Q tiles it loads. It
+      // The first of these warps walks the CTA's runs and publishes their items, one ahead of the Q tiles it loads. It
       // looks at 32 tile slots at once, one a lane (the next of an item after the other cost 9 us an item).
       const bool finder = t == 0;
-      const Runs runs(finder ? plan[0] * Hkv : 0, gridDim.x);
-      const long long run_begin = finder && (int)blockIdx.x < runs.n ? runs.begin(blockIdx.x) : 0;
-      const long long run_end = finder && (int)blockIdx.x < runs.n ? runs.begin(blockIdx.x + 1) : 0;
+      int kind = 0;  // of the run at hand
       ChunkItem ci{};
-      int base = finder ? (int)plan[1] & ~31 : 0, head = finder ? (int)plan[3] : 0, loaded = -1;
-      // the place of the 32 slots from `base` on in this head, of the lane's item among them, the length of all
+      int base = 0, head = 0, loaded = -1;
+      // the place of the 32 slots from `base` on in this head (from the run's beginning on), of the lane's item among them,
+      // the length of all
       long long x = 0, before = 0, length = 0;
       int b0 = 0, b1 = 0;
       uint32_t todo = 0;  // the lanes whose items have blocks in the run and are not published yet
-      bool late = false;
+      bool late = false, ended = true;
       auto load_slots = [&]() {
         const int s = base + lane;
         ci = s < n_items ? chunk_item(pa, ca, s, find_tile_seq(pa.qo, pa.n, G, 2 * TM, s)) : ChunkItem{};
+        if (item_kind(ci.nrows) != kind) ci.nrows = 0;
         loaded = base;
         const long long len = ci.length();
         before = len;
@@ -453,51 +502,66 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         it.lim1 = max(0, min(ci.lim1 - it.key0, it.n_keys));
         it.dual = ci.nrows <= TM;
         if (it.dual) it.lim1 = it.lim0;
-        it.split = b0 == 0 && b1 == all ? -1 : 2 * (int)blockIdx.x + (b0 == 0 ? 1 : 0);
+        it.piece = b0 == 0 && b1 == all ? -1 : ca.piece(kind, plan[kind].run, b0 == 0);
         if (b0 == 0 && b1 < all) {
           ChunkRun r;
           r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
-          r.end = runs.of(x + before + (long long)(all - 1) * block_length(ci.nrows));
-          ca.runs[blockIdx.x] = r;
+          r.end = Runs(kind, plan[0].all * Hkv, plan[1].all * Hkv, gridDim.x).of(
+              plan[kind].begin + x + before + (long long)(all - 1) * kBlock);
+          ca.runs[kind * gridDim.x + plan[kind].run] = r;
         }
         return it;
       };
-      // The blocks of the slots' items that lie in the run: block j begins at x + before + j times a block's length.
+      // The blocks of the slots' items that lie in the run: block j begins at x + before + j kBlock.
       auto look = [&]() {
-        if (loaded != base) load_slots();
-        const int all = max(1, ci.n_blocks), len = block_length(ci.nrows);
+        if (loaded != base) {
+          const bool begins = loaded < 0;
+          load_slots();
+          if (begins) x -= __shfl_sync(0xffffffffu, before, plan[kind].slot & 31);
+        }
+        const int all = max(1, ci.n_blocks);
         auto first_from = [&](long long p) {
           p -= x + before;
-          return p <= 0 ? 0 : (int)min((long long)all, (p + len - 1) / len);
+          return p <= 0 ? 0 : (int)min((long long)all, (p + kBlock - 1) / kBlock);
         };
-        b0 = first_from(run_begin);
-        b1 = first_from(run_end);
+        b0 = first_from(0);
+        b1 = first_from(plan[kind].end - plan[kind].begin);
         const bool in = ci.nrows > 0 && b0 < b1;
         // The end of an item that began in another run comes last: the whole items of all runs then begin with their
         // first keys at about the same time, and L2 serves those that share a head.
-        const bool is_late = in && x + before < run_begin;
+        const bool is_late = in && x + before < 0;
         if (is_late) *late_item = my_item();
         __syncwarp();
         late = late || __any_sync(0xffffffffu, is_late);
         todo = __ballot_sync(0xffffffffu, in && !is_late);
       };
-      bool ended = run_begin == run_end;
-      if (!ended) {
-        load_slots();
-        x = plan[2] - __shfl_sync(0xffffffffu, before, (int)plan[1] & 31);
-        look();
-      }
-      // Publishes the run's next item, or its end.
+      const int first_kind = 2 * blockIdx.x < gridDim.x ? 0 : 1;
+      int begun = 0;  // kinds
+      // Publishes the next item, or the end.
       auto advance = [&]() {
-        while (todo == 0 && !ended) {
-          x += length;
-          base += 32;
-          if (base >= n_items) {
-            base = 0;
-            ++head;
+        while (todo == 0) {
+          if (ended) {
+            if (late || begun == 2) break;
+            kind = begun++ ? 1 - first_kind : first_kind;
+            if (plan[kind].begin == plan[kind].end) continue;
+            ended = false;
+            base = plan[kind].slot & ~31;
+            head = plan[kind].head;
+            loaded = -1;
+            x = plan[kind].x;  // (of the run's first item: those before it are taken off below)
+          } else {
+            x += length;
+            base += 32;
+            if (base >= n_items) {
+              base = 0;
+              ++head;
+            }
+            if (x >= plan[kind].end - plan[kind].begin) {
+              ended = true;
+              continue;
+            }
           }
-          if (x >= run_end) ended = true;
-          else look();
+          look();
         }
         if (!warp_wait(bar(IEMPTY + iq), iphase ^ 1u, timeout_ns, abort_flag, status, 51)) return false;
         int from = 0;
@@ -517,14 +581,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (++iq == kItems) { iq = 0; iphase ^= 1u; }
         return true;
       };
-      int mine = 0;  // the place of the finder's own next item
-      if (finder && !advance()) ended = true;
+      int mine = -1;  // the place of the finder's own next item (none is published yet)
       while (true) {
         Item it;
         if (finder) {
-          it = items[mine];
-          if (it.last || !advance()) break;
-          if (++mine == kItems) mine = 0;
+          if (mine >= 0) it = items[mine];
+          if ((mine >= 0 && it.last) || !advance()) break;
+          if (mine++ < 0) continue;
+          if (mine == kItems) mine = 0;
         } else {
           const Item* ip = next_item();
           if (ip == nullptr) break;
@@ -566,6 +630,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (lane == 0) mbar_arrive(bar(QFULL + t));
       }
       if (loads > 0) mbar_wait_bounded(bar(QFULL + t), (loads - 1) & 1u, timeout_ns);  // copies in flight
+      if (t == 1)  // (records what is out of range)
+        for (int i = blockIdx.x * 32 + lane; i < pa.n; i += gridDim.x * 32) load_chunk_seq(pa, ca.d, i);
     } else {
       // -------------------------------------------------------------- MMAs
       // The whole warp walks the loop and one elected thread issues: descriptors and addresses then stay in uniform
@@ -742,7 +808,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2, r = tid & 127;  // tile, row of it
     const int q4 = warp & 3;                 // TMEM lanes 32 q4 ..
     const float c2 = pa.scale * 1.4426950408889634f;
@@ -888,7 +954,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       place();
       if (ok && nrow_t > 0 && __any_sync(0xffffffffu, valid)) {
-        const bool part = it->split >= 0;  // a piece: the sums in fp32; a whole item: the results in bf16
+        const bool part = it->piece >= 0;  // a piece: the sums in fp32; a whole item: the results in bf16
         float f0 = 1.f, f1 = 0.f;          // factors of a tile's sums; of tile 0's and tile 1's
         if (dual) {
           // The tiles are the halves of the keys: each of the two warps that share TMEM lanes adds up half of the columns.
@@ -906,7 +972,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
         const float f = part ? 1.f : l == 0.f ? 0.f : 1.0f / l;
         const uint64_t f0p = f2_pack(f0 * f, f0 * f), f1p = f2_pack(f1 * f, f1 * f);
-        const long long at = part ? ((long long)it->split * ca.piece_rows + tile0 + r) * D
+        const long long at = part ? ((long long)it->piece + tile0 + r) * D
                                   : (long long)(it->q0 + tok) * pa.os + (long long)h * D;
         uint8_t* orow = part ? reinterpret_cast<uint8_t*>(ca.part_o + at) : (uint8_t*)pa.out + 2 * at;
         // 32 bytes a store: whole sectors, though each lane stores to a row of its own
@@ -972,7 +1038,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           ++given;
         }
         const bool first = !dual || t == 0;
-        if (valid && first && part) ca.part_ml[(long long)it->split * ca.piece_rows + tile0 + r] = make_float2(m * c2, l);
+        if (valid && first && part) ca.part_ml[it->piece + tile0 + r] = make_float2(m * c2, l);
         if (valid && first && !part && pa.lse != nullptr)
           pa.lse[(long long)(it->q0 + tok) * H + h] =
               lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
@@ -998,7 +1064,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                   ko = vo = (((long long)page * Hkv + it->hk) * cv.page_size + (p & (cv.page_size - 1))) * D;
                 },
                 D, __shfl_sync(0xffffffffu, lim, w), c2, mw == -INFINITY ? 0.f : mw * c2, o);
-            float* po = ca.part_o + ((long long)it->split * ca.piece_rows + tile0 + 32 * q4 + w) * D + lane * 8;
+            float* po = ca.part_o + ((long long)it->piece + tile0 + 32 * q4 + w) * D + lane * 8;
             __nv_bfloat16* dw =
                 (__nv_bfloat16*)pa.out + (long long)(it->q0 + tw) * pa.os + (long long)hw * D + lane * 8;
 #pragma unroll
@@ -1025,12 +1091,12 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 // Rows r0 .. r0 + ROWS - 1 of a shared item by a warp: n pieces each, in order, NP of them on their way at a time. Its
 // lanes lie in ROWS parts, one a row, to weight the pieces.
 template <int ROWS, int NP>
-__device__ __forceinline__ void join_rows(const PromptArgs& a, const ChunkArgs& ca, const ChunkRun& run, int c0, int n,
-                                          int r0) {
+__device__ __forceinline__ void join_rows(const PromptArgs& a, const ChunkArgs& ca, const ChunkRun& run, int kind, int c0,
+                                          int n, int r0) {
   constexpr int P = 32 / ROWS;
   const int lane = threadIdx.x & 31, k = lane / P, y0 = lane % P, rows = min(ROWS, run.nrows - r0);
   // run c0 has its last item's piece, the others their first's
-  auto at = [&](int i, int r) { return (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * ca.piece_rows + r0 + r; };
+  auto at = [&](int i, int r) { return (long long)ca.piece(kind, c0 + i, i == 0) + r0 + r; };
   auto ml = [&](int i) { return i < n && k < rows ? ca.part_ml[at(i, k)] : make_float2(-INFINITY, 0.f); };
   float M = -INFINITY, l = 0.f;
   for (int i = y0; i < n; i += P) M = fmaxf(M, ml(i).x);
@@ -1086,7 +1152,7 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const ChunkArgs& 
   }
 }
 
-// The rows that several runs share, by the run that such an item begins in (blockIdx.x), 32 a CTA. Two or three pieces,
+// The rows that several runs share, by the run that such an item begins in (blockIdx.x, either kind), 32 a CTA. Two or three pieces,
 // as most have: a warp takes four rows, whose loads go out together (a warp a row: 130 us a call of 4 sequences' 2048
 // tokens behind 8192, 122 so). Many, of a long sequence's few rows: a warp a row (one token behind 4096, 8 rows a head:
 // 20 us a call, 29 with four rows a warp).
@@ -1097,12 +1163,16 @@ chunk_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ 
   griddep_wait();
   griddep_launch_dependents();
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, first = blockIdx.y * kJoinRows;
-  const ChunkRun run = ca.runs[c0];
-  const int n = run.end - c0 + 1, end = min(run.nrows, first + kJoinRows);
-  if (n <= 4) {
-    if (first + 4 * warp < end) join_rows<4, 2>(a, ca, run, c0, n, first + 4 * warp);
-  } else {
-    for (int r = first + warp; r < end; r += 8) join_rows<1, 8>(a, ca, run, c0, n, r);
+  const ChunkRun runs[2] = {ca.runs[c0], ca.runs[ca.ctas + c0]};
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const ChunkRun& run = runs[kind];
+    const int n = run.end - c0 + 1, end = min(run.nrows, first + kJoinRows);
+    if (n <= 4) {
+      if (first + 4 * warp < end) join_rows<4, 2>(a, ca, run, kind, c0, n, first + 4 * warp);
+    } else {
+      for (int r = first + warp; r < end; r += 8) join_rows<1, 8>(a, ca, run, kind, c0, n, r);
+    }
   }
 }
 
@@ -1122,12 +1192,24 @@ cudaError_t launch(const CUtensorMap& tq, const CacheMaps& m, const PromptArgs& 
 
 }  // namespace
 
-int chunk_piece_rows(int Tq, int G) {
-  return (long long)Tq * G < 2 * TM ? Tq * G : 2 * TM;
+namespace {
+
+// Rows of a piece of either kind: no more than a call's rows of a head.
+int piece_rows(int kind, int Tq, int G) {
+  const long long rows = (long long)Tq * G;
+  return (int)(kind == 0 ? (rows <= TM ? 0 : rows < 2 * TM ? rows : 2 * TM) : (rows < TM ? rows : TM));
+}
+size_t runs_bytes(int ctas) { return ((sizeof(ChunkRun) * 2 * (size_t)ctas + 255) & ~(size_t)255); }
+
+}  // namespace
+
+size_t chunk_tc_bytes(int Tq, int G, int D) {
+  const int ctas = device_sm_count();
+  const size_t rows = 2 * (size_t)ctas * (piece_rows(0, Tq, G) + piece_rows(1, Tq, G));
+  return 256 + runs_bytes(ctas) + rows * (D + 2) * 4;  // (256: the workspace begins at any multiple of 16)
 }
 
-cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, ChunkRun* runs,
-                                 float* part, cudaStream_t s) {
+cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, void* scratch, cudaStream_t s) {
   EncodeTiledFn enc = tensor_map_encoder();
   CUtensorMap tq{};
   const int G = a.H / a.Hkv;
@@ -1135,20 +1217,24 @@ cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const
   if (enc == nullptr || !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma)) return cudaErrorInvalidValue;
   const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM);
   // one CTA an SM, as far as the longest sequences that the cache may hold make as many runs
-  const long long longest = kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kTwo;
+  const long long longest = kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kBlock;
   const long long runs_most = a.Hkv * (long long)slots * longest / kShortest;
   const int ctas = (int)(runs_most < 1 ? 1 : (runs_most < device_sm_count() ? runs_most : device_sm_count()));
   ChunkArgs ca{};
   ca.d = d;
-  ca.runs = runs;
-  ca.piece_rows = chunk_piece_rows(a.Tq, G);
-  ca.part_o = part;
-  ca.part_ml = reinterpret_cast<float2*>(part + 2LL * ctas * ca.piece_rows * a.D);
+  ca.ctas = ctas;
+  uint8_t* at = reinterpret_cast<uint8_t*>(((uintptr_t)scratch + 255) & ~(uintptr_t)255);
+  ca.runs = reinterpret_cast<ChunkRun*>(at);
+  ca.part_o = reinterpret_cast<float*>(at + runs_bytes(ctas));
+  long long rows = 0;
+  for (int k = 0; k < 2; ++k) rows += 2LL * ctas * (ca.rows[k] = piece_rows(k, a.Tq, G));
+  ca.part_ml = reinterpret_cast<float2*>(ca.part_o + rows * a.D);
   const cudaError_t e = a.D <= 64 ? launch<64>(tq, m, a, ca, ctas, slots, q_tma, s)
                                   : launch<128>(tq, m, a, ca, ctas, slots, q_tma, s);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((ca.piece_rows + kJoinRows - 1) / kJoinRows)),
-                    dim3(256), 0, s, a, ca);
+  const int most = ca.rows[0] > ca.rows[1] ? ca.rows[0] : ca.rows[1];
+  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((most + kJoinRows - 1) / kJoinRows)), dim3(256), 0, s, a,
+                    ca);
 }
 
 }  // namespace moe
