@@ -1,31 +1,34 @@
 // Chunks: the new tokens of each sequence against everything that its slot of the paged cache holds, theirs included
-// (bf16, heads of up to 128 elements, on the 5th-generation tensor cores). A prompt's piece, a draft of a few tokens and
-// single tokens lie in one call.
+// (bf16, heads of up to 128 elements, on the 5th-generation tensor cores). A prompt's piece, a draft of a few tokens
+// and single tokens lie in one call.
 //   S = Q K^T (scores), P = 2^(c S - c m) (weights, c = scale log2 e), O += P V, out = O / l
 // in one pass over the keys, as for packed prompts (attn_tc.cu), whose item, MMA order and rescaling these are: 256
-// packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 2^8, weights rounded
-// to bf16 for the MMA and their sum not. What is different here:
-// - Work is shared out by keys, not by items (below): one sequence of 100,000 keys beside a hundred short ones still takes
+// packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 8 in log2 units,
+// weights rounded to bf16 for the MMA (off by at most 2^-8 of each) and their sum not. What is different here:
+// - Work is shared out by keys, not by items (below): one sequence of 100,000 keys beside a hundred short ones takes
 //   every SM.
-// - Keys and values come from pages, by one TMA box a page and 64 elements (pages of 128 positions and up: a block of 128),
-//   and no byte past a sequence's last page is read. Values past its end become zeros in shared memory.
-// - An item of one tile (a decoding sequence's heads, a short draft) would leave one softmax group and half of the MMA's
-//   rhythm idle: both groups take the same rows then, each half of every block's keys, with scores two blocks ahead, and add
-//   up at the end. Single tokens of 64 sequences behind 8192 positions: 196 us, 5.8 TB/s.
+// - Keys and values come from pages, by one TMA box a page and 64 elements (of pages of 128 positions and more a box a
+//   block), and no page past a sequence's last is read. Values past its end become zeros in shared memory.
+// - An item of one tile (a decoding sequence's heads, a short draft) would leave one softmax group idle, and the MMAs
+//   waiting for the other: both groups take the same rows then, each half of every block's keys, with scores two blocks
+//   ahead, and add up at the end. (64 single tokens behind up to 8192: 182 us, 6.2 TB/s.)
+// - There is no output staging: rows are stored 32 bytes a lane, and the ring has a fifth stage in its place (a block
+//   that misses L2 takes up to 2.6 us to come: 64 sequences with 8 chunks 811 us with four, 772 with five).
 // Warps of a CTA (one an SM):
 //   0..3, 4..7  softmax of tile 0 / 1 (or of the halves of the keys); thread = row = TMEM lane
 //   8           allocates TMEM; one elected thread issues every MMA
-//   9           pages, K and V by TMA into a ring (K0 V0 K1 V1 ..)
-//   10          finds the run's items, one ahead, and loads tile 0's Q
+//   9           pages, K and V by TMA into a ring
+//   10          finds the items, one ahead, and loads tile 0's Q
 //   11          loads tile 1's Q
 // All waits are bounded; a wait that runs out records an error, and the CTA ends after its copies and MMAs have.
-// A CTA per item, as many as there are, would need a second kernel or a counter for the parts of long items; with the
-// runs, a launch of one CTA an SM ends within a block or two of the others wherever the lengths lie.
-// Measured (32 heads of 128 on 8): 4096 tokens behind 12288: 1.20 ms in a run of ten (1.60 PFLOP/s of 1.92 measured
-// for a dense product in a burst); 8 sequences' chunks of 500 tokens and 56 single tokens behind up to 32768: 0.80 ms, where
-// reading the keys and values once takes 0.39: the chunks' tile pairs (0.4 ms of MMAs) and the single tokens' reads lie in
-// different runs, of which each takes its time; 64 drafts of 4 tokens behind up to 16384: 358 us, 6.4 TB/s; 16 sequences
-// of 4 tokens behind 300: 15.7 us, four waits on memory one behind the other (lengths, pages, keys, pieces).
+// Measured, heads of 128: 4096 tokens behind 28672, 32 heads on 8, 1.15 ms in a run of ten (1.79 PFLOP/s, 92% of the
+// matrix rate measured in a burst), 1.25 in a loop of seconds: a block of a pair of tiles takes 1.31 to 1.36 us, of which
+// its MMAs are 1.13 at the nominal rate, an item 5 to 6 us more. 64 sequences, 64 heads on 8, up to 16384 positions, 8
+// with a piece of a prompt and 56 with 1 to 4 tokens: 0.69 ms; the chunks' MMAs alone would take 0.39, the reads 0.31.
+// The pairs of tiles take 1.45 us a block there, as their keys come from memory beside the others' reads. Fetching them
+// into L2 a few blocks ahead made it slower (772 -> 875 us: the lookups of L2 count). 64 drafts of 4 tokens behind up to
+// 16384: 340 us, 6.7 TB/s, 98% of the copy rate. 40 tokens of 3 sequences behind 100: 14 us, the code and five waits on
+// memory one behind the other (offsets, lengths, pages, keys, pieces).
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -57,7 +60,7 @@ template <int DP> struct Cfg {
   static constexpr int kStages = DP == 128 ? 5 : 10;
   static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
   static constexpr int kPlan = 2 * (sizeof(Plan) / 8 + kThreads / 32);
-  // tiles and ring, (m, l) of the rows of both tiles, items, the plan, barriers, and the TMEM address beside the abort flag
+  // tiles and ring, (m, l) of both tiles' rows, items, the plan, barriers, and the TMEM address beside the abort flag
   static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + 2 * TM * 8 + (kItems + 1) * sizeof(Item) +
                                   8 * kPlan + 8 * kBars + 16;
 };
@@ -82,7 +85,8 @@ __device__ __forceinline__ uint64_t l2_policy(bool first) {
 // Eight words to a multiple of 32 bytes.
 __device__ __forceinline__ void store_32(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+               ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 struct ChunkArgs {
@@ -102,15 +106,18 @@ struct ChunkArgs {
 // those of two tiles (0) and those of one (1). The items of a kind lie in a row (heads outside, tile slots inside), each
 // as long as its cost: kBlock a block of keys, and kItem for Q, the first scores and the results (measured, us: 1.45 a
 // block and 6 of two tiles, 1.06 and 5.5 of one). The row is cut into equally long runs, one a CTA, whatever items the
-// cuts fall into; runs are not shorter than kShortest. So each CTA has a run of either kind, if there are enough: the
-// tensor cores bound the one and the memory the other, and CTAs that hold more of one kind than others would end at
-// another time than these (with one row for both kinds, whose costs depend on what else is running: 800 us for 8 chunks
-// and 56 single tokens, 695 so). Half of the CTAs begin with one kind and half with the other.
+// cuts fall into; runs are not shorter than kShortest.
+// A long call gives each CTA a run of either kind: the tensor cores bound the one and the memory the other, and CTAs
+// that held more of one kind than others would end at another time than these. (8 chunks and 56 single tokens: 800 us
+// with one row for both kinds, 690 so. Half of the CTAs begin with one kind and half with the other: 735 where all
+// begin with the same.) That is one more cut item a CTA, so where all runs together are shorter than kBoth a CTA the
+// kinds take CTAs of their own, in proportion to their times: 4 chunks of 2048 tokens together behind 8192, heads of 64,
+// 125 us so and 141 with both kinds in each CTA; eight mixed batches of 220 us and more 422 so and 404 with both.
 // A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
 // several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order, so
 // that results do not depend on which CTA is done first. A run has at most two such items, its first and its last: 2
 // pieces a run are enough however long the keys.
-constexpr int kBlock = 4, kItem = 16, kShortest = 16, kBoth = 1200;
+constexpr int kBlock = 4, kItem = 16, kShortest = 16, kBoth = 400;
 
 __device__ __forceinline__ int item_kind(int rows) { return rows <= TM ? 1 : 0; }
 // Length of an item of so many blocks.
@@ -147,8 +154,9 @@ struct Runs {
   int n;
   __device__ __forceinline__ Runs(int kind, long long t0, long long t1, int ctas) : all(kind ? t1 : t0) {
     long long most = ctas;
-    if (t0 > 0 && t1 > 0 && ctas > 1 && 4 * t0 + 3 * t1 < 4LL * kBoth * ctas) {  // (a block of one tile takes 3/4 as long)
-      const long long ones = min(ctas - 1LL, max(1LL, ctas * (3 * t1) / (4 * t0 + 3 * t1)));
+    // (a block of one tile takes 3/4 as long)
+    if (t0 > 0 && t1 > 0 && ctas > 1 && 4 * t0 + 3 * t1 < 4LL * kBoth * ctas) {
+      const long long ones = min(ctas - 1LL, ctas * (3 * t1) / (4 * t0 + 3 * t1) + 1);
       most = kind ? ones : ctas - ones;
     }
     most = min(most, all / kShortest);
@@ -273,7 +281,12 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
     };
     long long sum[2] = {0, 0}, upto[2];
-    if (s0 < s1) walk([&](int, int kind, long long len) { sum[0] += kind ? 0 : len; sum[1] += kind ? len : 0; return true; });
+    if (s0 < s1)
+      walk([&](int, int kind, long long len) {
+        sum[0] += kind ? 0 : len;
+        sum[1] += kind ? len : 0;
+        return true;
+      });
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       upto[kind] = sum[kind];
@@ -340,6 +353,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   }
 
   if (warp >= kSoftWarps) {
+    // 8 * 32 * 216 + 4 * 32 * 72 = 64512, as at the launch. (With 224 and 56 the MMAs' warp spills: a block 1.36 us, 1.33 so.)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kSoftWarps + 1) {
       // -------------------------------------------------------------- K and V (warp 10 finds the items)
@@ -380,11 +394,11 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int slot = ip->k0, hk = ip->hk, n = blocks(ip->n_keys);
         int j0 = ip->key0, rest = ip->nk - j0;  // the block's first position, and what the sequence holds from there on
         const int seq = ip->seq;
-        // Keys that one item alone reads leave L2 first: they would push out those that the tile pairs of a longer
-        // chunk share (64 single tokens behind 8192: 203 -> 196 us).
+        // Keys that one item alone reads leave L2 first: they would push out those that the items of a longer chunk
+        // share (64 single tokens behind up to 8192: 203 us without, 196 so).
         const uint64_t policy = l2_policy((long long)ip->nq * G <= 2 * TM);
-        // Copies lie in the ring in the order in which the MMAs take them: K0 V0 K1 V1 .., and where the scores are computed
-        // two blocks ahead K0 K1 V0 K2 V1 .. (each copy then has two blocks' time to arrive).
+        // Copies lie in the ring in the order in which the MMAs take them: K0 V0 K1 V1 .., and where the scores are
+        // computed two blocks ahead K0 K1 V0 K2 V1 .. (each copy then has two blocks' time to arrive).
         const int lag = ip->dual;
         item_done();
         const int32_t* row = cv.table + (long long)slot * cv.width;
@@ -467,8 +481,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       int kind = 0;  // of the run at hand
       ChunkItem ci{};
       int base = 0, head = 0, loaded = -1;
-      // the place of the 32 slots from `base` on in this head (from the run's beginning on), of the lane's item among them,
-      // the length of all
+      // the place of the 32 slots from `base` on in this head (from the run's beginning on), of the lane's item among
+      // them, the length of all
       long long x = 0, before = 0, length = 0;
       int b0 = 0, b1 = 0;
       uint32_t todo = 0;  // the lanes whose items have blocks in the run and are not published yet
@@ -793,7 +807,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (ok && j < n1) {
             pp1 ^= 1u;
             pv(1, vs, j > 0);
-            if (leader) tc_commit(bar(EMPTY + vs));  // (before QK: the block that takes its place has 1/4 longer to come)
+            if (leader) tc_commit(bar(EMPTY + vs));  // (before QK: the block that takes its place has longer to come)
             if (j + 1 < n1) qk(1, ks);
             if (leader && j + 2 == n1) tc_commit(bar(QEMPTY + 1));
           } else if (ok && leader) {
@@ -957,7 +971,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const bool part = it->piece >= 0;  // a piece: the sums in fp32; a whole item: the results in bf16
         float f0 = 1.f, f1 = 0.f;          // factors of a tile's sums; of tile 0's and tile 1's
         if (dual) {
-          // The tiles are the halves of the keys: each of the two warps that share TMEM lanes adds up half of the columns.
+          // The tiles are the halves of the keys: of the two warps that share TMEM lanes each adds up half of the columns.
           given_ml[tid] = make_float2(m, l);
           tc_fence_before();
           __syncwarp();
@@ -1042,8 +1056,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (valid && first && !part && pa.lse != nullptr)
           pa.lse[(long long)(it->q0 + tok) * H + h] =
               lim == 0 ? -INFINITY : (m * c2 + log2f(l)) * 0.6931471805599453f;
-        // Rows whose results are looked at again. (One whose weights' sum is not finite sees a score that is not, and is NaN
-        // as a whole.)
+        // Rows whose results are looked at again. (One whose weights' sum is not finite sees a score that is not, and is
+        // NaN as a whole.)
         uint32_t again = __ballot_sync(0xffffffffu, valid && !(f2_lo(odd) + f2_hi(odd) == 0.f) && fabsf(l) <= 3.0e38f);
         if (again != 0) {
           Unseen unseen(min(n * BK, it->nk - it->key0));
@@ -1152,10 +1166,10 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const ChunkArgs& 
   }
 }
 
-// The rows that several runs share, by the run that such an item begins in (blockIdx.x, either kind), 32 a CTA. Two or three pieces,
-// as most have: a warp takes four rows, whose loads go out together (a warp a row: 130 us a call of 4 sequences' 2048
-// tokens behind 8192, 122 so). Many, of a long sequence's few rows: a warp a row (one token behind 4096, 8 rows a head:
-// 20 us a call, 29 with four rows a warp).
+// The rows that several runs share, by the run that such an item begins in (blockIdx.x, either kind), 32 a CTA. Two or
+// three pieces, as most have: a warp takes four rows, whose loads go out together (a warp a row: 130 us a call of 4
+// sequences' 2048 tokens behind 8192, 122 so). Many, of a long sequence's few rows: a warp a row (one token behind 4096,
+// 8 rows a head: 20 us a call, 29 with four rows a warp).
 constexpr int kJoinRows = 32;
 
 __global__ void __launch_bounds__(256, 4)
@@ -1163,10 +1177,10 @@ chunk_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ 
   griddep_wait();
   griddep_launch_dependents();
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, first = blockIdx.y * kJoinRows;
-  const ChunkRun runs[2] = {ca.runs[c0], ca.runs[ca.ctas + c0]};
-#pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const ChunkRun& run = runs[kind];
+  const bool some[2] = {ca.runs[c0].nrows > 0, ca.runs[ca.ctas + c0].nrows > 0};
+#pragma unroll 1  // (the code comes from memory: 1 us of a small call)
+  for (int kind = some[0] ? 0 : 1; kind < (some[1] ? 2 : 1); ++kind) {
+    const ChunkRun run = ca.runs[kind * ca.ctas + c0];
     const int n = run.end - c0 + 1, end = min(run.nrows, first + kJoinRows);
     if (n <= 4) {
       if (first + 4 * warp < end) join_rows<4, 2>(a, ca, run, kind, c0, n, first + 4 * warp);
@@ -1209,7 +1223,8 @@ size_t chunk_tc_bytes(int Tq, int G, int D) {
   return 256 + runs_bytes(ctas) + rows * (D + 2) * 4;  // (256: the workspace begins at any multiple of 16)
 }
 
-cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, void* scratch, cudaStream_t s) {
+cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, void* scratch,
+                                 cudaStream_t s) {
   EncodeTiledFn enc = tensor_map_encoder();
   CUtensorMap tq{};
   const int G = a.H / a.Hkv;
@@ -1233,8 +1248,8 @@ cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const
                                   : launch<128>(tq, m, a, ca, ctas, slots, q_tma, s);
   if (e != cudaSuccess) return e;
   const int most = ca.rows[0] > ca.rows[1] ? ca.rows[0] : ca.rows[1];
-  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((most + kJoinRows - 1) / kJoinRows)), dim3(256), 0, s, a,
-                    ca);
+  return launch_pdl(chunk_join_kernel, dim3((unsigned)ctas, (unsigned)((most + kJoinRows - 1) / kJoinRows)), dim3(256),
+                    0, s, a, ca);
 }
 
 }  // namespace moe
