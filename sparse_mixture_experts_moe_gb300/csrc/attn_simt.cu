@@ -55,7 +55,9 @@ constexpr size_t tile_smem(int DP) { return sizeof(float) * ((size_t)(kRows + KT
 
 // SHARED: rows and keys of a decode call, in pieces. SPLIT: a tile's keys over a cluster (in a kernel without it the
 // code for it would cost registers and 3% of the time).
-// PAGED: a chunk's rows over its slots' positions in the cache, in blockIdx.z pieces where there are several.
+// PAGED: a chunk's rows over its slots' positions in the cache, in blockIdx.z pieces where there are several. A tile's
+// rows are looked up in the table once. 256 tokens behind 2048, 16 heads of 128 on 4: 102 us, 26 TFLOP/s, bound like
+// prompts by shared memory and issue.
 template <int DP, bool SHARED, bool SPLIT, bool PAGED>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ SharedPart sp) {
@@ -746,11 +748,14 @@ cudaError_t launch_attn_prompt_simt(const PromptArgs& a, cudaStream_t s) {
 }
 
 // Few tiles: a row's keys in pieces, about kPieceCtas CTAs an SM altogether, at least kPieceTiles tiles of keys each at the
-// longest length that the cache may hold.
+// longest length that the cache may hold (lengths are only known on the device, and a piece behind its rows' last key
+// ends at once). With longer pieces, and a row looked up for every 16 bytes of it, 2048 tokens behind 4096, 16 heads of
+// 256 on 4, took 940 us, 446 so; 40 tokens of small fp32 heads 23 and 16.
 constexpr int kPieceCtas = 8, kPieceTiles = 1;
 int chunk_tile_pieces(const CacheView& c, int n, int Tq, int H) {
   const long long ctas = prompt_tile_slots(Tq, n, H / c.Hkv, kRows) * c.Hkv, rows = (long long)Tq * H;
-  const long long most = ((long long)c.width * c.page_size + kPieceTiles * KT - 1) / (kPieceTiles * KT), fit = rows > 0 ? decode_pieces(rows) / rows : 1;
+  const long long most = ((long long)c.width * c.page_size + kPieceTiles * KT - 1) / (kPieceTiles * KT);
+  const long long fit = rows > 0 ? decode_pieces(rows) / rows : 1;
   long long p = (long long)kPieceCtas * device_sm_count() / (ctas > 0 ? ctas : 1);
   p = p > most ? most : p;
   p = p > fit ? fit : p;
