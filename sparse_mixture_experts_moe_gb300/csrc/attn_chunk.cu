@@ -395,7 +395,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         int j0 = ip->key0, rest = ip->nk - j0;  // the block's first position, and what the sequence holds from there on
         const int seq = ip->seq;
         // Keys that one item alone reads leave L2 first: they would push out those that the items of a longer chunk
-        // share (64 single tokens behind up to 8192: 203 us without, 196 so).
+        // share (64 single tokens behind up to 8192: 194 us without, 183 so; 64 drafts behind 16384 shared positions, whose
+        // items read the same pages: 475 and 469).
         const uint64_t policy = l2_policy((long long)ip->nq * G <= 2 * TM);
         // Copies lie in the ring in the order in which the MMAs take them: K0 V0 K1 V1 .., and where the scores are
         // computed two blocks ahead K0 K1 V0 K2 V1 .. (each copy then has two blocks' time to arrive).

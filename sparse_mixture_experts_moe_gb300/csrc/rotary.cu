@@ -13,18 +13,19 @@
 // of VEC elements. In the half layout those are elements p .. p + VEC - 1 and R/2 + p ..: both parts of its pairs, so no
 // rotation crosses lanes. (VEC is 16 bytes, or what divides R / 2 where that is less.)
 //
-// The rows of all tokens lie in a row, kUnroll * 32 / LPR at a time (a unit), and each warp takes a run of them: it computes
-// its lanes' sines and cosines once a token and looks for the token's place in the cache only where the sequence or the page
-// changes. A lane copies its chunks of the next kStages units into shared memory while it works on the oldest, and reads
-// back what it copied itself, so no barrier is needed. (Loads into registers, two rows ahead: 146 us for 16384 tokens of
-// 72 heads with a norm, 108 so; with 6 or 8 stages 110. One or three CTAs an SM: 112, and 83 us instead of 68 into pages.)
+// The rows of all tokens lie in a row, kUnroll * 32 / LPR at a time (a unit), and each warp takes a run of them: it
+// computes its lanes' sines and cosines once a token and looks for the token's place in the cache only where the
+// sequence or the page changes. A lane copies its chunks of the next kStages units into shared memory while it works on
+// the oldest, and reads back what it copied itself, so no barrier is needed. (Loads into registers, two rows ahead: 146
+// us for 16384 tokens of 72 heads with a norm, 108 so; with 6 or 8 stages 110. One or three CTAs an SM: 112, and 83 us
+// instead of 68 into pages.)
 //
-// Bound by memory: each element is read once and written once. Measured, bf16 heads of 128, 16384 tokens: 40 heads turned
-// 58.8 us (5.7 TB/s, 84% of the copy rate); 72 heads normed and turned 108 us (5.6 TB/s, issue slots 60% busy: packed fp32
-// products and sums, weights in shared memory: 62 -> 58 us and 84 -> 69 before and after); 32 heads' queries and 8 heads'
-// keys normed and turned, with values, into pages 68 us (5.9 TB/s). A decode step's call takes 2.5 to 5 us on the GPU:
-// the launch, the first row's latency and, into a cache, four loads that wait for one another (offsets, slot, length,
-// table).
+// Bound by memory: each element is read once and written once. Measured, bf16 heads of 128, 16384 tokens: 40 heads
+// turned 58.8 us (5.7 TB/s, 84% of the copy rate); 72 heads normed and turned 108 us (5.6 TB/s, issue slots 60% busy:
+// packed fp32 products and sums and weights in shared memory took 62 us to 58, 84 to 69 into pages); 32 heads' queries
+// and 8 heads' keys normed and turned, with values, into pages 68 us (5.9 TB/s). A decode step's call takes 2.5 to 5 us
+// on the GPU: the launch, the first row's latency and, into a cache, four loads that wait for one another (offsets, slot,
+// length, table).
 #include "attn.cuh"
 #include "kernels.cuh"
 

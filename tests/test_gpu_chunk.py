@@ -129,6 +129,47 @@ def test_short_sequences_behind_cut_blocks(lens, D):
     run_chunk([1] * 700, nk, 8, 4, D, BF16, page=64, seed=2)
 
 
+@pytest.mark.parametrize("nq,nk", [([1] * 30 + [200, 150] + [3] * 6, 2300), ([140] * 12 + [2] * 20, 1700),
+                                   ([130] * 10 + [1] * 20 + [257, 129, 128], 500)])
+def test_long_runs_of_both_kinds(nq, nk):
+    """Items of one tile and of two, enough of them that a CTA has a run of either kind, and (the last) just not."""
+    r = random.Random(nk)
+    lens = [n + r.randint(nk - 200, nk) for n in nq]
+    run_chunk(nq, lens, 32, 32, 16, BF16, page=64, seed=6)
+
+
+@pytest.mark.parametrize("D", [16, 64, 72, 128])
+@pytest.mark.parametrize("shift", [8, 16])
+def test_outputs_and_scratch_at_any_16_bytes(shift, D):
+    """Results whose rows, and pieces whose memory, begin at a multiple of 16 bytes and of no more."""
+    H, Hk, nq, nk = 6, 2, [150, 1, 5, 40], [900, 1500, 300, 40]
+    cache, held = pool(nk, 64, Hk, D, BF16, 3)
+    T, offs = sum(nq), offsets(nq)
+    q = tensor((T, H, D), 5, BF16, DEV)
+    buf = torch.full((T * (H * D + shift) + shift,), float("nan"), dtype=BF16, device=DEV)
+    out = buf[shift:].as_strided((T, H, D), (H * D + shift, D, 1))
+    a = moe.Attention(H, Hk, D, BF16)
+    s, o = i32([0, 1, 2, 3], DEV), i32(offs, DEV)
+    a.chunk(q, cache, s, o, out=out)
+    check(out, None, reference(q, held, [0, 1, 2, 3], offs, True, D ** -0.5), max(nk), D, BF16)
+    assert torch.isnan(buf[:shift]).all()
+    assert torch.isnan(buf[shift:].as_strided((T, shift), (H * D + shift, 1), H * D + shift)).all()
+    need = a._lib.moe_attention_chunk_workspace_bytes(cache._ref, 4, T, H) - 256
+    header = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    scratch = torch.full((need + 256,), 0xff, dtype=torch.uint8, device=DEV)
+    again = torch.zeros((T, H, D), dtype=BF16, device=DEV)
+    for at in (16, 32, 48, 240):
+        rc = a._lib.moe_attention_chunk_ex(cache._ref, 0, q.data_ptr(), s.data_ptr(), o.data_ptr(), 4, T, H, H * D, H * D,
+                                           a.scale, 1, again.data_ptr(), None, header.data_ptr(), 256,
+                                           scratch.data_ptr() + at, need, torch.cuda.current_stream().cuda_stream)
+        assert rc == moe.MOE_OK
+        assert torch.equal(again, out)
+        again.zero_()
+        torch.cuda.synchronize()
+        assert (scratch[:at] == 0xff).all() and (scratch[at + need:] == 0xff).all()
+    assert not header.any()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_slots_in_any_order_and_twice(dtype):
     """Slots named in another order than the table's, some not at all, one by two sequences."""
