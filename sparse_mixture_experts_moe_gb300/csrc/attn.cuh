@@ -135,8 +135,9 @@ cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s);
 // of chunk_tc_bytes.
 size_t chunk_tc_bytes(int Tq, int G, int D);
 cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const CacheMaps& m, void* scratch, cudaStream_t s);
-// The other types and heads: rows in `pieces` parts, d.part [Tq H][pieces][D + 2].
+// The other types and heads: rows in `pieces` parts, d.part [Tq H][pieces][D + 2] (none where clusters hold them).
 int chunk_tile_pieces(const CacheView& c, int n, int Tq, int H);
+bool chunk_tiles_in_clusters(const CacheView& c, int n, int Tq, int H, int pieces);
 cudaError_t launch_attn_chunk_tiles(const PromptArgs& a, const DecodeArgs& d, int pieces, cudaStream_t s);
 cudaError_t launch_attn_chunk_mma(const PromptArgs& a, const SharedPart& sp, dim3 grid, cudaStream_t s);
 

@@ -128,7 +128,8 @@ ChunkScratch chunk_scratch(const CacheView& c, int n, int Tq, int H) {
   if (c.dt == MOE_DTYPE_BF16 && c.D <= 128)
     return {align256(chunk_tc_bytes(Tq, H / c.Hkv, c.D)), 0};
   const int pieces = chunk_tile_pieces(c, n, Tq, H);
-  return {pieces > 1 ? align256((size_t)Tq * H * pieces * (c.D + 2) * 4) : 0, pieces};
+  const bool none = pieces == 1 || chunk_tiles_in_clusters(c, n, Tq, H, pieces);
+  return {none ? 0 : align256((size_t)Tq * H * pieces * (c.D + 2) * 4), pieces};
 }
 // rows and work items are numbered with 32 bits
 bool chunk_sizes_ok(const moe_kv_cache* c, int n, int Tq, int H) {
