@@ -24,7 +24,7 @@ import ctypes
 import threading
 
 from . import _lib
-from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _check, _ptr, _stream
+from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _allocator, _check, _ptr, _stream
 from .rotary import Rotary, _check_overlap, _result, _tokens, _weight
 
 
@@ -76,7 +76,7 @@ class _Bound:
         self._lib = _lib.lib()
         self._i32 = torch.int32
         self._f32 = torch.float32
-        self._empty, self._empty_like = torch.empty, torch.empty_like
+        self._empty, self._empty_like, self._new = torch.empty, torch.empty_like, _allocator(torch)
         # the current stream's handle alone, without a stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._current_device, self._many = torch._C._cuda_getDevice, torch.cuda.device_count() > 1
@@ -403,7 +403,9 @@ class KVCache(_Bound):
         last = self._last_append
         if last[0] != look:
             last = self._last_append = (look, self._checked_append(k, v, slots, offsets, pos, q, q_weight, k_weight))
-        n, total, ks, vs, H, qs, q_shape = last[1]
+        n, total, ks, vs, H, qs, q_new = last[1]
+        if self._many and self._current_device() != self._dev:  # kernels run on the current device
+            self._elsewhere(self._dev)
         if rotary is None:
             turn = None
         else:
@@ -420,9 +422,7 @@ class KVCache(_Bound):
         elif q is not None:
             if stream is not None:  # a tensor made here belongs to the current stream
                 raise ValueError("moe: pass q_out with an explicit stream")
-            q_out = self._empty(q_shape, dtype=self.dtype, device=self.device)
-        if self._many and self._current_device() != self._dev:  # kernels run on the current device
-            self._elsewhere(self._dev)
+            q_out = self._new(*q_new)
         s = self._raw_stream(self._dev) if stream is None else _stream(stream)
         with self._lock:
             ws = self._workspace(s)
@@ -453,7 +453,7 @@ class KVCache(_Bound):
         tq, H, qs = _tokens(q, "q", D, dtype, dev)
         if tq != total or H == 0:
             raise ValueError(f"moe: k has {total} tokens, q {tq} with {H} heads")
-        return n, total, ks, vs, H, qs, (total, H, D)
+        return n, total, ks, vs, H, qs, ((total, H, D), (H * D, D, 1), dtype)
 
     def fork(self, src, dst, stream=None):
         """Slot dst[i] becomes a copy of slot src[i], sharing its full pages; what dst[i] held is released."""
@@ -645,14 +645,15 @@ class Attention(_Bound):
             Tq, qs = _heads(q, "q", self.heads, self.head_dim, self.dtype, dev)
             n = _ints(slots, "slots", None, dev, self._i32)
             _ints(q_offsets, "q_offsets", n + 1, dev, self._i32)
-            last = self._last_chunk = (look, (n, Tq, qs, (Tq, self.heads, self.head_dim)))
-        n, Tq, qs, shape = last[1]
-        if out is None and lse is None and stream is None:
-            out, so = self._empty(shape, dtype=self.dtype, device=q.device), self.heads * self.head_dim
-        else:
-            out, so = self._out(q, qs, out, lse, stream, dev)
+            new = (Tq, self.heads, self.head_dim), (self.heads * self.head_dim, self.head_dim, 1), self.dtype
+            last = self._last_chunk = (look, (n, Tq, qs, new))
+        n, Tq, qs, new = last[1]
         if self._many and self._current_device() != dev:  # kernels run on the current device
             self._elsewhere(dev)
+        if out is None and lse is None and stream is None:
+            out, so = self._new(*new), self.heads * self.head_dim
+        else:
+            out, so = self._out(q, qs, out, lse, stream, dev)
         s = self._raw_stream(dev) if stream is None else _stream(stream)
         with self._lock:
             sizes = (n, Tq, cache.width, cache.page_size, dev)

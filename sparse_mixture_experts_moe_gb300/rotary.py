@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _stream
+from ._lib import MOE_ERR_INVALID_ARG, MOE_OK, MoeError, _allocator, _stream
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {None: 0, "linear": 1, "base": 2, "turns": 3, "pairs": 4}
@@ -141,9 +141,9 @@ class Rotary:
             raise MoeError(rc, "moe_rotary_init")
         self._i32 = torch.int32
         self._dtypes = {torch.bfloat16: _lib.MOE_DTYPE_BF16, torch.float32: _lib.MOE_DTYPE_F32}
-        self._empty = torch.empty
+        self._new = _allocator(torch)
         self._call = self._lib.moe_rotary_apply
-        self._last = (None, None)
+        self._last = self._last_outs = (None, None)
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._current_device, self._many = torch._C._cuda_getDevice, torch.cuda.device_count() > 1
 
@@ -172,18 +172,18 @@ class Rotary:
         last = self._last
         if last[0] != look:
             last = self._last = (look, self._checked(q, positions, k, q_weight, k_weight))
-        dev, dtype, dt, T, H, qs, Hk, ks, q_shape, k_shape = last[1]
+        dev, dtype, dt, T, H, qs, Hk, ks, q_new, k_new = last[1]
+        if self._many and self._current_device() != dev:  # kernels run on the current device
+            raise ValueError(f"moe: the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
         if out is None and k_out is None:
             if stream is not None:  # tensors made here belong to the current stream
                 raise ValueError("moe: pass out (and k_out) with an explicit stream")
-            out, qso = self._empty(q_shape, dtype=dtype, device=q.device), H * self.head_dim
+            out, qso = self._new(*q_new), H * self.head_dim
             if k is not None:
-                k_out = self._empty(k_shape, dtype=dtype, device=q.device)
+                k_out = self._new(*k_new)
             kso = Hk * self.head_dim
         else:
             out, qso, k_out, kso = self._outs(q, k, out, k_out, last[1], stream)
-        if self._many and self._current_device() != dev:  # kernels run on the current device
-            raise ValueError(f"moe: the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
         rc = self._call(self._ref, q.data_ptr(), qs, H, k if k is None else k.data_ptr(), ks, Hk, positions.data_ptr(), T, dt,
                         q_weight if q_weight is None else q_weight.data_ptr(), k_weight if k_weight is None else k_weight.data_ptr(),
                         eps, out.data_ptr(), qso, k if k is None else k_out.data_ptr(), kso,
@@ -216,22 +216,37 @@ class Rotary:
             Tk, Hk, ks = _tokens(k, "k", D, dtype, dev)
             if Tk != T or Hk == 0:
                 raise ValueError(f"moe: q has {T} tokens, k {Tk} with {Hk} heads")
-        return dev, dtype, dt, T, H, qs, Hk, ks, (T, H, D), (T, Hk, D)
+        return dev, dtype, dt, T, H, qs, Hk, ks, ((T, H, D), (H * D, D, 1), dtype), ((T, Hk, D), (Hk * D, D, 1), dtype)
 
     def _outs(self, q, k, out, k_out, call, stream):
         """Outputs of which the caller gave one or both, and their token strides."""
-        dev, dtype, _, T, H, _, Hk, _, q_shape, k_shape = call
+        dev, dtype, _, T, H, qs, Hk, ks, q_new, k_new = call
         if stream is not None and (out is None or (k is not None and k_out is None)):
             raise ValueError("moe: pass out (and k_out) with an explicit stream")
         if k is None and k_out is not None:
             raise ValueError("moe: k_out needs k")
         if out is None:
-            out = self._empty(q_shape, dtype=dtype, device=q.device)
-        qso, kso = _result(out, "out", T, H, self.head_dim, dtype, dev), 0
-        if k is not None:
-            if k_out is None:
-                k_out = self._empty(k_shape, dtype=dtype, device=q.device)
-            kso = _result(k_out, "k_out", T, Hk, self.head_dim, dtype, dev)
+            out = self._new(*q_new)
+        if k is not None and k_out is None:
+            k_out = self._new(*k_new)
+        look = (call, out.shape, out.stride(), out.dtype, out.get_device(),
+                k if k is None else (k_out.shape, k_out.stride(), k_out.dtype, k_out.get_device()))
+        last = self._last_outs
+        if last[0] != look:
+            qso, kso, D = _result(out, "out", T, H, self.head_dim, dtype, dev), 0, self.head_dim
+            if k is not None:
+                kso = _result(k_out, "k_out", T, Hk, D, dtype, dev)
+            size = q.element_size()  # and the bytes from the first element's to the last's end
+            ends = [((T - 1) * s + h * D) * size if h else 0 for s, h in ((qso, H), (kso, Hk), (qs, H), (ks, Hk))]
+            last = self._last_outs = (look, (qso, kso, *ends))
+        qso, kso, n_out, n_k_out, n_q, n_k = last[1]
         if T > 0:
-            _check_overlap((("out", out), ("k_out", k_out)), (q, k))
+            o, x = out.data_ptr(), q.data_ptr()
+            fine = o + n_out <= x or x + n_q <= o or (o == x and qso == qs)
+            if k is not None:
+                p, y = k_out.data_ptr(), k.data_ptr()
+                fine = (fine and (p + n_k_out <= y or y + n_k <= p or (p == y and kso == ks)) and (o + n_out <= p or p + n_k_out <= o)
+                        and (o + n_out <= y or y + n_k <= o) and (p + n_k_out <= x or x + n_q <= p))
+            if not fine:  # (heads of one fused tensor lie between each other)
+                _check_overlap((("out", out), ("k_out", k_out)), (q, k))
         return out, qso, k_out, kso

@@ -186,7 +186,7 @@ def rotary(called, many=False, current=0, **kw):
     r._raw_stream = lambda dev: 0
     r._current_device, r._many = (lambda: current), many
     r._call = lambda *a: called.append(a) or moe.MOE_OK
-    r._empty = lambda shape, dtype, device: Fake(shape, dtype, device.index)
+    r._new = lambda shape, strides, dtype: Fake(shape, dtype, 0)
     return r
 
 
