@@ -353,7 +353,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   }
 
   if (warp >= kSoftWarps) {
-    // 8 * 32 * 216 + 4 * 32 * 72 = 64512, as at the launch. (With 224 and 56 the MMAs' warp spills: a block 1.36 us, 1.33 so.)
+    // 8 * 32 * 216 + 4 * 32 * 72 = 64512, as at the launch. (With 224 and 56 these warps spill twice as much: 4096 tokens
+    // behind 28672 1167 us, 1150 so.)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kSoftWarps + 1) {
       // -------------------------------------------------------------- K and V (warp 10 finds the items)
