@@ -6,6 +6,7 @@
 
 #include <atomic>
 
+#include "attn_plan.cuh"
 #include "common.cuh"
 
 namespace moe {
@@ -210,18 +211,6 @@ __device__ __forceinline__ void check_shared(const DecodeArgs& a, int i, int me,
   }
 }
 
-// A tile slot of packed prompts: with R rows a tile, sequence i (L_i tokens) owns the slots
-// floor(q_offsets[i] G / R) + i up to the next sequence's first, which are never fewer than its
-// ceil(L_i G / R) tiles. So tile slots are found from the offsets alone, with no scan over the
-// sequences' tile counts: the largest i whose first slot is <= s, by bisection.
-__device__ __forceinline__ int find_tile_seq(const int32_t* qo, int n, int G, int R, long long s) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)qo[mid] * G / R + mid <= s) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
 inline long long prompt_tile_slots(int Tq, int n, int G, int R) { return (long long)Tq * G / R + n; }
 
 // Sequence i of a prompt call, its offsets checked (a bad one is recorded and has no rows).
@@ -251,7 +240,7 @@ __device__ __forceinline__ Seq load_chunk_seq(const PromptArgs& a, const DecodeA
   s.nq = q1 - s.q0;
   s.k0 = d.slots[i];
   s.nk = slot_len(d.c, s.k0);
-  if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq) {
+  if (bad_offsets(s.q0, q1, a.Tq)) {
     record_error(a.status, MOE_ERR_DEVICE_CHECK, i);
     s.nq = 0;
     s.nk = 0;
@@ -290,12 +279,6 @@ __device__ __forceinline__ Seq load_seq_warp(const PromptArgs& a, int i) {
     s.nk = 0;
   }
   return s;
-}
-// Keys that query token t sees.
-__device__ __forceinline__ int visible_keys(int t, int nq, int nk, int causal) {
-  if (!causal) return nk;
-  const int lim = t + 1 + nk - nq;
-  return lim < 0 ? 0 : (lim > nk ? nk : lim);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {

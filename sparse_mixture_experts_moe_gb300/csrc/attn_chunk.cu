@@ -5,7 +5,7 @@
 // in one pass over the keys, as for packed prompts (attn_tc.cu), whose item, MMA order and rescaling these are: 256
 // packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 8 in log2 units,
 // weights rounded to bf16 for the MMA (off by at most 2^-8 of each) and their sum not. What is different here:
-// - Work is shared out by keys, not by items (below): one sequence of 100,000 keys beside a hundred short ones takes
+// - Work is shared out by keys, not by items (attn_plan.cuh): one sequence of 100,000 keys beside a hundred short ones takes
 //   every SM.
 // - Keys and values come from pages, by one TMA box a page and 64 elements (of pages of 128 positions and more a box a
 //   block), and no page past a sequence's last is read. Values past its end become zeros in shared memory.
@@ -20,7 +20,8 @@
 //   9           pages, K and V by TMA into a ring
 //   10          finds the items, one ahead, and loads tile 0's Q
 //   11          loads tile 1's Q
-// All waits are bounded; a wait that runs out records an error, and the CTA ends after its copies and MMAs have.
+// All waits are bounded; a wait that runs out records an error, and the CTA ends after its copies and MMAs have. So are
+// the loops over sequences and slots, and the heads and runs that they name, whatever the offsets and lengths hold.
 // Measured, heads of 128: 4096 tokens behind 28672, 32 heads on 8, 1.15 ms in a run of ten (1.79 PFLOP/s, 92% of the
 // matrix rate measured in a burst), 1.25 in a loop of seconds: a block of a pair of tiles takes 1.31 to 1.36 us, of which
 // its MMAs are 1.13 at the nominal rate, an item 5 to 6 us more. 64 sequences, 64 heads on 8, up to 16384 positions, 8
@@ -48,10 +49,10 @@ constexpr int kItems = 3;   // items published: one worked on, one ahead, one be
 constexpr int kItemReaders = 1 + 8 + 2;
 
 // What a CTA has of a kind: the length of all items of a head, its run's number, beginning and end, and the slot, place
-// and head of the item that the run begins in.
+// and head of the item that the run begins in; and the sequences in front of the first bad offsets.
 struct Plan {
   long long all, begin, end, x;
-  int run, slot, head, unused;
+  int run, slot, head, seqs;
 };
 
 template <int DP> struct Cfg {
@@ -60,7 +61,8 @@ template <int DP> struct Cfg {
   static constexpr int kStages = DP == 128 ? 5 : 10;
   static constexpr int kBars = 2 * kStages + 7 * 2 + 1 + 2 * kItems + 1 + 8;
   static constexpr int kPlan = 2 * (sizeof(Plan) / 8 + kThreads / 32);
-  // tiles and ring, (m, l) of both tiles' rows, items, the plan, barriers, and the TMEM address beside the abort flag
+  // tiles and ring, (m, l) of both tiles' rows, items, the plan, barriers, and the TMEM address beside the abort flag and
+  // the first sequence of bad offsets
   static constexpr size_t kSmem = (size_t)(2 + kStages) * kTileBytes + 2 * TM * 8 + (kItems + 1) * sizeof(Item) +
                                   8 * kPlan + 8 * kBars + 16;
 };
@@ -102,76 +104,7 @@ struct ChunkArgs {
   }
 };
 
-// How a chunk call is shared out. An item is, as for prompts, 256 packed rows of one key/value head. There are two kinds:
-// those of two tiles (0) and those of one (1). The items of a kind lie in a row (heads outside, tile slots inside), each
-// as long as its cost: kBlock a block of keys, and kItem for Q, the first scores and the results (measured, us: 1.45 a
-// block and 6 of two tiles, 1.06 and 5.5 of one). The row is cut into equally long runs, one a CTA, whatever items the
-// cuts fall into; runs are not shorter than kShortest.
-// A long call gives each CTA a run of either kind: the tensor cores bound the one and the memory the other, and CTAs
-// that held more of one kind than others would end at another time than these. (8 chunks and 56 single tokens: 800 us
-// with one row for both kinds, 690 so. Half of the CTAs begin with one kind and half with the other: 735 where all
-// begin with the same.) That is one more cut item a CTA, so where all runs together are shorter than kBoth a CTA the
-// kinds take CTAs of their own, in proportion to their times: 4 chunks of 2048 tokens together behind 8192, heads of 64,
-// 125 us so and 141 with both kinds in each CTA; eight mixed batches of 220 us and more 422 so and 404 with both.
-// A block belongs to the run that its beginning lies in. An item inside one run goes to the output; of one that
-// several runs share, each puts its part (a piece) into the workspace, and chunk_join_kernel adds them up in order, so
-// that results do not depend on which CTA is done first. A run has at most two such items, its first and its last: 2
-// pieces a run are enough however long the keys.
-constexpr int kBlock = 4, kItem = 16, kShortest = 16, kBoth = 400;
-
-__device__ __forceinline__ int item_kind(int rows) { return rows <= TM ? 1 : 0; }
-// Length of an item of so many blocks.
-__device__ __forceinline__ long long item_length(int blocks) { return kItem + (long long)blocks * kBlock; }
-
-struct ChunkItem {
-  int seq, row0, nrows, q0, nq, nk, slot;
-  int lim0, lim1, n_blocks;
-  __device__ __forceinline__ long long length() const { return nrows > 0 ? item_length(n_blocks) : 0; }
-};
-// What fills tile slot s (nrows = 0: nothing).
-__device__ __forceinline__ ChunkItem chunk_item(const PromptArgs& pa, const ChunkArgs& ca, int s, int i) {
-  const int G = pa.H / pa.Hkv;
-  ChunkItem it{};
-  it.seq = i;
-  const int q0 = pa.qo[i], q1 = pa.qo[i + 1];
-  it.slot = ca.d.slots[i];
-  if (q0 < 0 || q1 < q0 || q1 > pa.Tq) return it;
-  it.q0 = q0;
-  it.nq = q1 - q0;
-  const long long r0 = ((long long)s - ((long long)q0 * G / (2 * TM) + i)) * (2 * TM);
-  if (r0 < 0 || r0 >= (long long)it.nq * G) return it;
-  it.nk = slot_len(ca.d.c, it.slot);
-  it.row0 = (int)r0;
-  it.nrows = min(2 * TM, it.nq * G - it.row0);
-  it.lim0 = visible_keys((it.row0 + min(it.nrows, TM) - 1) / G, it.nq, it.nk, pa.causal);
-  it.lim1 = it.nrows > TM ? visible_keys((it.row0 + it.nrows - 1) / G, it.nq, it.nk, pa.causal) : 0;
-  it.n_blocks = (max(it.lim0, it.lim1) + BK - 1) / BK;
-  return it;
-}
-// The runs of a kind: how many, their beginnings, and the run that place x lies in. t0, t1: the lengths of the two rows.
-struct Runs {
-  long long all;
-  int n;
-  __device__ __forceinline__ Runs(int kind, long long t0, long long t1, int ctas) : all(kind ? t1 : t0) {
-    long long most = ctas;
-    // (a block of one tile takes 3/4 as long)
-    if (t0 > 0 && t1 > 0 && ctas > 1 && 4 * t0 + 3 * t1 < 4LL * kBoth * ctas) {
-      const long long ones = min(ctas - 1LL, ctas * (3 * t1) / (4 * t0 + 3 * t1) + 1);
-      most = kind ? ones : ctas - ones;
-    }
-    most = min(most, all / kShortest);
-    n = most < 1 ? 1 : (int)most;
-  }
-  __device__ __forceinline__ long long begin(int c) const { return all * c / n; }
-  __device__ __forceinline__ int of(long long x) const { return (int)(((x + 1) * n - 1) / all); }
-};
-// Which run of a kind a CTA takes: those of kind 1 go on where those of kind 0 end, so that a short call's lie in CTAs of
-// their own.
-__device__ __forceinline__ int run_of(int kind, const Runs& runs0) {
-  if (kind == 0) return blockIdx.x;
-  const int c = (int)blockIdx.x - (runs0.all > 0 ? runs0.n % (int)gridDim.x : 0);
-  return c < 0 ? c + gridDim.x : c;
-}
+static_assert(chunk::kTile == TM && chunk::kKeys == BK, "tiles");
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -193,6 +126,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   uint64_t* bars = reinterpret_cast<uint64_t*>(warp_sums + 2 * (kThreads / 32));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* first_bad = reinterpret_cast<int*>(tmem_slot + 2);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int FULL = 0, EMPTY = C::kStages, QFULL = 2 * C::kStages, SFULL = QFULL + 2, PFULL = SFULL + 4,
                 ODONE = PFULL + 4, QEMPTY = ODONE + 2, DONE = QEMPTY + 2, IFULL = DONE + 1, IEMPTY = IFULL + kItems,
@@ -217,6 +151,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     for (int i = 0; i < 8; ++i) mbar_init(bar(GIVEN + i), 2);
     fence_mbar_init();
     *abort_flag = 0;
+    *first_bad = pa.n;
+    for (int kind = 0; kind < 2; ++kind) plan[kind].x = plan[kind].slot = plan[kind].head = 0;
     if (q_tma) tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -250,54 +186,46 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (lane == 0) mbar_arrive(bar(IEMPTY + iq));
     if (++iq == kItems) { iq = 0; iphase ^= 1u; }
   };
-  auto blocks = [](int keys) { return (keys + BK - 1) / BK; };
+  auto blocks = [](int keys) { return chunk::blocks_of(keys); };
 
   // This CTA's runs: a scan over the lengths of all tile slots, each thread with some of them in a row.
   {
     const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
-    // f(slot, kind, length) for the slots of [s0, s1) that a tile fills, as long as it returns true. The sequences lie in
-    // the slots' order, so what is read of them is read ahead, four at a time.
+    // The offsets are looked at beside the walk, and it is done again without the sequences from the first bad ones on:
+    // in the usual case that costs no wait of its own.
+    int seqs = pa.n;
     auto walk = [&](auto f) {
-      int s = s0, i = find_tile_seq(pa.qo, pa.n, G, 2 * TM, s0);
-      while (s < s1 && i < pa.n) {
-        int q[5], len[4];
-#pragma unroll
-        for (int k = 0; k < 5; ++k) q[k] = pa.qo[min(i + k, pa.n)];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) len[k] = slot_len(ca.d.c, ca.d.slots[min(i + k, pa.n - 1)]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (i + k >= pa.n || q[k] < 0 || q[k + 1] < q[k] || q[k + 1] > pa.Tq) continue;
-          const long long first = (long long)q[k] * G / (2 * TM) + i + k, rows = (long long)(q[k + 1] - q[k]) * G;
-          const long long end = min((long long)s1, first + (rows + 2 * TM - 1) / (2 * TM));
-          for (s = max(s, (int)min(first, (long long)s1)); s < end; ++s) {
-            const int row0 = (int)(s - first) * 2 * TM, nrows = min(2 * TM, (int)rows - row0), nq = q[k + 1] - q[k];
-            const int lim0 = visible_keys((row0 + min(nrows, TM) - 1) / G, nq, len[k], pa.causal);
-            const int lim1 = nrows > TM ? visible_keys((row0 + nrows - 1) / G, nq, len[k], pa.causal) : 0;
-            if (!f(s, item_kind(nrows), item_length(blocks(max(lim0, lim1))))) return;
-          }
-        }
-        i += 4;
-      }
+      chunk::walk_slots(pa.qo, seqs, pa.Tq, G, pa.causal, s0, s1,
+                        [&](int i) { return slot_len(ca.d.c, ca.d.slots[i]); }, f);
     };
-    long long sum[2] = {0, 0}, upto[2];
-    if (s0 < s1)
-      walk([&](int, int kind, long long len) {
-        sum[0] += kind ? 0 : len;
-        sum[1] += kind ? len : 0;
-        return true;
-      });
+    long long sum[2], upto[2];
+    while (true) {
+      int bad = seqs;  // (from the last thread on: those of a short call have no slots to walk)
+#pragma unroll 1
+      for (int i = kThreads - 1 - tid; i < seqs && bad == seqs; i += kThreads)
+        if (bad_offsets(pa.qo[i], pa.qo[i + 1], pa.Tq)) bad = i;
+      sum[0] = sum[1] = 0;
+      if (s0 < s1)
+        walk([&](int, int kind, long long len) {
+          sum[0] += kind ? 0 : len;
+          sum[1] += kind ? len : 0;
+          return true;
+        });
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      upto[kind] = sum[kind];
+      for (int kind = 0; kind < 2; ++kind) {
+        upto[kind] = sum[kind];
 #pragma unroll
-      for (int w = 1; w < 32; w <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto[kind], w);
-        if (lane >= w) upto[kind] += x;
+        for (int w = 1; w < 32; w <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, upto[kind], w);
+          if (lane >= w) upto[kind] += x;
+        }
+        if (lane == 31) warp_sums[kind * (kThreads / 32) + warp] = upto[kind];
       }
-      if (lane == 31) warp_sums[kind * (kThreads / 32) + warp] = upto[kind];
+      if (!__syncthreads_or(bad < seqs)) break;
+      if (bad < seqs) atomicMin(first_bad, bad);
+      __syncthreads();
+      seqs = *first_bad;
     }
-    __syncthreads();
     long long total[2] = {0, 0};
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind)
@@ -306,17 +234,17 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (w == warp) upto[kind] += total[kind];
         total[kind] += warp_sums[kind * (kThreads / 32) + w];
       }
-    const Runs runs0(0, total[0] * Hkv, total[1] * Hkv, gridDim.x);
+    const chunk::Runs runs0(0, total[0] * Hkv, total[1] * Hkv, gridDim.x);
     long long at[2], x[2];  // the run's beginning in its head; the item's after the ones looked through
     bool here[2];           // it lies in one of this thread's slots
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const long long all = total[kind];
-      const int c = run_of(kind, runs0);
+      const int c = chunk::run_of(kind, runs0, blockIdx.x, gridDim.x);
       long long begin = 0, end = 0;
       here[kind] = false;
       if (all > 0) {
-        const Runs runs(kind, total[0] * Hkv, total[1] * Hkv, gridDim.x);
+        const chunk::Runs runs(kind, total[0] * Hkv, total[1] * Hkv, gridDim.x);
         if (c < runs.n) {
           begin = runs.begin(c);
           end = runs.begin(c + 1);
@@ -332,6 +260,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         plan[kind].run = c;
         plan[kind].begin = begin;
         plan[kind].end = end;
+        plan[kind].seqs = seqs;
         ChunkRun none;
         none.nrows = 0;
         ca.runs[kind * gridDim.x + c] = none;
@@ -481,19 +410,23 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       // looks at 32 tile slots at once, one a lane (the next of an item after the other cost 9 us an item).
       const bool finder = t == 0;
       int kind = 0;  // of the run at hand
-      ChunkItem ci{};
-      int base = 0, head = 0, loaded = -1;
-      // the place of the 32 slots from `base` on in this head (from the run's beginning on), of the lane's item among
-      // them, the length of all
-      long long x = 0, before = 0, length = 0;
+      chunk::SlotItem ci{};
+      // the 32 slots at hand, the place of the lane's item among them, the length of all
+      chunk::Place at{0, 0, 0};
+      int loaded = -1;
+      long long before = 0, length = 0;
       int b0 = 0, b1 = 0;
       uint32_t todo = 0;  // the lanes whose items have blocks in the run and are not published yet
       bool late = false, ended = true;
       auto load_slots = [&]() {
-        const int s = base + lane;
-        ci = s < n_items ? chunk_item(pa, ca, s, find_tile_seq(pa.qo, pa.n, G, 2 * TM, s)) : ChunkItem{};
-        if (item_kind(ci.nrows) != kind) ci.nrows = 0;
-        loaded = base;
+        const int s = at.base + lane;
+        ci = chunk::SlotItem{};
+        if (s < n_items)
+          ci = chunk::slot_item(pa.qo, ca.d.slots, pa.Tq, G, pa.causal, s,
+                                find_tile_seq(pa.qo, plan[0].seqs, G, chunk::kRows, s),
+                                [&](int slot) { return slot_len(ca.d.c, slot); });
+        if (chunk::item_kind(ci.nrows) != kind) ci.nrows = 0;
+        loaded = at.base;
         const long long len = ci.length();
         before = len;
 #pragma unroll
@@ -507,7 +440,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       auto my_item = [&]() {
         const int all = max(1, ci.n_blocks);  // (without a key: an item all the same, whose results are 0)
         Item it{};
-        it.hk = head;
+        it.hk = at.head;
         it.seq = ci.seq;
         it.row0 = ci.row0;
         it.nrows = ci.nrows;
@@ -521,31 +454,27 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         it.piece = b0 == 0 && b1 == all ? -1 : ca.piece(kind, plan[kind].run, b0 == 0);
         if (b0 == 0 && b1 < all) {
           ChunkRun r;
-          r.hk = head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
-          r.end = Runs(kind, plan[0].all * Hkv, plan[1].all * Hkv, gridDim.x).of(
-              plan[kind].begin + x + before + (long long)(all - 1) * kBlock);
+          r.hk = at.head; r.q0 = ci.q0; r.row0 = ci.row0; r.nrows = ci.nrows;
+          r.end = chunk::Runs(kind, plan[0].all * Hkv, plan[1].all * Hkv, gridDim.x).of(
+              plan[kind].begin + at.x + before + (long long)(all - 1) * chunk::kBlock);
           ca.runs[kind * gridDim.x + plan[kind].run] = r;
         }
         return it;
       };
-      // The blocks of the slots' items that lie in the run: block j begins at x + before + j kBlock.
+      // The blocks of the slots' items that lie in the run: block j begins at at.x + before + j kBlock.
       auto look = [&]() {
-        if (loaded != base) {
+        if (loaded != at.base) {
           const bool begins = loaded < 0;
           load_slots();
-          if (begins) x -= __shfl_sync(0xffffffffu, before, plan[kind].slot & 31);
+          if (begins) at.x -= __shfl_sync(0xffffffffu, before, plan[kind].slot & 31);
         }
         const int all = max(1, ci.n_blocks);
-        auto first_from = [&](long long p) {
-          p -= x + before;
-          return p <= 0 ? 0 : (int)min((long long)all, (p + kBlock - 1) / kBlock);
-        };
-        b0 = first_from(0);
-        b1 = first_from(plan[kind].end - plan[kind].begin);
+        b0 = chunk::first_block(0, at.x + before, all);
+        b1 = chunk::first_block(plan[kind].end - plan[kind].begin, at.x + before, all);
         const bool in = ci.nrows > 0 && b0 < b1;
         // The end of an item that began in another run comes last: the whole items of all runs then begin with their
         // first keys at about the same time, and L2 serves those that share a head.
-        const bool is_late = in && x + before < 0;
+        const bool is_late = in && at.x + before < 0;
         if (is_late) *late_item = my_item();
         __syncwarp();
         late = late || __any_sync(0xffffffffu, is_late);
@@ -561,21 +490,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             kind = begun++ ? 1 - first_kind : first_kind;
             if (plan[kind].begin == plan[kind].end) continue;
             ended = false;
-            base = plan[kind].slot & ~31;
-            head = plan[kind].head;
+            at.base = plan[kind].slot & ~31;
+            at.head = plan[kind].head;
             loaded = -1;
-            x = plan[kind].x;  // (of the run's first item: those before it are taken off below)
-          } else {
-            x += length;
-            base += 32;
-            if (base >= n_items) {
-              base = 0;
-              ++head;
-            }
-            if (x >= plan[kind].end - plan[kind].begin) {
-              ended = true;
-              continue;
-            }
+            at.x = plan[kind].x;  // (of the run's first item: those before it are taken off below)
+          } else if (!at.next(length, plan[kind].end - plan[kind].begin, n_items, Hkv)) {
+            ended = true;
+            continue;
           }
           look();
         }
@@ -1234,8 +1155,8 @@ cudaError_t launch_attn_chunk_tc(const PromptArgs& a, const DecodeArgs& d, const
   if (enc == nullptr || !encode_q(enc, &tq, a.q, a.D, a.H, G, a.Tq, a.qs, &q_tma)) return cudaErrorInvalidValue;
   const int slots = (int)prompt_tile_slots(a.Tq, a.n, G, 2 * TM);
   // one CTA an SM, as far as the longest sequences that the cache may hold make as many runs
-  const long long longest = kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * kBlock;
-  const long long runs_most = a.Hkv * (long long)slots * longest / kShortest;
+  const long long longest = chunk::kItem + ((long long)d.c.width * d.c.page_size + BK - 1) / BK * chunk::kBlock;
+  const long long runs_most = a.Hkv * (long long)slots * longest / chunk::kShortest;
   const int ctas = (int)(runs_most < 1 ? 1 : (runs_most < device_sm_count() ? runs_most : device_sm_count()));
   ChunkArgs ca{};
   ca.d = d;
