@@ -533,8 +533,9 @@ moe_status moe_attention_decode_ex(const moe_kv_cache* cache, int layer, const v
  * Workspace: moe_attention_chunk_workspace_bytes(cache, n, Tq, H) bytes (0 on bad sizes), prepared with
  *   moe_workspace_init. moe_attention_chunk_ex: scratch memory apart, as in moe_attention_prompt_ex.
  * Device checks: offsets that decrease or leave [0, Tq], a slot, a length or a page out of range record
- *   MOE_ERR_DEVICE_CHECK (detail = sequence). With such offsets that sequence's rows are not computed, with such a slot or
- *   length they see nothing; page 0 stands in for such a page. */
+ *   MOE_ERR_DEVICE_CHECK (detail = sequence). With such offsets that sequence's rows are not computed, and those of
+ *   other sequences need not be: a row is right or as it was (or, where two valid sequences have it, anything). With such a
+ *   slot or length a sequence's rows see nothing; page 0 stands in for such a page. */
 size_t moe_attention_chunk_workspace_bytes(const moe_kv_cache* cache, int n, int Tq, int H);
 moe_status moe_attention_chunk(const moe_kv_cache* cache, int layer, const void* q, const int32_t* slots,
                                const int32_t* q_offsets, int n, int Tq, int H, int64_t q_stride, int64_t out_stride,

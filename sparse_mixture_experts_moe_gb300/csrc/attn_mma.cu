@@ -63,6 +63,8 @@ attn_mma_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Sh
     pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
     const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
+    // (records what is out of range: bad offsets' own slot may be found by nobody)
+    if (PAGED && tid == 0 && hk == 0 && blockIdx.z == 0 && (int)blockIdx.x < a.n) load_chunk_seq(a, da, blockIdx.x);
     seq = find_tile_seq(a.qo, a.n, G, kRows, slot);
     sq = PAGED ? load_chunk_seq(a, da, seq) : load_seq(a, seq);
     const long long r0 = ((long long)slot - ((long long)sq.q0 * G / kRows + seq)) * kRows;

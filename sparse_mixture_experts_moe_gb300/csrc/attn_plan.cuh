@@ -31,9 +31,9 @@ MOE_PLAN int visible_keys(int t, int nq, int nk, int causal) {
   return lim < 0 ? 0 : (lim > nk ? nk : lim);
 }
 
-// Whether a sequence's offsets are out of order or range. Bisection needs them in order, and a plan, a tile and a join, which
-// look for a sequence each in its own way, agree only then. So a chunk call's sequences end in front of the first one with
-// such offsets.
+// Whether a sequence's offsets are out of order or range. Bisection needs them in order, and what looks for a sequence in two
+// ways agrees only then: attn_chunk.cu's plan and its walk along the items take the sequences in front of the first one with
+// such offsets, and the join behind the tile kernels asks whether a tile would have been found.
 MOE_PLAN bool bad_offsets(int q0, int q1, int Tq) { return q0 < 0 || q1 < q0 || q1 > Tq; }
 
 // ------------------------------------------------------------------ attn_chunk.cu
@@ -134,7 +134,8 @@ struct Runs {
   }
   MOE_PLAN long long begin(int c) const { return all * c / n; }
   MOE_PLAN int of(long long x) const {  // (the last one behind the end: pieces are numbered by it)
-    return (int)least(n - 1LL, ((x + 1) * n - 1) / all);
+    const int c = (int)(((x + 1) * n - 1) / all);
+    return least(c, n - 1);
   }
 };
 // Which run of a kind a CTA takes: those of kind 1 go on where those of kind 0 end, so that a short call's lie in CTAs of

@@ -88,8 +88,13 @@ attn_tile_kernel(const __grid_constant__ PromptArgs pa, const __grid_constant__ 
     pages = da.c.table + (long long)(s0 < 0 || s0 >= da.c.n_slots ? 0 : s0) * da.c.width;
   } else {
     const int slot = gridDim.x - 1 - blockIdx.x;  // a prompt's last rows see the most keys: they start first
+    // (Bad offsets' own slot may be found by nobody: CTA i looks at sequence i's, asked for here and looked at once the
+    // slot's are there.)
+    const int own = PAGED ? min((int)blockIdx.x, pa.n - 1) : 0;
+    const int own0 = PAGED ? pa.qo[own] : 0, own1 = PAGED ? pa.qo[own + 1] : 0;
     seq = find_tile_seq(pa.qo, pa.n, G, kRows, slot);
     sq = PAGED ? load_chunk_seq(pa, da, seq) : load_seq(pa, seq);
+    if (PAGED && bad_offsets(own0, own1, pa.Tq)) record_error(pa.status, MOE_ERR_DEVICE_CHECK, own);
     if (PAGED) pages = da.c.table + (long long)sq.k0 * da.c.width;
     const long long first = (long long)sq.q0 * G / kRows + seq;
     const long long r0 = ((long long)slot - first) * kRows;
@@ -640,18 +645,29 @@ decode_join_simt_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
 }
 
 // A chunk's rows, whose keys were taken in `pieces` parts: a warp a row, the parts in their order. A lane holds elements
-// 4 lane + 128 x. A row of no sequence (or of one with bad offsets) stays as it is.
+// 4 lane + 128 x. A row of no sequence (or of one with bad offsets) stays as it is. Tiles find a slot's sequence and the join a
+// token's: over offsets out of order it may come to one whose tile nobody found, and whose pieces are another call's.
+constexpr int kJoinThreads = 128;
 template <typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
 chunk_rows_join_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ DecodeArgs d, int pieces) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, D = a.D;
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int tok = (int)(row / a.H), h = (int)(row % a.H), seq = find_tile_seq_warp(a.qo, a.n, 1, 1, tok, 0);
+  bool bad = false;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < a.n; i += kJoinThreads) bad = bad || bad_offsets(a.qo[i], a.qo[i + 1], a.Tq);
+  bad = __syncthreads_or(bad);
   if (row >= (long long)a.Tq * a.H) return;
-  const int tok = (int)(row / a.H), h = (int)(row % a.H);
-  const Seq sq = load_chunk_seq(a, d, find_tile_seq_warp(a.qo, a.n, 1, 1, tok, 0));
+  const Seq sq = load_chunk_seq(a, d, seq);
   if (tok < sq.q0 || tok >= sq.q0 + sq.nq) return;
+  if (bad) {
+    const int G = a.H / a.Hkv;
+    const long long slot = (long long)sq.q0 * G / kRows + seq + ((long long)(tok - sq.q0) * G + h % G) / kRows;
+    if (find_tile_seq(a.qo, a.n, G, kRows, slot) != seq) return;
+  }
   const float* p = d.part + row * pieces * (D + 2);
   auto ml = [&](int i) { return *reinterpret_cast<const float2*>(p + (long long)i * (D + 2) + D); };
   float M = -INFINITY, l = 0.f;
@@ -782,8 +798,8 @@ cudaError_t launch_attn_chunk_tiles(const PromptArgs& a, const DecodeArgs& d, in
                                                : launch_tiles<false, false, true>(a, sp, a.D, grid, s);
   if (e != cudaSuccess || pieces == 1) return e;
   const dim3 rows((unsigned)(((long long)a.Tq * a.H + 3) / 4));
-  return a.dt == MOE_DTYPE_BF16 ? launch_pdl(chunk_rows_join_kernel<__nv_bfloat16>, rows, dim3(128), 0, s, a, d, pieces)
-                                : launch_pdl(chunk_rows_join_kernel<float>, rows, dim3(128), 0, s, a, d, pieces);
+  return a.dt == MOE_DTYPE_BF16 ? launch_pdl(chunk_rows_join_kernel<__nv_bfloat16>, rows, dim3(kJoinThreads), 0, s, a, d, pieces)
+                                : launch_pdl(chunk_rows_join_kernel<float>, rows, dim3(kJoinThreads), 0, s, a, d, pieces);
 }
 
 cudaError_t launch_attn_decode_simt(const DecodeArgs& a, cudaStream_t s) {

@@ -115,3 +115,35 @@ extern "C" int chunk_plan(const int32_t* qo, int n, int Tq, int G, int Hkv, int 
   }
   return count;
 }
+
+// The tile kernels and their join: written[t] whether the tile of 64 rows of a slot has the first or the last row of token t,
+// joined[t] whether the join, which looks for the token's own sequence (32 places a step, a lane each), takes those.
+extern "C" void chunk_rows(const int32_t* qo, int n, int Tq, int G, uint8_t* written, uint8_t* joined) {
+  constexpr int R = 64;
+  const long long slots = (long long)Tq * G / R + n;
+  auto ok = [&](int i) { return !bad_offsets(qo[i], qo[i + 1], Tq); };
+  for (long long s = 0; s < slots; ++s) {
+    const int i = find_tile_seq(qo, n, G, R, s);
+    const long long r0 = (s - ((long long)qo[i] * G / R + i)) * R, rows = ok(i) ? (long long)(qo[i + 1] - qo[i]) * G : 0;
+    for (long long r = r0; r0 >= 0 && r < std::min(rows, r0 + R); ++r)
+      written[qo[i] + r / G] |= (r % G == 0 ? 1 : 0) | (r % G == G - 1 ? 2 : 0);
+  }
+  bool bad = false;
+  for (int i = 0; i < n; ++i) bad = bad || !ok(i);
+  for (int t = 0; t < Tq; ++t) {
+    int i = 0, len = n;
+    while (len > 1) {
+      const int step = (len + 31) / 32;
+      int k = -1;
+      for (int lane = 0; lane < 32; ++lane) k += lane * step < len && qo[i + lane * step] <= t ? 1 : 0;
+      const int skip = std::max(k, 0) * step;
+      i += skip;
+      len = std::min(len - skip, step);
+    }
+    if (!ok(i) || t < qo[i] || t >= qo[i + 1]) continue;
+    for (int h = 0; h < G; h += std::max(1, G - 1)) {
+      const long long slot = (long long)qo[i] * G / R + i + ((long long)(t - qo[i]) * G + h) / R;
+      if (!bad || find_tile_seq(qo, n, G, R, slot) == i) joined[t] |= (h == 0 ? 1 : 0) | (h == G - 1 ? 2 : 0);
+    }
+  }
+}

@@ -14,11 +14,16 @@ TILE, ROWS, KEYS = 128, 256, 128
 
 
 @pytest.fixture(scope="module")
-def plan(tmp_path_factory):
-    lib = str(tmp_path_factory.mktemp("plan") / "plan.so")
+def lib(tmp_path_factory):
+    path = str(tmp_path_factory.mktemp("plan") / "plan.so")
     subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", CSRC, os.path.join(ROOT, "tests", "chunk_plan.cpp"),
-                    "-o", lib], check=True)
-    f = ctypes.CDLL(lib).chunk_plan
+                    "-o", path], check=True)
+    return ctypes.CDLL(path)
+
+
+@pytest.fixture(scope="module")
+def plan(lib):
+    f = lib.chunk_plan
 
     def run(offs, Tq, G, Hkv, lens, found_lens=None, causal=True, ctas=152):
         """The items found: tuples (CTA, kind, run, head, sequence, row0, rows, b0, b1, blocks, last run)."""
@@ -134,6 +139,27 @@ def test_random_bad_offsets(plan, seed, kind):
             offs[i] = r.randint(0, max(1, Tq)) if kind == "decreasing" else r.choice(
                 [-1, Tq + 1, 2 * Tq + 5, 2 ** 31 - 1, -2 ** 31, r.randint(-50, Tq + 50)])
         check(plan(offs, Tq, G, Hkv, lens, causal=causal, ctas=ctas), offs, Tq, G, Hkv, lens, causal)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_joined_rows_are_written(lib, seed):
+    """The tile kernels find a slot's sequence, their join a token's. It takes no row that no tile wrote, and over good offsets
+    every sequence's."""
+    r = random.Random(seed)
+    for k in range(16):
+        offs, Tq, G, _, lens, _, _ = draw(r)
+        if k % 4 == 0:  # more sequences than the join's lanes
+            nq = [r.choice([0, 1, 3]) for _ in range(r.randint(33, 200))]
+            offs, Tq, lens = [sum(nq[:i]) for i in range(len(nq) + 1)], sum(nq), nq
+        for _ in range(k % 3):
+            offs[r.randrange(len(offs))] = r.choice([r.randint(0, Tq), r.randint(-50, Tq + 50), 2 ** 31 - 1, -2 ** 31])
+        at = np.array(offs, dtype=np.int32)
+        written, joined = np.zeros(Tq + 1, dtype=np.uint8), np.zeros(Tq + 1, dtype=np.uint8)
+        lib.chunk_rows(at.ctypes.data_as(ctypes.c_void_p), len(lens), Tq, G, written.ctypes.data_as(ctypes.c_void_p),
+                       joined.ctypes.data_as(ctypes.c_void_p))
+        assert (joined & ~written == 0).all()
+        if good(offs, Tq) == len(lens):
+            assert (joined[offs[0]:offs[-1]] == 3).all() and not joined[offs[-1]:].any() and (joined == written).all()
 
 
 @pytest.mark.parametrize("seed", range(30))

@@ -1,5 +1,6 @@
-"""Chunk calls over offsets out of order or range: the sequences in front of the first such ones are right, and nothing else is
-written, in the results or behind them."""
+"""Chunk calls over offsets out of order or range: they are recorded, what is computed is right, and nothing else is written, in
+the results or behind them."""
+import numpy as np
 import pytest
 import torch
 
@@ -11,7 +12,7 @@ from test_gpu_chunk import pool, reference
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF16, F32 = torch.bfloat16, torch.float32
-KINDS = [(BF16, 64), (BF16, 128)]  # tcgen05
+KINDS = [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 64), (F32, 128)]  # tcgen05, warp MMAs, CUDA cores
 
 # offsets, Tq, query heads a key/value head, key/value heads, lengths
 CALLS = [
@@ -41,14 +42,27 @@ def test_bad_offsets(call, dtype, D):
     assert a.device_status() == (moe.MOE_OK, 0)
     out = torch.full((Tq + guard, H, D), 5.0, dtype=dtype, device=DEV)
     lse = torch.full((Tq + guard, H), 5.0, dtype=F32, device=DEV)
+    valid = [i for i in range(n) if 0 <= offs[i] <= offs[i + 1] <= Tq]
     for _ in range(2):
         a.chunk(q, cache, slots, i32(offs, DEV), out=out[:Tq], lse=lse[:Tq])
         status, detail = a.device_status()
-        bad = [i for i in range(n) if offs[i] < 0 or offs[i + 1] < offs[i] or offs[i + 1] > Tq]
-        assert status == moe.MOE_ERR_DEVICE_CHECK and detail in bad
-        seqs = good(offs, Tq)
-        end = offs[seqs] if seqs else 0
-        assert (out[end:] == 5).all() and (lse[end:] == 5).all()
-        if seqs:
-            ref = reference(q[:end], held, list(range(seqs)), offs[:seqs + 1], True, D ** -0.5)
-            check(out[:end], lse[:end], ref, max(lens), D, dtype)
+        assert status == moe.MOE_ERR_DEVICE_CHECK and 0 <= detail < n and detail not in valid
+        left = ((out == 5).all(-1) & (lse == 5)).cpu().numpy()
+        assert left[Tq:].all()
+        claims = np.zeros(Tq, dtype=int)
+        for i in valid:
+            claims[offs[i]:offs[i + 1]] += 1
+        assert left[:Tq][claims == 0].all()
+        for i in valid:  # rows that one sequence alone has are right, or as they were
+            rows = np.arange(offs[i], offs[i + 1])[claims[offs[i]:offs[i + 1]] == 1]
+            if len(rows) == 0:
+                continue
+            ref = reference(q[offs[i]:offs[i + 1]], held, [i], [0, offs[i + 1] - offs[i]], True, D ** -0.5)
+            ref = tuple(np.where(left[rows].reshape(left[rows].shape + (1,) * (x.ndim - 2)), 0 if k else 5.0, x[rows - offs[i]])
+                        for k, x in enumerate(ref))
+            ours = out[rows], torch.where(torch.tensor(left[rows], device=DEV), 0.0, lse[rows])
+            check(*ours, ref, max(lens), D, dtype)
+        if dtype == BF16 and D <= 128:  # the sequences end in front of the first bad offsets
+            seqs = good(offs, Tq)
+            end = offs[seqs] if seqs else 0
+            assert left[end:].all() and not left[:end].any()
