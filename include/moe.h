@@ -552,8 +552,9 @@ moe_status moe_attention_chunk_ex(const moe_kv_cache* cache, int layer, const vo
  *   (x_a, x_b) -> (x_a c - x_b s, x_b c + x_a s),  c, s = magnitude * cos, sin(position * f_p)
  *   with (a, b) = (p, p + R/2) (MOE_ROTARY_HALF) or (2p, 2p + 1) (MOE_ROTARY_INTERLEAVED). Elements from R on stay.
  * With norm weights w [D] (`dt`, 16-byte aligned; NULL: no norm) a head is first x / sqrt(mean x^2 + eps) * w, over
- *   all D elements. Everything is fp32 up to one rounding to `dt`; the angles are exact to 2^-31 of a circle at any int32
- *   position (negative ones turn back).
+ *   all D elements. Everything is fp32 up to one rounding to `dt`. Positions are any int32 (negative ones turn back): an
+ *   angle is off by at most 2^-25 of a circle, from fp32, and position * 2^-52, from the doubles that its frequency is
+ *   computed in (of more than a radian a position: that many times as much).
  *
  * moe_rotary: host memory that the caller owns and the calls read.
  * moe_rotary_init: f_p = base^(-2p / R), base > 1, changed for contexts longer than the trained original_len positions:

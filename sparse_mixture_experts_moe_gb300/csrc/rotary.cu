@@ -5,9 +5,11 @@
 // and one rounding to the heads' type at the end.
 //
 // An angle only matters modulo a circle, so f_p is held as a 64-bit fraction of a circle a position and multiplied by the
-// position modulo 2^64: the product's upper bits are the angle, off by at most position * 2^-65 + 2^-32 of a circle
-// however far the position (fp32 products lose all of it near 2^24). The two upper bits are the quadrant; sine and cosine
-// of the rest, |x| <= pi / 4, are their Taylor sums to x^9 and x^10 (the first term left out is below 2.5e-9 of the value).
+// position modulo 2^64: the product's upper bits are the angle, however far the position (fp32 products lose all of it
+// near 2^24). The fraction comes from doubles: pow, a scaling and the division by 2 pi leave less than 2^-52 of a circle a
+// position for f_p <= 1 (2^-55 seen). The two upper bits of the product are the quadrant, the next 30 the rest, which
+// fp32 holds to three roundings of 2^-24 of it, less than 2^-25 of a circle; sine and cosine of it, |x| <= pi / 4, are
+// their Taylor sums to x^9 and x^10 (the first term left out is below 2.5e-9 of the value).
 //
 // LPR lanes share a row (a head of a token), so that a warp has 32 / LPR rows under way; a lane holds NC pairs of chunks
 // of VEC elements. In the half layout those are elements p .. p + VEC - 1 and R/2 + p ..: both parts of its pairs, so no
