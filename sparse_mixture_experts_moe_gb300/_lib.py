@@ -201,11 +201,19 @@ def _stream(stream) -> Optional[int]:
 def _allocator(torch):
     """empty(shape, strides, dtype): a new tensor's memory on the current CUDA device, as torch.empty gives it. torch.empty
     itself looks at its arguments and dispatches for longer than a kernel's launch takes (two results: 11.7 us a call of
-    apply, 7.7 so); its entry for compiled programs, where this torch has it, goes straight to the allocator."""
+    apply, 7.9 so); its entry for compiled programs goes straight to the allocator. Where the dispatcher has something to do
+    (deterministic algorithms, which fill new memory, or a dispatch mode), or this torch lacks the entry, torch.empty_strided."""
+    def dispatched(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
     entry = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
-    if entry is not None:
-        return entry
-    return lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+    if entry is None or modes is None:
+        return dispatched
+    deterministic = torch.are_deterministic_algorithms_enabled
+
+    def empty(shape, strides, dtype):
+        return dispatched(shape, strides, dtype) if deterministic() or modes() else entry(shape, strides, dtype)
+    return empty
 
 
 def _check(rc: int, where: str) -> int:
