@@ -68,7 +68,7 @@ def _apart(a, b):
     if at >= end[1] or bt >= end[0]:
         return True
     row = a.stride()[0] * size
-    if a.stride()[0] != b.stride()[0] or a.shape[0] < 2 or b.shape[0] < 2:
+    if row == 0 or a.stride()[0] != b.stride()[0] or a.shape[0] < 2 or b.shape[0] < 2:  # (0: one row, broadcast)
         return False
     off = (bt - at) % row  # of b's heads behind a's in a token's row
     return off >= a.shape[1] * a.shape[2] * size and off + b.shape[1] * b.shape[2] * size <= row
