@@ -3,8 +3,11 @@
 // and single tokens lie in one call.
 //   S = Q K^T (scores), P = 2^(c S - c m) (weights, c = scale log2 e), O += P V, out = O / l
 // in one pass over the keys, as for packed prompts (attn_tc.cu), whose item, MMA order and rescaling these are: 256
-// packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 8 in log2 units,
-// weights rounded to bf16 for the MMA (off by at most 2^-8 of each) and their sum not. What is different here:
+// packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 8 in log2 units.
+// A weight is rounded to bf16 (off by at most 2^-8 of it) because the MMA takes both operands in one type; the weights' sum,
+// O and the pieces of rows are fp32. That moves results by 5.5e-4 to 7.2e-4 of their norm (64 sequences with 8 chunks; 4096
+// tokens behind 28672), below the 1.6e-3 that their own rounding to bf16 is: against 64 bits they are as far off as with
+// fp32 weights (1.6e-3 and 1.7e-3 both ways). What is different here:
 // - Work is shared out by keys, not by items (attn_plan.cuh): one sequence of 100,000 keys beside a hundred short ones takes
 //   every SM.
 // - Keys and values come from pages, by one TMA box a page and 64 elements (of pages of 128 positions and more a box a
@@ -166,8 +169,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
-  // Only after TMEM is allocated: a dependent kernel that starts on this SM may allocate some before it waits for
-  // this grid. And only after the wait: the decode's own-key kernel relies on everything before this grid being done.
+  // Only after TMEM is allocated: a dependent kernel that starts on this SM may allocate some before it waits for this grid.
   griddep_launch_dependents();
 
   const int H = pa.H, Hkv = pa.Hkv, D = pa.D, G = H / Hkv;

@@ -144,6 +144,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   auto blocks = [](int keys) { return (keys + BK - 1) / BK; };
 
   if (warp >= kSoftWarps) {
+    // 8 * 32 * 232 + 4 * 32 * 40 = 64512, as at the launch.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kSoftWarps + 1) {
       // -------------------------------------------------------------- items, K and V

@@ -11,8 +11,8 @@ namespace {
 
 constexpr int BK = 128;       // keys per block
 constexpr int TM = 128;       // rows per tile
-// Registers: 12 warps of 168 at launch (64512); the softmax warps take 232 each (a row of 128 scores stays in
-// registers), the other four keep 40: 8 * 32 * 232 + 4 * 32 * 40 = 64512.
+// 12 warps of 168 registers at launch (64512), which each kernel then shares out among its softmax warps (a row of 128
+// scores stays in registers) and the other four.
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr int kMaxSmem = 232448;
