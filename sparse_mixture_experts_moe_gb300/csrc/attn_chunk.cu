@@ -52,10 +52,10 @@ constexpr int kItems = 3;   // items published: one worked on, one ahead, one be
 constexpr int kItemReaders = 1 + 8 + 2;
 
 // What a CTA has of a kind: the length of all items of a head, its run's number, beginning and end, and the slot, place
-// and head of the item that the run begins in; and the sequences in front of the first bad offsets.
+// and head of the item that the run begins in.
 struct Plan {
   long long all, begin, end, x;
-  int run, slot, head, seqs;
+  int run, slot, head, unused;
 };
 
 template <int DP> struct Cfg {
@@ -190,12 +190,12 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   };
   auto blocks = [](int keys) { return chunk::blocks_of(keys); };
 
+  int seqs = pa.n;  // in front of the first bad offsets
   // This CTA's runs: a scan over the lengths of all tile slots, each thread with some of them in a row.
   {
     const int per = (n_items + kThreads - 1) / kThreads, s0 = min(n_items, tid * per), s1 = min(n_items, s0 + per);
     // The offsets are looked at beside the walk, and it is done again without the sequences from the first bad ones on:
     // in the usual case that costs no wait of its own.
-    int seqs = pa.n;
     auto walk = [&](auto f) {
       chunk::walk_slots(pa.qo, seqs, pa.Tq, G, pa.causal, s0, s1,
                         [&](int i) { return slot_len(ca.d.c, ca.d.slots[i]); }, f);
@@ -262,7 +262,6 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         plan[kind].run = c;
         plan[kind].begin = begin;
         plan[kind].end = end;
-        plan[kind].seqs = seqs;
         ChunkRun none;
         none.nrows = 0;
         ca.runs[kind * gridDim.x + c] = none;
@@ -425,7 +424,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         ci = chunk::SlotItem{};
         if (s < n_items)
           ci = chunk::slot_item(pa.qo, ca.d.slots, pa.Tq, G, pa.causal, s,
-                                find_tile_seq(pa.qo, plan[0].seqs, G, chunk::kRows, s),
+                                find_tile_seq(pa.qo, seqs, G, chunk::kRows, s),
                                 [&](int slot) { return slot_len(ca.d.c, slot); });
         if (chunk::item_kind(ci.nrows) != kind) ci.nrows = 0;
         loaded = at.base;

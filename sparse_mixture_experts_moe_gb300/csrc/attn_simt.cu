@@ -655,10 +655,12 @@ chunk_rows_join_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, D = a.D;
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  int i = min((int)threadIdx.x, a.n - 1);
+  const int q0 = a.qo[i], q1 = a.qo[i + 1];  // (asked for ahead of the search)
   const int tok = (int)(row / a.H), h = (int)(row % a.H), seq = find_tile_seq_warp(a.qo, a.n, 1, 1, tok, 0);
-  bool bad = false;
+  bool bad = bad_offsets(q0, q1, a.Tq);
 #pragma unroll 1
-  for (int i = threadIdx.x; i < a.n; i += kJoinThreads) bad = bad || bad_offsets(a.qo[i], a.qo[i + 1], a.Tq);
+  while ((i += kJoinThreads) < a.n) bad = bad || bad_offsets(a.qo[i], a.qo[i + 1], a.Tq);
   bad = __syncthreads_or(bad);
   if (row >= (long long)a.Tq * a.H) return;
   const Seq sq = load_chunk_seq(a, d, seq);
