@@ -5,9 +5,9 @@
 // in one pass over the keys, as for packed prompts (attn_tc.cu), whose item, MMA order and rescaling these are: 256
 // packed rows (two tiles of 128) of one key/value head, with m only raised when a maximum exceeds it by 8 in log2 units.
 // A weight is rounded to bf16 (off by at most 2^-8 of it) because the MMA takes both operands in one type; the weights' sum,
-// O and the pieces of rows are fp32. That moves results by 5.5e-4 to 7.2e-4 of their norm (64 sequences with 8 chunks; 4096
-// tokens behind 28672), below the 1.6e-3 that their own rounding to bf16 is: against 64 bits they are as far off as with
-// fp32 weights (1.6e-3 and 1.7e-3 both ways). What is different here:
+// O and the pieces of rows are fp32. That moves results by 5.4e-4 to 7.2e-4 of their norm (64 sequences with 8 chunks; 4096
+// tokens behind 28672) and by up to 1.6e-3 where rows see few keys, beside the 1.7e-3 that their own rounding to bf16 is:
+// from 64 bits they are 1.7e-3 with either weights, and 1.8e-3 over few keys. What is different here:
 // - Work is shared out by keys, not by items (attn_plan.cuh): one sequence of 100,000 keys beside a hundred short ones takes
 //   every SM.
 // - Keys and values come from pages, by one TMA box a page and 64 elements (of pages of 128 positions and more a box a

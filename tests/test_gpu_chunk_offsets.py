@@ -1,5 +1,7 @@
 """Chunk calls over offsets out of order or range: they are recorded, what is computed is right, and nothing else is written, in
 the results or behind them."""
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -28,10 +30,7 @@ CALLS = [
 ]
 
 
-@pytest.mark.parametrize("dtype,D", KINDS)
-@pytest.mark.parametrize("call", range(len(CALLS)))
-def test_bad_offsets(call, dtype, D):
-    offs, Tq, G, Hk, lens = CALLS[call]
+def run(offs, Tq, G, Hk, lens, dtype, D):
     n, H, guard = len(lens), G * Hk, 300
     cache, held = pool(lens, 64, Hk, D, dtype, 1)
     q = tensor((Tq, H, D), 5, dtype, DEV)
@@ -46,7 +45,10 @@ def test_bad_offsets(call, dtype, D):
     for _ in range(2):
         a.chunk(q, cache, slots, i32(offs, DEV), out=out[:Tq], lse=lse[:Tq])
         status, detail = a.device_status()
-        assert status == moe.MOE_ERR_DEVICE_CHECK and 0 <= detail < n and detail not in valid
+        if len(valid) < n:
+            assert status == moe.MOE_ERR_DEVICE_CHECK and 0 <= detail < n and detail not in valid
+        else:
+            assert status == moe.MOE_OK
         left = ((out == 5).all(-1) & (lse == 5)).cpu().numpy()
         assert left[Tq:].all()
         claims = np.zeros(Tq, dtype=int)
@@ -64,5 +66,27 @@ def test_bad_offsets(call, dtype, D):
             check(*ours, ref, max(lens), D, dtype)
         if dtype == BF16 and D <= 128:  # the sequences end in front of the first bad offsets
             seqs = good(offs, Tq)
-            end = offs[seqs] if seqs else 0
-            assert left[end:].all() and not left[:end].any()
+            mine = np.zeros(Tq, dtype=bool)
+            mine[offs[0]:offs[seqs]] = seqs > 0
+            assert (left[:Tq].all(-1) != mine).all() and (left[:Tq].any(-1) != mine).all()
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+@pytest.mark.parametrize("call", range(len(CALLS)))
+def test_bad_offsets(call, dtype, D):
+    run(*CALLS[call], dtype, D)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+@pytest.mark.parametrize("seed", range(12))
+def test_random_bad_offsets(seed, dtype, D):
+    r = random.Random(seed)
+    n = r.choice([2, 3, 5, 9, 40])
+    nq = [r.choice([0, 1, 2, 5, r.randint(1, 30), r.randint(1, 150 if n < 9 else 30)]) for _ in range(n)] + [1]
+    lens = [r.choice([0, a, a + r.randint(0, 900)]) for a in nq]
+    offs = offsets(nq)
+    Tq = offs[-1] + r.choice([0, 3])
+    for _ in range(r.choice([1, 1, 2, 4])):
+        offs[r.randrange(len(offs))] = r.choice([r.randint(0, Tq), r.randint(0, Tq), r.randint(-40, Tq + 40), 2 ** 31 - 1,
+                                                 -2 ** 31, -1, Tq + 1])
+    run(offs, Tq, r.choice([1, 2, 7, 8]), r.choice([1, 2]), lens, dtype, D)
